@@ -38,6 +38,15 @@ CanonError.
                                        -> elements per scan tile
     set_schedule(knob, value), schedule(grid=..., reduce_partials=..., spin_limit=...)
                                        -> the schedule override (tests)
+
+The operators of sequence models (``include/canon_seq.h``, module ``seq``):
+
+    embedding(weight, ids, scale)      -> scale * weight[ids]
+    embedding_grad(dout, ids, rows, scale, ...)
+                                       -> its gradient, a canonical reduction by id
+    causal_conv(x, weight, bias, ...), causal_conv_grad(...), causal_conv_step(...)
+    selective_scan(u, delta, A, B, C, ...), selective_scan_grad(...),
+    selective_scan_step(...)
 """
 from __future__ import annotations
 
@@ -507,3 +516,11 @@ class schedule:
         for k, v in self.saved.items():
             set_schedule(k, v)
         return False
+
+
+from .seq import (  # noqa: E402
+    CausalConvGrads, SelectiveScanGrads, causal_conv, causal_conv_grad,
+    causal_conv_grad_workspace_bytes, causal_conv_step, embedding, embedding_grad,
+    embedding_grad_workspace_bytes, selective_scan, selective_scan_grad,
+    selective_scan_grad_workspace_bytes, selective_scan_states, selective_scan_step,
+    selective_scan_workspace_bytes)

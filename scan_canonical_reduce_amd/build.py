@@ -21,6 +21,10 @@ SOURCES = [
     "scan_ip1.hip", "scan_ip1_narrow_f64.hip", "scan_ip1_narrow_f32.hip",
     "ops_mul_f64.hip", "ops_mul_f32.hip", "ops_min_f64.hip", "ops_min_f32.hip",
     "ops_max_f64.hip", "ops_max_f32.hip", "scan_noalloc.cpp",
+    "seq_api.cpp", "embedding.hip", "embedding_group.hip",
+    "causal_conv_f32.hip", "causal_conv_bf16.hip", "causal_conv_f16.hip",
+    "selective_scan_f32.hip", "selective_scan_bf16.hip", "selective_scan_f16.hip",
+    "selective_scan_grad_f32.hip", "selective_scan_grad_bf16.hip", "selective_scan_grad_f16.hip",
 ]
 
 # -ffp-contract=off: no FMA contraction; no fast-math; subnormals kept (no

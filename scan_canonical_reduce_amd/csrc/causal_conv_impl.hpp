@@ -1,0 +1,381 @@
+// Causal depthwise convolution over a few rows: forward, backward, one row.
+//
+// A thread owns V neighbouring channels (16 bytes) and walks a run of rows
+// with the last rows in registers, so each row is read once (plus taps - 1
+// rows in front of each run, out of the cache).  Bound by memory traffic: 2 K
+// multiply-adds per 2 elements moved.
+#pragma once
+
+#include "causal_conv.hpp"
+#include "column_sum.hpp"
+#include "launch.hpp"
+
+namespace canon {
+namespace seq {
+
+template <typename T>
+__device__ __forceinline__ float ld_param(const void* p, bool f32, int64_t i)
+{
+    return f32 ? static_cast<const float*>(p)[i]
+               : ld<T>(static_cast<const typename T::store_t*>(p) + i);
+}
+
+template <typename T, int V>
+__device__ __forceinline__ void unpack(const Vec<T, V>& x, float (&v)[V])
+{
+#pragma unroll
+    for (int i = 0; i < V; ++i) v[i] = T::load(x.e[i]);
+}
+
+template <typename T, int K, int V>
+struct ConvParams {
+    float w[K][V], b[V];
+
+    __device__ __forceinline__ void load(const ConvArgs& a, int32_t ch)
+    {
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+#pragma unroll
+            for (int k = 0; k < K; ++k)
+                w[k][i] = ld_param<T>(a.weight, a.param_f32, (int64_t)(ch + i) * K + k);
+            b[i] = a.bias ? ld_param<T>(a.bias, a.param_f32, ch + i) : 0.f;
+        }
+    }
+};
+
+// Row t of the sequence, or of the initial state in front of it (t < 0).
+template <typename T, int K, int V>
+__device__ __forceinline__ void conv_row(const ConvArgs& a, const typename T::store_t* x,
+                                         int64_t s, int32_t t, int32_t ch, float (&v)[V])
+{
+    if (t >= 0) {
+        unpack<T, V>(ld_vec<T, V>(x + (int64_t)t * a.x.row), v);
+    } else if (a.init) {
+        const typename T::store_t* p = static_cast<const typename T::store_t*>(a.init);
+        unpack<T, V>(ld_vec<T, V>(p + (s * (K - 1) + (K - 1 + t)) * a.channels + ch), v);
+    } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i) v[i] = 0.f;
+    }
+}
+
+template <int K, int V>
+__device__ __forceinline__ float conv_sum(const float (&win)[K][V], const float (&w)[K][V],
+                                          float b, int i)
+{
+    float p = b;
+#pragma unroll
+    for (int k = 0; k < K; ++k) p = fma32(w[k][i], win[k][i], p);
+    return p;
+}
+
+// RUN rows per thread (at least K - 1, so that only a sequence's first run
+// reads the initial state).
+template <typename T, int K, int V, int RUN>
+__global__ __launch_bounds__(256) void k_causal_conv(ConvArgs a)
+{
+    const int32_t nv = a.channels / V;
+    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    const int64_t slot = i / nv;
+    const int32_t ch = (int32_t)(i - slot * nv) * V;
+    if (slot >= slot_count<RUN>(a.q.seqs, a.q.rows, a.q.starts != nullptr)) return;
+    const Chunk ck = slot_chunk<RUN>(a.q, slot);
+    if (ck.row > 0 && ck.len <= 0) return;
+    const typename T::store_t* x = rows_ptr<T>(a.x, ck.s, a.q, ck.span.first) + ch;
+    typename T::store_t* out = rows_ptr<T>(a.out, ck.s, a.q, ck.span.first) + ch;
+
+    float win[K][V];  // the rows up to the current one, oldest first
+#pragma unroll
+    for (int k = 0; k + 1 < K; ++k) conv_row<T, K, V>(a, x, ck.s, ck.row - (K - 1) + k, ch, win[k + 1]);
+
+    if (a.final && ck.row == 0) {
+        // By the thread that has read the initial state, which may be the
+        // same buffer: the last K - 1 rows of initial state and sequence.
+        typename T::store_t* f =
+            static_cast<typename T::store_t*>(a.final) + ck.s * (K - 1) * a.channels + ch;
+#pragma unroll
+        for (int k = 0; k + 1 < K; ++k) {
+            const int32_t t = ck.span.len - (K - 1) + k;
+            float v[V];
+            if (t >= 0) {
+                conv_row<T, K, V>(a, x, ck.s, t, ch, v);
+            } else {  // row K - 1 + t of the initial state, in win[K + t]
+#pragma unroll
+                for (int m = 0; m + 1 < K; ++m)
+                    if (m == K - 1 + t)
+#pragma unroll
+                        for (int j = 0; j < V; ++j) v[j] = win[m + 1][j];
+            }
+            st_vec<T, V>(f + (int64_t)k * a.channels, v);
+        }
+    }
+
+    ConvParams<T, K, V> p;
+    p.load(a, ch);
+    constexpr int U = RUN < 8 ? RUN : 8;  // rows in flight
+    for (int32_t t0 = 0; t0 < ck.len; t0 += U) {
+        Vec<T, V> in[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int32_t t = t0 + u < ck.len ? t0 + u : ck.len - 1;
+            in[u] = ld_vec<T, V>(x + (int64_t)(ck.row + t) * a.x.row);
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            if (t0 + u >= ck.len) break;
+#pragma unroll
+            for (int k = 0; k + 1 < K; ++k)
+#pragma unroll
+                for (int j = 0; j < V; ++j) win[k][j] = win[k + 1][j];
+            unpack<T, V>(in[u], win[K - 1]);
+            float y[V];
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                y[j] = conv_sum<K, V>(win, p.w, p.b[j], j);
+                if (a.silu) y[j] = silu_f(y[j], sigmoid_f(y[j]));
+            }
+            st_vec<T, V>(out + (int64_t)(ck.row + t0 + u) * a.out.row, y);
+        }
+    }
+}
+
+// Backward: with dp = dout silu'(p), dx[t] = sum_k w[k] dp[t + K - 1 - k].  A
+// thread walks its run and K - 1 rows beyond it, p recomputed from x.
+// Its rows' part of dw and db goes to the workspace, per slot.
+template <typename T, int K, int V>
+__global__ __launch_bounds__(256) void k_causal_conv_grad(ConvArgs a)
+{
+    constexpr int RUN = CANON_CONV_CHUNK;
+    const int32_t nv = a.channels / V;
+    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    const int64_t slot = i / nv;
+    const int32_t ch = (int32_t)(i - slot * nv) * V;
+    if (slot >= slot_count<RUN>(a.q.seqs, a.q.rows, a.q.starts != nullptr)) return;
+    const Chunk ck = slot_chunk<RUN>(a.q, slot);
+    float dw[K][V], db[V];
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+        db[j] = 0.f;
+#pragma unroll
+        for (int k = 0; k < K; ++k) dw[k][j] = 0.f;
+    }
+    if (ck.row == 0 || ck.len > 0) {
+        const int64_t first = ck.span.first;
+        const typename T::store_t* x = rows_ptr<T>(a.x, ck.s, a.q, first) + ch;
+        const typename T::store_t* go = rows_ptr<T>(a.dout, ck.s, a.q, first) + ch;
+        typename T::store_t* dx = rows_ptr<T>(a.dx, ck.s, a.q, first) + ch;
+        const typename T::store_t* df =
+            a.dfinal ? static_cast<const typename T::store_t*>(a.dfinal) +
+                           ck.s * (K - 1) * a.channels + ch
+                     : nullptr;
+        typename T::store_t* di = a.dinit ? static_cast<typename T::store_t*>(a.dinit) +
+                                                ck.s * (K - 1) * a.channels + ch
+                                          : nullptr;
+        ConvParams<T, K, V> p;
+        p.load(a, ch);
+        float win[K][V], dp[K][V];
+#pragma unroll
+        for (int k = 0; k < K; ++k)
+#pragma unroll
+            for (int j = 0; j < V; ++j) win[k][j] = dp[k][j] = 0.f;
+        if (ck.len > 0)
+#pragma unroll
+            for (int k = 0; k + 1 < K; ++k)
+                conv_row<T, K, V>(a, x, ck.s, ck.row - (K - 1) + k, ch, win[k + 1]);
+        const int32_t len = ck.span.len;
+        const int32_t end = ck.row + ck.len;  // of the run
+        const int32_t stop = end + K - 1;
+        constexpr int U = 4;
+        for (int32_t t0 = ck.row; t0 < stop; t0 += U) {
+            Vec<T, V> in[U], gin[U];
+            if (len > 0)
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    const int32_t t = t0 + u < len ? t0 + u : len - 1;
+                    in[u] = ld_vec<T, V>(x + (int64_t)t * a.x.row);
+                    gin[u] = ld_vec<T, V>(go + (int64_t)t * a.dout.row);
+                }
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int32_t t = t0 + u;
+                if (t >= stop) break;
+#pragma unroll
+                for (int k = 0; k + 1 < K; ++k)
+#pragma unroll
+                    for (int j = 0; j < V; ++j) {
+                        win[k][j] = win[k + 1][j];
+                        dp[k][j] = dp[k + 1][j];
+                    }
+                if (t < len) {
+                    unpack<T, V>(in[u], win[K - 1]);
+                    unpack<T, V>(gin[u], dp[K - 1]);
+                    if (a.silu)
+#pragma unroll
+                        for (int j = 0; j < V; ++j) {
+                            const float s = conv_sum<K, V>(win, p.w, p.b[j], j);
+                            dp[K - 1][j] *= silu_slope(s, sigmoid_f(s));
+                        }
+                    if (t < end)
+#pragma unroll
+                        for (int j = 0; j < V; ++j) {
+                            db[j] += dp[K - 1][j];
+#pragma unroll
+                            for (int k = 0; k < K; ++k)
+                                dw[k][j] = fma32(dp[K - 1][j], win[k][j], dw[k][j]);
+                        }
+                } else {
+#pragma unroll
+                    for (int j = 0; j < V; ++j) dp[K - 1][j] = 0.f;
+                }
+                // row m = t - (K - 1) has all of dp[m .. t]: w[K - 1] dp[m] first
+                const int32_t m = t - (K - 1);
+                const bool initial = m < 0;
+                if (initial ? di == nullptr : m < ck.row) continue;
+                float y[V];
+#pragma unroll
+                for (int j = 0; j < V; ++j) {
+                    y[j] = p.w[K - 1][j] * dp[0][j];
+#pragma unroll
+                    for (int k = 1; k < K; ++k) y[j] = fma32(p.w[K - 1 - k][j], dp[k][j], y[j]);
+                }
+                // the final state's row that is row m
+                const int32_t f = m - (len - (K - 1));
+                if (df && f >= 0) {
+                    float g[V];
+                    unpack<T, V>(ld_vec<T, V>(df + (int64_t)f * a.channels), g);
+#pragma unroll
+                    for (int j = 0; j < V; ++j) y[j] += g[j];
+                }
+                if (initial)
+                    st_vec<T, V>(di + (int64_t)(K - 1 + m) * a.channels, y);
+                else
+                    st_vec<T, V>(dx + (int64_t)m * a.dx.row, y);
+            }
+        }
+    }
+    float* pw = a.ws_w + (slot * a.channels + ch) * K;
+#pragma unroll
+    for (int j = 0; j < V; ++j)
+#pragma unroll
+        for (int k = 0; k < K; ++k) pw[j * K + k] = dw[k][j];
+    if (a.dbias)
+#pragma unroll
+        for (int j = 0; j < V; ++j) a.ws_b[slot * a.channels + ch + j] = db[j];
+}
+
+// One row of each sequence; the state's rows move up by one.
+template <typename T, int K, int V>
+__global__ __launch_bounds__(256) void k_causal_conv_step(ConvArgs a)
+{
+    const int32_t nv = a.channels / V;
+    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    const int64_t s = i / nv;
+    const int32_t ch = (int32_t)(i - s * nv) * V;
+    if (s >= a.q.seqs) return;
+    const typename T::store_t* x = static_cast<typename T::store_t*>(a.x.p) + s * a.x.seq + ch;
+    float win[K][V];
+#pragma unroll
+    for (int k = 0; k + 1 < K; ++k) conv_row<T, K, V>(a, x, s, k - (K - 1), ch, win[k]);
+    const Vec<T, V> in = ld_vec<T, V>(x);
+    unpack<T, V>(in, win[K - 1]);
+    ConvParams<T, K, V> p;
+    p.load(a, ch);
+    float y[V];
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+        y[j] = conv_sum<K, V>(win, p.w, p.b[j], j);
+        if (a.silu) y[j] = silu_f(y[j], sigmoid_f(y[j]));
+    }
+    if (a.final) {
+        typename T::store_t* f =
+            static_cast<typename T::store_t*>(a.final) + s * (K - 1) * a.channels + ch;
+#pragma unroll
+        for (int k = 0; k + 1 < K; ++k) st_vec<T, V>(f + (int64_t)k * a.channels, win[k + 1]);
+    }
+    st_vec<T, V>(static_cast<typename T::store_t*>(a.out.p) + s * a.out.seq + ch, y);
+}
+
+// --------------------------------------------------------------------- launches
+template <int RUN>
+unsigned conv_grid(const ConvArgs& a, int v)
+{
+    const int64_t slots = slot_count<RUN>(a.q.seqs, a.q.rows, a.q.starts != nullptr);
+    return (unsigned)((slots * (a.channels / v) + 255) / 256);
+}
+
+template <typename T, int K, int V>
+hipError_t launch_conv_v(const ConvArgs& a, hipStream_t st)
+{
+    // Long runs read fewer rows twice; short ones are for launches that would
+    // leave compute units without work.
+    const int64_t threads = slot_count<32>(a.q.seqs, a.q.rows, a.q.starts != nullptr) *
+                            (a.channels / V);
+    if (threads >= (int64_t)device_cus() * 512)
+        k_causal_conv<T, K, V, 32><<<dim3(conv_grid<32>(a, V)), dim3(256), 0, st>>>(a);
+    else
+        k_causal_conv<T, K, V, 8><<<dim3(conv_grid<8>(a, V)), dim3(256), 0, st>>>(a);
+    return hipGetLastError();
+}
+
+template <typename T, int K, int V>
+hipError_t launch_conv_grad_v(const ConvArgs& a, hipStream_t st)
+{
+    const int64_t slots =
+        slot_count<CANON_CONV_CHUNK>(a.q.seqs, a.q.rows, a.q.starts != nullptr);
+    const unsigned grid = conv_grid<CANON_CONV_CHUNK>(a, V);
+    if (grid) k_causal_conv_grad<T, K, V><<<dim3(grid), dim3(256), 0, st>>>(a);
+    if (hipError_t e = hipGetLastError()) return e;
+    if (hipError_t e =
+            launch_column_sum(a.ws_w, slots, (int64_t)a.channels * K, K, K, a.dweight, st))
+        return e;
+    return a.dbias ? launch_column_sum(a.ws_b, slots, a.channels, 1, 1, a.dbias, st) : hipSuccess;
+}
+
+template <typename T, int K, int V>
+hipError_t launch_conv_step_v(const ConvArgs& a, hipStream_t st)
+{
+    const int64_t n = a.q.seqs * (a.channels / V);
+    k_causal_conv_step<T, K, V><<<dim3((unsigned)((n + 255) / 256)), dim3(256), 0, st>>>(a);
+    return hipGetLastError();
+}
+
+#define CANON_CONV_TAPS(FN, V)                 \
+    switch (taps) {                            \
+        case 1: return FN<T, 1, V>(a, st);     \
+        case 2: return FN<T, 2, V>(a, st);     \
+        case 3: return FN<T, 3, V>(a, st);     \
+        case 4: return FN<T, 4, V>(a, st);     \
+        case 5: return FN<T, 5, V>(a, st);     \
+        case 6: return FN<T, 6, V>(a, st);     \
+        case 7: return FN<T, 7, V>(a, st);     \
+        default: return FN<T, 8, V>(a, st);    \
+    }
+
+// Elements of a 16-byte access; the backward pass, which keeps two windows and
+// the sums of dw, takes half as many 16-bit ones.
+template <typename T>
+constexpr int kConvV = 16 / (int)sizeof(typename T::store_t);
+
+template <typename T>
+hipError_t launch_causal_conv(const ConvArgs& a, int taps, hipStream_t st)
+{
+    if (a.vec) CANON_CONV_TAPS(launch_conv_v, kConvV<T>)
+    CANON_CONV_TAPS(launch_conv_v, 1)
+}
+
+template <typename T>
+hipError_t launch_causal_conv_grad(const ConvArgs& a, int taps, hipStream_t st)
+{
+    if (a.vec) CANON_CONV_TAPS(launch_conv_grad_v, 4)
+    CANON_CONV_TAPS(launch_conv_grad_v, 1)
+}
+
+template <typename T>
+hipError_t launch_causal_conv_step(const ConvArgs& a, int taps, hipStream_t st)
+{
+    if (a.vec) CANON_CONV_TAPS(launch_conv_step_v, kConvV<T>)
+    CANON_CONV_TAPS(launch_conv_step_v, 1)
+}
+
+}  // namespace seq
+}  // namespace canon

@@ -1,0 +1,63 @@
+// Launchers of the embedding lookup and its gradient (internal).
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "seq_device.hpp"
+
+namespace canon {
+namespace seq {
+
+struct EmbedArgs {
+    const void* weight;
+    int64_t ld_weight, rows, width;
+    const void* ids;
+    bool ids64, vec;
+    int64_t tokens;
+    float scale;
+    void* out;
+    int64_t ld_out;
+};
+
+struct EmbedGradArgs {
+    const void* dout;
+    int64_t ld_dout;
+    const void* ids;
+    bool ids64, vec, accumulate;
+    int64_t tokens, rows, width;
+    float scale;
+    int64_t padding_id;
+    void* dw;
+    int64_t ld_dw;
+    // workspace
+    int32_t *order, *offset;    // tokens by id; the first of each id (rows + 1)
+    int64_t* items;             // tokens + rows
+    int32_t *n_items, *n_long, *before;  // per group of ids
+    int32_t* longs;
+    float *part, *part_last;
+    int64_t ld_part;
+};
+
+constexpr int kEmbedChunk = 64;  // occurrences that one wave sums
+
+// Ids of a workgroup of the grouping kernel, and the number of workgroups.
+inline int64_t ids_per_group(int64_t rows)
+{
+    const int64_t r = (rows + 255) / 256;
+    return r < 16 ? 16 : r > 512 ? 512 : r;  // 16 waves' counts of 512 ids: 32 KiB of LDS
+}
+inline int64_t id_groups(int64_t rows)
+{
+    const int64_t r = ids_per_group(rows);
+    return (rows + r - 1) / r;
+}
+
+template <typename T>
+hipError_t launch_embedding(const EmbedArgs& a, hipStream_t st);
+hipError_t launch_embedding_group(const EmbedGradArgs& a, hipStream_t st);
+template <typename T, typename G>
+hipError_t launch_embedding_grad(const EmbedGradArgs& a, hipStream_t st);
+
+}  // namespace seq
+}  // namespace canon

@@ -1,0 +1,376 @@
+// Embedding lookup, and its gradient as a canonical reduction by key.
+//
+// Lookup: 16-byte accesses, one row's vectors in neighbouring threads; bound
+// by memory traffic.
+//
+// Gradient, three kernels:
+//  1. k_embed_group: tokens by id, ascending within an id, without a sort
+//     pass over memory.  Workgroup b owns the ids [b R, b R + R) and reads all
+//     ids twice (they stay in cache): once to count its own ids, per wave, and
+//     the ids below its range, which place it in the order; once to place its
+//     tokens, each wave its own stretch, in token order.  No workgroup needs
+//     another's result, so there is one launch and no wait.  It also lists the
+//     work: (row, chunk of 64 occurrences), one entry for a row no token names
+//     when that row is to be written as zero.
+//  2. k_embed_sum: a wave takes one entry and a slab of 64 vectors of columns,
+//     and adds the rows of dout in the order of the pairwise tree (8 rows in
+//     flight, a binary counter of complete subtrees above them).  An aligned
+//     chunk of a sequence is a subtree of its pairwise tree, so the rows of an
+//     id with more than 64 occurrences leave one partial value per chunk.
+//  3. k_embed_finish: the tree over the partial values of those.
+#pragma once
+
+#include "embedding.hpp"
+#include "launch.hpp"
+
+namespace canon {
+namespace seq {
+
+__device__ __forceinline__ int64_t token_id(const void* ids, bool ids64, int64_t t)
+{
+    return ids64 ? static_cast<const int64_t*>(ids)[t]
+                 : (int64_t) static_cast<const int32_t*>(ids)[t];
+}
+
+template <typename T, int V>
+__global__ __launch_bounds__(256) void k_embedding(EmbedArgs a)
+{
+    using E = typename T::store_t;
+    const int64_t nv = a.width / V;
+    const int64_t n = a.tokens * nv;
+    constexpr int U = 4;
+    const int64_t i0 = (int64_t)blockIdx.x * (256 * U) + threadIdx.x;
+    Vec<T, V> x[U];
+    E* dst[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        const int64_t i = i0 + u * 256;
+        dst[u] = nullptr;
+        x[u] = Vec<T, V>{};
+        if (i < n) {
+            const int64_t t = i / nv, c = (i - t * nv) * V;
+            const int64_t id = token_id(a.ids, a.ids64, t);
+            dst[u] = static_cast<E*>(a.out) + t * a.ld_out + c;
+            if (id >= 0 && id < a.rows)
+                x[u] = ld_vec<T, V>(static_cast<const E*>(a.weight) + id * a.ld_weight + c);
+        }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        if (!dst[u]) continue;
+        float y[V];
+#pragma unroll
+        for (int j = 0; j < V; ++j) y[j] = T::load(x[u].e[j]) * a.scale;
+        st_vec<T, V>(dst[u], y);
+    }
+}
+
+// x[r][j] (r < 8) becomes the pairwise tree's value over r, in x[0][j]
+template <int V>
+__device__ __forceinline__ void tree8(float (&x)[8][V])
+{
+#pragma unroll
+    for (int d = 1; d < 8; d *= 2)
+#pragma unroll
+        for (int r = 0; r < 8; r += 2 * d)
+#pragma unroll
+            for (int j = 0; j < V; ++j) x[r][j] += x[r + d][j];
+}
+
+template <typename G, int V>
+__device__ __forceinline__ void store_grad(const EmbedGradArgs& a, int64_t v, int64_t c,
+                                           const float (&sum)[V])
+{
+    typename G::store_t* p = static_cast<typename G::store_t*>(a.dw) + v * a.ld_dw + c;
+    float y[V];
+#pragma unroll
+    for (int j = 0; j < V; ++j) y[j] = sum[j] * a.scale;
+    if (a.accumulate) {
+        const Vec<G, V> old = ld_vec<G, V>(p);
+#pragma unroll
+        for (int j = 0; j < V; ++j) y[j] = G::load(old.e[j]) + y[j];
+    }
+    st_vec<G, V>(p, y);
+}
+
+// Groups whose prefix sums a workgroup keeps in LDS; callers walk more groups
+// in blocks of that many.
+constexpr int kGroupsInLds = 1024;
+
+// Prefix sums of the counts of groups [first, first + kGroupsInLds), by 256
+// threads; returns the total.
+__device__ __forceinline__ int64_t group_prefix(const int32_t* counts, int64_t first,
+                                                int64_t groups, int32_t* prefix)
+{
+    __shared__ int32_t wave_sum[4];
+    const int tid = threadIdx.x;
+    int32_t c[4], s = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int64_t g = first + tid * 4 + i;
+        c[i] = g < groups ? counts[g] : 0;
+        s += c[i];
+    }
+    int32_t run = s;
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2) {
+        const int32_t o = __shfl_up(run, d, 64);
+        if ((tid & 63) >= d) run += o;
+    }
+    __syncthreads();  // the previous block's prefix is no longer read
+    if ((tid & 63) == 63) wave_sum[tid >> 6] = run;
+    __syncthreads();
+    int32_t base = run - s;
+    for (int w = 0; w < (tid >> 6); ++w) base += wave_sum[w];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        prefix[tid * 4 + i] = base;
+        base += c[i];
+    }
+    if (tid == 255) prefix[kGroupsInLds] = base;
+    __syncthreads();
+    return prefix[kGroupsInLds];
+}
+
+// The group holding entry i of a block: the last g with prefix[g] <= i among
+// those with entries.
+__device__ __forceinline__ int find_group(const int32_t* prefix, int32_t i)
+{
+    int lo = 0, hi = kGroupsInLds - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (prefix[mid] <= i)
+            lo = mid;
+        else
+            hi = mid - 1;
+    }
+    return lo;
+}
+
+// Sums occurrences [64 c, ...) of row v: V columns of this lane.
+template <typename T, typename G, int V>
+__device__ __forceinline__ void sum_entry(const EmbedGradArgs& a, int64_t v, int64_t c,
+                                          int64_t col, int lane)
+{
+    const int32_t off = a.offset[v], n = a.offset[v + 1] - off;
+    const bool in = col < a.width;
+    float acc[V];
+#pragma unroll
+    for (int j = 0; j < V; ++j) acc[j] = 0.f;
+    if (n == 0) {
+        if (in && !a.accumulate) store_grad<G, V>(a, v, col, acc);
+        return;
+    }
+    const int64_t p0 = off + c * kEmbedChunk;
+    const int m = n - c * kEmbedChunk < kEmbedChunk ? (int)(n - c * kEmbedChunk) : kEmbedChunk;
+    const int32_t mine = a.order[p0 + (lane < m ? lane : 0)];
+    const typename T::store_t* x = static_cast<const typename T::store_t*>(a.dout) + (in ? col : 0);
+    float sub[3][V];  // complete subtrees of 8, 16, 32 rows
+    float all[V];
+    for (int b = 0; b * 8 < m; ++b) {
+        Vec<T, V> raw[8];
+#pragma unroll
+        for (int r = 0; r < 8; ++r) {
+            const int k = b * 8 + r < m ? b * 8 + r : 0;
+            raw[r] = ld_vec<T, V>(x + (int64_t)__builtin_amdgcn_readlane(mine, k) * a.ld_dout);
+        }
+        float t[8][V];
+#pragma unroll
+        for (int r = 0; r < 8; ++r)
+#pragma unroll
+            for (int j = 0; j < V; ++j)  // -0: the exact identity of an addition
+                t[r][j] = b * 8 + r < m ? T::load(raw[r].e[j]) : -0.f;
+        tree8<V>(t);
+        // b counts in binary; the value climbs over the set bits
+        int l = 0;
+#pragma unroll
+        for (int lev = 0; lev < 3; ++lev) {
+            if (l != lev) continue;
+            if (b >> lev & 1) {
+#pragma unroll
+                for (int j = 0; j < V; ++j) t[0][j] = sub[lev][j] + t[0][j];
+                l = lev + 1;
+            } else {
+#pragma unroll
+                for (int j = 0; j < V; ++j) sub[lev][j] = t[0][j];
+            }
+        }
+        if (l == 3)
+#pragma unroll
+            for (int j = 0; j < V; ++j) all[j] = t[0][j];
+    }
+    const int nb = (m + 7) / 8;
+    if (nb == 8) {
+#pragma unroll
+        for (int j = 0; j < V; ++j) acc[j] = all[j];
+    } else {
+#pragma unroll
+        for (int j = 0; j < V; ++j) acc[j] = -0.f;
+#pragma unroll
+        for (int lev = 0; lev < 3; ++lev)
+            if (nb >> lev & 1)
+#pragma unroll
+                for (int j = 0; j < V; ++j) acc[j] = sub[lev][j] + acc[j];
+    }
+    if (!in) return;
+    if (n <= kEmbedChunk) {
+        store_grad<G, V>(a, v, col, acc);
+        return;
+    }
+    // Full chunks and last chunks of long rows each start at least 64
+    // occurrences apart, so start / 64 numbers them.
+    const bool last = (c + 1) * kEmbedChunk >= n;
+    float* part = (last ? a.part_last + p0 / kEmbedChunk * a.ld_part
+                        : a.part + (off / kEmbedChunk + c) * a.ld_part) + col;
+#pragma unroll
+    for (int j = 0; j < V; ++j) part[j] = acc[j];
+}
+
+template <typename T, typename G, int V>
+__global__ __launch_bounds__(256) void k_embed_sum(EmbedGradArgs a, int64_t groups, int64_t ids)
+{
+    __shared__ int32_t prefix[kGroupsInLds + 1];
+    const int lane = threadIdx.x & 63;
+    const int64_t wave = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6), waves = gridDim.x * 4ll;
+    const int64_t slabs = (a.width + 64 * V - 1) / (64 * V);
+    for (int64_t g0 = 0; g0 < groups; g0 += kGroupsInLds) {
+        const int64_t total = group_prefix(a.n_items, g0, groups, prefix);
+        for (int64_t i = wave; i < total * slabs; i += waves) {
+            const int32_t e = (int32_t)(i / slabs);
+            const int64_t slab = i - e * slabs;
+            const int k = find_group(prefix, e);
+            const int64_t g = g0 + k;
+            const int64_t item = a.items[(int64_t)a.before[g] + g * ids + (e - prefix[k])];
+            sum_entry<T, G, V>(a, item & 0xffffffff, item >> 32, slab * 64 * V + lane * V, lane);
+        }
+    }
+}
+
+// Rows with more than 64 occurrences: the pairwise tree over the partial
+// values, an aligned power-of-two range of them per wave, then over the 16
+// waves.
+template <typename G>
+__global__ __launch_bounds__(1024) void k_embed_finish(EmbedGradArgs a, int64_t groups)
+{
+    __shared__ int32_t prefix[kGroupsInLds + 1];
+    __shared__ int32_t wsum[16];
+    __shared__ float waves[16][64];
+    const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+    const int64_t slabs = (a.width + 63) / 64;
+    for (int64_t g0 = 0; g0 < groups; g0 += kGroupsInLds) {
+        const int32_t c = g0 + threadIdx.x < groups ? a.n_long[g0 + threadIdx.x] : 0;
+        int32_t run = c;
+#pragma unroll
+        for (int d = 1; d < 64; d *= 2) {
+            const int32_t o = __shfl_up(run, d, 64);
+            if (lane >= d) run += o;
+        }
+        __syncthreads();
+        if (lane == 63) wsum[w] = run;
+        __syncthreads();
+        int32_t base = run - c;
+        for (int k = 0; k < w; ++k) base += wsum[k];
+        prefix[threadIdx.x] = base;
+        if (threadIdx.x == 1023) prefix[kGroupsInLds] = base + c;
+        __syncthreads();
+        const int64_t total = prefix[kGroupsInLds];
+        for (int64_t i = blockIdx.x; i < total * slabs; i += gridDim.x) {
+            const int32_t e = (int32_t)(i / slabs);
+            const int64_t col = (i - e * slabs) * 64 + lane;
+            const int k = find_group(prefix, e);
+            const int64_t v = a.longs[a.before[g0 + k] / (kEmbedChunk + 1) + (e - prefix[k])];
+            const int32_t off = a.offset[v], n = a.offset[v + 1] - off;
+            const int64_t m = (n + kEmbedChunk - 1) / kEmbedChunk;
+            int64_t range = 1;  // partial values per wave
+            while (range * 16 < m) range *= 2;
+            const int64_t lo = w * range, hi = lo + range < m ? lo + range : m;
+            constexpr int kLevels = 26;  // 2^31 / 64 partial values
+            float st[kLevels];
+            int64_t count = 0;
+            for (int64_t b = lo; b < hi; b += 8) {
+                float x[8][1];
+#pragma unroll
+                for (int r = 0; r < 8; ++r) {
+                    const int64_t j = b + r;
+                    x[r][0] = -0.f;
+                    if (j < hi && col < a.width)
+                        x[r][0] = j == m - 1
+                                      ? a.part_last[(off + j * kEmbedChunk) / kEmbedChunk * a.ld_part + col]
+                                      : a.part[(off / kEmbedChunk + j) * a.ld_part + col];
+                }
+                tree8<1>(x);
+                float t = x[0][0];
+                bool done = false;
+#pragma unroll
+                for (int lev = 0; lev < kLevels; ++lev) {
+                    if (done) continue;
+                    if (count >> lev & 1) {
+                        t = st[lev] + t;
+                    } else {
+                        st[lev] = t;
+                        done = true;
+                    }
+                }
+                ++count;
+            }
+            float acc = -0.f;
+#pragma unroll
+            for (int lev = 0; lev < kLevels; ++lev)
+                if (count >> lev & 1) acc = st[lev] + acc;
+            waves[w][lane] = acc;
+            __syncthreads();
+            if (w == 0 && col < a.width) {
+                float x[16];
+#pragma unroll
+                for (int j = 0; j < 16; ++j) x[j] = waves[j][lane];
+#pragma unroll
+                for (int d = 1; d < 16; d *= 2)
+#pragma unroll
+                    for (int j = 0; j < 16; j += 2 * d) x[j] += x[j + d];
+                float s[1] = {x[0]};
+                store_grad<G, 1>(a, v, col, s);
+            }
+            __syncthreads();
+        }
+    }
+}
+
+template <typename T>
+hipError_t launch_embedding(const EmbedArgs& a, hipStream_t st)
+{
+    constexpr int V = 16 / (int)sizeof(typename T::store_t);
+    const int64_t n = a.tokens * (a.vec ? a.width / V : a.width);
+    const unsigned grid = (unsigned)((n + 1023) / 1024);
+    if (grid == 0) return hipSuccess;
+    if (a.vec)
+        k_embedding<T, V><<<dim3(grid), dim3(256), 0, st>>>(a);
+    else
+        k_embedding<T, 1><<<dim3(grid), dim3(256), 0, st>>>(a);
+    return hipGetLastError();
+}
+
+template <typename T, typename G>
+hipError_t launch_embedding_grad(const EmbedGradArgs& a, hipStream_t st)
+{
+    constexpr int V = 16 / (int)sizeof(typename T::store_t);
+    const int64_t groups = id_groups(a.rows), ids = ids_per_group(a.rows);
+    if (hipError_t e = launch_embedding_group(a, st)) return e;
+    const int64_t cap = (int64_t)device_cus() * 8;
+    const int64_t slabs = (a.width + 64 * (a.vec ? V : 1) - 1) / (64 * (a.vec ? V : 1));
+    const int64_t want = ((a.tokens + a.rows) * slabs + 3) / 4;
+    const dim3 grid((unsigned)capped_grid(want < cap ? want : cap));
+    if (a.vec)
+        k_embed_sum<T, G, V><<<grid, dim3(256), 0, st>>>(a, groups, ids);
+    else
+        k_embed_sum<T, G, 1><<<grid, dim3(256), 0, st>>>(a, groups, ids);
+    if (hipError_t e = hipGetLastError()) return e;
+    if (a.tokens <= kEmbedChunk) return hipSuccess;
+    const int64_t most = a.tokens / (kEmbedChunk + 1) * ((a.width + 63) / 64);
+    const int64_t cus = (int64_t)device_cus();
+    k_embed_finish<G><<<dim3((unsigned)capped_grid(most < cus ? (most ? most : 1) : cus)), dim3(1024),
+                        0, st>>>(a, groups);
+    return hipGetLastError();
+}
+
+}  // namespace seq
+}  // namespace canon

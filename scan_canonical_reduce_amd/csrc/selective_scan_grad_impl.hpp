@@ -1,0 +1,438 @@
+// Selective state space scan: backward pass.
+//
+// With lam[t] the gradient of h[t] and R[t] = a[t+1] lam[t+1] what reaches
+// h[t] from later rows,
+//   lam = C dy + R,  R[t-1] = a lam,  dy = dout z sigmoid(z)
+//   dB[t,n] = sum_d lam dl u      dC[t,n] = sum_d dy h
+//   through = sum_n B lam         decay   = R[t-1] h[t-1]  (= a h[t-1] lam)
+//   du  = through dl + D dy       ddl = sum_n A decay + through u
+//   dA  = sum_t dl decay          dD  = sum_t dy u        dz = dout y silu'(z)
+// Three passes over chunks of 64 rows: each chunk's fold of lam from zero,
+// backwards; the carries R between chunks; then each chunk with its carry.
+// The last pass reads the h that the forward pass saved every 16 rows, keeps
+// a and h of 16 rows in registers (lane layout of selective_scan_impl.hpp) and
+// walks them backwards.
+//
+// dB and dC are sums over channels, i.e. across the 16 lanes of a row of
+// lanes: sequence rows are folded into lanes two at a time (each level halves
+// both the number of values and the lanes a value is spread over: 15 additions
+// for 16 values where a plain butterfly takes 64), which leaves lane c with
+// sequence row bitrev(c).  The four waves of a workgroup are summed through LDS
+// and the workgroups' sums by a second kernel, in slab order.
+#pragma once
+
+#include "column_sum.hpp"
+#include "selective_scan_impl.hpp"
+
+namespace canon {
+namespace seq {
+
+// Inputs of a 16-row tile of the backward passes, loaded as in Tile.
+template <typename T, int KS, bool MAIN>
+struct GradTile {
+    typename T::store_t u[4], dl[4], z[4], go[4];
+    float B[KS], C[KS];
+
+    __device__ __forceinline__ void load(const ScanArgs& a, const Lane& l, int64_t s,
+                                         const Span& span, int32_t row, int32_t len, bool gate)
+    {
+        const int64_t first = span.first + row;
+        const typename T::store_t* pu = MAIN ? rows_ptr<T>(a.u, s, a.q, first) + l.ch : nullptr;
+        const typename T::store_t* pd = rows_ptr<T>(a.delta, s, a.q, first) + l.ch;
+        const typename T::store_t* pg = rows_ptr<T>(a.dout, s, a.q, first) + l.ch;
+        const typename T::store_t* pz = gate ? rows_ptr<T>(a.z, s, a.q, first) + l.ch : nullptr;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            const int64_t t = 4 * r + l.q < len ? 4 * r + l.q : len - 1;
+            if (MAIN) u[r] = pu[t * a.u.row];
+            dl[r] = pd[t * a.delta.row];
+            go[r] = pg[t * a.dout.row];
+            if (gate) z[r] = pz[t * a.z.row];
+        }
+        const int64_t t = l.c < len ? l.c : len - 1;
+        const int64_t gb = (int64_t)l.g * a.states;
+        load_bc<T, KS>(a, rows_ptr<T>(a.C, s, a.q, first + t) + gb, l.q, l.c < len, C);
+        if (MAIN)
+            load_bc<T, KS>(a, rows_ptr<T>(a.B, s, a.q, first + t) + gb, l.q, l.c < len, B);
+    }
+};
+
+template <int KS, int T>
+__device__ __forceinline__ void back_row(const float2 (*ex)[16], int c, const float (&A2)[KS],
+                                         const float (&C)[KS], float (&R)[KS], float& sdl)
+{
+    const float2 x = ex[T][c];  // dl, dy
+    sdl += x.x;
+#pragma unroll
+    for (int i = 0; i < KS; ++i)
+        R[i] = exp2_hw(x.x * A2[i]) * fma32(row_bcast<T>(C[i]), x.y, R[i]);
+}
+
+template <int KS, int T>
+__device__ __forceinline__ void back_rows(const float2 (*ex)[16], int c, const float (&A2)[KS],
+                                          const float (&C)[KS], float (&R)[KS], float& sdl)
+{
+    back_row<KS, T>(ex, c, A2, C, R, sdl);
+    if constexpr (T > 0) back_rows<KS, T - 1>(ex, c, A2, C, R, sdl);
+}
+
+// Each chunk's backward fold from zero, and its sum of dl.
+template <typename T, int KS>
+__global__ __launch_bounds__(256) void k_scan_back_sum(ScanArgs a)
+{
+    constexpr int NP = 4 * KS;
+    __shared__ float2 ex_all[4][kSub][16];
+    const int slabs = a.slabs * (a.channels / a.dg);
+    const int64_t slot = blockIdx.x / slabs;
+    const Lane l = lane_place(a, (int)(blockIdx.x - slot * slabs));
+    if (l.wch >= a.dg) return;
+    float2(*ex)[16] = ex_all[threadIdx.x >> 6];
+    const Chunk ck = slot_chunk<kCh>(a.q, slot);
+    if (ck.len <= 0) return;
+
+    float A2[KS], R[KS];
+#pragma unroll
+    for (int i = 0; i < KS; ++i) {
+        const int n = l.q * KS + i;
+        A2[i] = n < a.states ? a.A[(int64_t)l.ch * a.states + n] * kLog2e : 0.f;
+        R[i] = 0.f;
+    }
+    const float bias = a.bias ? a.bias[l.ch] : 0.f;
+    const bool gate = a.z.p != nullptr;
+    float sdl = 0.f;
+    int sub = (ck.len - 1) / kSub;
+    GradTile<T, KS, false> tile;
+    tile.load(a, l, ck.s, ck.span, ck.row + sub * kSub, ck.len - sub * kSub, gate);
+    for (; sub >= 0; --sub) {
+        const int32_t len = ck.len - sub * kSub;
+        float C[KS];
+#pragma unroll
+        for (int i = 0; i < KS; ++i) C[i] = tile.C[i];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            const float raw = T::load(tile.dl[r]) + bias;
+            const float d = a.softplus ? softplus_f(raw, nullptr) : raw;
+            float dy = T::load(tile.go[r]);
+            if (gate) {
+                const float z = T::load(tile.z[r]);
+                dy *= silu_f(z, sigmoid_f(z));
+            }
+            ex[4 * r + l.q][l.c] =
+                4 * r + l.q < len ? make_float2(d, dy) : make_float2(0.f, 0.f);
+        }
+        wave_lds_fence();
+        if (sub > 0)
+            tile.load(a, l, ck.s, ck.span, ck.row + (sub - 1) * kSub, kSub, gate);
+        back_rows<KS, kSub - 1>(ex, l.c, A2, C, R, sdl);
+        wave_lds_fence();
+    }
+    if (!l.active) return;
+    st_states<KS>(a.ws_state + (slot * a.channels + l.ch) * NP + l.q * KS, R);
+    if (l.q == 0) a.ws_dl[slot * a.channels + l.ch] = sdl;
+}
+
+// One level of the sum over a row's 16 lanes: lanes without bit `bit` of c keep
+// x and take the mirrored lane's x, lanes with it y.
+template <int CTRL>
+__device__ __forceinline__ float fold_lanes(float x, float y, bool upper)
+{
+    const float keep = upper ? y : x, send = upper ? x : y;
+    return keep + dpp<CTRL>(send);
+}
+
+constexpr int kMirror16 = 0x140, kMirror8 = 0x141, kMirror4 = 0x1b, kMirror2 = 0xb1;
+
+// Sums over the lanes of a row, sequence rows arriving in descending order T =
+// 15 .. 0; v[L] holds what waits for its partner at level L.
+template <int KS>
+struct LaneSum {
+    float wait[4][KS];
+
+    template <int T>
+    __device__ __forceinline__ void add(float (&x)[KS], int c)
+    {
+#pragma unroll
+        for (int i = 0; i < KS; ++i) {
+            if constexpr (T & 1) {
+                wait[0][i] = x[i];
+            } else {
+                const float a = fold_lanes<kMirror16>(x[i], wait[0][i], c & 8);
+                if constexpr (T & 2) {
+                    wait[1][i] = a;
+                } else {
+                    const float b = fold_lanes<kMirror8>(a, wait[1][i], c & 4);
+                    if constexpr (T & 4) {
+                        wait[2][i] = b;
+                    } else {
+                        const float d = fold_lanes<kMirror4>(b, wait[2][i], c & 2);
+                        if constexpr (T & 8)
+                            wait[3][i] = d;
+                        else
+                            x[i] = fold_lanes<kMirror2>(d, wait[3][i], c & 1);
+                    }
+                }
+            }
+        }
+    }
+};
+
+template <int KS>
+struct GradRegs {
+    float a[kSub][KS], h[kSub + 1][KS];  // h[t]: before row t
+    float A2[KS], R[KS], dA[KS], B[KS], C[KS];
+    float dBt[KS], dCt[KS];  // the tile's sums, once row 0 is folded
+    LaneSum<KS> sb, sc;
+    float th[4], dc[4], y[4];
+};
+
+template <int KS, int T>
+__device__ __forceinline__ void grad_forward(const float4 (*ex)[16], int c, bool gate,
+                                             GradRegs<KS>& g, float (&y)[4])
+{
+    const float4 x = ex[T][c];  // dl, dl u, dy
+    float acc = 0.f;
+#pragma unroll
+    for (int i = 0; i < KS; ++i) {
+        g.a[T][i] = exp2_hw(x.x * g.A2[i]);
+        g.h[T + 1][i] = fma32(g.a[T][i], g.h[T][i], row_bcast<T>(g.B[i]) * x.y);
+        acc = i == 0 ? row_bcast<T>(g.C[i]) * g.h[T + 1][i]
+                     : fma32(row_bcast<T>(g.C[i]), g.h[T + 1][i], acc);
+    }
+    y[T & 3] = acc;
+    if constexpr ((T & 3) == 3) {
+        if (gate) g.y[T >> 2] = fold_quad(y[0], y[1], y[2], y[3]);
+    }
+    if constexpr (T + 1 < kSub) grad_forward<KS, T + 1>(ex, c, gate, g, y);
+}
+
+template <int KS, int T>
+__device__ __forceinline__ void grad_backward(const float4 (*ex)[16], int c, GradRegs<KS>& g,
+                                              float (&th)[4], float (&dc)[4])
+{
+    const float4 x = ex[T][c];
+    float b[KS], s[KS], through = 0.f, decay = 0.f;
+#pragma unroll
+    for (int i = 0; i < KS; ++i) {
+        const float lam = fma32(row_bcast<T>(g.C[i]), x.z, g.R[i]);
+        b[i] = lam * x.y;
+        s[i] = x.z * g.h[T + 1][i];
+        through = i == 0 ? row_bcast<T>(g.B[i]) * lam : fma32(row_bcast<T>(g.B[i]), lam, through);
+        g.R[i] = g.a[T][i] * lam;
+        const float d = g.R[i] * g.h[T][i];
+        g.dA[i] = fma32(x.x, d, g.dA[i]);
+        decay = i == 0 ? g.A2[i] * d : fma32(g.A2[i], d, decay);
+    }
+    g.sb.template add<T>(b, c);
+    g.sc.template add<T>(s, c);
+    if constexpr (T == 0) {
+#pragma unroll
+        for (int i = 0; i < KS; ++i) {
+            g.dBt[i] = b[i];
+            g.dCt[i] = s[i];
+        }
+    }
+    th[T & 3] = through;
+    dc[T & 3] = decay;
+    if constexpr ((T & 3) == 0) {
+        g.th[T >> 2] = fold_quad(th[0], th[1], th[2], th[3]);
+        g.dc[T >> 2] = fold_quad(dc[0], dc[1], dc[2], dc[3]);
+    }
+    if constexpr (T > 0) grad_backward<KS, T - 1>(ex, c, g, th, dc);
+}
+
+// One chunk, given the carry R that enters it from later rows (a.ws_state,
+// which then takes the chunk's part of dA).
+template <typename T, int KS>
+__global__ __launch_bounds__(256, 2) void k_selective_scan_grad(ScanArgs a)
+{
+    constexpr int NP = 4 * KS;
+    __shared__ float4 ex_all[4][kSub][16];
+    alignas(16) __shared__ float bc[2][4][kSub][2 * NP];  // two buffers: one barrier a tile
+    const int slabs = a.slabs * (a.channels / a.dg);
+    const int64_t slot = blockIdx.x / slabs;
+    const int slab = (int)(blockIdx.x - slot * slabs);
+    const Lane l = lane_place(a, slab);
+    const int w = threadIdx.x >> 6;
+    float4(*ex)[16] = ex_all[w];
+    const Chunk ck = slot_chunk<kCh>(a.q, slot);
+    const int64_t at = (slot * a.channels + l.ch) * NP + l.q * KS;
+    if (ck.len <= 0) {  // an empty slot: its partial sums are zero
+        if (l.active) {
+            const float zero[KS] = {};
+            st_states<KS>(a.ws_state + at, zero);
+            if (l.q == 0) {
+                a.ws_dD[slot * a.channels + l.ch] = 0.f;
+                a.ws_dbias[slot * a.channels + l.ch] = 0.f;
+            }
+        }
+        return;
+    }
+
+    GradRegs<KS> g;
+#pragma unroll
+    for (int i = 0; i < KS; ++i) {
+        const int n = l.q * KS + i;
+        g.A2[i] = n < a.states ? a.A[(int64_t)l.ch * a.states + n] * kLog2e : 0.f;
+        g.R[i] = 0.f;
+        g.dA[i] = 0.f;
+    }
+    if (l.active) ld_states<KS>(a.ws_state + at, g.R);
+    const float bias = a.bias ? a.bias[l.ch] : 0.f, Dc = a.D ? a.D[l.ch] : 0.f;
+    const bool gate = a.z.p != nullptr;
+    float dD = 0.f, dbias = 0.f;
+    const int brev = (l.c & 1) << 3 | (l.c & 2) << 1 | (l.c & 4) >> 1 | (l.c & 8) >> 3;
+    // the rows of the partial sums of dB and dC: packed rows, or sequence by sequence
+    const int64_t bc_row = (a.q.starts ? 0 : ck.s * a.q.rows) + ck.span.first + ck.row;
+    const int64_t bc_rows = a.q.starts ? a.q.rows : a.q.seqs * a.q.rows;
+
+    int sub = (ck.len - 1) / kSub;
+    GradTile<T, KS, true> tile;
+    tile.load(a, l, ck.s, ck.span, ck.row + sub * kSub, ck.len - sub * kSub, gate);
+    for (; sub >= 0; --sub) {
+        const int32_t row = ck.row + sub * kSub, len = ck.len - sub * kSub;
+        float u[4], dl[4], slope[4], dy[4], go[4], z[4];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            const bool valid = l.active && 4 * r + l.q < len;
+            u[r] = T::load(tile.u[r]);
+            const float raw = T::load(tile.dl[r]) + bias;
+            slope[r] = 1.f;
+            dl[r] = a.softplus ? softplus_f(raw, &slope[r]) : raw;
+            go[r] = T::load(tile.go[r]);
+            dy[r] = go[r];
+            if (gate) {
+                z[r] = T::load(tile.z[r]);
+                dy[r] *= silu_f(z[r], sigmoid_f(z[r]));
+            }
+            // rows past the end and channels past the last: nothing is added
+            if (!valid) dl[r] = u[r] = dy[r] = 0.f;
+            ex[4 * r + l.q][l.c] = make_float4(dl[r], dl[r] * u[r], dy[r], 0.f);
+        }
+#pragma unroll
+        for (int i = 0; i < KS; ++i) {
+            g.B[i] = tile.B[i];
+            g.C[i] = tile.C[i];
+            g.h[0][i] = 0.f;
+        }
+        if (l.active)
+            ld_states<KS>(a.cs + ((slot * kSubs + sub) * a.channels + l.ch) * NP + l.q * KS, g.h[0]);
+        wave_lds_fence();
+        if (sub > 0) tile.load(a, l, ck.s, ck.span, row - kSub, kSub, gate);
+
+        float t0[4], t1[4];
+        grad_forward<KS, 0>(ex, l.c, gate, g, t0);
+        grad_backward<KS, kSub - 1>(ex, l.c, g, t0, t1);
+        wave_lds_fence();
+
+        float(*mine)[2 * NP] = bc[sub & 1][w];
+        st_states<KS>(&mine[brev][l.q * KS], g.dBt);
+        st_states<KS>(&mine[brev][NP + l.q * KS], g.dCt);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            const int t = 4 * r + l.q;
+            const float ddl = fma32(g.th[r], u[r], g.dc[r] * kLn2);
+            const float dd = ddl * slope[r];
+            if (l.active && t < len) {
+                const int64_t first = ck.span.first + row + t;
+                st<T>(rows_ptr<T>(a.du, ck.s, a.q, first) + l.ch,
+                      fma32(g.th[r], dl[r], Dc * dy[r]));
+                st<T>(rows_ptr<T>(a.ddelta, ck.s, a.q, first) + l.ch, dd);
+                if (gate) {
+                    const float y = fma32(Dc, u[r], g.y[r]);
+                    st<T>(rows_ptr<T>(a.dz, ck.s, a.q, first) + l.ch,
+                          go[r] * y * silu_slope(z[r], sigmoid_f(z[r])));
+                }
+                dD = fma32(dy[r], u[r], dD);
+                dbias += dd;
+            }
+        }
+        __syncthreads();
+        for (int i = threadIdx.x; i < kSub * 2 * NP; i += 256) {
+            const int t = i / (2 * NP), n = i - t * 2 * NP;
+            const float v = (bc[sub & 1][0][t][n] + bc[sub & 1][1][t][n]) +
+                            (bc[sub & 1][2][t][n] + bc[sub & 1][3][t][n]);
+            if (t < len)
+                a.ws_bc[((int64_t)slab * bc_rows + bc_row + sub * kSub + t) * (2 * NP) + n] = v;
+        }
+    }
+    dD = fold_quad(dD, dD, dD, dD);
+    dbias = fold_quad(dbias, dbias, dbias, dbias);
+    if (!l.active) return;
+    st_states<KS>(a.ws_state + at, g.dA);
+    if (l.q == 0) {
+        a.ws_dD[slot * a.channels + l.ch] = dD;
+        a.ws_dbias[slot * a.channels + l.ch] = dbias;
+    }
+}
+
+// dB and dC of each row: the slabs' sums in order, rounded once.
+template <typename T, int NP>
+__global__ __launch_bounds__(256) void k_scan_sum_bc(ScanArgs a, int groups)
+{
+    const int64_t bc_rows = a.q.starts ? a.q.rows : a.q.seqs * a.q.rows;
+    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    const int64_t rg = i / (2 * NP);
+    const int n = (int)(i - rg * (2 * NP));
+    const int64_t r = rg / groups;
+    const int g = (int)(rg - r * groups);
+    const int st_n = n < NP ? n : n - NP;
+    if (r >= bc_rows || st_n >= a.states) return;
+    int64_t s = 0, row = r;
+    if (a.q.starts) {
+        if (r < clamp_start(a.q, 0) || r >= clamp_start(a.q, a.q.seqs)) return;
+    } else {
+        s = r / a.q.rows;
+        row = r - s * a.q.rows;
+    }
+    const float* p = a.ws_bc + ((int64_t)g * a.slabs * bc_rows + r) * (2 * NP) + n;
+    const int64_t step = bc_rows * (2 * NP);
+    float v = 0.f;
+    int k = 0;
+    for (; k + 8 <= a.slabs; k += 8) {
+        float x[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) x[j] = p[(k + j) * step];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v += x[j];
+    }
+    for (; k < a.slabs; ++k) v += p[k * step];
+    const canon_rows_t& o = n < NP ? a.dB : a.dC;
+    st<T>(rows_ptr<T>(o, s, a.q, row) + (int64_t)g * a.states + st_n, v);
+}
+
+template <typename T, int KS>
+hipError_t launch_scan_grad_ks(const ScanArgs& a, int64_t groups, hipStream_t st)
+{
+    constexpr int NP = 4 * KS;
+    const int64_t slots = slot_count<kCh>(a.q.seqs, a.q.rows, a.q.starts != nullptr);
+    const unsigned grid = (unsigned)(slots * groups * a.slabs);
+    if (grid) k_scan_back_sum<T, KS><<<dim3(grid), dim3(256), 0, st>>>(a);
+    if (hipError_t e = hipGetLastError()) return e;
+    if (hipError_t e = launch_scan_carry<NP, true>(a, a.dfinal, a.dinit, st)) return e;
+    if (grid) k_selective_scan_grad<T, KS><<<dim3(grid), dim3(256), 0, st>>>(a);
+    if (hipError_t e = hipGetLastError()) return e;
+    const int64_t d = a.channels;
+    if (hipError_t e = launch_column_sum(a.ws_state, slots, d * NP, NP, a.states, a.dA, st))
+        return e;
+    if (a.dD)
+        if (hipError_t e = launch_column_sum(a.ws_dD, slots, d, 1, 1, a.dD, st)) return e;
+    if (a.dbias)
+        if (hipError_t e = launch_column_sum(a.ws_dbias, slots, d, 1, 1, a.dbias, st)) return e;
+    const int64_t bc = (a.q.starts ? a.q.rows : a.q.seqs * a.q.rows) * groups * 2 * NP;
+    if (bc == 0) return hipSuccess;
+    k_scan_sum_bc<T, NP><<<dim3((unsigned)((bc + 255) / 256)), dim3(256), 0, st>>>(a, (int)groups);
+    return hipGetLastError();
+}
+
+template <typename T>
+hipError_t launch_selective_scan_grad(const ScanArgs& a, int64_t groups, hipStream_t st)
+{
+    switch (scan_ks(a.states)) {
+        case 1: return launch_scan_grad_ks<T, 1>(a, groups, st);
+        case 2: return launch_scan_grad_ks<T, 2>(a, groups, st);
+        default: return launch_scan_grad_ks<T, 4>(a, groups, st);
+    }
+}
+
+}  // namespace seq
+}  // namespace canon

@@ -1,0 +1,298 @@
+// Device helpers of the sequence operators (canon_seq.h): element types,
+// scalar functions, lane moves and the walk over sequences.
+#pragma once
+
+#include <hip/hip_bf16.h>
+#include <hip/hip_fp16.h>
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "../../include/canon_seq.h"
+
+namespace canon {
+namespace seq {
+
+// ---------------------------------------------------------------- element types
+struct F32 {
+    using store_t = float;
+    static __device__ __forceinline__ float load(float v) { return v; }
+    static __device__ __forceinline__ float round(float v) { return v; }
+};
+struct BF16 {
+    using store_t = uint16_t;
+    static __device__ __forceinline__ float load(uint16_t v)
+    {
+        return __uint_as_float((uint32_t)v << 16);
+    }
+    // to nearest even; a NaN keeps its upper bits and stays a NaN
+    static __device__ __forceinline__ uint16_t round(float v)
+    {
+        return __builtin_bit_cast(uint16_t, (__bf16)v);
+    }
+};
+struct F16 {
+    using store_t = uint16_t;
+    static __device__ __forceinline__ float load(uint16_t v)
+    {
+        return (float)__builtin_bit_cast(_Float16, v);
+    }
+    // The empty asm keeps the 32-bit value a value: without it a product before
+    // the conversion becomes one mixed-precision FMA, which rounds the exact
+    // product to 16 bits, and the stored bits would depend on the code around.
+    static __device__ __forceinline__ uint16_t round(float v)
+    {
+        asm("" : "+v"(v));
+        return __builtin_bit_cast(uint16_t, (_Float16)v);
+    }
+};
+
+template <typename T>
+__device__ __forceinline__ float ld(const typename T::store_t* p)
+{
+    return T::load(*p);
+}
+
+template <typename T>
+__device__ __forceinline__ void st(typename T::store_t* p, float v)
+{
+    *p = T::round(v);
+}
+
+// V consecutive elements as one (or, for 32-bit elements beyond 16 bytes,
+// several) vector accesses; p aligned to min(16, V * sizeof) bytes.
+template <typename T, int V>
+struct alignas((V * sizeof(typename T::store_t) < 16) ? V * sizeof(typename T::store_t) : 16) Vec {
+    typename T::store_t e[V];
+};
+
+template <typename T, int V>
+__device__ __forceinline__ Vec<T, V> ld_vec(const typename T::store_t* p)
+{
+    return *reinterpret_cast<const Vec<T, V>*>(p);
+}
+
+template <typename T, int V>
+__device__ __forceinline__ void st_vec(typename T::store_t* p, const float (&v)[V])
+{
+    Vec<T, V> o;
+#pragma unroll
+    for (int i = 0; i < V; ++i) o.e[i] = T::round(v[i]);
+    *reinterpret_cast<Vec<T, V>*>(p) = o;
+}
+
+// --------------------------------------------------------------- scalar functions
+constexpr float kLog2e = 0x1.715476p+0f;     // log2(e) to 24 bits
+constexpr float kLog2eLo = 0x1.4ae0bep-26f;  // and the rest
+constexpr float kLn2 = 0x1.62e43p-1f;
+
+__device__ __forceinline__ float fma32(float a, float b, float c) { return __builtin_fmaf(a, b, c); }
+__device__ __forceinline__ float exp2_hw(float x) { return __builtin_amdgcn_exp2f(x); }
+
+// exp(x) to about 1.5 ulp: the product x log2(e) in two parts, the lower one
+// through exp2(r) = 1 + r ln 2.  (Beyond 128 the high part alone decides: the
+// remainder of an infinite product would be a NaN.)
+__device__ __forceinline__ float exp_f(float x)
+{
+    const float t = x * kLog2e;
+    const float r = fma32(x, kLog2eLo, fma32(x, kLog2e, -t));
+    const float e = exp2_hw(t);
+    return __builtin_fabsf(t) < 128.f ? fma32(e, r * kLn2, e) : e;
+}
+
+// 1 / x to about 1 ulp, x normal: the hardware reciprocal and one Newton step.
+__device__ __forceinline__ float rcp_f(float x)
+{
+    const float r = __builtin_amdgcn_rcpf(x);
+    const float n = fma32(fma32(-x, r, 1.f), r, r);
+    return __builtin_fabsf(x) < 0x1p126f ? n : r;  // an infinite x has 0, not a NaN
+}
+
+__device__ __forceinline__ float sigmoid_f(float x)
+{
+    const float e = exp_f(-__builtin_fabsf(x));  // in (0, 1]: no overflow
+    const float r = rcp_f(1.f + e);
+    return x >= 0.f ? r : e * r;  // NaN: e is NaN
+}
+
+// softplus(x) = max(x, 0) + log(1 + e), e = exp(-|x|) <= 1, with the logarithm
+// as 2 artanh(s), s = e / (2 + e) <= 1/3: 2 (s + s^3/3 + s^5/5 + ...); the
+// first term left out, s^17/17, is below 2^-30 of s.  No cancellation at any
+// x, so small step sizes keep their relative precision.  *slope = sigmoid(x),
+// the derivative.
+__device__ __forceinline__ float softplus_f(float x, float* slope)
+{
+    const float e = exp_f(-__builtin_fabsf(x));
+    const float s = e * rcp_f(2.f + e);
+    const float s2 = s * s;
+    float p = fma32(s2, 1.f / 15.f, 1.f / 13.f);
+    p = fma32(p, s2, 1.f / 11.f);
+    p = fma32(p, s2, 1.f / 9.f);
+    p = fma32(p, s2, 1.f / 7.f);
+    p = fma32(p, s2, 1.f / 5.f);
+    p = fma32(p, s2, 1.f / 3.f);
+    const float l = 2.f * fma32(s * s2, p, s);
+    if (slope) {
+        const float r = rcp_f(1.f + e);
+        *slope = x >= 0.f ? r : e * r;
+    }
+    return (x > 0.f ? x : 0.f) + l;
+}
+
+// d/dx of x sigmoid(x), given q = sigmoid(x): q (1 + x (1 - q)), with its
+// limits 0 and 1 where x is infinite
+__device__ __forceinline__ float silu_slope(float x, float q)
+{
+    const float r = 1.f - q;
+    return fma32(q, q == 0.f || r == 0.f ? 0.f : x * r, q);
+}
+
+// x sigmoid(x): 0, not a NaN, at minus infinity
+__device__ __forceinline__ float silu_f(float x, float q) { return q == 0.f ? 0.f * q : x * q; }
+
+// ------------------------------------------------------------------- lane moves
+template <int CTRL>
+__device__ __forceinline__ float dpp(float v)
+{
+    return __uint_as_float((uint32_t)__builtin_amdgcn_update_dpp(
+        0, (int)__float_as_uint(v), CTRL, 0xf, 0xf, true));
+}
+
+// lane T of each row of 16 lanes, to the whole row
+template <int T>
+__device__ __forceinline__ float row_bcast(float v)
+{
+    return dpp<0x150 + T>(v);
+}
+
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+
+// lower half wave: x summed over lane and lane + 32; upper half: y likewise
+__device__ __forceinline__ float fold_halves(float x, float y)
+{
+    const u32x2 r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(y), false,
+                                                     false);
+    return __uint_as_float(r.x) + __uint_as_float(r.y);
+}
+
+// even rows of 16 lanes: x summed over the row and the next; odd rows: y
+// likewise over the row and the one before
+__device__ __forceinline__ float fold_rows(float x, float y)
+{
+    const u32x2 r = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(y), false,
+                                                     false);
+    return __uint_as_float(r.x) + __uint_as_float(r.y);
+}
+
+// Rows of a wave's lanes hold partial sums of four values; row q gets the
+// total of value q.
+__device__ __forceinline__ float fold_quad(float v0, float v1, float v2, float v3)
+{
+    return fold_rows(fold_halves(v0, v2), fold_halves(v1, v3));
+}
+
+// Orders a wave's shared-memory writes before its later reads of them by
+// other lanes (the hardware keeps a wave's LDS accesses in order; this keeps
+// the compiler from moving them).
+__device__ __forceinline__ void wave_lds_fence()
+{
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+}
+
+// ------------------------------------------------------------------- sequences
+struct Seqs {
+    int64_t seqs, rows;
+    const int32_t* starts;
+};
+
+// Rows [first, first + len) of a sequence (first: 0 unless packed).
+struct Span {
+    int64_t first;
+    int32_t len;
+};
+
+__device__ __forceinline__ int32_t clamp_start(const Seqs& q, int64_t s)
+{
+    const int32_t v = q.starts[s];
+    return v < 0 ? 0 : (v > (int32_t)q.rows ? (int32_t)q.rows : v);
+}
+
+__device__ __forceinline__ Span seq_span(const Seqs& q, int64_t s)
+{
+    if (q.starts == nullptr) return Span{0, (int32_t)q.rows};
+    const int32_t a = clamp_start(q, s), b = clamp_start(q, s + 1);
+    return Span{a, b > a ? b - a : 0};
+}
+
+// Chunks of CH rows from each sequence's start have slots of their own,
+// numbered without a prefix sum: chunk c of sequence s has slot base(s) + c,
+// with base(s) = s max(1, ceil(rows / CH)), or, packed, s + floor(starts[s] /
+// CH) (a sequence of n rows from row a takes ceil(n / CH) <= floor((a + n) /
+// CH) - floor(a / CH) + 1 slots).  Every sequence has a slot; some slots stay
+// empty.
+template <int CH>
+__host__ __device__ __forceinline__ int64_t chunks_per_seq(int64_t rows)
+{
+    return rows > CH ? (rows + CH - 1) / CH : 1;
+}
+
+template <int CH>
+__host__ __device__ __forceinline__ int64_t slot_count(int64_t seqs, int64_t rows, bool packed)
+{
+    return packed ? seqs + rows / CH : seqs * chunks_per_seq<CH>(rows);
+}
+
+template <int CH>
+__device__ __forceinline__ int64_t slot_base(const Seqs& q, int64_t s)
+{
+    if (q.starts == nullptr) return s * chunks_per_seq<CH>(q.rows);
+    return s + clamp_start(q, s) / CH;
+}
+
+// The chunk of a slot: its sequence, rows [row, row + len) of it (row counted
+// from the sequence's start) and the sequence's span; len <= 0 for an empty
+// slot.
+struct Chunk {
+    int64_t s;
+    Span span;
+    int32_t row;
+    int32_t len;
+};
+
+template <int CH>
+__device__ __forceinline__ Chunk slot_chunk(const Seqs& q, int64_t slot)
+{
+    Chunk c;
+    if (q.starts == nullptr) {
+        const int64_t per = chunks_per_seq<CH>(q.rows);
+        c.s = slot / per;
+        c.span = Span{0, (int32_t)q.rows};
+        c.row = (int32_t)((slot - c.s * per) * CH);
+    } else {
+        int64_t lo = 0, hi = q.seqs - 1;  // the last sequence with base <= slot
+        while (lo < hi) {
+            const int64_t mid = (lo + hi + 1) >> 1;
+            if (slot_base<CH>(q, mid) <= slot)
+                lo = mid;
+            else
+                hi = mid - 1;
+        }
+        c.s = lo;
+        c.span = seq_span(q, lo);
+        const int64_t k = slot - slot_base<CH>(q, lo);
+        c.row = k < 0 || k > (int64_t)(0x7fffffff / CH) ? 0x7fffffff / CH * CH : (int32_t)k * CH;
+    }
+    const int32_t left = c.span.len - c.row;
+    c.len = left < CH ? left : CH;
+    return c;
+}
+
+template <typename T>
+__device__ __forceinline__ typename T::store_t* rows_ptr(const canon_rows_t& r, int64_t s,
+                                                         const Seqs& q, int64_t first)
+{
+    return static_cast<typename T::store_t*>(r.p) + (q.starts ? 0 : s * r.seq) + first * r.row;
+}
+
+}  // namespace seq
+}  // namespace canon

@@ -1,0 +1,258 @@
+"""Causal convolution against its float64 form: forward, backward, single rows."""
+import pytest
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+
+import seq_ref  # noqa: E402
+
+F32, BF16, F16 = torch.float32, torch.bfloat16, torch.float16
+
+
+@pytest.fixture(scope="module")
+def canon():
+    import scan_canonical_reduce_amd as c
+    return c
+
+
+def inputs(dtype, lens, channels, taps, packed, seed=0, param=F32):
+    g = torch.Generator().manual_seed(seed)
+
+    def normal(*shape):
+        return torch.randn(*shape, generator=g)
+
+    lead = (sum(lens),) if packed else (len(lens), lens[0])
+    starts = torch.tensor([0] + lens).cumsum(0).int() if packed else None
+    return dict(x=normal(*lead, channels).to(dtype), w=normal(channels, taps).to(param),
+                b=normal(channels).to(param), init=normal(len(lens), taps - 1, channels).to(dtype),
+                dout=normal(*lead, channels).to(dtype),
+                dfinal=normal(len(lens), taps - 1, channels).to(dtype), starts=starts)
+
+
+def cuda(d):
+    return {k: v.cuda() if torch.is_tensor(v) else v for k, v in d.items()}
+
+
+def reference(d, act, bias=True, init=True, grad=False):
+    """float64 values, and the sums of absolute terms behind them."""
+    x, w = d["x"].double(), d["w"].double()
+    b = d["b"].double() if bias else None
+    st = d["init"].double() if init else torch.zeros_like(d["init"]).double()
+    leaves = [t.requires_grad_() for t in (x, w, st)] + ([b.requires_grad_()] if bias else [])
+    outs, sizes, finals = [], [], []
+    for i, at in enumerate(seq_ref.spans(d["x"], d["starts"])):
+        y, f = seq_ref.conv_one(x[at], w, b, act, st[i])
+        s, _ = seq_ref.conv_one(x[at].abs(), w.abs(), None if b is None else b.abs(), False,
+                                st[i].abs())
+        outs.append(y), sizes.append(s), finals.append(f)
+    join = torch.stack if d["starts"] is None else torch.cat
+    out, size, final = join(outs), join(sizes), torch.stack(finals)
+    if not grad:
+        return out, size, final
+    loss = (out * d["dout"].double()).sum() + (final * d["dfinal"].double()).sum()
+    return out, torch.autograd.grad(loss, leaves)
+
+
+# p adds taps + 1 terms in FMAs (one rounding each); silu multiplies by a
+# sigmoid with a relative error below 8 roundings, whose argument's error is
+# at most the error of p (slope of p sigmoid(p) below 1.1): 2 (taps + 2) + 12
+# roundings of the absolute sum cover both.
+def terms(taps):
+    return 2 * (taps + 2) + 12
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16, F16])
+@pytest.mark.parametrize("taps", [1, 2, 3, 4, 8])
+@pytest.mark.parametrize("channels", [1, 24, 37, 264])
+@pytest.mark.parametrize("act", [None, "silu"])
+def test_forward(canon, dtype, taps, channels, act):
+    for packed, lens in ((False, [1, 1]), (False, [33, 33, 33]),
+                         (True, [5, 0, 64, 1, 31, 0, 2, 100])):
+        d = inputs(dtype, lens, channels, taps, packed, taps + channels)
+        g = cuda(d)
+        final = torch.empty_like(g["init"])
+        got = canon.causal_conv(g["x"], g["w"], g["b"], act, g["starts"], g["init"], final)
+        out, size, last = reference(d, act)
+        seq_ref.close(got, out, size, terms(taps), (lens, packed))
+        assert torch.equal(final.cpu().double(), last)
+        got = canon.causal_conv(g["x"], g["w"], None, act, g["starts"])
+        out, size, _ = reference(d, act, bias=False, init=False)
+        seq_ref.close(got, out, size, terms(taps), (lens, packed, "plain"))
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16, F16])
+def test_long_runs(canon, dtype):
+    """Enough rows for the long-run variant, which must give the same bits as
+    the short one on each sequence alone."""
+    d = cuda(inputs(dtype, [1040] * 8, 4096, 4, False))
+    got = canon.causal_conv(d["x"], d["w"], d["b"], "silu", None, d["init"])
+    one = canon.causal_conv(d["x"][2:3, :100], d["w"], d["b"], "silu", None,
+                            d["init"][2:3].contiguous())
+    assert torch.equal(got[2:3, :100], one)
+    tail = canon.causal_conv(d["x"][5:6, 900:], d["w"], d["b"], "silu", None,
+                             d["x"][5:6, 897:900].contiguous())
+    assert torch.equal(got[5:6, 900:], tail)
+
+
+def test_parameters_of_the_activation_type(canon):
+    d = inputs(BF16, [50], 48, 4, False, param=BF16)
+    g = cuda(d)
+    got = canon.causal_conv(g["x"], g["w"], g["b"], "silu", None, g["init"])
+    out, size, _ = reference(d, "silu")
+    seq_ref.close(got, out, size, terms(4))
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16, F16])
+@pytest.mark.parametrize("taps", [1, 2, 4, 7])
+@pytest.mark.parametrize("channels", [24, 37])
+@pytest.mark.parametrize("act", [None, "silu"])
+def test_backward(canon, dtype, taps, channels, act):
+    for packed, lens in ((False, [1]), (False, [70, 70]), (True, [3, 0, 65, 1, 32, 2, 0])):
+        d = inputs(dtype, lens, channels, taps, packed, 7 * taps + channels)
+        g = cuda(d)
+        got = canon.causal_conv_grad(g["dout"], g["x"], g["w"], g["b"], act, g["starts"],
+                                     g["init"], g["dfinal"])
+        _, (dx, dw, dst, db) = reference(d, act, grad=True)
+        # Sums of absolute terms: |silu'| <= 1.1, and p's relative error enters
+        # through silu'' <= 0.5 times the absolute sum of p (at most ~ 6 taps
+        # here): the bounds below use 1.1 + that.
+        w = d["w"].double().abs()
+        _, psize, _ = reference(d, None)
+        psize = float(psize.detach().max()) if psize.numel() else 0.0
+        gmax = 1.1 + psize
+        gout = d["dout"].double().abs().max() if d["dout"].numel() else 0.0
+        big = float(gout) * gmax
+        size = (w.sum(1) * big + float(d["dfinal"].abs().max() if taps > 1 else 0)).expand_as(dx)
+        n = 2 * terms(taps)
+        seq_ref.close(got.dx, dx, size, n, (lens, "dx"))
+        rows = sum(lens)
+        seq_ref.close(got.dweight, dw, torch.full_like(dw, rows * big * 5), n + 64, (lens, "dw"))
+        seq_ref.close(got.dbias, db, torch.full_like(db, rows * big), n + 64, (lens, "db"))
+        seq_ref.close(got.dinit_state, dst, size.max().expand_as(dst) if dst.numel() else dst, n,
+                      (lens, "dinit"))
+
+
+def test_backward_against_differences(canon):
+    """<gradient, v> against a central difference of the float64 form along v:
+    with step 1e-5 its error is about 1e-10 |f'''| + 1e-11 |f|."""
+    d = inputs(F32, [40, 0, 7], 24, 4, True)
+    g = cuda(d)
+    got = canon.causal_conv_grad(g["dout"], g["x"], g["w"], g["b"], "silu", g["starts"],
+                                 g["init"], g["dfinal"])
+    for key, grad in (("x", got.dx), ("w", got.dweight), ("b", got.dbias),
+                      ("init", got.dinit_state)):
+        v = torch.randn(d[key].shape, generator=torch.Generator().manual_seed(1)).double()
+
+        def f(step):
+            e = {k: t.double() if torch.is_tensor(t) and t.is_floating_point() else t
+                 for k, t in d.items()}
+            e[key] = e[key] + step * v
+            out, _, final = reference(e, "silu")
+            return float(((out * e["dout"]).sum() + (final * e["dfinal"]).sum()).detach())
+
+        want = (f(1e-5) - f(-1e-5)) / 2e-5
+        assert float((grad.double().cpu() * v).sum()) == pytest.approx(want, rel=1e-5, abs=1e-4)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16, F16])
+@pytest.mark.parametrize("taps", [1, 3, 4])
+@pytest.mark.parametrize("channels", [37, 48])
+def test_step_equals_the_sequence(canon, dtype, taps, channels):
+    """Row after row, the step gives the sequence's bits, in place or not."""
+    d = cuda(inputs(dtype, [9] * 5, channels, taps, False))
+    final = torch.empty_like(d["init"])
+    want = canon.causal_conv(d["x"], d["w"], d["b"], "silu", None, d["init"], final)
+    state, other = d["init"].clone(), d["init"].clone()
+    for t in range(9):
+        nxt = torch.empty_like(other)
+        a = canon.causal_conv_step(d["x"][:, t], state, d["w"], d["b"], "silu")
+        b = canon.causal_conv_step(d["x"][:, t], other, d["w"], d["b"], "silu", out_state=nxt)
+        other = nxt
+        assert torch.equal(a, want[:, t]) and torch.equal(b, want[:, t])
+        assert torch.equal(state, other)
+    assert torch.equal(state, final)
+
+
+def test_state_in_place_and_pieces(canon):
+    """A sequence in pieces, the state handed on in one buffer: the same bits."""
+    d = cuda(inputs(BF16, [77] * 3, 64, 4, False))
+    want = canon.causal_conv(d["x"], d["w"], d["b"], "silu", None, d["init"])
+    state = d["init"].clone()
+    at = 0
+    for n in (1, 2, 40, 0, 34):
+        got = canon.causal_conv(d["x"][:, at:at + n], d["w"], d["b"], "silu", None, state, state)
+        assert torch.equal(got, want[:, at:at + n])
+        at += n
+    assert torch.equal(state, d["x"][:, 74:])
+
+
+def test_rows_outside_sequences_and_strides(canon):
+    x = torch.randn(50, 130).to(BF16).cuda()
+    w, b = torch.randn(64, 4).cuda(), torch.randn(64).cuda()
+    starts = torch.tensor([3, 20, 20, 41], dtype=torch.int32).cuda()
+    out = torch.full((50, 70), 7.0, dtype=BF16, device="cuda")
+    canon.causal_conv(x[:, 2:66], w, b, "silu", starts, out=out[:, 4:68])
+    want = canon.causal_conv(x[3:41, 2:66].contiguous(), w, b, "silu",
+                             (starts - 3).int())
+    assert torch.equal(out[3:41, 4:68], want)
+    assert (out[:3] == 7).all() and (out[41:] == 7).all() and (out[:, :4] == 7).all()
+    # NaN behind the sequences and in the next sequence reach nothing
+    y = x.clone()
+    y[41:], y[:3], y[20:41] = float("nan"), float("inf"), float("nan")
+    got = canon.causal_conv(y[:, 2:66], w, b, "silu", starts)
+    assert torch.equal(got[3:20], want[:17])
+    # interleaved sequences: [rows, sequences, channels] transposed
+    z = torch.randn(30, 2, 64).cuda()
+    got = canon.causal_conv(z.transpose(0, 1), w, b)
+    assert torch.equal(got, canon.causal_conv(z.transpose(0, 1).contiguous(), w, b))
+    g1 = canon.causal_conv_grad(x[:, 2:66], x[:, 66:130], w, b, "silu", starts)
+    y = x.clone()
+    y[:3], y[41:] = float("nan"), float("inf")
+    g2 = canon.causal_conv_grad(y[:, 2:66], y[:, 66:130], w, b, "silu", starts)
+    assert torch.equal(g1.dweight, g2.dweight) and torch.equal(g1.dbias, g2.dbias)
+    assert torch.equal(g1.dx[3:41], g2.dx[3:41])
+
+
+def test_broadcast_input_and_empty(canon):
+    w, b = torch.randn(8, 4).cuda(), torch.randn(8).cuda()
+    x = torch.randn(1, 20, 8).cuda()
+    got = canon.causal_conv(x.expand(3, 20, 8), w, b)
+    assert torch.equal(got[2], got[0])
+    assert torch.equal(got[:1], canon.causal_conv(x, w, b))
+    assert canon.causal_conv(x[:, :0], w, b).shape == (1, 0, 8)
+    assert canon.causal_conv(x[:0], w, b).shape == (0, 20, 8)
+    g = canon.causal_conv_grad(x[:, :0], x[:, :0], w, b)
+    assert not g.dweight.any() and not g.dbias.any()
+    g = canon.causal_conv_grad(x[:0], x[:0], w, b)
+    assert not g.dweight.any() and not g.dbias.any()
+
+
+def test_refusals(canon):
+    x, w = torch.randn(2, 9, 8).cuda(), torch.randn(8, 4).cuda()
+    with pytest.raises(TypeError):
+        canon.causal_conv(x.double(), w)
+    with pytest.raises(TypeError):
+        canon.causal_conv(x, w.half())
+    with pytest.raises(ValueError):
+        canon.causal_conv(x, w, activation="relu")
+    with pytest.raises(ValueError):
+        canon.causal_conv(x, torch.randn(8, 9).cuda())  # too many taps
+    with pytest.raises(ValueError):
+        canon.causal_conv(x, w[:7])
+    with pytest.raises(ValueError):
+        canon.causal_conv(x[0], w)
+    with pytest.raises(ValueError):
+        canon.causal_conv(x, w, starts=torch.tensor([0, 9]).int().cuda())
+    with pytest.raises(ValueError):
+        canon.causal_conv(x[0], w, starts=torch.tensor([0, 9]).cuda())  # 64-bit
+    with pytest.raises(ValueError):
+        canon.causal_conv(x.transpose(1, 2), w[:, :4])
+    with pytest.raises(ValueError):
+        canon.causal_conv(x, w, init_state=torch.zeros(2, 4, 8).cuda())
+    with pytest.raises(ValueError):
+        canon.causal_conv(x, w, out=torch.empty(1, 9, 8).cuda().expand(2, 9, 8))
+    with pytest.raises(ValueError):
+        canon.causal_conv(x.cpu(), w)
+    with pytest.raises(ValueError):
+        canon.causal_conv_step(x, torch.zeros(2, 3, 8).cuda(), w)

@@ -1,0 +1,208 @@
+"""Checks of the sequence operators that need no GPU: exports, struct layout,
+workspace sizes, and every refusal (no call here reaches a launch: each fails
+validation, or has nothing to do)."""
+import ctypes
+import os
+import re
+
+import pytest
+
+torch = pytest.importorskip("torch")
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+HEADER = os.path.join(ROOT, "include", "canon_seq.h")
+FAKE = 0x10000  # never dereferenced
+
+
+@pytest.fixture(scope="module")
+def seq():
+    import scan_canonical_reduce_amd as c
+    if not os.path.exists(c.LIB_PATH):
+        from scan_canonical_reduce_amd import build
+        build.build()
+    from scan_canonical_reduce_amd import seq as s
+    s._lib()
+    return s
+
+
+def header():
+    return re.sub(r"/\*.*?\*/", "", open(HEADER).read(), flags=re.S)
+
+
+def test_header_exports(seq):
+    names = sorted(set(re.findall(r"\b(canon_[a-z0-9_]+)\s*\(", header())))
+    assert names == sorted(seq.SEQ_EXPORTS)
+    out = os.popen(f"nm -D --defined-only {seq._lib()._name}").read()
+    for name in names:
+        assert re.search(rf"\bT {name}\b", out), name
+
+
+@pytest.mark.parametrize("cls,struct", [("Conv", "canon_conv_t"),
+                                        ("Scan", "canon_selective_scan_t"),
+                                        ("Rows", "canon_rows_t")])
+def test_struct_fields(seq, cls, struct):
+    """The binding's structs list the header's fields in the header's order."""
+    body = re.search(r"typedef struct \{([^}]*)\} " + struct + ";", header()).group(1)
+    names = []
+    for decl in body.split(";"):
+        decl = decl.strip()
+        if decl:
+            decl = re.sub(r"^(const )?\w+", "", decl)
+            names += [n.strip(" *\n") for n in decl.split(",")]
+    assert names == [f[0] for f in getattr(seq, cls)._fields_]
+
+
+def test_limits_match_the_header(seq):
+    text = header()
+    for name, value in (("CANON_CONV_CHUNK", seq.CONV_CHUNK), ("CANON_SCAN_CHUNK", seq.SCAN_CHUNK),
+                        ("CANON_MAX_STATES", seq.MAX_STATES), ("CANON_MAX_TAPS", seq.MAX_TAPS),
+                        ("CANON_SEQ_VERSION", seq.SEQ_VERSION)):
+        assert int(re.search(rf"#define {name} (\d+)", text).group(1)) == value
+    assert seq._lib().canon_seq_version() == seq.SEQ_VERSION
+
+
+def test_workspace_sizes(seq):
+    w = seq.embedding_grad_workspace_bytes
+    assert w(100, 0, 8) == 0 and w(100, 10, 0) == 0 and w(1 << 30, 10, 8) == 0
+    assert w(100, 10, 8) % 256 == 0 and w(100, 10, 8) > 100 * 4 + 110 * 8
+    assert w(0, 10, 8) > 0
+    c = seq.causal_conv_grad_workspace_bytes
+    assert c(1, 32, False, 64, 4) == (4 + 1) * 64 * 4
+    assert c(1, 33, False, 64, 4) == 2 * (4 + 1) * 64 * 4
+    assert c(3, 64, True, 64, 4) == 5 * (4 + 1) * 64 * 4
+    assert c(1, 32, False, 64, 0) == 0 and c(1, 32, False, 64, 9) == 0
+    s = seq.selective_scan_workspace_bytes
+    assert s(2, 65, False, 64, 16) == 4 * 64 * (16 + 1) * 4
+    assert s(2, 65, False, 64, 17) == 0 and s(2, 65, False, 64, 0) == 0
+    g = seq.selective_scan_grad_workspace_bytes
+    assert g(1, 64, False, 64, 1, 16) > s(1, 64, False, 64, 16)
+    assert g(1, 64, False, 64, 3, 16) == 0 and g(1, 64, False, 64, 0, 16) == 0
+    # large sizes do not wrap
+    assert s(1, (1 << 30) - 1, False, (1 << 24) - 1, 16) > 1 << 50
+
+
+def test_embedding_refusals(seq):
+    L = seq._lib()
+
+    def emb(dtype=1, w=FAKE, ld=8, rows=10, width=8, ids=FAKE, nb=8, tokens=4, out=FAKE, ldo=8):
+        return L.canon_embedding(dtype, w, ld, rows, width, ids, nb, tokens, 1.0, out, ldo, None)
+
+    for bad in (dict(dtype=3), dict(dtype=-1), dict(nb=2), dict(ld=7), dict(ldo=7),
+                dict(w=None), dict(ids=None), dict(out=None)):
+        assert emb(**bad) == 1, bad
+    assert emb(tokens=0, ids=None, out=None) == 0
+    assert emb(tokens=1 << 30) == 2 and emb(rows=1 << 31) == 2
+
+    n = seq.embedding_grad_workspace_bytes(100, 10, 8)
+
+    def grad(dtype=1, d=FAKE, ld=8, ids=FAKE, nb=8, tokens=100, rows=10, width=8, pad=-1, acc=0,
+             gd=0, dw=FAKE, lw=8, ws=FAKE, wb=n):
+        return L.canon_embedding_grad(dtype, d, ld, ids, nb, tokens, rows, width, 1.0, pad, acc,
+                                      gd, dw, lw, ws, wb, None)
+
+    for bad in (dict(dtype=3), dict(gd=2), dict(nb=1), dict(acc=2), dict(ld=7), dict(lw=7),
+                dict(pad=-2), dict(dw=None), dict(ids=None), dict(d=None)):
+        assert grad(**bad) == 1, bad
+    for bad in (dict(ws=None), dict(wb=n - 1), dict(ws=FAKE + 8)):
+        assert grad(**bad) == 3, bad
+    assert grad(rows=0) == 0 and grad(width=0) == 0
+    assert grad(tokens=1 << 30) == 2
+
+
+def conv(seq, **kw):
+    c = seq.Conv()
+    c.dtype, c.taps, c.silu, c.param_dtype = 1, 4, 1, 0
+    c.seqs, c.rows, c.channels = 2, 9, 8
+    r = seq.Rows(FAKE, 72, 8)
+    c.x = c.out = c.dout = c.dx = r
+    c.weight = c.bias = c.dweight = c.dbias = FAKE
+    for k, v in kw.items():
+        setattr(c, k, v)
+    return ctypes.byref(c)
+
+
+def test_conv_refusals(seq):
+    L = seq._lib()
+    n = seq.causal_conv_grad_workspace_bytes(2, 9, False, 8, 4)
+    R = seq.Rows
+    for bad in (dict(dtype=7), dict(taps=0), dict(silu=2), dict(param_dtype=2), dict(seqs=-1),
+                dict(rows=-1), dict(channels=-1), dict(weight=None), dict(x=R(None, 0, 0)),
+                dict(x=R(FAKE, 72, -8))):
+        assert L.canon_causal_conv(conv(seq, **bad), None) == 1, bad
+        assert L.canon_causal_conv_grad(conv(seq, **bad), FAKE, n, None) == 1, bad
+    for bad in (R(None, 0, 0), R(FAKE, 0, 8), R(FAKE, 72, 7), R(FAKE, 71, 8), R(FAKE, 8, 15)):
+        assert L.canon_causal_conv(conv(seq, out=bad), None) == 1, (bad.seq, bad.row)
+        assert L.canon_causal_conv_grad(conv(seq, dx=bad), FAKE, n, None) == 1
+    assert L.canon_causal_conv(None, None) == 1
+    for bad in (dict(taps=9), dict(rows=1 << 30), dict(channels=1 << 24)):
+        assert L.canon_causal_conv(conv(seq, **bad), None) == 2, bad
+    assert L.canon_causal_conv(conv(seq, rows=(1 << 30) - 1, seqs=1, channels=(1 << 24) - 1),
+                               None) == 2
+    assert L.canon_causal_conv_grad(conv(seq), FAKE, n - 1, None) == 3
+    assert L.canon_causal_conv_grad(conv(seq), FAKE + 4, n, None) == 3
+    assert L.canon_causal_conv_grad(conv(seq, dweight=None), FAKE, n, None) == 1
+    assert L.canon_causal_conv_grad(conv(seq, bias=None), FAKE, n, None) == 1  # dbias, no bias
+    assert L.canon_causal_conv_step(conv(seq, starts=FAKE), None) == 1
+    assert L.canon_causal_conv(conv(seq, seqs=0, x=R(None, 0, 0)), None) == 0
+    assert L.canon_causal_conv_step(conv(seq, channels=0), None) == 0
+
+
+def scan(seq, **kw):
+    c = seq.Scan()
+    c.dtype, c.softplus = 1, 1
+    c.seqs, c.rows, c.channels, c.groups, c.states = 2, 9, 8, 2, 16
+    r = seq.Rows(FAKE, 72, 8)
+    b = seq.Rows(FAKE, 9 * 32, 32)
+    c.u = c.delta = c.z = c.out = c.dout = c.du = c.ddelta = c.dz = r
+    c.B = c.C = c.dB = c.dC = b
+    c.A = c.D = c.delta_bias = c.dA = c.dD = c.ddelta_bias = c.chunk_states = FAKE
+    for k, v in kw.items():
+        setattr(c, k, v)
+    return ctypes.byref(c)
+
+
+def test_scan_refusals(seq):
+    L = seq._lib()
+    R = seq.Rows
+    n = seq.selective_scan_grad_workspace_bytes(2, 9, False, 8, 2, 16)
+    common = [dict(dtype=5), dict(softplus=2), dict(seqs=-1), dict(rows=-1), dict(groups=0),
+              dict(groups=3), dict(states=0), dict(A=None), dict(u=R(None, 0, 0)),
+              dict(delta=R(None, 0, 0)), dict(B=R(None, 0, 0)), dict(C=R(FAKE, -1, 1)),
+              dict(z=R(FAKE, 72, -8)), dict(chunk_states=FAKE + 4)]
+    for bad in common:
+        assert L.canon_selective_scan(scan(seq, **bad), FAKE, n, None) == 1, bad
+        assert L.canon_selective_scan_grad(scan(seq, **bad), FAKE, n, None) == 1, bad
+    for bad in (R(None, 0, 0), R(FAKE, 0, 8), R(FAKE, 72, 7)):
+        assert L.canon_selective_scan(scan(seq, out=bad), FAKE, n, None) == 1
+        for name in ("du", "ddelta", "dz"):
+            assert L.canon_selective_scan_grad(scan(seq, **{name: bad}), FAKE, n, None) == 1, name
+    for name in ("dB", "dC"):
+        assert L.canon_selective_scan_grad(scan(seq, **{name: R(FAKE, 9 * 32, 31)}), FAKE, n,
+                                           None) == 1
+    for bad in (dict(dA=None), dict(D=None), dict(delta_bias=None), dict(chunk_states=None),
+                dict(dout=R(None, 0, 0))):
+        assert L.canon_selective_scan_grad(scan(seq, **bad), FAKE, n, None) == 1, bad
+    for bad in (dict(states=17), dict(rows=1 << 30), dict(channels=1 << 24)):
+        assert L.canon_selective_scan(scan(seq, **bad), FAKE, n, None) == 2, bad
+    assert L.canon_selective_scan(scan(seq), FAKE, 255, None) == 3
+    assert L.canon_selective_scan(scan(seq), None, 0, None) == 3
+    assert L.canon_selective_scan_grad(scan(seq), FAKE, n - 1, None) == 3
+    assert L.canon_selective_scan_step(scan(seq, starts=FAKE), None) == 1
+    assert L.canon_selective_scan(None, FAKE, n, None) == 1
+    assert L.canon_selective_scan(scan(seq, seqs=0, u=R(None, 0, 0)), None, 0, None) == 0
+    assert L.canon_selective_scan_step(scan(seq, channels=0, groups=1), None) == 0
+
+
+def test_the_binding_has_no_cpu_path(seq):
+    import scan_canonical_reduce_amd as canon
+    x, w = torch.zeros(1, 3, 8), torch.zeros(8, 4)
+    A, B = torch.zeros(8, 16), torch.zeros(1, 3, 16)
+    ids = torch.zeros(3, dtype=torch.int64)
+    for call in (lambda: canon.embedding(w, ids), lambda: canon.embedding_grad(w[:3], ids, 9),
+                 lambda: canon.causal_conv(x, w), lambda: canon.causal_conv_grad(x, x, w),
+                 lambda: canon.causal_conv_step(x[0], x, w),
+                 lambda: canon.selective_scan(x, x, A, B, B),
+                 lambda: canon.selective_scan_grad(x, x, x, A, B, B, A),
+                 lambda: canon.selective_scan_step(A[None], x[0], x[0], A, B[0], B[0])):
+        with pytest.raises(ValueError, match="GPU"):
+            call()
