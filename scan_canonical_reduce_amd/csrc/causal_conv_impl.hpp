@@ -132,7 +132,7 @@ __global__ __launch_bounds__(256) void k_causal_conv(ConvArgs a)
 #pragma unroll
             for (int j = 0; j < V; ++j) {
                 y[j] = conv_sum<K, V>(win, p.w, p.b[j], j);
-                if (a.silu) y[j] = silu_f(y[j], sigmoid_f(y[j]));
+                if (a.silu) y[j] = silu_f(y[j], sigmoid_f<T>(y[j]));
             }
             st_vec<T, V>(out + (int64_t)(ck.row + t0 + u) * a.out.row, y);
         }
@@ -213,7 +213,7 @@ __global__ __launch_bounds__(256) void k_causal_conv_grad(ConvArgs a)
 #pragma unroll
                         for (int j = 0; j < V; ++j) {
                             const float s = conv_sum<K, V>(win, p.w, p.b[j], j);
-                            dp[K - 1][j] *= silu_slope(s, sigmoid_f(s));
+                            dp[K - 1][j] *= silu_slope(s, sigmoid_f<T>(s));
                         }
                     if (t < end)
 #pragma unroll
@@ -284,7 +284,7 @@ __global__ __launch_bounds__(256) void k_causal_conv_step(ConvArgs a)
 #pragma unroll
     for (int j = 0; j < V; ++j) {
         y[j] = conv_sum<K, V>(win, p.w, p.b[j], j);
-        if (a.silu) y[j] = silu_f(y[j], sigmoid_f(y[j]));
+        if (a.silu) y[j] = silu_f(y[j], sigmoid_f<T>(y[j]));
     }
     if (a.final) {
         typename T::store_t* f =

@@ -30,32 +30,45 @@ namespace seq {
 // Inputs of a 16-row tile of the backward passes, loaded as in Tile.
 template <typename T, int KS, bool MAIN>
 struct GradTile {
+    LaneRows<T> ru, rd, rz, rg;
     typename T::store_t u[4], dl[4], z[4], go[4];
-    float B[KS], C[KS];
+    LaneBC<T, KS> B, C;
 
-    __device__ __forceinline__ void load(const ScanArgs& a, const Lane& l, int64_t s,
-                                         const Span& span, int32_t row, int32_t len, bool gate)
+    __device__ __forceinline__ void init(const ScanArgs& a, const Lane& l)
     {
-        const int64_t first = span.first + row;
-        const typename T::store_t* pu = MAIN ? rows_ptr<T>(a.u, s, a.q, first) + l.ch : nullptr;
-        const typename T::store_t* pd = rows_ptr<T>(a.delta, s, a.q, first) + l.ch;
-        const typename T::store_t* pg = rows_ptr<T>(a.dout, s, a.q, first) + l.ch;
-        const typename T::store_t* pz = gate ? rows_ptr<T>(a.z, s, a.q, first) + l.ch : nullptr;
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-            const int64_t t = 4 * r + l.q < len ? 4 * r + l.q : len - 1;
-            if (MAIN) u[r] = pu[t * a.u.row];
-            dl[r] = pd[t * a.delta.row];
-            go[r] = pg[t * a.dout.row];
-            if (gate) z[r] = pz[t * a.z.row];
-        }
-        const int64_t t = l.c < len ? l.c : len - 1;
-        const int64_t gb = (int64_t)l.g * a.states;
-        load_bc<T, KS>(a, rows_ptr<T>(a.C, s, a.q, first + t) + gb, l.q, l.c < len, C);
-        if (MAIN)
-            load_bc<T, KS>(a, rows_ptr<T>(a.B, s, a.q, first + t) + gb, l.q, l.c < len, B);
+        if (MAIN) ru.init(a.u, l);
+        rd.init(a.delta, l);
+        rz.init(a.z, l);
+        rg.init(a.dout, l);
+    }
+    __device__ __forceinline__ void load(const ScanArgs& a, const Lane& l, int64_t s,
+                                         int64_t first, int32_t len, bool gate)
+    {
+        if (MAIN) ru.load(a.u, rows_ptr<T>(a.u, s, a.q, first), l, len, u);
+        rd.load(a.delta, rows_ptr<T>(a.delta, s, a.q, first), l, len, dl);
+        rg.load(a.dout, rows_ptr<T>(a.dout, s, a.q, first), l, len, go);
+        if (gate) rz.load(a.z, rows_ptr<T>(a.z, s, a.q, first), l, len, z);
+        C.load(a, a.C, rows_ptr<T>(a.C, s, a.q, first), l, len);
+        if (MAIN) B.load(a, a.B, rows_ptr<T>(a.B, s, a.q, first), l, len);
     }
 };
+
+// b[i] of lane T times x, added to y[i]
+template <int T, int KS>
+__device__ __forceinline__ void bcast_fma(const float (&b)[KS], float x, float (&y)[KS])
+{
+    if constexpr (KS == 4)
+        asm("s_nop 1\n\t"
+            "v_fmac_f32_dpp %0, %4, %8 row_newbcast:%9 row_mask:0xf bank_mask:0xf\n\t"
+            "v_fmac_f32_dpp %1, %5, %8 row_newbcast:%9 row_mask:0xf bank_mask:0xf\n\t"
+            "v_fmac_f32_dpp %2, %6, %8 row_newbcast:%9 row_mask:0xf bank_mask:0xf\n\t"
+            "v_fmac_f32_dpp %3, %7, %8 row_newbcast:%9 row_mask:0xf bank_mask:0xf"
+            : "+v"(y[0]), "+v"(y[1]), "+v"(y[2]), "+v"(y[3])
+            : "v"(b[0]), "v"(b[1]), "v"(b[2]), "v"(b[3]), "v"(x), "n"(T));
+    else
+#pragma unroll
+        for (int i = 0; i < KS; ++i) y[i] = fma32(row_bcast<T>(b[i]), x, y[i]);
+}
 
 template <int KS, int T>
 __device__ __forceinline__ void back_row(const float2 (*ex)[16], int c, const float (&A2)[KS],
@@ -63,9 +76,9 @@ __device__ __forceinline__ void back_row(const float2 (*ex)[16], int c, const fl
 {
     const float2 x = ex[T][c];  // dl, dy
     sdl += x.x;
+    bcast_fma<T, KS>(C, x.y, R);
 #pragma unroll
-    for (int i = 0; i < KS; ++i)
-        R[i] = exp2_hw(x.x * A2[i]) * fma32(row_bcast<T>(C[i]), x.y, R[i]);
+    for (int i = 0; i < KS; ++i) R[i] *= exp2_hw(x.x * A2[i]);
 }
 
 template <int KS, int T>
@@ -87,7 +100,7 @@ __global__ __launch_bounds__(256) void k_scan_back_sum(ScanArgs a)
     const Lane l = lane_place(a, (int)(blockIdx.x - slot * slabs));
     if (l.wch >= a.dg) return;
     float2(*ex)[16] = ex_all[threadIdx.x >> 6];
-    const Chunk ck = slot_chunk<kCh>(a.q, slot);
+    const Chunk ck = uniform(slot_chunk<kCh>(a.q, slot));
     if (ck.len <= 0) return;
 
     float A2[KS], R[KS];
@@ -102,27 +115,28 @@ __global__ __launch_bounds__(256) void k_scan_back_sum(ScanArgs a)
     float sdl = 0.f;
     int sub = (ck.len - 1) / kSub;
     GradTile<T, KS, false> tile;
-    tile.load(a, l, ck.s, ck.span, ck.row + sub * kSub, ck.len - sub * kSub, gate);
+    tile.init(a, l);
+    tile.load(a, l, ck.s, ck.span.first + ck.row + sub * kSub, ck.len - sub * kSub, gate);
     for (; sub >= 0; --sub) {
         const int32_t len = ck.len - sub * kSub;
-        float C[KS];
+        float C[KS], dl[4], raw[4], dy[4];
+        tile.C.get(C);
+        step_sizes<T>(a, tile.dl, bias, raw, dl);
 #pragma unroll
-        for (int i = 0; i < KS; ++i) C[i] = tile.C[i];
+        for (int r = 0; r < 4; ++r) dy[r] = T::load(tile.go[r]);
+        if (gate)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const float z = T::load(tile.z[r]);
+                dy[r] *= silu_f(z, sigmoid_f<T>(z));
+            }
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-            const float raw = T::load(tile.dl[r]) + bias;
-            const float d = a.softplus ? softplus_f(raw, nullptr) : raw;
-            float dy = T::load(tile.go[r]);
-            if (gate) {
-                const float z = T::load(tile.z[r]);
-                dy *= silu_f(z, sigmoid_f(z));
-            }
-            ex[4 * r + l.q][l.c] =
-                4 * r + l.q < len ? make_float2(d, dy) : make_float2(0.f, 0.f);
+            const bool valid = 4 * r + l.q < len;
+            ex[4 * r + l.q][l.c] = make_float2(valid ? dl[r] : 0.f, valid ? dy[r] : 0.f);
         }
         wave_lds_fence();
-        if (sub > 0)
-            tile.load(a, l, ck.s, ck.span, ck.row + (sub - 1) * kSub, kSub, gate);
+        if (sub > 0) tile.load(a, l, ck.s, ck.span.first + ck.row + (sub - 1) * kSub, kSub, gate);
         back_rows<KS, kSub - 1>(ex, l.c, A2, C, R, sdl);
         wave_lds_fence();
     }
@@ -176,6 +190,14 @@ struct LaneSum {
     }
 };
 
+// What a lane passes to the other lanes of its channel, per row.
+struct GradRow {
+    float dl, dlu, dy, u;  // u times dl; the gated gradient of y
+};
+struct GradRow2 {
+    float slope, w;  // d dl / d delta; dout silu'(z)
+};
+
 template <int KS>
 struct GradRegs {
     float a[kSub][KS], h[kSub + 1][KS];  // h[t]: before row t
@@ -186,42 +208,41 @@ struct GradRegs {
 };
 
 template <int KS, int T>
-__device__ __forceinline__ void grad_forward(const float4 (*ex)[16], int c, bool gate,
+__device__ __forceinline__ void grad_forward(const GradRow (*ex)[16], int c, bool gate,
                                              GradRegs<KS>& g, float (&y)[4])
 {
-    const float4 x = ex[T][c];  // dl, dl u, dy
-    float acc = 0.f;
+    const float dl = ex[T][c].dl, dlu = ex[T][c].dlu;
+    float hn[KS];
 #pragma unroll
     for (int i = 0; i < KS; ++i) {
-        g.a[T][i] = exp2_hw(x.x * g.A2[i]);
-        g.h[T + 1][i] = fma32(g.a[T][i], g.h[T][i], row_bcast<T>(g.B[i]) * x.y);
-        acc = i == 0 ? row_bcast<T>(g.C[i]) * g.h[T + 1][i]
-                     : fma32(row_bcast<T>(g.C[i]), g.h[T + 1][i], acc);
+        g.a[T][i] = exp2_hw(dl * g.A2[i]);
+        hn[i] = fma32(g.a[T][i], g.h[T][i], row_bcast<T>(g.B[i]) * dlu);
     }
-    y[T & 3] = acc;
-    if constexpr ((T & 3) == 3) {
-        if (gate) g.y[T >> 2] = fold_quad(y[0], y[1], y[2], y[3]);
-    }
+    y[T & 3] = bcast_dot<T, KS>(g.C, hn);
+#pragma unroll
+    for (int i = 0; i < KS; ++i) g.h[T + 1][i] = hn[i];
+    if constexpr ((T & 3) == 3) g.y[T >> 2] = fold_quad(y[0], y[1], y[2], y[3]);
     if constexpr (T + 1 < kSub) grad_forward<KS, T + 1>(ex, c, gate, g, y);
 }
 
-template <int KS, int T>
-__device__ __forceinline__ void grad_backward(const float4 (*ex)[16], int c, GradRegs<KS>& g,
+template <int KS, int T, int STOP>
+__device__ __forceinline__ void grad_backward(const GradRow (*ex)[16], int c, GradRegs<KS>& g,
                                               float (&th)[4], float (&dc)[4])
 {
-    const float4 x = ex[T][c];
-    float b[KS], s[KS], through = 0.f, decay = 0.f;
+    const float dl = ex[T][c].dl, dlu = ex[T][c].dlu, dy = ex[T][c].dy;
+    float b[KS], s[KS], decay = 0.f;
+    bcast_fma<T, KS>(g.C, dy, g.R);  // lam
+    th[T & 3] = bcast_dot<T, KS>(g.B, g.R);
 #pragma unroll
     for (int i = 0; i < KS; ++i) {
-        const float lam = fma32(row_bcast<T>(g.C[i]), x.z, g.R[i]);
-        b[i] = lam * x.y;
-        s[i] = x.z * g.h[T + 1][i];
-        through = i == 0 ? row_bcast<T>(g.B[i]) * lam : fma32(row_bcast<T>(g.B[i]), lam, through);
-        g.R[i] = g.a[T][i] * lam;
+        b[i] = g.R[i] * dlu;
+        s[i] = dy * g.h[T + 1][i];
+        g.R[i] *= g.a[T][i];
         const float d = g.R[i] * g.h[T][i];
-        g.dA[i] = fma32(x.x, d, g.dA[i]);
+        g.dA[i] = fma32(dl, d, g.dA[i]);
         decay = i == 0 ? g.A2[i] * d : fma32(g.A2[i], d, decay);
     }
+    dc[T & 3] = decay;
     g.sb.template add<T>(b, c);
     g.sc.template add<T>(s, c);
     if constexpr (T == 0) {
@@ -231,13 +252,11 @@ __device__ __forceinline__ void grad_backward(const float4 (*ex)[16], int c, Gra
             g.dCt[i] = s[i];
         }
     }
-    th[T & 3] = through;
-    dc[T & 3] = decay;
     if constexpr ((T & 3) == 0) {
         g.th[T >> 2] = fold_quad(th[0], th[1], th[2], th[3]);
         g.dc[T >> 2] = fold_quad(dc[0], dc[1], dc[2], dc[3]);
     }
-    if constexpr (T > 0) grad_backward<KS, T - 1>(ex, c, g, th, dc);
+    if constexpr (T > STOP) grad_backward<KS, T - 1, STOP>(ex, c, g, th, dc);
 }
 
 // One chunk, given the carry R that enters it from later rows (a.ws_state,
@@ -246,15 +265,17 @@ template <typename T, int KS>
 __global__ __launch_bounds__(256, 2) void k_selective_scan_grad(ScanArgs a)
 {
     constexpr int NP = 4 * KS;
-    __shared__ float4 ex_all[4][kSub][16];
+    __shared__ GradRow ex_all[4][kSub][16];
+    __shared__ GradRow2 ex2_all[4][kSub][16];
     alignas(16) __shared__ float bc[2][4][kSub][2 * NP];  // two buffers: one barrier a tile
     const int slabs = a.slabs * (a.channels / a.dg);
     const int64_t slot = blockIdx.x / slabs;
     const int slab = (int)(blockIdx.x - slot * slabs);
     const Lane l = lane_place(a, slab);
-    const int w = threadIdx.x >> 6;
-    float4(*ex)[16] = ex_all[w];
-    const Chunk ck = slot_chunk<kCh>(a.q, slot);
+    const int w = uniform((int32_t)(threadIdx.x >> 6));
+    GradRow(*ex)[16] = ex_all[w];
+    GradRow2(*ex2)[16] = ex2_all[w];
+    const Chunk ck = uniform(slot_chunk<kCh>(a.q, slot));
     const int64_t at = (slot * a.channels + l.ch) * NP + l.q * KS;
     if (ck.len <= 0) {  // an empty slot: its partial sums are zero
         if (l.active) {
@@ -287,64 +308,79 @@ __global__ __launch_bounds__(256, 2) void k_selective_scan_grad(ScanArgs a)
 
     int sub = (ck.len - 1) / kSub;
     GradTile<T, KS, true> tile;
-    tile.load(a, l, ck.s, ck.span, ck.row + sub * kSub, ck.len - sub * kSub, gate);
+    tile.init(a, l);
+    tile.load(a, l, ck.s, ck.span.first + ck.row + sub * kSub, ck.len - sub * kSub, gate);
     for (; sub >= 0; --sub) {
-        const int32_t row = ck.row + sub * kSub, len = ck.len - sub * kSub;
-        float u[4], dl[4], slope[4], dy[4], go[4], z[4];
+        const int64_t first = ck.span.first + ck.row + sub * kSub;
+        const int32_t len = ck.len - sub * kSub;
+        {
+            float raw[4], dl[4], dy[4], slope[4], gw[4];
+            step_sizes<T>(a, tile.dl, bias, raw, dl);
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-            const bool valid = l.active && 4 * r + l.q < len;
-            u[r] = T::load(tile.u[r]);
-            const float raw = T::load(tile.dl[r]) + bias;
-            slope[r] = 1.f;
-            dl[r] = a.softplus ? softplus_f(raw, &slope[r]) : raw;
-            go[r] = T::load(tile.go[r]);
-            dy[r] = go[r];
-            if (gate) {
-                z[r] = T::load(tile.z[r]);
-                dy[r] *= silu_f(z[r], sigmoid_f(z[r]));
+            for (int r = 0; r < 4; ++r) {
+                dy[r] = T::load(tile.go[r]);
+                slope[r] = 1.f;
+                gw[r] = 0.f;
             }
-            // rows past the end and channels past the last: nothing is added
-            if (!valid) dl[r] = u[r] = dy[r] = 0.f;
-            ex[4 * r + l.q][l.c] = make_float4(dl[r], dl[r] * u[r], dy[r], 0.f);
-        }
+            if (a.softplus)
 #pragma unroll
-        for (int i = 0; i < KS; ++i) {
-            g.B[i] = tile.B[i];
-            g.C[i] = tile.C[i];
-            g.h[0][i] = 0.f;
+                for (int r = 0; r < 4; ++r) slope[r] = sigmoid_f<T>(raw[r]);
+            if (gate)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const float z = T::load(tile.z[r]), q = sigmoid_f<T>(z);
+                    gw[r] = dy[r] * silu_slope(z, q);
+                    dy[r] *= silu_f(z, q);
+                }
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                // rows past the end and channels past the last: nothing is added
+                const bool valid = l.active && 4 * r + l.q < len;
+                const float u = valid ? T::load(tile.u[r]) : 0.f;
+                const float d = valid ? dl[r] : 0.f;
+                ex[4 * r + l.q][l.c] = GradRow{d, d * u, valid ? dy[r] : 0.f, u};
+                ex2[4 * r + l.q][l.c] = GradRow2{slope[r], gw[r]};
+            }
         }
+        tile.B.get(g.B);
+        tile.C.get(g.C);
+#pragma unroll
+        for (int i = 0; i < KS; ++i) g.h[0][i] = 0.f;
         if (l.active)
             ld_states<KS>(a.cs + ((slot * kSubs + sub) * a.channels + l.ch) * NP + l.q * KS, g.h[0]);
         wave_lds_fence();
-        if (sub > 0) tile.load(a, l, ck.s, ck.span, row - kSub, kSub, gate);
 
         float t0[4], t1[4];
         grad_forward<KS, 0>(ex, l.c, gate, g, t0);
-        grad_backward<KS, kSub - 1>(ex, l.c, g, t0, t1);
-        wave_lds_fence();
+        grad_backward<KS, kSub - 1, 8>(ex, l.c, g, t0, t1);
+        // the next tile's loads, into the registers that half the rows have left
+        __builtin_amdgcn_sched_barrier(0);
+        if (sub > 0) tile.load(a, l, ck.s, first - kSub, kSub, gate);
+        __builtin_amdgcn_sched_barrier(0);
+        grad_backward<KS, 7, 0>(ex, l.c, g, t0, t1);
 
         float(*mine)[2 * NP] = bc[sub & 1][w];
         st_states<KS>(&mine[brev][l.q * KS], g.dBt);
         st_states<KS>(&mine[brev][NP + l.q * KS], g.dCt);
+        float du[4], dd[4], dz[4];
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-            const int t = 4 * r + l.q;
-            const float ddl = fma32(g.th[r], u[r], g.dc[r] * kLn2);
-            const float dd = ddl * slope[r];
-            if (l.active && t < len) {
-                const int64_t first = ck.span.first + row + t;
-                st<T>(rows_ptr<T>(a.du, ck.s, a.q, first) + l.ch,
-                      fma32(g.th[r], dl[r], Dc * dy[r]));
-                st<T>(rows_ptr<T>(a.ddelta, ck.s, a.q, first) + l.ch, dd);
-                if (gate) {
-                    const float y = fma32(Dc, u[r], g.y[r]);
-                    st<T>(rows_ptr<T>(a.dz, ck.s, a.q, first) + l.ch,
-                          go[r] * y * silu_slope(z[r], sigmoid_f(z[r])));
-                }
-                dD = fma32(dy[r], u[r], dD);
-                dbias += dd;
-            }
+            const GradRow x = ex[4 * r + l.q][l.c];
+            const GradRow2 x2 = ex2[4 * r + l.q][l.c];
+            du[r] = fma32(g.th[r], x.dl, Dc * x.dy);
+            dd[r] = fma32(g.th[r], x.u, g.dc[r] * kLn2) * x2.slope;
+            dz[r] = x2.w * fma32(Dc, x.u, g.y[r]);
+            dD = fma32(x.dy, x.u, dD);
+            if (l.active && 4 * r + l.q < len) dbias += dd[r];
+        }
+        LaneRows<T> ro;
+        ro.init(a.du, l);
+        ro.store(a.du, rows_ptr<T>(a.du, ck.s, a.q, first), l, len, du);
+        ro.init(a.ddelta, l);
+        ro.store(a.ddelta, rows_ptr<T>(a.ddelta, ck.s, a.q, first), l, len, dd);
+        if (gate) {
+            ro.init(a.dz, l);
+            ro.store(a.dz, rows_ptr<T>(a.dz, ck.s, a.q, first), l, len, dz);
         }
         __syncthreads();
         for (int i = threadIdx.x; i < kSub * 2 * NP; i += 256) {

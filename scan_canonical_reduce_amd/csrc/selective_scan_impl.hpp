@@ -57,77 +57,169 @@ __device__ __forceinline__ Lane lane_place(const ScanArgs& a, int slab)
     return l;
 }
 
-// B or C of one sequence row, this lane's states (0 beyond the last one).
-template <typename T, int KS>
-__device__ __forceinline__ void load_bc(const ScanArgs& a, const typename T::store_t* p, int q,
-                                        bool valid, float (&v)[KS])
+template <typename T>
+__device__ __forceinline__ uint32_t tile_off(const canon_rows_t& r, uint32_t t, uint32_t col)
 {
-    if (a.bc_vec) {
-        Vec<T, KS> x{};
-        if (q * KS < a.states) x = ld_vec<T, KS>(p + q * KS);
-#pragma unroll
-        for (int i = 0; i < KS; ++i) v[i] = valid ? T::load(x.e[i]) : 0.f;
-    } else {
-#pragma unroll
-        for (int i = 0; i < KS; ++i)
-            v[i] = valid && q * KS + i < a.states ? ld<T>(p + q * KS + i) : 0.f;
-    }
+    return (t * (uint32_t)r.row + col) * (uint32_t)sizeof(typename T::store_t);
 }
 
-// The inputs of a tile as this lane loads them: rows 4 r + q of its channel,
-// and B and C of row c.
-template <typename T, int KS, bool EMIT>
-struct Tile {
-    typename T::store_t u[4], dl[4], z[4];
-    float B[KS], C[KS];
+// Element `off` bytes behind a wave-uniform address.
+template <typename E>
+__device__ __forceinline__ const E* at_off(const E* base, uint32_t off)
+{
+    return reinterpret_cast<const E*>(reinterpret_cast<const char*>(base) + off);
+}
+template <typename E>
+__device__ __forceinline__ E* at_off(E* base, uint32_t off)
+{
+    return reinterpret_cast<E*>(reinterpret_cast<char*>(base) + off);
+}
 
-    __device__ __forceinline__ void load(const ScanArgs& a, const Lane& l, int64_t s,
-                                         const Span& span, int32_t row, int32_t len, bool gate)
+// A lane's rows 4 r + q of one activation.
+template <typename T>
+struct LaneRows {
+    uint32_t off;  // row q
+
+    __device__ __forceinline__ void init(const canon_rows_t& r, const Lane& l)
     {
-        // rows past the sequence's end are read as its last row and not used
-        const typename T::store_t* pu = rows_ptr<T>(a.u, s, a.q, span.first + row) + l.ch;
-        const typename T::store_t* pd = rows_ptr<T>(a.delta, s, a.q, span.first + row) + l.ch;
-        const typename T::store_t* pz =
-            gate ? rows_ptr<T>(a.z, s, a.q, span.first + row) + l.ch : nullptr;
+        off = tile_off<T>(r, l.q, l.ch);
+    }
+    // rows past the sequence's end are read as its last row and not used
+    __device__ __forceinline__ void load(const canon_rows_t& a, const typename T::store_t* base,
+                                         const Lane& l, int32_t len,
+                                         typename T::store_t (&v)[4]) const
+    {
+        if (len >= kSub) {
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-            const int64_t t = 4 * r + l.q < len ? 4 * r + l.q : len - 1;
-            u[r] = pu[t * a.u.row];
-            dl[r] = pd[t * a.delta.row];
-            if (EMIT && gate) z[r] = pz[t * a.z.row];
+            for (int r = 0; r < 4; ++r) v[r] = *at_off(base + 4 * r * a.row, off);
+        } else {
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const int t = 4 * r + l.q < len ? 4 * r + l.q : len - 1;
+                v[r] = *at_off(base, tile_off<T>(a, t, l.ch));
+            }
         }
-        const int64_t t = l.c < len ? l.c : len - 1;
-        load_bc<T, KS>(a,
-                       rows_ptr<T>(a.B, s, a.q, span.first + row + t) + (int64_t)l.g * a.states,
-                       l.q, l.c < len, B);
-        if (EMIT)
-            load_bc<T, KS>(
-                a, rows_ptr<T>(a.C, s, a.q, span.first + row + t) + (int64_t)l.g * a.states, l.q,
-                l.c < len, C);
+    }
+    __device__ __forceinline__ void store(const canon_rows_t& a, typename T::store_t* base,
+                                          const Lane& l, int32_t len, const float (&v)[4]) const
+    {
+        if (!l.active) return;
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+            if (4 * r + l.q < len) st<T>(at_off(base + 4 * r * a.row, off), v[r]);
     }
 };
 
+// B or C of the tile's row c: this lane's states (0 beyond the last one, and
+// for rows past the end).
+template <typename T, int KS>
+struct LaneBC {
+    Vec<T, KS> x;
+
+    __device__ __forceinline__ void load(const ScanArgs& a, const canon_rows_t& r,
+                                         const typename T::store_t* base, const Lane& l,
+                                         int32_t len)
+    {
+        const uint32_t t = l.c < len ? l.c : len - 1;
+        const typename T::store_t* p =
+            at_off(base, tile_off<T>(r, t, l.g * a.states + l.q * KS));
+        x = Vec<T, KS>{};
+        if (l.c >= len) return;
+        if (a.bc_vec) {
+            if (l.q * KS < a.states) x = ld_vec<T, KS>(p);
+        } else {
+#pragma unroll
+            for (int i = 0; i < KS; ++i)
+                if (l.q * KS + i < a.states) x.e[i] = p[i];
+        }
+    }
+    __device__ __forceinline__ void get(float (&v)[KS]) const
+    {
+#pragma unroll
+        for (int i = 0; i < KS; ++i) v[i] = T::load(x.e[i]);
+    }
+};
+
+// The inputs of a tile as this lane loads them.
+template <typename T, int KS, bool EMIT>
+struct Tile {
+    LaneRows<T> ru, rd, rz;
+    typename T::store_t u[4], dl[4], z[4];
+    LaneBC<T, KS> B, C;
+
+    __device__ __forceinline__ void init(const ScanArgs& a, const Lane& l)
+    {
+        ru.init(a.u, l);
+        rd.init(a.delta, l);
+        if (EMIT) rz.init(a.z, l);
+    }
+    __device__ __forceinline__ void load(const ScanArgs& a, const Lane& l, int64_t s,
+                                         int64_t first, int32_t len, bool gate)
+    {
+        ru.load(a.u, rows_ptr<T>(a.u, s, a.q, first), l, len, u);
+        rd.load(a.delta, rows_ptr<T>(a.delta, s, a.q, first), l, len, dl);
+        if (EMIT && gate) rz.load(a.z, rows_ptr<T>(a.z, s, a.q, first), l, len, z);
+        B.load(a, a.B, rows_ptr<T>(a.B, s, a.q, first), l, len);
+        if (EMIT) C.load(a, a.C, rows_ptr<T>(a.C, s, a.q, first), l, len);
+    }
+};
+
+// dl of a lane's four rows.
+template <typename T>
+__device__ __forceinline__ void step_sizes(const ScanArgs& a, const typename T::store_t (&x)[4],
+                                           float bias, float (&raw)[4], float (&dl)[4])
+{
+#pragma unroll
+    for (int r = 0; r < 4; ++r) dl[r] = raw[r] = T::load(x[r]) + bias;
+    if (a.softplus)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) dl[r] = softplus_f<T>(raw[r]);
+}
+
+// sum over i of lane T's b[i] (of each row of 16 lanes) times x[i], as one
+// product and KS - 1 FMAs that take b through DPP; the compiler would broadcast
+// each b[i] by an instruction of its own.  The s_nop covers the two wait states
+// between a write of b and its use by DPP, which the compiler does not see here.
+template <int T, int KS>
+__device__ __forceinline__ float bcast_dot(const float (&b)[KS], const float (&x)[KS])
+{
+    float y;
+    if constexpr (KS == 4)
+        asm("s_nop 1\n\t"
+            "v_mul_f32_dpp %0, %1, %5 row_newbcast:%9 row_mask:0xf bank_mask:0xf\n\t"
+            "v_fmac_f32_dpp %0, %2, %6 row_newbcast:%9 row_mask:0xf bank_mask:0xf\n\t"
+            "v_fmac_f32_dpp %0, %3, %7 row_newbcast:%9 row_mask:0xf bank_mask:0xf\n\t"
+            "v_fmac_f32_dpp %0, %4, %8 row_newbcast:%9 row_mask:0xf bank_mask:0xf"
+            : "=&v"(y)
+            : "v"(b[0]), "v"(b[1]), "v"(b[2]), "v"(b[3]), "v"(x[0]), "v"(x[1]), "v"(x[2]),
+              "v"(x[3]), "n"(T));
+    else if constexpr (KS == 2)
+        asm("s_nop 1\n\t"
+            "v_mul_f32_dpp %0, %1, %3 row_newbcast:%5 row_mask:0xf bank_mask:0xf\n\t"
+            "v_fmac_f32_dpp %0, %2, %4 row_newbcast:%5 row_mask:0xf bank_mask:0xf"
+            : "=&v"(y)
+            : "v"(b[0]), "v"(b[1]), "v"(x[0]), "v"(x[1]), "n"(T));
+    else
+        y = row_bcast<T>(b[0]) * x[0];
+    return y;
+}
+
 // One step of the recurrence for row T of the tile.
 template <int KS, int MODE, int T>
-__device__ __forceinline__ void scan_row(const float2 (*ex)[16], int c, const float (&A2)[KS],
-                                         const float (&B)[KS], const float (&C)[KS],
-                                         float (&h)[KS], float (&S)[KS], float& sdl,
-                                         float (&y)[4])
+__device__ __forceinline__ float scan_row(const float2 (*ex)[16], int c, const float (&A2)[KS],
+                                          const float (&B)[KS], const float (&C)[KS],
+                                          float (&h)[KS], float (&S)[KS], float& sdl)
 {
     const float2 x = ex[T][c];  // dl, dl u
     if (MODE != kEmit) sdl += x.x;
-    float acc = 0.f;
 #pragma unroll
     for (int i = 0; i < KS; ++i) {
         const float e = exp2_hw(x.x * A2[i]);
         const float b = row_bcast<T>(B[i]) * x.y;
         if (MODE != kEmit) S[i] = fma32(e, S[i], b);
-        if (MODE != kSum) {
-            h[i] = fma32(e, h[i], b);
-            acc = i == 0 ? row_bcast<T>(C[i]) * h[i] : fma32(row_bcast<T>(C[i]), h[i], acc);
-        }
+        if (MODE != kSum) h[i] = fma32(e, h[i], b);
     }
-    if (MODE != kSum) y[T & 3] = acc;
+    return MODE != kSum ? bcast_dot<T, KS>(C, h) : 0.f;
 }
 
 template <int KS, int MODE, int R>
@@ -136,12 +228,11 @@ __device__ __forceinline__ void scan_rows4(const float2 (*ex)[16], int c, const 
                                            float (&h)[KS], float (&S)[KS], float& sdl,
                                            float (&yr)[4])
 {
-    float y[4];
-    scan_row<KS, MODE, 4 * R + 0>(ex, c, A2, B, C, h, S, sdl, y);
-    scan_row<KS, MODE, 4 * R + 1>(ex, c, A2, B, C, h, S, sdl, y);
-    scan_row<KS, MODE, 4 * R + 2>(ex, c, A2, B, C, h, S, sdl, y);
-    scan_row<KS, MODE, 4 * R + 3>(ex, c, A2, B, C, h, S, sdl, y);
-    if (MODE != kSum) yr[R] = fold_quad(y[0], y[1], y[2], y[3]);
+    const float y0 = scan_row<KS, MODE, 4 * R + 0>(ex, c, A2, B, C, h, S, sdl);
+    const float y1 = scan_row<KS, MODE, 4 * R + 1>(ex, c, A2, B, C, h, S, sdl);
+    const float y2 = scan_row<KS, MODE, 4 * R + 2>(ex, c, A2, B, C, h, S, sdl);
+    const float y3 = scan_row<KS, MODE, 4 * R + 3>(ex, c, A2, B, C, h, S, sdl);
+    if (MODE != kSum) yr[R] = fold_quad(y0, y1, y2, y3);
 }
 
 template <int KS>
@@ -181,12 +272,12 @@ __global__ __launch_bounds__(256) void k_selective_scan(ScanArgs a)
     int64_t slot = slot_id;
     if (MODE == kSeq) {
         ck.s = slot_id;
-        ck.span = seq_span(a.q, ck.s);
-        slot = slot_base<kCh>(a.q, ck.s);
+        ck.span = uniform(seq_span(a.q, ck.s));
+        slot = uniform(slot_base<kCh>(a.q, ck.s));
         ck.row = 0;
         ck.len = ck.span.len < kCh ? ck.span.len : kCh;
     } else {
-        ck = slot_chunk<kCh>(a.q, slot);
+        ck = uniform(slot_chunk<kCh>(a.q, slot));
         if (ck.len <= 0) return;
     }
 
@@ -205,57 +296,58 @@ __global__ __launch_bounds__(256) void k_selective_scan(ScanArgs a)
     const bool gate = a.z.p != nullptr;
     if (MODE == kEmit)
         ld_states<KS>(a.ws_state + (slot * a.channels + l.ch) * NP + l.q * KS, h);
-
     float H[KS];  // the chunk's start state
 #pragma unroll
     for (int i = 0; i < KS; ++i) H[i] = h[i];
 
     Tile<T, KS, MODE != kSum> tile;
-    if (ck.len > 0) tile.load(a, l, ck.s, ck.span, ck.row, ck.len, gate);
+    tile.init(a, l);
+    LaneRows<T> ro;
+    ro.init(a.out, l);
+    if (ck.len > 0) tile.load(a, l, ck.s, ck.span.first + ck.row, ck.len, gate);
     float sdl = 0.f;
     while (ck.len > 0) {
-        typename T::store_t* po =
-            MODE != kSum ? rows_ptr<T>(a.out, ck.s, a.q, ck.span.first + ck.row) + l.ch : nullptr;
         for (int sub = 0; sub * kSub < ck.len; ++sub) {
             const int32_t row = ck.row + sub * kSub, len = ck.len - sub * kSub;
-            float u[4], z[4], B[KS], C[KS];
+            float u[4], dl[4], raw[4], gz[4], B[KS], C[KS];
+            step_sizes<T>(a, tile.dl, bias, raw, dl);
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
-                const bool valid = 4 * r + l.q < len;
                 u[r] = T::load(tile.u[r]);
-                if (MODE != kSum && gate) z[r] = T::load(tile.z[r]);
-                const float raw = T::load(tile.dl[r]) + bias;
-                const float d = a.softplus ? softplus_f(raw, nullptr) : raw;
                 // a row past the end: exp(0) = 1 and nothing added
-                ex[4 * r + l.q][l.c] = valid ? make_float2(d, d * u[r]) : make_float2(0.f, 0.f);
+                const bool valid = 4 * r + l.q < len;
+                ex[4 * r + l.q][l.c] =
+                    make_float2(valid ? dl[r] : 0.f, valid ? dl[r] * u[r] : 0.f);
             }
+            if (MODE != kSum && gate)
 #pragma unroll
-            for (int i = 0; i < KS; ++i) {
-                B[i] = tile.B[i];
-                if (MODE != kSum) C[i] = tile.C[i];
-            }
+                for (int r = 0; r < 4; ++r) {
+                    const float z = T::load(tile.z[r]);
+                    gz[r] = silu_f(z, sigmoid_f<T>(z));
+                }
+            tile.B.get(B);
+            if (MODE != kSum) tile.C.get(C);
             wave_lds_fence();
             if (MODE != kSum && a.cs && l.active)
                 st_states<KS>(a.cs + ((slot * kSubs + sub) * a.channels + l.ch) * NP + l.q * KS, h);
             // the next tile's loads, in flight while this one is computed
             const int32_t left = ck.span.len - row - kSub;
             if (left > 0 && (MODE == kSeq || sub + 1 < kSubs))
-                tile.load(a, l, ck.s, ck.span, row + kSub, left, gate);
+                tile.load(a, l, ck.s, ck.span.first + row + kSub, left, gate);
 
-            float yr[4];
-            scan_rows4<KS, MODE, 0>(ex, l.c, A2, B, C, h, S, sdl, yr);
-            scan_rows4<KS, MODE, 1>(ex, l.c, A2, B, C, h, S, sdl, yr);
-            scan_rows4<KS, MODE, 2>(ex, l.c, A2, B, C, h, S, sdl, yr);
-            scan_rows4<KS, MODE, 3>(ex, l.c, A2, B, C, h, S, sdl, yr);
+            float y[4];
+            scan_rows4<KS, MODE, 0>(ex, l.c, A2, B, C, h, S, sdl, y);
+            scan_rows4<KS, MODE, 1>(ex, l.c, A2, B, C, h, S, sdl, y);
+            scan_rows4<KS, MODE, 2>(ex, l.c, A2, B, C, h, S, sdl, y);
+            scan_rows4<KS, MODE, 3>(ex, l.c, A2, B, C, h, S, sdl, y);
             wave_lds_fence();
             if (MODE != kSum) {
 #pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    float y = fma32(Dc, u[r], yr[r]);
-                    if (gate) y *= silu_f(z[r], sigmoid_f(z[r]));
-                    if (l.active && 4 * r + l.q < len)
-                        st<T>(po + (int64_t)(sub * kSub + 4 * r + l.q) * a.out.row, y);
-                }
+                for (int r = 0; r < 4; ++r) y[r] = fma32(Dc, u[r], y[r]);
+                if (gate)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) y[r] *= gz[r];
+                ro.store(a.out, rows_ptr<T>(a.out, ck.s, a.q, ck.span.first + row), l, len, y);
             }
         }
         if (MODE != kSeq) break;
@@ -354,12 +446,17 @@ __global__ __launch_bounds__(256) void k_selective_scan_step(ScanArgs a)
     const float u = ld<T>(static_cast<typename T::store_t*>(a.u.p) + s * a.u.seq + ch);
     float raw = ld<T>(static_cast<typename T::store_t*>(a.delta.p) + s * a.delta.seq + ch);
     if (a.bias) raw += a.bias[ch];
-    const float d = a.softplus ? softplus_f(raw, nullptr) : raw;
+    const float d = a.softplus ? softplus_f<T>(raw) : raw;
     const float du = d * u;
+    Lane l{};
+    l.q = q;
+    l.g = g;
+    LaneBC<T, KS> xb, xc;
+    xb.load(a, a.B, static_cast<typename T::store_t*>(a.B.p) + s * a.B.seq, l, 1);
+    xc.load(a, a.C, static_cast<typename T::store_t*>(a.C.p) + s * a.C.seq, l, 1);
     float B[KS], C[KS];
-    const int64_t gb = (int64_t)g * a.states;
-    load_bc<T, KS>(a, static_cast<typename T::store_t*>(a.B.p) + s * a.B.seq + gb, q, true, B);
-    load_bc<T, KS>(a, static_cast<typename T::store_t*>(a.C.p) + s * a.C.seq + gb, q, true, C);
+    xb.get(B);
+    xc.get(C);
     const int64_t at = (s * a.channels + ch) * a.states + q * KS;
     const bool vec = a.st_vec;
     float h[KS], A2[KS];
@@ -397,7 +494,7 @@ __global__ __launch_bounds__(256) void k_selective_scan_step(ScanArgs a)
     if (a.D) y = fma32(a.D[ch], u, y);
     if (a.z.p) {
         const float z = ld<T>(static_cast<typename T::store_t*>(a.z.p) + s * a.z.seq + ch);
-        y *= silu_f(z, sigmoid_f(z));
+        y *= silu_f(z, sigmoid_f<T>(z));
     }
     st<T>(static_cast<typename T::store_t*>(a.out.p) + s * a.out.seq + ch, y);
 }

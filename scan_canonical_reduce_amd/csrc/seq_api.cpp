@@ -230,6 +230,10 @@ canon_status_t scan_args(const canon_selective_scan_t* c, bool step, bool grad, 
                  (c->ddelta_bias != nullptr && c->delta_bias == nullptr)))
         return CANON_EINVAL;
     if (!ptr_aligned(c->chunk_states, 16)) return CANON_EINVAL;
+    for (const canon_rows_t* r : {&c->u, &c->delta, &c->z, &c->out, &c->B, &c->C, &c->dout, &c->du,
+                                  &c->ddelta, &c->dz, &c->dB, &c->dC})
+        if (r->p != nullptr && r->row >= kMaxPitch) return CANON_EUNSUPPORTED;
+    if (bc_cols >= ((int64_t)1 << 24)) return CANON_EUNSUPPORTED;
     const size_t es = elem_bytes(c->dtype);
     const int ks = scan_ks(c->states);
     *a = ScanArgs{};

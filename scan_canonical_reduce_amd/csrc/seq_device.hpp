@@ -87,67 +87,59 @@ constexpr float kLn2 = 0x1.62e43p-1f;
 
 __device__ __forceinline__ float fma32(float a, float b, float c) { return __builtin_fmaf(a, b, c); }
 __device__ __forceinline__ float exp2_hw(float x) { return __builtin_amdgcn_exp2f(x); }
+// 1 / x to 1 ulp
+__device__ __forceinline__ float rcp_hw(float x) { return __builtin_amdgcn_rcpf(x); }
 
-// exp(x) to about 1.5 ulp: the product x log2(e) in two parts, the lower one
-// through exp2(r) = 1 + r ln 2.  (Beyond 128 the high part alone decides: the
-// remainder of an infinite product would be a NaN.)
+// exp(x).  float32 activations: to about 1.5 ulp, with the product x log2(e)
+// in two parts, the lower one through exp2(r) = 1 + r ln 2 (an infinite or
+// vanishing result has no lower part: the remainder of an infinite product
+// would be a NaN).  16-bit activations: the high part alone, whose relative
+// error, |x| 2^-24 and the exponential's ulp, is far below theirs.
+template <typename T>
 __device__ __forceinline__ float exp_f(float x)
 {
     const float t = x * kLog2e;
-    const float r = fma32(x, kLog2eLo, fma32(x, kLog2e, -t));
     const float e = exp2_hw(t);
+    if (sizeof(typename T::store_t) == 2) return e;
+    const float r = fma32(x, kLog2eLo, fma32(x, kLog2e, -t));
     return __builtin_fabsf(t) < 128.f ? fma32(e, r * kLn2, e) : e;
 }
 
-// 1 / x to about 1 ulp, x normal: the hardware reciprocal and one Newton step.
-__device__ __forceinline__ float rcp_f(float x)
-{
-    const float r = __builtin_amdgcn_rcpf(x);
-    const float n = fma32(fma32(-x, r, 1.f), r, r);
-    return __builtin_fabsf(x) < 0x1p126f ? n : r;  // an infinite x has 0, not a NaN
-}
-
+// 1 / (1 + exp(-x)): 0 and 1 in the limits
+template <typename T>
 __device__ __forceinline__ float sigmoid_f(float x)
 {
-    const float e = exp_f(-__builtin_fabsf(x));  // in (0, 1]: no overflow
-    const float r = rcp_f(1.f + e);
-    return x >= 0.f ? r : e * r;  // NaN: e is NaN
+    return rcp_hw(1.f + exp_f<T>(-x));
 }
 
 // softplus(x) = max(x, 0) + log(1 + e), e = exp(-|x|) <= 1, with the logarithm
-// as 2 artanh(s), s = e / (2 + e) <= 1/3: 2 (s + s^3/3 + s^5/5 + ...); the
-// first term left out, s^17/17, is below 2^-30 of s.  No cancellation at any
-// x, so small step sizes keep their relative precision.  *slope = sigmoid(x),
-// the derivative.
-__device__ __forceinline__ float softplus_f(float x, float* slope)
+// as 2 artanh(s) = s P(s^2), s = e / (2 + e) <= 1/3.  P is the polynomial of
+// degree 4 whose largest relative error on [0, 1/9] is smallest (0.07 2^-24;
+// found by exchange on 2 artanh(sqrt v) / sqrt v).  No cancellation at any x,
+// so small step sizes keep their relative precision.
+template <typename T>
+__device__ __forceinline__ float softplus_f(float x)
 {
-    const float e = exp_f(-__builtin_fabsf(x));
-    const float s = e * rcp_f(2.f + e);
-    const float s2 = s * s;
-    float p = fma32(s2, 1.f / 15.f, 1.f / 13.f);
-    p = fma32(p, s2, 1.f / 11.f);
-    p = fma32(p, s2, 1.f / 9.f);
-    p = fma32(p, s2, 1.f / 7.f);
-    p = fma32(p, s2, 1.f / 5.f);
-    p = fma32(p, s2, 1.f / 3.f);
-    const float l = 2.f * fma32(s * s2, p, s);
-    if (slope) {
-        const float r = rcp_f(1.f + e);
-        *slope = x >= 0.f ? r : e * r;
-    }
-    return (x > 0.f ? x : 0.f) + l;
+    const float e = exp_f<T>(-__builtin_fabsf(x));
+    const float s = e * rcp_hw(2.f + e);
+    const float v = s * s;
+    float p = fma32(v, 0x1.208bdp-2f, 0x1.1e510ap-2f);
+    p = fma32(p, v, 0x1.99dae6p-2f);
+    p = fma32(p, v, 0x1.5554e0p-1f);
+    p = fma32(p, v, 2.f);
+    return fma32(s, p, x < 0.f ? 0.f : x);  // a NaN stays one
 }
 
-// d/dx of x sigmoid(x), given q = sigmoid(x): q (1 + x (1 - q)), with its
-// limits 0 and 1 where x is infinite
+// x sigmoid(x) given q = sigmoid(x): 0, not a NaN, at minus infinity
+__device__ __forceinline__ float silu_f(float x, float q) { return q == 0.f ? q : x * q; }
+
+// d/dx of x sigmoid(x), given q = sigmoid(x): q + x q (1 - q), with its limits
+// 0 and 1 where x is infinite
 __device__ __forceinline__ float silu_slope(float x, float q)
 {
-    const float r = 1.f - q;
-    return fma32(q, q == 0.f || r == 0.f ? 0.f : x * r, q);
+    const float r = q - q * q;
+    return r == 0.f ? q : fma32(x, r, q);
 }
-
-// x sigmoid(x): 0, not a NaN, at minus infinity
-__device__ __forceinline__ float silu_f(float x, float q) { return q == 0.f ? 0.f * q : x * q; }
 
 // ------------------------------------------------------------------- lane moves
 template <int CTRL>
@@ -285,6 +277,21 @@ __device__ __forceinline__ Chunk slot_chunk(const Seqs& q, int64_t slot)
     const int32_t left = c.span.len - c.row;
     c.len = left < CH ? left : CH;
     return c;
+}
+
+// The value of a wave's first lane, in scalar registers: for values that are
+// the same in every lane but were read or computed lane by lane.
+__device__ __forceinline__ int32_t uniform(int32_t v) { return __builtin_amdgcn_readfirstlane(v); }
+__device__ __forceinline__ int64_t uniform(int64_t v)
+{
+    const uint32_t lo = (uint32_t)__builtin_amdgcn_readfirstlane((int32_t)(uint32_t)v);
+    const uint32_t hi = (uint32_t)__builtin_amdgcn_readfirstlane((int32_t)(v >> 32));
+    return (int64_t)((uint64_t)hi << 32 | lo);
+}
+__device__ __forceinline__ Span uniform(Span s) { return Span{uniform(s.first), uniform(s.len)}; }
+__device__ __forceinline__ Chunk uniform(Chunk c)
+{
+    return Chunk{uniform(c.s), uniform(c.span), uniform(c.row), uniform(c.len)};
 }
 
 template <typename T>
