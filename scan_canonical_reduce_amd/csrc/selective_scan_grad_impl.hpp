@@ -145,8 +145,42 @@ __global__ __launch_bounds__(256) void k_scan_back_sum(ScanArgs a)
     if (l.q == 0) a.ws_dl[slot * a.channels + l.ch] = sdl;
 }
 
-// One level of the sum over a row's 16 lanes: lanes without bit `bit` of c keep
-// x and take the mirrored lane's x, lanes with it y.
+// One level of the sum over a row's 16 lanes: a lane without the level's bit of
+// c gets x plus the mirrored lane's x, a lane with it y plus the mirrored
+// lane's y.  Mirrors over 16 and 8 lanes pair whole banks of four, so both sums
+// write their own banks of the result (two instructions; the s_nop covers the
+// wait states between a write and its use by DPP, which the compiler does not
+// see here); below that the lanes select first (three).
+#define CANON_FOLD_BANKS(NAME, CTRL, LOWER, UPPER)                                              \
+    template <int KS>                                                                           \
+    __device__ __forceinline__ void NAME(const float (&x)[KS], const float (&y)[KS],            \
+                                         float (&r)[KS])                                        \
+    {                                                                                           \
+        if constexpr (KS == 4)                                                                  \
+            asm("s_nop 1\n\t"                                                                   \
+                "v_add_f32_dpp %0, %4, %4 " CTRL " row_mask:0xf bank_mask:" LOWER "\n\t"        \
+                "v_add_f32_dpp %1, %5, %5 " CTRL " row_mask:0xf bank_mask:" LOWER "\n\t"        \
+                "v_add_f32_dpp %2, %6, %6 " CTRL " row_mask:0xf bank_mask:" LOWER "\n\t"        \
+                "v_add_f32_dpp %3, %7, %7 " CTRL " row_mask:0xf bank_mask:" LOWER "\n\t"        \
+                "v_add_f32_dpp %0, %8, %8 " CTRL " row_mask:0xf bank_mask:" UPPER "\n\t"        \
+                "v_add_f32_dpp %1, %9, %9 " CTRL " row_mask:0xf bank_mask:" UPPER "\n\t"        \
+                "v_add_f32_dpp %2, %10, %10 " CTRL " row_mask:0xf bank_mask:" UPPER "\n\t"      \
+                "v_add_f32_dpp %3, %11, %11 " CTRL " row_mask:0xf bank_mask:" UPPER              \
+                : "=&v"(r[0]), "=&v"(r[1]), "=&v"(r[2]), "=&v"(r[3])                            \
+                : "v"(x[0]), "v"(x[1]), "v"(x[2]), "v"(x[3]), "v"(y[0]), "v"(y[1]), "v"(y[2]),  \
+                  "v"(y[3]));                                                                   \
+        else                                                                                    \
+            for (int i = 0; i < KS; ++i)                                                        \
+                asm("s_nop 1\n\t"                                                               \
+                    "v_add_f32_dpp %0, %1, %1 " CTRL " row_mask:0xf bank_mask:" LOWER "\n\t"    \
+                    "v_add_f32_dpp %0, %2, %2 " CTRL " row_mask:0xf bank_mask:" UPPER            \
+                    : "=&v"(r[i])                                                               \
+                    : "v"(x[i]), "v"(y[i]));                                                    \
+    }
+CANON_FOLD_BANKS(fold16, "row_mirror", "0x3", "0xc")
+CANON_FOLD_BANKS(fold8, "row_half_mirror", "0x5", "0xa")
+#undef CANON_FOLD_BANKS
+
 template <int CTRL>
 __device__ __forceinline__ float fold_lanes(float x, float y, bool upper)
 {
@@ -154,7 +188,7 @@ __device__ __forceinline__ float fold_lanes(float x, float y, bool upper)
     return keep + dpp<CTRL>(send);
 }
 
-constexpr int kMirror16 = 0x140, kMirror8 = 0x141, kMirror4 = 0x1b, kMirror2 = 0xb1;
+constexpr int kMirror4 = 0x1b, kMirror2 = 0xb1;
 
 // Sums over the lanes of a row, sequence rows arriving in descending order T =
 // 15 .. 0; v[L] holds what waits for its partner at level L.
@@ -165,20 +199,21 @@ struct LaneSum {
     template <int T>
     __device__ __forceinline__ void add(float (&x)[KS], int c)
     {
-#pragma unroll
-        for (int i = 0; i < KS; ++i) {
-            if constexpr (T & 1) {
-                wait[0][i] = x[i];
+        float a[KS], b[KS];
+        if constexpr (T & 1) {
+            copy(x, wait[0]);
+        } else {
+            fold16<KS>(x, wait[0], a);
+            if constexpr (T & 2) {
+                copy(a, wait[1]);
             } else {
-                const float a = fold_lanes<kMirror16>(x[i], wait[0][i], c & 8);
-                if constexpr (T & 2) {
-                    wait[1][i] = a;
-                } else {
-                    const float b = fold_lanes<kMirror8>(a, wait[1][i], c & 4);
+                fold8<KS>(a, wait[1], b);
+#pragma unroll
+                for (int i = 0; i < KS; ++i) {
                     if constexpr (T & 4) {
-                        wait[2][i] = b;
+                        wait[2][i] = b[i];
                     } else {
-                        const float d = fold_lanes<kMirror4>(b, wait[2][i], c & 2);
+                        const float d = fold_lanes<kMirror4>(b[i], wait[2][i], c & 2);
                         if constexpr (T & 8)
                             wait[3][i] = d;
                         else
@@ -187,6 +222,11 @@ struct LaneSum {
                 }
             }
         }
+    }
+    static __device__ __forceinline__ void copy(const float (&x)[KS], float (&y)[KS])
+    {
+#pragma unroll
+        for (int i = 0; i < KS; ++i) y[i] = x[i];
     }
 };
 
@@ -240,6 +280,7 @@ __device__ __forceinline__ void grad_backward(const GradRow (*ex)[16], int c, Gr
         g.R[i] *= g.a[T][i];
         const float d = g.R[i] * g.h[T][i];
         g.dA[i] = fma32(dl, d, g.dA[i]);
+        pin(g.dA[i]);
         decay = i == 0 ? g.A2[i] * d : fma32(g.A2[i], d, decay);
     }
     dc[T & 3] = decay;
@@ -260,31 +301,52 @@ __device__ __forceinline__ void grad_backward(const GradRow (*ex)[16], int c, Gr
 }
 
 // One chunk, given the carry R that enters it from later rows (a.ws_state,
-// which then takes the chunk's part of dA).
-template <typename T, int KS>
+// which then takes the chunk's part of dA); or, SEQ, a whole sequence from its
+// end, the carry kept in registers.
+template <typename T, int KS, bool SEQ>
 __global__ __launch_bounds__(256, 2) void k_selective_scan_grad(ScanArgs a)
 {
     constexpr int NP = 4 * KS;
     __shared__ GradRow ex_all[4][kSub][16];
     __shared__ GradRow2 ex2_all[4][kSub][16];
-    alignas(16) __shared__ float bc[2][4][kSub][2 * NP];  // two buffers: one barrier a tile
+    // two buffers: one barrier a tile; rows padded by 16 bytes against bank conflicts
+    alignas(16) __shared__ float bc[2][4][kSub][2 * NP + 4];
     const int slabs = a.slabs * (a.channels / a.dg);
-    const int64_t slot = blockIdx.x / slabs;
-    const int slab = (int)(blockIdx.x - slot * slabs);
+    const int64_t id = blockIdx.x / slabs;
+    const int slab = (int)(blockIdx.x - id * slabs);
     const Lane l = lane_place(a, slab);
     const int w = uniform((int32_t)(threadIdx.x >> 6));
     GradRow(*ex)[16] = ex_all[w];
     GradRow2(*ex2)[16] = ex2_all[w];
-    const Chunk ck = uniform(slot_chunk<kCh>(a.q, slot));
-    const int64_t at = (slot * a.channels + l.ch) * NP + l.q * KS;
-    if (ck.len <= 0) {  // an empty slot: its partial sums are zero
+    int64_t s, slot;  // the sequence, and the slot of its chunk (SEQ: the last one)
+    int32_t lo, hi;   // rows of the sequence
+    Span span;
+    if (SEQ) {
+        s = id;
+        span = uniform(seq_span(a.q, s));
+        lo = 0;
+        hi = span.len;
+        slot = uniform(slot_base<kCh>(a.q, s)) + (hi > 0 ? (hi - 1) / kCh : 0);
+    } else {
+        slot = id;
+        const Chunk ck = uniform(slot_chunk<kCh>(a.q, slot));
+        s = ck.s;
+        span = ck.span;
+        lo = ck.row;
+        hi = ck.row + ck.len;
+    }
+    const int64_t own = ((SEQ ? s : slot) * a.channels + l.ch) * (SEQ ? a.states : NP) + l.q * KS;
+    if (hi <= lo) {  // an empty slot: its partial sums are zero
         if (l.active) {
             const float zero[KS] = {};
-            st_states<KS>(a.ws_state + at, zero);
+            st_states<KS>(a.ws_state + (slot * a.channels + l.ch) * NP + l.q * KS, zero);
             if (l.q == 0) {
                 a.ws_dD[slot * a.channels + l.ch] = 0.f;
                 a.ws_dbias[slot * a.channels + l.ch] = 0.f;
             }
+            if (SEQ && a.dinit)
+                for (int i = 0; i < KS; ++i)
+                    if (l.q * KS + i < a.states) a.dinit[own + i] = a.dfinal ? a.dfinal[own + i] : 0.f;
         }
         return;
     }
@@ -294,25 +356,26 @@ __global__ __launch_bounds__(256, 2) void k_selective_scan_grad(ScanArgs a)
     for (int i = 0; i < KS; ++i) {
         const int n = l.q * KS + i;
         g.A2[i] = n < a.states ? a.A[(int64_t)l.ch * a.states + n] * kLog2e : 0.f;
-        g.R[i] = 0.f;
+        g.R[i] = SEQ && a.dfinal && l.active && n < a.states ? a.dfinal[own + i] : 0.f;
         g.dA[i] = 0.f;
     }
-    if (l.active) ld_states<KS>(a.ws_state + at, g.R);
+    if (!SEQ && l.active) ld_states<KS>(a.ws_state + own, g.R);
     const float bias = a.bias ? a.bias[l.ch] : 0.f, Dc = a.D ? a.D[l.ch] : 0.f;
     const bool gate = a.z.p != nullptr;
     float dD = 0.f, dbias = 0.f;
     const int brev = (l.c & 1) << 3 | (l.c & 2) << 1 | (l.c & 4) >> 1 | (l.c & 8) >> 3;
     // the rows of the partial sums of dB and dC: packed rows, or sequence by sequence
-    const int64_t bc_row = (a.q.starts ? 0 : ck.s * a.q.rows) + ck.span.first + ck.row;
+    const int64_t bc_row = (a.q.starts ? 0 : s * a.q.rows) + span.first;
     const int64_t bc_rows = a.q.starts ? a.q.rows : a.q.seqs * a.q.rows;
 
-    int sub = (ck.len - 1) / kSub;
+    int32_t row = (hi - 1) / kSub * kSub;
     GradTile<T, KS, true> tile;
     tile.init(a, l);
-    tile.load(a, l, ck.s, ck.span.first + ck.row + sub * kSub, ck.len - sub * kSub, gate);
-    for (; sub >= 0; --sub) {
-        const int64_t first = ck.span.first + ck.row + sub * kSub;
-        const int32_t len = ck.len - sub * kSub;
+    tile.load(a, l, s, span.first + row, hi - row, gate);
+    for (; row >= lo; row -= kSub) {
+        const int64_t first = span.first + row;
+        const int32_t len = hi - row;
+        const int sub = row / kSub % kSubs;
         {
             float raw[4], dl[4], dy[4], slope[4], gw[4];
             step_sizes<T>(a, tile.dl, bias, raw, dl);
@@ -355,11 +418,11 @@ __global__ __launch_bounds__(256, 2) void k_selective_scan_grad(ScanArgs a)
         grad_backward<KS, kSub - 1, 8>(ex, l.c, g, t0, t1);
         // the next tile's loads, into the registers that half the rows have left
         __builtin_amdgcn_sched_barrier(0);
-        if (sub > 0) tile.load(a, l, ck.s, first - kSub, kSub, gate);
+        if (row > lo) tile.load(a, l, s, first - kSub, kSub, gate);
         __builtin_amdgcn_sched_barrier(0);
         grad_backward<KS, 7, 0>(ex, l.c, g, t0, t1);
 
-        float(*mine)[2 * NP] = bc[sub & 1][w];
+        float(*mine)[2 * NP + 4] = bc[sub & 1][w];
         st_states<KS>(&mine[brev][l.q * KS], g.dBt);
         st_states<KS>(&mine[brev][NP + l.q * KS], g.dCt);
         float du[4], dd[4], dz[4];
@@ -375,12 +438,12 @@ __global__ __launch_bounds__(256, 2) void k_selective_scan_grad(ScanArgs a)
         }
         LaneRows<T> ro;
         ro.init(a.du, l);
-        ro.store(a.du, rows_ptr<T>(a.du, ck.s, a.q, first), l, len, du);
+        ro.store(a.du, rows_ptr<T>(a.du, s, a.q, first), l, len, du);
         ro.init(a.ddelta, l);
-        ro.store(a.ddelta, rows_ptr<T>(a.ddelta, ck.s, a.q, first), l, len, dd);
+        ro.store(a.ddelta, rows_ptr<T>(a.ddelta, s, a.q, first), l, len, dd);
         if (gate) {
             ro.init(a.dz, l);
-            ro.store(a.dz, rows_ptr<T>(a.dz, ck.s, a.q, first), l, len, dz);
+            ro.store(a.dz, rows_ptr<T>(a.dz, s, a.q, first), l, len, dz);
         }
         __syncthreads();
         for (int i = threadIdx.x; i < kSub * 2 * NP; i += 256) {
@@ -388,17 +451,30 @@ __global__ __launch_bounds__(256, 2) void k_selective_scan_grad(ScanArgs a)
             const float v = (bc[sub & 1][0][t][n] + bc[sub & 1][1][t][n]) +
                             (bc[sub & 1][2][t][n] + bc[sub & 1][3][t][n]);
             if (t < len)
-                a.ws_bc[((int64_t)slab * bc_rows + bc_row + sub * kSub + t) * (2 * NP) + n] = v;
+                a.ws_bc[((int64_t)slab * bc_rows + bc_row + row + t) * (2 * NP) + n] = v;
         }
+        if (sub != 0) continue;
+        // the chunk is done: its parts of the parameters' gradients
+        const float sum_D = fold_quad(dD, dD, dD, dD);
+        const float sum_b = fold_quad(dbias, dbias, dbias, dbias);
+        if (l.active) {
+            const int64_t part = slot * a.channels + l.ch;
+            st_states<KS>(a.ws_state + part * NP + l.q * KS, g.dA);
+            if (l.q == 0) {
+                a.ws_dD[part] = sum_D;
+                a.ws_dbias[part] = sum_b;
+            }
+        }
+        if (!SEQ) continue;
+        --slot;
+        dD = dbias = 0.f;
+#pragma unroll
+        for (int i = 0; i < KS; ++i) g.dA[i] = 0.f;
     }
-    dD = fold_quad(dD, dD, dD, dD);
-    dbias = fold_quad(dbias, dbias, dbias, dbias);
-    if (!l.active) return;
-    st_states<KS>(a.ws_state + at, g.dA);
-    if (l.q == 0) {
-        a.ws_dD[slot * a.channels + l.ch] = dD;
-        a.ws_dbias[slot * a.channels + l.ch] = dbias;
-    }
+    if (SEQ && a.dinit && l.active)
+#pragma unroll
+        for (int i = 0; i < KS; ++i)
+            if (l.q * KS + i < a.states) a.dinit[own + i] = g.R[i];
 }
 
 // dB and dC of each row: the slabs' sums in order, rounded once.
@@ -436,17 +512,33 @@ __global__ __launch_bounds__(256) void k_scan_sum_bc(ScanArgs a, int groups)
     st<T>(rows_ptr<T>(o, s, a.q, row) + (int64_t)g * a.states + st_n, v);
 }
 
+// Whole sequences, one after the other in a workgroup, where those fill the
+// chip's 512 places (two workgroups on each of 256 compute units) to seven
+// eighths; else chunks.  Packed sequences' lengths are not known here.
+inline bool grad_whole_sequences(const ScanArgs& a, int64_t slabs)
+{
+    const int64_t groups = a.q.seqs * slabs, rounds = (groups + 511) / 512;
+    return a.q.starts == nullptr && groups > 0 && groups >= 448 * rounds;
+}
+
 template <typename T, int KS>
 hipError_t launch_scan_grad_ks(const ScanArgs& a, int64_t groups, hipStream_t st)
 {
     constexpr int NP = 4 * KS;
     const int64_t slots = slot_count<kCh>(a.q.seqs, a.q.rows, a.q.starts != nullptr);
-    const unsigned grid = (unsigned)(slots * groups * a.slabs);
-    if (grid) k_scan_back_sum<T, KS><<<dim3(grid), dim3(256), 0, st>>>(a);
-    if (hipError_t e = hipGetLastError()) return e;
-    if (hipError_t e = launch_scan_carry<NP, true>(a, a.dfinal, a.dinit, st)) return e;
-    if (grid) k_selective_scan_grad<T, KS><<<dim3(grid), dim3(256), 0, st>>>(a);
-    if (hipError_t e = hipGetLastError()) return e;
+    const int64_t slabs = groups * a.slabs;
+    if (grad_whole_sequences(a, slabs)) {
+        k_selective_scan_grad<T, KS, true>
+            <<<dim3((unsigned)(a.q.seqs * slabs)), dim3(256), 0, st>>>(a);
+        if (hipError_t e = hipGetLastError()) return e;
+    } else {
+        const unsigned grid = (unsigned)(slots * slabs);
+        if (grid) k_scan_back_sum<T, KS><<<dim3(grid), dim3(256), 0, st>>>(a);
+        if (hipError_t e = hipGetLastError()) return e;
+        if (hipError_t e = launch_scan_carry<NP, true>(a, a.dfinal, a.dinit, st)) return e;
+        if (grid) k_selective_scan_grad<T, KS, false><<<dim3(grid), dim3(256), 0, st>>>(a);
+        if (hipError_t e = hipGetLastError()) return e;
+    }
     const int64_t d = a.channels;
     if (hipError_t e = launch_column_sum(a.ws_state, slots, d * NP, NP, a.states, a.dA, st))
         return e;

@@ -218,7 +218,9 @@ __device__ __forceinline__ float scan_row(const float2 (*ex)[16], int c, const f
         const float b = row_bcast<T>(B[i]) * x.y;
         if (MODE != kEmit) S[i] = fma32(e, S[i], b);
         if (MODE != kSum) h[i] = fma32(e, h[i], b);
+        if (MODE == kSeq) pin(S[i]);
     }
+    if (MODE == kSeq) pin(sdl);
     return MODE != kSum ? bcast_dot<T, KS>(C, h) : 0.f;
 }
 
@@ -258,7 +260,7 @@ __device__ __forceinline__ void st_states(float* p, const float (&v)[KS])
 }
 
 template <typename T, int KS, int MODE>
-__global__ __launch_bounds__(256) void k_selective_scan(ScanArgs a)
+__global__ __launch_bounds__(256, 4) void k_selective_scan(ScanArgs a)
 {
     constexpr int NP = 4 * KS;
     __shared__ float2 ex_all[4][kSub][16];
@@ -268,17 +270,22 @@ __global__ __launch_bounds__(256) void k_selective_scan(ScanArgs a)
     if (l.wch >= a.dg) return;
     float2(*ex)[16] = ex_all[threadIdx.x >> 6];
 
-    Chunk ck;
-    int64_t slot = slot_id;
+    int64_t s, slot = slot_id;  // the sequence, and the slot of its chunk
+    int32_t lo, hi;             // rows of the sequence
+    Span span;
     if (MODE == kSeq) {
-        ck.s = slot_id;
-        ck.span = uniform(seq_span(a.q, ck.s));
-        slot = uniform(slot_base<kCh>(a.q, ck.s));
-        ck.row = 0;
-        ck.len = ck.span.len < kCh ? ck.span.len : kCh;
+        s = slot_id;
+        span = uniform(seq_span(a.q, s));
+        slot = uniform(slot_base<kCh>(a.q, s));
+        lo = 0;
+        hi = span.len;
     } else {
-        ck = uniform(slot_chunk<kCh>(a.q, slot));
+        const Chunk ck = uniform(slot_chunk<kCh>(a.q, slot));
         if (ck.len <= 0) return;
+        s = ck.s;
+        span = ck.span;
+        lo = ck.row;
+        hi = ck.row + ck.len;
     }
 
     float A2[KS], h[KS], S[KS];
@@ -289,7 +296,7 @@ __global__ __launch_bounds__(256) void k_selective_scan(ScanArgs a)
         h[i] = 0.f;
         S[i] = 0.f;
         if (MODE == kSeq && a.init && n < a.states)
-            h[i] = a.init[(ck.s * a.channels + l.ch) * a.states + n];
+            h[i] = a.init[(s * a.channels + l.ch) * a.states + n];
     }
     const float bias = a.bias ? a.bias[l.ch] : 0.f;
     const float Dc = MODE != kSum && a.D ? a.D[l.ch] : 0.f;
@@ -304,63 +311,60 @@ __global__ __launch_bounds__(256) void k_selective_scan(ScanArgs a)
     tile.init(a, l);
     LaneRows<T> ro;
     ro.init(a.out, l);
-    if (ck.len > 0) tile.load(a, l, ck.s, ck.span.first + ck.row, ck.len, gate);
+    if (lo < hi) tile.load(a, l, s, span.first + lo, hi - lo, gate);
     float sdl = 0.f;
-    while (ck.len > 0) {
-        for (int sub = 0; sub * kSub < ck.len; ++sub) {
-            const int32_t row = ck.row + sub * kSub, len = ck.len - sub * kSub;
-            float u[4], dl[4], raw[4], gz[4], B[KS], C[KS];
-            step_sizes<T>(a, tile.dl, bias, raw, dl);
+#pragma unroll 1
+    for (int32_t row = lo; row < hi; row += kSub) {
+        const int64_t first = span.first + row;
+        const int32_t len = hi - row;
+        const int sub = row / kSub % kSubs;
+        float u[4], dl[4], raw[4], gz[4], B[KS], C[KS];
+        step_sizes<T>(a, tile.dl, bias, raw, dl);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            u[r] = T::load(tile.u[r]);
+            // a row past the end: exp(0) = 1 and nothing added
+            const bool valid = 4 * r + l.q < len;
+            ex[4 * r + l.q][l.c] = make_float2(valid ? dl[r] : 0.f, valid ? dl[r] * u[r] : 0.f);
+        }
+        if (MODE != kSum && gate)
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
-                u[r] = T::load(tile.u[r]);
-                // a row past the end: exp(0) = 1 and nothing added
-                const bool valid = 4 * r + l.q < len;
-                ex[4 * r + l.q][l.c] =
-                    make_float2(valid ? dl[r] : 0.f, valid ? dl[r] * u[r] : 0.f);
+                const float z = T::load(tile.z[r]);
+                gz[r] = silu_f(z, sigmoid_f<T>(z));
             }
-            if (MODE != kSum && gate)
-#pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const float z = T::load(tile.z[r]);
-                    gz[r] = silu_f(z, sigmoid_f<T>(z));
-                }
-            tile.B.get(B);
-            if (MODE != kSum) tile.C.get(C);
-            wave_lds_fence();
-            if (MODE != kSum && a.cs && l.active)
-                st_states<KS>(a.cs + ((slot * kSubs + sub) * a.channels + l.ch) * NP + l.q * KS, h);
-            // the next tile's loads, in flight while this one is computed
-            const int32_t left = ck.span.len - row - kSub;
-            if (left > 0 && (MODE == kSeq || sub + 1 < kSubs))
-                tile.load(a, l, ck.s, ck.span.first + row + kSub, left, gate);
+        tile.B.get(B);
+        if (MODE != kSum) tile.C.get(C);
+        wave_lds_fence();
+        if (MODE != kSum && a.cs && l.active)
+            st_states<KS>(a.cs + ((slot * kSubs + sub) * a.channels + l.ch) * NP + l.q * KS, h);
+        // the next tile's loads, in flight while this one is computed
+        if (len > kSub) tile.load(a, l, s, first + kSub, len - kSub, gate);
 
-            float y[4];
-            scan_rows4<KS, MODE, 0>(ex, l.c, A2, B, C, h, S, sdl, y);
-            scan_rows4<KS, MODE, 1>(ex, l.c, A2, B, C, h, S, sdl, y);
-            scan_rows4<KS, MODE, 2>(ex, l.c, A2, B, C, h, S, sdl, y);
-            scan_rows4<KS, MODE, 3>(ex, l.c, A2, B, C, h, S, sdl, y);
-            wave_lds_fence();
-            if (MODE != kSum) {
+        float y[4];
+        scan_rows4<KS, MODE, 0>(ex, l.c, A2, B, C, h, S, sdl, y);
+        scan_rows4<KS, MODE, 1>(ex, l.c, A2, B, C, h, S, sdl, y);
+        scan_rows4<KS, MODE, 2>(ex, l.c, A2, B, C, h, S, sdl, y);
+        scan_rows4<KS, MODE, 3>(ex, l.c, A2, B, C, h, S, sdl, y);
+        wave_lds_fence();
+        if (MODE != kSum) {
 #pragma unroll
-                for (int r = 0; r < 4; ++r) y[r] = fma32(Dc, u[r], y[r]);
-                if (gate)
+            for (int r = 0; r < 4; ++r) y[r] = fma32(Dc, u[r], y[r]);
+            if (gate)
 #pragma unroll
-                    for (int r = 0; r < 4; ++r) y[r] *= gz[r];
-                ro.store(a.out, rows_ptr<T>(a.out, ck.s, a.q, ck.span.first + row), l, len, y);
+                for (int r = 0; r < 4; ++r) y[r] *= gz[r];
+            ro.store(a.out, rows_ptr<T>(a.out, s, a.q, first), l, len, y);
+        }
+        if (MODE == kSeq && (sub == kSubs - 1 || len <= kSub)) {
+#pragma unroll
+            for (int i = 0; i < KS; ++i) {  // the next chunk's start state
+                H[i] = fma32(exp2_hw(sdl * A2[i]), H[i], S[i]);
+                h[i] = H[i];
+                S[i] = 0.f;
             }
+            sdl = 0.f;
+            ++slot;
         }
-        if (MODE != kSeq) break;
-#pragma unroll
-        for (int i = 0; i < KS; ++i) {  // the next chunk's start state
-            H[i] = fma32(exp2_hw(sdl * A2[i]), H[i], S[i]);
-            h[i] = H[i];
-            S[i] = 0.f;
-        }
-        sdl = 0.f;
-        ++slot;
-        ck.row += kCh;
-        ck.len = ck.span.len - ck.row < kCh ? ck.span.len - ck.row : kCh;
     }
     if (!l.active) return;
     if (MODE == kSum) {
@@ -371,7 +375,7 @@ __global__ __launch_bounds__(256) void k_selective_scan(ScanArgs a)
 #pragma unroll
         for (int i = 0; i < KS; ++i)
             if (l.q * KS + i < a.states)
-                a.final[(ck.s * a.channels + l.ch) * a.states + l.q * KS + i] = h[i];
+                a.final[(s * a.channels + l.ch) * a.states + l.q * KS + i] = h[i];
     }
 }
 
@@ -396,22 +400,34 @@ __global__ __launch_bounds__(256) void k_scan_carry(ScanArgs a, const float* __r
     const float A2 = real ? a.A[d * a.states + n] * kLog2e : 0.f;
     const int64_t own = (s * a.channels + d) * a.states + n;
     float carry = first && real ? first[own] : 0.f;
-    constexpr int U = 8;
-    for (int64_t k0 = 0; k0 < chunks; k0 += U) {
-        float S[U], P[U];
+    // The loads of the next U chunks are in flight while the carry passes
+    // through U: the chain itself is one FMA per chunk.
+    constexpr int U = 16;
+    float S[U], P[U];
+    auto load = [&](int64_t k0) {
 #pragma unroll
         for (int j = 0; j < U; ++j) {
             const int64_t k = k0 + j < chunks ? k0 + j : chunks - 1;
             const int64_t slot = base + (REV ? chunks - 1 - k : k);
             S[j] = a.ws_state[slot * dn + i];
-            P[j] = exp2_hw(a.ws_dl[slot * a.channels + d] * A2);
+            P[j] = a.ws_dl[slot * a.channels + d];
         }
+    };
+    if (chunks > 0) load(0);
+    for (int64_t k0 = 0; k0 < chunks; k0 += U) {
+        float s[U], p[U];
+#pragma unroll
+        for (int j = 0; j < U; ++j) {
+            s[j] = S[j];
+            p[j] = exp2_hw(P[j] * A2);
+        }
+        if (k0 + U < chunks) load(k0 + U);
 #pragma unroll
         for (int j = 0; j < U; ++j) {
             if (k0 + j >= chunks) break;
             const int64_t slot = base + (REV ? chunks - 1 - k0 - j : k0 + j);
             a.ws_state[slot * dn + i] = carry;
-            carry = fma32(P[j], carry, S[j]);
+            carry = fma32(p[j], carry, s[j]);
         }
     }
     if (last && real) last[own] = carry;
@@ -500,11 +516,21 @@ __global__ __launch_bounds__(256) void k_selective_scan_step(ScanArgs a)
 }
 
 // ---------------------------------------------------------------------- launches
+constexpr int64_t kSeqWorkgroups = 384;
+
 template <typename T, int KS>
 hipError_t launch_scan_ks(const ScanArgs& a, int64_t groups, hipStream_t st)
 {
+    const int64_t slabs = groups * a.slabs;
+    // Whole sequences, one exponential per value instead of two, where their
+    // waves (4 a workgroup) give each of the 1024 SIMDs at least one and a half.
+    // Packed sequences' lengths are not known here.
+    if (a.q.starts == nullptr && a.q.seqs * slabs >= kSeqWorkgroups) {
+        k_selective_scan<T, KS, kSeq><<<dim3((unsigned)(a.q.seqs * slabs)), dim3(256), 0, st>>>(a);
+        return hipGetLastError();
+    }
     const int64_t slots = slot_count<kCh>(a.q.seqs, a.q.rows, a.q.starts != nullptr);
-    const unsigned grid = (unsigned)(slots * groups * a.slabs);
+    const unsigned grid = (unsigned)(slots * slabs);
     k_selective_scan<T, KS, kSum><<<dim3(grid), dim3(256), 0, st>>>(a);
     if (hipError_t e = hipGetLastError()) return e;
     if (hipError_t e = launch_scan_carry<4 * KS, false>(a, a.init, a.final, st)) return e;

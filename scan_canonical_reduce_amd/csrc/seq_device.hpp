@@ -141,6 +141,11 @@ __device__ __forceinline__ float silu_slope(float x, float q)
     return r == 0.f ? q : fma32(x, r, q);
 }
 
+// Keeps the compiler from putting off the computation of x: a sum that is only
+// read after a loop or a branch would be added up there, its terms all kept in
+// registers until then.
+__device__ __forceinline__ void pin(float& x) { asm volatile("" : "+v"(x)); }
+
 // ------------------------------------------------------------------- lane moves
 template <int CTRL>
 __device__ __forceinline__ float dpp(float v)

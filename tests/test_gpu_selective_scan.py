@@ -236,6 +236,55 @@ def test_bits_of_packing_batch_and_pieces(canon, dtype):
         assert torch.equal(call(canon, d), want)
 
 
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("rows,channels,groups,states", [(70, 40, 1, 16), (128, 17, 1, 7),
+                                                         (1, 40, 2, 16), (67, 30, 2, 3)])
+def test_many_sequences(canon, dtype, rows, channels, groups, states):
+    """Enough sequences that each is walked whole: the forward bits of each
+    alone (walked in chunks); gradients against the float64 form for some, the
+    parameters' against the packed call's (walked in chunks)."""
+    n = 460
+    d = cuda(inputs(dtype, [rows] * n, channels, groups, states, False, rows))
+    final = torch.empty_like(d["init"])
+    keep = canon.selective_scan_states(d["u"], states)
+    out = call(canon, d, final_state=final, states=keep)
+
+    def grads(d, keep):
+        return canon.selective_scan_grad(
+            d["dout"], d["u"], d["delta"], d["A"], d["B"], d["C"], keep, D=d["D"], z=d["z"],
+            delta_bias=d["bias"], delta_softplus=True, starts=d["starts"],
+            d_final_state=d["dfinal"])
+
+    got = grads(d, keep)
+    per_seq = ("u", "delta", "z", "B", "C", "init", "dout", "dfinal")
+    for i in (0, 201, 459):
+        one = {k: v[i:i + 1].contiguous() if k in per_seq else v for k, v in d.items()}
+        f = torch.empty_like(one["init"])
+        assert torch.equal(call(canon, one, final_state=f), out[i:i + 1])
+        assert torch.equal(f, final[i:i + 1])
+        host = {k: v.cpu() if torch.is_tensor(v) else v for k, v in one.items()}
+        names = ["u", "delta", "B", "C", "z", "init"]
+        o, h, e = reference(host, leaves=names)
+        want = torch.autograd.grad((o * e["dout"]).sum() + (h * e["dfinal"]).sum(),
+                                   [e[k] for k in names])
+        size = grad_sizes(host, True, names + ["A", "D", "bias"])
+        mine = [got.du, got.ddelta, got.dB, got.dC, got.dz, got.dinit_state]
+        for k, a, b in zip(names, mine, want):
+            seq_ref.close(a[i:i + 1], b, size[k], 2 * terms(rows) + channels, (i, k))
+    flat = ("u", "delta", "z", "B", "C", "dout")
+    packed = {k: v.flatten(0, 1) if k in flat else v for k, v in d.items()}
+    packed["starts"] = (torch.arange(n + 1) * rows).int().cuda()
+    keep = canon.selective_scan_states(packed["u"], states, packed["starts"])
+    assert torch.equal(call(canon, packed, states=keep), out.flatten(0, 1))
+    other = grads(packed, keep)
+    # each sum is within (2 terms + rows n) roundings of its absolute terms, of
+    # which a value of n random ones is at least a 1 / sqrt(n rows) part
+    bound = 2 * (2 * terms(rows) + 64) * seq_ref.U32 * (n * rows) ** 0.5
+    for k in ("dA", "dD", "ddelta_bias"):
+        a, b = getattr(got, k).double(), getattr(other, k).double()
+        assert float((a - b).abs().max() / b.abs().max()) <= bound, k
+
+
 @pytest.mark.parametrize("dtype", [F32, BF16, F16])
 @pytest.mark.parametrize("channels,groups,states", [(1, 1, 1), (40, 2, 16), (65, 1, 8),
                                                     (96, 3, 13), (20, 1, 3), (130, 1, 4)])
