@@ -32,9 +32,9 @@ inline int scan_ks(int64_t states) { return states <= 4 ? 1 : states <= 8 ? 2 : 
 constexpr int kSlab = 64;  // channels of a workgroup: 4 waves of 16
 constexpr int kSub = 16;   // rows between saved states, and of a register tile
 
-// Byte offsets within a 16-row tile are 32-bit: fewer than 16 rows of a pitch
-// below 2^26 elements, and a column below 2^24 (the host checks both).
-constexpr int64_t kMaxPitch = (int64_t)1 << 26;
+// Byte offsets within a 16-row tile are 32-bit (below 2^31): fewer than 16 rows
+// of a pitch below 2^24 elements, and a column below 2^24 (the host checks both).
+constexpr int64_t kMaxPitch = (int64_t)1 << 24;
 
 template <typename T>
 hipError_t launch_selective_scan(const ScanArgs& a, int64_t groups, hipStream_t st);

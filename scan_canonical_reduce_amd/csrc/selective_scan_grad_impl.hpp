@@ -27,29 +27,38 @@
 namespace canon {
 namespace seq {
 
-// Inputs of a 16-row tile of the backward passes, loaded as in Tile.
+// Inputs of a 16-row tile of the backward passes, loaded as in Tile, from the
+// last tile to the first.
 template <typename T, int KS, bool MAIN>
 struct GradTile {
     LaneRows<T> ru, rd, rz, rg;
     typename T::store_t u[4], dl[4], z[4], go[4];
     LaneBC<T, KS> B, C;
 
-    __device__ __forceinline__ void init(const ScanArgs& a, const Lane& l)
+    __device__ __forceinline__ void init(const ScanArgs& a, const Lane& l, int64_t s,
+                                         int64_t first)
     {
-        if (MAIN) ru.init(a.u, l);
-        rd.init(a.delta, l);
-        rz.init(a.z, l);
-        rg.init(a.dout, l);
+        if (MAIN) ru.init(a.u, l, s, a.q, first);
+        rd.init(a.delta, l, s, a.q, first);
+        rz.init(a.z, l, s, a.q, first);
+        rg.init(a.dout, l, s, a.q, first);
+        if (MAIN) B.init(a, a.B, l, s, first);
+        C.init(a, a.C, l, s, first);
     }
-    __device__ __forceinline__ void load(const ScanArgs& a, const Lane& l, int64_t s,
-                                         int64_t first, int32_t len, bool gate)
+    __device__ __forceinline__ void load(const ScanArgs& a, const Lane& l, int32_t len, bool gate)
     {
-        if (MAIN) ru.load(a.u, rows_ptr<T>(a.u, s, a.q, first), l, len, u);
-        rd.load(a.delta, rows_ptr<T>(a.delta, s, a.q, first), l, len, dl);
-        rg.load(a.dout, rows_ptr<T>(a.dout, s, a.q, first), l, len, go);
-        if (gate) rz.load(a.z, rows_ptr<T>(a.z, s, a.q, first), l, len, z);
-        C.load(a, a.C, rows_ptr<T>(a.C, s, a.q, first), l, len);
-        if (MAIN) B.load(a, a.B, rows_ptr<T>(a.B, s, a.q, first), l, len);
+        if (MAIN) ru.load(a.u, l, len, u);
+        rd.load(a.delta, l, len, dl);
+        rg.load(a.dout, l, len, go);
+        if (gate) rz.load(a.z, l, len, z);
+        C.load(a, l, len);
+        if (MAIN) B.load(a, l, len);
+        if (MAIN) ru.prev();
+        rd.prev();
+        rg.prev();
+        rz.prev();
+        C.prev();
+        if (MAIN) B.prev();
     }
 };
 
@@ -115,8 +124,8 @@ __global__ __launch_bounds__(256) void k_scan_back_sum(ScanArgs a)
     float sdl = 0.f;
     int sub = (ck.len - 1) / kSub;
     GradTile<T, KS, false> tile;
-    tile.init(a, l);
-    tile.load(a, l, ck.s, ck.span.first + ck.row + sub * kSub, ck.len - sub * kSub, gate);
+    tile.init(a, l, ck.s, ck.span.first + ck.row + sub * kSub);
+    tile.load(a, l, ck.len - sub * kSub, gate);
     for (; sub >= 0; --sub) {
         const int32_t len = ck.len - sub * kSub;
         float C[KS], dl[4], raw[4], dy[4];
@@ -136,7 +145,7 @@ __global__ __launch_bounds__(256) void k_scan_back_sum(ScanArgs a)
             ex[4 * r + l.q][l.c] = make_float2(valid ? dl[r] : 0.f, valid ? dy[r] : 0.f);
         }
         wave_lds_fence();
-        if (sub > 0) tile.load(a, l, ck.s, ck.span.first + ck.row + (sub - 1) * kSub, kSub, gate);
+        if (sub > 0) tile.load(a, l, kSub, gate);
         back_rows<KS, kSub - 1>(ex, l.c, A2, C, R, sdl);
         wave_lds_fence();
     }
@@ -230,12 +239,12 @@ struct LaneSum {
     }
 };
 
-// What a lane passes to the other lanes of its channel, per row.
-struct GradRow {
-    float dl, dlu, dy, u;  // u times dl; the gated gradient of y
-};
-struct GradRow2 {
-    float slope, w;  // d dl / d delta; dout silu'(z)
+// What a lane passes to the other lanes of its channel, per row, and keeps for
+// itself until the row's sums are there: three arrays of pairs.
+struct GradRows {
+    float2 a[kSub][16];  // dl, dl u
+    float2 b[kSub][16];  // dy (the gated gradient of y), u
+    float2 c[kSub][16];  // d dl / d delta, dout silu'(z)
 };
 
 template <int KS>
@@ -248,10 +257,10 @@ struct GradRegs {
 };
 
 template <int KS, int T>
-__device__ __forceinline__ void grad_forward(const GradRow (*ex)[16], int c, bool gate,
+__device__ __forceinline__ void grad_forward(const GradRows& ex, int c, bool gate,
                                              GradRegs<KS>& g, float (&y)[4])
 {
-    const float dl = ex[T][c].dl, dlu = ex[T][c].dlu;
+    const float dl = ex.a[T][c].x, dlu = ex.a[T][c].y;
     float hn[KS];
 #pragma unroll
     for (int i = 0; i < KS; ++i) {
@@ -265,25 +274,30 @@ __device__ __forceinline__ void grad_forward(const GradRow (*ex)[16], int c, boo
     if constexpr (T + 1 < kSub) grad_forward<KS, T + 1>(ex, c, gate, g, y);
 }
 
-template <int KS, int T, int STOP>
-__device__ __forceinline__ void grad_backward(const GradRow (*ex)[16], int c, GradRegs<KS>& g,
-                                              float (&th)[4], float (&dc)[4])
+// What a row's backward step needs of the other lanes.
+struct RowIn {
+    float2 a;  // dl, dl u
+    float dy;
+};
+
+template <int KS, int T>
+__device__ __forceinline__ void grad_row(const RowIn& x, int c, GradRegs<KS>& g, float& th,
+                                         float& dc)
 {
-    const float dl = ex[T][c].dl, dlu = ex[T][c].dlu, dy = ex[T][c].dy;
     float b[KS], s[KS], decay = 0.f;
-    bcast_fma<T, KS>(g.C, dy, g.R);  // lam
-    th[T & 3] = bcast_dot<T, KS>(g.B, g.R);
+    bcast_fma<T, KS>(g.C, x.dy, g.R);  // lam
+    th = bcast_dot<T, KS>(g.B, g.R);
 #pragma unroll
     for (int i = 0; i < KS; ++i) {
-        b[i] = g.R[i] * dlu;
-        s[i] = dy * g.h[T + 1][i];
+        b[i] = g.R[i] * x.a.y;
+        s[i] = x.dy * g.h[T + 1][i];
         g.R[i] *= g.a[T][i];
         const float d = g.R[i] * g.h[T][i];
-        g.dA[i] = fma32(dl, d, g.dA[i]);
+        g.dA[i] = fma32(x.a.x, d, g.dA[i]);
         pin(g.dA[i]);
         decay = i == 0 ? g.A2[i] * d : fma32(g.A2[i], d, decay);
     }
-    dc[T & 3] = decay;
+    dc = decay;
     g.sb.template add<T>(b, c);
     g.sc.template add<T>(s, c);
     if constexpr (T == 0) {
@@ -293,11 +307,36 @@ __device__ __forceinline__ void grad_backward(const GradRow (*ex)[16], int c, Gr
             g.dCt[i] = s[i];
         }
     }
-    if constexpr ((T & 3) == 0) {
-        g.th[T >> 2] = fold_quad(th[0], th[1], th[2], th[3]);
-        g.dc[T >> 2] = fold_quad(dc[0], dc[1], dc[2], dc[3]);
+}
+
+template <int R>
+__device__ __forceinline__ void read_rows(const GradRows& ex, int c, RowIn (&x)[4])
+{
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        x[k].a = ex.a[4 * R + k][c];
+        x[k].dy = ex.b[4 * R + k][c].x;
     }
-    if constexpr (T > STOP) grad_backward<KS, T - 1, STOP>(ex, c, g, th, dc);
+}
+
+// Rows 4 R + 3 .. 4 R, whose values x are in registers; the four before them
+// are read from LDS meanwhile.
+template <int KS, int R>
+__device__ __forceinline__ void grad_rows4(const GradRows& ex, int c, RowIn (&x)[4],
+                                           GradRegs<KS>& g)
+{
+    RowIn nx[4];
+    if constexpr (R > 0) read_rows<R - 1>(ex, c, nx);
+    float th[4], dc[4];
+    grad_row<KS, 4 * R + 3>(x[3], c, g, th[3], dc[3]);
+    grad_row<KS, 4 * R + 2>(x[2], c, g, th[2], dc[2]);
+    grad_row<KS, 4 * R + 1>(x[1], c, g, th[1], dc[1]);
+    grad_row<KS, 4 * R + 0>(x[0], c, g, th[0], dc[0]);
+    g.th[R] = fold_quad(th[0], th[1], th[2], th[3]);
+    g.dc[R] = fold_quad(dc[0], dc[1], dc[2], dc[3]);
+    if constexpr (R > 0)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) x[k] = nx[k];
 }
 
 // One chunk, given the carry R that enters it from later rows (a.ws_state,
@@ -307,8 +346,7 @@ template <typename T, int KS, bool SEQ>
 __global__ __launch_bounds__(256, 2) void k_selective_scan_grad(ScanArgs a)
 {
     constexpr int NP = 4 * KS;
-    __shared__ GradRow ex_all[4][kSub][16];
-    __shared__ GradRow2 ex2_all[4][kSub][16];
+    __shared__ GradRows ex_all[4];
     // two buffers: one barrier a tile; rows padded by 16 bytes against bank conflicts
     alignas(16) __shared__ float bc[2][4][kSub][2 * NP + 4];
     const int slabs = a.slabs * (a.channels / a.dg);
@@ -316,8 +354,7 @@ __global__ __launch_bounds__(256, 2) void k_selective_scan_grad(ScanArgs a)
     const int slab = (int)(blockIdx.x - id * slabs);
     const Lane l = lane_place(a, slab);
     const int w = uniform((int32_t)(threadIdx.x >> 6));
-    GradRow(*ex)[16] = ex_all[w];
-    GradRow2(*ex2)[16] = ex2_all[w];
+    GradRows& ex = ex_all[w];
     int64_t s, slot;  // the sequence, and the slot of its chunk (SEQ: the last one)
     int32_t lo, hi;   // rows of the sequence
     Span span;
@@ -370,10 +407,13 @@ __global__ __launch_bounds__(256, 2) void k_selective_scan_grad(ScanArgs a)
 
     int32_t row = (hi - 1) / kSub * kSub;
     GradTile<T, KS, true> tile;
-    tile.init(a, l);
-    tile.load(a, l, s, span.first + row, hi - row, gate);
+    tile.init(a, l, s, span.first + row);
+    tile.load(a, l, hi - row, gate);
+    LaneRows<T> o_du, o_dd, o_dz;
+    o_du.init(a.du, l, s, a.q, span.first + row);
+    o_dd.init(a.ddelta, l, s, a.q, span.first + row);
+    o_dz.init(a.dz, l, s, a.q, span.first + row);
     for (; row >= lo; row -= kSub) {
-        const int64_t first = span.first + row;
         const int32_t len = hi - row;
         const int sub = row / kSub % kSubs;
         {
@@ -401,8 +441,9 @@ __global__ __launch_bounds__(256, 2) void k_selective_scan_grad(ScanArgs a)
                 const bool valid = l.active && 4 * r + l.q < len;
                 const float u = valid ? T::load(tile.u[r]) : 0.f;
                 const float d = valid ? dl[r] : 0.f;
-                ex[4 * r + l.q][l.c] = GradRow{d, d * u, valid ? dy[r] : 0.f, u};
-                ex2[4 * r + l.q][l.c] = GradRow2{slope[r], gw[r]};
+                ex.a[4 * r + l.q][l.c] = make_float2(d, d * u);
+                ex.b[4 * r + l.q][l.c] = make_float2(valid ? dy[r] : 0.f, u);
+                ex.c[4 * r + l.q][l.c] = make_float2(slope[r], gw[r]);
             }
         }
         tile.B.get(g.B);
@@ -413,14 +454,18 @@ __global__ __launch_bounds__(256, 2) void k_selective_scan_grad(ScanArgs a)
             ld_states<KS>(a.cs + ((slot * kSubs + sub) * a.channels + l.ch) * NP + l.q * KS, g.h[0]);
         wave_lds_fence();
 
-        float t0[4], t1[4];
+        float t0[4];
         grad_forward<KS, 0>(ex, l.c, gate, g, t0);
-        grad_backward<KS, kSub - 1, 8>(ex, l.c, g, t0, t1);
+        RowIn x[4];
+        read_rows<3>(ex, l.c, x);
+        grad_rows4<KS, 3>(ex, l.c, x, g);
+        grad_rows4<KS, 2>(ex, l.c, x, g);
         // the next tile's loads, into the registers that half the rows have left
         __builtin_amdgcn_sched_barrier(0);
-        if (row > lo) tile.load(a, l, s, first - kSub, kSub, gate);
+        if (row > lo) tile.load(a, l, kSub, gate);
         __builtin_amdgcn_sched_barrier(0);
-        grad_backward<KS, 7, 0>(ex, l.c, g, t0, t1);
+        grad_rows4<KS, 1>(ex, l.c, x, g);
+        grad_rows4<KS, 0>(ex, l.c, x, g);
 
         float(*mine)[2 * NP + 4] = bc[sub & 1][w];
         st_states<KS>(&mine[brev][l.q * KS], g.dBt);
@@ -428,23 +473,20 @@ __global__ __launch_bounds__(256, 2) void k_selective_scan_grad(ScanArgs a)
         float du[4], dd[4], dz[4];
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-            const GradRow x = ex[4 * r + l.q][l.c];
-            const GradRow2 x2 = ex2[4 * r + l.q][l.c];
-            du[r] = fma32(g.th[r], x.dl, Dc * x.dy);
-            dd[r] = fma32(g.th[r], x.u, g.dc[r] * kLn2) * x2.slope;
-            dz[r] = x2.w * fma32(Dc, x.u, g.y[r]);
-            dD = fma32(x.dy, x.u, dD);
+            const float row_dl = ex.a[4 * r + l.q][l.c].x;
+            const float2 dy_u = ex.b[4 * r + l.q][l.c], sw = ex.c[4 * r + l.q][l.c];
+            du[r] = fma32(g.th[r], row_dl, Dc * dy_u.x);
+            dd[r] = fma32(g.th[r], dy_u.y, g.dc[r] * kLn2) * sw.x;
+            dz[r] = sw.y * fma32(Dc, dy_u.y, g.y[r]);
+            dD = fma32(dy_u.x, dy_u.y, dD);
             if (l.active && 4 * r + l.q < len) dbias += dd[r];
         }
-        LaneRows<T> ro;
-        ro.init(a.du, l);
-        ro.store(a.du, rows_ptr<T>(a.du, s, a.q, first), l, len, du);
-        ro.init(a.ddelta, l);
-        ro.store(a.ddelta, rows_ptr<T>(a.ddelta, s, a.q, first), l, len, dd);
-        if (gate) {
-            ro.init(a.dz, l);
-            ro.store(a.dz, rows_ptr<T>(a.dz, s, a.q, first), l, len, dz);
-        }
+        o_du.store(l, len, du);
+        o_du.prev();
+        o_dd.store(l, len, dd);
+        o_dd.prev();
+        if (gate) o_dz.store(l, len, dz);
+        o_dz.prev();
         __syncthreads();
         for (int i = threadIdx.x; i < kSub * 2 * NP; i += 256) {
             const int t = i / (2 * NP), n = i - t * 2 * NP;

@@ -63,50 +63,79 @@ __device__ __forceinline__ uint32_t tile_off(const canon_rows_t& r, uint32_t t, 
     return (t * (uint32_t)r.row + col) * (uint32_t)sizeof(typename T::store_t);
 }
 
-// Element `off` bytes behind a wave-uniform address.
-template <typename E>
-__device__ __forceinline__ const E* at_off(const E* base, uint32_t off)
+// Accesses relative to a wave-uniform address, which stays in scalar registers
+// with the offset of the row: base + row offset + the lane's offset, without
+// vector additions (the buffer form; its range is not limited).
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t tile_rsrc(const void* base)
 {
-    return reinterpret_cast<const E*>(reinterpret_cast<const char*>(base) + off);
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), 0, -1, 0x00020000);
 }
-template <typename E>
-__device__ __forceinline__ E* at_off(E* base, uint32_t off)
+__device__ __forceinline__ void rsrc_load(__amdgpu_buffer_rsrc_t b, uint32_t off, uint32_t row,
+                                          uint16_t& v)
 {
-    return reinterpret_cast<E*>(reinterpret_cast<char*>(base) + off);
+    v = __builtin_amdgcn_raw_buffer_load_b16(b, off, row, 0);
+}
+__device__ __forceinline__ void rsrc_load(__amdgpu_buffer_rsrc_t b, uint32_t off, uint32_t row,
+                                          float& v)
+{
+    v = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(b, off, row, 0));
+}
+__device__ __forceinline__ void rsrc_store(__amdgpu_buffer_rsrc_t b, uint32_t off, uint32_t row,
+                                           uint16_t v)
+{
+    __builtin_amdgcn_raw_buffer_store_b16(v, b, off, row, 0);
+}
+__device__ __forceinline__ void rsrc_store(__amdgpu_buffer_rsrc_t b, uint32_t off, uint32_t row,
+                                           float v)
+{
+    __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(v), b, off, row, 0);
 }
 
-// A lane's rows 4 r + q of one activation.
+// A lane's rows 4 r + q of one activation's current 16-row tile.
 template <typename T>
 struct LaneRows {
-    uint32_t off;  // row q
+    using E = typename T::store_t;
+    E* base;        // the tile's first row (wave-uniform)
+    uint32_t step;  // 4 rows, in bytes
+    uint32_t off;   // row q, this lane's channel
 
-    __device__ __forceinline__ void init(const canon_rows_t& r, const Lane& l)
+    __device__ __forceinline__ void init(const canon_rows_t& r, const Lane& l, int64_t s,
+                                         const Seqs& q, int64_t first)
     {
+        base = rows_ptr<T>(r, s, q, first);
+        step = tile_off<T>(r, 4, 0);
         off = tile_off<T>(r, l.q, l.ch);
     }
+    __device__ __forceinline__ void next() { base += 4 * (uint64_t)step / sizeof(E); }
+    __device__ __forceinline__ void prev() { base -= 4 * (uint64_t)step / sizeof(E); }
     // rows past the sequence's end are read as its last row and not used
-    __device__ __forceinline__ void load(const canon_rows_t& a, const typename T::store_t* base,
-                                         const Lane& l, int32_t len,
-                                         typename T::store_t (&v)[4]) const
+    __device__ __forceinline__ void load(const canon_rows_t& a, const Lane& l, int32_t len,
+                                         E (&v)[4]) const
     {
+        const __amdgpu_buffer_rsrc_t b = tile_rsrc(base);
         if (len >= kSub) {
 #pragma unroll
-            for (int r = 0; r < 4; ++r) v[r] = *at_off(base + 4 * r * a.row, off);
+            for (int r = 0; r < 4; ++r) rsrc_load(b, off, r * step, v[r]);
         } else {
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
                 const int t = 4 * r + l.q < len ? 4 * r + l.q : len - 1;
-                v[r] = *at_off(base, tile_off<T>(a, t, l.ch));
+                rsrc_load(b, tile_off<T>(a, t, l.ch), 0, v[r]);
             }
         }
     }
-    __device__ __forceinline__ void store(const canon_rows_t& a, typename T::store_t* base,
-                                          const Lane& l, int32_t len, const float (&v)[4]) const
+    __device__ __forceinline__ void store(const Lane& l, int32_t len, const float (&v)[4]) const
     {
         if (!l.active) return;
+        const __amdgpu_buffer_rsrc_t b = tile_rsrc(base);
+        if (len >= kSub) {
 #pragma unroll
-        for (int r = 0; r < 4; ++r)
-            if (4 * r + l.q < len) st<T>(at_off(base + 4 * r * a.row, off), v[r]);
+            for (int r = 0; r < 4; ++r) rsrc_store(b, off, r * step, T::round(v[r]));
+        } else {
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+                if (4 * r + l.q < len) rsrc_store(b, off, r * step, T::round(v[r]));
+        }
     }
 };
 
@@ -114,23 +143,32 @@ struct LaneRows {
 // for rows past the end).
 template <typename T, int KS>
 struct LaneBC {
+    using E = typename T::store_t;
+    E* base;
+    int64_t step;  // 16 rows
+    uint32_t off;
     Vec<T, KS> x;
 
-    __device__ __forceinline__ void load(const ScanArgs& a, const canon_rows_t& r,
-                                         const typename T::store_t* base, const Lane& l,
-                                         int32_t len)
+    __device__ __forceinline__ void init(const ScanArgs& a, const canon_rows_t& r, const Lane& l,
+                                         int64_t s, int64_t first)
     {
-        const uint32_t t = l.c < len ? l.c : len - 1;
-        const typename T::store_t* p =
-            at_off(base, tile_off<T>(r, t, l.g * a.states + l.q * KS));
+        base = rows_ptr<T>(r, s, a.q, first);
+        step = kSub * r.row;
+        off = tile_off<T>(r, l.c, l.g * a.states + l.q * KS);
+    }
+    __device__ __forceinline__ void next() { base += step; }
+    __device__ __forceinline__ void prev() { base -= step; }
+    __device__ __forceinline__ void load(const ScanArgs& a, const Lane& l, int32_t len)
+    {
         x = Vec<T, KS>{};
-        if (l.c >= len) return;
+        if (l.c >= len || l.q * KS >= a.states) return;
         if (a.bc_vec) {
-            if (l.q * KS < a.states) x = ld_vec<T, KS>(p);
+            x = ld_vec<T, KS>(reinterpret_cast<const E*>(reinterpret_cast<const char*>(base) + off));
         } else {
+            const __amdgpu_buffer_rsrc_t b = tile_rsrc(base);
 #pragma unroll
             for (int i = 0; i < KS; ++i)
-                if (l.q * KS + i < a.states) x.e[i] = p[i];
+                if (l.q * KS + i < a.states) rsrc_load(b, off, i * sizeof(E), x.e[i]);
         }
     }
     __device__ __forceinline__ void get(float (&v)[KS]) const
@@ -147,20 +185,29 @@ struct Tile {
     typename T::store_t u[4], dl[4], z[4];
     LaneBC<T, KS> B, C;
 
-    __device__ __forceinline__ void init(const ScanArgs& a, const Lane& l)
+    __device__ __forceinline__ void init(const ScanArgs& a, const Lane& l, int64_t s,
+                                         int64_t first)
     {
-        ru.init(a.u, l);
-        rd.init(a.delta, l);
-        if (EMIT) rz.init(a.z, l);
+        ru.init(a.u, l, s, a.q, first);
+        rd.init(a.delta, l, s, a.q, first);
+        B.init(a, a.B, l, s, first);
+        if (!EMIT) return;
+        rz.init(a.z, l, s, a.q, first);
+        C.init(a, a.C, l, s, first);
     }
-    __device__ __forceinline__ void load(const ScanArgs& a, const Lane& l, int64_t s,
-                                         int64_t first, int32_t len, bool gate)
+    __device__ __forceinline__ void load(const ScanArgs& a, const Lane& l, int32_t len, bool gate)
     {
-        ru.load(a.u, rows_ptr<T>(a.u, s, a.q, first), l, len, u);
-        rd.load(a.delta, rows_ptr<T>(a.delta, s, a.q, first), l, len, dl);
-        if (EMIT && gate) rz.load(a.z, rows_ptr<T>(a.z, s, a.q, first), l, len, z);
-        B.load(a, a.B, rows_ptr<T>(a.B, s, a.q, first), l, len);
-        if (EMIT) C.load(a, a.C, rows_ptr<T>(a.C, s, a.q, first), l, len);
+        ru.load(a.u, l, len, u);
+        rd.load(a.delta, l, len, dl);
+        if (EMIT && gate) rz.load(a.z, l, len, z);
+        B.load(a, l, len);
+        if (EMIT) C.load(a, l, len);
+        ru.next();
+        rd.next();
+        B.next();
+        if (!EMIT) return;
+        rz.next();
+        C.next();
     }
 };
 
@@ -204,13 +251,12 @@ __device__ __forceinline__ float bcast_dot(const float (&b)[KS], const float (&x
     return y;
 }
 
-// One step of the recurrence for row T of the tile.
+// One step of the recurrence for row T of the tile; x = dl, dl u.
 template <int KS, int MODE, int T>
-__device__ __forceinline__ float scan_row(const float2 (*ex)[16], int c, const float (&A2)[KS],
+__device__ __forceinline__ float scan_row(const float2 x, const float (&A2)[KS],
                                           const float (&B)[KS], const float (&C)[KS],
                                           float (&h)[KS], float (&S)[KS], float& sdl)
 {
-    const float2 x = ex[T][c];  // dl, dl u
     if (MODE != kEmit) sdl += x.x;
 #pragma unroll
     for (int i = 0; i < KS; ++i) {
@@ -224,17 +270,26 @@ __device__ __forceinline__ float scan_row(const float2 (*ex)[16], int c, const f
     return MODE != kSum ? bcast_dot<T, KS>(C, h) : 0.f;
 }
 
+// Rows 4 R .. 4 R + 3 of the tile, whose values x are in registers; the next
+// four are read from LDS meanwhile.
 template <int KS, int MODE, int R>
-__device__ __forceinline__ void scan_rows4(const float2 (*ex)[16], int c, const float (&A2)[KS],
-                                           const float (&B)[KS], const float (&C)[KS],
-                                           float (&h)[KS], float (&S)[KS], float& sdl,
-                                           float (&yr)[4])
+__device__ __forceinline__ void scan_rows4(const float2 (*ex)[16], int c, float2 (&x)[4],
+                                           const float (&A2)[KS], const float (&B)[KS],
+                                           const float (&C)[KS], float (&h)[KS], float (&S)[KS],
+                                           float& sdl, float (&yr)[4])
 {
-    const float y0 = scan_row<KS, MODE, 4 * R + 0>(ex, c, A2, B, C, h, S, sdl);
-    const float y1 = scan_row<KS, MODE, 4 * R + 1>(ex, c, A2, B, C, h, S, sdl);
-    const float y2 = scan_row<KS, MODE, 4 * R + 2>(ex, c, A2, B, C, h, S, sdl);
-    const float y3 = scan_row<KS, MODE, 4 * R + 3>(ex, c, A2, B, C, h, S, sdl);
+    float2 nx[4];
+    if constexpr (R < 3)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) nx[k] = ex[4 * R + 4 + k][c];
+    const float y0 = scan_row<KS, MODE, 4 * R + 0>(x[0], A2, B, C, h, S, sdl);
+    const float y1 = scan_row<KS, MODE, 4 * R + 1>(x[1], A2, B, C, h, S, sdl);
+    const float y2 = scan_row<KS, MODE, 4 * R + 2>(x[2], A2, B, C, h, S, sdl);
+    const float y3 = scan_row<KS, MODE, 4 * R + 3>(x[3], A2, B, C, h, S, sdl);
     if (MODE != kSum) yr[R] = fold_quad(y0, y1, y2, y3);
+    if constexpr (R < 3)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) x[k] = nx[k];
 }
 
 template <int KS>
@@ -308,14 +363,13 @@ __global__ __launch_bounds__(256, 4) void k_selective_scan(ScanArgs a)
     for (int i = 0; i < KS; ++i) H[i] = h[i];
 
     Tile<T, KS, MODE != kSum> tile;
-    tile.init(a, l);
+    tile.init(a, l, s, span.first + lo);
     LaneRows<T> ro;
-    ro.init(a.out, l);
-    if (lo < hi) tile.load(a, l, s, span.first + lo, hi - lo, gate);
+    ro.init(a.out, l, s, a.q, span.first + lo);
+    if (lo < hi) tile.load(a, l, hi - lo, gate);
     float sdl = 0.f;
 #pragma unroll 1
     for (int32_t row = lo; row < hi; row += kSub) {
-        const int64_t first = span.first + row;
         const int32_t len = hi - row;
         const int sub = row / kSub % kSubs;
         float u[4], dl[4], raw[4], gz[4], B[KS], C[KS];
@@ -339,13 +393,16 @@ __global__ __launch_bounds__(256, 4) void k_selective_scan(ScanArgs a)
         if (MODE != kSum && a.cs && l.active)
             st_states<KS>(a.cs + ((slot * kSubs + sub) * a.channels + l.ch) * NP + l.q * KS, h);
         // the next tile's loads, in flight while this one is computed
-        if (len > kSub) tile.load(a, l, s, first + kSub, len - kSub, gate);
+        if (len > kSub) tile.load(a, l, len - kSub, gate);
 
         float y[4];
-        scan_rows4<KS, MODE, 0>(ex, l.c, A2, B, C, h, S, sdl, y);
-        scan_rows4<KS, MODE, 1>(ex, l.c, A2, B, C, h, S, sdl, y);
-        scan_rows4<KS, MODE, 2>(ex, l.c, A2, B, C, h, S, sdl, y);
-        scan_rows4<KS, MODE, 3>(ex, l.c, A2, B, C, h, S, sdl, y);
+        float2 x[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) x[k] = ex[k][l.c];
+        scan_rows4<KS, MODE, 0>(ex, l.c, x, A2, B, C, h, S, sdl, y);
+        scan_rows4<KS, MODE, 1>(ex, l.c, x, A2, B, C, h, S, sdl, y);
+        scan_rows4<KS, MODE, 2>(ex, l.c, x, A2, B, C, h, S, sdl, y);
+        scan_rows4<KS, MODE, 3>(ex, l.c, x, A2, B, C, h, S, sdl, y);
         wave_lds_fence();
         if (MODE != kSum) {
 #pragma unroll
@@ -353,7 +410,8 @@ __global__ __launch_bounds__(256, 4) void k_selective_scan(ScanArgs a)
             if (gate)
 #pragma unroll
                 for (int r = 0; r < 4; ++r) y[r] *= gz[r];
-            ro.store(a.out, rows_ptr<T>(a.out, s, a.q, first), l, len, y);
+            ro.store(l, len, y);
+            ro.next();
         }
         if (MODE == kSeq && (sub == kSubs - 1 || len <= kSub)) {
 #pragma unroll
@@ -468,8 +526,10 @@ __global__ __launch_bounds__(256) void k_selective_scan_step(ScanArgs a)
     l.q = q;
     l.g = g;
     LaneBC<T, KS> xb, xc;
-    xb.load(a, a.B, static_cast<typename T::store_t*>(a.B.p) + s * a.B.seq, l, 1);
-    xc.load(a, a.C, static_cast<typename T::store_t*>(a.C.p) + s * a.C.seq, l, 1);
+    xb.init(a, a.B, l, s, 0);
+    xc.init(a, a.C, l, s, 0);
+    xb.load(a, l, 1);
+    xc.load(a, l, 1);
     float B[KS], C[KS];
     xb.get(B);
     xc.get(C);
