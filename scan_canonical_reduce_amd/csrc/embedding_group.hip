@@ -86,7 +86,7 @@ __global__ __launch_bounds__(1024) void k_embed_group(EmbedGradArgs a, int R)
         }
     const bool is_row = lo + tid < hi && tid < R;
     const int32_t chunks = (n + kEmbedChunk - 1) / kEmbedChunk;
-    const int32_t items = !is_row ? 0 : chunks > 0 ? chunks : a.accumulate ? 0 : 1;
+    const int32_t items = is_row ? chunks : 0;
     const bool is_long = is_row && n > kEmbedChunk;
     uint64_t both;
     const uint64_t pos = block_exclusive((uint64_t)(uint32_t)n | (uint64_t)(uint32_t)items << 32,
@@ -111,8 +111,8 @@ __global__ __launch_bounds__(1024) void k_embed_group(EmbedGradArgs a, int R)
         a.before[b] = (int32_t)all_below;
     }
     __syncthreads();
-    // the list of work, from the tokens and rows before this group on
-    int64_t* list = a.items + (int64_t)all_below + lo;
+    // the list of work, from the tokens before this group on
+    int64_t* list = a.items + (int64_t)all_below;
     for (int32_t i = tid; i < n_items; i += 1024) {
         int r0 = 0, r1 = 1023;  // the last id with first_item <= i
         while (r0 < r1) {

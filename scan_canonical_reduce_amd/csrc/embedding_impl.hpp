@@ -10,14 +10,16 @@
 //     the ids below its range, which place it in the order; once to place its
 //     tokens, each wave its own stretch, in token order.  No workgroup needs
 //     another's result, so there is one launch and no wait.  It also lists the
-//     work: (row, chunk of 64 occurrences), one entry for a row no token names
-//     when that row is to be written as zero.
+//     work: (row, chunk of 64 occurrences).
 //  2. k_embed_sum: a wave takes one entry and a slab of 64 vectors of columns,
 //     and adds the rows of dout in the order of the pairwise tree (8 rows in
 //     flight, a binary counter of complete subtrees above them).  An aligned
 //     chunk of a sequence is a subtree of its pairwise tree, so the rows of an
-//     id with more than 64 occurrences leave one partial value per chunk.
-//  3. k_embed_finish: the tree over the partial values of those.
+//     id with more than 64 occurrences leave one partial value per chunk.  The
+//     rows that no token names are set to zero by the same waves, 64 rows'
+//     offsets at a time; every other workgroup does that first, so that the
+//     writes overlap the others' gathers.
+//  3. k_embed_finish: the tree over the partial values.
 #pragma once
 
 #include "embedding.hpp"
@@ -152,15 +154,9 @@ template <typename T, typename G, int V>
 __device__ __forceinline__ void sum_entry(const EmbedGradArgs& a, int64_t v, int64_t c,
                                           int64_t col, int lane)
 {
-    const int32_t off = a.offset[v], n = a.offset[v + 1] - off;
+    const int32_t off = uniform(a.offset[v]), n = uniform(a.offset[v + 1]) - off;
     const bool in = col < a.width;
     float acc[V];
-#pragma unroll
-    for (int j = 0; j < V; ++j) acc[j] = 0.f;
-    if (n == 0) {
-        if (in && !a.accumulate) store_grad<G, V>(a, v, col, acc);
-        return;
-    }
     const int64_t p0 = off + c * kEmbedChunk;
     const int m = n - c * kEmbedChunk < kEmbedChunk ? (int)(n - c * kEmbedChunk) : kEmbedChunk;
     const int32_t mine = a.order[p0 + (lane < m ? lane : 0)];
@@ -226,37 +222,62 @@ __device__ __forceinline__ void sum_entry(const EmbedGradArgs& a, int64_t v, int
     for (int j = 0; j < V; ++j) part[j] = acc[j];
 }
 
+// Zero rows for ids without tokens: a wave takes 64 rows at a time.
+template <typename G, int V>
+__device__ __forceinline__ void zero_rows(const EmbedGradArgs& a, int64_t wave, int64_t waves,
+                                          int lane)
+{
+    for (int64_t v0 = wave * 64; v0 < a.rows; v0 += waves * 64) {
+        const int64_t v = v0 + lane;
+        const bool none = v < a.rows && a.offset[v] == a.offset[v + 1];
+        uint64_t left = __ballot(none);
+        while (left) {
+            const int64_t row = v0 + __builtin_ctzll(left);
+            left &= left - 1;
+            typename G::store_t* p = static_cast<typename G::store_t*>(a.dw) + row * a.ld_dw;
+            const float zero[V] = {};
+            for (int64_t c = lane * V; c < a.width; c += 64 * V) st_vec<G, V>(p + c, zero);
+        }
+    }
+}
+
 template <typename T, typename G, int V>
-__global__ __launch_bounds__(256) void k_embed_sum(EmbedGradArgs a, int64_t groups, int64_t ids)
+__global__ __launch_bounds__(256, 4) void k_embed_sum(EmbedGradArgs a, int64_t groups)
 {
     __shared__ int32_t prefix[kGroupsInLds + 1];
     const int lane = threadIdx.x & 63;
-    const int64_t wave = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6), waves = gridDim.x * 4ll;
+    const int64_t wave = (int64_t)blockIdx.x * 4 + uniform((int32_t)(threadIdx.x >> 6));
+    const int64_t waves = gridDim.x * 4ll;
     const int64_t slabs = (a.width + 64 * V - 1) / (64 * V);
+    // 16-byte stores of the gradient's type
+    constexpr int VZ = V == 1 ? 1 : 16 / (int)sizeof(typename G::store_t);
+    const bool zero = !a.accumulate;
+    if (zero && (blockIdx.x & 1)) zero_rows<G, VZ>(a, wave, waves, lane);
     for (int64_t g0 = 0; g0 < groups; g0 += kGroupsInLds) {
         const int64_t total = group_prefix(a.n_items, g0, groups, prefix);
         for (int64_t i = wave; i < total * slabs; i += waves) {
             const int32_t e = (int32_t)(i / slabs);
             const int64_t slab = i - e * slabs;
             const int k = find_group(prefix, e);
-            const int64_t g = g0 + k;
-            const int64_t item = a.items[(int64_t)a.before[g] + g * ids + (e - prefix[k])];
+            const int64_t item = uniform(a.items[(int64_t)a.before[g0 + k] + (e - prefix[k])]);
             sum_entry<T, G, V>(a, item & 0xffffffff, item >> 32, slab * 64 * V + lane * V, lane);
         }
     }
+    if (zero && !(blockIdx.x & 1)) zero_rows<G, VZ>(a, wave, waves, lane);
 }
 
 // Rows with more than 64 occurrences: the pairwise tree over the partial
 // values, an aligned power-of-two range of them per wave, then over the 16
-// waves.
+// waves.  A lane holds four neighbouring columns (the partial values' rows are
+// padded to that).
 template <typename G>
 __global__ __launch_bounds__(1024) void k_embed_finish(EmbedGradArgs a, int64_t groups)
 {
     __shared__ int32_t prefix[kGroupsInLds + 1];
     __shared__ int32_t wsum[16];
-    __shared__ float waves[16][64];
-    const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
-    const int64_t slabs = (a.width + 63) / 64;
+    __shared__ float4 waves[16][64];
+    const int lane = threadIdx.x & 63, w = uniform((int32_t)(threadIdx.x >> 6));
+    const int64_t slabs = (a.width + 255) / 256;
     for (int64_t g0 = 0; g0 < groups; g0 += kGroupsInLds) {
         const int32_t c = g0 + threadIdx.x < groups ? a.n_long[g0 + threadIdx.x] : 0;
         int32_t run = c;
@@ -276,59 +297,68 @@ __global__ __launch_bounds__(1024) void k_embed_finish(EmbedGradArgs a, int64_t 
         const int64_t total = prefix[kGroupsInLds];
         for (int64_t i = blockIdx.x; i < total * slabs; i += gridDim.x) {
             const int32_t e = (int32_t)(i / slabs);
-            const int64_t col = (i - e * slabs) * 64 + lane;
+            const int64_t col = (i - e * slabs) * 256 + lane * 4;
+            const bool in = col < a.width;
             const int k = find_group(prefix, e);
-            const int64_t v = a.longs[a.before[g0 + k] / (kEmbedChunk + 1) + (e - prefix[k])];
-            const int32_t off = a.offset[v], n = a.offset[v + 1] - off;
-            const int64_t m = (n + kEmbedChunk - 1) / kEmbedChunk;
-            int64_t range = 1;  // partial values per wave
+            const int32_t v = uniform(a.longs[a.before[g0 + k] / (kEmbedChunk + 1) + (e - prefix[k])]);
+            const int32_t off = uniform(a.offset[v]), n = uniform(a.offset[v + 1]) - off;
+            const int32_t m = (n + kEmbedChunk - 1) / kEmbedChunk;
+            int32_t range = 1;  // partial values per wave
             while (range * 16 < m) range *= 2;
-            const int64_t lo = w * range, hi = lo + range < m ? lo + range : m;
-            constexpr int kLevels = 26;  // 2^31 / 64 partial values
-            float st[kLevels];
-            int64_t count = 0;
-            for (int64_t b = lo; b < hi; b += 8) {
-                float x[8][1];
+            const int32_t lo = w * range, hi = lo + range < m ? lo + range : m;
+            const float* part = a.part + off / kEmbedChunk * a.ld_part + (in ? col : 0);
+            const float* last =
+                a.part_last + (off + (m - 1) * kEmbedChunk) / kEmbedChunk * a.ld_part + (in ? col : 0);
+            constexpr int kLevels = 18;  // 2^30 / 64 / 16 / 8 batches
+            float st[kLevels][4];
+            int32_t count = 0;
+            for (int32_t b = lo; b < hi; b += 8) {
+                float x[8][4];
 #pragma unroll
                 for (int r = 0; r < 8; ++r) {
-                    const int64_t j = b + r;
-                    x[r][0] = -0.f;
-                    if (j < hi && col < a.width)
-                        x[r][0] = j == m - 1
-                                      ? a.part_last[(off + j * kEmbedChunk) / kEmbedChunk * a.ld_part + col]
-                                      : a.part[(off / kEmbedChunk + j) * a.ld_part + col];
+                    const int32_t j = b + r;
+                    float4 p = make_float4(-0.f, -0.f, -0.f, -0.f);
+                    if (j < hi)
+                        p = *reinterpret_cast<const float4*>(j == m - 1 ? last : part + j * a.ld_part);
+                    x[r][0] = p.x, x[r][1] = p.y, x[r][2] = p.z, x[r][3] = p.w;
                 }
-                tree8<1>(x);
-                float t = x[0][0];
+                tree8<4>(x);
                 bool done = false;
 #pragma unroll
                 for (int lev = 0; lev < kLevels; ++lev) {
                     if (done) continue;
-                    if (count >> lev & 1) {
-                        t = st[lev] + t;
-                    } else {
-                        st[lev] = t;
-                        done = true;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        if (count >> lev & 1)
+                            x[0][j] = st[lev][j] + x[0][j];
+                        else
+                            st[lev][j] = x[0][j];
                     }
+                    done = !(count >> lev & 1);
                 }
                 ++count;
             }
-            float acc = -0.f;
+            float acc[4] = {-0.f, -0.f, -0.f, -0.f};
 #pragma unroll
             for (int lev = 0; lev < kLevels; ++lev)
-                if (count >> lev & 1) acc = st[lev] + acc;
-            waves[w][lane] = acc;
-            __syncthreads();
-            if (w == 0 && col < a.width) {
-                float x[16];
+                if (count >> lev & 1)
 #pragma unroll
-                for (int j = 0; j < 16; ++j) x[j] = waves[j][lane];
+                    for (int j = 0; j < 4; ++j) acc[j] = st[lev][j] + acc[j];
+            waves[w][lane] = make_float4(acc[0], acc[1], acc[2], acc[3]);
+            __syncthreads();
+            // wave w finishes columns 16 w .. of the 256, one lane each
+            if (lane < 16) {
+                const int x = w * 16 + lane;
+                const int64_t at = (i - e * slabs) * 256 + x;
+                float s[16];
+#pragma unroll
+                for (int j = 0; j < 16; ++j) s[j] = reinterpret_cast<const float*>(waves[j])[x];
 #pragma unroll
                 for (int d = 1; d < 16; d *= 2)
 #pragma unroll
-                    for (int j = 0; j < 16; j += 2 * d) x[j] += x[j + d];
-                float s[1] = {x[0]};
-                store_grad<G, 1>(a, v, col, s);
+                    for (int j = 0; j < 16; j += 2 * d) s[j] += s[j + d];
+                const float one[1] = {s[0]};
+                if (at < a.width) store_grad<G, 1>(a, v, at, one);
             }
             __syncthreads();
         }
@@ -353,22 +383,22 @@ template <typename T, typename G>
 hipError_t launch_embedding_grad(const EmbedGradArgs& a, hipStream_t st)
 {
     constexpr int V = 16 / (int)sizeof(typename T::store_t);
-    const int64_t groups = id_groups(a.rows), ids = ids_per_group(a.rows);
+    const int64_t groups = id_groups(a.rows);
     if (hipError_t e = launch_embedding_group(a, st)) return e;
-    const int64_t cap = (int64_t)device_cus() * 8;
+    // four workgroups fit a compute unit (k_embed_sum's launch bound)
+    const int64_t cus = (int64_t)device_cus(), cap = cus * 4;
     const int64_t slabs = (a.width + 64 * (a.vec ? V : 1) - 1) / (64 * (a.vec ? V : 1));
-    const int64_t want = ((a.tokens + a.rows) * slabs + 3) / 4;
-    const dim3 grid((unsigned)capped_grid(want < cap ? want : cap));
+    const int64_t want = (a.tokens * slabs + (a.accumulate ? 0 : a.rows) + 3) / 4;
+    const dim3 grid((unsigned)capped_grid(want < 1 ? 1 : want < cap ? want : cap));
     if (a.vec)
-        k_embed_sum<T, G, V><<<grid, dim3(256), 0, st>>>(a, groups, ids);
+        k_embed_sum<T, G, V><<<grid, dim3(256), 0, st>>>(a, groups);
     else
-        k_embed_sum<T, G, 1><<<grid, dim3(256), 0, st>>>(a, groups, ids);
+        k_embed_sum<T, G, 1><<<grid, dim3(256), 0, st>>>(a, groups);
     if (hipError_t e = hipGetLastError()) return e;
-    if (a.tokens <= kEmbedChunk) return hipSuccess;
-    const int64_t most = a.tokens / (kEmbedChunk + 1) * ((a.width + 63) / 64);
-    const int64_t cus = (int64_t)device_cus();
-    k_embed_finish<G><<<dim3((unsigned)capped_grid(most < cus ? (most ? most : 1) : cus)), dim3(1024),
-                        0, st>>>(a, groups);
+    const int64_t most = a.tokens / (kEmbedChunk + 1) * ((a.width + 255) / 256);
+    if (most == 0) return hipSuccess;  // too few tokens for a row with partial values
+    k_embed_finish<G><<<dim3((unsigned)capped_grid(most < cus ? most : cus)), dim3(1024), 0,
+                        st>>>(a, groups);
     return hipGetLastError();
 }
 

@@ -440,52 +440,62 @@ __global__ __launch_bounds__(256, 4) void k_selective_scan(ScanArgs a)
 // The states between chunks, one thread per (sequence, channel, state):
 // carry <- exp(A sum dl) carry + S over the chunks in order, each chunk's S in
 // the workspace replaced by the carry that enters it.  REV: from the last
-// chunk to the first, for the gradient (S: the chunk's backward fold).
+// chunk to the first, for the gradient (S: the chunk's backward fold).  The
+// chain is one FMA per chunk; the loads of the next chunks are in flight while
+// the carry passes through these.  Workgroups of one wave, so that few states
+// spread over all compute units.
 template <int NP, bool REV>
-__global__ __launch_bounds__(256) void k_scan_carry(ScanArgs a, const float* __restrict__ first,
-                                                    float* __restrict__ last)
+__global__ __launch_bounds__(64) void k_scan_carry(ScanArgs a, const float* __restrict__ first,
+                                                   float* __restrict__ last)
 {
     const int64_t dn = (int64_t)a.channels * NP;
-    const int64_t per = (dn + 255) / 256;
+    const int64_t per = (dn + 63) / 64;
     const int64_t s = blockIdx.x / per;
-    const int64_t i = (blockIdx.x - s * per) * 256 + threadIdx.x;
+    const int64_t i = (blockIdx.x - s * per) * 64 + threadIdx.x;
     if (i >= dn) return;
     const int64_t d = i / NP;
     const int n = (int)(i - d * NP);
     const bool real = n < a.states;
-    const Span span = seq_span(a.q, s);
-    const int64_t chunks = (span.len + kCh - 1) / kCh, base = slot_base<kCh>(a.q, s);
+    const Span span = uniform(seq_span(a.q, s));
+    const int64_t base = uniform(slot_base<kCh>(a.q, s));
+    const int32_t chunks = (span.len + kCh - 1) / kCh;
     const float A2 = real ? a.A[d * a.states + n] * kLog2e : 0.f;
     const int64_t own = (s * a.channels + d) * a.states + n;
     float carry = first && real ? first[own] : 0.f;
-    // The loads of the next U chunks are in flight while the carry passes
-    // through U: the chain itself is one FMA per chunk.
     constexpr int U = 16;
-    float S[U], P[U];
-    auto load = [&](int64_t k0) {
+    const int64_t step = REV ? -1 : 1;
+    const int64_t at = base + (REV ? chunks - 1 : 0);
+    float* state = a.ws_state + at * dn + i;  // the next chunk to store
+    const float* ps = state;                  // the next to load
+    const float* pd = a.ws_dl + at * a.channels + d;
+    float S[2][U], P[2][U];
+    auto load = [&](int b, int32_t k0) {
 #pragma unroll
         for (int j = 0; j < U; ++j) {
-            const int64_t k = k0 + j < chunks ? k0 + j : chunks - 1;
-            const int64_t slot = base + (REV ? chunks - 1 - k : k);
-            S[j] = a.ws_state[slot * dn + i];
-            P[j] = a.ws_dl[slot * a.channels + d];
+            S[b][j] = *ps;
+            P[b][j] = *pd;
+            if (k0 + j + 1 < chunks) {
+                ps += step * dn;
+                pd += step * a.channels;
+            }
         }
     };
-    if (chunks > 0) load(0);
-    for (int64_t k0 = 0; k0 < chunks; k0 += U) {
-        float s[U], p[U];
-#pragma unroll
-        for (int j = 0; j < U; ++j) {
-            s[j] = S[j];
-            p[j] = exp2_hw(P[j] * A2);
-        }
-        if (k0 + U < chunks) load(k0 + U);
+    auto pass = [&](int b, int32_t k0) {
 #pragma unroll
         for (int j = 0; j < U; ++j) {
             if (k0 + j >= chunks) break;
-            const int64_t slot = base + (REV ? chunks - 1 - k0 - j : k0 + j);
-            a.ws_state[slot * dn + i] = carry;
-            carry = fma32(p[j], carry, s[j]);
+            *state = carry;
+            state += step * dn;
+            carry = fma32(exp2_hw(P[b][j] * A2), carry, S[b][j]);
+        }
+    };
+    if (chunks > 0) {
+        load(0, 0);
+        for (int32_t k0 = 0; k0 < chunks; k0 += 2 * U) {
+            if (k0 + U < chunks) load(1, k0 + U);
+            pass(0, k0);
+            if (k0 + 2 * U < chunks) load(0, k0 + 2 * U);
+            pass(1, k0 + U);
         }
     }
     if (last && real) last[own] = carry;
@@ -494,9 +504,9 @@ __global__ __launch_bounds__(256) void k_scan_carry(ScanArgs a, const float* __r
 template <int NP, bool REV>
 hipError_t launch_scan_carry(const ScanArgs& a, const float* first, float* last, hipStream_t st)
 {
-    const int64_t per = ((int64_t)a.channels * NP + 255) / 256;
+    const int64_t per = ((int64_t)a.channels * NP + 63) / 64;
     if (a.q.seqs * per == 0) return hipSuccess;
-    k_scan_carry<NP, REV><<<dim3((unsigned)(a.q.seqs * per)), dim3(256), 0, st>>>(a, first, last);
+    k_scan_carry<NP, REV><<<dim3((unsigned)(a.q.seqs * per)), dim3(64), 0, st>>>(a, first, last);
     return hipGetLastError();
 }
 

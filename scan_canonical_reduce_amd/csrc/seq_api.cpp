@@ -84,7 +84,7 @@ struct EmbedLayout : Layout {
         const size_t groups = (size_t)id_groups(rows);
         order = take(4 * (size_t)tokens);
         offset = take(4 * ((size_t)rows + 1));
-        items = take(8 * ((size_t)tokens + (size_t)rows));
+        items = take(8 * (size_t)tokens);
         n_items = take(4 * groups);
         n_long = take(4 * groups);
         before = take(4 * groups);
@@ -273,7 +273,7 @@ canon_status_t scan_args(const canon_selective_scan_t* c, bool step, bool grad, 
     const int64_t slots =
         step ? c->seqs : slot_count<CANON_SCAN_CHUNK>(c->seqs, rows, packed);
     if (!mul_fits(slots, c->groups * a->slabs, kMaxGrid256 - 1) ||
-        !mul_fits(c->seqs, (c->channels * 4 * ks + 255) / 256, kMaxGrid256 - 1) ||
+        !mul_fits(c->seqs, (c->channels * 4 * ks + 63) / 64, 4 * kMaxGrid256 - 1) ||
         (grad && !mul_fits((packed ? rows : c->seqs * rows), c->groups * 8 * ks,
                            (int64_t)1 << 31)))
         return CANON_EUNSUPPORTED;
