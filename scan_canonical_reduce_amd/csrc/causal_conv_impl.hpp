@@ -1,6 +1,7 @@
 // Causal depthwise convolution over a few rows: forward, backward, one row.
 //
-// A thread owns V neighbouring channels (16 bytes) and walks a run of rows
+// A thread owns V = 4 neighbouring channels (one, where rows are not aligned
+// for that) and walks a run of rows
 // with the last rows in registers, so each row is read once (plus taps - 1
 // rows in front of each run, out of the cache).  Bound by memory traffic: 2 K
 // multiply-adds per 2 elements moved.
@@ -13,12 +14,7 @@
 namespace canon {
 namespace seq {
 
-template <typename T>
-__device__ __forceinline__ float ld_param(const void* p, bool f32, int64_t i)
-{
-    return f32 ? static_cast<const float*>(p)[i]
-               : ld<T>(static_cast<const typename T::store_t*>(p) + i);
-}
+constexpr int kConvV = 4;
 
 template <typename T, int V>
 __device__ __forceinline__ void unpack(const Vec<T, V>& x, float (&v)[V])
@@ -33,13 +29,27 @@ struct ConvParams {
 
     __device__ __forceinline__ void load(const ConvArgs& a, int32_t ch)
     {
+        // the channels' taps are consecutive: one branch, so that the loads merge
+        if (a.param_f32)
+            fill<F32>(a, ch);
+        else
+            fill<T>(a, ch);
+    }
+    template <typename P>
+    __device__ __forceinline__ void fill(const ConvArgs& a, int32_t ch)
+    {
+        const typename P::store_t* pw =
+            static_cast<const typename P::store_t*>(a.weight) + (int64_t)ch * K;
+        const typename P::store_t* pb = static_cast<const typename P::store_t*>(a.bias) + ch;
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
+        for (int i = 0; i < V; ++i)
 #pragma unroll
-            for (int k = 0; k < K; ++k)
-                w[k][i] = ld_param<T>(a.weight, a.param_f32, (int64_t)(ch + i) * K + k);
-            b[i] = a.bias ? ld_param<T>(a.bias, a.param_f32, ch + i) : 0.f;
-        }
+            for (int k = 0; k < K; ++k) w[k][i] = P::load(pw[i * K + k]);
+#pragma unroll
+        for (int i = 0; i < V; ++i) b[i] = 0.f;
+        if (a.bias)
+#pragma unroll
+            for (int i = 0; i < V; ++i) b[i] = P::load(pb[i]);
     }
 };
 
@@ -72,7 +82,7 @@ __device__ __forceinline__ float conv_sum(const float (&win)[K][V], const float 
 // RUN rows per thread (at least K - 1, so that only a sequence's first run
 // reads the initial state).
 template <typename T, int K, int V, int RUN>
-__global__ __launch_bounds__(256) void k_causal_conv(ConvArgs a)
+__global__ __launch_bounds__(256, K <= 4 ? 4 : 2) void k_causal_conv(ConvArgs a)
 {
     const int32_t nv = a.channels / V;
     const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
@@ -110,31 +120,53 @@ __global__ __launch_bounds__(256) void k_causal_conv(ConvArgs a)
         }
     }
 
+    // Rows r0 .. r0 + U - 1 are computed while the next U are on their way.  Runs
+    // that are full in every lane of the wave need no checks.
+    constexpr int U = 4;
+    Vec<T, V> in[2][U];
+    const typename T::store_t* xr = x + (int64_t)ck.row * a.x.row;
+    typename T::store_t* outr = out + (int64_t)ck.row * a.out.row;
+    auto fetch = [&](int b, int32_t r0, bool full) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int32_t r = full || r0 + u < ck.len ? r0 + u : ck.len - 1;
+            in[b][u] = ld_vec<T, V>(xr + (int64_t)r * a.x.row);
+        }
+    };
+    if (ck.len > 0) fetch(0, 0, false);
     ConvParams<T, K, V> p;
     p.load(a, ch);
-    constexpr int U = RUN < 8 ? RUN : 8;  // rows in flight
-    for (int32_t t0 = 0; t0 < ck.len; t0 += U) {
-        Vec<T, V> in[U];
+    auto rows = [&](int b, int32_t r0, bool full) {
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const int32_t t = t0 + u < ck.len ? t0 + u : ck.len - 1;
-            in[u] = ld_vec<T, V>(x + (int64_t)(ck.row + t) * a.x.row);
-        }
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            if (t0 + u >= ck.len) break;
+            if (!full && r0 + u >= ck.len) break;
 #pragma unroll
             for (int k = 0; k + 1 < K; ++k)
 #pragma unroll
                 for (int j = 0; j < V; ++j) win[k][j] = win[k + 1][j];
-            unpack<T, V>(in[u], win[K - 1]);
+            unpack<T, V>(in[b][u], win[K - 1]);
             float y[V];
 #pragma unroll
-            for (int j = 0; j < V; ++j) {
-                y[j] = conv_sum<K, V>(win, p.w, p.b[j], j);
-                if (a.silu) y[j] = silu_f(y[j], sigmoid_f<T>(y[j]));
-            }
-            st_vec<T, V>(out + (int64_t)(ck.row + t0 + u) * a.out.row, y);
+            for (int j = 0; j < V; ++j) y[j] = conv_sum<K, V>(win, p.w, p.b[j], j);
+            if (a.silu)
+#pragma unroll
+                for (int j = 0; j < V; ++j) y[j] = silu_f(y[j], sigmoid_f<T>(y[j]));
+            st_vec<T, V>(outr + (int64_t)(r0 + u) * a.out.row, y);
+        }
+    };
+    if (__all(ck.len == RUN)) {
+#pragma unroll 1
+        for (int32_t r0 = 0; r0 < RUN; r0 += 2 * U) {
+            fetch(1, r0 + U, true);
+            rows(0, r0, true);
+            if (r0 + 2 * U < RUN) fetch(0, r0 + 2 * U, true);
+            rows(1, r0 + U, true);
+        }
+    } else {
+#pragma unroll 1
+        for (int32_t r0 = 0; r0 < ck.len; r0 += U) {
+            if (r0 > 0) fetch(0, r0, false);
+            rows(0, r0, false);
         }
     }
 }
@@ -143,7 +175,7 @@ __global__ __launch_bounds__(256) void k_causal_conv(ConvArgs a)
 // thread walks its run and K - 1 rows beyond it, p recomputed from x.
 // Its rows' part of dw and db goes to the workspace, per slot.
 template <typename T, int K, int V>
-__global__ __launch_bounds__(256) void k_causal_conv_grad(ConvArgs a)
+__global__ __launch_bounds__(256, K <= 4 ? 3 : 2) void k_causal_conv_grad(ConvArgs a)
 {
     constexpr int RUN = CANON_CONV_CHUNK;
     const int32_t nv = a.channels / V;
@@ -171,8 +203,6 @@ __global__ __launch_bounds__(256) void k_causal_conv_grad(ConvArgs a)
         typename T::store_t* di = a.dinit ? static_cast<typename T::store_t*>(a.dinit) +
                                                 ck.s * (K - 1) * a.channels + ch
                                           : nullptr;
-        ConvParams<T, K, V> p;
-        p.load(a, ch);
         float win[K][V], dp[K][V];
 #pragma unroll
         for (int k = 0; k < K; ++k)
@@ -185,71 +215,97 @@ __global__ __launch_bounds__(256) void k_causal_conv_grad(ConvArgs a)
         const int32_t len = ck.span.len;
         const int32_t end = ck.row + ck.len;  // of the run
         const int32_t stop = end + K - 1;
+        // As in the forward kernel; a run without a sequence's end or start near
+        // it (INNER, in every lane of the wave) needs no checks but r's.
         constexpr int U = 4;
-        for (int32_t t0 = ck.row; t0 < stop; t0 += U) {
-            Vec<T, V> in[U], gin[U];
-            if (len > 0)
-#pragma unroll
-                for (int u = 0; u < U; ++u) {
-                    const int32_t t = t0 + u < len ? t0 + u : len - 1;
-                    in[u] = ld_vec<T, V>(x + (int64_t)t * a.x.row);
-                    gin[u] = ld_vec<T, V>(go + (int64_t)t * a.dout.row);
-                }
+        Vec<T, V> in[2][U], gin[2][U];
+        auto fetch = [&](int b, int32_t r0, bool inner) {
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                const int32_t t = t0 + u;
-                if (t >= stop) break;
+                const int32_t t = ck.row + r0 + u;
+                const int64_t row = inner || t < len ? t : len - 1;
+                in[b][u] = ld_vec<T, V>(x + row * a.x.row);
+                gin[b][u] = ld_vec<T, V>(go + row * a.dout.row);
+            }
+        };
+        if (len > 0) fetch(0, 0, false);
+        ConvParams<T, K, V> p;
+        p.load(a, ch);
+        // r: the row within the run; row r - (K - 1) gets its gradient at row r
+        auto one_row = [&](int b, int u, int32_t r, bool inner) {
+            const int32_t t = ck.row + r;
 #pragma unroll
-                for (int k = 0; k + 1 < K; ++k)
-#pragma unroll
-                    for (int j = 0; j < V; ++j) {
-                        win[k][j] = win[k + 1][j];
-                        dp[k][j] = dp[k + 1][j];
-                    }
-                if (t < len) {
-                    unpack<T, V>(in[u], win[K - 1]);
-                    unpack<T, V>(gin[u], dp[K - 1]);
-                    if (a.silu)
-#pragma unroll
-                        for (int j = 0; j < V; ++j) {
-                            const float s = conv_sum<K, V>(win, p.w, p.b[j], j);
-                            dp[K - 1][j] *= silu_slope(s, sigmoid_f<T>(s));
-                        }
-                    if (t < end)
-#pragma unroll
-                        for (int j = 0; j < V; ++j) {
-                            db[j] += dp[K - 1][j];
-#pragma unroll
-                            for (int k = 0; k < K; ++k)
-                                dw[k][j] = fma32(dp[K - 1][j], win[k][j], dw[k][j]);
-                        }
-                } else {
-#pragma unroll
-                    for (int j = 0; j < V; ++j) dp[K - 1][j] = 0.f;
-                }
-                // row m = t - (K - 1) has all of dp[m .. t]: w[K - 1] dp[m] first
-                const int32_t m = t - (K - 1);
-                const bool initial = m < 0;
-                if (initial ? di == nullptr : m < ck.row) continue;
-                float y[V];
+            for (int k = 0; k + 1 < K; ++k)
 #pragma unroll
                 for (int j = 0; j < V; ++j) {
-                    y[j] = p.w[K - 1][j] * dp[0][j];
-#pragma unroll
-                    for (int k = 1; k < K; ++k) y[j] = fma32(p.w[K - 1 - k][j], dp[k][j], y[j]);
+                    win[k][j] = win[k + 1][j];
+                    dp[k][j] = dp[k + 1][j];
                 }
-                // the final state's row that is row m
-                const int32_t f = m - (len - (K - 1));
-                if (df && f >= 0) {
-                    float g[V];
-                    unpack<T, V>(ld_vec<T, V>(df + (int64_t)f * a.channels), g);
+            if (inner || t < len) {
+                unpack<T, V>(in[b][u], win[K - 1]);
+                unpack<T, V>(gin[b][u], dp[K - 1]);
+                if (a.silu)
 #pragma unroll
-                    for (int j = 0; j < V; ++j) y[j] += g[j];
-                }
-                if (initial)
-                    st_vec<T, V>(di + (int64_t)(K - 1 + m) * a.channels, y);
-                else
-                    st_vec<T, V>(dx + (int64_t)m * a.dx.row, y);
+                    for (int j = 0; j < V; ++j) {
+                        const float s = conv_sum<K, V>(win, p.w, p.b[j], j);
+                        dp[K - 1][j] *= silu_slope(s, sigmoid_f<T>(s));
+                    }
+                if (inner ? r < RUN : t < end)
+#pragma unroll
+                    for (int j = 0; j < V; ++j) {
+                        db[j] += dp[K - 1][j];
+#pragma unroll
+                        for (int k = 0; k < K; ++k)
+                            dw[k][j] = fma32(dp[K - 1][j], win[k][j], dw[k][j]);
+                    }
+            } else {
+#pragma unroll
+                for (int j = 0; j < V; ++j) dp[K - 1][j] = 0.f;
+            }
+            // row m has all of dp[m .. t]: w[K - 1] dp[m] first
+            const int32_t m = t - (K - 1);
+            const bool initial = !inner && m < 0;
+            if (initial ? di == nullptr : r < K - 1) return;
+            float y[V];
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                y[j] = p.w[K - 1][j] * dp[0][j];
+#pragma unroll
+                for (int k = 1; k < K; ++k) y[j] = fma32(p.w[K - 1 - k][j], dp[k][j], y[j]);
+            }
+            // the final state's row that is row m
+            const int32_t f = m - (len - (K - 1));
+            if (!inner && df && f >= 0) {
+                float g[V];
+                unpack<T, V>(ld_vec<T, V>(df + (int64_t)f * a.channels), g);
+#pragma unroll
+                for (int j = 0; j < V; ++j) y[j] += g[j];
+            }
+            if (initial)
+                st_vec<T, V>(di + (int64_t)(K - 1 + m) * a.channels, y);
+            else
+                st_vec<T, V>(dx + (int64_t)m * a.dx.row, y);
+        };
+        constexpr int ALL = RUN + K - 1;
+        if (__all(ck.len == RUN && ck.row > 0 && ck.row + ALL <= len - (K - 1))) {
+#pragma unroll 1
+            for (int32_t r0 = 0; r0 < ALL; r0 += 2 * U) {
+                if (r0 + U < ALL) fetch(1, r0 + U, true);
+#pragma unroll
+                for (int u = 0; u < U; ++u) one_row(0, u, r0 + u, true);
+                if (r0 + 2 * U < ALL) fetch(0, r0 + 2 * U, true);
+                if (r0 + U < ALL)
+#pragma unroll
+                    for (int u = 0; u < U; ++u)
+                        if (r0 + U + u < ALL) one_row(1, u, r0 + U + u, true);
+            }
+        } else {
+#pragma unroll 1
+            for (int32_t r0 = 0; r0 < stop - ck.row; r0 += U) {
+                if (r0 > 0 && len > 0) fetch(0, r0, false);
+#pragma unroll
+                for (int u = 0; u < U; ++u)
+                    if (r0 + u < stop - ck.row) one_row(0, u, r0 + u, false);
             }
         }
     }
@@ -351,29 +407,24 @@ hipError_t launch_conv_step_v(const ConvArgs& a, hipStream_t st)
         default: return FN<T, 8, V>(a, st);    \
     }
 
-// Elements of a 16-byte access; the backward pass, which keeps two windows and
-// the sums of dw, takes half as many 16-bit ones.
-template <typename T>
-constexpr int kConvV = 16 / (int)sizeof(typename T::store_t);
-
 template <typename T>
 hipError_t launch_causal_conv(const ConvArgs& a, int taps, hipStream_t st)
 {
-    if (a.vec) CANON_CONV_TAPS(launch_conv_v, kConvV<T>)
+    if (a.vec) CANON_CONV_TAPS(launch_conv_v, kConvV)
     CANON_CONV_TAPS(launch_conv_v, 1)
 }
 
 template <typename T>
 hipError_t launch_causal_conv_grad(const ConvArgs& a, int taps, hipStream_t st)
 {
-    if (a.vec) CANON_CONV_TAPS(launch_conv_grad_v, 4)
+    if (a.vec) CANON_CONV_TAPS(launch_conv_grad_v, kConvV)
     CANON_CONV_TAPS(launch_conv_grad_v, 1)
 }
 
 template <typename T>
 hipError_t launch_causal_conv_step(const ConvArgs& a, int taps, hipStream_t st)
 {
-    if (a.vec) CANON_CONV_TAPS(launch_conv_step_v, kConvV<T>)
+    if (a.vec) CANON_CONV_TAPS(launch_conv_step_v, kConvV)
     CANON_CONV_TAPS(launch_conv_step_v, 1)
 }
 

@@ -162,7 +162,7 @@ canon_status_t conv_args(const canon_conv_t* c, bool step, bool grad, ConvArgs* 
     a->dbias = c->dbias;
     a->dfinal = c->taps > 1 ? c->d_final_state : nullptr;
     a->dinit = c->taps > 1 ? c->d_init_state : nullptr;
-    const size_t v = 16;
+    const size_t v = 4 * es;  // four channels
     a->vec = (size_t)c->channels * es % v == 0 && rows_aligned(a->x, es, v, false) &&
              rows_aligned(a->out, es, v, false) && rows_aligned(a->dout, es, v, false) &&
              rows_aligned(a->dx, es, v, false) && ptr_aligned(a->init, v) &&
