@@ -1,9 +1,9 @@
 // Causal depthwise convolution over a few rows: forward, backward, one row.
 //
-// A thread owns V = 4 neighbouring channels (one, where rows are not aligned
-// for that) and walks a run of rows
-// with the last rows in registers, so each row is read once (plus taps - 1
-// rows in front of each run, out of the cache).  Bound by memory traffic: 2 K
+// A thread owns V = 4 neighbouring channels (2 in the backward pass, which keeps
+// two windows and the sums of dw; one, where rows are not aligned for that) and
+// walks a run of rows with the last rows in registers, so each row is read once
+// (plus taps - 1 rows in front of each run, out of the cache).  Bound by memory traffic: 2 K
 // multiply-adds per 2 elements moved.
 #pragma once
 
@@ -175,7 +175,7 @@ __global__ __launch_bounds__(256, K <= 4 ? 4 : 2) void k_causal_conv(ConvArgs a)
 // thread walks its run and K - 1 rows beyond it, p recomputed from x.
 // Its rows' part of dw and db goes to the workspace, per slot.
 template <typename T, int K, int V>
-__global__ __launch_bounds__(256, K <= 4 ? 3 : 2) void k_causal_conv_grad(ConvArgs a)
+__global__ __launch_bounds__(256, K <= 4 ? 5 : 2) void k_causal_conv_grad(ConvArgs a)
 {
     constexpr int RUN = CANON_CONV_CHUNK;
     const int32_t nv = a.channels / V;
@@ -381,10 +381,10 @@ hipError_t launch_conv_grad_v(const ConvArgs& a, hipStream_t st)
     const unsigned grid = conv_grid<CANON_CONV_CHUNK>(a, V);
     if (grid) k_causal_conv_grad<T, K, V><<<dim3(grid), dim3(256), 0, st>>>(a);
     if (hipError_t e = hipGetLastError()) return e;
-    if (hipError_t e =
-            launch_column_sum(a.ws_w, slots, (int64_t)a.channels * K, K, K, a.dweight, st))
-        return e;
-    return a.dbias ? launch_column_sum(a.ws_b, slots, a.channels, 1, 1, a.dbias, st) : hipSuccess;
+    const int64_t d = a.channels;
+    return launch_column_sums({{{a.ws_w, d * K, K, K, a.dweight}, {a.ws_b, d, 1, 1, a.dbias}, {}},
+                               slots},
+                              st);
 }
 
 template <typename T, int K, int V>
@@ -417,7 +417,7 @@ hipError_t launch_causal_conv(const ConvArgs& a, int taps, hipStream_t st)
 template <typename T>
 hipError_t launch_causal_conv_grad(const ConvArgs& a, int taps, hipStream_t st)
 {
-    if (a.vec) CANON_CONV_TAPS(launch_conv_grad_v, kConvV)
+    if (a.vec) CANON_CONV_TAPS(launch_conv_grad_v, 2)
     CANON_CONV_TAPS(launch_conv_grad_v, 1)
 }
 

@@ -582,12 +582,12 @@ hipError_t launch_scan_grad_ks(const ScanArgs& a, int64_t groups, hipStream_t st
         if (hipError_t e = hipGetLastError()) return e;
     }
     const int64_t d = a.channels;
-    if (hipError_t e = launch_column_sum(a.ws_state, slots, d * NP, NP, a.states, a.dA, st))
+    if (hipError_t e = launch_column_sums({{{a.ws_state, d * NP, NP, a.states, a.dA},
+                                            {a.ws_dD, d, 1, 1, a.dD},
+                                            {a.ws_dbias, d, 1, 1, a.dbias}},
+                                           slots},
+                                          st))
         return e;
-    if (a.dD)
-        if (hipError_t e = launch_column_sum(a.ws_dD, slots, d, 1, 1, a.dD, st)) return e;
-    if (a.dbias)
-        if (hipError_t e = launch_column_sum(a.ws_dbias, slots, d, 1, 1, a.dbias, st)) return e;
     const int64_t bc = (a.q.starts ? a.q.rows : a.q.seqs * a.q.rows) * groups * 2 * NP;
     if (bc == 0) return hipSuccess;
     k_scan_sum_bc<T, NP><<<dim3((unsigned)((bc + 255) / 256)), dim3(256), 0, st>>>(a, (int)groups);
