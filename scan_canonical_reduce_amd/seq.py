@@ -17,6 +17,7 @@ or if it is too small, the call allocates its own.
 from __future__ import annotations
 
 import ctypes
+import struct
 from typing import NamedTuple, Optional
 
 import torch
@@ -41,30 +42,13 @@ SEQ_EXPORTS = [
 
 _I64, _P = ctypes.c_int64, ctypes.c_void_p
 
-
-class Rows(ctypes.Structure):
-    """canon_rows_t"""
-    _fields_ = [("p", _P), ("seq", _I64), ("row", _I64)]
-
-
-class Conv(ctypes.Structure):
-    """canon_conv_t"""
-    _fields_ = [(n, _I64) for n in
-                ("dtype", "taps", "silu", "param_dtype", "seqs", "rows", "channels")] + [
-        ("starts", _P), ("x", Rows), ("out", Rows), ("weight", _P), ("bias", _P),
-        ("init_state", _P), ("final_state", _P), ("dout", Rows), ("dx", Rows), ("dweight", _P),
-        ("dbias", _P), ("d_final_state", _P), ("d_init_state", _P)]
-
-
-class Scan(ctypes.Structure):
-    """canon_selective_scan_t"""
-    _fields_ = [(n, _I64) for n in
-                ("dtype", "softplus", "seqs", "rows", "channels", "groups", "states")] + [
-        ("starts", _P)] + [(n, Rows) for n in ("u", "delta", "z", "out", "B", "C")] + [
-        (n, _P) for n in ("A", "D", "delta_bias", "init_state", "final_state",
-                          "chunk_states")] + [
-        (n, Rows) for n in ("dout", "du", "ddelta", "dz", "dB", "dC")] + [
-        (n, _P) for n in ("dA", "dD", "ddelta_bias", "d_final_state", "d_init_state")]
+# canon_conv_t and canon_selective_scan_t: fields of 8 bytes, pointers included
+# (0: NULL), a canon_rows_t being three of them.  Packed in one go: a call's time
+# is mostly the host's for small sizes, and a ctypes structure filled field by
+# field takes three microseconds more.
+CONV = struct.Struct("=28q")
+SCAN = struct.Struct("=55q")
+_NONE = (0, 0, 0)
 
 
 _seq = None
@@ -115,59 +99,58 @@ def _same(what: str, device: torch.device, *ts: Optional[torch.Tensor]) -> None:
             raise ValueError(f"{what}: tensors are on {device} and {t.device}")
 
 
-class _On:
-    """The device of a call, made current if it is not, and its stream."""
-    __slots__ = ("device", "guard")
-
-    def __init__(self, device: torch.device):
-        self.device = device
-        self.guard = None
-
-    def __enter__(self) -> int:
-        if self.device.index != torch.cuda.current_device():
-            self.guard = torch.cuda.device(self.device)
-            self.guard.__enter__()
-        return torch.cuda.current_stream(self.device).cuda_stream
-
-    def __exit__(self, *exc):
-        if self.guard is not None:
-            self.guard.__exit__(*exc)
-        return False
+def _call(what: str, device: torch.device, fn, *args) -> None:
+    """fn(*args, stream) on the device's current stream, the device made
+    current if it is not."""
+    index = device.index
+    stream = torch._C._cuda_getCurrentRawStream(index)
+    if index == torch._C._cuda_getDevice():
+        st = fn(*args, stream)
+    else:
+        with torch.cuda.device(index):
+            st = fn(*args, stream)
+    if st:
+        _check(st, what)
 
 
-def _shape(what: str, name: str, t: torch.Tensor, shape, dtype=None) -> None:
-    if t.shape != tuple(shape) or (dtype is not None and t.dtype != dtype):
-        want = f" {dtype}" if dtype is not None else ""
-        raise ValueError(f"{what}: {name} must be{want} of shape {tuple(shape)}, "
-                         f"not {t.dtype} {tuple(t.shape)}")
+def _wrong(what: str, name: str, t: torch.Tensor, shape, dtype) -> ValueError:
+    return ValueError(f"{what}: {name} must be {dtype} of shape {tuple(shape)}, "
+                      f"not {t.dtype} {tuple(t.shape)}")
 
 
-def _flat(what: str, name: str, t: Optional[torch.Tensor], shape, dtype) -> Optional[int]:
-    """Pointer of a contiguous tensor of that shape and type (None if absent)."""
+def _flat(what: str, name: str, t: Optional[torch.Tensor], shape, dtype) -> int:
+    """Pointer of a contiguous tensor of that shape and type (0 if absent)."""
     if t is None:
-        return None
-    _shape(what, name, t, shape, dtype)
+        return 0
+    if t.shape != shape or t.dtype != dtype:
+        raise _wrong(what, name, t, shape, dtype)
     if not t.is_contiguous():
         raise ValueError(f"{what}: {name} must be contiguous")
     return t.data_ptr()
 
 
-def _rows(what: str, name: str, t: torch.Tensor, shape, dtype, lead: int) -> Rows:
+def _rows(what: str, name: str, t: torch.Tensor, shape, dtype, lead: int):
     """canon_rows_t of an activation whose first `lead` dimensions are rows
-    (1), or sequences and rows (2); the others are its columns, contiguous.
-    Strides of dimensions of one element are never used and passed as 0."""
-    _shape(what, name, t, shape, dtype)
+    (1), or sequences and rows (2); the one or two others are its columns,
+    contiguous.  Strides of dimensions of one element are never used and passed
+    as 0."""
+    if t.shape != shape or t.dtype != dtype:
+        raise _wrong(what, name, t, shape, dtype)
     st = t.stride()
-    run = 1
-    for i in range(t.dim() - 1, lead - 1, -1):
-        if shape[i] != 1 and st[i] != run and t.numel():
-            raise ValueError(f"{what}: the columns of {name} must be contiguous")
-        run *= shape[i]
-    return Rows(t.data_ptr(), st[0] if lead == 2 and shape[0] > 1 else 0,
-                st[lead - 1] if shape[lead - 1] > 1 else 0)
+    cols = shape[-1]
+    if ((st[-1] != 1 and cols != 1)
+            or (len(st) > lead + 1 and st[-2] != cols and shape[-2] != 1)) and t.numel():
+        raise ValueError(f"{what}: the columns of {name} must be contiguous")
+    row = st[lead - 1] if shape[lead - 1] > 1 else 0
+    if lead == 1:
+        return t.data_ptr(), 0, row
+    return t.data_ptr(), st[0] if shape[0] > 1 else 0, row
 
 
-_NONE = Rows(None, 0, 0)
+def _step_rows(what: str, name: str, t: torch.Tensor, shape, dtype):
+    """canon_rows_t of one row per sequence."""
+    p, _, row = _rows(what, name, t, shape, dtype, 1)
+    return p, row, 0
 
 
 def _sequences(what: str, x: torch.Tensor, starts: Optional[torch.Tensor]):
@@ -176,7 +159,7 @@ def _sequences(what: str, x: torch.Tensor, starts: Optional[torch.Tensor]):
         if x.dim() != 3:
             raise ValueError(f"{what} takes [sequences, rows, channels], or packed rows with "
                              "starts")
-        return x.shape[0], x.shape[1], None, 2
+        return x.shape[0], x.shape[1], 0, 2
     if x.dim() != 2:
         raise ValueError(f"{what} with starts takes [rows, channels]")
     if starts.dtype != torch.int32 or starts.dim() != 1 or starts.numel() < 1 \
@@ -219,19 +202,20 @@ def embedding(weight: torch.Tensor, ids: torch.Tensor, scale: float = 1.0,
     d = _dtype(weight, what)
     rows, width, ld = _matrix(what, "weight", weight)
     p, nb, tokens = _ids(what, ids)
+    shape = ids.shape + (width,)
     if out is None:
-        out = torch.empty(ids.shape + (width,), dtype=weight.dtype, device=weight.device)
-    _shape(what, "out", out, ids.shape + (width,), weight.dtype)
-    if out.dim() != 2:
-        if not out.is_contiguous():
-            raise ValueError(f"{what}: out must be contiguous unless it is 2-d")
+        out = torch.empty(shape, dtype=weight.dtype, device=weight.device)
+        ld_out = width
+    elif out.shape != shape or out.dtype != weight.dtype:
+        raise _wrong(what, "out", out, shape, weight.dtype)
+    elif out.dim() == 2:
+        ld_out = _matrix(what, "out", out)[2]
+    elif out.is_contiguous():
         ld_out = width
     else:
-        ld_out = _matrix(what, "out", out)[2]
-    with _On(weight.device) as stream:
-        st = _lib().canon_embedding(d, weight.data_ptr(), ld, rows, width, p, nb, tokens, scale,
-                                    out.data_ptr(), ld_out, stream)
-    _check(st, what)
+        raise ValueError(f"{what}: out must be contiguous unless it is 2-d")
+    _call(what, weight.device, _lib().canon_embedding, d, weight.data_ptr(), ld, rows, width, p,
+          nb, tokens, scale, out.data_ptr(), ld_out)
     return out
 
 
@@ -266,19 +250,16 @@ def embedding_grad(dout: torch.Tensor, ids: torch.Tensor, rows: int, scale: floa
         if accumulate:
             raise ValueError(f"{what}: accumulate needs out")
         out = torch.empty((rows, width), dtype=dtype or dout.dtype, device=dout.device)
-    _shape(what, "out", out, (rows, width), dtype)
-    if out.dtype not in (dout.dtype, torch.float32):
+    elif out.shape != (rows, width) or (dtype is not None and out.dtype != dtype):
+        raise _wrong(what, "out", out, (rows, width), dtype or out.dtype)
+    if out.dtype != dout.dtype and out.dtype != torch.float32:
         raise TypeError(f"{what}: the gradient must be {dout.dtype} or float32, not {out.dtype}")
     ld_out = _matrix(what, "out", out)[2]
     L = _lib()
-    n = L.canon_embedding_grad_workspace_bytes(tokens, rows, width)
-    with _On(dout.device) as stream:
-        w = _workspace(n, dout.device, ws)
-        st = L.canon_embedding_grad(d, dout.data_ptr(), ld, p, nb, tokens, rows, width, scale,
-                                    -1 if padding_id is None else padding_id, int(accumulate),
-                                    DTYPES[out.dtype], out.data_ptr(), ld_out, w.data_ptr(),
-                                    w.numel(), stream)
-    _check(st, what)
+    w = _workspace(L.canon_embedding_grad_workspace_bytes(tokens, rows, width), dout.device, ws)
+    _call(what, dout.device, L.canon_embedding_grad, d, dout.data_ptr(), ld, p, nb, tokens, rows,
+          width, scale, -1 if padding_id is None else padding_id, int(accumulate),
+          DTYPES[out.dtype], out.data_ptr(), ld_out, w.data_ptr(), w.numel())
     return out
 
 
@@ -296,22 +277,17 @@ def _activation(what: str, a) -> int:
     return int(a == "silu")
 
 
-def _conv(what, x, weight, bias, activation, seqs, rows, starts, lead) -> Conv:
-    c = Conv()
-    c.dtype = _dtype(x, what)
+def _conv(what, x, weight, bias, activation):
+    """(dtype, taps, silu, param_dtype), channels, (weight, bias)"""
+    d = _dtype(x, what)
     channels = x.shape[-1]
     if weight.dim() != 2 or weight.shape[0] != channels:
         raise ValueError(f"{what}: weight must be [{channels}, taps]")
-    c.taps = weight.shape[1]
-    c.silu = _activation(what, activation)
-    if weight.dtype not in (x.dtype, torch.float32):
+    if weight.dtype != x.dtype and weight.dtype != torch.float32:
         raise TypeError(f"{what}: weight must be {x.dtype} or float32, not {weight.dtype}")
-    c.param_dtype = DTYPES[weight.dtype]
-    c.seqs, c.rows, c.channels, c.starts = seqs, rows, channels, starts
-    c.x = _rows(what, "x", x, x.shape, x.dtype, lead)
-    c.weight = _flat(what, "weight", weight, weight.shape, weight.dtype)
-    c.bias = _flat(what, "bias", bias, (channels,), weight.dtype)
-    return c
+    head = (d, weight.shape[1], _activation(what, activation), DTYPES[weight.dtype])
+    return head, channels, (_flat(what, "weight", weight, weight.shape, weight.dtype),
+                            _flat(what, "bias", bias, (channels,), weight.dtype))
 
 
 def causal_conv(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Tensor] = None,
@@ -327,15 +303,16 @@ def causal_conv(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Tens
     what = "causal_conv"
     _same(what, x.device, weight, bias, starts, init_state, final_state, out)
     seqs, rows, sp, lead = _sequences(what, x, starts)
-    c = _conv(what, x, weight, bias, activation, seqs, rows, sp, lead)
-    state = (seqs, c.taps - 1, x.shape[-1])
-    c.init_state = _flat(what, "init_state", init_state, state, x.dtype)
-    c.final_state = _flat(what, "final_state", final_state, state, x.dtype)
-    with _On(x.device) as stream:
-        if out is None:
-            out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-        c.out = _rows(what, "out", out, x.shape, x.dtype, lead)
-        _check(_lib().canon_causal_conv(ctypes.byref(c), stream), what)
+    head, channels, params = _conv(what, x, weight, bias, activation)
+    state = (seqs, head[1] - 1, channels)
+    if out is None:
+        out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    c = CONV.pack(*head, seqs, rows, channels, sp, *_rows(what, "x", x, x.shape, x.dtype, lead),
+                  *_rows(what, "out", out, x.shape, x.dtype, lead), *params,
+                  _flat(what, "init_state", init_state, state, x.dtype),
+                  _flat(what, "final_state", final_state, state, x.dtype),
+                  *_NONE, *_NONE, 0, 0, 0, 0)
+    _call(what, x.device, _lib().canon_causal_conv, c)
     return out
 
 
@@ -357,26 +334,25 @@ def causal_conv_grad(dout: torch.Tensor, x: torch.Tensor, weight: torch.Tensor,
     what = "causal_conv_grad"
     _same(what, x.device, dout, weight, bias, starts, init_state, d_final_state, dx, ws)
     seqs, rows, sp, lead = _sequences(what, x, starts)
-    c = _conv(what, x, weight, bias, activation, seqs, rows, sp, lead)
-    channels = x.shape[-1]
-    state = (seqs, c.taps - 1, channels)
-    c.init_state = _flat(what, "init_state", init_state, state, x.dtype)
-    c.d_final_state = _flat(what, "d_final_state", d_final_state, state, x.dtype)
-    c.dout = _rows(what, "dout", dout, x.shape, x.dtype, lead)
+    head, channels, params = _conv(what, x, weight, bias, activation)
+    state = (seqs, head[1] - 1, channels)
+    device = x.device
+    if dx is None:
+        dx = torch.empty(x.shape, dtype=x.dtype, device=device)
+    dw = torch.empty(weight.shape, dtype=torch.float32, device=device)
+    db = None if bias is None else torch.empty(channels, dtype=torch.float32, device=device)
+    di = None if init_state is None else torch.empty_like(init_state)
+    c = CONV.pack(*head, seqs, rows, channels, sp, *_rows(what, "x", x, x.shape, x.dtype, lead),
+                  *_NONE, *params, _flat(what, "init_state", init_state, state, x.dtype), 0,
+                  *_rows(what, "dout", dout, x.shape, x.dtype, lead),
+                  *_rows(what, "dx", dx, x.shape, x.dtype, lead), dw.data_ptr(),
+                  0 if db is None else db.data_ptr(),
+                  _flat(what, "d_final_state", d_final_state, state, x.dtype),
+                  0 if di is None else di.data_ptr())
     L = _lib()
-    n = L.canon_causal_conv_grad_workspace_bytes(seqs, rows, int(sp is not None), channels, c.taps)
-    with _On(x.device) as stream:
-        if dx is None:
-            dx = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-        dw = torch.empty(weight.shape, dtype=torch.float32, device=x.device)
-        db = None if bias is None else torch.empty(channels, dtype=torch.float32, device=x.device)
-        di = None if init_state is None else torch.empty_like(init_state)
-        w = _workspace(n, x.device, ws)
-        c.dx = _rows(what, "dx", dx, x.shape, x.dtype, lead)
-        c.dweight = dw.data_ptr()
-        c.dbias = None if db is None else db.data_ptr()
-        c.d_init_state = None if di is None else di.data_ptr()
-        _check(L.canon_causal_conv_grad(ctypes.byref(c), w.data_ptr(), w.numel(), stream), what)
+    w = _workspace(L.canon_causal_conv_grad_workspace_bytes(seqs, rows, int(lead == 1), channels,
+                                                            head[1]), device, ws)
+    _call(what, device, L.canon_causal_conv_grad, c, w.data_ptr(), w.numel())
     return CausalConvGrads(dx, dw, db, di)
 
 
@@ -391,18 +367,16 @@ def causal_conv_step(x: torch.Tensor, state: torch.Tensor, weight: torch.Tensor,
     _same(what, x.device, weight, bias, state, out_state, out)
     if x.dim() != 2:
         raise ValueError(f"{what} takes [sequences, channels]")
-    c = _conv(what, x, weight, bias, activation, x.shape[0], 1, None, 1)
-    c.x = Rows(c.x.p, c.x.row, 0)
-    shape = (x.shape[0], c.taps - 1, x.shape[1])
-    c.init_state = _flat(what, "state", state, shape, x.dtype)
-    c.final_state = c.init_state if out_state is None else \
-        _flat(what, "out_state", out_state, shape, x.dtype)
-    with _On(x.device) as stream:
-        if out is None:
-            out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-        o = _rows(what, "out", out, x.shape, x.dtype, 1)
-        c.out = Rows(o.p, o.row, 0)
-        _check(_lib().canon_causal_conv_step(ctypes.byref(c), stream), what)
+    head, channels, params = _conv(what, x, weight, bias, activation)
+    shape = (x.shape[0], head[1] - 1, channels)
+    old = _flat(what, "state", state, shape, x.dtype)
+    if out is None:
+        out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    c = CONV.pack(*head, x.shape[0], 1, channels, 0, *_step_rows(what, "x", x, x.shape, x.dtype),
+                  *_step_rows(what, "out", out, x.shape, x.dtype), *params, old,
+                  old if out_state is None else _flat(what, "out_state", out_state, shape, x.dtype),
+                  *_NONE, *_NONE, 0, 0, 0, 0)
+    _call(what, x.device, _lib().canon_causal_conv_step, c)
     return out
 
 
@@ -419,31 +393,26 @@ class SelectiveScanGrads(NamedTuple):
     dinit_state: Optional[torch.Tensor]
 
 
-def _scan(what, u, delta, A, B, C, D, z, delta_bias, softplus, seqs, rows, starts, lead) -> Scan:
-    c = Scan()
-    c.dtype = _dtype(u, what)
+def _scan(what, u, A, B, D, delta_bias, softplus):
+    """(dtype, softplus), (channels, groups, states), shape of B and C, (A, D,
+    delta_bias)"""
+    d = _dtype(u, what)
     channels = u.shape[-1]
     if A.dim() != 2 or A.shape[0] != channels:
         raise ValueError(f"{what}: A must be [{channels}, states]")
     states = A.shape[1]
-    groups = B.shape[-2] if B.dim() == u.dim() + 1 else 1
-    bc = u.shape[:-1] + ((groups, states) if B.dim() == u.dim() + 1 else (states,))
+    if B.dim() == u.dim() + 1:
+        groups = B.shape[-2]
+        bc = u.shape[:-1] + (groups, states)
+    else:
+        groups = 1
+        bc = u.shape[:-1] + (states,)
     if groups < 1 or channels % groups:
         raise ValueError(f"{what}: {channels} channels do not divide into {groups} groups")
-    c.softplus = int(bool(softplus))
-    c.seqs, c.rows, c.channels, c.groups, c.states = seqs, rows, channels, groups, states
-    c.starts = starts
-    c.u = _rows(what, "u", u, u.shape, u.dtype, lead)
-    c.delta = _rows(what, "delta", delta, u.shape, u.dtype, lead)
-    c.B = _rows(what, "B", B, bc, u.dtype, lead)
-    c.C = _rows(what, "C", C, bc, u.dtype, lead)
-    if z is not None:
-        c.z = _rows(what, "z", z, u.shape, u.dtype, lead)
     f32 = torch.float32
-    c.A = _flat(what, "A", A, A.shape, f32)
-    c.D = _flat(what, "D", D, (channels,), f32)
-    c.delta_bias = _flat(what, "delta_bias", delta_bias, (channels,), f32)
-    return c
+    return (d, int(bool(softplus))), (channels, groups, states), bc, (
+        _flat(what, "A", A, A.shape, f32), _flat(what, "D", D, (channels,), f32),
+        _flat(what, "delta_bias", delta_bias, (channels,), f32))
 
 
 def selective_scan_workspace_bytes(seqs: int, rows: int, packed: bool, channels: int,
@@ -462,8 +431,8 @@ def selective_scan_states(u: torch.Tensor, states: int,
     """An uninitialised buffer for selective_scan's `states` argument: what the
     forward pass of u saves for the backward pass (4 bytes per element of u and
     16 states)."""
-    seqs, rows, sp, _ = _sequences("selective_scan_states", u, starts)
-    n = _lib().canon_selective_scan_states(seqs, rows, int(sp is not None), u.shape[-1], states)
+    seqs, rows, _, lead = _sequences("selective_scan_states", u, starts)
+    n = _lib().canon_selective_scan_states(seqs, rows, int(lead == 1), u.shape[-1], states)
     return torch.empty(n, dtype=torch.float32, device=u.device)
 
 
@@ -487,22 +456,27 @@ def selective_scan(u: torch.Tensor, delta: torch.Tensor, A: torch.Tensor, B: tor
     _same(what, u.device, delta, A, B, C, D, z, delta_bias, starts, init_state, final_state,
           states, out, ws)
     seqs, rows, sp, lead = _sequences(what, u, starts)
-    c = _scan(what, u, delta, A, B, C, D, z, delta_bias, delta_softplus, seqs, rows, sp, lead)
-    shape = (seqs, c.channels, c.states)
-    c.init_state = _flat(what, "init_state", init_state, shape, torch.float32)
-    c.final_state = _flat(what, "final_state", final_state, shape, torch.float32)
+    head, sizes, bc, params = _scan(what, u, A, B, D, delta_bias, delta_softplus)
+    channels, _, n = sizes
+    shape, f32, dtype, packed = (seqs, channels, n), torch.float32, u.dtype, int(lead == 1)
     L = _lib()
+    kept = 0
     if states is not None:
-        n = L.canon_selective_scan_states(seqs, rows, int(sp is not None), c.channels, c.states)
-        c.chunk_states = _flat(what, "states", states, (n,), torch.float32)
-    n = L.canon_selective_scan_workspace_bytes(seqs, rows, int(sp is not None), c.channels,
-                                               c.states)
-    with _On(u.device) as stream:
-        if out is None:
-            out = torch.empty(u.shape, dtype=u.dtype, device=u.device)
-        c.out = _rows(what, "out", out, u.shape, u.dtype, lead)
-        w = _workspace(n, u.device, ws)
-        _check(L.canon_selective_scan(ctypes.byref(c), w.data_ptr(), w.numel(), stream), what)
+        size = L.canon_selective_scan_states(seqs, rows, packed, channels, n)
+        kept = _flat(what, "states", states, (size,), f32)
+    if out is None:
+        out = torch.empty(u.shape, dtype=dtype, device=u.device)
+    c = SCAN.pack(*head, seqs, rows, *sizes, sp, *_rows(what, "u", u, u.shape, dtype, lead),
+                  *_rows(what, "delta", delta, u.shape, dtype, lead),
+                  *(_NONE if z is None else _rows(what, "z", z, u.shape, dtype, lead)),
+                  *_rows(what, "out", out, u.shape, dtype, lead),
+                  *_rows(what, "B", B, bc, dtype, lead), *_rows(what, "C", C, bc, dtype, lead),
+                  *params, _flat(what, "init_state", init_state, shape, f32),
+                  _flat(what, "final_state", final_state, shape, f32), kept, *_NONE, *_NONE,
+                  *_NONE, *_NONE, *_NONE, *_NONE, 0, 0, 0, 0, 0)
+    w = _workspace(L.canon_selective_scan_workspace_bytes(seqs, rows, packed, channels, n),
+                   u.device, ws)
+    _call(what, u.device, L.canon_selective_scan, c, w.data_ptr(), w.numel())
     return out
 
 
@@ -522,40 +496,41 @@ def selective_scan_grad(dout: torch.Tensor, u: torch.Tensor, delta: torch.Tensor
     _same(what, u.device, dout, delta, A, B, C, D, z, delta_bias, starts, states, d_final_state,
           ws)
     seqs, rows, sp, lead = _sequences(what, u, starts)
-    c = _scan(what, u, delta, A, B, C, D, z, delta_bias, delta_softplus, seqs, rows, sp, lead)
-    shape = (seqs, c.channels, c.states)
-    f32, device = torch.float32, u.device
-    c.dout = _rows(what, "dout", dout, u.shape, u.dtype, lead)
-    c.d_final_state = _flat(what, "d_final_state", d_final_state, shape, f32)
+    head, sizes, bc, params = _scan(what, u, A, B, D, delta_bias, delta_softplus)
+    channels, groups, n = sizes
+    shape, f32, packed = (seqs, channels, n), torch.float32, int(lead == 1)
+    device, dtype = u.device, u.dtype
     L = _lib()
-    n = L.canon_selective_scan_states(seqs, rows, int(sp is not None), c.channels, c.states)
-    c.chunk_states = _flat(what, "states", states, (n,), f32)
-    n = L.canon_selective_scan_grad_workspace_bytes(seqs, rows, int(sp is not None), c.channels,
-                                                    c.groups, c.states)
-    with _On(device) as stream:
-        w = _workspace(n, device, ws)
-        g = SelectiveScanGrads(
-            du=torch.empty(u.shape, dtype=u.dtype, device=device),
-            ddelta=torch.empty(u.shape, dtype=u.dtype, device=device),
-            dA=torch.empty(A.shape, dtype=f32, device=device),
-            dB=torch.empty(B.shape, dtype=u.dtype, device=device),
-            dC=torch.empty(C.shape, dtype=u.dtype, device=device),
-            dD=None if D is None else torch.empty(c.channels, dtype=f32, device=device),
-            dz=None if z is None else torch.empty(u.shape, dtype=u.dtype, device=device),
-            ddelta_bias=None if delta_bias is None else
-            torch.empty(c.channels, dtype=f32, device=device),
-            dinit_state=torch.empty(shape, dtype=f32, device=device))
-        c.du = _rows(what, "du", g.du, u.shape, u.dtype, lead)
-        c.ddelta = _rows(what, "ddelta", g.ddelta, u.shape, u.dtype, lead)
-        c.dB = _rows(what, "dB", g.dB, B.shape, u.dtype, lead)
-        c.dC = _rows(what, "dC", g.dC, C.shape, u.dtype, lead)
-        if z is not None:
-            c.dz = _rows(what, "dz", g.dz, u.shape, u.dtype, lead)
-        c.dA = g.dA.data_ptr()
-        c.dD = None if D is None else g.dD.data_ptr()
-        c.ddelta_bias = None if delta_bias is None else g.ddelta_bias.data_ptr()
-        c.d_init_state = g.dinit_state.data_ptr()
-        _check(L.canon_selective_scan_grad(ctypes.byref(c), w.data_ptr(), w.numel(), stream), what)
+    size = L.canon_selective_scan_states(seqs, rows, packed, channels, n)
+    g = SelectiveScanGrads(
+        du=torch.empty(u.shape, dtype=dtype, device=device),
+        ddelta=torch.empty(u.shape, dtype=dtype, device=device),
+        dA=torch.empty(A.shape, dtype=f32, device=device),
+        dB=torch.empty(bc, dtype=dtype, device=device),
+        dC=torch.empty(bc, dtype=dtype, device=device),
+        dD=None if D is None else torch.empty(channels, dtype=f32, device=device),
+        dz=None if z is None else torch.empty(u.shape, dtype=dtype, device=device),
+        ddelta_bias=None if delta_bias is None else
+        torch.empty(channels, dtype=f32, device=device),
+        dinit_state=torch.empty(shape, dtype=f32, device=device))
+    c = SCAN.pack(*head, seqs, rows, *sizes, sp, *_rows(what, "u", u, u.shape, dtype, lead),
+                  *_rows(what, "delta", delta, u.shape, dtype, lead),
+                  *(_NONE if z is None else _rows(what, "z", z, u.shape, dtype, lead)), *_NONE,
+                  *_rows(what, "B", B, bc, dtype, lead), *_rows(what, "C", C, bc, dtype, lead),
+                  *params, 0, 0, _flat(what, "states", states, (size,), f32),
+                  *_rows(what, "dout", dout, u.shape, dtype, lead),
+                  *_rows(what, "du", g.du, u.shape, dtype, lead),
+                  *_rows(what, "ddelta", g.ddelta, u.shape, dtype, lead),
+                  *(_NONE if z is None else _rows(what, "dz", g.dz, u.shape, dtype, lead)),
+                  *_rows(what, "dB", g.dB, bc, dtype, lead),
+                  *_rows(what, "dC", g.dC, bc, dtype, lead), g.dA.data_ptr(),
+                  0 if D is None else g.dD.data_ptr(),
+                  0 if delta_bias is None else g.ddelta_bias.data_ptr(),
+                  _flat(what, "d_final_state", d_final_state, shape, f32),
+                  g.dinit_state.data_ptr())
+    w = _workspace(L.canon_selective_scan_grad_workspace_bytes(seqs, rows, packed, channels,
+                                                               groups, n), device, ws)
+    _call(what, device, L.canon_selective_scan_grad, c, w.data_ptr(), w.numel())
     return g
 
 
@@ -573,18 +548,19 @@ def selective_scan_step(state: torch.Tensor, u: torch.Tensor, delta: torch.Tenso
     _same(what, u.device, state, delta, A, B, C, D, z, delta_bias, out_state, out)
     if u.dim() != 2:
         raise ValueError(f"{what} takes [sequences, channels]")
-    c = _scan(what, u, delta, A, B, C, D, z, delta_bias, delta_softplus, u.shape[0], 1, None, 1)
-    for name in ("u", "delta", "z", "B", "C"):  # one row per sequence
-        r = getattr(c, name)
-        setattr(c, name, Rows(r.p, r.row, 0))
-    shape = (u.shape[0], c.channels, c.states)
-    c.init_state = _flat(what, "state", state, shape, torch.float32)
-    c.final_state = c.init_state if out_state is None else \
-        _flat(what, "out_state", out_state, shape, torch.float32)
-    with _On(u.device) as stream:
-        if out is None:
-            out = torch.empty(u.shape, dtype=u.dtype, device=u.device)
-        o = _rows(what, "out", out, u.shape, u.dtype, 1)
-        c.out = Rows(o.p, o.row, 0)
-        _check(_lib().canon_selective_scan_step(ctypes.byref(c), stream), what)
+    head, sizes, bc, params = _scan(what, u, A, B, D, delta_bias, delta_softplus)
+    seqs, dtype, f32 = u.shape[0], u.dtype, torch.float32
+    shape = (seqs, sizes[0], sizes[2])
+    old = _flat(what, "state", state, shape, f32)
+    if out is None:
+        out = torch.empty(u.shape, dtype=dtype, device=u.device)
+    c = SCAN.pack(*head, seqs, 1, *sizes, 0, *_step_rows(what, "u", u, u.shape, dtype),
+                  *_step_rows(what, "delta", delta, u.shape, dtype),
+                  *(_NONE if z is None else _step_rows(what, "z", z, u.shape, dtype)),
+                  *_step_rows(what, "out", out, u.shape, dtype),
+                  *_step_rows(what, "B", B, bc, dtype), *_step_rows(what, "C", C, bc, dtype),
+                  *params, old,
+                  old if out_state is None else _flat(what, "out_state", out_state, shape, f32),
+                  0, *_NONE, *_NONE, *_NONE, *_NONE, *_NONE, *_NONE, 0, 0, 0, 0, 0)
+    _call(what, u.device, _lib().canon_selective_scan_step, c)
     return out

@@ -37,19 +37,29 @@ def test_header_exports(seq):
         assert re.search(rf"\bT {name}\b", out), name
 
 
-@pytest.mark.parametrize("cls,struct", [("Conv", "canon_conv_t"),
-                                        ("Scan", "canon_selective_scan_t"),
-                                        ("Rows", "canon_rows_t")])
-def test_struct_fields(seq, cls, struct):
-    """The binding's structs list the header's fields in the header's order."""
-    body = re.search(r"typedef struct \{([^}]*)\} " + struct + ";", header()).group(1)
-    names = []
-    for decl in body.split(";"):
-        decl = decl.strip()
-        if decl:
-            decl = re.sub(r"^(const )?\w+", "", decl)
-            names += [n.strip(" *\n") for n in decl.split(",")]
-    assert names == [f[0] for f in getattr(seq, cls)._fields_]
+class Rows(ctypes.Structure):
+    _fields_ = [("p", ctypes.c_void_p), ("seq", ctypes.c_int64), ("row", ctypes.c_int64)]
+
+
+def struct_of(name):
+    """The header's struct as a ctypes one."""
+    body = re.search(r"typedef struct \{([^}]*)\} " + name + ";", header()).group(1)
+    fields = []
+    for decl in filter(None, (d.strip() for d in body.split(";"))):
+        kind, names = re.match(r"(?:const )?(\w+)(.*)", decl, re.S).groups()
+        for n in names.split(","):
+            c = ctypes.c_void_p if "*" in n else Rows if kind == "canon_rows_t" else ctypes.c_int64
+            assert "*" in n or kind in ("canon_rows_t", "int64_t")
+            fields.append((n.strip(" *\n"), c))
+    return type(name, (ctypes.Structure,), {"_fields_": fields})
+
+
+Conv, Scan = struct_of("canon_conv_t"), struct_of("canon_selective_scan_t")
+
+
+def test_struct_sizes(seq):
+    assert [f[0] for f in struct_of("canon_rows_t")._fields_] == ["p", "seq", "row"]
+    assert ctypes.sizeof(Conv) == seq.CONV.size and ctypes.sizeof(Scan) == seq.SCAN.size
 
 
 def test_limits_match_the_header(seq):
@@ -110,10 +120,10 @@ def test_embedding_refusals(seq):
 
 
 def conv(seq, **kw):
-    c = seq.Conv()
+    c = Conv()
     c.dtype, c.taps, c.silu, c.param_dtype = 1, 4, 1, 0
     c.seqs, c.rows, c.channels = 2, 9, 8
-    r = seq.Rows(FAKE, 72, 8)
+    r = Rows(FAKE, 72, 8)
     c.x = c.out = c.dout = c.dx = r
     c.weight = c.bias = c.dweight = c.dbias = FAKE
     for k, v in kw.items():
@@ -124,7 +134,7 @@ def conv(seq, **kw):
 def test_conv_refusals(seq):
     L = seq._lib()
     n = seq.causal_conv_grad_workspace_bytes(2, 9, False, 8, 4)
-    R = seq.Rows
+    R = Rows
     for bad in (dict(dtype=7), dict(taps=0), dict(silu=2), dict(param_dtype=2), dict(seqs=-1),
                 dict(rows=-1), dict(channels=-1), dict(weight=None), dict(x=R(None, 0, 0)),
                 dict(x=R(FAKE, 72, -8))):
@@ -148,11 +158,11 @@ def test_conv_refusals(seq):
 
 
 def scan(seq, **kw):
-    c = seq.Scan()
+    c = Scan()
     c.dtype, c.softplus = 1, 1
     c.seqs, c.rows, c.channels, c.groups, c.states = 2, 9, 8, 2, 16
-    r = seq.Rows(FAKE, 72, 8)
-    b = seq.Rows(FAKE, 9 * 32, 32)
+    r = Rows(FAKE, 72, 8)
+    b = Rows(FAKE, 9 * 32, 32)
     c.u = c.delta = c.z = c.out = c.dout = c.du = c.ddelta = c.dz = r
     c.B = c.C = c.dB = c.dC = b
     c.A = c.D = c.delta_bias = c.dA = c.dD = c.ddelta_bias = c.chunk_states = FAKE
@@ -163,7 +173,7 @@ def scan(seq, **kw):
 
 def test_scan_refusals(seq):
     L = seq._lib()
-    R = seq.Rows
+    R = Rows
     n = seq.selective_scan_grad_workspace_bytes(2, 9, False, 8, 2, 16)
     common = [dict(dtype=5), dict(softplus=2), dict(seqs=-1), dict(rows=-1), dict(groups=0),
               dict(groups=3), dict(states=0), dict(A=None), dict(u=R(None, 0, 0)),
