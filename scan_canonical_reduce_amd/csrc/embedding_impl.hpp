@@ -16,7 +16,7 @@
 //     flight, a binary counter of complete subtrees above them).  An aligned
 //     chunk of a sequence is a subtree of its pairwise tree, so the rows of an
 //     id with more than 64 occurrences leave one partial value per chunk.  The
-//     rows that no token names are set to zero by the same waves, 64 rows'
+//     rows that no token names are set to zero by the same waves, some rows'
 //     offsets at a time; every other workgroup does that first, so that the
 //     writes overlap the others' gathers.
 //  3. k_embed_finish: the tree over the partial values.
@@ -67,17 +67,49 @@ __global__ __launch_bounds__(256) void k_embedding(EmbedArgs a)
     }
 }
 
-// x[r][j] (r < 8) becomes the pairwise tree's value over r, in x[0][j]
-template <int V>
-__device__ __forceinline__ void tree8(float (&x)[8][V])
-{
+// The pairwise tree over rows that arrive eight at a time, V columns each: a
+// binary counter of complete subtrees.  Missing rows of the last batch are -0,
+// the exact identity of an addition.
+template <int V, int LEVELS>
+struct PairCounter {
+    float sub[LEVELS][V];  // subtrees of 8, 16, 32, ... rows
+    uint32_t batches = 0;
+
+    __device__ __forceinline__ void add(float (&x)[8][V])
+    {
 #pragma unroll
-    for (int d = 1; d < 8; d *= 2)
+        for (int d = 1; d < 8; d *= 2)
 #pragma unroll
-        for (int r = 0; r < 8; r += 2 * d)
+            for (int r = 0; r < 8; r += 2 * d)
 #pragma unroll
-            for (int j = 0; j < V; ++j) x[r][j] += x[r + d][j];
-}
+                for (int j = 0; j < V; ++j) x[r][j] += x[r + d][j];
+        // the value goes up over the set bits of the count, to the first clear one
+        bool done = false;
+#pragma unroll
+        for (int l = 0; l < LEVELS; ++l) {
+            if (done) continue;
+            if (batches >> l & 1) {
+#pragma unroll
+                for (int j = 0; j < V; ++j) x[0][j] = sub[l][j] + x[0][j];
+            } else {
+#pragma unroll
+                for (int j = 0; j < V; ++j) sub[l][j] = x[0][j];
+                done = true;
+            }
+        }
+        ++batches;
+    }
+    __device__ __forceinline__ void total(float (&acc)[V]) const
+    {
+#pragma unroll
+        for (int j = 0; j < V; ++j) acc[j] = -0.f;
+#pragma unroll
+        for (int l = 0; l < LEVELS; ++l)
+            if (batches >> l & 1)
+#pragma unroll
+                for (int j = 0; j < V; ++j) acc[j] = sub[l][j] + acc[j];
+    }
+};
 
 template <typename G, int V>
 __device__ __forceinline__ void store_grad(const EmbedGradArgs& a, int64_t v, int64_t c,
@@ -99,8 +131,8 @@ __device__ __forceinline__ void store_grad(const EmbedGradArgs& a, int64_t v, in
 // in blocks of that many.
 constexpr int kGroupsInLds = 1024;
 
-// Prefix sums of the counts of groups [first, first + kGroupsInLds), by 256
-// threads; returns the total.
+// Prefix sums of the counts of groups [first, first + kGroupsInLds), by the
+// first 256 threads of the workgroup; returns the total to all.
 __device__ __forceinline__ int64_t group_prefix(const int32_t* counts, int64_t first,
                                                 int64_t groups, int32_t* prefix)
 {
@@ -110,7 +142,7 @@ __device__ __forceinline__ int64_t group_prefix(const int32_t* counts, int64_t f
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const int64_t g = first + tid * 4 + i;
-        c[i] = g < groups ? counts[g] : 0;
+        c[i] = tid < 256 && g < groups ? counts[g] : 0;
         s += c[i];
     }
     int32_t run = s;
@@ -120,16 +152,18 @@ __device__ __forceinline__ int64_t group_prefix(const int32_t* counts, int64_t f
         if ((tid & 63) >= d) run += o;
     }
     __syncthreads();  // the previous block's prefix is no longer read
-    if ((tid & 63) == 63) wave_sum[tid >> 6] = run;
+    if (tid < 256 && (tid & 63) == 63) wave_sum[tid >> 6] = run;
     __syncthreads();
-    int32_t base = run - s;
-    for (int w = 0; w < (tid >> 6); ++w) base += wave_sum[w];
+    if (tid < 256) {
+        int32_t base = run - s;
+        for (int w = 0; w < (tid >> 6); ++w) base += wave_sum[w];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        prefix[tid * 4 + i] = base;
-        base += c[i];
+        for (int i = 0; i < 4; ++i) {
+            prefix[tid * 4 + i] = base;
+            base += c[i];
+        }
+        if (tid == 255) prefix[kGroupsInLds] = base;
     }
-    if (tid == 255) prefix[kGroupsInLds] = base;
     __syncthreads();
     return prefix[kGroupsInLds];
 }
@@ -161,8 +195,7 @@ __device__ __forceinline__ void sum_entry(const EmbedGradArgs& a, int64_t v, int
     const int m = n - c * kEmbedChunk < kEmbedChunk ? (int)(n - c * kEmbedChunk) : kEmbedChunk;
     const int32_t mine = a.order[p0 + (lane < m ? lane : 0)];
     const typename T::store_t* x = static_cast<const typename T::store_t*>(a.dout) + (in ? col : 0);
-    float sub[3][V];  // complete subtrees of 8, 16, 32 rows
-    float all[V];
+    PairCounter<V, 4> tree;
     for (int b = 0; b * 8 < m; ++b) {
         Vec<T, V> raw[8];
 #pragma unroll
@@ -174,40 +207,10 @@ __device__ __forceinline__ void sum_entry(const EmbedGradArgs& a, int64_t v, int
 #pragma unroll
         for (int r = 0; r < 8; ++r)
 #pragma unroll
-            for (int j = 0; j < V; ++j)  // -0: the exact identity of an addition
-                t[r][j] = b * 8 + r < m ? T::load(raw[r].e[j]) : -0.f;
-        tree8<V>(t);
-        // b counts in binary; the value climbs over the set bits
-        int l = 0;
-#pragma unroll
-        for (int lev = 0; lev < 3; ++lev) {
-            if (l != lev) continue;
-            if (b >> lev & 1) {
-#pragma unroll
-                for (int j = 0; j < V; ++j) t[0][j] = sub[lev][j] + t[0][j];
-                l = lev + 1;
-            } else {
-#pragma unroll
-                for (int j = 0; j < V; ++j) sub[lev][j] = t[0][j];
-            }
-        }
-        if (l == 3)
-#pragma unroll
-            for (int j = 0; j < V; ++j) all[j] = t[0][j];
+            for (int j = 0; j < V; ++j) t[r][j] = b * 8 + r < m ? T::load(raw[r].e[j]) : -0.f;
+        tree.add(t);
     }
-    const int nb = (m + 7) / 8;
-    if (nb == 8) {
-#pragma unroll
-        for (int j = 0; j < V; ++j) acc[j] = all[j];
-    } else {
-#pragma unroll
-        for (int j = 0; j < V; ++j) acc[j] = -0.f;
-#pragma unroll
-        for (int lev = 0; lev < 3; ++lev)
-            if (nb >> lev & 1)
-#pragma unroll
-                for (int j = 0; j < V; ++j) acc[j] = sub[lev][j] + acc[j];
-    }
+    tree.total(acc);
     if (!in) return;
     if (n <= kEmbedChunk) {
         store_grad<G, V>(a, v, col, acc);
@@ -222,22 +225,34 @@ __device__ __forceinline__ void sum_entry(const EmbedGradArgs& a, int64_t v, int
     for (int j = 0; j < V; ++j) part[j] = acc[j];
 }
 
-// Zero rows for ids without tokens: a wave takes 64 rows at a time.
+// Sets the rows v0 + (set bits of left) to zero.
+template <typename G, int V>
+__device__ __forceinline__ void zero_listed(const EmbedGradArgs& a, int64_t v0, uint64_t left,
+                                            int lane)
+{
+    while (left) {
+        const int64_t row = v0 + __builtin_ctzll(left);
+        left &= left - 1;
+        typename G::store_t* p = static_cast<typename G::store_t*>(a.dw) + row * a.ld_dw;
+        const float zero[V] = {};
+        for (int64_t c = lane * V; c < a.width; c += 64 * V) st_vec<G, V>(p + c, zero);
+    }
+}
+
+// Rows a wave looks at at a time for ones to set to zero: few enough that a
+// table of 65536 rows keeps 4096 waves busy.
+constexpr int kZeroRows = 16;
+
+// Zero rows for ids without tokens.
 template <typename G, int V>
 __device__ __forceinline__ void zero_rows(const EmbedGradArgs& a, int64_t wave, int64_t waves,
                                           int lane)
 {
-    for (int64_t v0 = wave * 64; v0 < a.rows; v0 += waves * 64) {
+    for (int64_t v0 = wave * kZeroRows; v0 < a.rows; v0 += waves * kZeroRows) {
         const int64_t v = v0 + lane;
-        const bool none = v < a.rows && a.offset[v] == a.offset[v + 1];
-        uint64_t left = __ballot(none);
-        while (left) {
-            const int64_t row = v0 + __builtin_ctzll(left);
-            left &= left - 1;
-            typename G::store_t* p = static_cast<typename G::store_t*>(a.dw) + row * a.ld_dw;
-            const float zero[V] = {};
-            for (int64_t c = lane * V; c < a.width; c += 64 * V) st_vec<G, V>(p + c, zero);
-        }
+        const bool none =
+            lane < kZeroRows && v < a.rows && a.offset[v] == a.offset[v + 1];
+        zero_listed<G, V>(a, v0, __ballot(none), lane);
     }
 }
 
@@ -266,35 +281,116 @@ __global__ __launch_bounds__(256, 4) void k_embed_sum(EmbedGradArgs a, int64_t g
     if (zero && !(blockIdx.x & 1)) zero_rows<G, VZ>(a, wave, waves, lane);
 }
 
+// Up to 256 tokens, one launch and no workspace: a wave keeps all ids, four a
+// lane.  For each (token, slab of columns) it takes, the ballots of "same id" tell
+// whether the token is its id's first, and are the list of occurrences, in order;
+// rows of the table without a token are found the same way.  One
+// launch instead of three (for 100 tokens of 4096 columns, 3000 rows: 36 -> 22
+// us), but an id's occurrences are added by one wave in sequence, which beyond
+// 256 tokens costs more than it saves.
+constexpr int kEmbedDirect = 256;
+
+template <typename T, typename G, int V>
+__global__ __launch_bounds__(256) void k_embed_direct(EmbedGradArgs a)
+{
+    const int lane = threadIdx.x & 63;
+    const int64_t wave = (int64_t)blockIdx.x * 4 + uniform((int32_t)(threadIdx.x >> 6));
+    const int64_t waves = gridDim.x * 4ll;
+    constexpr int C = kEmbedDirect / 64;
+    int32_t id[C];  // of tokens 64 k + lane; -1: none
+#pragma unroll
+    for (int k = 0; k < C; ++k) {
+        const int64_t t = k * 64 + lane;
+        const int64_t v = t < a.tokens ? token_id(a.ids, a.ids64, t) : -1;
+        id[k] = v >= 0 && v < a.rows && v != a.padding_id ? (int32_t)v : -1;
+    }
+    const int32_t slabs = (int32_t)((a.width + 64 * V - 1) / (64 * V));
+    for (int64_t i = wave; i < a.tokens * slabs; i += waves) {
+        const int32_t t = (int32_t)i / slabs, slab = (int32_t)i - t * slabs;
+        int32_t v = -1;
+#pragma unroll
+        for (int k = 0; k < C; ++k)
+            if (t >> 6 == k) v = __builtin_amdgcn_readlane(id[k], t & 63);
+        if (v < 0) continue;
+        uint64_t same[C];
+        int32_t first = -1;
+#pragma unroll
+        for (int k = C - 1; k >= 0; --k) {
+            same[k] = __ballot(id[k] == v);
+            if (same[k]) first = k * 64 + __builtin_ctzll(same[k]);
+        }
+        if (first != t) continue;
+        const int64_t col = (int64_t)slab * 64 * V + lane * V;
+        const bool in = col < a.width;
+        const typename T::store_t* x =
+            static_cast<const typename T::store_t*>(a.dout) + (in ? col : 0);
+        PairCounter<V, 6> tree;
+        int k = 0;
+        uint64_t cur = same[0];
+        bool more = true;
+        while (more) {
+            Vec<T, V> raw[8];
+            int n = 0;
+#pragma unroll
+            for (int r = 0; r < 8; ++r) {
+#pragma unroll
+                for (int q = 1; q < C; ++q)
+                    if (cur == 0 && k < q) {
+                        k = q;
+                        cur = same[q];
+                    }
+                if (cur) {
+                    const int64_t row = k * 64 + __builtin_ctzll(cur);
+                    cur &= cur - 1;
+                    raw[r] = ld_vec<T, V>(x + row * a.ld_dout);
+                    n = r + 1;
+                }
+            }
+            more = n == 8;  // a full batch may be the last: then the next is empty
+            if (n == 0) break;
+            float s[8][V];
+#pragma unroll
+            for (int r = 0; r < 8; ++r)
+#pragma unroll
+                for (int j = 0; j < V; ++j) s[r][j] = r < n ? T::load(raw[r].e[j]) : -0.f;
+            tree.add(s);
+        }
+        float acc[V];
+        tree.total(acc);
+        if (in) store_grad<G, V>(a, v, col, acc);
+    }
+    if (a.accumulate) return;
+    constexpr int VZ = V == 1 ? 1 : 16 / (int)sizeof(typename G::store_t);
+    for (int64_t v0 = wave * kZeroRows; v0 < a.rows; v0 += waves * kZeroRows) {
+        uint64_t left = (1ull << (a.rows - v0 < kZeroRows ? a.rows - v0 : kZeroRows)) - 1;
+#pragma unroll
+        for (int k = 0; k < C; ++k) {
+            uint64_t hit = __ballot(id[k] >= v0 && id[k] < v0 + kZeroRows);
+            while (hit) {
+                const int32_t v = __builtin_amdgcn_readlane(id[k], __builtin_ctzll(hit));
+                hit &= hit - 1;
+                left &= ~(1ull << (v - v0));
+            }
+        }
+        zero_listed<G, VZ>(a, v0, left, lane);
+    }
+}
+
 // Rows with more than 64 occurrences: the pairwise tree over the partial
-// values, an aligned power-of-two range of them per wave, then over the 16
+// values, an aligned power-of-two range of them per wave, then over the
 // waves.  A lane holds four neighbouring columns (the partial values' rows are
 // padded to that).
+constexpr int kFinishWaves = 8;
+
 template <typename G>
-__global__ __launch_bounds__(1024) void k_embed_finish(EmbedGradArgs a, int64_t groups)
+__global__ __launch_bounds__(64 * kFinishWaves) void k_embed_finish(EmbedGradArgs a, int64_t groups)
 {
     __shared__ int32_t prefix[kGroupsInLds + 1];
-    __shared__ int32_t wsum[16];
-    __shared__ float4 waves[16][64];
+    __shared__ float4 waves[kFinishWaves][64];
     const int lane = threadIdx.x & 63, w = uniform((int32_t)(threadIdx.x >> 6));
     const int64_t slabs = (a.width + 255) / 256;
     for (int64_t g0 = 0; g0 < groups; g0 += kGroupsInLds) {
-        const int32_t c = g0 + threadIdx.x < groups ? a.n_long[g0 + threadIdx.x] : 0;
-        int32_t run = c;
-#pragma unroll
-        for (int d = 1; d < 64; d *= 2) {
-            const int32_t o = __shfl_up(run, d, 64);
-            if (lane >= d) run += o;
-        }
-        __syncthreads();
-        if (lane == 63) wsum[w] = run;
-        __syncthreads();
-        int32_t base = run - c;
-        for (int k = 0; k < w; ++k) base += wsum[k];
-        prefix[threadIdx.x] = base;
-        if (threadIdx.x == 1023) prefix[kGroupsInLds] = base + c;
-        __syncthreads();
-        const int64_t total = prefix[kGroupsInLds];
+        const int64_t total = group_prefix(a.n_long, g0, groups, prefix);
         for (int64_t i = blockIdx.x; i < total * slabs; i += gridDim.x) {
             const int32_t e = (int32_t)(i / slabs);
             const int64_t col = (i - e * slabs) * 256 + lane * 4;
@@ -304,14 +400,12 @@ __global__ __launch_bounds__(1024) void k_embed_finish(EmbedGradArgs a, int64_t 
             const int32_t off = uniform(a.offset[v]), n = uniform(a.offset[v + 1]) - off;
             const int32_t m = (n + kEmbedChunk - 1) / kEmbedChunk;
             int32_t range = 1;  // partial values per wave
-            while (range * 16 < m) range *= 2;
+            while (range * kFinishWaves < m) range *= 2;
             const int32_t lo = w * range, hi = lo + range < m ? lo + range : m;
             const float* part = a.part + off / kEmbedChunk * a.ld_part + (in ? col : 0);
             const float* last =
                 a.part_last + (off + (m - 1) * kEmbedChunk) / kEmbedChunk * a.ld_part + (in ? col : 0);
-            constexpr int kLevels = 18;  // 2^30 / 64 / 16 / 8 batches
-            float st[kLevels][4];
-            int32_t count = 0;
+            PairCounter<4, 19> tree;  // up to 2^30 / 64 / 8 / 8 batches
             for (int32_t b = lo; b < hi; b += 8) {
                 float x[8][4];
 #pragma unroll
@@ -322,41 +416,24 @@ __global__ __launch_bounds__(1024) void k_embed_finish(EmbedGradArgs a, int64_t 
                         p = *reinterpret_cast<const float4*>(j == m - 1 ? last : part + j * a.ld_part);
                     x[r][0] = p.x, x[r][1] = p.y, x[r][2] = p.z, x[r][3] = p.w;
                 }
-                tree8<4>(x);
-                bool done = false;
-#pragma unroll
-                for (int lev = 0; lev < kLevels; ++lev) {
-                    if (done) continue;
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        if (count >> lev & 1)
-                            x[0][j] = st[lev][j] + x[0][j];
-                        else
-                            st[lev][j] = x[0][j];
-                    }
-                    done = !(count >> lev & 1);
-                }
-                ++count;
+                tree.add(x);
             }
-            float acc[4] = {-0.f, -0.f, -0.f, -0.f};
-#pragma unroll
-            for (int lev = 0; lev < kLevels; ++lev)
-                if (count >> lev & 1)
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) acc[j] = st[lev][j] + acc[j];
+            float acc[4];
+            tree.total(acc);
             waves[w][lane] = make_float4(acc[0], acc[1], acc[2], acc[3]);
             __syncthreads();
-            // wave w finishes columns 16 w .. of the 256, one lane each
-            if (lane < 16) {
-                const int x = w * 16 + lane;
+            // wave w finishes its 256 / kFinishWaves columns, one a lane
+            if (lane < 256 / kFinishWaves) {
+                const int x = w * (256 / kFinishWaves) + lane;
                 const int64_t at = (i - e * slabs) * 256 + x;
-                float s[16];
+                float s[kFinishWaves];
 #pragma unroll
-                for (int j = 0; j < 16; ++j) s[j] = reinterpret_cast<const float*>(waves[j])[x];
+                for (int j = 0; j < kFinishWaves; ++j)
+                    s[j] = reinterpret_cast<const float*>(waves[j])[x];
 #pragma unroll
-                for (int d = 1; d < 16; d *= 2)
+                for (int d = 1; d < kFinishWaves; d *= 2)
 #pragma unroll
-                    for (int j = 0; j < 16; j += 2 * d) s[j] += s[j + d];
+                    for (int j = 0; j < kFinishWaves; j += 2 * d) s[j] += s[j + d];
                 const float one[1] = {s[0]};
                 if (at < a.width) store_grad<G, 1>(a, v, at, one);
             }
@@ -383,22 +460,28 @@ template <typename T, typename G>
 hipError_t launch_embedding_grad(const EmbedGradArgs& a, hipStream_t st)
 {
     constexpr int V = 16 / (int)sizeof(typename T::store_t);
-    const int64_t groups = id_groups(a.rows);
-    if (hipError_t e = launch_embedding_group(a, st)) return e;
     // four workgroups fit a compute unit (k_embed_sum's launch bound)
     const int64_t cus = (int64_t)device_cus(), cap = cus * 4;
     const int64_t slabs = (a.width + 64 * (a.vec ? V : 1) - 1) / (64 * (a.vec ? V : 1));
     const int64_t want = (a.tokens * slabs + (a.accumulate ? 0 : a.rows) + 3) / 4;
     const dim3 grid((unsigned)capped_grid(want < 1 ? 1 : want < cap ? want : cap));
+    if (a.tokens <= kEmbedDirect) {
+        if (a.vec)
+            k_embed_direct<T, G, V><<<grid, dim3(256), 0, st>>>(a);
+        else
+            k_embed_direct<T, G, 1><<<grid, dim3(256), 0, st>>>(a);
+        return hipGetLastError();
+    }
+    const int64_t groups = id_groups(a.rows);
+    if (hipError_t e = launch_embedding_group(a, st)) return e;
     if (a.vec)
         k_embed_sum<T, G, V><<<grid, dim3(256), 0, st>>>(a, groups);
     else
         k_embed_sum<T, G, 1><<<grid, dim3(256), 0, st>>>(a, groups);
     if (hipError_t e = hipGetLastError()) return e;
     const int64_t most = a.tokens / (kEmbedChunk + 1) * ((a.width + 255) / 256);
-    if (most == 0) return hipSuccess;  // too few tokens for a row with partial values
-    k_embed_finish<G><<<dim3((unsigned)capped_grid(most < cus ? most : cus)), dim3(1024), 0,
-                        st>>>(a, groups);
+    k_embed_finish<G><<<dim3((unsigned)capped_grid(most < cus ? most : cus)), dim3(64 * kFinishWaves),
+                        0, st>>>(a, groups);
     return hipGetLastError();
 }
 
