@@ -510,79 +510,96 @@ hipError_t launch_scan_carry(const ScanArgs& a, const float* first, float* last,
     return hipGetLastError();
 }
 
-// One row of each sequence: a lane holds KS states of a channel and four rows
-// of lanes a channel, as above; the state is read and written once, which is
-// nearly all of the traffic.
-template <typename T, int KS>
+// One row of each sequence: a lane holds KS states of a channel and four
+// neighbouring lanes a channel, so a wave's state accesses are contiguous; the
+// state is read and written once, which is nearly all of the traffic.  A thread
+// takes SEQS sequences, all their loads in flight together.
+template <typename T, int KS, int SEQS>
 __global__ __launch_bounds__(256) void k_selective_scan_step(ScanArgs a)
 {
     const int slabs = a.slabs * (a.channels / a.dg);
-    const int64_t s = blockIdx.x / slabs;
-    // states of a channel in neighbouring lanes, so a wave's state accesses are
-    // contiguous: q = lane mod 4 here
+    const int64_t part = blockIdx.x / slabs;
     const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
-    const int slab = (int)(blockIdx.x - s * slabs);
-    const int g = slab / a.slabs, q = lane & 3;
-    const int32_t in_g = (slab - g * a.slabs) * kSlab + w * 16 + (lane >> 2);
-    if (in_g >= a.dg) return;  // whole groups of four lanes
-    const int32_t ch = g * a.dg + in_g;
-
-    const float u = ld<T>(static_cast<typename T::store_t*>(a.u.p) + s * a.u.seq + ch);
-    float raw = ld<T>(static_cast<typename T::store_t*>(a.delta.p) + s * a.delta.seq + ch);
-    if (a.bias) raw += a.bias[ch];
-    const float d = a.softplus ? softplus_f<T>(raw) : raw;
-    const float du = d * u;
+    const int slab = (int)(blockIdx.x - part * slabs);
     Lane l{};
-    l.q = q;
-    l.g = g;
-    LaneBC<T, KS> xb, xc;
-    xb.init(a, a.B, l, s, 0);
-    xc.init(a, a.C, l, s, 0);
-    xb.load(a, l, 1);
-    xc.load(a, l, 1);
-    float B[KS], C[KS];
-    xb.get(B);
-    xc.get(C);
-    const int64_t at = (s * a.channels + ch) * a.states + q * KS;
-    const bool vec = a.st_vec;
-    float h[KS], A2[KS];
+    l.g = slab / a.slabs;
+    l.q = lane & 3;
+    const int32_t in_g = (slab - l.g * a.slabs) * kSlab + w * 16 + (lane >> 2);
+    if (in_g >= a.dg) return;  // whole groups of four lanes
+    const int32_t ch = l.g * a.dg + in_g;
+    const int64_t s0 = part * SEQS;
+    const int seqs = a.q.seqs - s0 < SEQS ? (int)(a.q.seqs - s0) : SEQS;
+    const int64_t at = ch * (int64_t)a.states + l.q * KS;
+    const int64_t per = (int64_t)a.channels * a.states;
+    const bool gate = a.z.p != nullptr;
+
+    typename T::store_t u[SEQS], dl[SEQS], z[SEQS];
+    LaneBC<T, KS> B[SEQS], C[SEQS];
+    float h[SEQS][KS], A2[KS];
 #pragma unroll
-    for (int i = 0; i < KS; ++i) h[i] = 0.f;
-    if (vec) {
-        ld_states<KS>(a.A + (int64_t)ch * a.states + q * KS, A2);
-        if (a.init) ld_states<KS>(a.init + at, h);
+    for (int j = 0; j < SEQS; ++j) {
+        const int64_t s = s0 + (j < seqs ? j : 0);
+        u[j] = static_cast<typename T::store_t*>(a.u.p)[s * a.u.seq + ch];
+        dl[j] = static_cast<typename T::store_t*>(a.delta.p)[s * a.delta.seq + ch];
+        if (gate) z[j] = static_cast<typename T::store_t*>(a.z.p)[s * a.z.seq + ch];
+        B[j].init(a, a.B, l, s, 0);
+        C[j].init(a, a.C, l, s, 0);
+        B[j].load(a, l, 1);
+        C[j].load(a, l, 1);
+#pragma unroll
+        for (int i = 0; i < KS; ++i) h[j][i] = 0.f;
+        if (a.init) {
+            if (a.st_vec) {
+                ld_states<KS>(a.init + s * per + at, h[j]);
+            } else {
+#pragma unroll
+                for (int i = 0; i < KS; ++i)
+                    if (l.q * KS + i < a.states) h[j][i] = a.init[s * per + at + i];
+            }
+        }
+    }
+    if (a.st_vec) {
+        ld_states<KS>(a.A + at, A2);
     } else {
 #pragma unroll
+        for (int i = 0; i < KS; ++i) A2[i] = l.q * KS + i < a.states ? a.A[at + i] : 0.f;
+    }
+#pragma unroll
+    for (int i = 0; i < KS; ++i) A2[i] *= kLog2e;
+    const float bias = a.bias ? a.bias[ch] : 0.f, Dc = a.D ? a.D[ch] : 0.f;
+#pragma unroll
+    for (int j = 0; j < SEQS; ++j) {
+        if (j >= seqs) break;
+        const int64_t s = s0 + j;
+        const float x = T::load(u[j]), raw = T::load(dl[j]) + bias;
+        const float d = a.softplus ? softplus_f<T>(raw) : raw;
+        const float du = d * x;
+        float b[KS], c[KS], y = 0.f;
+        B[j].get(b);
+        C[j].get(c);
+#pragma unroll
         for (int i = 0; i < KS; ++i) {
-            const bool real = q * KS + i < a.states;
-            A2[i] = real ? a.A[(int64_t)ch * a.states + q * KS + i] : 0.f;
-            if (a.init && real) h[i] = a.init[at + i];
+            h[j][i] = fma32(exp2_hw(d * A2[i]), h[j][i], b[i] * du);
+            y = i == 0 ? c[i] * h[j][i] : fma32(c[i], h[j][i], y);
         }
-    }
-    float y = 0.f;
+        if (a.final) {
+            if (a.st_vec) {
+                st_states<KS>(a.final + s * per + at, h[j]);
+            } else {
 #pragma unroll
-    for (int i = 0; i < KS; ++i) {
-        h[i] = fma32(exp2_hw(d * (A2[i] * kLog2e)), h[i], B[i] * du);
-        y = i == 0 ? C[i] * h[i] : fma32(C[i], h[i], y);
-    }
-    if (a.final) {
-        if (vec) {
-            st_states<KS>(a.final + at, h);
-        } else {
-#pragma unroll
-            for (int i = 0; i < KS; ++i)
-                if (q * KS + i < a.states) a.final[at + i] = h[i];
+                for (int i = 0; i < KS; ++i)
+                    if (l.q * KS + i < a.states) a.final[s * per + at + i] = h[j][i];
+            }
         }
+        y += dpp<0xb1>(y);  // lanes of the channel: neighbour, then pair
+        y += dpp<0x4e>(y);
+        y = fma32(Dc, x, y);
+        if (gate) {
+            const float zz = T::load(z[j]);
+            y *= silu_f(zz, sigmoid_f<T>(zz));
+        }
+        if (l.q == 0) static_cast<typename T::store_t*>(a.out.p)[s * a.out.seq + ch] = T::round(y);
     }
-    y += dpp<0xb1>(y);  // lanes of the channel: neighbour, then pair
-    y += dpp<0x4e>(y);
-    if (q != 0) return;
-    if (a.D) y = fma32(a.D[ch], u, y);
-    if (a.z.p) {
-        const float z = ld<T>(static_cast<typename T::store_t*>(a.z.p) + s * a.z.seq + ch);
-        y *= silu_f(z, sigmoid_f<T>(z));
-    }
-    st<T>(static_cast<typename T::store_t*>(a.out.p) + s * a.out.seq + ch, y);
 }
 
 // ---------------------------------------------------------------------- launches
@@ -618,16 +635,28 @@ hipError_t launch_selective_scan(const ScanArgs& a, int64_t groups, hipStream_t 
     }
 }
 
+template <typename T, int KS>
+hipError_t launch_scan_step_ks(const ScanArgs& a, int64_t groups, hipStream_t st)
+{
+    const int64_t slabs = groups * a.slabs;
+    // four sequences a thread once that still gives every compute unit several
+    // workgroups
+    if (a.q.seqs * slabs >= 8192)
+        k_selective_scan_step<T, KS, 4>
+            <<<dim3((unsigned)((a.q.seqs + 3) / 4 * slabs)), dim3(256), 0, st>>>(a);
+    else
+        k_selective_scan_step<T, KS, 1><<<dim3((unsigned)(a.q.seqs * slabs)), dim3(256), 0, st>>>(a);
+    return hipGetLastError();
+}
+
 template <typename T>
 hipError_t launch_selective_scan_step(const ScanArgs& a, int64_t groups, hipStream_t st)
 {
-    const dim3 grid((unsigned)(a.q.seqs * groups * a.slabs)), block(256);
     switch (scan_ks(a.states)) {
-        case 1: k_selective_scan_step<T, 1><<<grid, block, 0, st>>>(a); break;
-        case 2: k_selective_scan_step<T, 2><<<grid, block, 0, st>>>(a); break;
-        default: k_selective_scan_step<T, 4><<<grid, block, 0, st>>>(a); break;
+        case 1: return launch_scan_step_ks<T, 1>(a, groups, st);
+        case 2: return launch_scan_step_ks<T, 2>(a, groups, st);
+        default: return launch_scan_step_ks<T, 4>(a, groups, st);
     }
-    return hipGetLastError();
 }
 
 }  // namespace seq

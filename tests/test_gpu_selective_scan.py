@@ -308,6 +308,25 @@ def test_step(canon, dtype, channels, groups, states):
         seq_ref.close(state, h, hsize, terms(1), "state")
 
 
+@pytest.mark.parametrize("channels,groups,states", [(40, 2, 16), (17, 1, 13), (64, 1, 8)])
+def test_step_of_many_sequences(canon, channels, groups, states):
+    """Enough sequences that a thread takes four: the bits of a few alone."""
+    n = 8195
+    d = cuda(inputs(BF16, [1] * n, channels, groups, states, False, channels))
+    row = {k: v[:, 0] if k in ("u", "delta", "z", "B", "C") else v for k, v in d.items()}
+
+    def go(at, state):
+        return canon.selective_scan_step(state, row["u"][at], row["delta"][at], row["A"],
+                                         row["B"][at], row["C"][at], D=row["D"], z=row["z"][at],
+                                         delta_bias=row["bias"], delta_softplus=True)
+
+    state = d["init"].clone()
+    out = go(slice(None), state)
+    for at in (slice(0, 9), slice(4095, 4100), slice(n - 3, n)):
+        few = d["init"][at].clone()
+        assert torch.equal(go(at, few), out[at]) and torch.equal(few, state[at])
+
+
 def test_step_without_groups_dimension_and_strides(canon):
     d = cuda(inputs(BF16, [1] * 6, 48, 1, 16, False))
     big = torch.randn(6, 300, device="cuda").to(BF16)
