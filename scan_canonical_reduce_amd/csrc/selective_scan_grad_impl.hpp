@@ -71,7 +71,8 @@ __device__ __forceinline__ void bcast_fma(const float (&b)[KS], float x, float (
             "v_fmac_f32_dpp %0, %4, %8 row_newbcast:%9 row_mask:0xf bank_mask:0xf\n\t"
             "v_fmac_f32_dpp %1, %5, %8 row_newbcast:%9 row_mask:0xf bank_mask:0xf\n\t"
             "v_fmac_f32_dpp %2, %6, %8 row_newbcast:%9 row_mask:0xf bank_mask:0xf\n\t"
-            "v_fmac_f32_dpp %3, %7, %8 row_newbcast:%9 row_mask:0xf bank_mask:0xf"
+            "v_fmac_f32_dpp %3, %7, %8 row_newbcast:%9 row_mask:0xf bank_mask:0xf\n\t"
+            "s_nop 1"
             : "+v"(y[0]), "+v"(y[1]), "+v"(y[2]), "+v"(y[3])
             : "v"(b[0]), "v"(b[1]), "v"(b[2]), "v"(b[3]), "v"(x), "n"(T));
     else
@@ -139,11 +140,12 @@ __global__ __launch_bounds__(256) void k_scan_back_sum(ScanArgs a)
                 const float z = T::load(tile.z[r]);
                 dy[r] *= silu_f(z, sigmoid_f<T>(z));
             }
+        if (len < kSub)
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-            const bool valid = 4 * r + l.q < len;
-            ex[4 * r + l.q][l.c] = make_float2(valid ? dl[r] : 0.f, valid ? dy[r] : 0.f);
-        }
+            for (int r = 0; r < 4; ++r)
+                if (4 * r + l.q >= len) dl[r] = dy[r] = 0.f;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) ex[4 * r + l.q][l.c] = make_float2(dl[r], dy[r]);
         wave_lds_fence();
         if (sub > 0) tile.load(a, l, kSub, gate);
         back_rows<KS, kSub - 1>(ex, l.c, A2, C, R, sdl);
@@ -154,12 +156,12 @@ __global__ __launch_bounds__(256) void k_scan_back_sum(ScanArgs a)
     if (l.q == 0) a.ws_dl[slot * a.channels + l.ch] = sdl;
 }
 
-// One level of the sum over a row's 16 lanes: a lane without the level's bit of
-// c gets x plus the mirrored lane's x, a lane with it y plus the mirrored
-// lane's y.  Mirrors over 16 and 8 lanes pair whole banks of four, so both sums
-// write their own banks of the result (two instructions; the s_nop covers the
-// wait states between a write and its use by DPP, which the compiler does not
-// see here); below that the lanes select first (three).
+// One level of the sum over a row's 16 lanes, for KS values: a lane without the
+// level's bit of c gets x plus the mirrored lane's x, a lane with it y plus the
+// mirrored lane's y.  Mirrors over 16 and 8 lanes pair whole banks of four, so
+// both sums write their own banks of the result, two instructions a value; below
+// that the lanes select first, three instructions, by masks that are constants
+// in scalar registers.
 #define CANON_FOLD_BANKS(NAME, CTRL, LOWER, UPPER)                                              \
     template <int KS>                                                                           \
     __device__ __forceinline__ void NAME(const float (&x)[KS], const float (&y)[KS],            \
@@ -174,7 +176,8 @@ __global__ __launch_bounds__(256) void k_scan_back_sum(ScanArgs a)
                 "v_add_f32_dpp %0, %8, %8 " CTRL " row_mask:0xf bank_mask:" UPPER "\n\t"        \
                 "v_add_f32_dpp %1, %9, %9 " CTRL " row_mask:0xf bank_mask:" UPPER "\n\t"        \
                 "v_add_f32_dpp %2, %10, %10 " CTRL " row_mask:0xf bank_mask:" UPPER "\n\t"      \
-                "v_add_f32_dpp %3, %11, %11 " CTRL " row_mask:0xf bank_mask:" UPPER              \
+                "v_add_f32_dpp %3, %11, %11 " CTRL " row_mask:0xf bank_mask:" UPPER "\n\t"      \
+                "s_nop 1"                                                                       \
                 : "=&v"(r[0]), "=&v"(r[1]), "=&v"(r[2]), "=&v"(r[3])                            \
                 : "v"(x[0]), "v"(x[1]), "v"(x[2]), "v"(x[3]), "v"(y[0]), "v"(y[1]), "v"(y[2]),  \
                   "v"(y[3]));                                                                   \
@@ -182,7 +185,8 @@ __global__ __launch_bounds__(256) void k_scan_back_sum(ScanArgs a)
             for (int i = 0; i < KS; ++i)                                                        \
                 asm("s_nop 1\n\t"                                                               \
                     "v_add_f32_dpp %0, %1, %1 " CTRL " row_mask:0xf bank_mask:" LOWER "\n\t"    \
-                    "v_add_f32_dpp %0, %2, %2 " CTRL " row_mask:0xf bank_mask:" UPPER            \
+                    "v_add_f32_dpp %0, %2, %2 " CTRL " row_mask:0xf bank_mask:" UPPER "\n\t"    \
+                    "s_nop 1"                                                                   \
                     : "=&v"(r[i])                                                               \
                     : "v"(x[i]), "v"(y[i]));                                                    \
     }
@@ -190,14 +194,44 @@ CANON_FOLD_BANKS(fold16, "row_mirror", "0x3", "0xc")
 CANON_FOLD_BANKS(fold8, "row_half_mirror", "0x5", "0xa")
 #undef CANON_FOLD_BANKS
 
-template <int CTRL>
-__device__ __forceinline__ float fold_lanes(float x, float y, bool upper)
-{
-    const float keep = upper ? y : x, send = upper ? x : y;
-    return keep + dpp<CTRL>(send);
-}
-
-constexpr int kMirror4 = 0x1b, kMirror2 = 0xb1;
+#define CANON_FOLD_SELECT(NAME, CTRL, MASK)                                                     \
+    template <int KS>                                                                           \
+    __device__ __forceinline__ void NAME(const float (&x)[KS], const float (&y)[KS],            \
+                                         float (&r)[KS])                                        \
+    {                                                                                           \
+        const uint64_t upper = MASK;                                                            \
+        float t[KS];                                                                            \
+        if constexpr (KS == 4)                                                                  \
+            asm("v_cndmask_b32_e64 %4, %12, %8, %16\n\t"                                        \
+                "v_cndmask_b32_e64 %5, %13, %9, %16\n\t"                                        \
+                "v_cndmask_b32_e64 %6, %14, %10, %16\n\t"                                       \
+                "v_cndmask_b32_e64 %7, %15, %11, %16\n\t"                                       \
+                "v_cndmask_b32_e64 %0, %8, %12, %16\n\t"                                        \
+                "v_cndmask_b32_e64 %1, %9, %13, %16\n\t"                                        \
+                "v_cndmask_b32_e64 %2, %10, %14, %16\n\t"                                       \
+                "v_cndmask_b32_e64 %3, %11, %15, %16\n\t"                                       \
+                "v_add_f32_dpp %0, %4, %0 " CTRL " row_mask:0xf bank_mask:0xf\n\t"              \
+                "v_add_f32_dpp %1, %5, %1 " CTRL " row_mask:0xf bank_mask:0xf\n\t"              \
+                "v_add_f32_dpp %2, %6, %2 " CTRL " row_mask:0xf bank_mask:0xf\n\t"              \
+                "v_add_f32_dpp %3, %7, %3 " CTRL " row_mask:0xf bank_mask:0xf\n\t"              \
+                "s_nop 1"                                                                       \
+                : "=&v"(r[0]), "=&v"(r[1]), "=&v"(r[2]), "=&v"(r[3]), "=&v"(t[0]), "=&v"(t[1]), \
+                  "=&v"(t[2]), "=&v"(t[3])                                                      \
+                : "v"(x[0]), "v"(x[1]), "v"(x[2]), "v"(x[3]), "v"(y[0]), "v"(y[1]), "v"(y[2]),  \
+                  "v"(y[3]), "s"(upper));                                                       \
+        else                                                                                    \
+            for (int i = 0; i < KS; ++i)                                                        \
+                asm("v_cndmask_b32_e64 %1, %3, %2, %4\n\t"                                      \
+                    "v_cndmask_b32_e64 %0, %2, %3, %4\n\t"                                      \
+                    "s_nop 1\n\t"                                                               \
+                    "v_add_f32_dpp %0, %1, %0 " CTRL " row_mask:0xf bank_mask:0xf\n\t"          \
+                    "s_nop 1"                                                                   \
+                    : "=&v"(r[i]), "=&v"(t[i])                                                  \
+                    : "v"(x[i]), "v"(y[i]), "s"(upper));                                        \
+    }
+CANON_FOLD_SELECT(fold4, "quad_perm:[3,2,1,0]", 0xccccccccccccccccull)
+CANON_FOLD_SELECT(fold2, "quad_perm:[1,0,3,2]", 0xaaaaaaaaaaaaaaaaull)
+#undef CANON_FOLD_SELECT
 
 // Sums over the lanes of a row, sequence rows arriving in descending order T =
 // 15 .. 0; v[L] holds what waits for its partner at level L.
@@ -206,28 +240,27 @@ struct LaneSum {
     float wait[4][KS];
 
     template <int T>
-    __device__ __forceinline__ void add(float (&x)[KS], int c)
+    __device__ __forceinline__ void add(float (&x)[KS])
     {
-        float a[KS], b[KS];
         if constexpr (T & 1) {
             copy(x, wait[0]);
         } else {
+            float a[KS];
             fold16<KS>(x, wait[0], a);
             if constexpr (T & 2) {
                 copy(a, wait[1]);
             } else {
+                float b[KS];
                 fold8<KS>(a, wait[1], b);
-#pragma unroll
-                for (int i = 0; i < KS; ++i) {
-                    if constexpr (T & 4) {
-                        wait[2][i] = b[i];
-                    } else {
-                        const float d = fold_lanes<kMirror4>(b[i], wait[2][i], c & 2);
-                        if constexpr (T & 8)
-                            wait[3][i] = d;
-                        else
-                            x[i] = fold_lanes<kMirror2>(d, wait[3][i], c & 1);
-                    }
+                if constexpr (T & 4) {
+                    copy(b, wait[2]);
+                } else {
+                    float d[KS];
+                    fold4<KS>(b, wait[2], d);
+                    if constexpr (T & 8)
+                        copy(d, wait[3]);
+                    else
+                        fold2<KS>(d, wait[3], x);
                 }
             }
         }
@@ -298,8 +331,8 @@ __device__ __forceinline__ void grad_row(const RowIn& x, int c, GradRegs<KS>& g,
         decay = i == 0 ? g.A2[i] * d : fma32(g.A2[i], d, decay);
     }
     dc = decay;
-    g.sb.template add<T>(b, c);
-    g.sc.template add<T>(s, c);
+    g.sb.template add<T>(b);
+    g.sc.template add<T>(s);
     if constexpr (T == 0) {
 #pragma unroll
         for (int i = 0; i < KS; ++i) {
@@ -435,14 +468,18 @@ __global__ __launch_bounds__(256, 2) void k_selective_scan_grad(ScanArgs a)
                     gw[r] = dy[r] * silu_slope(z, q);
                     dy[r] *= silu_f(z, q);
                 }
+            float u[4];
+#pragma unroll
+            for (int r = 0; r < 4; ++r) u[r] = T::load(tile.u[r]);
+            // rows past the end and channels past the last: nothing is added
+            if (len < kSub || l.wch + 16 > a.dg)
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+                    if (!l.active || 4 * r + l.q >= len) dl[r] = u[r] = dy[r] = 0.f;
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
-                // rows past the end and channels past the last: nothing is added
-                const bool valid = l.active && 4 * r + l.q < len;
-                const float u = valid ? T::load(tile.u[r]) : 0.f;
-                const float d = valid ? dl[r] : 0.f;
-                ex.a[4 * r + l.q][l.c] = make_float2(d, d * u);
-                ex.b[4 * r + l.q][l.c] = make_float2(valid ? dy[r] : 0.f, u);
+                ex.a[4 * r + l.q][l.c] = make_float2(dl[r], dl[r] * u[r]);
+                ex.b[4 * r + l.q][l.c] = make_float2(dy[r], u[r]);
                 ex.c[4 * r + l.q][l.c] = make_float2(slope[r], gw[r]);
             }
         }

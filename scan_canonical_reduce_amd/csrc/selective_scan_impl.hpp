@@ -14,9 +14,14 @@
 //   - y is summed over a lane's states, then over the four rows of lanes, four
 //     sequence rows at a time (permlane swaps: 6 instructions for 4 rows),
 //     which leaves it where the gate and the store want it.
-// Per (row, channel, state) that is 2 multiplications, 1 exponential (two
-// issue slots) and 2 FMAs, so the kernel is bound by vector issue: a pass
-// without recomputation needs 6 slots of 4 cycles for 64 lanes.
+// Per (row, channel, state) that is 2 multiplications, 1 exponential and 2 FMAs
+// (3 in the kernel that walks whole sequences).  Measured on one SIMD of an
+// MI355X, in cycles a wave: FMA or product of vector registers 2.8, with a DPP
+// operand 4.5, exponential 8.4, lane swap 8; so about 23 cycles for 64 values,
+// and the kernel is bound by vector issue, not by memory: at 8 x 2048 x 4096 and
+// 16 states the values alone take 170 us of the 400 (whole sequences, which also
+// save the states for the backward pass), of 142 for one sequence of 16384 x 2048
+// in chunks, whose sums from zero take another 107.
 #pragma once
 
 #include "launch.hpp"
@@ -225,8 +230,11 @@ __device__ __forceinline__ void step_sizes(const ScanArgs& a, const typename T::
 
 // sum over i of lane T's b[i] (of each row of 16 lanes) times x[i], as one
 // product and KS - 1 FMAs that take b through DPP; the compiler would broadcast
-// each b[i] by an instruction of its own.  The s_nop covers the two wait states
-// between a write of b and its use by DPP, which the compiler does not see here.
+// each b[i] by an instruction of its own.  DPP and lane swaps read a register
+// only two wait states after a vector instruction wrote it, and the compiler
+// does not see into these blocks: the first s_nop is for a b[i] written just
+// before, the last for a user of the result.  (Every block of this kind here
+// and in the backward pass opens and closes so.)
 template <int T, int KS>
 __device__ __forceinline__ float bcast_dot(const float (&b)[KS], const float (&x)[KS])
 {
@@ -236,14 +244,16 @@ __device__ __forceinline__ float bcast_dot(const float (&b)[KS], const float (&x
             "v_mul_f32_dpp %0, %1, %5 row_newbcast:%9 row_mask:0xf bank_mask:0xf\n\t"
             "v_fmac_f32_dpp %0, %2, %6 row_newbcast:%9 row_mask:0xf bank_mask:0xf\n\t"
             "v_fmac_f32_dpp %0, %3, %7 row_newbcast:%9 row_mask:0xf bank_mask:0xf\n\t"
-            "v_fmac_f32_dpp %0, %4, %8 row_newbcast:%9 row_mask:0xf bank_mask:0xf"
+            "v_fmac_f32_dpp %0, %4, %8 row_newbcast:%9 row_mask:0xf bank_mask:0xf\n\t"
+            "s_nop 1"
             : "=&v"(y)
             : "v"(b[0]), "v"(b[1]), "v"(b[2]), "v"(b[3]), "v"(x[0]), "v"(x[1]), "v"(x[2]),
               "v"(x[3]), "n"(T));
     else if constexpr (KS == 2)
         asm("s_nop 1\n\t"
             "v_mul_f32_dpp %0, %1, %3 row_newbcast:%5 row_mask:0xf bank_mask:0xf\n\t"
-            "v_fmac_f32_dpp %0, %2, %4 row_newbcast:%5 row_mask:0xf bank_mask:0xf"
+            "v_fmac_f32_dpp %0, %2, %4 row_newbcast:%5 row_mask:0xf bank_mask:0xf\n\t"
+            "s_nop 1"
             : "=&v"(y)
             : "v"(b[0]), "v"(b[1]), "v"(x[0]), "v"(x[1]), "n"(T));
     else
@@ -372,15 +382,19 @@ __global__ __launch_bounds__(256, 4) void k_selective_scan(ScanArgs a)
     for (int32_t row = lo; row < hi; row += kSub) {
         const int32_t len = hi - row;
         const int sub = row / kSub % kSubs;
-        float u[4], dl[4], raw[4], gz[4], B[KS], C[KS];
+        float u[4], dl[4], raw[4], dlu[4], gz[4], B[KS], C[KS];
         step_sizes<T>(a, tile.dl, bias, raw, dl);
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
             u[r] = T::load(tile.u[r]);
-            // a row past the end: exp(0) = 1 and nothing added
-            const bool valid = 4 * r + l.q < len;
-            ex[4 * r + l.q][l.c] = make_float2(valid ? dl[r] : 0.f, valid ? dl[r] * u[r] : 0.f);
+            dlu[r] = dl[r] * u[r];
         }
+        if (len < kSub)  // rows past the end: exp(0) = 1 and nothing added
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+                if (4 * r + l.q >= len) dl[r] = dlu[r] = 0.f;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) ex[4 * r + l.q][l.c] = make_float2(dl[r], dlu[r]);
         if (MODE != kSum && gate)
 #pragma unroll
             for (int r = 0; r < 4; ++r) {

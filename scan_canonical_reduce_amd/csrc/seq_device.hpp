@@ -90,19 +90,26 @@ __device__ __forceinline__ float exp2_hw(float x) { return __builtin_amdgcn_exp2
 // 1 / x to 1 ulp
 __device__ __forceinline__ float rcp_hw(float x) { return __builtin_amdgcn_rcpf(x); }
 
-// exp(x).  float32 activations: to about 1.5 ulp, with the product x log2(e)
-// in two parts, the lower one through exp2(r) = 1 + r ln 2 (an infinite or
-// vanishing result has no lower part: the remainder of an infinite product
-// would be a NaN).  16-bit activations: the high part alone, whose relative
-// error, |x| 2^-24 and the exponential's ulp, is far below theirs.
+// Limits are taken by clamps (one instruction), not by comparison and selection
+// (two).
+constexpr float kMaxF = 0x1.fffffep+127f;
+__device__ __forceinline__ float clamp_f(float x, float lo, float hi)
+{
+    return __builtin_amdgcn_fmed3f(x, lo, hi);  // lo for a NaN
+}
+
+// exp(x).  float32 activations: to about 2 ulp, with the product x log2(e) in
+// two parts, the lower one, below 2^-16, through exp2(r) = 1 + r ln 2.  16-bit
+// activations: the high part alone, whose relative error, |x| 2^-24 and the
+// exponential's ulp, is far below theirs.
 template <typename T>
 __device__ __forceinline__ float exp_f(float x)
 {
-    const float t = x * kLog2e;
-    const float e = exp2_hw(t);
+    const float e = exp2_hw(x * kLog2e);  // 0, infinity or NaN included
     if (sizeof(typename T::store_t) == 2) return e;
-    const float r = fma32(x, kLog2eLo, fma32(x, kLog2e, -t));
-    return __builtin_fabsf(t) < 128.f ? fma32(e, r * kLn2, e) : e;
+    const float c = clamp_f(x, -200.f, 200.f);
+    const float r = fma32(c, kLog2eLo, fma32(c, kLog2e, -(c * kLog2e)));
+    return e * fma32(r, kLn2, 1.f);
 }
 
 // 1 / (1 + exp(-x)): 0 and 1 in the limits
@@ -127,18 +134,20 @@ __device__ __forceinline__ float softplus_f(float x)
     p = fma32(p, v, 0x1.99dae6p-2f);
     p = fma32(p, v, 0x1.5554e0p-1f);
     p = fma32(p, v, 2.f);
-    return fma32(s, p, x < 0.f ? 0.f : x);  // a NaN stays one
+    return fma32(s, p, clamp_f(x, 0.f, __builtin_inff()));  // a NaN is one in s
 }
 
 // x sigmoid(x) given q = sigmoid(x): 0, not a NaN, at minus infinity
-__device__ __forceinline__ float silu_f(float x, float q) { return q == 0.f ? q : x * q; }
+__device__ __forceinline__ float silu_f(float x, float q)
+{
+    return clamp_f(x, -kMaxF, __builtin_inff()) * q;
+}
 
 // d/dx of x sigmoid(x), given q = sigmoid(x): q + x q (1 - q), with its limits
 // 0 and 1 where x is infinite
 __device__ __forceinline__ float silu_slope(float x, float q)
 {
-    const float r = q - q * q;
-    return r == 0.f ? q : fma32(x, r, q);
+    return fma32(clamp_f(x, -kMaxF, kMaxF), q - q * q, q);
 }
 
 // Keeps the compiler from putting off the computation of x: a sum that is only
