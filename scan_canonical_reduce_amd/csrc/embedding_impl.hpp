@@ -285,9 +285,9 @@ __global__ __launch_bounds__(256, 4) void k_embed_sum(EmbedGradArgs a, int64_t g
 // lane.  For each (token, slab of columns) it takes, the ballots of "same id" tell
 // whether the token is its id's first, and are the list of occurrences, in order;
 // rows of the table without a token are found the same way.  One
-// launch instead of three (for 100 tokens of 4096 columns, 3000 rows: 36 -> 22
-// us), but an id's occurrences are added by one wave in sequence, which beyond
-// 256 tokens costs more than it saves.
+// launch instead of three: for 257 and 256 tokens of 4096 columns over 3000 rows
+// 22 and 12 us a call.  But an id's occurrences are added by one wave, 16 rows in
+// flight: where all tokens are one, 29 and 52 us.
 constexpr int kEmbedDirect = 256;
 
 template <typename T, typename G, int V>
@@ -329,10 +329,10 @@ __global__ __launch_bounds__(256) void k_embed_direct(EmbedGradArgs a)
         uint64_t cur = same[0];
         bool more = true;
         while (more) {
-            Vec<T, V> raw[8];
+            Vec<T, V> raw[2 * 8];
             int n = 0;
 #pragma unroll
-            for (int r = 0; r < 8; ++r) {
+            for (int r = 0; r < 2 * 8; ++r) {
 #pragma unroll
                 for (int q = 1; q < C; ++q)
                     if (cur == 0 && k < q) {
@@ -346,20 +346,25 @@ __global__ __launch_bounds__(256) void k_embed_direct(EmbedGradArgs a)
                     n = r + 1;
                 }
             }
-            more = n == 8;  // a full batch may be the last: then the next is empty
-            if (n == 0) break;
-            float s[8][V];
+            more = n == 2 * 8;  // these may be the last: then there is no next one
 #pragma unroll
-            for (int r = 0; r < 8; ++r)
+            for (int half = 0; half < 2 * 8; half += 8) {
+                if (n <= half) break;
+                float s[8][V];
 #pragma unroll
-                for (int j = 0; j < V; ++j) s[r][j] = r < n ? T::load(raw[r].e[j]) : -0.f;
-            tree.add(s);
+                for (int r = 0; r < 8; ++r)
+#pragma unroll
+                    for (int j = 0; j < V; ++j)
+                        s[r][j] = half + r < n ? T::load(raw[half + r].e[j]) : -0.f;
+                tree.add(s);
+            }
         }
         float acc[V];
         tree.total(acc);
         if (in) store_grad<G, V>(a, v, col, acc);
     }
     if (a.accumulate) return;
+    // 16-byte stores of the gradient's type
     constexpr int VZ = V == 1 ? 1 : 16 / (int)sizeof(typename G::store_t);
     for (int64_t v0 = wave * kZeroRows; v0 < a.rows; v0 += waves * kZeroRows) {
         uint64_t left = (1ull << (a.rows - v0 < kZeroRows ? a.rows - v0 : kZeroRows)) - 1;
@@ -466,10 +471,12 @@ hipError_t launch_embedding_grad(const EmbedGradArgs& a, hipStream_t st)
     const int64_t want = (a.tokens * slabs + (a.accumulate ? 0 : a.rows) + 3) / 4;
     const dim3 grid((unsigned)capped_grid(want < 1 ? 1 : want < cap ? want : cap));
     if (a.tokens <= kEmbedDirect) {
+        const int64_t waves = a.tokens * slabs * (a.vec ? 2 : 1) + (a.accumulate ? 0 : a.rows);
+        const dim3 direct((unsigned)capped_grid(waves < 4 ? 1 : waves / 4 < cap ? waves / 4 : cap));
         if (a.vec)
-            k_embed_direct<T, G, V><<<grid, dim3(256), 0, st>>>(a);
+            k_embed_direct<T, G, V / 2><<<direct, dim3(256), 0, st>>>(a);
         else
-            k_embed_direct<T, G, 1><<<grid, dim3(256), 0, st>>>(a);
+            k_embed_direct<T, G, 1><<<direct, dim3(256), 0, st>>>(a);
         return hipGetLastError();
     }
     const int64_t groups = id_groups(a.rows);

@@ -591,13 +591,16 @@ __global__ __launch_bounds__(256) void k_scan_sum_bc(ScanArgs a, int groups)
     st<T>(rows_ptr<T>(o, s, a.q, row) + (int64_t)g * a.states + st_n, v);
 }
 
-// Whole sequences, one after the other in a workgroup, where those fill the
-// chip's 512 places (two workgroups on each of 256 compute units) to seven
-// eighths; else chunks.  Packed sequences' lengths are not known here.
+// Whole sequences save the pass that folds each chunk from zero, where there
+// are enough for the chip's 512 places (two workgroups on each of 256 compute
+// units).  Measured as for the forward pass, at 64, 128, 256, 320, 384, 448, 512,
+// 576, 640, 768, 1024 workgroups: whole 323, 323, 344, 455, 459, 462, 467, 716,
+// 725, 737, 911; in chunks 99, 167, 305, 378, 446, 515, 584, 655, 723, 862, 1146.
 inline bool grad_whole_sequences(const ScanArgs& a, int64_t slabs)
 {
-    const int64_t groups = a.q.seqs * slabs, rounds = (groups + 511) / 512;
-    return a.q.starts == nullptr && groups > 0 && groups >= 448 * rounds;
+    const int64_t w = a.q.seqs * slabs, full = w / 512, rest = w % 512;
+    const int64_t last = rest > 256 ? 455 : rest > 0 ? (full ? 265 : 330) : 0;
+    return a.q.starts == nullptr && w > 0 && 467 * full + last <= 28 + w * 35 / 32;
 }
 
 template <typename T, int KS>

@@ -617,16 +617,24 @@ __global__ __launch_bounds__(256) void k_selective_scan_step(ScanArgs a)
 }
 
 // ---------------------------------------------------------------------- launches
-constexpr int64_t kSeqWorkgroups = 384;
+// Whole sequences take one exponential per value instead of two, but need
+// enough of them: a workgroup holds 64 channels of one, and 256 compute units
+// fill in steps.  Measured for 1024 rows of 4096 channels (bf16, 16 states), in
+// us, at 64, 128, 192, 256, 320, 384, 512, 576, 1024 workgroups: whole 123, 124,
+// 124, 123, 177, 179, 180, 242, 310; in chunks 47, 78, 106, 132, 162, 187, 242,
+// 273, 470; and in the same proportion for 256 rows.  Packed sequences' lengths
+// are not known here.
+inline bool scan_whole_sequences(const ScanArgs& a, int64_t slabs)
+{
+    const int64_t w = a.q.seqs * slabs;
+    return a.q.starts == nullptr && 60 + 62 * ((w + 255) / 256) <= 18 + w * 57 / 128;
+}
 
 template <typename T, int KS>
 hipError_t launch_scan_ks(const ScanArgs& a, int64_t groups, hipStream_t st)
 {
     const int64_t slabs = groups * a.slabs;
-    // Whole sequences, one exponential per value instead of two, where their
-    // waves (4 a workgroup) give each of the 1024 SIMDs at least one and a half.
-    // Packed sequences' lengths are not known here.
-    if (a.q.starts == nullptr && a.q.seqs * slabs >= kSeqWorkgroups) {
+    if (scan_whole_sequences(a, slabs)) {
         k_selective_scan<T, KS, kSeq><<<dim3((unsigned)(a.q.seqs * slabs)), dim3(256), 0, st>>>(a);
         return hipGetLastError();
     }
