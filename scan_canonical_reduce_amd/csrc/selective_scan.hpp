@@ -36,6 +36,10 @@ constexpr int kSub = 16;   // rows between saved states, and of a register tile
 // of a pitch below 2^24 elements, and a column below 2^24 (the host checks both).
 constexpr int64_t kMaxPitch = (int64_t)1 << 24;
 
+// Up to this many rows (of all sequences together where they are packed) every
+// sequence is walked whole: one launch costs less than three.
+constexpr int64_t kShortRows = 2 * CANON_SCAN_CHUNK;
+
 template <typename T>
 hipError_t launch_selective_scan(const ScanArgs& a, int64_t groups, hipStream_t st);
 template <typename T>

@@ -372,6 +372,19 @@ __device__ __forceinline__ void grad_rows4(const GradRows& ex, int c, RowIn (&x)
         for (int k = 0; k < 4; ++k) x[k] = nx[k];
 }
 
+// The partial sums of a slot without rows.
+template <int KS>
+__device__ __forceinline__ void zero_slot(const ScanArgs& a, const Lane& l, int64_t slot)
+{
+    const float zero[KS] = {};
+    const int64_t at = slot * a.channels + l.ch;
+    st_states<KS>(a.ws_state + at * (4 * KS) + l.q * KS, zero);
+    if (l.q == 0) {
+        a.ws_dD[at] = 0.f;
+        a.ws_dbias[at] = 0.f;
+    }
+}
+
 // One chunk, given the carry R that enters it from later rows (a.ws_state,
 // which then takes the chunk's part of dA); or, SEQ, a whole sequence from its
 // end, the carry kept in registers.
@@ -405,15 +418,19 @@ __global__ __launch_bounds__(256, 2) void k_selective_scan_grad(ScanArgs a)
         lo = ck.row;
         hi = ck.row + ck.len;
     }
+    if (SEQ && a.q.starts && l.active) {
+        // slots between this sequence's chunks and the next sequence's (the first
+        // sequence: also those before it) take no part in the sums: zero
+        const int64_t base = uniform(slot_base<kCh>(a.q, s));
+        const int64_t end = s + 1 < a.q.seqs ? uniform(slot_base<kCh>(a.q, s + 1))
+                                             : slot_count<kCh>(a.q.seqs, a.q.rows, true);
+        for (int64_t k = s == 0 ? 0 : base; k < end; ++k)
+            if (k < base || k > slot) zero_slot<KS>(a, l, k);
+    }
     const int64_t own = ((SEQ ? s : slot) * a.channels + l.ch) * (SEQ ? a.states : NP) + l.q * KS;
     if (hi <= lo) {  // an empty slot: its partial sums are zero
         if (l.active) {
-            const float zero[KS] = {};
-            st_states<KS>(a.ws_state + (slot * a.channels + l.ch) * NP + l.q * KS, zero);
-            if (l.q == 0) {
-                a.ws_dD[slot * a.channels + l.ch] = 0.f;
-                a.ws_dbias[slot * a.channels + l.ch] = 0.f;
-            }
+            zero_slot<KS>(a, l, slot);
             if (SEQ && a.dinit)
                 for (int i = 0; i < KS; ++i)
                     if (l.q * KS + i < a.states) a.dinit[own + i] = a.dfinal ? a.dfinal[own + i] : 0.f;
@@ -599,6 +616,7 @@ __global__ __launch_bounds__(256) void k_scan_sum_bc(ScanArgs a, int groups)
 inline bool grad_whole_sequences(const ScanArgs& a, int64_t slabs)
 {
     const int64_t w = a.q.seqs * slabs, full = w / 512, rest = w % 512;
+    if (a.q.rows <= kShortRows) return w > 0;
     const int64_t last = rest > 256 ? 455 : rest > 0 ? (full ? 265 : 330) : 0;
     return a.q.starts == nullptr && w > 0 && 467 * full + last <= 28 + w * 35 / 32;
 }

@@ -324,6 +324,13 @@ __device__ __forceinline__ void st_states(float* p, const float (&v)[KS])
     *reinterpret_cast<StateVec<KS>*>(p) = x;
 }
 
+// A chunk's effect on the state that enters it: 2^x H + S, x = log2(e) A sum dl.
+// A zero state stays S where 2^x overflows (A above zero).
+__device__ __forceinline__ float next_state(float x, float H, float S)
+{
+    return H == 0.f ? S : fma32(exp2_hw(x), H, S);
+}
+
 template <typename T, int KS, int MODE>
 __global__ __launch_bounds__(256, 4) void k_selective_scan(ScanArgs a)
 {
@@ -430,7 +437,7 @@ __global__ __launch_bounds__(256, 4) void k_selective_scan(ScanArgs a)
         if (MODE == kSeq && (sub == kSubs - 1 || len <= kSub)) {
 #pragma unroll
             for (int i = 0; i < KS; ++i) {  // the next chunk's start state
-                H[i] = fma32(exp2_hw(sdl * A2[i]), H[i], S[i]);
+                H[i] = next_state(sdl * A2[i], H[i], S[i]);
                 h[i] = H[i];
                 S[i] = 0.f;
             }
@@ -500,7 +507,7 @@ __global__ __launch_bounds__(64) void k_scan_carry(ScanArgs a, const float* __re
             if (k0 + j >= chunks) break;
             *state = carry;
             state += step * dn;
-            carry = fma32(exp2_hw(P[b][j] * A2), carry, S[b][j]);
+            carry = next_state(P[b][j] * A2, carry, S[b][j]);
         }
     };
     if (chunks > 0) {
@@ -622,11 +629,12 @@ __global__ __launch_bounds__(256) void k_selective_scan_step(ScanArgs a)
 // fill in steps.  Measured for 1024 rows of 4096 channels (bf16, 16 states), in
 // us, at 64, 128, 192, 256, 320, 384, 512, 576, 1024 workgroups: whole 123, 124,
 // 124, 123, 177, 179, 180, 242, 310; in chunks 47, 78, 106, 132, 162, 187, 242,
-// 273, 470; and in the same proportion for 256 rows.  Packed sequences' lengths
-// are not known here.
+// 273, 470; and in the same proportion for 256 rows (34 and 22 at 64 workgroups,
+// 48 and 79 at 512).  Packed sequences' lengths are not known here.
 inline bool scan_whole_sequences(const ScanArgs& a, int64_t slabs)
 {
     const int64_t w = a.q.seqs * slabs;
+    if (a.q.rows <= kShortRows) return true;
     return a.q.starts == nullptr && 60 + 62 * ((w + 255) / 256) <= 18 + w * 57 / 128;
 }
 

@@ -226,7 +226,8 @@ canon_status_t scan_args(const canon_selective_scan_t* c, bool step, bool grad, 
                      c->chunk_states == nullptr))
             return CANON_EINVAL;
     }
-    if (grad && c->channels > 0 && (c->dA == nullptr || (c->dD != nullptr && c->D == nullptr) ||
+    // without channels nothing would be written to dB and dC
+    if (grad && (c->channels == 0 || c->dA == nullptr || (c->dD != nullptr && c->D == nullptr) ||
                  (c->ddelta_bias != nullptr && c->delta_bias == nullptr)))
         return CANON_EINVAL;
     if (!ptr_aligned(c->chunk_states, 16)) return CANON_EINVAL;
@@ -462,7 +463,6 @@ canon_status_t canon_selective_scan_grad(const canon_selective_scan_t* c, void* 
 {
     ScanArgs a;
     if (canon_status_t s = scan_args(c, false, true, &a)) return s;
-    if (a.channels == 0) return CANON_OK;
     const SelectiveScanLayout l(a.q.seqs, a.q.rows, a.q.starts != nullptr, a.channels, a.states, c->groups,
                        true);
     if (canon_status_t s = check_ws(ws, ws_bytes, l.bytes)) return s;

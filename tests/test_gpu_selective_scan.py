@@ -86,7 +86,8 @@ SHAPES = [  # lens, channels, groups, states, packed
     ([64], 64, 1, 16, False), ([65], 65, 1, 8, False), ([130], 96, 3, 13, False),
     ([200, 200], 72, 1, 5, False), ([150], 20, 1, 3, False), ([129], 130, 1, 4, False),
     ([3, 0, 64, 1, 129, 63, 0], 40, 1, 16, True), ([100, 65, 0, 1], 36, 2, 7, True),
-    ([0, 0, 5], 17, 1, 2, True),
+    ([0, 0, 5], 17, 1, 2, True), ([30, 0, 64, 1, 33], 40, 1, 16, True), ([0, 65, 0, 62, 0], 70, 2, 8, True),
+    ([128, 128], 24, 1, 16, False),
 ]
 
 
@@ -402,6 +403,13 @@ def test_rows_outside_sequences_and_special_values(canon):
     e["delta"].fill_(float("-inf"))  # softplus 0: nothing decays, nothing is added
     call(canon, e, final_state=final)
     assert torch.equal(final, e["init"])
+    # growing states: a zero one stays what the rows add, though exp(A sum dl)
+    # over a chunk overflows
+    e = {k: v.clone() if torch.is_tensor(v) else v for k, v in d.items()}
+    e["A"] = e["A"].abs() * 0 + 40.0
+    e["init"].zero_()
+    e["u"].zero_()
+    assert not call(canon, e, final_state=final)[3:171].any() and not final.any()
     # gradients: rows of other sequences do not count
     e = {k: v.clone() if torch.is_tensor(v) else v for k, v in d.items()}
     for k in ("u", "delta", "z", "B", "C", "dout"):
@@ -417,6 +425,40 @@ def test_rows_outside_sequences_and_special_values(canon):
         if name in ("du", "ddelta", "dB", "dC", "dz"):
             a, b = a[3:171], b[3:171]
         assert torch.equal(a, b), name
+
+
+def test_few_packed_rows_not_from_the_first(canon):
+    """Few packed rows (each sequence walked whole), rows in front of and behind
+    the sequences, empty ones between: as the sequences alone; the parameters'
+    gradients take nothing from slots without rows."""
+    d = cuda(inputs(F32, [120], 24, 1, 16, True, 4))
+    d["starts"] = torch.tensor([7, 7, 70, 70, 70, 101]).int().cuda()
+    d["init"] = torch.randn(5, 24, 16).cuda()
+    names = ("u", "delta", "z", "B", "C", "dout")
+    parts, total = [], 0
+    for s, (a, b) in enumerate(((7, 7), (7, 70), (70, 70), (70, 70), (70, 101))):
+        one = {k: v[None, a:b].contiguous() if k in names else v for k, v in d.items()}
+        one["starts"], one["init"] = None, d["init"][s:s + 1]
+        keep = canon.selective_scan_states(one["u"], 16)
+        out = call(canon, one, states=keep)
+        parts.append((out[0], canon.selective_scan_grad(
+            one["dout"], one["u"], one["delta"], one["A"], one["B"], one["C"], keep, D=one["D"],
+            z=one["z"], delta_bias=one["bias"], delta_softplus=True)))
+    ws = torch.full((canon.selective_scan_grad_workspace_bytes(5, 120, True, 24, 1, 16),), 255,
+                    dtype=torch.uint8, device="cuda")  # NaN wherever it is not written
+    keep = canon.selective_scan_states(d["u"], 16, d["starts"])
+    out = call(canon, d, states=keep)
+    g = canon.selective_scan_grad(d["dout"], d["u"], d["delta"], d["A"], d["B"], d["C"], keep,
+                                  D=d["D"], z=d["z"], delta_bias=d["bias"], delta_softplus=True,
+                                  starts=d["starts"], ws=ws)
+    assert torch.equal(out[7:101], torch.cat([p[0] for p in parts]))
+    assert torch.equal(g.du[7:101], torch.cat([p[1].du[0] for p in parts]))
+    assert torch.equal(g.dB[7:101], torch.cat([p[1].dB[0] for p in parts]))
+    assert torch.equal(g.dinit_state, torch.cat([p[1].dinit_state for p in parts]))
+    for k in ("dA", "dD", "ddelta_bias"):  # the same chunks' sums, in another order
+        want = sum(getattr(p[1], k).double() for p in parts)
+        got = getattr(g, k).double()
+        assert float((got - want).abs().max() / want.abs().max()) <= 8 * seq_ref.U32, k
 
 
 def test_empty(canon):

@@ -190,6 +190,7 @@ def test_scan_refusals(seq):
         assert L.canon_selective_scan_grad(scan(seq, **{name: R(FAKE, 9 * 32, 31)}), FAKE, n,
                                            None) == 1
     for bad in (dict(dA=None), dict(D=None), dict(delta_bias=None), dict(chunk_states=None),
+                dict(channels=0, groups=1),
                 dict(dout=R(None, 0, 0))):
         assert L.canon_selective_scan_grad(scan(seq, **bad), FAKE, n, None) == 1, bad
     for bad in (dict(states=17), dict(rows=1 << 30), dict(channels=1 << 24)):
