@@ -234,8 +234,15 @@ __device__ __forceinline__ void zero_listed(const EmbedGradArgs& a, int64_t v0, 
         const int64_t row = v0 + __builtin_ctzll(left);
         left &= left - 1;
         typename G::store_t* p = static_cast<typename G::store_t*>(a.dw) + row * a.ld_dw;
-        const float zero[V] = {};
-        for (int64_t c = lane * V; c < a.width; c += 64 * V) st_vec<G, V>(p + c, zero);
+        if constexpr (V * sizeof(typename G::store_t) == 16) {
+            typedef uint32_t u4 __attribute__((ext_vector_type(4)));
+            const u4 zero = {0, 0, 0, 0};
+            for (int64_t c = lane * V; c < a.width; c += 64 * V)
+                __builtin_nontemporal_store(zero, reinterpret_cast<u4*>(p + c));
+        } else {
+            const float zero[V] = {};
+            for (int64_t c = lane * V; c < a.width; c += 64 * V) st_vec<G, V>(p + c, zero);
+        }
     }
 }
 
