@@ -287,7 +287,8 @@ __global__ __launch_bounds__(256, K <= 4 ? 5 : 2) void k_causal_conv_grad(ConvAr
                 st_vec<T, V>(dx + (int64_t)m * a.dx.row, y);
         };
         constexpr int ALL = RUN + K - 1;
-        if (__all(ck.len == RUN && ck.row > 0 && ck.row + ALL <= len - (K - 1))) {
+        constexpr int READ = (ALL + U - 1) / U * U;  // rows that whole fetches read
+        if (__all(ck.len == RUN && ck.row > 0 && ck.row + READ <= len)) {
 #pragma unroll 1
             for (int32_t r0 = 0; r0 < ALL; r0 += 2 * U) {
                 if (r0 + U < ALL) fetch(1, r0 + U, true);

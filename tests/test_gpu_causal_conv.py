@@ -256,3 +256,25 @@ def test_refusals(canon):
         canon.causal_conv(x.cpu(), w)
     with pytest.raises(ValueError):
         canon.causal_conv_step(x, torch.zeros(2, 3, 8).cuda(), w)
+
+
+@pytest.mark.parametrize("taps", [2, 3, 4, 8])
+@pytest.mark.parametrize("rows", [64, 65, 66, 67, 68, 71, 72, 97])
+def test_backward_near_the_end(canon, taps, rows):
+    """A sequence that ends a few rows behind a run's: the gradients of the whole
+    are those of the same rows in a longer buffer, whatever comes after them."""
+    d = cuda(inputs(F32, [rows], 64, taps, False, seed=rows))
+    want = canon.causal_conv_grad(d["dout"], d["x"], d["w"], d["b"], "silu")
+    x, dout = (torch.full((2, rows + 8, 64), float("nan"), device="cuda") for _ in range(2))
+    x[:, :rows], dout[:, :rows] = d["x"], d["dout"]
+    got = canon.causal_conv_grad(dout[:1, :rows], x[:1, :rows], d["w"], d["b"], "silu")
+    assert torch.equal(got.dx, want.dx) and torch.equal(got.dweight, want.dweight)
+    e = {k: v.double().cpu() if torch.is_tensor(v) else v for k, v in d.items()}
+    e["init"].zero_()
+    e["dfinal"].zero_()
+    _, (dx, dw, _, db) = reference(e, "silu", grad=True)
+    # rounding of the sums over rows: at most 2^-24 of 12 + rows per absolute term,
+    # the terms themselves below 8 * 8 * 1.1
+    assert (want.dx.double().cpu() - dx).abs().max() < 2**-24 * 40 * taps * 64
+    assert (want.dweight.double().cpu() - dw).abs().max() < 2**-24 * (rows + 40) * rows * 64
+    assert (want.dbias.double().cpu() - db).abs().max() < 2**-24 * (rows + 40) * rows * 8
