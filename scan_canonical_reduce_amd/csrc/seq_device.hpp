@@ -245,6 +245,7 @@ __host__ __device__ __forceinline__ int64_t chunks_per_seq(int64_t rows)
 template <int CH>
 __host__ __device__ __forceinline__ int64_t slot_count(int64_t seqs, int64_t rows, bool packed)
 {
+    if (seqs == 0) return 0;  // rows of no sequence
     return packed ? seqs + rows / CH : seqs * chunks_per_seq<CH>(rows);
 }
 

@@ -154,3 +154,24 @@ def test_same_bits_every_run(canon):
         x, u, keep, y = forward(canon, p)
         got = [y] + backward(canon, p, x, u, keep)
         assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+@pytest.mark.parametrize("rows", [0, 5, 64, 300])
+def test_rows_of_no_sequence(canon, rows):
+    """starts of one value: no sequence, so the parameters' gradients are zero and
+    no row is written."""
+    starts = torch.tensor([2], dtype=torch.int32, device="cuda")
+    x = torch.randn(rows, 40, device="cuda")
+    w, b = torch.randn(40, 4, device="cuda"), torch.randn(40, device="cuda")
+    out = torch.full_like(x, 7.0)
+    canon.causal_conv(x, w, b, "silu", starts, out=out)
+    assert (out == 7).all()
+    g = canon.causal_conv_grad(x, x, w, b, "silu", starts, dx=out)
+    assert (out == 7).all() and not g.dweight.any() and not g.dbias.any()
+    A, B, D = -torch.rand(40, 8, device="cuda"), torch.randn(rows, 8, device="cuda"), b
+    keep = canon.selective_scan_states(x, 8, starts)
+    canon.selective_scan(x, x, A, B, B, D, x, b, True, starts, states=keep, out=out)
+    assert (out == 7).all()
+    g = canon.selective_scan_grad(x, x, x, A, B, B, keep, D, x, b, True, starts)
+    assert not g.dA.any() and not g.dD.any() and not g.ddelta_bias.any()
+    assert g.dinit_state.shape == (0, 40, 8)

@@ -217,3 +217,12 @@ def test_the_binding_has_no_cpu_path(seq):
                  lambda: canon.selective_scan_step(A[None], x[0], x[0], A, B[0], B[0])):
         with pytest.raises(ValueError, match="GPU"):
             call()
+
+
+def test_no_sequences_need_no_workspace(seq):
+    """Rows that belong to no sequence have no chunks."""
+    for rows in (0, 64, 1000):
+        for packed in (False, True):
+            assert seq.causal_conv_grad_workspace_bytes(0, rows, packed, 64, 4) == 0
+            assert seq.selective_scan_workspace_bytes(0, rows, packed, 64, 16) == 0
+            assert seq._lib().canon_selective_scan_states(0, rows, int(packed), 64, 16) == 0
