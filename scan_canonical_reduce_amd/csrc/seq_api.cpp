@@ -167,8 +167,9 @@ canon_status_t conv_args(const canon_conv_t* c, bool step, bool grad, ConvArgs* 
              rows_aligned(a->out, es, v, false) && rows_aligned(a->dout, es, v, false) &&
              rows_aligned(a->dx, es, v, false) && ptr_aligned(a->init, v) &&
              ptr_aligned(a->final, v) && ptr_aligned(a->dfinal, v) && ptr_aligned(a->dinit, v);
-    // threads of the shortest runs, one channel each where not vectorised
-    const int64_t per = a->vec ? c->channels / (int64_t)(v / es) : c->channels;
+    // threads of the shortest runs: four channels each, two in the backward
+    // pass, one where not vectorised
+    const int64_t per = a->vec ? c->channels / (grad ? 2 : 4) : c->channels;
     if (!mul_fits(per, slot_count<8>(c->seqs, rows, packed), kMaxGrid256 * 255))
         return CANON_EUNSUPPORTED;
     return CANON_OK;
@@ -275,8 +276,9 @@ canon_status_t scan_args(const canon_selective_scan_t* c, bool step, bool grad, 
         step ? c->seqs : slot_count<CANON_SCAN_CHUNK>(c->seqs, rows, packed);
     if (!mul_fits(slots, c->groups * a->slabs, kMaxGrid256 - 1) ||
         !mul_fits(c->seqs, (c->channels * 4 * ks + 63) / 64, 4 * kMaxGrid256 - 1) ||
-        (grad && !mul_fits((packed ? rows : c->seqs * rows), c->groups * 8 * ks,
-                           (int64_t)1 << 31)))
+        (grad && (!mul_fits((packed ? rows : c->seqs * rows), c->groups * 8 * ks,
+                            (int64_t)1 << 31) ||
+                  !mul_fits(c->channels, 4 * ks + 2, (int64_t)1 << 27))))  // column sums
         return CANON_EUNSUPPORTED;
     return CANON_OK;
 }

@@ -226,3 +226,18 @@ def test_no_sequences_need_no_workspace(seq):
             assert seq.causal_conv_grad_workspace_bytes(0, rows, packed, 64, 4) == 0
             assert seq.selective_scan_workspace_bytes(0, rows, packed, 64, 16) == 0
             assert seq._lib().canon_selective_scan_states(0, rows, int(packed), 64, 16) == 0
+
+
+def test_backward_launch_limits(seq):
+    """Two channels a thread in the convolution's backward pass, and the column
+    sums of the parameters' gradients: launches below 2^32 threads."""
+    L = seq._lib()
+    r = Rows(FAKE, 4096, 4096)
+    big = dict(seqs=5 << 19, rows=1, channels=4096, x=r, out=r, dout=r, dx=r)
+    assert L.canon_causal_conv_grad(conv(seq, **big), None, 0, None) == 2
+    n = 1 << 23
+    r = Rows(FAKE, n, n)
+    wide = dict(seqs=1, rows=1, channels=n, groups=1, u=r, delta=r, z=r, out=r, dout=r, du=r,
+                ddelta=r, dz=r)
+    assert L.canon_selective_scan_grad(scan(seq, **wide), None, 0, None) == 2
+    assert L.canon_selective_scan(scan(seq, **wide), None, 0, None) == 3  # no workspace
