@@ -117,7 +117,7 @@ __global__ __launch_bounds__(256) void k_scan_back_sum(ScanArgs a)
 #pragma unroll
     for (int i = 0; i < KS; ++i) {
         const int n = l.q * KS + i;
-        A2[i] = n < a.states ? a.A[(int64_t)l.ch * a.states + n] * kLog2e : 0.f;
+        A2[i] = n < a.states ? decay_rate(a.A[(int64_t)l.ch * a.states + n]) : 0.f;
         R[i] = 0.f;
     }
     const float bias = a.bias ? a.bias[l.ch] : 0.f;
@@ -442,7 +442,7 @@ __global__ __launch_bounds__(256, 2) void k_selective_scan_grad(ScanArgs a)
 #pragma unroll
     for (int i = 0; i < KS; ++i) {
         const int n = l.q * KS + i;
-        g.A2[i] = n < a.states ? a.A[(int64_t)l.ch * a.states + n] * kLog2e : 0.f;
+        g.A2[i] = n < a.states ? decay_rate(a.A[(int64_t)l.ch * a.states + n]) : 0.f;
         g.R[i] = SEQ && a.dfinal && l.active && n < a.states ? a.dfinal[own + i] : 0.f;
         g.dA[i] = 0.f;
     }

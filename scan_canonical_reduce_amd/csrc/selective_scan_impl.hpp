@@ -324,6 +324,15 @@ __device__ __forceinline__ void st_states(float* p, const float (&v)[KS])
     *reinterpret_cast<StateVec<KS>*>(p) = x;
 }
 
+// log2(e) A.  Minus infinity becomes the lowest finite value: the same
+// exponential, 0, of any step size above zero, and 1 of the rows past the end,
+// whose step size is 0.
+__device__ __forceinline__ float decay_rate(float A)
+{
+    const float x = A * kLog2e;
+    return x < -kMaxF ? -kMaxF : x;
+}
+
 // A chunk's effect on the state that enters it: 2^x H + S, x = log2(e) A sum dl.
 // A zero state stays S where 2^x overflows (A above zero).
 __device__ __forceinline__ float next_state(float x, float H, float S)
@@ -364,7 +373,7 @@ __global__ __launch_bounds__(256, 4) void k_selective_scan(ScanArgs a)
 #pragma unroll
     for (int i = 0; i < KS; ++i) {
         const int n = l.q * KS + i;
-        A2[i] = n < a.states ? a.A[(int64_t)l.ch * a.states + n] * kLog2e : 0.f;
+        A2[i] = n < a.states ? decay_rate(a.A[(int64_t)l.ch * a.states + n]) : 0.f;
         h[i] = 0.f;
         S[i] = 0.f;
         if (MODE == kSeq && a.init && n < a.states)
@@ -480,7 +489,7 @@ __global__ __launch_bounds__(64) void k_scan_carry(ScanArgs a, const float* __re
     const Span span = uniform(seq_span(a.q, s));
     const int64_t base = uniform(slot_base<kCh>(a.q, s));
     const int32_t chunks = (span.len + kCh - 1) / kCh;
-    const float A2 = real ? a.A[d * a.states + n] * kLog2e : 0.f;
+    const float A2 = real ? decay_rate(a.A[d * a.states + n]) : 0.f;
     const int64_t own = (s * a.channels + d) * a.states + n;
     float carry = first && real ? first[own] : 0.f;
     constexpr int U = 16;
@@ -586,7 +595,7 @@ __global__ __launch_bounds__(256) void k_selective_scan_step(ScanArgs a)
         for (int i = 0; i < KS; ++i) A2[i] = l.q * KS + i < a.states ? a.A[at + i] : 0.f;
     }
 #pragma unroll
-    for (int i = 0; i < KS; ++i) A2[i] *= kLog2e;
+    for (int i = 0; i < KS; ++i) A2[i] = decay_rate(A2[i]);
     const float bias = a.bias ? a.bias[ch] : 0.f, Dc = a.D ? a.D[ch] : 0.f;
 #pragma unroll
     for (int j = 0; j < SEQS; ++j) {

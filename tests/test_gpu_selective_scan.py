@@ -506,3 +506,38 @@ def test_refusals(canon):
     with pytest.raises(ValueError):
         canon.selective_scan_grad(d["dout"], d["u"], d["delta"], d["A"], d["B"], d["C"],
                                   torch.zeros(3, device="cuda"))
+
+
+@pytest.mark.parametrize("lens,packed", [([17], False), ([100, 100], False), ([300], False),
+                                         ([130, 9, 70], True)])
+def test_states_that_keep_nothing(canon, lens, packed):
+    """A of minus infinity, or beyond float32 once it is scaled: exp(dl A) is 0, so
+    the state is the last row's alone.  Rows past a sequence's end inside a tile,
+    whose step size is 0, change nothing."""
+    d = inputs(F32, lens, 40, 1, 16, packed, 21)
+    finite = dict(d, A=d["A"].clone())
+    finite["A"][:, 3:9] = -1e30
+    for low in (float("-inf"), -3.3e38):
+        d["A"] = finite["A"].clone()
+        d["A"][:, 3:9] = low
+        g = cuda(d)
+        final = torch.empty_like(g["init"])
+        keep = canon.selective_scan_states(g["u"], 16, g["starts"])
+        got = call(canon, g, final_state=final, states=keep)
+        out, h, _ = reference(finite)
+        size, hsize, _ = reference(finite, absolute=True)
+        n = terms(max(lens))
+        seq_ref.close(got, out, size, n, "out")
+        seq_ref.close(final, h, hsize, n, "final")
+        grads = canon.selective_scan_grad(
+            g["dout"], g["u"], g["delta"], g["A"], g["B"], g["C"], keep, D=g["D"], z=g["z"],
+            delta_bias=g["bias"], delta_softplus=True, starts=g["starts"])
+        for name, t in zip(grads._fields, grads):
+            assert torch.isfinite(t).all(), name
+        assert not grads.dA[:, 3:9].any()
+        step = torch.empty_like(final)
+        one = {k: g[k].reshape(-1, *g[k].shape[1 if packed else 2:])[:len(lens)]
+               for k in ("u", "delta", "z", "B", "C")}
+        canon.selective_scan_step(g["init"], one["u"], one["delta"], g["A"], one["B"], one["C"],
+                                  g["D"], one["z"], g["bias"], True, out_state=step)
+        assert torch.isfinite(step).all()
