@@ -301,6 +301,7 @@ canon_status_t canon_embedding(int dtype, const void* weight, size_t ld_weight, 
     if (!embed_sizes_ok(tokens, rows, width) ||
         !mul_fits((int64_t)tokens, (int64_t)width, (int64_t)1 << 33))
         return CANON_EUNSUPPORTED;
+    if (out == weight) return CANON_EINVAL;
     const size_t es = elem_bytes(dtype);
     EmbedArgs a{weight, (int64_t)ld_weight, (int64_t)rows, (int64_t)width, ids, id_bytes == 8,
                 false, (int64_t)tokens, scale, out, (int64_t)ld_out};
@@ -332,6 +333,7 @@ canon_status_t canon_embedding_grad(int dtype, const void* dout, size_t ld_dout,
     if (!embed_sizes_ok(tokens, rows, width)) return CANON_EUNSUPPORTED;
     const EmbedLayout l((int64_t)tokens, (int64_t)rows, (int64_t)width);
     if (canon_status_t s = check_ws(ws, ws_bytes, l.bytes)) return s;
+    if (tokens > 0 && dw == dout) return CANON_EINVAL;
     const size_t es = elem_bytes(dtype), gs = elem_bytes(dw_dtype);
     EmbedGradArgs a{};
     a.dout = dout;
@@ -375,6 +377,8 @@ canon_status_t canon_causal_conv(const canon_conv_t* c, void* stream)
     ConvArgs a;
     if (canon_status_t s = conv_args(c, false, false, &a)) return s;
     if (a.q.seqs == 0 || a.channels == 0) return CANON_OK;
+    // in place a run would read rows that its neighbour has overwritten
+    if (a.q.rows > 0 && a.out.p == a.x.p) return CANON_EINVAL;
     return with_dtype(c->dtype, [&](auto t) {
         return hip_status(launch_causal_conv<decltype(t)>(a, (int)c->taps,
                                                           static_cast<hipStream_t>(stream)));
@@ -399,6 +403,8 @@ canon_status_t canon_causal_conv_grad(const canon_conv_t* c, void* ws, size_t ws
     if (a.channels == 0) return CANON_OK;
     const ConvLayout l(a.q.seqs, a.q.rows, a.q.starts != nullptr, a.channels, c->taps);
     if (canon_status_t s = check_ws(ws, ws_bytes, l.bytes)) return s;
+    if (a.q.seqs > 0 && a.q.rows > 0 && (a.dx.p == a.x.p || a.dx.p == a.dout.p))
+        return CANON_EINVAL;
     a.ws_w = l.at<float>(ws, l.w);
     a.ws_b = l.at<float>(ws, l.b);
     return with_dtype(c->dtype, [&](auto t) {

@@ -241,3 +241,18 @@ def test_backward_launch_limits(seq):
                 ddelta=r, dz=r)
     assert L.canon_selective_scan_grad(scan(seq, **wide), None, 0, None) == 2
     assert L.canon_selective_scan(scan(seq, **wide), None, 0, None) == 3  # no workspace
+
+
+def test_in_place_refusals(seq):
+    """Outputs in an input's place, where that would read what it has written."""
+    L = seq._lib()
+    n = seq.causal_conv_grad_workspace_bytes(2, 9, False, 8, 4)
+    x, y, z = (Rows(FAKE + i * 4096, 72, 8) for i in range(3))
+    assert L.canon_causal_conv(conv(seq, x=x, out=x), None) == 1
+    for a, b in ((x, z), (z, x)):
+        assert L.canon_causal_conv_grad(conv(seq, x=a, dout=b, dx=x), FAKE, n, None) == 1
+    assert L.canon_causal_conv_grad(conv(seq, x=x, dout=y, dx=z), FAKE, n - 1, None) == 3
+    assert L.canon_embedding(1, FAKE, 8, 10, 8, FAKE, 8, 4, 1.0, FAKE, 8, None) == 1
+    m = seq.embedding_grad_workspace_bytes(100, 10, 8)
+    assert L.canon_embedding_grad(1, FAKE, 8, FAKE, 8, 100, 10, 8, 1.0, -1, 0, 0, FAKE, 8, FAKE,
+                                  m, None) == 1
