@@ -27,11 +27,10 @@ struct ColumnSums {
 // The rows go to 16 lanes, row r to lane r mod 16; each lane is summed in row
 // order and the lanes by the pairwise tree, so the value depends on the rows
 // alone.  A workgroup holds 64 columns; its 16 waves are the lanes.
-__global__ __launch_bounds__(1024) static void k_column_sum(ColumnSums a)
+__device__ __forceinline__ void column_sum_block(const ColumnSums& a, int64_t block)
 {
     __shared__ float lanes[kColLanes][64];
     const int x = threadIdx.x & 63, w = threadIdx.x >> 6;
-    int64_t block = blockIdx.x;
     ColumnSum j = a.sum[0];
 #pragma unroll
     for (int k = 1; k < 3; ++k) {
@@ -67,10 +66,21 @@ __global__ __launch_bounds__(1024) static void k_column_sum(ColumnSums a)
     j.out[c / j.np * j.n + c % j.np] = v[0];
 }
 
-inline hipError_t launch_column_sums(const ColumnSums& a, hipStream_t st)
+__global__ __launch_bounds__(1024) static void k_column_sum(ColumnSums a)
+{
+    column_sum_block(a, blockIdx.x);
+}
+
+inline int64_t column_sum_blocks(const ColumnSums& a)
 {
     int64_t blocks = 0;
     for (const ColumnSum& j : a.sum) blocks += j.out ? (j.cols + 63) / 64 : 0;
+    return blocks;
+}
+
+inline hipError_t launch_column_sums(const ColumnSums& a, hipStream_t st)
+{
+    const int64_t blocks = column_sum_blocks(a);
     if (blocks == 0) return hipSuccess;
     k_column_sum<<<dim3((unsigned)blocks), dim3(1024), 0, st>>>(a);
     return hipGetLastError();

@@ -573,12 +573,19 @@ __global__ __launch_bounds__(256, 2) void k_selective_scan_grad(ScanArgs a)
             if (l.q * KS + i < a.states) a.dinit[own + i] = g.R[i];
 }
 
-// dB and dC of each row: the slabs' sums in order, rounded once.
+// What is left to sum, in one launch: the first workgroups take the parameters'
+// gradients over the chunks, the others dB and dC of each row, the slabs' sums in
+// order, rounded once.
 template <typename T, int NP>
-__global__ __launch_bounds__(256) void k_scan_sum_bc(ScanArgs a, int groups)
+__global__ __launch_bounds__(1024) void k_scan_grad_sums(ScanArgs a, ColumnSums params,
+                                                         uint32_t param_blocks, int groups)
 {
+    if (blockIdx.x < param_blocks) {
+        column_sum_block(params, blockIdx.x);
+        return;
+    }
     const int64_t bc_rows = a.q.starts ? a.q.rows : a.q.seqs * a.q.rows;
-    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    const int64_t i = (int64_t)(blockIdx.x - param_blocks) * 1024 + threadIdx.x;
     const int64_t rg = i / (2 * NP);
     const int n = (int)(i - rg * (2 * NP));
     const int64_t r = rg / groups;
@@ -640,15 +647,14 @@ hipError_t launch_scan_grad_ks(const ScanArgs& a, int64_t groups, hipStream_t st
         if (hipError_t e = hipGetLastError()) return e;
     }
     const int64_t d = a.channels;
-    if (hipError_t e = launch_column_sums({{{a.ws_state, d * NP, NP, a.states, a.dA},
-                                            {a.ws_dD, d, 1, 1, a.dD},
-                                            {a.ws_dbias, d, 1, 1, a.dbias}},
-                                           slots},
-                                          st))
-        return e;
+    const ColumnSums params = {{{a.ws_state, d * NP, NP, a.states, a.dA},
+                                {a.ws_dD, d, 1, 1, a.dD},
+                                {a.ws_dbias, d, 1, 1, a.dbias}},
+                               slots};
+    const int64_t blocks = column_sum_blocks(params);
     const int64_t bc = (a.q.starts ? a.q.rows : a.q.seqs * a.q.rows) * groups * 2 * NP;
-    if (bc == 0) return hipSuccess;
-    k_scan_sum_bc<T, NP><<<dim3((unsigned)((bc + 255) / 256)), dim3(256), 0, st>>>(a, (int)groups);
+    k_scan_grad_sums<T, NP><<<dim3((unsigned)(blocks + (bc + 1023) / 1024)), dim3(1024), 0, st>>>(
+        a, params, (uint32_t)blocks, (int)groups);
     return hipGetLastError();
 }
 

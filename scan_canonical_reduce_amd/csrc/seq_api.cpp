@@ -278,7 +278,7 @@ canon_status_t scan_args(const canon_selective_scan_t* c, bool step, bool grad, 
         !mul_fits(c->seqs, (c->channels * 4 * ks + 63) / 64, 4 * kMaxGrid256 - 1) ||
         (grad && (!mul_fits((packed ? rows : c->seqs * rows), c->groups * 8 * ks,
                             (int64_t)1 << 31) ||
-                  !mul_fits(c->channels, 4 * ks + 2, (int64_t)1 << 27))))  // column sums
+                  !mul_fits(c->channels, 4 * ks + 2, (int64_t)1 << 26))))  // column sums
         return CANON_EUNSUPPORTED;
     return CANON_OK;
 }
