@@ -15,27 +15,32 @@ __device__ __forceinline__ int64_t id_at(const void* ids, int64_t t)
                  : (int64_t) static_cast<const int32_t*>(ids)[t];
 }
 
-// Exclusive sum over the workgroup's 1024 threads of two counts at once.
-__device__ __forceinline__ uint64_t block_exclusive(uint64_t x, uint64_t* total, uint64_t* lds)
+// Exclusive sums over the workgroup's 1024 threads, of two pairs of counts at
+// once (each pair in the halves of 64 bits); x and y become the sums of all.
+struct Pairs {
+    uint64_t x, y;
+};
+__device__ __forceinline__ Pairs block_exclusive(uint64_t& x, uint64_t& y, Pairs* lds)
 {
     const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
-    uint64_t run = x;
+    Pairs run = {x, y};
 #pragma unroll
     for (int d = 1; d < 64; d *= 2) {
-        const uint64_t o = __shfl_up((unsigned long long)run, d, 64);
-        if (lane >= d) run += o;
+        const uint64_t ox = __shfl_up((unsigned long long)run.x, d, 64);
+        const uint64_t oy = __shfl_up((unsigned long long)run.y, d, 64);
+        if (lane >= d) run.x += ox, run.y += oy;
     }
-    __syncthreads();
     if (lane == 63) lds[w] = run;
     __syncthreads();
-    uint64_t base = 0, all = 0;
+    Pairs base = {0, 0}, all = {0, 0};
 #pragma unroll
     for (int k = 0; k < kWaves; ++k) {
         if (k == w) base = all;
-        all += lds[k];
+        all.x += lds[k].x, all.y += lds[k].y;
     }
-    *total = all;
-    return base + run - x;
+    base.x += run.x - x, base.y += run.y - y;
+    x = all.x, y = all.y;
+    return base;
 }
 
 // R ids a workgroup (R <= 512); dynamic LDS: kWaves x R counts.
@@ -43,7 +48,7 @@ template <bool IDS64>
 __global__ __launch_bounds__(1024) void k_embed_group(EmbedGradArgs a, int R)
 {
     extern __shared__ int32_t hist[];  // [wave][id]: count, then the next position
-    __shared__ uint64_t scan[kWaves];
+    __shared__ Pairs scan[kWaves];
     __shared__ int32_t first_item[1025];
     const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
     const int64_t b = blockIdx.x, lo = b * R;
@@ -56,14 +61,17 @@ __global__ __launch_bounds__(1024) void k_embed_group(EmbedGradArgs a, int R)
     const int64_t t_lo = w * per < a.tokens ? w * per : a.tokens;
     const int64_t t_hi = t_lo + per < a.tokens ? t_lo + per : a.tokens;
     constexpr int U = 8;  // ids in flight per lane
-    uint32_t below = 0;
-    for (int64_t t0 = t_lo; t0 < t_hi; t0 += 64 * U) {
-        int64_t id[U];
+    int64_t id[U];
+    auto load = [&](int64_t t0) {
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const int64_t t = t0 + u * 64 + lane;
             id[u] = t < t_hi ? id_at<IDS64>(a.ids, t) : -1;
         }
+    };
+    uint32_t below = 0;
+    for (int64_t t0 = t_lo; t0 < t_hi; t0 += 64 * U) {
+        load(t0);
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const bool real = id[u] >= 0 && id[u] < a.rows && id[u] != a.padding_id;
@@ -73,8 +81,6 @@ __global__ __launch_bounds__(1024) void k_embed_group(EmbedGradArgs a, int R)
         }
     }
     __syncthreads();
-    uint64_t all_below, unused;
-    block_exclusive(below, &all_below, scan);
     // thread r: the counts of id lo + r over the waves, in wave order
     int32_t n = 0;
     if (tid < R)
@@ -88,10 +94,11 @@ __global__ __launch_bounds__(1024) void k_embed_group(EmbedGradArgs a, int R)
     const int32_t chunks = (n + kEmbedChunk - 1) / kEmbedChunk;
     const int32_t items = is_row ? chunks : 0;
     const bool is_long = is_row && n > kEmbedChunk;
-    uint64_t both;
-    const uint64_t pos = block_exclusive((uint64_t)(uint32_t)n | (uint64_t)(uint32_t)items << 32,
-                                         &both, scan);
-    const uint64_t long_pos = block_exclusive(is_long ? 1u : 0u, &unused, scan);
+    uint64_t x = (uint64_t)(uint32_t)n | (uint64_t)(uint32_t)items << 32;
+    uint64_t y = (uint64_t)is_long | (uint64_t)below << 32;
+    const Pairs before = block_exclusive(x, y, scan);
+    const uint64_t pos = before.x, both = x, long_pos = (uint32_t)before.y;
+    const int64_t all_below = (int64_t)(y >> 32);
     const int32_t off = (int32_t)all_below + (int32_t)(uint32_t)pos;
     const int32_t item = (int32_t)(pos >> 32), n_items = (int32_t)(both >> 32);
     if (tid < R)
@@ -107,7 +114,7 @@ __global__ __launch_bounds__(1024) void k_embed_group(EmbedGradArgs a, int R)
     if (tid == 0) {
         first_item[1024] = n_items;
         a.n_items[b] = n_items;
-        a.n_long[b] = (int32_t)unused;
+        a.n_long[b] = (int32_t)(uint32_t)y;
         a.before[b] = (int32_t)all_below;
     }
     __syncthreads();
@@ -125,14 +132,10 @@ __global__ __launch_bounds__(1024) void k_embed_group(EmbedGradArgs a, int R)
         list[i] = (lo + r0) | (int64_t)(i - first_item[r0]) << 32;
     }
 
-    // Placing: a wave's lanes with the same id take consecutive positions.
+    // Placing: a wave's lanes with the same id take consecutive positions.  Ids of
+    // a stretch of one batch are still in registers.
     for (int64_t t0 = t_lo; t0 < t_hi; t0 += 64 * U) {
-        int64_t id[U];
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int64_t t = t0 + u * 64 + lane;
-            id[u] = t < t_hi ? id_at<IDS64>(a.ids, t) : -1;
-        }
+        if (per > 64 * U) load(t0);
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             bool todo = id[u] >= lo && id[u] < hi && id[u] != a.padding_id;
