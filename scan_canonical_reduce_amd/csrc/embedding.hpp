@@ -32,7 +32,7 @@ struct EmbedGradArgs {
     int64_t ld_dw;
     // workspace
     int32_t *order, *offset;    // tokens by id; the first of each id (rows + 1)
-    int64_t* items;             // (row, chunk), at most one per token
+    int4* items;                // row, chunk, offset, tokens of the row; at most one per token
     int32_t *n_items, *n_long, *before;  // per group of ids
     int32_t* longs;
     float *part, *part_last;

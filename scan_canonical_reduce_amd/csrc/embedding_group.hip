@@ -49,7 +49,7 @@ __global__ __launch_bounds__(1024) void k_embed_group(EmbedGradArgs a, int R)
 {
     extern __shared__ int32_t hist[];  // [wave][id]: count, then the next position
     __shared__ Pairs scan[kWaves];
-    __shared__ int32_t first_item[1025];
+    __shared__ int32_t first_item[1025], first_token[1025];
     const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
     const int64_t b = blockIdx.x, lo = b * R;
     const int64_t hi = lo + R < a.rows ? lo + R : a.rows;
@@ -111,15 +111,17 @@ __global__ __launch_bounds__(1024) void k_embed_group(EmbedGradArgs a, int R)
     // entries of rows >= kEmbedChunk + 1 tokens long, from before / 65 on
     if (is_long) a.longs[all_below / (kEmbedChunk + 1) + long_pos] = (int32_t)(lo + tid);
     first_item[tid] = item;
+    first_token[tid] = off;
     if (tid == 0) {
         first_item[1024] = n_items;
+        first_token[1024] = (int32_t)all_below + (int32_t)(uint32_t)both;
         a.n_items[b] = n_items;
         a.n_long[b] = (int32_t)(uint32_t)y;
         a.before[b] = (int32_t)all_below;
     }
     __syncthreads();
     // the list of work, from the tokens before this group on
-    int64_t* list = a.items + (int64_t)all_below;
+    int4* list = a.items + all_below;
     for (int32_t i = tid; i < n_items; i += 1024) {
         int r0 = 0, r1 = 1023;  // the last id with first_item <= i
         while (r0 < r1) {
@@ -129,7 +131,8 @@ __global__ __launch_bounds__(1024) void k_embed_group(EmbedGradArgs a, int R)
             else
                 r1 = mid - 1;
         }
-        list[i] = (lo + r0) | (int64_t)(i - first_item[r0]) << 32;
+        list[i] = make_int4((int32_t)(lo + r0), i - first_item[r0], first_token[r0],
+                            first_token[r0 + 1] - first_token[r0]);
     }
 
     // Placing: a wave's lanes with the same id take consecutive positions.  Ids of

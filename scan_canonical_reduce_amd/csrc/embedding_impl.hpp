@@ -183,12 +183,12 @@ __device__ __forceinline__ int find_group(const int32_t* prefix, int32_t i)
     return lo;
 }
 
-// Sums occurrences [64 c, ...) of row v: V columns of this lane.
+// Sums an entry's occurrences [64 chunk, ...) of its row: V columns of this lane.
 template <typename T, typename G, int V>
-__device__ __forceinline__ void sum_entry(const EmbedGradArgs& a, int64_t v, int64_t c,
-                                          int64_t col, int lane)
+__device__ __forceinline__ void sum_entry(const EmbedGradArgs& a, int4 item, int64_t col, int lane)
 {
-    const int32_t off = uniform(a.offset[v]), n = uniform(a.offset[v + 1]) - off;
+    const int64_t v = uniform(item.x), c = uniform(item.y);
+    const int32_t off = uniform(item.z), n = uniform(item.w);
     const bool in = col < a.width;
     float acc[V];
     const int64_t p0 = off + c * kEmbedChunk;
@@ -281,8 +281,8 @@ __global__ __launch_bounds__(256, 4) void k_embed_sum(EmbedGradArgs a, int64_t g
             const int32_t e = (int32_t)(i / slabs);
             const int64_t slab = i - e * slabs;
             const int k = find_group(prefix, e);
-            const int64_t item = uniform(a.items[(int64_t)a.before[g0 + k] + (e - prefix[k])]);
-            sum_entry<T, G, V>(a, item & 0xffffffff, item >> 32, slab * 64 * V + lane * V, lane);
+            const int4 item = a.items[(int64_t)a.before[g0 + k] + (e - prefix[k])];
+            sum_entry<T, G, V>(a, item, slab * 64 * V + lane * V, lane);
         }
     }
     if (zero && !(blockIdx.x & 1)) zero_rows<G, VZ>(a, wave, waves, lane);

@@ -84,7 +84,7 @@ struct EmbedLayout : Layout {
         const size_t groups = (size_t)id_groups(rows);
         order = take(4 * (size_t)tokens);
         offset = take(4 * ((size_t)rows + 1));
-        items = take(8 * (size_t)tokens);
+        items = take(16 * (size_t)tokens);
         n_items = take(4 * groups);
         n_long = take(4 * groups);
         before = take(4 * groups);
@@ -352,7 +352,7 @@ canon_status_t canon_embedding_grad(int dtype, const void* dout, size_t ld_dout,
     a.ld_dw = (int64_t)ld_dw;
     a.order = l.at<int32_t>(ws, l.order);
     a.offset = l.at<int32_t>(ws, l.offset);
-    a.items = l.at<int64_t>(ws, l.items);
+    a.items = l.at<int4>(ws, l.items);
     a.n_items = l.at<int32_t>(ws, l.n_items);
     a.n_long = l.at<int32_t>(ws, l.n_long);
     a.before = l.at<int32_t>(ws, l.before);
