@@ -110,7 +110,7 @@ __global__ __launch_bounds__(256) void k_scan_back_sum(ScanArgs a)
     const Lane l = lane_place(a, (int)(blockIdx.x - slot * slabs));
     if (l.wch >= a.dg) return;
     float2(*ex)[16] = ex_all[threadIdx.x >> 6];
-    const Chunk ck = uniform(slot_chunk<kCh>(a.q, slot));
+    const Chunk ck = wave_slot_chunk<kCh>(a.q, slot);
     if (ck.len <= 0) return;
 
     float A2[KS], R[KS];
@@ -412,7 +412,7 @@ __global__ __launch_bounds__(256, 2) void k_selective_scan_grad(ScanArgs a)
         slot = uniform(slot_base<kCh>(a.q, s)) + (hi > 0 ? (hi - 1) / kCh : 0);
     } else {
         slot = id;
-        const Chunk ck = uniform(slot_chunk<kCh>(a.q, slot));
+        const Chunk ck = wave_slot_chunk<kCh>(a.q, slot);
         s = ck.s;
         span = ck.span;
         lo = ck.row;

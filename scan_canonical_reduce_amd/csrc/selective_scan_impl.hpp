@@ -361,7 +361,7 @@ __global__ __launch_bounds__(256, 4) void k_selective_scan(ScanArgs a)
         lo = 0;
         hi = span.len;
     } else {
-        const Chunk ck = uniform(slot_chunk<kCh>(a.q, slot));
+        const Chunk ck = wave_slot_chunk<kCh>(a.q, slot);
         if (ck.len <= 0) return;
         s = ck.s;
         span = ck.span;

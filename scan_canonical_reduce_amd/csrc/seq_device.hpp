@@ -266,32 +266,46 @@ struct Chunk {
     int32_t len;
 };
 
+// Chunk `slot - base` of sequence s, packed.
 template <int CH>
-__device__ __forceinline__ Chunk slot_chunk(const Seqs& q, int64_t slot)
+__device__ __forceinline__ Chunk packed_chunk(const Seqs& q, int64_t s, int64_t slot)
 {
     Chunk c;
-    if (q.starts == nullptr) {
-        const int64_t per = chunks_per_seq<CH>(q.rows);
-        c.s = slot / per;
-        c.span = Span{0, (int32_t)q.rows};
-        c.row = (int32_t)((slot - c.s * per) * CH);
-    } else {
-        int64_t lo = 0, hi = q.seqs - 1;  // the last sequence with base <= slot
-        while (lo < hi) {
-            const int64_t mid = (lo + hi + 1) >> 1;
-            if (slot_base<CH>(q, mid) <= slot)
-                lo = mid;
-            else
-                hi = mid - 1;
-        }
-        c.s = lo;
-        c.span = seq_span(q, lo);
-        const int64_t k = slot - slot_base<CH>(q, lo);
-        c.row = k < 0 || k > (int64_t)(0x7fffffff / CH) ? 0x7fffffff / CH * CH : (int32_t)k * CH;
-    }
+    c.s = s;
+    c.span = seq_span(q, s);
+    const int64_t k = slot - s - c.span.first / CH;
+    c.row = k < 0 || k > (int64_t)(0x7fffffff / CH) ? 0x7fffffff / CH * CH : (int32_t)k * CH;
     const int32_t left = c.span.len - c.row;
     c.len = left < CH ? left : CH;
     return c;
+}
+
+template <int CH>
+__device__ __forceinline__ Chunk even_chunk(const Seqs& q, int64_t slot)
+{
+    Chunk c;
+    const int64_t per = chunks_per_seq<CH>(q.rows);
+    c.s = slot / per;
+    c.span = Span{0, (int32_t)q.rows};
+    c.row = (int32_t)((slot - c.s * per) * CH);
+    const int32_t left = c.span.len - c.row;
+    c.len = left < CH ? left : CH;
+    return c;
+}
+
+template <int CH>
+__device__ __forceinline__ Chunk slot_chunk(const Seqs& q, int64_t slot)
+{
+    if (q.starts == nullptr) return even_chunk<CH>(q, slot);
+    int64_t lo = 0, hi = q.seqs - 1;  // the last sequence with base <= slot
+    while (lo < hi) {
+        const int64_t mid = (lo + hi + 1) >> 1;
+        if (slot_base<CH>(q, mid) <= slot)
+            lo = mid;
+        else
+            hi = mid - 1;
+    }
+    return packed_chunk<CH>(q, lo, slot);
 }
 
 // The value of a wave's first lane, in scalar registers: for values that are
@@ -307,6 +321,25 @@ __device__ __forceinline__ Span uniform(Span s) { return Span{uniform(s.first), 
 __device__ __forceinline__ Chunk uniform(Chunk c)
 {
     return Chunk{uniform(c.s), uniform(c.span), uniform(c.row), uniform(c.len)};
+}
+
+// slot_chunk for a slot that is the same in all lanes of a wave: 64 sequences are
+// looked at at a time, so that up to 64 take one load instead of one after the
+// other.
+template <int CH>
+__device__ __forceinline__ Chunk wave_slot_chunk(const Seqs& q, int64_t slot)
+{
+    if (q.starts == nullptr) return even_chunk<CH>(q, slot);
+    const int lane = threadIdx.x & 63;
+    int64_t lo = 0, n = q.seqs;  // it is one of the n sequences from lo on
+    while (n > 1) {
+        const int64_t step = (n + 63) / 64, at = lane * step;
+        const uint64_t hit = __ballot(at < n && slot_base<CH>(q, lo + (at < n ? at : 0)) <= slot);
+        const int64_t k = hit ? (63 - __builtin_clzll(hit)) * step : 0;
+        lo += k;
+        n = n - k < step ? n - k : step;
+    }
+    return uniform(packed_chunk<CH>(q, lo, slot));
 }
 
 template <typename T>
