@@ -72,7 +72,7 @@ __global__ __launch_bounds__(256) void k_embedding(EmbedArgs a)
 // the exact identity of an addition.
 template <int V, int LEVELS>
 struct PairCounter {
-    float sub[LEVELS][V];  // subtrees of 8, 16, 32, ... rows
+    float sub[LEVELS][V] = {};  // subtrees of 8, 16, 32, ... rows
     uint32_t batches = 0;
 
     __device__ __forceinline__ void add(float (&x)[8][V])
@@ -87,6 +87,16 @@ struct PairCounter {
         bool done = false;
 #pragma unroll
         for (int l = 0; l < LEVELS; ++l) {
+            if (V == 1) {
+                // selections: of branches that store one value the compiler makes
+                // one store to an array in memory
+                const bool up = batches >> l & 1, here = !up && !done;
+                const float sum = sub[l][0] + x[0][0];
+                sub[l][0] = here ? x[0][0] : sub[l][0];
+                x[0][0] = up && !done ? sum : x[0][0];
+                done |= here;
+                continue;
+            }
             if (done) continue;
             if (batches >> l & 1) {
 #pragma unroll
@@ -225,10 +235,10 @@ __device__ __forceinline__ void sum_entry(const EmbedGradArgs& a, int4 item, int
     for (int j = 0; j < V; ++j) part[j] = acc[j];
 }
 
-// Sets the rows v0 + (set bits of left) to zero.
+// Sets columns [c0, c1) of the rows v0 + (set bits of left) to zero.
 template <typename G, int V>
 __device__ __forceinline__ void zero_listed(const EmbedGradArgs& a, int64_t v0, uint64_t left,
-                                            int lane)
+                                            int64_t c0, int64_t c1, int lane)
 {
     while (left) {
         const int64_t row = v0 + __builtin_ctzll(left);
@@ -237,11 +247,11 @@ __device__ __forceinline__ void zero_listed(const EmbedGradArgs& a, int64_t v0, 
         if constexpr (V * sizeof(typename G::store_t) == 16) {
             typedef uint32_t u4 __attribute__((ext_vector_type(4)));
             const u4 zero = {0, 0, 0, 0};
-            for (int64_t c = lane * V; c < a.width; c += 64 * V)
+            for (int64_t c = c0 + lane * V; c < c1; c += 64 * V)
                 __builtin_nontemporal_store(zero, reinterpret_cast<u4*>(p + c));
         } else {
             const float zero[V] = {};
-            for (int64_t c = lane * V; c < a.width; c += 64 * V) st_vec<G, V>(p + c, zero);
+            for (int64_t c = c0 + lane * V; c < c1; c += 64 * V) st_vec<G, V>(p + c, zero);
         }
     }
 }
@@ -250,17 +260,37 @@ __device__ __forceinline__ void zero_listed(const EmbedGradArgs& a, int64_t v0, 
 // table of 65536 rows keeps 4096 waves busy.
 constexpr int kZeroRows = 16;
 
+// Rows to set to zero, kZeroRows at a time, and where they are few, cut into
+// parts of their columns, of two accesses or more, so that every wave has some (4
+// tokens, 118 rows of 3443 float32: 27 -> 10 us): f(first row, first column, end).
+template <int V, class F>
+__device__ __forceinline__ void each_zero_part(const EmbedGradArgs& a, int64_t wave,
+                                               int64_t waves, F&& f)
+{
+    const uint32_t blocks = (uint32_t)((a.rows + kZeroRows - 1) / kZeroRows);
+    const uint32_t steps = (uint32_t)((a.width + 64 * V - 1) / (64 * V));
+    uint32_t parts = (uint32_t)waves / blocks;
+    parts = parts < steps / 2 ? parts : steps / 2;
+    if (parts < 1) parts = 1;
+    const int64_t per = (int64_t)((steps + parts - 1) / parts) * (64 * V);
+    for (uint32_t i = (uint32_t)wave; i < blocks * parts; i += (uint32_t)waves) {
+        const uint32_t b = i / parts;
+        const int64_t c0 = (i - b * parts) * per;
+        f((int64_t)b * kZeroRows, c0, c0 + per < a.width ? c0 + per : a.width);
+    }
+}
+
 // Zero rows for ids without tokens.
 template <typename G, int V>
 __device__ __forceinline__ void zero_rows(const EmbedGradArgs& a, int64_t wave, int64_t waves,
                                           int lane)
 {
-    for (int64_t v0 = wave * kZeroRows; v0 < a.rows; v0 += waves * kZeroRows) {
+    each_zero_part<V>(a, wave, waves, [&](int64_t v0, int64_t c0, int64_t c1) {
         const int64_t v = v0 + lane;
         const bool none =
             lane < kZeroRows && v < a.rows && a.offset[v] == a.offset[v + 1];
-        zero_listed<G, V>(a, v0, __ballot(none), lane);
-    }
+        zero_listed<G, V>(a, v0, __ballot(none), c0, c1, lane);
+    });
 }
 
 template <typename T, typename G, int V>
@@ -373,7 +403,7 @@ __global__ __launch_bounds__(256) void k_embed_direct(EmbedGradArgs a)
     if (a.accumulate) return;
     // 16-byte stores of the gradient's type
     constexpr int VZ = V == 1 ? 1 : 16 / (int)sizeof(typename G::store_t);
-    for (int64_t v0 = wave * kZeroRows; v0 < a.rows; v0 += waves * kZeroRows) {
+    each_zero_part<VZ>(a, wave, waves, [&](int64_t v0, int64_t c0, int64_t c1) {
         uint64_t left = (1ull << (a.rows - v0 < kZeroRows ? a.rows - v0 : kZeroRows)) - 1;
 #pragma unroll
         for (int k = 0; k < C; ++k) {
@@ -384,8 +414,8 @@ __global__ __launch_bounds__(256) void k_embed_direct(EmbedGradArgs a)
                 left &= ~(1ull << (v - v0));
             }
         }
-        zero_listed<G, VZ>(a, v0, left, lane);
-    }
+        zero_listed<G, VZ>(a, v0, left, c0, c1, lane);
+    });
 }
 
 // Rows with more than 64 occurrences: the pairwise tree over the partial

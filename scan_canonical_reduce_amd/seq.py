@@ -204,7 +204,7 @@ def embedding(weight: torch.Tensor, ids: torch.Tensor, scale: float = 1.0,
     p, nb, tokens = _ids(what, ids)
     shape = ids.shape + (width,)
     if out is None:
-        out = torch.empty(shape, dtype=weight.dtype, device=weight.device)
+        out = weight.new_empty(shape)
         ld_out = width
     elif out.shape != shape or out.dtype != weight.dtype:
         raise _wrong(what, "out", out, shape, weight.dtype)
@@ -306,7 +306,7 @@ def causal_conv(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Tens
     head, channels, params = _conv(what, x, weight, bias, activation)
     state = (seqs, head[1] - 1, channels)
     if out is None:
-        out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        out = x.new_empty(x.shape)
     c = CONV.pack(*head, seqs, rows, channels, sp, *_rows(what, "x", x, x.shape, x.dtype, lead),
                   *_rows(what, "out", out, x.shape, x.dtype, lead), *params,
                   _flat(what, "init_state", init_state, state, x.dtype),
@@ -338,7 +338,7 @@ def causal_conv_grad(dout: torch.Tensor, x: torch.Tensor, weight: torch.Tensor,
     state = (seqs, head[1] - 1, channels)
     device = x.device
     if dx is None:
-        dx = torch.empty(x.shape, dtype=x.dtype, device=device)
+        dx = x.new_empty(x.shape)
     dw = torch.empty(weight.shape, dtype=torch.float32, device=device)
     db = None if bias is None else torch.empty(channels, dtype=torch.float32, device=device)
     di = None if init_state is None else torch.empty_like(init_state)
@@ -371,7 +371,7 @@ def causal_conv_step(x: torch.Tensor, state: torch.Tensor, weight: torch.Tensor,
     shape = (x.shape[0], head[1] - 1, channels)
     old = _flat(what, "state", state, shape, x.dtype)
     if out is None:
-        out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        out = x.new_empty(x.shape)
     c = CONV.pack(*head, x.shape[0], 1, channels, 0, *_step_rows(what, "x", x, x.shape, x.dtype),
                   *_step_rows(what, "out", out, x.shape, x.dtype), *params, old,
                   old if out_state is None else _flat(what, "out_state", out_state, shape, x.dtype),
@@ -465,7 +465,7 @@ def selective_scan(u: torch.Tensor, delta: torch.Tensor, A: torch.Tensor, B: tor
         size = L.canon_selective_scan_states(seqs, rows, packed, channels, n)
         kept = _flat(what, "states", states, (size,), f32)
     if out is None:
-        out = torch.empty(u.shape, dtype=dtype, device=u.device)
+        out = u.new_empty(u.shape)
     c = SCAN.pack(*head, seqs, rows, *sizes, sp, *_rows(what, "u", u, u.shape, dtype, lead),
                   *_rows(what, "delta", delta, u.shape, dtype, lead),
                   *(_NONE if z is None else _rows(what, "z", z, u.shape, dtype, lead)),
@@ -503,16 +503,11 @@ def selective_scan_grad(dout: torch.Tensor, u: torch.Tensor, delta: torch.Tensor
     L = _lib()
     size = L.canon_selective_scan_states(seqs, rows, packed, channels, n)
     g = SelectiveScanGrads(
-        du=torch.empty(u.shape, dtype=dtype, device=device),
-        ddelta=torch.empty(u.shape, dtype=dtype, device=device),
-        dA=torch.empty(A.shape, dtype=f32, device=device),
-        dB=torch.empty(bc, dtype=dtype, device=device),
-        dC=torch.empty(bc, dtype=dtype, device=device),
-        dD=None if D is None else torch.empty(channels, dtype=f32, device=device),
-        dz=None if z is None else torch.empty(u.shape, dtype=dtype, device=device),
-        ddelta_bias=None if delta_bias is None else
-        torch.empty(channels, dtype=f32, device=device),
-        dinit_state=torch.empty(shape, dtype=f32, device=device))
+        du=u.new_empty(u.shape), ddelta=u.new_empty(u.shape), dA=A.new_empty(A.shape),
+        dB=u.new_empty(bc), dC=u.new_empty(bc), dD=None if D is None else D.new_empty(channels),
+        dz=None if z is None else u.new_empty(u.shape),
+        ddelta_bias=None if delta_bias is None else delta_bias.new_empty(channels),
+        dinit_state=A.new_empty(shape))
     c = SCAN.pack(*head, seqs, rows, *sizes, sp, *_rows(what, "u", u, u.shape, dtype, lead),
                   *_rows(what, "delta", delta, u.shape, dtype, lead),
                   *(_NONE if z is None else _rows(what, "z", z, u.shape, dtype, lead)), *_NONE,
@@ -553,7 +548,7 @@ def selective_scan_step(state: torch.Tensor, u: torch.Tensor, delta: torch.Tenso
     shape = (seqs, sizes[0], sizes[2])
     old = _flat(what, "state", state, shape, f32)
     if out is None:
-        out = torch.empty(u.shape, dtype=dtype, device=u.device)
+        out = u.new_empty(u.shape)
     c = SCAN.pack(*head, seqs, 1, *sizes, 0, *_step_rows(what, "u", u, u.shape, dtype),
                   *_step_rows(what, "delta", delta, u.shape, dtype),
                   *(_NONE if z is None else _step_rows(what, "z", z, u.shape, dtype)),
