@@ -22,6 +22,8 @@
 //  3. k_embed_finish: the tree over the partial values.
 #pragma once
 
+#include <type_traits>
+
 #include "embedding.hpp"
 #include "launch.hpp"
 
@@ -34,11 +36,40 @@ __device__ __forceinline__ int64_t token_id(const void* ids, bool ids64, int64_t
                  : (int64_t) static_cast<const int32_t*>(ids)[t];
 }
 
-template <typename T, int V>
+// V elements as one access, at its own alignment (AL) or the element's.
+template <typename T, int V, bool AL>
+__device__ __forceinline__ Vec<T, V> ld_any(const typename T::store_t* p)
+{
+    if constexpr (AL) return ld_vec<T, V>(p);
+    Vec<T, V> v;
+    __builtin_memcpy(&v, p, sizeof(v));
+    return v;
+}
+template <typename T, int V, bool AL>
+__device__ __forceinline__ void st_any(typename T::store_t* p, const float (&v)[V])
+{
+    Vec<T, V> o;
+#pragma unroll
+    for (int i = 0; i < V; ++i) o.e[i] = T::round(v[i]);
+    if constexpr (AL)
+        *reinterpret_cast<Vec<T, V>*>(p) = o;
+    else
+        __builtin_memcpy(p, &o, sizeof(o));
+}
+
+// The column of a lane's vector: where rows are not whole vectors (they are at
+// least one) the last one is moved back over the one before it.
+template <int V, bool AL>
+__device__ __forceinline__ int64_t vec_col(int64_t col, int64_t width)
+{
+    return AL || col + V <= width ? col : width - V;
+}
+
+template <typename T, int V, bool AL>
 __global__ __launch_bounds__(256) void k_embedding(EmbedArgs a)
 {
     using E = typename T::store_t;
-    const int64_t nv = a.width / V;
+    const int64_t nv = (a.width + V - 1) / V;
     const int64_t n = a.tokens * nv;
     constexpr int U = 4;
     const int64_t i0 = (int64_t)blockIdx.x * (256 * U) + threadIdx.x;
@@ -50,11 +81,11 @@ __global__ __launch_bounds__(256) void k_embedding(EmbedArgs a)
         dst[u] = nullptr;
         x[u] = Vec<T, V>{};
         if (i < n) {
-            const int64_t t = i / nv, c = (i - t * nv) * V;
+            const int64_t t = i / nv, c = vec_col<V, AL>((i - t * nv) * V, a.width);
             const int64_t id = token_id(a.ids, a.ids64, t);
             dst[u] = static_cast<E*>(a.out) + t * a.ld_out + c;
             if (id >= 0 && id < a.rows)
-                x[u] = ld_vec<T, V>(static_cast<const E*>(a.weight) + id * a.ld_weight + c);
+                x[u] = ld_any<T, V, AL>(static_cast<const E*>(a.weight) + id * a.ld_weight + c);
         }
     }
 #pragma unroll
@@ -63,7 +94,7 @@ __global__ __launch_bounds__(256) void k_embedding(EmbedArgs a)
         float y[V];
 #pragma unroll
         for (int j = 0; j < V; ++j) y[j] = T::load(x[u].e[j]) * a.scale;
-        st_vec<T, V>(dst[u], y);
+        st_any<T, V, AL>(dst[u], y);
     }
 }
 
@@ -121,20 +152,28 @@ struct PairCounter {
     }
 };
 
-template <typename G, int V>
+// Stores V columns from c on, all but the first `skip` (which the vector before
+// has stored).
+template <typename G, int V, bool AL>
 __device__ __forceinline__ void store_grad(const EmbedGradArgs& a, int64_t v, int64_t c,
-                                           const float (&sum)[V])
+                                           const float (&sum)[V], int skip)
 {
     typename G::store_t* p = static_cast<typename G::store_t*>(a.dw) + v * a.ld_dw + c;
     float y[V];
 #pragma unroll
     for (int j = 0; j < V; ++j) y[j] = sum[j] * a.scale;
+    if (!AL && skip) {
+#pragma unroll
+        for (int j = 0; j < V; ++j)
+            if (j >= skip) p[j] = G::round(a.accumulate ? G::load(p[j]) + y[j] : y[j]);
+        return;
+    }
     if (a.accumulate) {
-        const Vec<G, V> old = ld_vec<G, V>(p);
+        const Vec<G, V> old = ld_any<G, V, AL>(p);
 #pragma unroll
         for (int j = 0; j < V; ++j) y[j] = G::load(old.e[j]) + y[j];
     }
-    st_vec<G, V>(p, y);
+    st_any<G, V, AL>(p, y);
 }
 
 // Groups whose prefix sums a workgroup keeps in LDS; callers walk more groups
@@ -194,12 +233,14 @@ __device__ __forceinline__ int find_group(const int32_t* prefix, int32_t i)
 }
 
 // Sums an entry's occurrences [64 chunk, ...) of its row: V columns of this lane.
-template <typename T, typename G, int V>
-__device__ __forceinline__ void sum_entry(const EmbedGradArgs& a, int4 item, int64_t col, int lane)
+template <typename T, typename G, int V, bool AL>
+__device__ __forceinline__ void sum_entry(const EmbedGradArgs& a, int4 item, int64_t lane_col,
+                                          int lane)
 {
     const int64_t v = uniform(item.x), c = uniform(item.y);
     const int32_t off = uniform(item.z), n = uniform(item.w);
-    const bool in = col < a.width;
+    const bool in = lane_col < a.width;
+    const int64_t col = vec_col<V, AL>(lane_col, a.width);
     float acc[V];
     const int64_t p0 = off + c * kEmbedChunk;
     const int m = n - c * kEmbedChunk < kEmbedChunk ? (int)(n - c * kEmbedChunk) : kEmbedChunk;
@@ -211,7 +252,7 @@ __device__ __forceinline__ void sum_entry(const EmbedGradArgs& a, int4 item, int
 #pragma unroll
         for (int r = 0; r < 8; ++r) {
             const int k = b * 8 + r < m ? b * 8 + r : 0;
-            raw[r] = ld_vec<T, V>(x + (int64_t)__builtin_amdgcn_readlane(mine, k) * a.ld_dout);
+            raw[r] = ld_any<T, V, AL>(x + (int64_t)__builtin_amdgcn_readlane(mine, k) * a.ld_dout);
         }
         float t[8][V];
 #pragma unroll
@@ -223,7 +264,7 @@ __device__ __forceinline__ void sum_entry(const EmbedGradArgs& a, int4 item, int
     tree.total(acc);
     if (!in) return;
     if (n <= kEmbedChunk) {
-        store_grad<G, V>(a, v, col, acc);
+        store_grad<G, V, AL>(a, v, col, acc, (int)(lane_col - col));
         return;
     }
     // Full chunks and last chunks of long rows each start at least 64
@@ -236,7 +277,7 @@ __device__ __forceinline__ void sum_entry(const EmbedGradArgs& a, int4 item, int
 }
 
 // Sets columns [c0, c1) of the rows v0 + (set bits of left) to zero.
-template <typename G, int V>
+template <typename G, int V, bool AL>
 __device__ __forceinline__ void zero_listed(const EmbedGradArgs& a, int64_t v0, uint64_t left,
                                             int64_t c0, int64_t c1, int lane)
 {
@@ -247,11 +288,22 @@ __device__ __forceinline__ void zero_listed(const EmbedGradArgs& a, int64_t v0, 
         if constexpr (V * sizeof(typename G::store_t) == 16) {
             typedef uint32_t u4 __attribute__((ext_vector_type(4)));
             const u4 zero = {0, 0, 0, 0};
-            for (int64_t c = c0 + lane * V; c < c1; c += 64 * V)
+            int64_t b = c0, e = c1;
+            if (!AL) {
+                // whole cache lines go past the caches; elements before the first one
+                // and after the last, at most 63, share theirs with other rows
+                constexpr int line = 128 / (int)sizeof(typename G::store_t);
+                const int64_t head = (int64_t)((0 - reinterpret_cast<uintptr_t>(p + c0)) % 128) /
+                                     (int64_t)sizeof(*p);
+                b = head < c1 - c0 ? c0 + head : c1;
+                e = c1 - (c1 - b) % line;
+                if (lane < b - c0) p[c0 + lane] = 0;
+                if (lane < c1 - e) p[e + lane] = 0;
+            }
+            for (int64_t c = b + lane * V; c < e; c += 64 * V)
                 __builtin_nontemporal_store(zero, reinterpret_cast<u4*>(p + c));
         } else {
-            const float zero[V] = {};
-            for (int64_t c = c0 + lane * V; c < c1; c += 64 * V) st_vec<G, V>(p + c, zero);
+            for (int64_t c = c0 + lane; c < c1; c += 64) p[c] = 0;
         }
     }
 }
@@ -281,7 +333,7 @@ __device__ __forceinline__ void each_zero_part(const EmbedGradArgs& a, int64_t w
 }
 
 // Zero rows for ids without tokens.
-template <typename G, int V>
+template <typename G, int V, bool AL>
 __device__ __forceinline__ void zero_rows(const EmbedGradArgs& a, int64_t wave, int64_t waves,
                                           int lane)
 {
@@ -289,11 +341,11 @@ __device__ __forceinline__ void zero_rows(const EmbedGradArgs& a, int64_t wave, 
         const int64_t v = v0 + lane;
         const bool none =
             lane < kZeroRows && v < a.rows && a.offset[v] == a.offset[v + 1];
-        zero_listed<G, V>(a, v0, __ballot(none), c0, c1, lane);
+        zero_listed<G, V, AL>(a, v0, __ballot(none), c0, c1, lane);
     });
 }
 
-template <typename T, typename G, int V>
+template <typename T, typename G, int V, bool AL>
 __global__ __launch_bounds__(256, 4) void k_embed_sum(EmbedGradArgs a, int64_t groups)
 {
     __shared__ int32_t prefix[kGroupsInLds + 1];
@@ -304,7 +356,7 @@ __global__ __launch_bounds__(256, 4) void k_embed_sum(EmbedGradArgs a, int64_t g
     // 16-byte stores of the gradient's type
     constexpr int VZ = V == 1 ? 1 : 16 / (int)sizeof(typename G::store_t);
     const bool zero = !a.accumulate;
-    if (zero && (blockIdx.x & 1)) zero_rows<G, VZ>(a, wave, waves, lane);
+    if (zero && (blockIdx.x & 1)) zero_rows<G, VZ, AL>(a, wave, waves, lane);
     for (int64_t g0 = 0; g0 < groups; g0 += kGroupsInLds) {
         const int64_t total = group_prefix(a.n_items, g0, groups, prefix);
         for (int64_t i = wave; i < total * slabs; i += waves) {
@@ -312,10 +364,10 @@ __global__ __launch_bounds__(256, 4) void k_embed_sum(EmbedGradArgs a, int64_t g
             const int64_t slab = i - e * slabs;
             const int k = find_group(prefix, e);
             const int4 item = a.items[(int64_t)a.before[g0 + k] + (e - prefix[k])];
-            sum_entry<T, G, V>(a, item, slab * 64 * V + lane * V, lane);
+            sum_entry<T, G, V, AL>(a, item, slab * 64 * V + lane * V, lane);
         }
     }
-    if (zero && !(blockIdx.x & 1)) zero_rows<G, VZ>(a, wave, waves, lane);
+    if (zero && !(blockIdx.x & 1)) zero_rows<G, VZ, AL>(a, wave, waves, lane);
 }
 
 // Up to 256 tokens, one launch and no workspace: a wave keeps all ids, four a
@@ -327,7 +379,7 @@ __global__ __launch_bounds__(256, 4) void k_embed_sum(EmbedGradArgs a, int64_t g
 // flight: where all tokens are one, 29 and 52 us.
 constexpr int kEmbedDirect = 256;
 
-template <typename T, typename G, int V>
+template <typename T, typename G, int V, bool AL>
 __global__ __launch_bounds__(256) void k_embed_direct(EmbedGradArgs a)
 {
     const int lane = threadIdx.x & 63;
@@ -357,8 +409,9 @@ __global__ __launch_bounds__(256) void k_embed_direct(EmbedGradArgs a)
             if (same[k]) first = k * 64 + __builtin_ctzll(same[k]);
         }
         if (first != t) continue;
-        const int64_t col = (int64_t)slab * 64 * V + lane * V;
-        const bool in = col < a.width;
+        const int64_t lane_col = (int64_t)slab * 64 * V + lane * V;
+        const bool in = lane_col < a.width;
+        const int64_t col = vec_col<V, AL>(lane_col, a.width);
         const typename T::store_t* x =
             static_cast<const typename T::store_t*>(a.dout) + (in ? col : 0);
         PairCounter<V, 6> tree;
@@ -379,7 +432,7 @@ __global__ __launch_bounds__(256) void k_embed_direct(EmbedGradArgs a)
                 if (cur) {
                     const int64_t row = k * 64 + __builtin_ctzll(cur);
                     cur &= cur - 1;
-                    raw[r] = ld_vec<T, V>(x + row * a.ld_dout);
+                    raw[r] = ld_any<T, V, AL>(x + row * a.ld_dout);
                     n = r + 1;
                 }
             }
@@ -398,7 +451,7 @@ __global__ __launch_bounds__(256) void k_embed_direct(EmbedGradArgs a)
         }
         float acc[V];
         tree.total(acc);
-        if (in) store_grad<G, V>(a, v, col, acc);
+        if (in) store_grad<G, V, AL>(a, v, col, acc, (int)(lane_col - col));
     }
     if (a.accumulate) return;
     // 16-byte stores of the gradient's type
@@ -414,7 +467,7 @@ __global__ __launch_bounds__(256) void k_embed_direct(EmbedGradArgs a)
                 left &= ~(1ull << (v - v0));
             }
         }
-        zero_listed<G, VZ>(a, v0, left, c0, c1, lane);
+        zero_listed<G, VZ, AL>(a, v0, left, c0, c1, lane);
     });
 }
 
@@ -477,56 +530,66 @@ __global__ __launch_bounds__(64 * kFinishWaves) void k_embed_finish(EmbedGradArg
 #pragma unroll
                     for (int j = 0; j < kFinishWaves; j += 2 * d) s[j] += s[j + d];
                 const float one[1] = {s[0]};
-                if (at < a.width) store_grad<G, 1>(a, v, at, one);
+                if (at < a.width) store_grad<G, 1, true>(a, v, at, one, 0);
             }
             __syncthreads();
         }
     }
 }
 
+// f(V, AL): 16-byte accesses, at any alignment where rows are not aligned to
+// that (16384 x 4095 bf16 rows: lookup 114 -> 41 us, gradient to
+// 65536 float32 rows 820 -> 340), or
+// single elements where a row has fewer.
+template <typename T, class F>
+hipError_t with_access(bool aligned, int64_t width, F&& f)
+{
+    constexpr int V = 16 / (int)sizeof(typename T::store_t);
+    if (aligned) return f(std::integral_constant<int, V>{}, std::true_type{});
+    if (width >= V) return f(std::integral_constant<int, V>{}, std::false_type{});
+    return f(std::integral_constant<int, 1>{}, std::true_type{});
+}
+
 template <typename T>
 hipError_t launch_embedding(const EmbedArgs& a, hipStream_t st)
 {
-    constexpr int V = 16 / (int)sizeof(typename T::store_t);
-    const int64_t n = a.tokens * (a.vec ? a.width / V : a.width);
-    const unsigned grid = (unsigned)((n + 1023) / 1024);
-    if (grid == 0) return hipSuccess;
-    if (a.vec)
-        k_embedding<T, V><<<dim3(grid), dim3(256), 0, st>>>(a);
-    else
-        k_embedding<T, 1><<<dim3(grid), dim3(256), 0, st>>>(a);
-    return hipGetLastError();
+    return with_access<T>(a.vec, a.width, [&](auto v, auto al) {
+        constexpr int V = decltype(v)::value;
+        const int64_t n = a.tokens * ((a.width + V - 1) / V);
+        k_embedding<T, V, decltype(al)::value>
+            <<<dim3((unsigned)((n + 1023) / 1024)), dim3(256), 0, st>>>(a);
+        return hipGetLastError();
+    });
 }
 
 template <typename T, typename G>
 hipError_t launch_embedding_grad(const EmbedGradArgs& a, hipStream_t st)
 {
-    constexpr int V = 16 / (int)sizeof(typename T::store_t);
-    // four workgroups fit a compute unit (k_embed_sum's launch bound)
-    const int64_t cus = (int64_t)device_cus(), cap = cus * 4;
-    const int64_t slabs = (a.width + 64 * (a.vec ? V : 1) - 1) / (64 * (a.vec ? V : 1));
-    const int64_t want = (a.tokens * slabs + (a.accumulate ? 0 : a.rows) + 3) / 4;
-    const dim3 grid((unsigned)capped_grid(want < 1 ? 1 : want < cap ? want : cap));
-    if (a.tokens <= kEmbedDirect) {
-        const int64_t waves = a.tokens * slabs * (a.vec ? 2 : 1) + (a.accumulate ? 0 : a.rows);
-        const dim3 direct((unsigned)capped_grid(waves < 4 ? 1 : waves / 4 < cap ? waves / 4 : cap));
-        if (a.vec)
-            k_embed_direct<T, G, V / 2><<<direct, dim3(256), 0, st>>>(a);
-        else
-            k_embed_direct<T, G, 1><<<direct, dim3(256), 0, st>>>(a);
+    return with_access<T>(a.vec, a.width, [&](auto v, auto al) {
+        constexpr int V = decltype(v)::value;
+        constexpr bool AL = decltype(al)::value;
+        // four workgroups fit a compute unit (k_embed_sum's launch bound)
+        const int64_t cus = (int64_t)device_cus(), cap = cus * 4;
+        const int64_t slabs = (a.width + 64 * V - 1) / (64 * V);
+        if (a.tokens <= kEmbedDirect) {
+            const int64_t waves =
+                a.tokens * slabs * (V > 1 ? 2 : 1) + (a.accumulate ? 0 : a.rows);
+            const dim3 direct(
+                (unsigned)capped_grid(waves < 4 ? 1 : waves / 4 < cap ? waves / 4 : cap));
+            k_embed_direct<T, G, V == 1 ? 1 : V / 2, AL><<<direct, dim3(256), 0, st>>>(a);
+            return hipGetLastError();
+        }
+        const int64_t groups = id_groups(a.rows);
+        if (hipError_t e = launch_embedding_group(a, st)) return e;
+        const int64_t want = (a.tokens * slabs + (a.accumulate ? 0 : a.rows) + 3) / 4;
+        const dim3 grid((unsigned)capped_grid(want < 1 ? 1 : want < cap ? want : cap));
+        k_embed_sum<T, G, V, AL><<<grid, dim3(256), 0, st>>>(a, groups);
+        if (hipError_t e = hipGetLastError()) return e;
+        const int64_t most = a.tokens / (kEmbedChunk + 1) * ((a.width + 255) / 256);
+        k_embed_finish<G><<<dim3((unsigned)capped_grid(most < cus ? most : cus)),
+                            dim3(64 * kFinishWaves), 0, st>>>(a, groups);
         return hipGetLastError();
-    }
-    const int64_t groups = id_groups(a.rows);
-    if (hipError_t e = launch_embedding_group(a, st)) return e;
-    if (a.vec)
-        k_embed_sum<T, G, V><<<grid, dim3(256), 0, st>>>(a, groups);
-    else
-        k_embed_sum<T, G, 1><<<grid, dim3(256), 0, st>>>(a, groups);
-    if (hipError_t e = hipGetLastError()) return e;
-    const int64_t most = a.tokens / (kEmbedChunk + 1) * ((a.width + 255) / 256);
-    k_embed_finish<G><<<dim3((unsigned)capped_grid(most < cus ? most : cus)), dim3(64 * kFinishWaves),
-                        0, st>>>(a, groups);
-    return hipGetLastError();
+    });
 }
 
 }  // namespace seq

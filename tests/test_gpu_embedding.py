@@ -188,3 +188,28 @@ def test_refusals(canon):
         canon.embedding_grad(w[:4], ids, 10, dtype=torch.float16)
     with pytest.raises(ValueError):
         canon.embedding_grad(w[:4], ids, 10, out=torch.empty(9, 8, device="cuda"))
+
+
+@pytest.mark.parametrize("dtype,grad", [(F32, F32), (BF16, F32), (BF16, BF16), (F16, F16)])
+@pytest.mark.parametrize("width", [3, 4, 5, 7, 8, 9, 15, 63, 515, 1001])
+def test_rows_of_any_width_and_place(canon, dtype, grad, width):
+    """Rows that are not whole 16-byte vectors, or not aligned to them: same bits,
+    each column added once, nothing written beside the rows."""
+    g = torch.Generator().manual_seed(width)
+    table = torch.randn(40, width + 9, generator=g).to(dtype).cuda()
+    for tokens, off, kind in ((3, 0, "zipf"), (200, 1, "few"), (900, 0, "zipf"), (900, 3, "one")):
+        ids = make_ids(tokens, 40, kind, tokens)
+        w = table[:, off:off + width]
+        out = torch.full((tokens, width + 4), 7.0, dtype=dtype, device="cuda")
+        canon.embedding(w, ids.cuda(), 0.5, out=out[:, off:off + width])
+        assert same_bits(out[:, off:off + width], (w.float() * 0.5)[ids.cuda()].to(dtype))
+        assert (out[:, :off] == 7).all() and (out[:, off + width:] == 7).all()
+        dout = torch.randn(tokens, width + 5, generator=g).to(dtype)[:, off:off + width]
+        dw = torch.full((40, width + 4), 7.0, dtype=grad, device="cuda")
+        canon.embedding_grad(dout.cuda(), ids.cuda(), 40, 1.5, out=dw[:, off:off + width])
+        assert same_bits(dw[:, off:off + width], grad_ref(dout, ids, 40, 1.5, dtype=grad))
+        old = dw[:, off:off + width].cpu()
+        canon.embedding_grad(dout.cuda(), ids.cuda(), 40, 1.5, out=dw[:, off:off + width],
+                             accumulate=True)
+        assert same_bits(dw[:, off:off + width], grad_ref(dout, ids, 40, 1.5, None, old, grad))
+        assert (dw[:, :off] == 7).all() and (dw[:, off + width:] == 7).all()
