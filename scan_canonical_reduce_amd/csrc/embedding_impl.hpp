@@ -36,35 +36,6 @@ __device__ __forceinline__ int64_t token_id(const void* ids, bool ids64, int64_t
                  : (int64_t) static_cast<const int32_t*>(ids)[t];
 }
 
-// V elements as one access, at its own alignment (AL) or the element's.
-template <typename T, int V, bool AL>
-__device__ __forceinline__ Vec<T, V> ld_any(const typename T::store_t* p)
-{
-    if constexpr (AL) return ld_vec<T, V>(p);
-    Vec<T, V> v;
-    __builtin_memcpy(&v, p, sizeof(v));
-    return v;
-}
-template <typename T, int V, bool AL>
-__device__ __forceinline__ void st_any(typename T::store_t* p, const float (&v)[V])
-{
-    Vec<T, V> o;
-#pragma unroll
-    for (int i = 0; i < V; ++i) o.e[i] = T::round(v[i]);
-    if constexpr (AL)
-        *reinterpret_cast<Vec<T, V>*>(p) = o;
-    else
-        __builtin_memcpy(p, &o, sizeof(o));
-}
-
-// The column of a lane's vector: where rows are not whole vectors (they are at
-// least one) the last one is moved back over the one before it.
-template <int V, bool AL>
-__device__ __forceinline__ int64_t vec_col(int64_t col, int64_t width)
-{
-    return AL || col + V <= width ? col : width - V;
-}
-
 template <typename T, int V, bool AL>
 __global__ __launch_bounds__(256) void k_embedding(EmbedArgs a)
 {
@@ -538,9 +509,8 @@ __global__ __launch_bounds__(64 * kFinishWaves) void k_embed_finish(EmbedGradArg
 }
 
 // f(V, AL): 16-byte accesses, at any alignment where rows are not aligned to
-// that (16384 x 4095 bf16 rows: lookup 114 -> 41 us, gradient to
-// 65536 float32 rows 820 -> 340), or
-// single elements where a row has fewer.
+// that (16384 x 4095 bf16 rows: lookup 114 -> 41 us, gradient to 65536 float32
+// rows 820 -> 340), or single elements where a row has fewer.
 template <typename T, class F>
 hipError_t with_access(bool aligned, int64_t width, F&& f)
 {

@@ -168,7 +168,7 @@ canon_status_t conv_args(const canon_conv_t* c, bool step, bool grad, ConvArgs* 
              rows_aligned(a->dx, es, v, false) && ptr_aligned(a->init, v) &&
              ptr_aligned(a->final, v) && ptr_aligned(a->dfinal, v) && ptr_aligned(a->dinit, v);
     // threads of the shortest runs: four channels each, two in the backward
-    // pass, one where not vectorised
+    // pass, or (counted so wherever it can be) one
     const int64_t per = a->vec ? c->channels / (grad ? 2 : 4) : c->channels;
     if (!mul_fits(per, slot_count<8>(c->seqs, rows, packed), kMaxGrid256 * 255))
         return CANON_EUNSUPPORTED;

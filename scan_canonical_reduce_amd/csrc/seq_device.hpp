@@ -80,6 +80,35 @@ __device__ __forceinline__ void st_vec(typename T::store_t* p, const float (&v)[
     *reinterpret_cast<Vec<T, V>*>(p) = o;
 }
 
+// V elements as one access, at its own alignment (AL) or the element's.
+template <typename T, int V, bool AL>
+__device__ __forceinline__ Vec<T, V> ld_any(const typename T::store_t* p)
+{
+    if constexpr (AL) return ld_vec<T, V>(p);
+    Vec<T, V> v;
+    __builtin_memcpy(&v, p, sizeof(v));
+    return v;
+}
+template <typename T, int V, bool AL>
+__device__ __forceinline__ void st_any(typename T::store_t* p, const float (&v)[V])
+{
+    Vec<T, V> o;
+#pragma unroll
+    for (int i = 0; i < V; ++i) o.e[i] = T::round(v[i]);
+    if constexpr (AL)
+        *reinterpret_cast<Vec<T, V>*>(p) = o;
+    else
+        __builtin_memcpy(p, &o, sizeof(o));
+}
+
+// The column of a lane's vector: where rows are not whole vectors (they are at
+// least one) the last one is moved back over the one before it.
+template <int V, bool AL>
+__device__ __forceinline__ int64_t vec_col(int64_t col, int64_t width)
+{
+    return AL || col + V <= width ? col : width - V;
+}
+
 // --------------------------------------------------------------- scalar functions
 constexpr float kLog2e = 0x1.715476p+0f;     // log2(e) to 24 bits
 constexpr float kLog2eLo = 0x1.4ae0bep-26f;  // and the rest

@@ -284,3 +284,42 @@ def test_backward_near_the_end(canon, taps, rows):
     tol = rows * (dp + (rows + 2) * half * 1.1 * gm)
     assert (want.dweight.double().cpu() - dw).abs().max() <= tol * xm
     assert (want.dbias.double().cpu() - db).abs().max() <= tol
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16, F16])
+@pytest.mark.parametrize("channels", [1, 2, 3, 4, 5, 6, 7, 9, 255, 1001])
+def test_channels_of_any_number_and_place(canon, dtype, channels):
+    """Channels that are not whole vectors, or not aligned to them: the bits of the
+    same channels among more, states updated in place, nothing written beside."""
+    wide, taps, rows, seqs = (channels + 15) // 8 * 8, 4, 77, 3
+    d = cuda(inputs(dtype, [rows] * seqs, wide, taps, False, seed=channels))
+    for off in (0, 1):
+        cut = slice(off, off + channels)
+
+        def own(t, dim=-1):  # the channels alone, contiguous
+            return t.narrow(dim, off, channels).contiguous()
+
+        w, b, init = own(d["w"], 0), own(d["b"]), own(d["init"])
+        final = torch.empty_like(d["init"])
+        want = canon.causal_conv(d["x"], d["w"], d["b"], "silu", None, d["init"], final)
+        state = init.clone()
+        out = torch.full_like(want, 7.0)
+        canon.causal_conv(d["x"][..., cut], w, b, "silu", None, state, state, out[..., cut])
+        assert torch.equal(out[..., cut], want[..., cut]) and torch.equal(state, own(final))
+        assert (out[..., :off] == 7).all() and (out[..., off + channels:] == 7).all()
+        g = canon.causal_conv_grad(d["dout"], d["x"], d["w"], d["b"], "silu", None, d["init"],
+                                   d["dfinal"])
+        dx = torch.full_like(want, 7.0)
+        h = canon.causal_conv_grad(d["dout"][..., cut], d["x"][..., cut], w, b, "silu", None,
+                                   init, own(d["dfinal"]), dx[..., cut])
+        assert torch.equal(dx[..., cut], g.dx[..., cut])
+        assert (dx[..., :off] == 7).all() and (dx[..., off + channels:] == 7).all()
+        assert torch.equal(h.dweight, own(g.dweight, 0)) and torch.equal(h.dbias, own(g.dbias))
+        assert torch.equal(h.dinit_state, own(g.dinit_state))
+        all_state, state = d["init"].clone(), init.clone()
+        for t in range(3):
+            a = canon.causal_conv_step(d["x"][:, t], all_state, d["w"], d["b"], "silu")
+            out = torch.full((seqs, channels + 5), 7.0, dtype=dtype, device="cuda")
+            canon.causal_conv_step(d["x"][:, t, cut], state, w, b, "silu", out=out[:, :channels])
+            assert torch.equal(out[:, :channels], a[:, cut]) and (out[:, channels:] == 7).all()
+            assert torch.equal(state, own(all_state))
