@@ -53,6 +53,36 @@ inline int64_t id_groups(int64_t rows)
     return (rows + r - 1) / r;
 }
 
+constexpr int kGroupWaves = 16;  // of a workgroup that groups tokens by id
+
+// Exclusive sums over the workgroup's 1024 threads, of two pairs of counts at
+// once (each pair in the halves of 64 bits); x and y become the sums of all.
+struct Pairs {
+    uint64_t x, y;
+};
+__device__ __forceinline__ Pairs block_exclusive(uint64_t& x, uint64_t& y, Pairs* lds)
+{
+    const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+    Pairs run = {x, y};
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2) {
+        const uint64_t ox = __shfl_up((unsigned long long)run.x, d, 64);
+        const uint64_t oy = __shfl_up((unsigned long long)run.y, d, 64);
+        if (lane >= d) run.x += ox, run.y += oy;
+    }
+    if (lane == 63) lds[w] = run;
+    __syncthreads();
+    Pairs base = {0, 0}, all = {0, 0};
+#pragma unroll
+    for (int k = 0; k < kGroupWaves; ++k) {
+        if (k == w) base = all;
+        all.x += lds[k].x, all.y += lds[k].y;
+    }
+    base.x += run.x - x, base.y += run.y - y;
+    x = all.x, y = all.y;
+    return base;
+}
+
 template <typename T>
 hipError_t launch_embedding(const EmbedArgs& a, hipStream_t st);
 hipError_t launch_embedding_group(const EmbedGradArgs& a, hipStream_t st);

@@ -6,8 +6,6 @@ namespace seq {
 
 namespace {
 
-constexpr int kWaves = 16;
-
 template <bool IDS64>
 __device__ __forceinline__ int64_t id_at(const void* ids, int64_t t)
 {
@@ -15,49 +13,21 @@ __device__ __forceinline__ int64_t id_at(const void* ids, int64_t t)
                  : (int64_t) static_cast<const int32_t*>(ids)[t];
 }
 
-// Exclusive sums over the workgroup's 1024 threads, of two pairs of counts at
-// once (each pair in the halves of 64 bits); x and y become the sums of all.
-struct Pairs {
-    uint64_t x, y;
-};
-__device__ __forceinline__ Pairs block_exclusive(uint64_t& x, uint64_t& y, Pairs* lds)
-{
-    const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
-    Pairs run = {x, y};
-#pragma unroll
-    for (int d = 1; d < 64; d *= 2) {
-        const uint64_t ox = __shfl_up((unsigned long long)run.x, d, 64);
-        const uint64_t oy = __shfl_up((unsigned long long)run.y, d, 64);
-        if (lane >= d) run.x += ox, run.y += oy;
-    }
-    if (lane == 63) lds[w] = run;
-    __syncthreads();
-    Pairs base = {0, 0}, all = {0, 0};
-#pragma unroll
-    for (int k = 0; k < kWaves; ++k) {
-        if (k == w) base = all;
-        all.x += lds[k].x, all.y += lds[k].y;
-    }
-    base.x += run.x - x, base.y += run.y - y;
-    x = all.x, y = all.y;
-    return base;
-}
-
-// R ids a workgroup (R <= 512); dynamic LDS: kWaves x R counts.
+// R ids a workgroup (R <= 512); dynamic LDS: kGroupWaves x R counts.
 template <bool IDS64>
 __global__ __launch_bounds__(1024) void k_embed_group(EmbedGradArgs a, int R)
 {
     extern __shared__ int32_t hist[];  // [wave][id]: count, then the next position
-    __shared__ Pairs scan[kWaves];
+    __shared__ Pairs scan[kGroupWaves];
     __shared__ int32_t first_item[1025], first_token[1025];
     const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
     const int64_t b = blockIdx.x, lo = b * R;
     const int64_t hi = lo + R < a.rows ? lo + R : a.rows;
-    for (int i = tid; i < kWaves * R; i += 1024) hist[i] = 0;
+    for (int i = tid; i < kGroupWaves * R; i += 1024) hist[i] = 0;
     __syncthreads();
 
     // Each wave's stretch of the tokens, whole batches of 64.
-    const int64_t per = ((a.tokens + kWaves * 64 - 1) / (kWaves * 64)) * 64;
+    const int64_t per = ((a.tokens + kGroupWaves * 64 - 1) / (kGroupWaves * 64)) * 64;
     const int64_t t_lo = w * per < a.tokens ? w * per : a.tokens;
     const int64_t t_hi = t_lo + per < a.tokens ? t_lo + per : a.tokens;
     constexpr int U = 8;  // ids in flight per lane
@@ -85,7 +55,7 @@ __global__ __launch_bounds__(1024) void k_embed_group(EmbedGradArgs a, int R)
     int32_t n = 0;
     if (tid < R)
 #pragma unroll
-        for (int k = 0; k < kWaves; ++k) {
+        for (int k = 0; k < kGroupWaves; ++k) {
             const int32_t c = hist[k * R + tid];
             hist[k * R + tid] = n;
             n += c;
@@ -103,7 +73,7 @@ __global__ __launch_bounds__(1024) void k_embed_group(EmbedGradArgs a, int R)
     const int32_t item = (int32_t)(pos >> 32), n_items = (int32_t)(both >> 32);
     if (tid < R)
 #pragma unroll
-        for (int k = 0; k < kWaves; ++k) hist[k * R + tid] += off;
+        for (int k = 0; k < kGroupWaves; ++k) hist[k * R + tid] += off;
     if (is_row) {
         a.offset[lo + tid] = off;
         if (lo + tid == a.rows - 1) a.offset[a.rows] = off + n;
@@ -169,7 +139,7 @@ hipError_t launch_embedding_group(const EmbedGradArgs& a, hipStream_t st)
 {
     const int R = (int)ids_per_group(a.rows);
     const dim3 grid((unsigned)id_groups(a.rows)), block(1024);
-    const size_t lds = (size_t)kWaves * R * sizeof(int32_t);
+    const size_t lds = (size_t)kGroupWaves * R * sizeof(int32_t);
     if (a.ids64)
         k_embed_group<true><<<grid, block, lds, st>>>(a, R);
     else

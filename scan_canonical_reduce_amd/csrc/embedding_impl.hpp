@@ -3,7 +3,7 @@
 // Lookup: 16-byte accesses, one row's vectors in neighbouring threads; bound
 // by memory traffic.
 //
-// Gradient, three kernels:
+// Gradient: one kernel for few tokens (k_embed_direct, k_embed_one), else three:
 //  1. k_embed_group: tokens by id, ascending within an id, without a sort
 //     pass over memory.  Workgroup b owns the ids [b R, b R + R) and reads all
 //     ids twice (they stay in cache): once to count its own ids, per wave, and
@@ -203,36 +203,51 @@ __device__ __forceinline__ int find_group(const int32_t* prefix, int32_t i)
     return lo;
 }
 
-// Sums an entry's occurrences [64 chunk, ...) of its row: V columns of this lane.
-template <typename T, typename G, int V, bool AL>
-__device__ __forceinline__ void sum_entry(const EmbedGradArgs& a, int4 item, int64_t lane_col,
-                                          int lane)
+// Occurrences of an entry's chunk.
+__device__ __forceinline__ int entry_tokens(int4 item)
 {
-    const int64_t v = uniform(item.x), c = uniform(item.y);
-    const int32_t off = uniform(item.z), n = uniform(item.w);
+    const int left = item.w - item.y * kEmbedChunk;
+    return left < kEmbedChunk ? left : kEmbedChunk;
+}
+
+// Sums an entry (row, chunk, the row's offset and number of tokens): the tokens
+// that the lanes hold in `mine`, V columns of this lane.
+template <typename T, typename G, int V, bool AL>
+__device__ __forceinline__ void sum_entry(const EmbedGradArgs& a, int4 item, int32_t mine,
+                                          int64_t lane_col)
+{
+    const int64_t v = item.x, c = item.y;
+    const int32_t off = item.z, n = item.w;
     const bool in = lane_col < a.width;
     const int64_t col = vec_col<V, AL>(lane_col, a.width);
     float acc[V];
     const int64_t p0 = off + c * kEmbedChunk;
-    const int m = n - c * kEmbedChunk < kEmbedChunk ? (int)(n - c * kEmbedChunk) : kEmbedChunk;
-    const int32_t mine = a.order[p0 + (lane < m ? lane : 0)];
+    const int m = entry_tokens(item);
     const typename T::store_t* x = static_cast<const typename T::store_t*>(a.dout) + (in ? col : 0);
-    PairCounter<V, 4> tree;
-    for (int b = 0; b * 8 < m; ++b) {
-        Vec<T, V> raw[8];
+    auto row = [&](int k) {
+        return ld_any<T, V, AL>(x + (int64_t)__builtin_amdgcn_readlane(mine, k) * a.ld_dout);
+    };
+    if (m == 1) {  // most rows of a large table
+        const Vec<T, V> raw = row(0);
 #pragma unroll
-        for (int r = 0; r < 8; ++r) {
-            const int k = b * 8 + r < m ? b * 8 + r : 0;
-            raw[r] = ld_any<T, V, AL>(x + (int64_t)__builtin_amdgcn_readlane(mine, k) * a.ld_dout);
+        for (int j = 0; j < V; ++j) acc[j] = T::load(raw.e[j]);
+    } else {
+        PairCounter<V, 4> tree;
+        for (int b = 0; b * 8 < m; ++b) {
+            Vec<T, V> raw[8];
+#pragma unroll
+            for (int r = 0; r < 8; ++r) raw[r] = row(b * 8 + r < m ? b * 8 + r : 0);
+            float t[8][V];
+#pragma unroll
+            for (int r = 0; r < 8; ++r) {
+                const Vec<T, V> one = whole(raw[r]);
+#pragma unroll
+                for (int j = 0; j < V; ++j) t[r][j] = b * 8 + r < m ? T::load(one.e[j]) : -0.f;
+            }
+            tree.add(t);
         }
-        float t[8][V];
-#pragma unroll
-        for (int r = 0; r < 8; ++r)
-#pragma unroll
-            for (int j = 0; j < V; ++j) t[r][j] = b * 8 + r < m ? T::load(raw[r].e[j]) : -0.f;
-        tree.add(t);
+        tree.total(acc);
     }
-    tree.total(acc);
     if (!in) return;
     if (n <= kEmbedChunk) {
         store_grad<G, V, AL>(a, v, col, acc, (int)(lane_col - col));
@@ -334,8 +349,11 @@ __global__ __launch_bounds__(256, 4) void k_embed_sum(EmbedGradArgs a, int64_t g
             const int32_t e = (int32_t)(i / slabs);
             const int64_t slab = i - e * slabs;
             const int k = find_group(prefix, e);
-            const int4 item = a.items[(int64_t)a.before[g0 + k] + (e - prefix[k])];
-            sum_entry<T, G, V, AL>(a, item, slab * 64 * V + lane * V, lane);
+            int4 item = a.items[(int64_t)a.before[g0 + k] + (e - prefix[k])];
+            item = make_int4(uniform(item.x), uniform(item.y), uniform(item.z), uniform(item.w));
+            const int32_t at = item.z + item.y * kEmbedChunk;
+            const int32_t mine = a.order[at + (lane < entry_tokens(item) ? lane : 0)];
+            sum_entry<T, G, V, AL>(a, item, mine, slab * 64 * V + lane * V);
         }
     }
     if (zero && !(blockIdx.x & 1)) zero_rows<G, VZ, AL>(a, wave, waves, lane);
@@ -442,6 +460,179 @@ __global__ __launch_bounds__(256) void k_embed_direct(EmbedGradArgs a)
     });
 }
 
+// The pairwise tree over a long row's partial values [lo, hi) of m, eight in
+// flight, four columns a lane.
+template <int LEVELS>
+__device__ __forceinline__ void tree_partials(const EmbedGradArgs& a, int32_t off, int32_t m,
+                                              int32_t lo, int32_t hi, int64_t col,
+                                              float (&acc)[4])
+{
+    const float* part = a.part + off / kEmbedChunk * a.ld_part + col;
+    const float* last =
+        a.part_last + (off + (m - 1) * kEmbedChunk) / kEmbedChunk * a.ld_part + col;
+    PairCounter<4, LEVELS> tree;
+    for (int32_t b = lo; b < hi; b += 8) {
+        float x[8][4];
+#pragma unroll
+        for (int r = 0; r < 8; ++r) {
+            const int32_t j = b + r;
+            float4 p = make_float4(-0.f, -0.f, -0.f, -0.f);
+            if (j < hi)
+                p = *reinterpret_cast<const float4*>(j == m - 1 ? last : part + j * a.ld_part);
+            x[r][0] = p.x, x[r][1] = p.y, x[r][2] = p.z, x[r][3] = p.w;
+        }
+        tree.add(x);
+    }
+    tree.total(acc);
+}
+
+// Up to 4096 tokens, one launch: a workgroup groups the tokens of its ids in LDS
+// (as k_embed_group; its ids are those equal to its number modulo a power of two,
+// so that neighbouring frequent ones fall to different workgroups) and sums their
+// rows in its part of the columns.  Measured against three launches, us a call,
+// frequencies falling as 1/rank (all tokens one id): 300 tokens x 1000 of 10007
+// rows bf16 11.5 and 18.4 (17 and 24), 1000 x 512 of 1000 rows 15 and 23 (24 and
+// 24), 3001 x 1000 of 10007 rows float16 19 and 25 (64 and 27: one workgroup for
+// each 512 columns), 4096 x 4096 of 32000 rows 117 and 118 (171 and 114).  Not
+// taken for fewer than 256 rows or so, where few workgroups would have all tokens.
+constexpr int kEmbedOne = 4096;
+constexpr int kOneIds = 512;
+
+struct OneShape {
+    int log_groups, ids, parts;  // ids: of a workgroup; parts: of the columns
+    int64_t blocks() const { return (int64_t)parts << log_groups; }
+};
+
+template <typename T, typename G, int V, bool AL>
+__global__ __launch_bounds__(64 * kGroupWaves) void k_embed_one(EmbedGradArgs a, OneShape shape)
+{
+    extern __shared__ int32_t hist[];  // [wave][id]: count, then the next position
+    __shared__ Pairs scan[kGroupWaves];
+    __shared__ int32_t order[kEmbedOne], first_item[kOneIds + 1], first_token[kOneIds + 1];
+    __shared__ int32_t longs[kEmbedOne / (kEmbedChunk + 1) + 1];
+    const int tid = threadIdx.x, lane = tid & 63, w = uniform((int32_t)(tid >> 6));
+    const int R = shape.ids;
+    const uint32_t mask = (1u << shape.log_groups) - 1, own = blockIdx.x & mask;
+    for (int i = tid; i < kGroupWaves * R; i += 64 * kGroupWaves) hist[i] = 0;
+    __syncthreads();
+
+    // Each wave's stretch of the tokens, whole batches of 64: ids in registers.
+    constexpr int U = kEmbedOne / (64 * kGroupWaves);
+    const int32_t batches = ((int32_t)a.tokens + 64 * kGroupWaves - 1) / (64 * kGroupWaves);
+    const int32_t t0 = w * batches * 64 + lane;
+    int32_t key[U];  // number of the id within the workgroup's, -1: none of them
+    uint32_t below = 0;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        const int32_t t = t0 + u * 64;
+        const int64_t id =
+            u < batches && t < a.tokens ? token_id(a.ids, a.ids64, t) : -1;
+        const bool real = id >= 0 && id < a.rows && id != a.padding_id;
+        const uint32_t group = (uint32_t)id & mask;
+        below += real && group < own;
+        key[u] = real && group == own ? (int32_t)(id >> shape.log_groups) : -1;
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+        if (key[u] >= 0) atomicAdd(&hist[w * R + key[u]], 1);
+    __syncthreads();
+
+    // thread r: the counts of its id over the waves, in wave order
+    int32_t n = 0;
+    if (tid < R)
+#pragma unroll
+        for (int k = 0; k < kGroupWaves; ++k) {
+            const int32_t c = hist[k * R + tid];
+            hist[k * R + tid] = n;
+            n += c;
+        }
+    const bool is_long = n > kEmbedChunk;
+    uint64_t x = (uint64_t)(uint32_t)n |
+                 (uint64_t)(uint32_t)((n + kEmbedChunk - 1) / kEmbedChunk) << 32;
+    uint64_t y = (uint64_t)is_long | (uint64_t)below << 32;
+    const Pairs at = block_exclusive(x, y, scan);
+    const int32_t off = (int32_t)(uint32_t)at.x, n_items = (int32_t)(x >> 32);
+    const int32_t n_long = (int32_t)(uint32_t)y, before = (int32_t)(y >> 32);
+    if (tid < R) {
+#pragma unroll
+        for (int k = 0; k < kGroupWaves; ++k) hist[k * R + tid] += off;
+        first_item[tid] = (int32_t)(at.x >> 32);
+        first_token[tid] = off;
+    }
+    if (is_long) longs[(uint32_t)at.y] = tid;
+    if (tid == 0) {
+        first_item[R] = n_items;
+        first_token[R] = (int32_t)(uint32_t)x;
+    }
+    __syncthreads();
+    // Placing: a wave's lanes with the same id take consecutive positions.
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        uint64_t left = __ballot(key[u] >= 0);
+        while (left) {
+            const int lead = __builtin_amdgcn_readlane(key[u], __builtin_ctzll(left));
+            const uint64_t same = __ballot(key[u] == lead);
+            if (key[u] == lead)
+                order[hist[w * R + lead] + __popcll(same & ((1ull << lane) - 1))] = t0 + u * 64;
+            wave_lds_fence();
+            if (lane == 0) hist[w * R + lead] += __popcll(same);
+            wave_lds_fence();
+            left &= ~same;
+        }
+    }
+    __syncthreads();
+
+    const int32_t part = (int32_t)(blockIdx.x >> shape.log_groups);
+    const int32_t steps = (int32_t)((a.width + 64 * V - 1) / (64 * V));
+    const int32_t per = (steps + shape.parts - 1) / shape.parts;
+    const int64_t c0 = (int64_t)part * per * (64 * V);
+    const int64_t c1 = c0 + per * (64 * V) < a.width ? c0 + per * (64 * V) : a.width;
+    const int32_t slabs = c1 > c0 ? (int32_t)((c1 - c0 + 64 * V - 1) / (64 * V)) : 0;
+    for (int32_t i = w; i < n_items * slabs; i += kGroupWaves) {
+        const int32_t e = i / slabs;
+        int r0 = 0, r1 = R - 1;  // the last id with first_item <= e
+        while (r0 < r1) {
+            const int mid = (r0 + r1 + 1) >> 1;
+            if (first_item[mid] <= e)
+                r0 = mid;
+            else
+                r1 = mid - 1;
+        }
+        const int32_t begin = uniform(first_token[r0]), chunk = e - uniform(first_item[r0]);
+        const int4 item =
+            make_int4((int32_t)(own + ((uint32_t)r0 << shape.log_groups)), chunk, before + begin,
+                      uniform(first_token[r0 + 1]) - begin);
+        const int32_t mine =
+            order[begin + chunk * kEmbedChunk + (lane < entry_tokens(item) ? lane : 0)];
+        sum_entry<T, G, V, AL>(a, item, mine, c0 + (i - e * slabs) * (64 * V) + lane * V);
+    }
+    if (!a.accumulate) {
+        constexpr int VZ = V == 1 ? 1 : 16 / (int)sizeof(typename G::store_t);
+        for (int r = w; r < R; r += kGroupWaves) {
+            const int64_t v = own + ((int64_t)r << shape.log_groups);
+            if (v < a.rows && uniform(first_token[r]) == uniform(first_token[r + 1]))
+                zero_listed<G, VZ, AL>(a, v, 1, c0, c1, lane);
+        }
+    }
+    if (n_long == 0) return;
+    __syncthreads();
+    const int32_t cols = c1 > c0 ? (int32_t)((c1 - c0 + 255) / 256) : 0;
+    for (int32_t i = w; i < n_long * cols; i += kGroupWaves) {
+        const int32_t e = i / cols, r = uniform(longs[e]);
+        const int64_t col = c0 + (int64_t)(i - e * cols) * 256 + lane * 4;
+        const int32_t begin = uniform(first_token[r]), count = uniform(first_token[r + 1]) - begin;
+        const int32_t m = (count + kEmbedChunk - 1) / kEmbedChunk;
+        float acc[4];
+        tree_partials<4>(a, before + begin, m, 0, m, col < c1 ? col : c0, acc);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const float one[1] = {acc[j]};
+            if (col + j < c1)
+                store_grad<G, 1, true>(a, own + ((int64_t)r << shape.log_groups), col + j, one, 0);
+        }
+    }
+}
+
 // Rows with more than 64 occurrences: the pairwise tree over the partial
 // values, an aligned power-of-two range of them per wave, then over the
 // waves.  A lane holds four neighbouring columns (the partial values' rows are
@@ -468,24 +659,8 @@ __global__ __launch_bounds__(64 * kFinishWaves) void k_embed_finish(EmbedGradArg
             int32_t range = 1;  // partial values per wave
             while (range * kFinishWaves < m) range *= 2;
             const int32_t lo = w * range, hi = lo + range < m ? lo + range : m;
-            const float* part = a.part + off / kEmbedChunk * a.ld_part + (in ? col : 0);
-            const float* last =
-                a.part_last + (off + (m - 1) * kEmbedChunk) / kEmbedChunk * a.ld_part + (in ? col : 0);
-            PairCounter<4, 19> tree;  // up to 2^30 / 64 / 8 / 8 batches
-            for (int32_t b = lo; b < hi; b += 8) {
-                float x[8][4];
-#pragma unroll
-                for (int r = 0; r < 8; ++r) {
-                    const int32_t j = b + r;
-                    float4 p = make_float4(-0.f, -0.f, -0.f, -0.f);
-                    if (j < hi)
-                        p = *reinterpret_cast<const float4*>(j == m - 1 ? last : part + j * a.ld_part);
-                    x[r][0] = p.x, x[r][1] = p.y, x[r][2] = p.z, x[r][3] = p.w;
-                }
-                tree.add(x);
-            }
             float acc[4];
-            tree.total(acc);
+            tree_partials<19>(a, off, m, lo, hi, in ? col : 0, acc);  // 2^30 / 64 / 8 / 8 batches
             waves[w][lane] = make_float4(acc[0], acc[1], acc[2], acc[3]);
             __syncthreads();
             // wave w finishes its 256 / kFinishWaves columns, one a lane
@@ -532,6 +707,18 @@ hipError_t launch_embedding(const EmbedArgs& a, hipStream_t st)
     });
 }
 
+inline OneShape one_shape(int64_t rows, int64_t slabs)
+{
+    OneShape s;
+    s.parts = slabs < 16 ? (int)slabs : 16;
+    s.log_groups = 0;  // up to 256 workgroups, of 16 ids or more and at most 512
+    while (((int64_t)2 * s.parts << s.log_groups) <= 256 && (rows >> s.log_groups) > 16)
+        ++s.log_groups;
+    while (s.log_groups < 24 && ((rows - 1) >> s.log_groups) + 1 > kOneIds) ++s.log_groups;
+    s.ids = (int)(((rows - 1) >> s.log_groups) + 1);
+    return s;
+}
+
 template <typename T, typename G>
 hipError_t launch_embedding_grad(const EmbedGradArgs& a, hipStream_t st)
 {
@@ -548,6 +735,15 @@ hipError_t launch_embedding_grad(const EmbedGradArgs& a, hipStream_t st)
                 (unsigned)capped_grid(waves < 4 ? 1 : waves / 4 < cap ? waves / 4 : cap));
             k_embed_direct<T, G, V == 1 ? 1 : V / 2, AL><<<direct, dim3(256), 0, st>>>(a);
             return hipGetLastError();
+        }
+        if (a.tokens <= kEmbedOne) {
+            const OneShape one = one_shape(a.rows, slabs);
+            if (one.blocks() <= 512 && one.log_groups >= 4) {
+                k_embed_one<T, G, V, AL>
+                    <<<dim3((unsigned)one.blocks()), dim3(64 * kGroupWaves),
+                       (size_t)kGroupWaves * one.ids * sizeof(int32_t), st>>>(a, one);
+                return hipGetLastError();
+            }
         }
         const int64_t groups = id_groups(a.rows);
         if (hipError_t e = launch_embedding_group(a, st)) return e;

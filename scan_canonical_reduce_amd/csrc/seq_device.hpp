@@ -65,10 +65,27 @@ struct alignas((V * sizeof(typename T::store_t) < 16) ? V * sizeof(typename T::s
     typename T::store_t e[V];
 };
 
+template <int BYTES>
+struct Words {
+    typedef uint32_t type __attribute__((ext_vector_type(BYTES / 4)));
+};
+template <>
+struct Words<4> {
+    typedef uint32_t type;
+};
+template <>
+struct Words<2> {
+    typedef uint16_t type;
+};
+template <>
+struct Words<32> {  // two accesses, aligned to 16
+    typedef uint32_t type __attribute__((ext_vector_type(8), aligned(16)));
+};
 template <typename T, int V>
 __device__ __forceinline__ Vec<T, V> ld_vec(const typename T::store_t* p)
 {
-    return *reinterpret_cast<const Vec<T, V>*>(p);
+    using W = typename Words<sizeof(Vec<T, V>)>::type;
+    return __builtin_bit_cast(Vec<T, V>, *reinterpret_cast<const W*>(p));
 }
 
 template <typename T, int V>
@@ -84,10 +101,22 @@ __device__ __forceinline__ void st_vec(typename T::store_t* p, const float (&v)[
 template <typename T, int V, bool AL>
 __device__ __forceinline__ Vec<T, V> ld_any(const typename T::store_t* p)
 {
-    if constexpr (AL) return ld_vec<T, V>(p);
-    Vec<T, V> v;
-    __builtin_memcpy(&v, p, sizeof(v));
-    return v;
+    if constexpr (AL) {
+        return ld_vec<T, V>(p);
+    } else {
+        typename Words<sizeof(Vec<T, V>)>::type w;
+        __builtin_memcpy(&w, p, sizeof(w));
+        return __builtin_bit_cast(Vec<T, V>, w);
+    }
+}
+// A loaded vector as one value, where its elements are used: else the compiler may
+// split the load by how they are.
+template <typename T, int V>
+__device__ __forceinline__ Vec<T, V> whole(const Vec<T, V>& v)
+{
+    auto w = __builtin_bit_cast(typename Words<sizeof(Vec<T, V>)>::type, v);
+    asm("" : "+v"(w));
+    return __builtin_bit_cast(Vec<T, V>, w);
 }
 template <typename T, int V, bool AL>
 __device__ __forceinline__ void st_any(typename T::store_t* p, const float (&v)[V])

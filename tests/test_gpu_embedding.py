@@ -213,3 +213,24 @@ def test_rows_of_any_width_and_place(canon, dtype, grad, width):
                              accumulate=True)
         assert same_bits(dw[:, off:off + width], grad_ref(dout, ids, 40, 1.5, None, old, grad))
         assert (dw[:, :off] == 7).all() and (dw[:, off + width:] == 7).all()
+
+
+@pytest.mark.parametrize("tokens", [257, 1000, 4096])
+@pytest.mark.parametrize("rows,width,off", [(256, 2056, 0), (300, 1001, 1), (3000, 130, 0),
+                                            (3000, 3, 0), (140001, 8, 0), (5000, 520, 0)])
+def test_grad_of_some_thousand_tokens(canon, tokens, rows, width, off):
+    g = torch.Generator().manual_seed(tokens + width)
+    dout = torch.randn(tokens, width + 8, generator=g).to(BF16)[:, off:off + width]
+    ws = torch.full((canon.embedding_grad_workspace_bytes(tokens, rows, width),), 255,
+                    dtype=torch.uint8, device="cuda")  # NaN wherever it is not written
+    for kind, grad in (("zipf", F32), ("one", BF16), ("stray", BF16), ("few", F32)):
+        ids = make_ids(tokens, rows, kind, tokens)
+        dw = torch.full((rows, width + 8), 7.0, dtype=grad, device="cuda")
+        got = dw[:, off:off + width]
+        canon.embedding_grad(dout.cuda(), ids.cuda(), rows, 0.75, padding_id=2, out=got, ws=ws)
+        want = grad_ref(dout, ids, rows, 0.75, 2, dtype=grad)
+        assert same_bits(got, want), kind
+        canon.embedding_grad(dout.cuda(), ids.int().cuda(), rows, 0.75, padding_id=2, out=got,
+                             accumulate=True, ws=ws)
+        assert same_bits(got, grad_ref(dout, ids, rows, 0.75, 2, want, grad)), kind
+        assert (dw[:, :off] == 7).all() and (dw[:, off + width:] == 7).all()
