@@ -496,8 +496,9 @@ __device__ __forceinline__ void tree_partials(const EmbedGradArgs& a, int32_t of
 // frequencies falling as 1/rank (all tokens one id): 300 tokens x 1000 of 10007
 // rows bf16 11.5 and 18.4 (17 and 24), 1000 x 512 of 1000 rows 15 and 23 (24 and
 // 24), 3001 x 1000 of 10007 rows float16 19 and 25 (64 and 27: one workgroup for
-// each 512 columns), 4096 x 4096 of 32000 rows 117 and 118 (171 and 114).  Not
-// taken for fewer than 256 rows or so, where few workgroups would have all tokens.
+// each 512 columns), 4096 x 4096 of 32000 rows 117 and 118 (171 and 114), 395 x
+// 1292 of 118 rows 12 and 20 (17 and 27).  Not taken above 1024 tokens for fewer
+// than 256 rows or so, where few workgroups would have all tokens.
 constexpr int kEmbedOne = 4096;
 constexpr int kOneIds = 512;
 
@@ -741,7 +742,7 @@ hipError_t launch_embedding_grad(const EmbedGradArgs& a, hipStream_t st)
         }
         if (a.tokens <= kEmbedOne) {
             const OneShape one = one_shape(a.rows, slabs);
-            if (one.blocks() <= 512 && one.log_groups >= 4) {
+            if (one.blocks() <= 512 && (one.log_groups >= 4 || a.tokens <= 1024)) {
                 k_embed_one<T, G, V, AL>
                     <<<dim3((unsigned)one.blocks()), dim3(64 * kGroupWaves),
                        (size_t)kGroupWaves * one.ids * sizeof(int32_t), st>>>(a, one);
