@@ -15,7 +15,7 @@ struct ConvArgs {
     const void *weight, *bias, *init;
     void* final;
     int32_t channels;
-    bool param_f32, silu, vec;  // vec: 16-byte accesses are aligned
+    bool param_f32, silu, vec;  // vec: accesses of four channels are aligned
     // backward
     canon_rows_t dout, dx;
     float *dweight, *dbias;

@@ -362,14 +362,14 @@ __global__ __launch_bounds__(256, 4) void k_embed_sum(EmbedGradArgs a, int64_t g
     if (zero && !(blockIdx.x & 1)) zero_rows<G, VZ, AL>(a, wave, waves, lane);
 }
 
-// Up to 256 tokens, one launch and no workspace: a wave keeps all ids, four a
+// Up to 128 tokens, one launch and no workspace: a wave keeps all ids, two a
 // lane.  For each (token, slab of columns) it takes, the ballots of "same id" tell
 // whether the token is its id's first, and are the list of occurrences, in order;
-// rows of the table without a token are found the same way.  One
-// launch instead of three: for 257 and 256 tokens of 4096 columns over 3000 rows
-// 22 and 12 us a call.  But an id's occurrences are added by one wave, 16 rows in
-// flight: where all tokens are one, 29 and 52 us.
-constexpr int kEmbedDirect = 256;
+// rows of the table without a token are found the same way.  Measured against
+// grouping in LDS (k_embed_one), us a call, frequencies falling as 1/rank (all tokens
+// one id, whose rows one wave adds, 16 in flight): 64 x 1000 of 10007 rows bf16 9.1
+// and 10.3 (12.5 and 15.5), 128 9.0 and 10.5 (18 and 17), 256 9.1 and 10.8 (40 and 17).
+constexpr int kEmbedDirect = 128;
 
 template <typename T, typename G, int V, bool AL>
 __global__ __launch_bounds__(256) void k_embed_direct(EmbedGradArgs a)
@@ -406,7 +406,7 @@ __global__ __launch_bounds__(256) void k_embed_direct(EmbedGradArgs a)
         const int64_t col = vec_col<V, AL>(lane_col, a.width);
         const typename T::store_t* x =
             static_cast<const typename T::store_t*>(a.dout) + (in ? col : 0);
-        PairCounter<V, 6> tree;
+        PairCounter<V, 5> tree;
         int k = 0;
         uint64_t cur = same[0];
         bool more = true;
