@@ -18,6 +18,7 @@
 #include "causal_conv.hpp"
 #include "column_sum.hpp"
 #include "launch.hpp"
+#include "row_walk.hpp"
 
 namespace canon {
 namespace seq {
@@ -323,17 +324,10 @@ __global__ __launch_bounds__(256, K <= 4 ? 5 : 2) void k_causal_conv_grad(ConvAr
         constexpr int ALL = RUN + K - 1;
         constexpr int READ = (ALL + U - 1) / U * U;  // rows that whole fetches read
         if (__all(ck.len == RUN && ck.row > 0 && ck.row + READ <= len)) {
-#pragma unroll 1
-            for (int32_t r0 = 0; r0 < ALL; r0 += 2 * U) {
-                if (r0 + U < ALL) fetch(1, r0 + U, true);
-#pragma unroll
-                for (int u = 0; u < U; ++u) one_row(0, u, r0 + u, true);
-                if (r0 + 2 * U < ALL) fetch(0, r0 + 2 * U, true);
-                if (r0 + U < ALL)
-#pragma unroll
-                    for (int u = 0; u < U; ++u)
-                        if (r0 + U + u < ALL) one_row(1, u, r0 + U + u, true);
-            }
+            // exactly ALL rows: the run's last row is r = ALL - 1's, and the rows of dx
+            // behind it are the next run's to store
+            walk_rows<ALL, U>([&](int b, int32_t r0) { fetch(b, r0, true); },
+                              [&](int b, int u, int32_t r) { one_row(b, u, r, true); });
         } else {
 #pragma unroll 1
             for (int32_t r0 = 0; r0 < stop - ck.row; r0 += U) {
