@@ -323,3 +323,66 @@ def test_channels_of_any_number_and_place(canon, dtype, channels):
             canon.causal_conv_step(d["x"][:, t, cut], state, w, b, "silu", out=out[:, :channels])
             assert torch.equal(out[:, :channels], a[:, cut]) and (out[:, channels:] == 7).all()
             assert torch.equal(state, own(all_state))
+
+
+def inner_waves(rows, channels, taps, per):
+    """Waves of the backward pass over one sequence of `rows` rows, `per` channels a
+    lane, that run the loop without checks: every lane's run of 32 rows is full, is
+    not the first, and has all the rows that whole fetches of 4 read."""
+    read = (32 + taps - 1 + 3) // 4 * 4
+    lanes = [32 * (i // -(-channels // per)) for i in range(-(-rows // 32) * -(-channels // per))]
+    inner = [r > 0 and r + 32 <= rows and r + read <= rows for r in lanes]
+    return sum(all(inner[i:i + 64]) for i in range(0, len(inner), 64))
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16, F16])
+@pytest.mark.parametrize("taps", [1, 2, 3, 4, 5, 8])
+@pytest.mark.parametrize("channels", [128, 133])
+def test_backward_without_checks(canon, dtype, taps, channels):
+    """Sequences whose ends lie on both sides of the rows that the loop without
+    checks needs, against the float64 form; NaN behind each sequence."""
+    per = 1 if channels == 133 and dtype == F32 else 2
+    need = 32 + (32 + taps - 1 + 3) // 4 * 4
+    if channels == 128:
+        assert not inner_waves(need - 1, channels, taps, per)
+        assert inner_waves(need, channels, taps, per)
+    assert inner_waves(230, channels, taps, per)
+    for rows in (need - 1, need, need + 1, 230):
+        d = inputs(dtype, [rows], channels, taps, False, seed=rows + taps)
+        d["init"].zero_()
+        d["dfinal"].zero_()
+        g = cuda(d)
+        x, dout = (torch.full((1, rows + 8, channels), float("nan"), dtype=dtype, device="cuda")
+                   for _ in range(2))
+        x[:, :rows], dout[:, :rows] = g["x"], g["dout"]
+        dx = torch.full_like(x, 7.0)
+        got = canon.causal_conv_grad(dout[:, :rows], x[:, :rows], g["w"], g["b"], "silu",
+                                     dx=dx[:, :rows])
+        assert (dx[:, rows:] == 7).all()
+        _, (want, dw, _, db) = reference(d, "silu", grad=True)
+        # With h = 2^-24 and pm the largest absolute sum of p: p is off by (taps + 2)
+        # h pm, and silu' has a slope below 1/2.  silu' = q + p (q - q q), q off by
+        # (1 - q) (2 |p| + 2) h + 3 h of itself, is off by 5 |p| h + 8 h more
+        # (p^2 q (1 - q) < 1/2); the product with dout by 2 h.  Then a sum of `taps`
+        # (dx) or `rows` terms of at most 1.1 gm, in FMAs.
+        h = 2.0**-24
+        xm, gm, wm, bm = (float(d[k].double().abs().max()) for k in ("x", "dout", "w", "b"))
+        pm = bm + taps * wm * xm
+        dp = gm * h * ((0.5 * (taps + 2) + 5) * pm + 10)
+        tol = taps * wm * (dp + (taps + 1) * h * 1.1 * gm)
+        err = (got.dx.double().cpu() - want).abs()
+        assert (err <= tol + seq_ref.half_step(dtype) * (want.abs() + tol)).all(), rows
+        tol = rows * (dp + (rows + 2) * h * 1.1 * gm)
+        assert (got.dweight.double().cpu() - dw).abs().max() <= tol * xm, rows
+        assert (got.dbias.double().cpu() - db).abs().max() <= tol, rows
+    # packed, sequences of other lengths around, none starting with a run's start
+    lens = [9, 0, 150, 31, need]
+    d = inputs(dtype, lens, channels, taps, True, seed=taps)
+    g = cuda(d)
+    got = canon.causal_conv_grad(g["dout"], g["x"], g["w"], g["b"], "silu", g["starts"], g["init"],
+                                 g["dfinal"])
+    for s, (a, b) in enumerate(zip(d["starts"][:-1].tolist(), d["starts"][1:].tolist())):
+        one = canon.causal_conv_grad(g["dout"][None, a:b], g["x"][None, a:b], g["w"], g["b"],
+                                     "silu", None, g["init"][s:s + 1], g["dfinal"][s:s + 1])
+        assert torch.equal(got.dx[a:b], one.dx[0])
+        assert torch.equal(got.dinit_state[s], one.dinit_state[0])
