@@ -52,3 +52,20 @@ def scan_rows_tile(dtype, policy="pairwise", param=0) -> int:
     t = c.scan_rows_tile_elems(policy, param, np.dtype(dtype).itemsize)
     assert t > 0
     return t
+
+
+def launches(call) -> int:
+    """Kernels that call() launches: the nodes of a captured graph."""
+    import ctypes
+    import scan_canonical_reduce_amd as c
+    call()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph(keep_graph=True)
+    with torch.cuda.graph(graph):
+        kept = call()
+    n = ctypes.c_size_t(0)
+    f = c.lib().hipGraphGetNodes
+    f.argtypes = [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p]
+    assert f(graph.raw_cuda_graph(), None, ctypes.byref(n)) == 0
+    del kept
+    return n.value

@@ -61,3 +61,54 @@ def close(got, want, size, terms, what=""):
         f"{what}: {int(bad.sum())} of {bad.numel()} beyond the bound; worst "
         f"{float(((got64 - want).abs() / tol)[bad].max())} times it at "
         f"{torch.nonzero(bad)[0].tolist()}")
+
+
+def scan_grads(d, absolute=False):
+    """selective_scan of everything (D, gate, softplus, states) and all gradients by
+    the formulas, in float64, for sequences of one length side by side, on the
+    tensors' device: d holds u, delta, z, dout [sequences, rows, channels], B, C
+    [.., groups, states], A, D, bias, init, dfinal.  absolute: the sums of the
+    absolute values of the terms instead."""
+    e = {k: v.double() for k, v in d.items() if torch.is_tensor(v) and v.is_floating_point()}
+    if absolute:
+        for k in ("u", "B", "C", "D", "init", "dout", "dfinal"):
+            e[k] = e[k].abs()
+    raw = e["delta"] + e["bias"]
+    dl = torch.nn.functional.softplus(raw, threshold=1e9)
+    slope = torch.sigmoid(raw)
+    A, size_A, z, q = e["A"], e["A"].abs() if absolute else e["A"], e["z"], torch.sigmoid(e["z"])
+    gate, dgate = (z.abs(), 1.1 + z.abs()) if absolute else (z * q, q + z * q * (1 - q))
+    groups = e["B"].shape[2]
+    per = e["u"].shape[2] // groups
+
+    def spread(x):
+        return x.repeat_interleave(per, 1)
+
+    rows, u = e["u"].shape[1], e["u"]
+    h = [e["init"]]
+    for t in range(rows):
+        a = torch.exp(dl[:, t, :, None] * A)
+        h.append(a * h[-1] + (dl[:, t] * u[:, t])[..., None] * spread(e["B"][:, t]))
+    g = {k: torch.zeros_like(e[k]) for k in ("u", "delta", "A", "B", "C", "D", "z", "bias")}
+    out = torch.zeros_like(u)
+    R = e["dfinal"]
+    for t in range(rows - 1, -1, -1):
+        B, C = spread(e["B"][:, t]), spread(e["C"][:, t])
+        y = (h[t + 1] * C).sum(-1) + e["D"] * u[:, t]
+        out[:, t] = y * gate[:, t]
+        dy = e["dout"][:, t] * gate[:, t]
+        lam = C * dy[..., None] + R
+        R = torch.exp(dl[:, t, :, None] * A) * lam
+        decay, through = R * h[t], (lam * B).sum(-1)
+        dd = ((decay * size_A).sum(-1) + through * u[:, t]) * slope[:, t]
+        g["u"][:, t] = through * dl[:, t] + e["D"] * dy
+        g["delta"][:, t] = dd
+        g["z"][:, t] = e["dout"][:, t] * y * dgate[:, t]
+        by_group = (y.shape[0], groups, per, -1)
+        g["B"][:, t] = (lam * (dl[:, t] * u[:, t])[..., None]).view(by_group).sum(2)
+        g["C"][:, t] = (h[t + 1] * dy[..., None]).view(by_group).sum(2)
+        g["A"] += (decay * dl[:, t][..., None]).sum(0)
+        g["D"] += (dy * u[:, t]).sum(0)
+        g["bias"] += dd.sum(0)
+    g["init"] = R
+    return out, h[-1], g

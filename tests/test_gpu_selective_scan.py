@@ -6,6 +6,7 @@ pytestmark = pytest.mark.gpu
 torch = pytest.importorskip("torch")
 
 import seq_ref  # noqa: E402
+from gpu_util import launches  # noqa: E402
 
 F32, BF16, F16 = torch.float32, torch.bfloat16, torch.float16
 
@@ -541,3 +542,71 @@ def test_states_that_keep_nothing(canon, lens, packed):
         canon.selective_scan_step(g["init"], one["u"], one["delta"], g["A"], one["B"], one["C"],
                                   g["D"], one["z"], g["bias"], True, out_state=step)
         assert torch.isfinite(step).all()
+
+
+def gradients(canon, d, keep, **kw):
+    return canon.selective_scan_grad(
+        d["dout"], d["u"], d["delta"], d["A"], d["B"], d["C"], keep, D=d["D"], z=d["z"],
+        delta_bias=d["bias"], delta_softplus=True, starts=d["starts"], d_final_state=d["dfinal"],
+        **kw)
+
+
+FIELDS = dict(u="du", delta="ddelta", A="dA", B="dB", C="dC", D="dD", z="dz", bias="ddelta_bias",
+              init="dinit_state")
+PARAMS = ("A", "D", "bias")
+
+
+def check_gradients(got, want, size, rows, chunks, what, names=tuple(FIELDS), at=slice(None)):
+    """rows: of a sequence; chunks: of all.  A parameter's gradient adds at most 64
+    rows of a chunk, then a 16th of the chunks, then 16 lanes; dB and dC add a
+    group's channels, 16 lanes by folding, then waves and slabs (below 64)."""
+    for k in names:
+        extra = 64 + chunks / 16 + 8 if k in PARAMS else 64
+        g = getattr(got, FIELDS[k])
+        seq_ref.close(g if k in PARAMS else g[at], want[k].cpu(), size[k].cpu(),
+                      2 * terms(rows) + extra, (what, k))
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16, F16])
+@pytest.mark.parametrize("n,rows,channels,groups,states", [
+    (400, 200, 24, 1, 16), (400, 257, 24, 1, 5), (256, 193, 24, 2, 3), (170, 129, 130, 1, 16)])
+def test_whole_sequences_of_many_chunks(canon, dtype, n, rows, channels, groups, states):
+    """Enough sequences of three chunks or more that a wave walks each whole, both
+    ways: the forward bits of each alone (in chunks), the gradients against the
+    float64 formulas; with the incoming gradient of one sequence alone the
+    parameters' gradients are that sequence's, every chunk of it."""
+    chunks = -(-rows // 64)
+    d = cuda(inputs(dtype, [rows] * n, channels, groups, states, False, rows + n))
+    # sums of one sign, so that no part of them is lost in the bound
+    for k in ("u", "B", "C", "D", "z", "dout", "init", "dfinal"):
+        d[k] = d[k].abs()
+    final, keep = torch.empty_like(d["init"]), canon.selective_scan_states(d["u"], states)
+    assert launches(lambda: call(canon, d)) == 1
+    out = call(canon, d, final_state=final, states=keep)
+    per = ("u", "delta", "z", "B", "C", "init", "dout", "dfinal")
+    for i in (0, n // 2 + 1, n - 1):
+        one = {k: v[i:i + 1].contiguous() if k in per else v for k, v in d.items()}
+        f, k1 = torch.empty_like(one["init"]), canon.selective_scan_states(one["u"], states)
+        assert launches(lambda: call(canon, one)) == 3
+        assert torch.equal(call(canon, one, final_state=f, states=k1), out[i:i + 1])
+        assert torch.equal(f, final[i:i + 1])
+        saved = -(-rows // 16)  # every 16 rows, of 4 places a chunk
+        assert torch.equal(k1.view(4 * chunks, -1)[:saved],
+                           keep.view(n, 4 * chunks, -1)[i, :saved])
+    assert launches(lambda: gradients(canon, d, keep)) == 2
+    got = gradients(canon, d, keep)
+    o, h, want = seq_ref.scan_grads(d)
+    so, sh, size = seq_ref.scan_grads(d, absolute=True)
+    seq_ref.close(out, o.cpu(), so.cpu(), terms(rows), "out")
+    seq_ref.close(final, h.cpu(), sh.cpu(), terms(rows), "final")
+    check_gradients(got, want, size, rows, n * chunks, "all")
+    for i in (0, n // 2 + 1, n - 1):
+        e = dict(d, dout=torch.zeros_like(d["dout"]), dfinal=torch.zeros_like(d["dfinal"]))
+        e["dout"][i], e["dfinal"][i] = d["dout"][i], d["dfinal"][i]
+        got = gradients(canon, e, keep)
+        one = {k: v[i:i + 1] if k in per else v for k, v in d.items()}
+        _, _, want = seq_ref.scan_grads(one)
+        _, _, size = seq_ref.scan_grads(one, absolute=True)
+        check_gradients(got, want, size, rows, chunks, i, at=slice(i, i + 1))
+        others = torch.arange(n, device="cuda") != i
+        assert not got.du[others].any() and not got.dinit_state[others].any()
