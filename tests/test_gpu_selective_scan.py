@@ -610,3 +610,45 @@ def test_whole_sequences_of_many_chunks(canon, dtype, n, rows, channels, groups,
         check_gradients(got, want, size, rows, chunks, i, at=slice(i, i + 1))
         others = torch.arange(n, device="cuda") != i
         assert not got.du[others].any() and not got.dinit_state[others].any()
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("rows,channels,groups,states", [
+    (1024, 40, 1, 16), (1025, 17, 1, 3), (2117, 20, 2, 7), (3100, 8, 1, 16)])
+def test_carries_of_many_chunks(canon, dtype, rows, channels, groups, states):
+    """16 chunks and more of one sequence, whose carries pass between the chunks
+    in batches of 16, both ways: forward the bits of pieces of one chunk, backward
+    the float64 formulas."""
+    d = cuda(inputs(dtype, [rows], channels, groups, states, False, rows))
+    d["bias"] -= 2.0  # smaller steps, so that states live through many chunks
+    for k in ("u", "B", "C", "D", "z", "dout", "init", "dfinal"):
+        d[k] = d[k].abs()
+    final, keep = torch.empty_like(d["init"]), canon.selective_scan_states(d["u"], states)
+    assert launches(lambda: call(canon, d)) == 3
+    out = call(canon, d, final_state=final, states=keep)
+    state = d["init"].clone()
+    for at in range(0, rows, 64):
+        piece = {k: v[:, at:at + 64] if k in ("u", "delta", "z", "B", "C") else v
+                 for k, v in d.items()}
+        piece["init"] = state
+        assert torch.equal(call(canon, piece, final_state=state), out[:, at:at + 64]), at
+    assert torch.equal(state, final)
+    assert launches(lambda: gradients(canon, d, keep)) == 4
+    got = gradients(canon, d, keep)
+    _, _, want = seq_ref.scan_grads(d)
+    _, _, size = seq_ref.scan_grads(d, absolute=True)
+    check_gradients(got, want, size, rows, -(-rows // 64), "alone")
+    # packed behind and before others: the same bits, those of parameters aside
+    lens = [70, rows, 0, 1100]
+    p = cuda(inputs(dtype, lens, channels, groups, states, True, 3))
+    p.update({k: d[k] for k in ("A", "D", "bias")})
+    for k in ("u", "delta", "z", "B", "C", "dout"):
+        p[k][70:70 + rows] = d[k][0]
+    p["init"][1], p["dfinal"][1] = d["init"][0], d["dfinal"][0]
+    f2, keep = torch.empty_like(p["init"]), canon.selective_scan_states(p["u"], states, p["starts"])
+    assert torch.equal(call(canon, p, final_state=f2, states=keep)[70:70 + rows], out[0])
+    assert torch.equal(f2[1], final[0])
+    other = gradients(canon, p, keep)
+    for k in ("du", "ddelta", "dB", "dC", "dz"):
+        assert torch.equal(getattr(other, k)[70:70 + rows], getattr(got, k)[0]), k
+    assert torch.equal(other.dinit_state[1], got.dinit_state[0])
