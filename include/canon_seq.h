@@ -135,7 +135,10 @@ canon_status_t canon_causal_conv(const canon_conv_t* c, void* stream);
 /* Reads x, weight, bias, init_state, dout, d_final_state; writes dx, dweight,
  * dbias, d_init_state.  dweight and dbias are summed over each chunk of
  * CANON_CONV_CHUNK rows of a sequence, rows ascending, then over the chunks:
- * chunk i to lane i mod 16, each lane in order, the lanes by the pairwise tree. */
+ * number i to lane i mod 16, each lane in order, the lanes by the pairwise tree.
+ * Chunk c of sequence s has the number s ceil(rows / CANON_CONV_CHUNK) + c, or,
+ * packed, s + floor(starts[s] / CANON_CONV_CHUNK) + c: there the bits of these
+ * two sums depend on where the sequences lie. */
 #define CANON_CONV_CHUNK 32
 size_t canon_causal_conv_grad_workspace_bytes(size_t seqs, size_t rows, int packed,
                                               size_t channels, size_t taps);
@@ -187,7 +190,9 @@ canon_status_t canon_selective_scan(const canon_selective_scan_t* c, void* ws, s
  * dout and d_final_state; writes du, ddelta, dz (with z), dB, dC, dA, dD,
  * ddelta_bias, d_init_state.  Every sum over rows or channels, and the fold of
  * the gradient backwards (over whole sequences, or in chunks as above), is one
- * fixed expression of the shapes and the sequences. */
+ * fixed expression of the shapes and the sequences' places.  dA, dD and
+ * ddelta_bias are summed over each chunk of CANON_SCAN_CHUNK rows, then over the
+ * chunks as the convolution's, numbered likewise. */
 size_t canon_selective_scan_grad_workspace_bytes(size_t seqs, size_t rows, int packed,
                                                  size_t channels, size_t groups, size_t states);
 canon_status_t canon_selective_scan_grad(const canon_selective_scan_t* c, void* ws,

@@ -1,4 +1,5 @@
 """Causal convolution against its float64 form: forward, backward, single rows."""
+import numpy as np
 import pytest
 
 pytestmark = pytest.mark.gpu
@@ -386,3 +387,52 @@ def test_backward_without_checks(canon, dtype, taps, channels):
                                      "silu", None, g["init"][s:s + 1], g["dfinal"][s:s + 1])
         assert torch.equal(got.dx[a:b], one.dx[0])
         assert torch.equal(got.dinit_state[s], one.dinit_state[0])
+
+
+def column_sum(parts, numbers):
+    """parts[i] under the number numbers[i]: 16 lanes, each in order, then the
+    pairwise tree over the lanes; float32."""
+    lanes = [np.zeros_like(parts[0]) for _ in range(16)]
+    for i, p in sorted(zip(numbers, parts), key=lambda x: x[0]):
+        lanes[i % 16] = lanes[i % 16] + p
+    while len(lanes) > 1:
+        lanes = [a + b for a, b in zip(lanes[::2], lanes[1::2])]
+    return lanes[0]
+
+
+@pytest.mark.parametrize("starts", [
+    None, [0, 32, 64], [0, 200, 200, 231, 600], [7, 7, 40, 41, 1000, 1640],
+    list(range(3, 2400, 47))])
+def test_parameter_sums_in_the_stated_order(canon, starts):
+    """dweight and dbias bit for bit in the order that canon_seq.h states: of packed
+    sequences by the numbers that starts gives the chunks.  The products of bfloat16
+    values are exact in float32, and a float32 plus one is exact in float64, so each
+    FMA is that sum rounded once."""
+    channels, taps = 6, 3
+    rows = 165 if starts is None else starts[-1] + 9
+    lead = (5, rows) if starts is None else (rows,)
+    g = torch.Generator().manual_seed(rows)
+    x, dout = (torch.randn(*lead, channels, generator=g).to(BF16) for _ in range(2))
+    w = torch.randn(channels, taps, generator=g)
+    got = canon.causal_conv_grad(
+        dout.cuda(), x.cuda(), w.cuda(), torch.zeros(channels).cuda(), None,
+        None if starts is None else torch.tensor(starts, dtype=torch.int32).cuda())
+    if starts is None:
+        seqs = [(x[s], dout[s], s * -(-rows // 32)) for s in range(5)]
+    else:
+        seqs = [(x[a:b], dout[a:b], s + a // 32)
+                for s, (a, b) in enumerate(zip(starts[:-1], starts[1:]))]
+    dw, db, numbers = [], [], []
+    for xs, ds, first in seqs:
+        full = np.concatenate([np.zeros((taps - 1, channels)), xs.double().numpy()])
+        ds = ds.double().numpy()
+        for c in range(-(-len(ds) // 32)):
+            w1, b1 = np.zeros((channels, taps), np.float32), np.zeros(channels, np.float32)
+            for t in range(32 * c, min(32 * c + 32, len(ds))):
+                b1 = (b1 + ds[t]).astype(np.float32)
+                w1 = (w1 + full[t:t + taps].T * ds[t][:, None]).astype(np.float32)
+            dw.append(w1), db.append(b1), numbers.append(first + c)
+    assert np.array_equal(got.dbias.cpu().numpy(), column_sum(db, numbers))
+    assert np.array_equal(got.dweight.cpu().numpy(), column_sum(dw, numbers))
+    if starts is not None and len(starts) > 3:  # the order shows in the bits
+        assert not np.array_equal(got.dweight.cpu().numpy(), column_sum(dw, range(len(dw))))
