@@ -46,8 +46,23 @@
  * nothing kept between calls.  No call waits on another workgroup, allocates,
  * or synchronises, so every call may be captured into a graph.  In addition:
  *   - Limits, beyond which calls return CANON_EUNSUPPORTED: seqs, rows and
- *     tokens below 2^30, channels and columns below 2^24, row pitches of the
- *     selective scan below 2^24 elements, and launches below 2^24 workgroups.
+ *     tokens below 2^30, a table's rows below 2^31, channels and columns below
+ *     2^24, and what keeps a launch below 2^32 threads:
+ *       embedding        tokens times the 16-byte accesses of a row (elements,
+ *                        of rows shorter than one) at most 2^34 - 2^10
+ *       causal_conv      seqs ceil(rows / 8), or, packed, seqs + rows / 8, times
+ *                        channels at most 2^40; times channels / 4 (backward
+ *                        / 2; / 1 where channels are no multiple of 4 or rows
+ *                        not aligned to 4 elements) at most 2^32 - 2^24
+ *       selective_scan   with S the states rounded up to 4, 8 or 16: row pitches
+ *                        below 2^24 elements; the convolution's 2^40;
+ *                        chunks (seqs ceil(rows / CANON_SCAN_CHUNK), packed
+ *                        seqs + rows / CANON_SCAN_CHUNK, single rows seqs) times
+ *                        groups ceil(channels / groups / 64) below 2^24; seqs
+ *                        ceil(channels S / 64) below 2^26; backward also groups
+ *                        S times the rows of all sequences at most 2^30 and
+ *                        channels (S + 2) at most 2^26
+ *     (sequences without rows count as one run or chunk).
  *   - Activations (dtype) are float32, bfloat16 or float16 and are passed as
  *     canon_rows_t: element (sequence s, row t, column d) is at
  *     p + s * seq + t * row + d elements.  Columns are contiguous, strides are

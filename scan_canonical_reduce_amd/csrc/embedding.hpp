@@ -53,6 +53,15 @@ inline int64_t id_groups(int64_t rows)
     return (rows + r - 1) / r;
 }
 
+// Accesses per row of width elements of es bytes: 16 bytes each, or single
+// elements where a row has fewer; 1024 of them to a workgroup of the lookup.
+inline int64_t embed_accesses(int64_t width, size_t es)
+{
+    const int64_t v = 16 / (int64_t)es;
+    return width >= v ? (width + v - 1) / v : width;
+}
+constexpr int kEmbedGridAccesses = 1024;
+
 constexpr int kGroupWaves = 16;  // of a workgroup that groups tokens by id
 
 // Exclusive sums over the workgroup's 1024 threads, of two pairs of counts at

@@ -705,8 +705,10 @@ hipError_t launch_embedding(const EmbedArgs& a, hipStream_t st)
     return with_access<T>(a.vec, a.width, [&](auto v, auto al) {
         constexpr int V = decltype(v)::value;
         const int64_t n = a.tokens * ((a.width + V - 1) / V);
+        static_assert(kEmbedGridAccesses == 4 * 256, "k_embedding: 4 a thread");
         k_embedding<T, V, decltype(al)::value>
-            <<<dim3((unsigned)((n + 1023) / 1024)), dim3(256), 0, st>>>(a);
+            <<<dim3((unsigned)((n + kEmbedGridAccesses - 1) / kEmbedGridAccesses)), dim3(256), 0,
+               st>>>(a);
         return hipGetLastError();
     });
 }

@@ -298,11 +298,12 @@ canon_status_t canon_embedding(int dtype, const void* weight, size_t ld_weight, 
         return CANON_EINVAL;
     if (tokens == 0 || width == 0) return CANON_OK;
     if (ids == nullptr || out == nullptr || (rows > 0 && weight == nullptr)) return CANON_EINVAL;
+    const size_t es = elem_bytes(dtype);
     if (!embed_sizes_ok(tokens, rows, width) ||
-        !mul_fits((int64_t)tokens, (int64_t)width, (int64_t)1 << 33))
+        !mul_fits((int64_t)tokens, embed_accesses((int64_t)width, es),
+                  (kMaxGrid256 - 1) * kEmbedGridAccesses))
         return CANON_EUNSUPPORTED;
     if (out == weight) return CANON_EINVAL;
-    const size_t es = elem_bytes(dtype);
     EmbedArgs a{weight, (int64_t)ld_weight, (int64_t)rows, (int64_t)width, ids, id_bytes == 8,
                 false, (int64_t)tokens, scale, out, (int64_t)ld_out};
     a.vec = width * es % 16 == 0 && ptr_aligned(weight, 16) && ptr_aligned(out, 16) &&

@@ -234,3 +234,15 @@ def test_grad_of_some_thousand_tokens(canon, tokens, rows, width, off):
                              accumulate=True, ws=ws)
         assert same_bits(got, grad_ref(dout, ids, rows, 0.75, 2, want, grad)), kind
         assert (dw[:, :off] == 7).all() and (dw[:, off + width:] == 7).all()
+
+
+def test_lookup_past_2_33_elements(canon):
+    """More elements than 2^33, of which 16-byte accesses make few workgroups."""
+    width, n = 8192, (1 << 20) + 5
+    w = torch.randn(7, width, device="cuda").to(BF16)
+    ids = torch.arange(n, device="cuda") % 8  # 7: outside the table
+    got = canon.embedding(w, ids, scale=2.0)
+    assert got.numel() > 1 << 33
+    want = torch.cat([(w.float() * 2).to(BF16), torch.zeros(1, width, device="cuda").to(BF16)])
+    for at in range(0, n, 1 << 17):
+        assert torch.equal(got[at:at + (1 << 17)], want[ids[at:at + (1 << 17)]]), at

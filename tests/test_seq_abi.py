@@ -256,3 +256,50 @@ def test_in_place_refusals(seq):
     m = seq.embedding_grad_workspace_bytes(100, 10, 8)
     assert L.canon_embedding_grad(1, FAKE, 8, FAKE, 8, 100, 10, 8, 1.0, -1, 0, 0, FAKE, 8, FAKE,
                                   m, None) == 1
+
+
+def test_limits_of_a_launch(seq):
+    """The header's limits at their edges: one step beyond is refused, at the edge a
+    call comes as far as the workspace that it is not given."""
+    L = seq._lib()
+
+    def emb(dtype, tokens, width):
+        return L.canon_embedding(dtype, FAKE, width, 10, width, FAKE, 8, tokens, 1.0, FAKE + 16,
+                                 width, None)
+
+    # 2^34 accesses of 16 bytes, and of single elements
+    assert emb(1, 1 << 25, 4096) == 2 and emb(0, 1 << 25, 2048) == 2
+    assert emb(1, (1 << 34) // 513 + 1, 4097) == 2
+    assert emb(1, 1 << 29, 1 << 10) == 2
+
+    def rows(n):
+        return Rows(FAKE, n, n)
+
+    def conv_grad(channels, seqs):
+        r = rows(channels)
+        return L.canon_causal_conv_grad(conv(seq, seqs=seqs, rows=1, channels=channels, x=r, out=r,
+                                             dout=r, dx=Rows(FAKE + 8, channels, channels)),
+                                        None, 0, None)
+
+    most = (1 << 32) - (1 << 24)
+    assert conv_grad(8192, most // 4096) == 3 and conv_grad(8192, most // 4096 + 1) == 2
+    assert conv_grad(8191, most // 8191) == 3 and conv_grad(8191, most // 8191 + 1) == 2
+
+    def scan_grad(channels, groups, states, seqs, n=1):
+        r, b = Rows(FAKE, n * channels, channels), Rows(FAKE, n * groups * states, groups * states)
+        return L.canon_selective_scan_grad(
+            scan(seq, channels=channels, groups=groups, states=states, seqs=seqs, rows=n, u=r,
+                 delta=r, z=r, out=r, dout=r, du=r, ddelta=r, dz=r, B=b, C=b, dB=b, dC=b),
+            None, 0, None)
+
+    # rows of all sequences x groups x padded states
+    for groups, states, padded in ((1, 16, 16), (2, 13, 16), (4, 7, 8), (1, 3, 4)):
+        n = (1 << 30) // (groups * padded)
+        assert scan_grad(64, groups, states, n // 64, 64) == 3
+        assert scan_grad(64, groups, states, n // 64 + 1, 64) == 2
+    # chunks x slabs
+    assert scan_grad(130, 1, 1, ((1 << 24) - 1) // 3) == 3
+    assert scan_grad(130, 1, 1, ((1 << 24) - 1) // 3 + 1) == 2
+    # columns of the parameters' sums
+    edge = (1 << 26) // 18
+    assert scan_grad(edge, 1, 16, 1) == 3 and scan_grad(edge + 1, 1, 16, 1) == 2
