@@ -112,7 +112,7 @@ canon_status_t canon_embedding(int dtype, const void* weight, size_t ld_weight, 
  *          ld_dw
  * padding_id  an id whose row takes no gradient; -1: none
  * accumulate  0: every row of dw is written; 1: added to dw as above
- * Limits: tokens < 2^30, rows < 2^31 (CANON_EUNSUPPORTED). */
+ * Limits: tokens < 2^30, rows <= 2^31 - 512 (CANON_EUNSUPPORTED). */
 size_t canon_embedding_grad_workspace_bytes(size_t tokens, size_t rows, size_t width);
 canon_status_t canon_embedding_grad(int dtype, const void* dout, size_t ld_dout, const void* ids,
                                     int id_bytes, size_t tokens, size_t rows, size_t width,

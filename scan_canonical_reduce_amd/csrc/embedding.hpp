@@ -52,6 +52,9 @@ inline int64_t id_groups(int64_t rows)
     const int64_t r = ids_per_group(rows);
     return (rows + r - 1) / r;
 }
+// Rows of a gradient's table: the grouping kernel's workgroups, of 1024 threads and
+// 512 ids, number below 2^22.
+constexpr int64_t kEmbedGradRows = ((int64_t)1 << 31) - 512;
 
 // Accesses per row of width elements of es bytes: 16 bytes each, or single
 // elements where a row has fewer; 1024 of them to a workgroup of the lookup.

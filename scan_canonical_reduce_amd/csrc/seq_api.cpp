@@ -102,6 +102,11 @@ bool embed_sizes_ok(size_t tokens, size_t rows, size_t width)
     return tokens < (size_t)kMaxRows && rows < ((size_t)1 << 31) && width < ((size_t)1 << 24);
 }
 
+bool embed_grad_sizes_ok(size_t tokens, size_t rows, size_t width)
+{
+    return embed_sizes_ok(tokens, rows, width) && rows <= (size_t)kEmbedGradRows;
+}
+
 // ---------------------------------------------------------------- convolution
 struct ConvLayout : Layout {
     size_t w, b;
@@ -315,7 +320,7 @@ canon_status_t canon_embedding(int dtype, const void* weight, size_t ld_weight, 
 
 size_t canon_embedding_grad_workspace_bytes(size_t tokens, size_t rows, size_t width)
 {
-    if (!embed_sizes_ok(tokens, rows, width) || rows == 0 || width == 0) return 0;
+    if (!embed_grad_sizes_ok(tokens, rows, width) || rows == 0 || width == 0) return 0;
     return EmbedLayout((int64_t)tokens, (int64_t)rows, (int64_t)width).bytes;
 }
 
@@ -331,7 +336,7 @@ canon_status_t canon_embedding_grad(int dtype, const void* dout, size_t ld_dout,
         return CANON_EINVAL;
     if (rows == 0 || width == 0) return CANON_OK;
     if (dw == nullptr || (tokens > 0 && (ids == nullptr || dout == nullptr))) return CANON_EINVAL;
-    if (!embed_sizes_ok(tokens, rows, width)) return CANON_EUNSUPPORTED;
+    if (!embed_grad_sizes_ok(tokens, rows, width)) return CANON_EUNSUPPORTED;
     const EmbedLayout l((int64_t)tokens, (int64_t)rows, (int64_t)width);
     if (canon_status_t s = check_ws(ws, ws_bytes, l.bytes)) return s;
     if (tokens > 0 && dw == dout) return CANON_EINVAL;

@@ -303,3 +303,14 @@ def test_limits_of_a_launch(seq):
     # columns of the parameters' sums
     edge = (1 << 26) // 18
     assert scan_grad(edge, 1, 16, 1) == 3 and scan_grad(edge + 1, 1, 16, 1) == 2
+
+
+def test_rows_of_the_largest_gradient(seq):
+    """Above 2^31 - 512 rows the grouping kernel would need 2^22 workgroups of 1024
+    threads: refused, whatever the number of tokens."""
+    L = seq._lib()
+    for rows, status in (((1 << 31) - 512, 3), ((1 << 31) - 511, 2), ((1 << 31) - 1, 2)):
+        for tokens in (0, 1, 1000, 5000):
+            assert L.canon_embedding_grad(1, FAKE, 8, FAKE, 8, tokens, rows, 8, 1.0, -1, 0, 0, FAKE,
+                                          8, None, 0, None) == status, (rows, tokens)
+        assert (seq.embedding_grad_workspace_bytes(5000, rows, 8) > 0) == (status == 3)
