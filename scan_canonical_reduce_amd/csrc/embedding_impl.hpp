@@ -49,17 +49,21 @@ __global__ __launch_bounds__(256) void k_embedding(EmbedArgs a)
     const int64_t i0 = (int64_t)blockIdx.x * (256 * U) + threadIdx.x;
     Vec<T, V> x[U];
     E* dst[U];
+    float scale[U];  // 0 for an id outside the table, whatever the scale
 #pragma unroll
     for (int u = 0; u < U; ++u) {
         const int64_t i = i0 + u * 256;
         dst[u] = nullptr;
         x[u] = Vec<T, V>{};
+        scale[u] = 0.f;
         if (i < n) {
             const int64_t t = i / nv, c = vec_col<V, AL>((i - t * nv) * V, a.width);
             const int64_t id = token_id(a.ids, a.ids64, t);
             dst[u] = static_cast<E*>(a.out) + t * a.ld_out + c;
-            if (id >= 0 && id < a.rows)
+            if (id >= 0 && id < a.rows) {
                 x[u] = ld_any<T, V, AL>(static_cast<const E*>(a.weight) + id * a.ld_weight + c);
+                scale[u] = a.scale;
+            }
         }
     }
 #pragma unroll
@@ -67,7 +71,7 @@ __global__ __launch_bounds__(256) void k_embedding(EmbedArgs a)
         if (!dst[u]) continue;
         float y[V];
 #pragma unroll
-        for (int j = 0; j < V; ++j) y[j] = T::load(x[u].e[j]) * a.scale;
+        for (int j = 0; j < V; ++j) y[j] = T::load(x[u].e[j]) * scale[u];
         st_any<T, V, AL>(dst[u], y);
     }
 }

@@ -246,3 +246,15 @@ def test_lookup_past_2_33_elements(canon):
     want = torch.cat([(w.float() * 2).to(BF16), torch.zeros(1, width, device="cuda").to(BF16)])
     for at in range(0, n, 1 << 17):
         assert torch.equal(got[at:at + (1 << 17)], want[ids[at:at + (1 << 17)]]), at
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16, F16])
+@pytest.mark.parametrize("scale", [-1.0, float("inf"), float("-inf"), float("nan")])
+def test_rows_outside_the_table_are_zero_for_any_scale(canon, dtype, scale):
+    w = torch.ones(3, 9, dtype=dtype, device="cuda")
+    ids = torch.tensor([-1, 1, 3, 2 ** 40], device="cuda")
+    got = canon.embedding(w, ids, scale=scale)
+    want = torch.zeros(4, 9, dtype=dtype)
+    want[1] = scale
+    assert torch.equal(torch.isnan(got).cpu(), torch.isnan(want))
+    assert same_bits(torch.where(torch.isnan(got), 0, got), torch.where(torch.isnan(want), 0, want))
