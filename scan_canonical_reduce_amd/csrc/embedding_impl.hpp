@@ -496,13 +496,22 @@ __device__ __forceinline__ void tree_partials(const EmbedGradArgs& a, int32_t of
 // Up to 4096 tokens, one launch: a workgroup groups the tokens of its ids in LDS
 // (as k_embed_group; its ids are those equal to its number modulo a power of two,
 // so that neighbouring frequent ones fall to different workgroups) and sums their
-// rows in its part of the columns.  Measured against three launches, us a call,
-// frequencies falling as 1/rank (all tokens one id): 300 tokens x 1000 of 10007
-// rows bf16 11.5 and 18.4 (17 and 24), 1000 x 512 of 1000 rows 15 and 23 (24 and
-// 24), 3001 x 1000 of 10007 rows float16 19 and 25 (64 and 27: one workgroup for
-// each 512 columns), 4096 x 4096 of 32000 rows 117 and 118 (171 and 114), 395 x
-// 1292 of 118 rows 12 and 20 (17 and 27).  Not taken above 1024 tokens for fewer
-// than 256 rows or so, where few workgroups would have all tokens.
+// rows in its part of the columns.  A frequent id is one workgroup's in each 512
+// (16-bit) or 256 columns, so beyond 1024 tokens it is taken where it gains with
+// spread ids: rows of fewer than 8 such parts, tables of up to 64 MiB.  Measured
+// against three launches, us a call, bf16, frequencies falling as 1/rank (half the
+// tokens one id; all):
+//   1000 x 512 of 10007 rows    16 and 25 (18 and 25; 25 and 25)
+//   1000 x 4096 of 10007 rows   27 and 33 (32 and 33; 35 and 34)
+//   3001 x 1000 of 10007 rows   18 and 26 (39 and 26; 66 and 28)
+//   4096 x 1000 of 10007 rows   20 and 27 (48 and 27; 86 and 30)
+// and not taken:
+//   4096 x 2048 of 32000 rows   42 and 44 (69 and 44; 99 and 43)
+//   3001 x 4096 of 10007 rows   34 and 36 (53 and 37; 73 and 38)
+//   4096 x 4096 of 32000 rows   78 and 70 (119 and 69; 138 and 68)
+//   4096 x 8192 of 10007 rows   65 and 56 (116 and 56; 185 and 53)
+// Nor above 1024 tokens for fewer than 256 rows or so, where few workgroups would
+// have all tokens.
 constexpr int kEmbedOne = 4096;
 constexpr int kOneIds = 512;
 
@@ -748,7 +757,9 @@ hipError_t launch_embedding_grad(const EmbedGradArgs& a, hipStream_t st)
         }
         if (a.tokens <= kEmbedOne) {
             const OneShape one = one_shape(a.rows, slabs);
-            if (one.blocks() <= 512 && (one.log_groups >= 4 || a.tokens <= 1024)) {
+            const int64_t bytes = a.rows * a.width * (int64_t)sizeof(typename G::store_t);
+            const bool spread = one.log_groups >= 4 && slabs < 8 && bytes <= (64 << 20);
+            if (one.blocks() <= 512 && (spread || a.tokens <= 1024)) {
                 k_embed_one<T, G, V, AL>
                     <<<dim3((unsigned)one.blocks()), dim3(64 * kGroupWaves),
                        (size_t)kGroupWaves * one.ids * sizeof(int32_t), st>>>(a, one);

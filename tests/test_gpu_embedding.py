@@ -4,6 +4,7 @@ import numpy as np
 import pytest
 
 import oracle
+from gpu_util import launches
 
 pytestmark = pytest.mark.gpu
 
@@ -258,3 +259,21 @@ def test_rows_outside_the_table_are_zero_for_any_scale(canon, dtype, scale):
     want[1] = scale
     assert torch.equal(torch.isnan(got).cpu(), torch.isnan(want))
     assert same_bits(torch.where(torch.isnan(got), 0, got), torch.where(torch.isnan(want), 0, want))
+
+
+@pytest.mark.parametrize("tokens,rows,width,kernels", [
+    (128, 1000, 4096, 1), (129, 1000, 4096, 1), (1024, 1000, 4096, 1), (1025, 1000, 4096, 3),
+    (4096, 300, 4090, 3), (4096, 1000, 3580, 1), (4096, 1000, 3590, 3), (2000, 33000, 1000, 1),
+    (2000, 34000, 1000, 3), (4097, 1000, 520, 3)])
+def test_one_launch_only_where_it_gains(canon, tokens, rows, width, kernels):
+    """Wide rows and large tables of more than 1024 tokens take three launches, whose
+    time does not depend on how frequent an id is; the bits are the same."""
+    dout = torch.randn(tokens, width, generator=torch.Generator().manual_seed(rows)).to(BF16)
+    for kind in ("one", "zipf"):
+        ids = make_ids(tokens, rows, kind, rows)
+        d, i = dout.cuda(), ids.cuda()
+        out = torch.full((rows, width), 7.0, dtype=BF16, device="cuda")
+        assert launches(lambda: canon.embedding_grad(d, i, rows, out=out)) == kernels
+        if rows <= 1000:
+            assert same_bits(canon.embedding_grad(d, i, rows), grad_ref(dout, ids, rows, 1.0,
+                                                                        dtype=BF16))
