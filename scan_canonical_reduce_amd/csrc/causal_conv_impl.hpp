@@ -8,11 +8,6 @@
 // taps takes 52 us forward (5.2 TB/s) and 107 backward, whose second window and
 // sums of dw leave less in flight (4, 5 or 6 waves a SIMD and chunks of 64 rows
 // measure the same).
-//
-// AL: the vectors are aligned.  Else they are read and written as they lie, and
-// where the channels are not whole vectors the last thread's are moved back over
-// those of the one before, whose channels it computes and does not store (an
-// initial state may be overwritten by then).
 #pragma once
 
 #include "causal_conv.hpp"
@@ -62,40 +57,16 @@ struct ConvParams {
     }
 };
 
-// Where a thread's channels are, and how many of them are another's.
-template <int V, bool AL>
-struct ConvCol {
-    int32_t ch, skip;
-    __device__ __forceinline__ ConvCol(const ConvArgs& a, int32_t first)
-        : ch((int32_t)vec_col<V, AL>(first, a.channels)), skip(first - ch)
-    {
-    }
-};
-
-// Stores all but the first `skip` values.
-template <typename T, int V, bool AL>
-__device__ __forceinline__ void conv_store(typename T::store_t* p, const float (&v)[V],
-                                           int32_t skip)
-{
-    if (!AL && skip) {
-#pragma unroll
-        for (int j = 0; j < V; ++j)
-            if (j >= skip) p[j] = T::round(v[j]);
-        return;
-    }
-    st_any<T, V, AL>(p, v);
-}
-
 // Row t of the sequence, or of the initial state in front of it (t < 0).
-template <typename T, int K, int V, bool AL>
+template <typename T, int K, int V>
 __device__ __forceinline__ void conv_row(const ConvArgs& a, const typename T::store_t* x,
                                          int64_t s, int32_t t, int32_t ch, float (&v)[V])
 {
     if (t >= 0) {
-        unpack<T, V>(ld_any<T, V, AL>(x + (int64_t)t * a.x.row), v);
+        unpack<T, V>(ld_vec<T, V>(x + (int64_t)t * a.x.row), v);
     } else if (a.init) {
         const typename T::store_t* p = static_cast<const typename T::store_t*>(a.init);
-        unpack<T, V>(ld_any<T, V, AL>(p + (s * (K - 1) + (K - 1 + t)) * a.channels + ch), v);
+        unpack<T, V>(ld_vec<T, V>(p + (s * (K - 1) + (K - 1 + t)) * a.channels + ch), v);
     } else {
 #pragma unroll
         for (int i = 0; i < V; ++i) v[i] = 0.f;
@@ -114,14 +85,13 @@ __device__ __forceinline__ float conv_sum(const float (&win)[K][V], const float 
 
 // RUN rows per thread (at least K - 1, so that only a sequence's first run
 // reads the initial state).
-template <typename T, int K, int V, bool AL, int RUN>
+template <typename T, int K, int V, int RUN>
 __global__ __launch_bounds__(256, K <= 4 ? 4 : 2) void k_causal_conv(ConvArgs a)
 {
-    const int32_t nv = (a.channels + V - 1) / V;
+    const int32_t nv = a.channels / V;  // whole vectors, or V = 1
     const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
     const int64_t slot = i / nv;
-    const ConvCol<V, AL> col(a, (int32_t)(i - slot * nv) * V);
-    const int32_t ch = col.ch;
+    const int32_t ch = (int32_t)(i - slot * nv) * V;
     if (slot >= slot_count<RUN>(a.q.seqs, a.q.rows, a.q.starts != nullptr)) return;
     const Chunk ck = slot_chunk<RUN>(a.q, slot);
     if (ck.row > 0 && ck.len <= 0) return;
@@ -130,7 +100,7 @@ __global__ __launch_bounds__(256, K <= 4 ? 4 : 2) void k_causal_conv(ConvArgs a)
 
     float win[K][V];  // the rows up to the current one, oldest first
 #pragma unroll
-    for (int k = 0; k + 1 < K; ++k) conv_row<T, K, V, AL>(a, x, ck.s, ck.row - (K - 1) + k, ch, win[k + 1]);
+    for (int k = 0; k + 1 < K; ++k) conv_row<T, K, V>(a, x, ck.s, ck.row - (K - 1) + k, ch, win[k + 1]);
 
     if (a.final && ck.row == 0) {
         // By the thread that has read the initial state, which may be the
@@ -142,7 +112,7 @@ __global__ __launch_bounds__(256, K <= 4 ? 4 : 2) void k_causal_conv(ConvArgs a)
             const int32_t t = ck.span.len - (K - 1) + k;
             float v[V];
             if (t >= 0) {
-                conv_row<T, K, V, AL>(a, x, ck.s, t, ch, v);
+                conv_row<T, K, V>(a, x, ck.s, t, ch, v);
             } else {  // row K - 1 + t of the initial state, in win[K + t]
 #pragma unroll
                 for (int m = 0; m + 1 < K; ++m)
@@ -150,7 +120,7 @@ __global__ __launch_bounds__(256, K <= 4 ? 4 : 2) void k_causal_conv(ConvArgs a)
 #pragma unroll
                         for (int j = 0; j < V; ++j) v[j] = win[m + 1][j];
             }
-            conv_store<T, V, AL>(f + (int64_t)k * a.channels, v, col.skip);
+            st_vec<T, V>(f + (int64_t)k * a.channels, v);
         }
     }
 
@@ -164,7 +134,7 @@ __global__ __launch_bounds__(256, K <= 4 ? 4 : 2) void k_causal_conv(ConvArgs a)
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const int32_t r = full || r0 + u < ck.len ? r0 + u : ck.len - 1;
-            in[b][u] = ld_any<T, V, AL>(xr + (int64_t)r * a.x.row);
+            in[b][u] = ld_vec<T, V>(xr + (int64_t)r * a.x.row);
         }
     };
     if (ck.len > 0) fetch(0, 0, false);
@@ -185,7 +155,7 @@ __global__ __launch_bounds__(256, K <= 4 ? 4 : 2) void k_causal_conv(ConvArgs a)
             if (a.silu)
 #pragma unroll
                 for (int j = 0; j < V; ++j) y[j] = silu_f(y[j], sigmoid_f<T>(y[j]));
-            conv_store<T, V, AL>(outr + (int64_t)(r0 + u) * a.out.row, y, col.skip);
+            st_vec<T, V>(outr + (int64_t)(r0 + u) * a.out.row, y);
         }
     };
     if (__all(ck.len == RUN)) {
@@ -208,15 +178,14 @@ __global__ __launch_bounds__(256, K <= 4 ? 4 : 2) void k_causal_conv(ConvArgs a)
 // Backward: with dp = dout silu'(p), dx[t] = sum_k w[k] dp[t + K - 1 - k].  A
 // thread walks its run and K - 1 rows beyond it, p recomputed from x.
 // Its rows' part of dw and db goes to the workspace, per slot.
-template <typename T, int K, int V, bool AL>
+template <typename T, int K, int V>
 __global__ __launch_bounds__(256, K <= 4 ? 5 : 2) void k_causal_conv_grad(ConvArgs a)
 {
     constexpr int RUN = CANON_CONV_CHUNK;
-    const int32_t nv = (a.channels + V - 1) / V;
+    const int32_t nv = a.channels / V;  // whole vectors, or V = 1
     const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
     const int64_t slot = i / nv;
-    const ConvCol<V, AL> col(a, (int32_t)(i - slot * nv) * V);
-    const int32_t ch = col.ch;
+    const int32_t ch = (int32_t)(i - slot * nv) * V;
     if (slot >= slot_count<RUN>(a.q.seqs, a.q.rows, a.q.starts != nullptr)) return;
     const Chunk ck = slot_chunk<RUN>(a.q, slot);
     float dw[K][V], db[V];
@@ -246,7 +215,7 @@ __global__ __launch_bounds__(256, K <= 4 ? 5 : 2) void k_causal_conv_grad(ConvAr
         if (ck.len > 0)
 #pragma unroll
             for (int k = 0; k + 1 < K; ++k)
-                conv_row<T, K, V, AL>(a, x, ck.s, ck.row - (K - 1) + k, ch, win[k + 1]);
+                conv_row<T, K, V>(a, x, ck.s, ck.row - (K - 1) + k, ch, win[k + 1]);
         const int32_t len = ck.span.len;
         const int32_t end = ck.row + ck.len;  // of the run
         const int32_t stop = end + K - 1;
@@ -259,8 +228,8 @@ __global__ __launch_bounds__(256, K <= 4 ? 5 : 2) void k_causal_conv_grad(ConvAr
             for (int u = 0; u < U; ++u) {
                 const int32_t t = ck.row + r0 + u;
                 const int64_t row = inner || t < len ? t : len - 1;
-                in[b][u] = ld_any<T, V, AL>(x + row * a.x.row);
-                gin[b][u] = ld_any<T, V, AL>(go + row * a.dout.row);
+                in[b][u] = ld_vec<T, V>(x + row * a.x.row);
+                gin[b][u] = ld_vec<T, V>(go + row * a.dout.row);
             }
         };
         if (len > 0) fetch(0, 0, false);
@@ -312,14 +281,14 @@ __global__ __launch_bounds__(256, K <= 4 ? 5 : 2) void k_causal_conv_grad(ConvAr
             const int32_t f = m - (len - (K - 1));
             if (!inner && df && f >= 0) {
                 float g[V];
-                unpack<T, V>(ld_any<T, V, AL>(df + (int64_t)f * a.channels), g);
+                unpack<T, V>(ld_vec<T, V>(df + (int64_t)f * a.channels), g);
 #pragma unroll
                 for (int j = 0; j < V; ++j) y[j] += g[j];
             }
             if (initial)
-                conv_store<T, V, AL>(di + (int64_t)(K - 1 + m) * a.channels, y, col.skip);
+                st_vec<T, V>(di + (int64_t)(K - 1 + m) * a.channels, y);
             else
-                conv_store<T, V, AL>(dx + (int64_t)m * a.dx.row, y, col.skip);
+                st_vec<T, V>(dx + (int64_t)m * a.dx.row, y);
         };
         constexpr int ALL = RUN + K - 1;
         constexpr int READ = (ALL + U - 1) / U * U;  // rows that whole fetches read
@@ -349,20 +318,19 @@ __global__ __launch_bounds__(256, K <= 4 ? 5 : 2) void k_causal_conv_grad(ConvAr
 }
 
 // One row of each sequence; the state's rows move up by one.
-template <typename T, int K, int V, bool AL>
+template <typename T, int K, int V>
 __global__ __launch_bounds__(256) void k_causal_conv_step(ConvArgs a)
 {
-    const int32_t nv = (a.channels + V - 1) / V;
+    const int32_t nv = a.channels / V;  // whole vectors, or V = 1
     const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
     const int64_t s = i / nv;
-    const ConvCol<V, AL> col(a, (int32_t)(i - s * nv) * V);
-    const int32_t ch = col.ch;
+    const int32_t ch = (int32_t)(i - s * nv) * V;
     if (s >= a.q.seqs) return;
     const typename T::store_t* x = static_cast<typename T::store_t*>(a.x.p) + s * a.x.seq + ch;
     float win[K][V];
 #pragma unroll
-    for (int k = 0; k + 1 < K; ++k) conv_row<T, K, V, AL>(a, x, s, k - (K - 1), ch, win[k]);
-    const Vec<T, V> in = ld_any<T, V, AL>(x);
+    for (int k = 0; k + 1 < K; ++k) conv_row<T, K, V>(a, x, s, k - (K - 1), ch, win[k]);
+    const Vec<T, V> in = ld_vec<T, V>(x);
     unpack<T, V>(in, win[K - 1]);
     ConvParams<T, K, V> p;
     p.load(a, ch);
@@ -377,10 +345,9 @@ __global__ __launch_bounds__(256) void k_causal_conv_step(ConvArgs a)
             static_cast<typename T::store_t*>(a.final) + s * (K - 1) * a.channels + ch;
 #pragma unroll
         for (int k = 0; k + 1 < K; ++k)
-            conv_store<T, V, AL>(f + (int64_t)k * a.channels, win[k + 1], col.skip);
+            st_vec<T, V>(f + (int64_t)k * a.channels, win[k + 1]);
     }
-    conv_store<T, V, AL>(static_cast<typename T::store_t*>(a.out.p) + s * a.out.seq + ch, y,
-                         col.skip);
+    st_vec<T, V>(static_cast<typename T::store_t*>(a.out.p) + s * a.out.seq + ch, y);
 }
 
 // --------------------------------------------------------------------- launches
@@ -388,10 +355,10 @@ template <int RUN>
 unsigned conv_grid(const ConvArgs& a, int v)
 {
     const int64_t slots = slot_count<RUN>(a.q.seqs, a.q.rows, a.q.starts != nullptr);
-    return (unsigned)((slots * ((a.channels + v - 1) / v) + 255) / 256);
+    return (unsigned)((slots * (a.channels / v) + 255) / 256);
 }
 
-template <typename T, int K, int V, bool AL>
+template <typename T, int K, int V>
 hipError_t launch_conv_v(const ConvArgs& a, hipStream_t st)
 {
     // Long runs read fewer rows twice; short ones are for launches that would
@@ -399,21 +366,21 @@ hipError_t launch_conv_v(const ConvArgs& a, hipStream_t st)
     // of 4096 bf16 channels (64 to 512 threads x 1024), us: runs of 32 rows 10.9,
     // 16.4, 24.0, 45.7; of 8 rows 9.1, 15.1, 26.5, 47.7.
     const int64_t threads = slot_count<32>(a.q.seqs, a.q.rows, a.q.starts != nullptr) *
-                            ((a.channels + V - 1) / V);
+                            (a.channels / V);
     if (threads >= (int64_t)device_cus() * 768)
-        k_causal_conv<T, K, V, AL, 32><<<dim3(conv_grid<32>(a, V)), dim3(256), 0, st>>>(a);
+        k_causal_conv<T, K, V, 32><<<dim3(conv_grid<32>(a, V)), dim3(256), 0, st>>>(a);
     else
-        k_causal_conv<T, K, V, AL, 8><<<dim3(conv_grid<8>(a, V)), dim3(256), 0, st>>>(a);
+        k_causal_conv<T, K, V, 8><<<dim3(conv_grid<8>(a, V)), dim3(256), 0, st>>>(a);
     return hipGetLastError();
 }
 
-template <typename T, int K, int V, bool AL>
+template <typename T, int K, int V>
 hipError_t launch_conv_grad_v(const ConvArgs& a, hipStream_t st)
 {
     const int64_t slots =
         slot_count<CANON_CONV_CHUNK>(a.q.seqs, a.q.rows, a.q.starts != nullptr);
     const unsigned grid = conv_grid<CANON_CONV_CHUNK>(a, V);
-    if (grid) k_causal_conv_grad<T, K, V, AL><<<dim3(grid), dim3(256), 0, st>>>(a);
+    if (grid) k_causal_conv_grad<T, K, V><<<dim3(grid), dim3(256), 0, st>>>(a);
     if (hipError_t e = hipGetLastError()) return e;
     const int64_t d = a.channels;
     return launch_column_sums({{{a.ws_w, d * K, K, K, a.dweight}, {a.ws_b, d, 1, 1, a.dbias}, {}},
@@ -421,42 +388,42 @@ hipError_t launch_conv_grad_v(const ConvArgs& a, hipStream_t st)
                               st);
 }
 
-template <typename T, int K, int V, bool AL>
+template <typename T, int K, int V>
 hipError_t launch_conv_step_v(const ConvArgs& a, hipStream_t st)
 {
-    const int64_t n = a.q.seqs * ((a.channels + V - 1) / V);
-    k_causal_conv_step<T, K, V, AL><<<dim3((unsigned)((n + 255) / 256)), dim3(256), 0, st>>>(a);
+    const int64_t n = a.q.seqs * (a.channels / V);
+    k_causal_conv_step<T, K, V><<<dim3((unsigned)((n + 255) / 256)), dim3(256), 0, st>>>(a);
     return hipGetLastError();
 }
 
-#define CANON_CONV_TAPS(FN, V, AL)                 \
-    switch (taps) {                                \
-        case 1: return FN<T, 1, V, AL>(a, st);     \
-        case 2: return FN<T, 2, V, AL>(a, st);     \
-        case 3: return FN<T, 3, V, AL>(a, st);     \
-        case 4: return FN<T, 4, V, AL>(a, st);     \
-        case 5: return FN<T, 5, V, AL>(a, st);     \
-        case 6: return FN<T, 6, V, AL>(a, st);     \
-        case 7: return FN<T, 7, V, AL>(a, st);     \
-        default: return FN<T, 8, V, AL>(a, st);    \
+#define CANON_CONV_TAPS(FN, V)                 \
+    switch (taps) {                            \
+        case 1: return FN<T, 1, V>(a, st);     \
+        case 2: return FN<T, 2, V>(a, st);     \
+        case 3: return FN<T, 3, V>(a, st);     \
+        case 4: return FN<T, 4, V>(a, st);     \
+        case 5: return FN<T, 5, V>(a, st);     \
+        case 6: return FN<T, 6, V>(a, st);     \
+        case 7: return FN<T, 7, V>(a, st);     \
+        default: return FN<T, 8, V>(a, st);    \
     }
 
-// V channels a thread; one where they are not aligned to that, except where
-// unaligned vectors measure faster: 16384 rows of 4095 channels, single channels
-// and vectors, us: forward bf16 56 and 59, float32 139 and 129; backward bf16 132
-// and 116, float32 169 and 187.
-#define CANON_CONV_LAUNCH(NAME, FN, V, UNALIGNED_BYTES)                                   \
-    template <typename T>                                                                 \
-    hipError_t NAME(const ConvArgs& a, int taps, hipStream_t st)                          \
-    {                                                                                     \
-        if (a.vec) CANON_CONV_TAPS(FN, V, true)                                           \
-        if constexpr (sizeof(typename T::store_t) == UNALIGNED_BYTES)                     \
-            if (a.channels >= V) CANON_CONV_TAPS(FN, V, false)                            \
-        CANON_CONV_TAPS(FN, 1, true)                                                      \
+// V channels a thread, or one where they are not aligned to that.  Vectors read and
+// written as they lie gain and lose too little to be worth theirs: 4 taps, single
+// channels and such vectors, us: forward float32 16384 x 4095 137 and 129, 16384 x
+// 1001 25.6 and 26.7, 2048 x 4095 13.1 and 15.4; backward bf16 16384 x 4095 123 and
+// 136, 16384 x 2047 60.7 and 58.2, 2048 x 2047 19.7 and 22.8; single rows float32
+// 2048 x 4095 45.5 and 42.3, 2048 x 1001 12.8 and 13.3.
+#define CANON_CONV_LAUNCH(NAME, FN, V)                              \
+    template <typename T>                                           \
+    hipError_t NAME(const ConvArgs& a, int taps, hipStream_t st)    \
+    {                                                               \
+        if (a.vec) CANON_CONV_TAPS(FN, V)                           \
+        CANON_CONV_TAPS(FN, 1)                                      \
     }
-CANON_CONV_LAUNCH(launch_causal_conv, launch_conv_v, kConvV, 4)
-CANON_CONV_LAUNCH(launch_causal_conv_grad, launch_conv_grad_v, 2, 2)
-CANON_CONV_LAUNCH(launch_causal_conv_step, launch_conv_step_v, kConvV, 4)
+CANON_CONV_LAUNCH(launch_causal_conv, launch_conv_v, kConvV)
+CANON_CONV_LAUNCH(launch_causal_conv_grad, launch_conv_grad_v, 2)
+CANON_CONV_LAUNCH(launch_causal_conv_step, launch_conv_step_v, kConvV)
 #undef CANON_CONV_LAUNCH
 #undef CANON_CONV_TAPS
 

@@ -342,7 +342,7 @@ def inner_waves(rows, channels, taps, per):
 def test_backward_without_checks(canon, dtype, taps, channels):
     """Sequences whose ends lie on both sides of the rows that the loop without
     checks needs, against the float64 form; NaN behind each sequence."""
-    per = 1 if channels == 133 and dtype == F32 else 2
+    per = 2 if channels == 128 else 1
     need = 32 + (32 + taps - 1 + 3) // 4 * 4
     if channels == 128:
         assert not inner_waves(need - 1, channels, taps, per)
