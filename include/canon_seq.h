@@ -37,7 +37,8 @@
  *
  * Everything is computed in 32 bits and rounded once where it is stored.  No
  * value is ever combined by an atomic, so each call is reproducible bit for
- * bit.
+ * bit.  An infinite u, dl or B of the scan leaves the channel's outputs from that
+ * row on not finite; which of them are infinite and which NaN is not specified.
  *
  * Conventions are those of canon.h: device pointers on the current HIP
  * device, work enqueued on `stream`, argument errors returned before anything
@@ -75,7 +76,7 @@
  *     starts[seqs]) are neither read nor written.  Values outside [0, rows]
  *     are taken as the nearest of the two.
  *   - Parameters, their gradients and scan states are float32 and contiguous
- *     unless said otherwise.
+ *     unless said otherwise; the convolution's states have the type dtype.
  *   - Outputs do not overlap inputs unless said otherwise.
  */
 #ifndef CANON_SEQ_H
@@ -184,7 +185,7 @@ typedef struct {
     float* final_state;      /* the same shape, or NULL */
     float* chunk_states;     /* canon_selective_scan_states(...) elements that
                                 the forward pass writes for the backward pass,
-                                or NULL */
+                                16-byte aligned, or NULL */
     /* backward */
     canon_rows_t dout, du, ddelta, dz, dB, dC;
     float *dA, *dD, *ddelta_bias; /* dD, ddelta_bias may be NULL */
@@ -207,7 +208,8 @@ canon_status_t canon_selective_scan(const canon_selective_scan_t* c, void* ws, s
  * the gradient backwards (over whole sequences, or in chunks as above), is one
  * fixed expression of the shapes and the sequences' places.  dA, dD and
  * ddelta_bias are summed over each chunk of CANON_SCAN_CHUNK rows, then over the
- * chunks as the convolution's, numbered likewise. */
+ * chunks as the convolution's, numbered likewise.  channels is at least 1
+ * (CANON_EINVAL). */
 size_t canon_selective_scan_grad_workspace_bytes(size_t seqs, size_t rows, int packed,
                                                  size_t channels, size_t groups, size_t states);
 canon_status_t canon_selective_scan_grad(const canon_selective_scan_t* c, void* ws,

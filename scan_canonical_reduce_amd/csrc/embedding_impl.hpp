@@ -730,7 +730,9 @@ inline OneShape one_shape(int64_t rows, int64_t slabs)
 {
     OneShape s;
     s.parts = slabs < 16 ? (int)slabs : 16;
-    s.log_groups = 0;  // up to 256 workgroups, of 16 ids or more and at most 512
+    // Groups are doubled up to 256 workgroups or down to 9 to 17 ids each, and on
+    // until none has more than 512 ids, which may take more than 256 workgroups.
+    s.log_groups = 0;
     while (((int64_t)2 * s.parts << s.log_groups) <= 256 && (rows >> s.log_groups) > 16)
         ++s.log_groups;
     while (s.log_groups < 24 && ((rows - 1) >> s.log_groups) + 1 > kOneIds) ++s.log_groups;

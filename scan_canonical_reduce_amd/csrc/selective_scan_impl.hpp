@@ -639,7 +639,9 @@ __global__ __launch_bounds__(256) void k_selective_scan_step(ScanArgs a)
 // us, at 64, 128, 192, 256, 320, 384, 512, 576, 1024 workgroups: whole 123, 124,
 // 124, 123, 177, 179, 180, 242, 310; in chunks 47, 78, 106, 132, 162, 187, 242,
 // 273, 470; and in the same proportion for 256 rows (34 and 22 at 64 workgroups,
-// 48 and 79 at 512).  Packed sequences' lengths are not known here.
+// 48 and 79 at 512).  float32 and 8 or 4 states change sides within 64 workgroups of
+// that: the other way would at most save 10% (4 states at 256: whole 77, in chunks
+// 70).  Packed sequences' lengths are not known here.
 inline bool scan_whole_sequences(const ScanArgs& a, int64_t slabs)
 {
     const int64_t w = a.q.seqs * slabs;

@@ -8,7 +8,8 @@ Shapes.  Activations (float32, bfloat16 or float16, one type per call) are
 ascending row offsets, on the GPU) ``[rows, columns]`` with the sequences
 packed one after the other; rows outside them are left as they are.  Columns
 have unit stride, rows and sequences any.  Parameters, their gradients and scan
-states are float32 and contiguous.
+states are float32 and contiguous, the convolution's states contiguous and of the
+activations' type.
 
 Calls run on the current stream of the tensors' device.  ``ws`` is a
 caller-owned uint8 workspace of ``*_workspace_bytes(...)`` bytes; without it,
