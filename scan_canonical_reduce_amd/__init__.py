@@ -524,3 +524,6 @@ from .seq import (  # noqa: E402
     embedding_grad_workspace_bytes, selective_scan, selective_scan_grad,
     selective_scan_grad_workspace_bytes, selective_scan_states, selective_scan_step,
     selective_scan_workspace_bytes)
+from .layer import (  # noqa: E402
+    LayerNormGrads, add_layer_norm, layer_norm, layer_norm_grad, layer_norm_grad_workspace_bytes,
+    layer_norm_stats)

@@ -1,0 +1,154 @@
+// C ABI of the layer operators (canon_layer.h): argument checking, workspace
+// layout, dispatch on the element type.
+#include "../../include/canon_layer.h"
+#include "layer_norm.hpp"
+#include "seq_args.hpp"
+
+using namespace canon;
+using namespace canon::seq;
+using canon::abi::check_ws;
+using canon::abi::hip_status;
+
+namespace {
+
+// An output in an input's place: the same elements, not a shifted or strided view.
+bool same_rows(const canon_rows_t& a, const canon_rows_t& b)
+{
+    return a.p == b.p && a.seq == b.seq && a.row == b.row;
+}
+bool in_place_ok(const canon_rows_t& out, const canon_rows_t& in)
+{
+    return in.p == nullptr || out.p != in.p || same_rows(out, in);
+}
+
+// ----------------------------------------------------------------- layer norm
+bool norm_sizes_ok(int64_t seqs, int64_t rows, int64_t width)
+{
+    return seqs < kMaxRows && rows < kMaxRows && width < ((int64_t)1 << 24) &&
+           mul_fits(seqs, rows, ((int64_t)1 << 31) - 1);
+}
+
+int64_t norm_chunks(int64_t total)
+{
+    const int64_t chunk = norm_chunk(total);
+    return (total + chunk - 1) / chunk;
+}
+
+struct NormLayout : Layout {
+    size_t w, b;
+    NormLayout(int64_t total, int64_t width)
+    {
+        const size_t part = 4 * (size_t)norm_chunks(total) * (size_t)width;
+        w = take(part);
+        b = take(part);
+    }
+};
+
+canon_status_t norm_args(const canon_norm_t* c, bool grad, NormArgs* a)
+{
+    if (c == nullptr) return CANON_EINVAL;
+    if (c->seqs < 0 || c->rows < 0 || c->width < 0 || !is_dtype(c->dtype) ||
+        (c->param_dtype != c->dtype && c->param_dtype != CANON_F32))
+        return CANON_EINVAL;
+    if (!norm_sizes_ok(c->seqs, c->rows, c->width)) return CANON_EUNSUPPORTED;
+    *a = NormArgs{};
+    a->total = (int32_t)(c->seqs * c->rows);
+    a->rows = (int32_t)c->rows;
+    a->width = (int32_t)c->width;
+    if (c->width > 0 && c->weight == nullptr) return CANON_EINVAL;
+    if (grad && c->width > 0 && c->dweight == nullptr) return CANON_EINVAL;
+    if (a->total > 0 && a->width > 0) {
+        auto out_ok = [&](const canon_rows_t& r) {
+            return out_valid(r, c->width, c->seqs, c->rows);
+        };
+        if (!rows_valid(c->x)) return CANON_EINVAL;
+        if (!grad) {
+            const bool res = c->residual.p != nullptr, sum = c->sum.p != nullptr;
+            if ((res && !rows_valid(c->residual)) || !out_ok(c->out) ||
+                (sum && (!res || !out_ok(c->sum) || c->sum.p == c->out.p)))
+                return CANON_EINVAL;
+            for (const canon_rows_t* in : {&c->x, &c->residual})
+                if (!in_place_ok(c->out, *in) || (sum && !in_place_ok(c->sum, *in)))
+                    return CANON_EINVAL;
+        } else {
+            if (!rows_valid(c->dout) || !out_ok(c->dx) || c->stats == nullptr ||
+                (c->dsum.p != nullptr && !rows_valid(c->dsum)) || c->dx.p == c->x.p ||
+                !in_place_ok(c->dx, c->dout) || !in_place_ok(c->dx, c->dsum))
+                return CANON_EINVAL;
+        }
+    }
+    a->inv_width = a->width > 0 ? 1.f / (float)a->width : 0.f;
+    a->eps = (float)c->eps;
+    a->x = c->x;
+    a->weight = c->weight;
+    a->stats = c->stats;
+    if (!grad) {
+        a->residual = c->residual;
+        a->sum = c->sum;
+        a->out = c->out;
+        a->bias = c->bias;
+        return CANON_OK;
+    }
+    a->dout = c->dout;
+    a->dsum = c->dsum;
+    a->dx = c->dx;
+    a->dweight = c->dweight;
+    a->dbias = c->dbias;
+    if (!mul_fits(norm_chunks(a->total), (c->width + 1023) / 1024, kMaxGrid256 - 1))
+        return CANON_EUNSUPPORTED;
+    return CANON_OK;
+}
+
+template <class F>
+canon_status_t with_params(int64_t dtype, int64_t param, F&& f)
+{
+    switch (dtype) {
+        case CANON_F32: return f(F32{}, F32{});
+        case CANON_BF16: return param == CANON_F32 ? f(BF16{}, F32{}) : f(BF16{}, BF16{});
+        case CANON_F16: return param == CANON_F32 ? f(F16{}, F32{}) : f(F16{}, F16{});
+        default: return CANON_EINVAL;
+    }
+}
+
+}  // namespace
+
+extern "C" {
+
+int canon_layer_version(void) { return CANON_LAYER_VERSION; }
+
+canon_status_t canon_layer_norm(const canon_norm_t* c, void* stream)
+{
+    NormArgs a;
+    if (canon_status_t s = norm_args(c, false, &a)) return s;
+    if (a.total == 0 || a.width == 0) return CANON_OK;
+    return with_params(c->dtype, c->param_dtype, [&](auto t, auto p) {
+        return hip_status(launch_layer_norm<decltype(t), decltype(p)>(
+            a, static_cast<hipStream_t>(stream)));
+    });
+}
+
+size_t canon_layer_norm_grad_workspace_bytes(size_t seqs, size_t rows, size_t width)
+{
+    if (seqs >= (size_t)kMaxRows || rows >= (size_t)kMaxRows || width >= ((size_t)1 << 24) ||
+        !norm_sizes_ok((int64_t)seqs, (int64_t)rows, (int64_t)width))
+        return 0;
+    return NormLayout((int64_t)(seqs * rows), (int64_t)width).bytes;
+}
+
+canon_status_t canon_layer_norm_grad(const canon_norm_t* c, void* ws, size_t ws_bytes,
+                                     void* stream)
+{
+    NormArgs a;
+    if (canon_status_t s = norm_args(c, true, &a)) return s;
+    if (a.width == 0) return CANON_OK;
+    const NormLayout l(a.total, a.width);
+    if (canon_status_t s = check_ws(ws, ws_bytes, l.bytes)) return s;
+    a.ws_w = l.at<float>(ws, l.w);
+    a.ws_b = l.at<float>(ws, l.b);
+    return with_params(c->dtype, c->param_dtype, [&](auto t, auto p) {
+        return hip_status(launch_layer_norm_grad<decltype(t), decltype(p)>(
+            a, static_cast<hipStream_t>(stream)));
+    });
+}
+
+}  // extern "C"

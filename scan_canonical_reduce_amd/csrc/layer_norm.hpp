@@ -1,0 +1,41 @@
+// Launchers of the layer norm (internal).
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "seq_device.hpp"
+
+namespace canon {
+namespace seq {
+
+struct NormArgs {
+    int32_t total, rows;  // rows of all sequences, of one
+    int32_t width;
+    float inv_width, eps;
+    canon_rows_t x, residual, sum, out;
+    const void *weight, *bias;
+    float* stats;
+    // backward
+    canon_rows_t dout, dsum, dx;
+    float *dweight, *dbias;
+    float *ws_w, *ws_b;  // per chunk of rows: width
+};
+
+// Rows of a chunk of the sums over rows: as many chunks as fill the chip twice,
+// then longer ones, whose partial sums are at most a 24th of the rows' bytes.
+constexpr int64_t kNormChunks = 512;
+constexpr int64_t kNormChunkMost = 64;
+inline int64_t norm_chunk(int64_t total)
+{
+    const int64_t n = (total + kNormChunks - 1) / kNormChunks;
+    return n < 1 ? 1 : n > kNormChunkMost ? kNormChunkMost : n;
+}
+
+template <typename T, typename P>
+hipError_t launch_layer_norm(const NormArgs& a, hipStream_t st);
+template <typename T, typename P>
+hipError_t launch_layer_norm_grad(const NormArgs& a, hipStream_t st);
+
+}  // namespace seq
+}  // namespace canon

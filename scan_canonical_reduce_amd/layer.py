@@ -1,0 +1,145 @@
+"""Operators of a recurrent language model's layers: layer norm with the residual
+sum, the gated linear recurrence, and sampling of the next token.
+
+Argument marshalling only, as in the package itself; the C ABI is declared in
+``include/canon_layer.h``, which states what each operator computes.  Shapes,
+types, streams and workspaces are those of the sequence operators (``seq.py``).
+"""
+from __future__ import annotations
+
+import ctypes
+import struct
+from typing import NamedTuple, Optional
+
+import torch
+
+from . import CanonError, lib
+from .seq import DTYPES, _NONE, _call, _dtype, _flat, _rows, _same, _workspace
+
+LAYER_VERSION = 1
+
+LAYER_EXPORTS = [
+    "canon_layer_version", "canon_layer_norm", "canon_layer_norm_grad_workspace_bytes",
+    "canon_layer_norm_grad",
+]
+
+# canon_norm_t: fields of 8 bytes, eps a double
+NORM = struct.Struct("=5qd26q")
+
+_layer = None
+
+
+def _lib() -> ctypes.CDLL:
+    global _layer
+    if _layer is not None:
+        return _layer
+    L = lib()
+    S, I, P = ctypes.c_size_t, ctypes.c_int, ctypes.c_void_p
+    for name in LAYER_EXPORTS:
+        f = getattr(L, name)
+        f.restype = S if name.endswith("_bytes") or name.endswith("_states") else I
+    L.canon_layer_norm.argtypes = [P, P]
+    L.canon_layer_norm_grad_workspace_bytes.argtypes = [S, S, S]
+    L.canon_layer_norm_grad.argtypes = [P, P, S, P]
+    if L.canon_layer_version() != LAYER_VERSION:
+        raise CanonError("libcanon layer operators: version mismatch")
+    _layer = L
+    return L
+
+
+# ------------------------------------------------------------------ layer norm
+class LayerNormGrads(NamedTuple):
+    dx: torch.Tensor
+    dweight: torch.Tensor
+    dbias: Optional[torch.Tensor]
+
+
+def _norm(what, x, weight, bias):
+    """(dtype, param_dtype, seqs, rows, width), leading dimensions, (weight, bias)"""
+    d = _dtype(x, what)
+    if x.dim() not in (2, 3):
+        raise ValueError(f"{what} takes [rows, width] or [sequences, rows, width]")
+    width = x.shape[-1]
+    if weight.dtype != x.dtype and weight.dtype != torch.float32:
+        raise TypeError(f"{what}: weight must be {x.dtype} or float32, not {weight.dtype}")
+    seqs = x.shape[0] if x.dim() == 3 else 1
+    head = (d, DTYPES[weight.dtype], seqs, x.shape[-2], width)
+    return head, x.dim() - 1, (_flat(what, "weight", weight, (width,), weight.dtype),
+                               _flat(what, "bias", bias, (width,), weight.dtype))
+
+
+def layer_norm_stats(x: torch.Tensor) -> torch.Tensor:
+    """An uninitialised buffer for the `stats` of layer_norm of x: each row's mean
+    and 1 / standard deviation, for the backward pass."""
+    return torch.empty(x.shape[:-1] + (2,), dtype=torch.float32, device=x.device)
+
+
+def _layer_norm(what, x, residual, weight, bias, eps, stats, total, out):
+    _same(what, x.device, residual, weight, bias, stats, total, out)
+    head, lead, params = _norm(what, x, weight, bias)
+    shape, dtype = x.shape, x.dtype
+    if out is None:
+        out = x.new_empty(shape)
+    c = NORM.pack(*head, eps, *_rows(what, "x", x, shape, dtype, lead),
+                  *(_NONE if residual is None else
+                    _rows(what, "residual", residual, shape, dtype, lead)),
+                  *(_NONE if total is None else _rows(what, "sum_out", total, shape, dtype, lead)),
+                  *_rows(what, "out", out, shape, dtype, lead), *params,
+                  _flat(what, "stats", stats, shape[:-1] + (2,), torch.float32),
+                  *_NONE, *_NONE, *_NONE, 0, 0)
+    _call(what, x.device, _lib().canon_layer_norm, c)
+    return out
+
+
+def layer_norm(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Tensor] = None,
+               eps: float = 1e-5, stats: Optional[torch.Tensor] = None,
+               out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Each row of x ([rows, width] or [sequences, rows, width], any row and sequence
+    strides) less its mean, over its standard deviation, times weight, plus bias
+    (float32 or x's type).  stats: a buffer of layer_norm_stats that is written for
+    layer_norm_grad.  out may be x."""
+    return _layer_norm("layer_norm", x, None, weight, bias, eps, stats, None, out)
+
+
+def add_layer_norm(x: torch.Tensor, residual: torch.Tensor, weight: torch.Tensor,
+                   bias: Optional[torch.Tensor] = None, eps: float = 1e-5,
+                   stats: Optional[torch.Tensor] = None, sum_out: Optional[torch.Tensor] = None,
+                   out: Optional[torch.Tensor] = None) -> tuple[torch.Tensor, torch.Tensor]:
+    """(layer_norm(s, ...), s) with s = x + residual, rounded to their type, in one
+    pass.  sum_out and out may each be x or residual (not the same one)."""
+    if sum_out is None:
+        sum_out = x.new_empty(x.shape)
+    return _layer_norm("add_layer_norm", x, residual, weight, bias, eps, stats, sum_out,
+                       out), sum_out
+
+
+def layer_norm_grad_workspace_bytes(seqs: int, rows: int, width: int) -> int:
+    return _lib().canon_layer_norm_grad_workspace_bytes(seqs, rows, width)
+
+
+def layer_norm_grad(dout: torch.Tensor, x: torch.Tensor, weight: torch.Tensor,
+                    stats: torch.Tensor, bias: Optional[torch.Tensor] = None,
+                    dsum: Optional[torch.Tensor] = None, dx: Optional[torch.Tensor] = None,
+                    ws: Optional[torch.Tensor] = None) -> LayerNormGrads:
+    """Gradients of layer_norm's inputs, given the `stats` that its call wrote; of
+    add_layer_norm's with x = its sum, whose own gradient dsum is added (dx is then
+    the gradient of both addends).  dweight and dbias (with bias) are float32.  dx may
+    be dout or dsum."""
+    what = "layer_norm_grad"
+    _same(what, x.device, dout, weight, stats, bias, dsum, dx, ws)
+    head, lead, params = _norm(what, x, weight, bias)
+    shape, dtype, device = x.shape, x.dtype, x.device
+    if dx is None:
+        dx = x.new_empty(shape)
+    dw = torch.empty(head[4], dtype=torch.float32, device=device)
+    db = None if bias is None else torch.empty(head[4], dtype=torch.float32, device=device)
+    c = NORM.pack(*head, 0.0, *_rows(what, "x", x, shape, dtype, lead), *_NONE, *_NONE, *_NONE,
+                  *params, _flat(what, "stats", stats, shape[:-1] + (2,), torch.float32),
+                  *_rows(what, "dout", dout, shape, dtype, lead),
+                  *(_NONE if dsum is None else _rows(what, "dsum", dsum, shape, dtype, lead)),
+                  *_rows(what, "dx", dx, shape, dtype, lead), dw.data_ptr(),
+                  0 if db is None else db.data_ptr())
+    L = _lib()
+    w = _workspace(L.canon_layer_norm_grad_workspace_bytes(*head[2:5]), device, ws)
+    _call(what, device, L.canon_layer_norm_grad, c, w.data_ptr(), w.numel())
+    return LayerNormGrads(dx, dw, db)
