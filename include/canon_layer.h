@@ -1,7 +1,7 @@
 /*
  * canon_layer.h — operators of a recurrent language model's layers on AMD MI355X
- * (gfx950), beside those of canon_seq.h: layer norm with the residual sum.  Part
- * of libcanon.
+ * (gfx950), beside those of canon_seq.h: layer norm with the residual sum, and
+ * the gated linear recurrence.  Part of libcanon.
  *
  * What is computed:
  *
@@ -12,13 +12,26 @@
  *                    dx = r (g - mean(g) - n mean(g n)) + dsum (the gradient that
  *                    reaches s itself; of both x and residual),
  *                    dweight = sum dout n, dbias = sum dout, over the rows.
+ *   gated_recurrence r = sigmoid(gate), i = sigmoid(input_gate) or 1,
+ *                    a = exp(-decay r), c = sqrt(1 - a^2), or, without decay,
+ *                    a = r, c = 1 - r;
+ *                    h[t,d] = a h[t-1,d] + c i x[t,d], out = h.
+ *                    Gradients are the formula's; where c is 0 (an a of 1), the
+ *                    slope of the square root counts as 0.
  *
- * Everything is computed in 32 bits and rounded once where it is stored.  Each sum is
- * one fixed expression of the shapes, so each call is reproducible bit for bit.  In
- * particular:
+ * Everything is computed in 32 bits and rounded once where it is stored, but for
+ * the recurrence's carried state, in 64.  Each sum is one fixed expression of the
+ * shapes, so each call is reproducible bit for bit.  In particular:
  *   - a row's norm depends on its width, type and values alone, not on the rows
  *     around it, strides or alignment;
- *   - sums over rows (dweight, dbias) go by chunks of rows and then over the
+ *   - the recurrence is evaluated in chunks of CANON_RECUR_CHUNK rows from the
+ *     sequence's first row: inside a chunk h folds from the chunk's start state, and
+ *     the next chunk starts from P H + S, P the product of the a and S the chunk's
+ *     fold from zero; the same way over blocks of CANON_RECUR_BLOCK rows.  So a
+ *     sequence's outputs do not depend on the other sequences, on packing or on how
+ *     the work is spread, and cutting a sequence at a multiple of CANON_RECUR_BLOCK
+ *     rows and passing the state on changes no bit;
+ *   - sums over rows (dweight, dbias, ddecay) go by chunks of rows and then over the
  *     chunks as the convolution's of canon_seq.h.
  *
  * Conventions are those of canon_seq.h: canon_rows_t, dtype, sequences and starts,
@@ -67,6 +80,53 @@ canon_status_t canon_layer_norm(const canon_norm_t* c, void* stream);
 size_t canon_layer_norm_grad_workspace_bytes(size_t seqs, size_t rows, size_t width);
 canon_status_t canon_layer_norm_grad(const canon_norm_t* c, void* ws, size_t ws_bytes,
                                      void* stream);
+
+/* ------------------------------------------------- gated linear recurrence */
+#define CANON_RECUR_CHUNK 16
+#define CANON_RECUR_BLOCK 512
+
+typedef struct {
+    int64_t dtype; /* canon_dtype_t of the canon_rows_t below */
+    int64_t seqs, rows, channels;
+    const int32_t* starts;
+    canon_rows_t x, gate, input_gate, out; /* input_gate.p may be NULL (i = 1) */
+    const float* decay;      /* channels, not negative, or NULL (a = sigmoid(gate)) */
+    const float* init_state; /* seqs x channels, or NULL (zero) */
+    float* final_state;      /* the same shape, or NULL */
+    float* kept_states;      /* canon_gated_recurrence_states(...) elements that the
+                                forward pass writes for the backward pass, or NULL */
+    /* backward */
+    canon_rows_t dout, dx, dgate, dinput_gate; /* dinput_gate with input_gate */
+    float* ddecay;               /* channels, with decay */
+    const float* d_final_state;  /* or NULL (zero) */
+    float* d_init_state;         /* or NULL */
+} canon_recur_t;
+
+/* Reads x, gate, input_gate, decay, init_state; writes out, final_state (which may be
+ * init_state's buffer), kept_states.  out may be the buffer of none of the inputs.  An
+ * x, gate or input_gate that is not finite can leave its channel's outputs from that
+ * row on not finite (a gate of minus or plus infinity is its limit, and one that
+ * makes c zero shuts out finite x only).
+ * Limits (CANON_EUNSUPPORTED): those of canon_seq.h on seqs, rows and channels;
+ * blocks (seqs ceil(rows / CANON_RECUR_BLOCK), packed seqs + rows /
+ * CANON_RECUR_BLOCK, single rows seqs) times ceil(channels / 64) below 2^22. */
+size_t canon_gated_recurrence_states(size_t seqs, size_t rows, int packed, size_t channels);
+size_t canon_gated_recurrence_workspace_bytes(size_t seqs, size_t rows, int packed,
+                                              size_t channels);
+canon_status_t canon_gated_recurrence(const canon_recur_t* c, void* ws, size_t ws_bytes,
+                                      void* stream);
+
+/* Reads the forward pass's inputs (without init_state), its kept_states, dout and
+ * d_final_state; writes dx, dgate, dinput_gate, ddecay, d_init_state.  No output may be
+ * an input's buffer. */
+size_t canon_gated_recurrence_grad_workspace_bytes(size_t seqs, size_t rows, int packed,
+                                                   size_t channels);
+canon_status_t canon_gated_recurrence_grad(const canon_recur_t* c, void* ws, size_t ws_bytes,
+                                           void* stream);
+
+/* One row of each of `seqs` sequences (rows is ignored; canon_rows_t.seq apart): h from
+ * init_state (NULL: zero), written to final_state, which may be the same buffer. */
+canon_status_t canon_gated_recurrence_step(const canon_recur_t* c, void* stream);
 
 #ifdef __cplusplus
 }

@@ -525,5 +525,7 @@ from .seq import (  # noqa: E402
     selective_scan_grad_workspace_bytes, selective_scan_states, selective_scan_step,
     selective_scan_workspace_bytes)
 from .layer import (  # noqa: E402
-    LayerNormGrads, add_layer_norm, layer_norm, layer_norm_grad, layer_norm_grad_workspace_bytes,
-    layer_norm_stats)
+    GatedRecurrenceGrads, LayerNormGrads, add_layer_norm, gated_recurrence, gated_recurrence_grad,
+    gated_recurrence_grad_workspace_bytes, gated_recurrence_states, gated_recurrence_step,
+    gated_recurrence_workspace_bytes, layer_norm, layer_norm_grad,
+    layer_norm_grad_workspace_bytes, layer_norm_stats)

@@ -2,6 +2,7 @@
 // layout, dispatch on the element type.
 #include "../../include/canon_layer.h"
 #include "layer_norm.hpp"
+#include "recurrence.hpp"
 #include "seq_args.hpp"
 
 using namespace canon;
@@ -110,6 +111,93 @@ canon_status_t with_params(int64_t dtype, int64_t param, F&& f)
     }
 }
 
+// ----------------------------------------------------------------- recurrence
+struct RecurLayout : Layout {
+    size_t q = 0, s = 0, h = 0, dd = 0;
+    bool carried;  // some sequence may have more than one block
+    RecurLayout(int64_t seqs, int64_t rows, bool packed, int64_t channels, bool grad)
+        : carried(rows > CANON_RECUR_BLOCK && seqs > 0)
+    {
+        const size_t n =
+            4 * (size_t)slot_count<CANON_RECUR_BLOCK>(seqs, rows, packed) * (size_t)channels;
+        if (carried) {
+            q = take(n);
+            s = take(n);
+            h = take(n);
+        }
+        if (grad) dd = take(n);
+    }
+    void place(RecurArgs* a, void* ws) const
+    {
+        if (!carried) return;
+        a->ws_q = at<float>(ws, q);
+        a->ws_s = at<float>(ws, s);
+        a->ws_h = at<float>(ws, h);
+    }
+};
+
+bool recur_query_ok(size_t seqs, size_t rows, size_t channels)
+{
+    return seqs < (size_t)kMaxRows && rows < (size_t)kMaxRows && channels < ((size_t)1 << 24);
+}
+
+canon_status_t recur_args(const canon_recur_t* c, bool step, bool grad, RecurArgs* a)
+{
+    if (c == nullptr) return CANON_EINVAL;
+    const bool packed = c->starts != nullptr, input = c->input_gate.p != nullptr;
+    if (step && packed) return CANON_EINVAL;
+    const int64_t rows = step ? 1 : c->rows, out_seqs = packed ? 1 : c->seqs;
+    if (canon_status_t s = seq_sizes(c->seqs, rows, c->channels, packed)) return s;
+    if (!is_dtype(c->dtype)) return CANON_EINVAL;
+    auto out_ok = [&](const canon_rows_t& r) { return out_valid(r, c->channels, out_seqs, rows); };
+    if (c->seqs > 0 && rows > 0 && c->channels > 0) {
+        if (!rows_valid(c->x) || !rows_valid(c->gate) || (input && !rows_valid(c->input_gate)))
+            return CANON_EINVAL;
+        const canon_rows_t* in[] = {&c->x, &c->gate, &c->input_gate, &c->dout};
+        const canon_rows_t* out[] = {grad ? &c->dx : &c->out, &c->dgate, &c->dinput_gate};
+        const int outs = !grad ? 1 : input ? 3 : 2, ins = grad ? 4 : 3;
+        if (grad && (!rows_valid(c->dout) || c->kept_states == nullptr)) return CANON_EINVAL;
+        for (int o = 0; o < outs; ++o) {
+            if (!out_ok(*out[o])) return CANON_EINVAL;
+            // rows are read again by other workgroups, or by a second pass
+            for (int i = 0; i < ins && !step; ++i)
+                if (out[o]->p == in[i]->p) return CANON_EINVAL;
+            for (int p = 0; p < o; ++p)
+                if (out[o]->p == out[p]->p) return CANON_EINVAL;
+        }
+    }
+    if (grad && c->channels > 0 && (c->ddecay == nullptr) != (c->decay == nullptr))
+        return CANON_EINVAL;
+    if (grad && c->d_init_state != nullptr && c->d_init_state == c->d_final_state)
+        return CANON_EINVAL;
+    *a = RecurArgs{};
+    a->q = Seqs{c->seqs, rows, c->starts};
+    a->x = c->x;
+    a->gate = c->gate;
+    a->input = c->input_gate;
+    a->decay = c->decay;
+    a->channels = (int32_t)c->channels;
+    a->slabs = (a->channels + 63) / 64;
+    a->kept = c->kept_states;
+    if (!grad) {
+        a->out = c->out;
+        a->init = c->init_state;
+        a->final = c->final_state;
+    } else {
+        a->dout = c->dout;
+        a->dx = c->dx;
+        a->dgate = c->dgate;
+        a->dinput = c->dinput_gate;
+        a->ddecay = c->ddecay;
+        a->dfinal = c->d_final_state;
+        a->dinit = c->d_init_state;
+    }
+    const int64_t slots =
+        step ? c->seqs : slot_count<CANON_RECUR_BLOCK>(c->seqs, rows, packed);
+    if (!mul_fits(slots, a->slabs, ((int64_t)1 << 22) - 1)) return CANON_EUNSUPPORTED;
+    return CANON_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -148,6 +236,66 @@ canon_status_t canon_layer_norm_grad(const canon_norm_t* c, void* ws, size_t ws_
     return with_params(c->dtype, c->param_dtype, [&](auto t, auto p) {
         return hip_status(launch_layer_norm_grad<decltype(t), decltype(p)>(
             a, static_cast<hipStream_t>(stream)));
+    });
+}
+
+size_t canon_gated_recurrence_states(size_t seqs, size_t rows, int packed, size_t channels)
+{
+    if (!recur_query_ok(seqs, rows, channels)) return 0;
+    return (size_t)slot_count<CANON_RECUR_BLOCK>((int64_t)seqs, (int64_t)rows, packed != 0) *
+           kRecurRounds * channels;
+}
+
+size_t canon_gated_recurrence_workspace_bytes(size_t seqs, size_t rows, int packed,
+                                              size_t channels)
+{
+    if (!recur_query_ok(seqs, rows, channels)) return 0;
+    return RecurLayout((int64_t)seqs, (int64_t)rows, packed != 0, (int64_t)channels, false).bytes;
+}
+
+canon_status_t canon_gated_recurrence(const canon_recur_t* c, void* ws, size_t ws_bytes,
+                                      void* stream)
+{
+    RecurArgs a;
+    if (canon_status_t s = recur_args(c, false, false, &a)) return s;
+    if (a.q.seqs == 0 || a.channels == 0) return CANON_OK;
+    const RecurLayout l(a.q.seqs, a.q.rows, a.q.starts != nullptr, a.channels, false);
+    if (canon_status_t s = check_ws(ws, ws_bytes, l.bytes)) return s;
+    l.place(&a, ws);
+    return with_dtype(c->dtype, [&](auto t) {
+        return hip_status(launch_recurrence<decltype(t)>(a, static_cast<hipStream_t>(stream)));
+    });
+}
+
+size_t canon_gated_recurrence_grad_workspace_bytes(size_t seqs, size_t rows, int packed,
+                                                   size_t channels)
+{
+    if (!recur_query_ok(seqs, rows, channels)) return 0;
+    return RecurLayout((int64_t)seqs, (int64_t)rows, packed != 0, (int64_t)channels, true).bytes;
+}
+
+canon_status_t canon_gated_recurrence_grad(const canon_recur_t* c, void* ws, size_t ws_bytes,
+                                           void* stream)
+{
+    RecurArgs a;
+    if (canon_status_t s = recur_args(c, false, true, &a)) return s;
+    if (a.channels == 0) return CANON_OK;
+    const RecurLayout l(a.q.seqs, a.q.rows, a.q.starts != nullptr, a.channels, true);
+    if (canon_status_t s = check_ws(ws, ws_bytes, l.bytes)) return s;
+    l.place(&a, ws);
+    a.ws_dd = l.at<float>(ws, l.dd);
+    return with_dtype(c->dtype, [&](auto t) {
+        return hip_status(launch_recurrence_grad<decltype(t)>(a, static_cast<hipStream_t>(stream)));
+    });
+}
+
+canon_status_t canon_gated_recurrence_step(const canon_recur_t* c, void* stream)
+{
+    RecurArgs a;
+    if (canon_status_t s = recur_args(c, true, false, &a)) return s;
+    if (a.q.seqs == 0 || a.channels == 0) return CANON_OK;
+    return with_dtype(c->dtype, [&](auto t) {
+        return hip_status(launch_recurrence_step<decltype(t)>(a, static_cast<hipStream_t>(stream)));
     });
 }
 

@@ -1,0 +1,39 @@
+// Launchers of the gated linear recurrence (internal).
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "../../include/canon_layer.h"
+#include "seq_device.hpp"
+
+namespace canon {
+namespace seq {
+
+constexpr int kRecurWaves = 8;                                // chunks of a round
+constexpr int kRecurRound = kRecurWaves * CANON_RECUR_CHUNK;  // rows between kept states
+constexpr int kRecurRounds = CANON_RECUR_BLOCK / kRecurRound;
+
+struct RecurArgs {
+    Seqs q;
+    canon_rows_t x, gate, input, out;
+    const float *decay, *init;
+    float *final, *kept;  // kept: per slot, kRecurRounds x channels
+    int32_t channels, slabs;
+    float *ws_q, *ws_s, *ws_h;  // per slot: channels; NULL where no sequence has two blocks
+    // backward
+    canon_rows_t dout, dx, dgate, dinput;
+    float *ddecay, *dinit;
+    const float* dfinal;
+    float* ws_dd;  // per slot: channels
+};
+
+template <typename T>
+hipError_t launch_recurrence(const RecurArgs& a, hipStream_t st);
+template <typename T>
+hipError_t launch_recurrence_grad(const RecurArgs& a, hipStream_t st);
+template <typename T>
+hipError_t launch_recurrence_step(const RecurArgs& a, hipStream_t st);
+
+}  // namespace seq
+}  // namespace canon

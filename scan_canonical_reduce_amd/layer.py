@@ -14,17 +14,22 @@ from typing import NamedTuple, Optional
 import torch
 
 from . import CanonError, lib
-from .seq import DTYPES, _NONE, _call, _dtype, _flat, _rows, _same, _workspace
+from .seq import (DTYPES, _NONE, _call, _dtype, _flat, _rows, _same, _sequences, _step_rows,
+                  _workspace)
 
 LAYER_VERSION = 1
 
 LAYER_EXPORTS = [
     "canon_layer_version", "canon_layer_norm", "canon_layer_norm_grad_workspace_bytes",
-    "canon_layer_norm_grad",
+    "canon_layer_norm_grad", "canon_gated_recurrence_states",
+    "canon_gated_recurrence_workspace_bytes", "canon_gated_recurrence",
+    "canon_gated_recurrence_grad_workspace_bytes", "canon_gated_recurrence_grad",
+    "canon_gated_recurrence_step",
 ]
 
-# canon_norm_t: fields of 8 bytes, eps a double
+# canon_norm_t (eps a double) and canon_recur_t: fields of 8 bytes
 NORM = struct.Struct("=5qd26q")
+RECUR = struct.Struct("=36q")
 
 _layer = None
 
@@ -41,6 +46,12 @@ def _lib() -> ctypes.CDLL:
     L.canon_layer_norm.argtypes = [P, P]
     L.canon_layer_norm_grad_workspace_bytes.argtypes = [S, S, S]
     L.canon_layer_norm_grad.argtypes = [P, P, S, P]
+    L.canon_gated_recurrence_states.argtypes = [S, S, I, S]
+    L.canon_gated_recurrence_workspace_bytes.argtypes = [S, S, I, S]
+    L.canon_gated_recurrence.argtypes = [P, P, S, P]
+    L.canon_gated_recurrence_grad_workspace_bytes.argtypes = [S, S, I, S]
+    L.canon_gated_recurrence_grad.argtypes = [P, P, S, P]
+    L.canon_gated_recurrence_step.argtypes = [P, P]
     if L.canon_layer_version() != LAYER_VERSION:
         raise CanonError("libcanon layer operators: version mismatch")
     _layer = L
@@ -143,3 +154,150 @@ def layer_norm_grad(dout: torch.Tensor, x: torch.Tensor, weight: torch.Tensor,
     w = _workspace(L.canon_layer_norm_grad_workspace_bytes(*head[2:5]), device, ws)
     _call(what, device, L.canon_layer_norm_grad, c, w.data_ptr(), w.numel())
     return LayerNormGrads(dx, dw, db)
+
+
+# ------------------------------------------------------ gated linear recurrence
+class GatedRecurrenceGrads(NamedTuple):
+    dx: torch.Tensor
+    dgate: torch.Tensor
+    ddecay: Optional[torch.Tensor]
+    dinput_gate: Optional[torch.Tensor]
+    dinit_state: torch.Tensor
+
+
+def gated_recurrence_workspace_bytes(seqs: int, rows: int, packed: bool, channels: int) -> int:
+    return _lib().canon_gated_recurrence_workspace_bytes(seqs, rows, int(packed), channels)
+
+
+def gated_recurrence_grad_workspace_bytes(seqs: int, rows: int, packed: bool,
+                                          channels: int) -> int:
+    return _lib().canon_gated_recurrence_grad_workspace_bytes(seqs, rows, int(packed), channels)
+
+
+def gated_recurrence_states(x: torch.Tensor,
+                            starts: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """An uninitialised buffer for gated_recurrence's `states` argument: what the
+    forward pass of x saves for the backward pass (4 bytes per 128 elements of x)."""
+    seqs, rows, _, lead = _sequences("gated_recurrence_states", x, starts)
+    n = _lib().canon_gated_recurrence_states(seqs, rows, int(lead == 1), x.shape[-1])
+    return torch.empty(n, dtype=torch.float32, device=x.device)
+
+
+def gated_recurrence(x: torch.Tensor, gate: torch.Tensor, decay: Optional[torch.Tensor] = None,
+                     input_gate: Optional[torch.Tensor] = None,
+                     starts: Optional[torch.Tensor] = None,
+                     init_state: Optional[torch.Tensor] = None,
+                     final_state: Optional[torch.Tensor] = None,
+                     states: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+                     ws: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """h[t] = a h[t-1] + c i x[t] over the rows of each sequence, channel by channel:
+    a = exp(-decay sigmoid(gate)) and c = sqrt(1 - a^2), or without decay
+    a = sigmoid(gate) and c = 1 - a; i = sigmoid(input_gate), or 1 without.
+
+    x, gate, input_gate: activations of one shape; decay [channels] float32, not
+    negative.  init_state, final_state [sequences, channels] float32: h before the
+    first row and after the last (written, and may be init_state).  states: a buffer of
+    gated_recurrence_states for the backward pass."""
+    what = "gated_recurrence"
+    _same(what, x.device, gate, decay, input_gate, starts, init_state, final_state, states, out, ws)
+    seqs, rows, sp, lead = _sequences(what, x, starts)
+    shape, dtype, f32, channels = x.shape, x.dtype, torch.float32, x.shape[-1]
+    packed = int(lead == 1)
+    L = _lib()
+    kept = 0
+    if states is not None:
+        kept = _flat(what, "states", states,
+                     (L.canon_gated_recurrence_states(seqs, rows, packed, channels),), f32)
+    d = _dtype(x, what)
+    if out is None:
+        out = x.new_empty(shape)
+    state = (seqs, channels)
+    c = RECUR.pack(d, seqs, rows, channels, sp, *_rows(what, "x", x, shape, dtype, lead),
+                   *_rows(what, "gate", gate, shape, dtype, lead),
+                   *(_NONE if input_gate is None else
+                     _rows(what, "input_gate", input_gate, shape, dtype, lead)),
+                   *_rows(what, "out", out, shape, dtype, lead),
+                   _flat(what, "decay", decay, (channels,), f32),
+                   _flat(what, "init_state", init_state, state, f32),
+                   _flat(what, "final_state", final_state, state, f32), kept,
+                   *_NONE, *_NONE, *_NONE, *_NONE, 0, 0, 0)
+    w = _workspace(L.canon_gated_recurrence_workspace_bytes(seqs, rows, packed, channels),
+                   x.device, ws)
+    _call(what, x.device, L.canon_gated_recurrence, c, w.data_ptr(), w.numel())
+    return out
+
+
+def gated_recurrence_grad(dout: torch.Tensor, x: torch.Tensor, gate: torch.Tensor,
+                          states: torch.Tensor, decay: Optional[torch.Tensor] = None,
+                          input_gate: Optional[torch.Tensor] = None,
+                          starts: Optional[torch.Tensor] = None,
+                          d_final_state: Optional[torch.Tensor] = None,
+                          ws: Optional[torch.Tensor] = None) -> GatedRecurrenceGrads:
+    """Gradients of gated_recurrence's inputs, given the `states` that its call with
+    these inputs wrote, and the gradients of its output and (optionally) final state.
+    Activations' gradients have their type, the others are float32; rows that belong to
+    no sequence have undefined gradients."""
+    what = "gated_recurrence_grad"
+    _same(what, x.device, dout, gate, states, decay, input_gate, starts, d_final_state, ws)
+    seqs, rows, sp, lead = _sequences(what, x, starts)
+    shape, dtype, f32, channels = x.shape, x.dtype, torch.float32, x.shape[-1]
+    packed, device = int(lead == 1), x.device
+    L = _lib()
+    size = L.canon_gated_recurrence_states(seqs, rows, packed, channels)
+    d = _dtype(x, what)
+
+    def empty(*s):
+        return torch.empty(s, dtype=f32, device=device)
+
+    g = GatedRecurrenceGrads(
+        dx=x.new_empty(shape), dgate=x.new_empty(shape),
+        ddecay=None if decay is None else empty(channels),
+        dinput_gate=None if input_gate is None else x.new_empty(shape),
+        dinit_state=empty(seqs, channels))
+    gi = _NONE, _NONE
+    if input_gate is not None:
+        gi = (_rows(what, "input_gate", input_gate, shape, dtype, lead),
+              _rows(what, "dinput_gate", g.dinput_gate, shape, dtype, lead))
+    c = RECUR.pack(d, seqs, rows, channels, sp, *_rows(what, "x", x, shape, dtype, lead),
+                   *_rows(what, "gate", gate, shape, dtype, lead), *gi[0], *_NONE,
+                   _flat(what, "decay", decay, (channels,), f32), 0, 0,
+                   _flat(what, "states", states, (size,), f32),
+                   *_rows(what, "dout", dout, shape, dtype, lead),
+                   *_rows(what, "dx", g.dx, shape, dtype, lead),
+                   *_rows(what, "dgate", g.dgate, shape, dtype, lead), *gi[1],
+                   0 if decay is None else g.ddecay.data_ptr(),
+                   _flat(what, "d_final_state", d_final_state, (seqs, channels), f32),
+                   g.dinit_state.data_ptr())
+    w = _workspace(L.canon_gated_recurrence_grad_workspace_bytes(seqs, rows, packed, channels),
+                   device, ws)
+    _call(what, device, L.canon_gated_recurrence_grad, c, w.data_ptr(), w.numel())
+    return g
+
+
+def gated_recurrence_step(state: torch.Tensor, x: torch.Tensor, gate: torch.Tensor,
+                          decay: Optional[torch.Tensor] = None,
+                          input_gate: Optional[torch.Tensor] = None,
+                          out_state: Optional[torch.Tensor] = None,
+                          out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """gated_recurrence for one row of each sequence: x, gate, input_gate [sequences,
+    channels].  The state [sequences, channels] is updated in place, or, with
+    out_state, read and written there."""
+    what = "gated_recurrence_step"
+    _same(what, x.device, state, gate, decay, input_gate, out_state, out)
+    if x.dim() != 2:
+        raise ValueError(f"{what} takes [sequences, channels]")
+    shape, dtype, f32 = x.shape, x.dtype, torch.float32
+    d = _dtype(x, what)
+    old = _flat(what, "state", state, shape, f32)
+    if out is None:
+        out = x.new_empty(shape)
+    c = RECUR.pack(d, shape[0], 1, shape[1], 0, *_step_rows(what, "x", x, shape, dtype),
+                   *_step_rows(what, "gate", gate, shape, dtype),
+                   *(_NONE if input_gate is None else
+                     _step_rows(what, "input_gate", input_gate, shape, dtype)),
+                   *_step_rows(what, "out", out, shape, dtype),
+                   _flat(what, "decay", decay, shape[1:], f32), old,
+                   old if out_state is None else _flat(what, "out_state", out_state, shape, f32),
+                   0, *_NONE, *_NONE, *_NONE, *_NONE, 0, 0, 0)
+    _call(what, x.device, _lib().canon_gated_recurrence_step, c)
+    return out

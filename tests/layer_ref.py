@@ -76,3 +76,94 @@ def norm_grad(dout, x, w, dsum, eps):
     dw = (dout * n).sum(flat)
     tw = (Dr + 3) * U * (dout * n).abs().sum(flat) + (dout.abs() * en).sum(flat)
     return (dx, tol), (dw, tw), (dout.sum(flat), Dr * U * dout.abs().sum(flat))
+
+
+# ------------------------------------------------------ gated linear recurrence
+BLOCK = 512  # rows
+
+
+def recur_parts(gate, input_gate, decay):
+    """float64: a, c, i, r, the slope -dc/d(log a), and whether a decay is given"""
+    r = torch.sigmoid(gate)
+    i = torch.ones_like(r) if input_gate is None else torch.sigmoid(input_gate)
+    if decay is None:
+        return r, torch.sigmoid(-gate), i, r, r
+    log_a = -decay * r
+    a = torch.exp(log_a)
+    c = torch.sqrt(-torch.expm1(2 * log_a))
+    return a, c, i, r, torch.where(c > 0, a * a / c.clamp(min=1e-300), torch.zeros_like(c))
+
+
+def recur(x, gate, input_gate=None, decay=None, init=None, dout=None, dfinal=None):
+    """Sequences of one length side by side, [sequences, rows, channels], in float64 on
+    the CPU: a dict of (value, bound) for out, final and, with dout, x, gate, input_gate,
+    decay, init.
+
+    Bounds, in float32 roundings U.  The sigmoid of y has a relative error of (|y| + 4) U
+    (its exponential's is |y| U and an ulp, the reciprocal's an ulp), e = a - 1 one of
+    (|gate| + 16) U, c i x one of (|gate| + |input_gate| + 26) U.  A chunk folds 16 rows
+    with two roundings each, relative to the absolute sum, and its ends go on as
+    32-bit values into a carry in 64 bits, rounded 3 times a block of 512 rows; an
+    output adds its own chunk's 32 roundings.  So with A the recurrence of absolute
+    values, an error E obeys
+      E <- a E + (48 + |gate|) U |e| A + (64 + |gate| + |input_gate|) U |c i x|."""
+    f = {k: None if v is None else v.detach().double().cpu()
+         for k, v in dict(x=x, g=gate, n=input_gate, D=decay, h=init, o=dout, F=dfinal).items()}
+    x, g, n = f["x"], f["g"], f["n"]
+    a, c, i, r, slope = recur_parts(g, n, f["D"])
+    rows = x.shape[1]
+    ng = torch.zeros_like(g) if n is None else n.abs()
+    v = c * i * x
+    ke = (48 + g.abs()) * U * (1 - a)
+    kv = (64 + g.abs() + ng) * U
+    zero = x.new_zeros(x.shape[0], x.shape[2])
+    h, A = [f["h"] if f["h"] is not None else zero], [zero if f["h"] is None else f["h"].abs()]
+    E, out, tol = zero, [], []
+    T = [E + 3 * U * A[0]]
+    for t in range(rows):
+        E = a[:, t] * E + ke[:, t] * A[t] + kv[:, t] * v[:, t].abs()
+        h.append(a[:, t] * h[t] + v[:, t])
+        A.append(a[:, t] * A[t] + v[:, t].abs())
+        if t % BLOCK == BLOCK - 1:
+            E = E + 3 * U * A[-1]
+        out.append(h[-1])
+        tol.append(E + 34 * U * A[-1])
+        T.append(E + 34 * U * A[-1])
+    res = {"out": (torch.stack(out, 1), torch.stack(tol, 1)) if rows else (x, x),
+           "final": (h[-1], E + 4 * U * A[-1])}
+    if f["o"] is None:
+        return res
+    dout = f["o"]
+    h, A, T = (torch.stack(q, 1) for q in (h, A, T))
+    R = f["F"] if f["F"] is not None else zero  # what comes in past row t
+    absR, E = R.abs(), zero
+    lam, L, TL = (torch.zeros_like(x) for _ in range(3))
+    for t in range(rows - 1, -1, -1):
+        lam[:, t] = dout[:, t] + R
+        L[:, t] = dout[:, t].abs() + absR
+        TL[:, t] = E + 34 * U * L[:, t]
+        E = a[:, t] * (E + 34 * U * dout[:, t].abs()) + ke[:, t] * L[:, t]
+        R, absR = a[:, t] * lam[:, t], a[:, t] * L[:, t]
+        if t % BLOCK == 0:
+            E = E + 3 * U * absR
+    res["init"] = (R, E + 4 * U * absR)
+    res["x"] = (lam * c * i, c * i * (TL + L * kv))
+    hp, Ap, Tp = h[:, :-1], A[:, :-1], T[:, :-1]
+    ix = i * x
+    if f["D"] is None:
+        res["gate"] = (lam * (hp - ix) * a * c,
+                       a * c * (TL * (Ap + ix.abs()) + L * (Tp + ix.abs() * U * (ng + 6))
+                                + L * (Ap + ix.abs()) * U * (2 * g.abs() + 16)))
+    else:
+        B, absB = a * hp - slope * ix, a * Ap + slope * ix.abs()
+        bound = (TL * absB + L * (a * Tp + slope * ix.abs() * 2 * kv + 8 * U * absB))
+        dr = f["D"] * r * (1 - r)
+        res["gate"] = (-dr * lam * B, dr * (bound + L * absB * U * (2 * g.abs() + 16)))
+        blocks = x.shape[0] * (rows // BLOCK + 1)
+        res["decay"] = (-(r * lam * B).sum((0, 1)),
+                        (r * (bound + L * absB * U * (g.abs() + 8))).sum((0, 1))
+                        + (64 + 10 + blocks // 16) * U * (r * L * absB).sum((0, 1)))
+    if n is not None:
+        res["input_gate"] = (lam * c * ix * (1 - i),
+                             c * ix.abs() * (1 - i) * (TL + L * (kv + U * (ng + 10))))
+    return res

@@ -56,7 +56,7 @@ def struct_of(name):
     return type(name, (ctypes.Structure,), {"_fields_": fields})
 
 
-Norm = struct_of("canon_norm_t")
+Norm, Recur = struct_of("canon_norm_t"), struct_of("canon_recur_t")
 
 
 def layout(struct):
@@ -69,7 +69,8 @@ def test_struct_layouts(layer):
     def spelt(s):
         return re.sub(r"(\d+)(\w)", lambda m: m.group(2) * int(m.group(1)), s.format.lstrip("="))
 
-    assert spelt(layer.NORM) == layout(Norm) and layer.NORM.size == ctypes.sizeof(Norm)
+    for packed, struct in ((layer.NORM, Norm), (layer.RECUR, Recur)):
+        assert spelt(packed) == layout(struct) and packed.size == ctypes.sizeof(struct)
 
 
 def norm(**kw):
@@ -148,10 +149,99 @@ def test_norm_launch_limits(layer):
                                         dsum=wide, dx=out), None, 0, None) == 2
 
 
+def recur(**kw):
+    c = Recur()
+    c.dtype, c.seqs, c.rows, c.channels = 1, 2, 9, 8
+    at = iter(range(2 * FAKE, 3 * FAKE, 4096))
+    for k in ("x", "gate", "input_gate", "out", "dout", "dx", "dgate", "dinput_gate"):
+        setattr(c, k, Rows(next(at), 72, 8))
+    c.decay = c.ddecay = c.kept_states = FAKE
+    for k, v in kw.items():
+        setattr(c, k, v)
+    return ctypes.byref(c)
+
+
+def test_recur_workspace(layer):
+    w, g = layer.gated_recurrence_workspace_bytes, layer.gated_recurrence_grad_workspace_bytes
+    s = layer._lib().canon_gated_recurrence_states
+    assert w(3, 512, False, 64) == 0 and g(3, 512, False, 64) == 3 * 256
+    assert w(3, 513, False, 64) == 3 * 6 * 256 and g(3, 513, False, 64) == 4 * 6 * 256
+    assert w(3, 1024, True, 64) == 3 * 5 * 256 and w(3, 512, True, 64) == 0
+    assert s(3, 513, 0, 64) == 6 * 4 * 64 and s(3, 1024, 1, 64) == 5 * 4 * 64
+    assert w(0, 1024, True, 64) == 0 and g(0, 1024, True, 64) == 0 and s(0, 99, 1, 64) == 0
+    for bad in ((1 << 30, 1, False, 8), (1, 1 << 30, False, 8), (1, 1, False, 1 << 24)):
+        assert w(*bad) == 0 and g(*bad) == 0 and s(*bad) == 0
+    assert w(1, (1 << 30) - 1, False, (1 << 24) - 1) > 1 << 46  # large sizes do not wrap
+
+
+def test_recur_refusals(layer):
+    L, R = layer._lib(), Rows
+    n = layer.gated_recurrence_grad_workspace_bytes(2, 9, False, 8)
+    calls = (lambda **b: L.canon_gated_recurrence(recur(**b), None, 0, None),
+             lambda **b: L.canon_gated_recurrence_grad(recur(**b), FAKE, n, None))
+    step = lambda **b: L.canon_gated_recurrence_step(recur(**b), None)  # noqa: E731
+    for bad in (dict(dtype=3), dict(seqs=-1), dict(rows=-1), dict(channels=-1),
+                dict(x=R(None, 0, 0)), dict(gate=R(None, 0, 0)), dict(gate=R(FAKE, -1, 8)),
+                dict(input_gate=R(FAKE, 72, -8))):
+        assert all(call(**bad) == 1 for call in calls), bad
+    for bad in (R(None, 0, 0), R(FAKE, 0, 8), R(FAKE, 72, 7), R(FAKE, 71, 8)):
+        assert calls[0](out=bad) == 1
+        for name in ("dx", "dgate", "dinput_gate"):
+            assert calls[1](**{name: bad}) == 1, name
+    x = R(2 * FAKE, 72, 8)
+    for name in ("x", "gate", "input_gate"):  # in place
+        assert calls[0](**{name: x, "out": x}) == 1
+    for name in ("x", "gate", "input_gate", "dout"):
+        for out in ("dx", "dgate", "dinput_gate"):
+            assert calls[1](**{name: x, out: x}) == 1, (name, out)
+    assert calls[1](dx=x, dgate=x) == 1 and calls[1](dx=x, dinput_gate=x) == 1
+    for bad in (dict(dout=R(None, 0, 0)), dict(kept_states=None), dict(ddecay=None),
+                dict(decay=None), dict(d_init_state=FAKE, d_final_state=FAKE)):
+        assert calls[1](**bad) == 1, bad
+    for bad in (dict(rows=1 << 30), dict(seqs=1 << 30), dict(channels=1 << 24)):
+        assert all(call(**bad) == 2 for call in calls), bad
+    assert L.canon_gated_recurrence(recur(rows=513, x=R(FAKE, 513 * 8, 8),
+                                          out=R(3 * FAKE, 513 * 8, 8)), None, 0, None) == 3
+    assert L.canon_gated_recurrence_grad(recur(), FAKE, n - 1, None) == 3
+    assert L.canon_gated_recurrence_grad(recur(), FAKE + 8, n, None) == 3
+    assert step(starts=FAKE) == 1 and step(x=R(None, 0, 0)) == 1
+    assert L.canon_gated_recurrence(None, None, 0, None) == 1
+    assert L.canon_gated_recurrence_grad(None, None, 0, None) == 1
+    assert L.canon_gated_recurrence_step(None, None) == 1
+    for none in (dict(seqs=0), dict(channels=0)):
+        assert calls[0](x=R(None, 0, 0), **none) == 0 and step(x=R(None, 0, 0), **none) == 0
+    assert calls[1](channels=0, x=R(None, 0, 0)) == 0
+
+
+def test_recur_launch_limits(layer):
+    """Blocks times slabs below 2^22."""
+    L = layer._lib()
+
+    def call(seqs, rows, channels, **kw):
+        r = Rows(FAKE, rows * channels, channels)
+        return L.canon_gated_recurrence(recur(seqs=seqs, rows=rows, channels=channels, x=r, gate=r,
+                                              input_gate=r,
+                                              out=Rows(3 * FAKE, rows * channels, channels), **kw),
+                                        None, 0, None)
+
+    assert call((1 << 21) - 1, 513, 64) == 3 and call(1 << 21, 513, 64) == 2
+    most = ((1 << 22) - 1) // 16383  # channels of 16383 slabs
+    assert call(1, 512 * most, 64 * 16383) == 3 and call(1, 512 * most + 1, 64 * 16383) == 2
+    p = dict(starts=FAKE)
+    assert call(1, 512 * most - 1, 64 * 16383, **p) == 3
+    assert call(1, 512 * most, 64 * 16383, **p) == 2
+    r = Rows(FAKE, 64, 64)
+    assert L.canon_gated_recurrence_step(recur(seqs=1 << 22, channels=64, x=r, gate=r, input_gate=r,
+                                               out=Rows(3 * FAKE, 64, 64)), None) == 2
+
+
 def test_the_binding_has_no_cpu_path(layer):
     import scan_canonical_reduce_amd as canon
     x, w = torch.zeros(3, 8), torch.ones(8)
     for call in (lambda: canon.layer_norm(x, w), lambda: canon.add_layer_norm(x, x, w),
-                 lambda: canon.layer_norm_grad(x, x, w, canon.layer_norm_stats(x))):
+                 lambda: canon.layer_norm_grad(x, x, w, canon.layer_norm_stats(x)),
+                 lambda: canon.gated_recurrence(x[None], x[None]),
+                 lambda: canon.gated_recurrence_grad(x[None], x[None], x[None], w),
+                 lambda: canon.gated_recurrence_step(x, x, x)):
         with pytest.raises(ValueError, match="GPU"):
             call()
