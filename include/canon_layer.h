@@ -1,7 +1,7 @@
 /*
  * canon_layer.h — operators of a recurrent language model's layers on AMD MI355X
- * (gfx950), beside those of canon_seq.h: layer norm with the residual sum, and
- * the gated linear recurrence.  Part of libcanon.
+ * (gfx950), beside those of canon_seq.h: layer norm with the residual sum, the
+ * gated linear recurrence, and sampling of the next token.  Part of libcanon.
  *
  * What is computed:
  *
@@ -18,10 +18,20 @@
  *                    h[t,d] = a h[t-1,d] + c i x[t,d], out = h.
  *                    Gradients are the formula's; where c is 0 (an a of 1), the
  *                    slope of the square root counts as 0.
+ *   sample           w[j] = exp((logits[j] - max) / temperature), held as a multiple
+ *                    of 2^-S, S = 62 - ceil(log2 vocab), 50 at most; tokens ranked by
+ *                    logits, the lowest index first among equals; kept are
+ *                      the top_k first ones (0: all),
+ *                      of those the fewest first ones whose weights add up to top_p
+ *                      of the sum (one at least; 1 or more: all),
+ *                      of those the ones whose weight is at least min_p;
+ *                    the token is the first one in index order at which the sum of
+ *                    the kept weights up to it exceeds u times their whole sum.
  *
  * Everything is computed in 32 bits and rounded once where it is stored, but for
- * the recurrence's carried state, in 64.  Each sum is one fixed expression of the
- * shapes, so each call is reproducible bit for bit.  In particular:
+ * the recurrence's carried state and the sampling's weights, in 64.  Each sum is
+ * one fixed expression of the shapes, and sums of sampling weights are sums of
+ * integers, so each call is reproducible bit for bit.  In particular:
  *   - a row's norm depends on its width, type and values alone, not on the rows
  *     around it, strides or alignment;
  *   - the recurrence is evaluated in chunks of CANON_RECUR_CHUNK rows from the
@@ -127,6 +137,31 @@ canon_status_t canon_gated_recurrence_grad(const canon_recur_t* c, void* ws, siz
 /* One row of each of `seqs` sequences (rows is ignored; canon_rows_t.seq apart): h from
  * init_state (NULL: zero), written to final_state, which may be the same buffer. */
 canon_status_t canon_gated_recurrence_step(const canon_recur_t* c, void* stream);
+
+/* --------------------------------------------------------------- sampling */
+typedef struct {
+    int64_t dtype; /* canon_dtype_t of logits */
+    int64_t rows, vocab;
+    const void* logits; /* rows of vocab elements, row pitch ld >= 0 */
+    int64_t ld;
+    const float* u; /* rows random numbers in [0, 1); others count as the nearest */
+    /* per row, or NULL: the value beside it for every row */
+    const float* temperature; /* not above 0: the largest logit's token */
+    const int32_t* top_k;     /* not above 0: no limit */
+    const float* top_p;
+    const float* min_p;
+    double temperature_all, top_p_all, min_p_all;
+    int64_t top_k_all;
+    void* ids;        /* rows, 64-bit if id_bytes is 8, 32-bit if 4 */
+    int64_t id_bytes;
+} canon_sample_t;
+
+/* Logits of minus infinity and NaN are masked: never chosen.  A row with nothing else
+ * gives -1.  Where the largest logit is plus infinity, the infinite ones have weight 1
+ * and the others 0.  A min_p above 1 counts as 1.
+ * Limits (CANON_EUNSUPPORTED): rows < 2^22, vocab < 2^24. */
+size_t canon_sample_workspace_bytes(size_t rows, size_t vocab);
+canon_status_t canon_sample(const canon_sample_t* c, void* ws, size_t ws_bytes, void* stream);
 
 #ifdef __cplusplus
 }

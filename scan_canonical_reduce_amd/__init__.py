@@ -528,4 +528,4 @@ from .layer import (  # noqa: E402
     GatedRecurrenceGrads, LayerNormGrads, add_layer_norm, gated_recurrence, gated_recurrence_grad,
     gated_recurrence_grad_workspace_bytes, gated_recurrence_states, gated_recurrence_step,
     gated_recurrence_workspace_bytes, layer_norm, layer_norm_grad,
-    layer_norm_grad_workspace_bytes, layer_norm_stats)
+    layer_norm_grad_workspace_bytes, layer_norm_stats, sample, sample_workspace_bytes)

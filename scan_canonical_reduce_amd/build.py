@@ -26,7 +26,7 @@ SOURCES = [
     "selective_scan_f32.hip", "selective_scan_bf16.hip", "selective_scan_f16.hip",
     "selective_scan_grad_f32.hip", "selective_scan_grad_bf16.hip", "selective_scan_grad_f16.hip",
     "layer_api.cpp", "layer_norm_f32.hip", "layer_norm_bf16.hip", "layer_norm_f16.hip",
-    "recurrence_f32.hip", "recurrence_bf16.hip", "recurrence_f16.hip",
+    "recurrence_f32.hip", "recurrence_bf16.hip", "recurrence_f16.hip", "sample.hip",
 ]
 
 # -ffp-contract=off: no FMA contraction; no fast-math; subnormals kept (no

@@ -3,6 +3,7 @@
 #include "../../include/canon_layer.h"
 #include "layer_norm.hpp"
 #include "recurrence.hpp"
+#include "sample.hpp"
 #include "seq_args.hpp"
 
 using namespace canon;
@@ -296,6 +297,49 @@ canon_status_t canon_gated_recurrence_step(const canon_recur_t* c, void* stream)
     if (a.q.seqs == 0 || a.channels == 0) return CANON_OK;
     return with_dtype(c->dtype, [&](auto t) {
         return hip_status(launch_recurrence_step<decltype(t)>(a, static_cast<hipStream_t>(stream)));
+    });
+}
+
+size_t canon_sample_workspace_bytes(size_t rows, size_t vocab)
+{
+    (void)rows;
+    (void)vocab;
+    return 0;
+}
+
+canon_status_t canon_sample(const canon_sample_t* c, void* ws, size_t ws_bytes, void* stream)
+{
+    if (c == nullptr || c->rows < 0 || c->vocab < 0 || c->ld < 0 || !is_dtype(c->dtype) ||
+        (c->id_bytes != 4 && c->id_bytes != 8))
+        return CANON_EINVAL;
+    if (c->rows >= ((int64_t)1 << 22) || c->vocab >= ((int64_t)1 << 24)) return CANON_EUNSUPPORTED;
+    if (c->rows == 0) return CANON_OK;
+    if (c->ids == nullptr || c->u == nullptr || (c->vocab > 0 && c->logits == nullptr))
+        return CANON_EINVAL;
+    if (canon_status_t s =
+            check_ws(ws, ws_bytes, canon_sample_workspace_bytes((size_t)c->rows, (size_t)c->vocab)))
+        return s;
+    SampleArgs a{};
+    a.logits = c->logits;
+    a.ld = c->ld;
+    a.rows = c->rows;
+    a.vocab = (int32_t)c->vocab;
+    int log = 0;
+    while (((int64_t)1 << log) < c->vocab) ++log;
+    a.bits = log < 12 ? 50 : 62 - log;
+    a.u = c->u;
+    a.temperature = c->temperature;
+    a.top_p = c->top_p;
+    a.min_p = c->min_p;
+    a.top_k = c->top_k;
+    a.temperature_all = c->temperature_all;
+    a.top_p_all = c->top_p_all;
+    a.min_p_all = c->min_p_all;
+    a.top_k_all = (int32_t)(c->top_k_all < 0 ? 0 : c->top_k_all > c->vocab ? 0 : c->top_k_all);
+    a.ids = c->ids;
+    a.ids64 = c->id_bytes == 8;
+    return with_dtype(c->dtype, [&](auto t) {
+        return hip_status(launch_sample<decltype(t)>(a, static_cast<hipStream_t>(stream)));
     });
 }
 

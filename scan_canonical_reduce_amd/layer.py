@@ -24,12 +24,13 @@ LAYER_EXPORTS = [
     "canon_layer_norm_grad", "canon_gated_recurrence_states",
     "canon_gated_recurrence_workspace_bytes", "canon_gated_recurrence",
     "canon_gated_recurrence_grad_workspace_bytes", "canon_gated_recurrence_grad",
-    "canon_gated_recurrence_step",
+    "canon_gated_recurrence_step", "canon_sample_workspace_bytes", "canon_sample",
 ]
 
-# canon_norm_t (eps a double) and canon_recur_t: fields of 8 bytes
+# canon_norm_t, canon_recur_t and canon_sample_t: fields of 8 bytes, doubles among them
 NORM = struct.Struct("=5qd26q")
 RECUR = struct.Struct("=36q")
+SAMPLE = struct.Struct("=10q3d3q")
 
 _layer = None
 
@@ -52,6 +53,8 @@ def _lib() -> ctypes.CDLL:
     L.canon_gated_recurrence_grad_workspace_bytes.argtypes = [S, S, I, S]
     L.canon_gated_recurrence_grad.argtypes = [P, P, S, P]
     L.canon_gated_recurrence_step.argtypes = [P, P]
+    L.canon_sample_workspace_bytes.argtypes = [S, S]
+    L.canon_sample.argtypes = [P, P, S, P]
     if L.canon_layer_version() != LAYER_VERSION:
         raise CanonError("libcanon layer operators: version mismatch")
     _layer = L
@@ -300,4 +303,57 @@ def gated_recurrence_step(state: torch.Tensor, x: torch.Tensor, gate: torch.Tens
                    old if out_state is None else _flat(what, "out_state", out_state, shape, f32),
                    0, *_NONE, *_NONE, *_NONE, *_NONE, 0, 0, 0)
     _call(what, x.device, _lib().canon_gated_recurrence_step, c)
+    return out
+
+
+# -------------------------------------------------------------------- sampling
+def _setting(what: str, name: str, v, rows: int, dtype: torch.dtype):
+    """(pointer, value) of a number for all rows, or one per row"""
+    if not torch.is_tensor(v):
+        return 0, v
+    return _flat(what, name, v, (rows,), dtype), 0
+
+
+def sample_workspace_bytes(rows: int, vocab: int) -> int:
+    return _lib().canon_sample_workspace_bytes(rows, vocab)
+
+
+def sample(logits: torch.Tensor, u: torch.Tensor, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0,
+           out: Optional[torch.Tensor] = None,
+           ws: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """One token of each row of logits ([rows, vocab], any row stride), int64 (or out's
+    int32): the softmax of logits / temperature, cut to the top_k largest, of those to
+    the fewest largest that have top_p of the sum, of those to the ones with at least
+    min_p times the largest's weight; the token at which the sum in index order passes
+    u (float32 [rows], in [0, 1)) times the whole.
+
+    Each setting is a number or a tensor of one per row (float32; top_k int32).  A
+    temperature of 0 takes the largest logit; top_k of 0, top_p of 1 and min_p of 0 keep
+    everything.  Ties go to the lowest index.  Logits of minus infinity and NaN are
+    never taken; a row of nothing else gives -1."""
+    what = "sample"
+    given = [t for t in (temperature, top_k, top_p, min_p) if torch.is_tensor(t)]
+    _same(what, logits.device, u, out, ws, *given)
+    d = _dtype(logits, what)
+    if logits.dim() != 2 or (logits.shape[1] > 1 and logits.numel() and logits.stride(1) != 1):
+        raise ValueError(f"{what}: logits must be 2-d with unit column stride")
+    rows, vocab = logits.shape
+    f32, i32 = torch.float32, torch.int32
+    tp, tv = _setting(what, "temperature", temperature, rows, f32)
+    kp, kv = _setting(what, "top_k", top_k, rows, i32)
+    pp, pv = _setting(what, "top_p", top_p, rows, f32)
+    mp, mv = _setting(what, "min_p", min_p, rows, f32)
+    if tv < 0 or kv < 0 or not 0 <= pv <= 1 or not 0 <= mv <= 1 or tv != tv:
+        raise ValueError(f"{what}: temperature and top_k must not be negative, top_p and min_p "
+                         "lie in [0, 1]")
+    if out is None:
+        out = torch.empty(rows, dtype=torch.int64, device=logits.device)
+    elif out.dtype not in (torch.int64, i32):
+        raise TypeError(f"{what}: out must be int64 or int32, not {out.dtype}")
+    c = SAMPLE.pack(d, rows, vocab, logits.data_ptr(), logits.stride(0) if rows > 1 else 0,
+                    _flat(what, "u", u, (rows,), f32), tp, kp, pp, mp, tv, pv, mv, kv,
+                    _flat(what, "out", out, (rows,), out.dtype), out.element_size())
+    L = _lib()
+    w = _workspace(L.canon_sample_workspace_bytes(rows, vocab), logits.device, ws)
+    _call(what, logits.device, L.canon_sample, c, w.data_ptr(), w.numel())
     return out

@@ -167,3 +167,43 @@ def recur(x, gate, input_gate=None, decay=None, init=None, dout=None, dfinal=Non
         res["input_gate"] = (lam * c * ix * (1 - i),
                              c * ix.abs() * (1 - i) * (TL + L * (kv + U * (ng + 10))))
     return res
+
+
+# -------------------------------------------------------------------- sampling
+def sample(x, u, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0):
+    """The token of one row by a sort and sums in 80-bit numbers (64 bits of
+    significand), and how far u is from the nearest token's border (1 where nothing
+    depends on it), and top_p from the nearest sum, in shares of the whole."""
+    import numpy as np
+    x = np.where(np.isnan(x), -np.inf, x.astype(np.longdouble))
+    order = np.lexsort((np.arange(x.size), -x))
+    order = order[x[order] > -np.inf]
+    if order.size == 0:
+        return -1, 1.0
+    if not temperature > 0:
+        return int(order[0]), 1.0
+    if top_k > 0:
+        order = order[:top_k]
+    top = x[order[0]]
+    with np.errstate(invalid="ignore"):
+        w = np.where(x[order] == top, np.longdouble(1),
+                     np.exp((x[order] - top) / np.longdouble(temperature)))
+    w = np.where(np.isnan(w), 0, w)
+    margin = 1.0
+    if top_p < 1:
+        total = np.cumsum(w)
+        want = np.longdouble(top_p) * total[-1]
+        keep = 1 + int(np.searchsorted(total, want))
+        margin = float(np.abs(total - want).min() / total[-1])
+        order, w = order[:keep], w[:keep]
+    keep = w >= min(min_p, 1.0)
+    order, w = order[keep], w[keep]
+    at = np.argsort(order)
+    order, total = order[at], np.cumsum(w[at])
+    want = np.longdouble(min(max(u, 0.0), 1.0)) * total[-1]
+    margin = min(margin, float(np.abs(total[:-1] - want).min() / total[-1]) if total.size > 1
+                 else 1.0)
+    i = min(int(np.searchsorted(total, want, side="right")), order.size - 1)
+    while w[at][i] == 0:  # u of 1
+        i -= 1
+    return int(order[i]), margin

@@ -57,6 +57,7 @@ def struct_of(name):
 
 
 Norm, Recur = struct_of("canon_norm_t"), struct_of("canon_recur_t")
+Sample = struct_of("canon_sample_t")
 
 
 def layout(struct):
@@ -69,7 +70,8 @@ def test_struct_layouts(layer):
     def spelt(s):
         return re.sub(r"(\d+)(\w)", lambda m: m.group(2) * int(m.group(1)), s.format.lstrip("="))
 
-    for packed, struct in ((layer.NORM, Norm), (layer.RECUR, Recur)):
+    for packed, struct in ((layer.NORM, Norm), (layer.RECUR, Recur),
+                           (layer.SAMPLE, Sample)):
         assert spelt(packed) == layout(struct) and packed.size == ctypes.sizeof(struct)
 
 
@@ -235,12 +237,35 @@ def test_recur_launch_limits(layer):
                                                out=Rows(3 * FAKE, 64, 64)), None) == 2
 
 
+def sample(**kw):
+    c = Sample()
+    c.dtype, c.rows, c.vocab, c.ld, c.id_bytes = 0, 3, 50, 50, 8
+    c.logits = c.u = c.ids = FAKE
+    c.temperature_all, c.top_p_all = 1.0, 1.0
+    for k, v in kw.items():
+        setattr(c, k, v)
+    return ctypes.byref(c)
+
+
+def test_sample_refusals(layer):
+    L = layer._lib()
+    ws = layer.sample_workspace_bytes
+    for bad in (dict(dtype=3), dict(rows=-1), dict(vocab=-1), dict(ld=-1), dict(id_bytes=2),
+                dict(logits=None), dict(u=None), dict(ids=None)):
+        assert L.canon_sample(sample(**bad), FAKE, ws(3, 50), None) == 1, bad
+    assert L.canon_sample(None, FAKE, 0, None) == 1
+    assert L.canon_sample(sample(rows=1 << 22), FAKE, 0, None) == 2
+    assert L.canon_sample(sample(vocab=1 << 24), FAKE, 0, None) == 2
+    assert L.canon_sample(sample(rows=0, ids=None, u=None, logits=None), None, 0, None) == 0
+
+
 def test_the_binding_has_no_cpu_path(layer):
     import scan_canonical_reduce_amd as canon
     x, w = torch.zeros(3, 8), torch.ones(8)
     for call in (lambda: canon.layer_norm(x, w), lambda: canon.add_layer_norm(x, x, w),
                  lambda: canon.layer_norm_grad(x, x, w, canon.layer_norm_stats(x)),
                  lambda: canon.gated_recurrence(x[None], x[None]),
+                 lambda: canon.sample(x, w),
                  lambda: canon.gated_recurrence_grad(x[None], x[None], x[None], w),
                  lambda: canon.gated_recurrence_step(x, x, x)):
         with pytest.raises(ValueError, match="GPU"):
