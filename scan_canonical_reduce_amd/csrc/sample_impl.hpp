@@ -7,12 +7,13 @@
 //
 // No sort: what top_k and top_p keep are the tokens up to a border (key, index) in
 // the order of descending keys, which ascend with the logit, and ascending indexes.
-//   1. The row's largest and smallest logit.
-//   2. With a filter, the tokens counted in kBins equal steps of the logit from the
-//      largest down.  The counts tell in which step the top_k-th token lies, and, as a
-//      step's weights are known to a step, between which two the top_p border lies.
-//   3. Those tokens go to a list in LDS: for top_k all from the border's step up, for
-//      top_p alone those of the steps in question, while all weights are summed.
+//   1. Each thread's largest logit, and the row's.
+//   2. With a filter, tokens counted in kBins equal steps of the logit from the largest
+//      down.  For top_k the threads' largest ones suffice: where k of them lie, k
+//      tokens do, and not many more.  For top_p (or a large k) all are counted; as a
+//      step's weights are known to a step, the border lies between two known steps.
+//   3. The tokens in question go to a list in LDS: for top_k all from the border's step
+//      up, for top_p those of its steps, while all weights are summed.
 //   4. The border is found in the list digit by digit, by counts or sums of weights.
 //   5. Sums of the kept weights by pieces of the row in index order, the piece in
 //      which u's share falls, and the token in it.
@@ -35,21 +36,21 @@ constexpr int kSampleWaves = kSampleThreads / 64;
 constexpr int kBins = 4 * kSampleThreads;
 constexpr int kList = 6144;
 constexpr int kSums = 8 * kSampleWaves;
+constexpr float kInf = __builtin_inff();
 
-// The key of a logit: ascending, one for both zeros, 0 for a masked one (NaN, minus
-// infinity); and the logit of a key that is not 0.  As wide as the type.
+// The key of a logit that is not masked: ascending, one for both zeros, as wide as the
+// type; and the logit of a key.
 template <typename T>
-__device__ __forceinline__ uint32_t logit_key(typename T::store_t raw)
+__device__ __forceinline__ uint32_t logit_key(float x)
 {
-    if constexpr (sizeof(raw) == 4) {
-        const uint32_t b = __float_as_uint(raw + 0.f);
-        const uint32_t k = b >> 31 ? ~b : b | 0x80000000u;
-        return raw > -__builtin_inff() ? k : 0u;
-    } else {
-        const uint32_t b = raw == 0x8000u ? 0u : raw;
-        const uint32_t k = b >> 15 ? ~b & 0xffffu : b | 0x8000u;
-        return T::load(raw) > -__builtin_inff() ? k : 0u;
-    }
+    constexpr bool wide = sizeof(typename T::store_t) == 4;
+    uint32_t b;
+    if constexpr (wide)
+        b = __float_as_uint(x + 0.f);
+    else
+        b = (uint32_t)T::round(x + 0.f) << 16;
+    const uint32_t k = b >> 31 ? ~b : b | 0x80000000u;
+    return wide ? k : k >> 16;
 }
 template <typename T>
 __device__ __forceinline__ float key_logit(uint32_t k)
@@ -59,26 +60,19 @@ __device__ __forceinline__ float key_logit(uint32_t k)
     else
         return T::load((uint16_t)(k >> 15 ? k & 0x7fffu : ~k));
 }
-template <typename T>
-__device__ __forceinline__ typename T::store_t masked_logit()
-{
-    if constexpr (sizeof(typename T::store_t) == 4)
-        return -__builtin_inff();
-    else
-        return T::round(-__builtin_inff());
-}
 
 // A row's weights.  2^y, y = (x - max) / temperature in binary steps, is 2^n times the
 // polynomial of degree 10 whose largest error on [-1/2, 1/2] is smallest (2^-51.5
 // relative with its rounded coefficients; 1 at 0).  Adding 2^(52 - bits) leaves the
-// rounded multiple of 2^-bits in the low bits of the sum.  Below 2^-60 it is 0.
+// rounded multiple of 2^-bits in the low bits of the sum: 0 below 2^-60, where y is
+// cut off, and for a masked logit.  Beside an infinite logit only such are kept; its y
+// is not a number, and the cut makes it 0.
 struct Weights {
     double max, scale, unit;  // scale: log2(e) / temperature
+    double cut;               // -60, or 0 where the largest is infinite
     __device__ __forceinline__ u64 operator()(float x) const
     {
-        // plus infinity as the largest number: where one is there, only such are kept
-        const double d = (double)__builtin_fminf(x, kMaxF) - max;
-        const double y = __builtin_fmax(d * scale, -60.);  // -60 for a NaN
+        const double y = __builtin_fmax(((double)x - max) * scale, cut);  // cut for a NaN
         const double t = y + 0x1.8p52, r = y - (t - 0x1.8p52);
         double p = 0x1.e6063f7217bc6p-28;
         p = __builtin_fma(p, r, 0x1.b675bca4eeebbp-24);
@@ -97,12 +91,13 @@ struct Weights {
     }
 };
 
-// The kept tokens: those above the key, and at it up to the index.
+// The kept tokens: those above the logit, and at it up to the index.
 struct Border {
-    uint32_t key, idx;
-    __device__ __forceinline__ bool keeps(uint32_t k, uint32_t i) const
+    float x;
+    uint32_t idx;
+    __device__ __forceinline__ bool keeps(float v, uint32_t i) const
     {
-        return k > key || (k == key && i <= idx);
+        return v > x || (v == x && i <= idx);
     }
 };
 
@@ -112,6 +107,41 @@ __device__ __forceinline__ u64 min_share(double p, u64 sum)
     const double want = __builtin_ceil(p * (double)sum);
     const u64 v = want >= 1. ? (u64)want : 1;
     return v < sum ? v : sum;
+}
+
+// ------------------------------------------------------------------- wave scans
+template <int CTRL, int ROWS, typename V>
+__device__ __forceinline__ V dpp_or_0(V v)
+{
+    if constexpr (sizeof(V) == 8) {
+        const u64 b = __builtin_bit_cast(u64, v);
+        const uint32_t lo = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)b, CTRL, ROWS,
+                                                                  0xf, false);
+        const uint32_t hi =
+            (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(b >> 32), CTRL, ROWS, 0xf, false);
+        return __builtin_bit_cast(V, (u64)hi << 32 | lo);
+    } else {
+        return __builtin_bit_cast(V, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v),
+                                                                 CTRL, ROWS, 0xf, false));
+    }
+}
+// the sum over the lanes up to this one
+template <typename V>
+__device__ __forceinline__ V wave_upto(V v)
+{
+    v += dpp_or_0<0x111, 0xf>(v);  // from 1, 2, 4, 8 lanes below in a row of 16
+    v += dpp_or_0<0x112, 0xf>(v);
+    v += dpp_or_0<0x114, 0xf>(v);
+    v += dpp_or_0<0x118, 0xf>(v);
+    v += dpp_or_0<0x142, 0xa>(v);  // the last lane of a row to the odd rows
+    v += dpp_or_0<0x143, 0xc>(v);  // and of the first half to the second
+    return v;
+}
+__device__ __forceinline__ u64 lane64(u64 v, int lane)
+{
+    const uint32_t lo = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)v, lane);
+    const uint32_t hi = (uint32_t)__builtin_amdgcn_readlane((int)(v >> 32), lane);
+    return (u64)hi << 32 | lo;
 }
 
 // From the highest of 256 bins down, the first at which the sum reaches target (which
@@ -126,12 +156,7 @@ __device__ __forceinline__ void pick_bin(const u64* hist, u64 target, Picked* ou
     u64 v[4], sum = 0;
 #pragma unroll
     for (int i = 0; i < 4; ++i) sum += v[i] = hist[b0 - i];
-    u64 upto = sum;
-#pragma unroll
-    for (int d = 1; d < 64; d *= 2) {
-        const u64 o = __shfl_up(upto, d);
-        if (lane >= d) upto += o;
-    }
+    const u64 upto = wave_upto(sum);
     u64 before = upto - sum;
     if (before >= target || upto < target) return;
 #pragma unroll
@@ -144,29 +169,33 @@ __device__ __forceinline__ void pick_bin(const u64* hist, u64 target, Picked* ou
     }
 }
 
-// The sum over the threads before this one, and of all.  lds: a value a wave, not to
-// be used again before the next barrier.
-template <typename V>
-__device__ __forceinline__ V scan_before(V v, V* lds, V& all)
+// The sums over the threads before this one, and of all, of N values at once.  lds: a
+// value of each a wave, not to be used again before the next barrier.
+template <typename V, int N>
+__device__ __forceinline__ void scan_before(V (&v)[N], V (*lds)[kSampleWaves], V (&all)[N])
 {
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    V upto = v;
 #pragma unroll
-    for (int d = 1; d < 64; d *= 2) {
-        const V o = __shfl_up(upto, d);
-        if (lane >= d) upto += o;
+    for (int i = 0; i < N; ++i) {
+        const V upto = wave_upto(v[i]);
+        if (lane == 63) lds[i][wave] = upto;
+        v[i] = upto - v[i];
     }
-    if (lane == 63) lds[wave] = upto;
     __syncthreads();
-    V before = upto - v;
-    all = 0;
 #pragma unroll
-    for (int w = 0; w < kSampleWaves; ++w) {
-        const V s = lds[w];
-        if (w < wave) before += s;
-        all += s;
+    for (int i = 0; i < N; ++i) {
+        // lane w of a row holds wave w's sum
+        const V upto = wave_upto(lane < kSampleWaves ? lds[i][lane] : V(0));
+        if constexpr (sizeof(V) == 8) {
+            const u64 b = __builtin_bit_cast(u64, upto);
+            all[i] = __builtin_bit_cast(V, lane64(b, kSampleWaves - 1));
+            if (wave > 0) v[i] += __builtin_bit_cast(V, lane64(b, wave - 1));
+        } else {
+            const int b = __builtin_bit_cast(int, upto);
+            all[i] = __builtin_bit_cast(V, __builtin_amdgcn_readlane(b, kSampleWaves - 1));
+            if (wave > 0) v[i] += __builtin_bit_cast(V, __builtin_amdgcn_readlane(b, wave - 1));
+        }
     }
-    return before;
 }
 
 // A row in pieces of 64 vectors.  Wave w has the pieces (16 g + w) G ... + G - 1 of
@@ -177,39 +206,36 @@ struct Row {
     static constexpr int V = 16 / sizeof(E), kPiece = 64 * V, U = 4;
     const E* x;
     int32_t n, G, groups;
-    __device__ __forceinline__ int32_t piece(int g, int w) const
+    // the vector of this lane in a piece that starts at `first` (below n)
+    __device__ __forceinline__ Vec<T, V> load(int32_t first) const
     {
-        return (g * kSampleWaves + w) * G;
-    }
-    __device__ __forceinline__ Vec<T, V> load(int32_t at) const
-    {
-        if (at + V <= n) return ld_any<T, V, false>(x + at);
+        const int32_t at = first + (threadIdx.x & 63) * V;
+        if (first + kPiece <= n) return ld_any<T, V, false>(x + at);
         Vec<T, V> v;
 #pragma unroll
-        for (int e = 0; e < V; ++e) v.e[e] = at + e < n ? x[at + e] : masked_logit<T>();
+        for (int e = 0; e < V; ++e) v.e[e] = at + e < n ? x[at + e] : T::round(-kInf);
         return v;
     }
     // f(g, index of the vector's first token, vector) over the wave's vectors
     template <class F>
     __device__ __forceinline__ void each(F&& f) const
     {
-        const int lane = threadIdx.x & 63, wave = uniform((int32_t)(threadIdx.x >> 6));
+        const int wave = uniform((int32_t)(threadIdx.x >> 6));
         int g = 0, i = 0;
         while (g < groups) {
             Vec<T, V> v[U];
-            int32_t at[U];
+            int32_t first[U];
             int gs[U];
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                const int32_t first = (piece(g, wave) + i) * kPiece;
-                gs[u] = g < groups && first < n ? g : -1;
-                at[u] = first + lane * V;
-                if (gs[u] >= 0) v[u] = load(at[u]);
+                first[u] = ((g * kSampleWaves + wave) * G + i) * kPiece;
+                gs[u] = g < groups && first[u] < n ? g : -1;
+                if (gs[u] >= 0) v[u] = load(first[u]);
                 if (++i == G) i = 0, ++g;
             }
 #pragma unroll
             for (int u = 0; u < U; ++u)
-                if (gs[u] >= 0) f(gs[u], at[u], v[u]);
+                if (gs[u] >= 0) f(gs[u], first[u] + (int32_t)(threadIdx.x & 63) * V, v[u]);
         }
     }
 };
@@ -225,13 +251,14 @@ __global__ __launch_bounds__(kSampleThreads) void k_sample(SampleArgs a)
         u64 sums[kSums];
     } sh;
     __shared__ uint32_t lkey[kList], lidx[kList];
-    __shared__ u64 hist[256], wave64[kSampleWaves];
-    __shared__ double wave_lo[kSampleWaves], wave_hi[kSampleWaves];
-    __shared__ uint32_t wave_a[kSampleWaves], wave_b[kSampleWaves];
+    __shared__ u64 hist[256], wave64[3][kSampleWaves];
+    __shared__ double bounds[2][kSampleWaves];
+    __shared__ uint32_t wave32[1][kSampleWaves];
+    __shared__ float wave_max[kSampleWaves];
     __shared__ Picked picked;
     __shared__ uint32_t s_n, s_first, s_b1, s_b2, s_c1, s_c2;
     const int64_t row = blockIdx.x;
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int tid = threadIdx.x, lane = tid & 63, wave = uniform((int32_t)(tid >> 6));
     R r;
     r.x = static_cast<const E*>(a.logits) + row * a.ld;
     r.n = a.vocab;
@@ -239,38 +266,28 @@ __global__ __launch_bounds__(kSampleThreads) void k_sample(SampleArgs a)
     r.G = (pieces + kSums - 1) / kSums;
     r.groups = r.G ? (pieces + kSampleWaves * r.G - 1) / (kSampleWaves * r.G) : 0;
 
-    // 1. the largest and the smallest key
-    uint32_t top = 0, low = 0xffffffffu;
+    // 1. the largest (a maximum takes the operand that is not NaN)
+    float mine = -kInf;
     r.each([&](int, int32_t, const Vec<T, V>& v) {
 #pragma unroll
-        for (int e = 0; e < V; ++e) {
-            const uint32_t k = logit_key<T>(v.e[e]);
-            top = k > top ? k : top;
-            low = k - 1 < low ? k - 1 : low;  // a masked one is the largest here
-        }
+        for (int e = 0; e < V; ++e) mine = __builtin_fmaxf(mine, T::load(v.e[e]));
     });
+    float top = mine;
 #pragma unroll
-    for (int d = 1; d < 64; d *= 2) {
-        const uint32_t o = __shfl_xor(top, d), p = __shfl_xor(low, d);
-        top = o > top ? o : top;
-        low = p < low ? p : low;
-    }
-    if (lane == 0) wave_a[wave] = top, wave_b[wave] = low;
+    for (int d = 1; d < 64; d *= 2) top = __builtin_fmaxf(top, __shfl_xor(top, d));
+    if (lane == 0) wave_max[wave] = top;
     for (int b = tid; b < kBins; b += kSampleThreads) sh.bins[b] = 0;
     if (tid == 0) s_n = 0, s_first = 0xffffffffu, s_b1 = s_b2 = kBins - 1;
     __syncthreads();
 #pragma unroll
-    for (int w = 0; w < kSampleWaves; ++w) {
-        top = wave_a[w] > top ? wave_a[w] : top;
-        low = wave_b[w] < low ? wave_b[w] : low;
-    }
+    for (int w = 0; w < kSampleWaves; ++w) top = __builtin_fmaxf(top, wave_max[w]);
     auto put = [&](int64_t id) {
         if (a.ids64)
             static_cast<int64_t*>(a.ids)[row] = id;
         else
             static_cast<int32_t*>(a.ids)[row] = (int32_t)id;
     };
-    if (top == 0) {
+    if (top == -kInf) {
         if (tid == 0) put(-1);
         return;
     }
@@ -278,55 +295,49 @@ __global__ __launch_bounds__(kSampleThreads) void k_sample(SampleArgs a)
     const int32_t k = !(t > 0.) ? 1 : a.top_k ? a.top_k[row] : a.top_k_all;
     const double p = a.top_p ? a.top_p[row] : a.top_p_all;
     const double min_p = a.min_p ? a.min_p[row] : a.min_p_all;
-    auto whole = [&](auto token) {
+    // f(x, index) over the row
+    auto whole = [&](auto f) {
         r.each([&](int, int32_t at, const Vec<T, V>& v) {
 #pragma unroll
-            for (int e = 0; e < V; ++e) token(logit_key<T>(v.e[e]), (uint32_t)(at + e));
+            for (int e = 0; e < V; ++e) f(T::load(v.e[e]), (uint32_t)(at + e));
         });
     };
-    if (k == 1) {  // the largest, whatever the other settings
-        uint32_t first = 0xffffffffu;
-        whole([&](uint32_t key, uint32_t i) { first = key == top && i < first ? i : first; });
-        if (first != 0xffffffffu) atomicMin(&s_first, first);
+    if (k == 1) {  // the largest, whatever the other settings; in the waves that saw it
+        if (__ballot(mine == top)) {
+            uint32_t first = 0xffffffffu;
+            whole([&](float x, uint32_t i) { first = x == top && i < first ? i : first; });
+            if (first != 0xffffffffu) atomicMin(&s_first, first);
+        }
         __syncthreads();
         if (tid == 0) put(s_first);
         return;
     }
 
-    const float fmax = key_logit<T>(top), fmin = key_logit<T>(low + 1);
-    const Weights weigh{(double)__builtin_fminf(fmax, kMaxF),
-                        __builtin_fmin(1.4426950408889634 / t, 1e300),
-                        __builtin_amdgcn_ldexp(1., 52 - a.bits)};
+    const Weights weigh{(double)top, __builtin_fmin(1.4426950408889634 / t, 1e300),
+                        __builtin_amdgcn_ldexp(1., 52 - a.bits), top < kInf ? -60. : 0.};
     const u64 one = 1ull << a.bits;
     const u64 least = !(min_p > 0.) ? 0 : min_p < 1. ? (u64)__builtin_ceil(min_p * (double)one) : one;
     // the row's unmasked tokens; beside an infinite one, those alone
-    const bool infinite = fmax == __builtin_inff();
-    Border border{infinite ? top : 1u, 0xffffffffu};
+    Border border{top == kInf ? kInf : -kMaxF, 0xffffffffu};
     bool in_list = false;  // the list holds all tokens that are still in question
 
-    auto tokens = [&](auto token) {
-        if (!in_list) return whole(token);
-        for (uint32_t i = tid; i < s_n; i += kSampleThreads) token(lkey[i], lidx[i]);
+    auto tokens = [&](auto f) {
+        if (!in_list) return whole(f);
+        for (uint32_t i = tid; i < s_n; i += kSampleThreads) f(key_logit<T>(lkey[i]), lidx[i]);
     };
-    auto append = [&](uint32_t key, uint32_t i) {
+    auto append = [&](float x, uint32_t i) {
         const uint32_t at = atomicAdd(&s_n, 1u);
-        if (at < kList) lkey[at] = key, lidx[at] = i;
-    };
-    auto sum_all = [&](u64 v) {
-        u64 sum;
-        __syncthreads();
-        scan_before(v, wave64, sum);
-        return sum;
+        if (at < kList) lkey[at] = logit_key<T>(x), lidx[at] = i;
     };
     // 4. the first tokens in order, of those in question and kept by the border, whose
     // values add up to target (at most the sum of all): the border behind them
     auto select = [&](auto weighted, u64 target) {
         uint32_t prefix = 0;
         u64 above = 0, here = 0;
-        auto digit = [&](auto token) {
+        auto digit = [&](auto f) {
             if (tid < 256) hist[tid] = 0;
             __syncthreads();
-            tokens(token);
+            tokens(f);
             __syncthreads();
             if (wave == 0) pick_bin(hist, target - above, &picked);
             __syncthreads();
@@ -336,54 +347,54 @@ __global__ __launch_bounds__(kSampleThreads) void k_sample(SampleArgs a)
         };
 #pragma unroll 1
         for (int shift = 8 * (kDigits - 1); shift >= 0; shift -= 8)
-            prefix |= digit([&](uint32_t key, uint32_t i) {
-                          if (border.keeps(key, i) &&
+            prefix |= digit([&](float x, uint32_t i) {
+                          const uint32_t key = logit_key<T>(x);
+                          if (border.keeps(x, i) &&
                               (u64)key >> (shift + 8) == (u64)prefix >> (shift + 8))
-                              atomicAdd(&hist[key >> shift & 255],
-                                        weighted.value ? weigh(key_logit<T>(key)) : 1ull);
+                              atomicAdd(&hist[key >> shift & 255], weighted.value ? weigh(x) : 1ull);
                       })
                       << shift;
+        const float at = key_logit<T>(prefix);
         u64 need = target - above;
         if (weighted.value) {
-            const u64 each = weigh(key_logit<T>(prefix));
+            const u64 each = weigh(at);
             need = (need + each - 1) / each;
             here /= each;
         }
-        uint32_t idx = prefix == border.key ? border.idx : 0xffffffffu;
-        if (need < here) {  // the lowest indexes of the ones at the key
+        uint32_t idx = at == border.x ? border.idx : 0xffffffffu;
+        if (need < here) {  // the lowest indexes of the ones at the logit
             idx = 0;
             target = need;
             above = 0;
 #pragma unroll 1
             for (int shift = 16; shift >= 0; shift -= 8) {
                 if (r.n <= 1 << shift) continue;
-                idx |= (255u - digit([&](uint32_t key, uint32_t i) {
-                            if (key == prefix && border.keeps(key, i) &&
+                idx |= (255u - digit([&](float x, uint32_t i) {
+                            if (x == at && border.keeps(x, i) &&
                                 i >> (shift + 8) == idx >> (shift + 8))
                                 atomicAdd(&hist[255 - (i >> shift & 255)], 1ull);
                         }))
                        << shift;
             }
         }
-        border = Border{prefix, idx};
+        border = Border{at, idx};
     };
-    // sums of value(raw logit, index) by group
+    // sums of value(x, index) by group
     auto group_sums = [&](auto value) {
         for (int i = tid; i < kSums; i += kSampleThreads) sh.sums[i] = 0;
         __syncthreads();
         int of = -1;
         u64 sum = 0;
         auto flush = [&]() {
-#pragma unroll
-            for (int d = 1; d < 64; d *= 2) sum += __shfl_xor(sum, d);
-            if (lane == 0 && of >= 0) sh.sums[of * kSampleWaves + wave] = sum;
+            sum = wave_upto(sum);
+            if (lane == 63 && of >= 0) sh.sums[of * kSampleWaves + wave] = sum;
             sum = 0;
         };
         r.each([&](int g, int32_t at, const Vec<T, V>& v) {
             if (g != of) flush();
             of = g;
 #pragma unroll
-            for (int e = 0; e < V; ++e) sum += value(v.e[e], (uint32_t)(at + e));
+            for (int e = 0; e < V; ++e) sum += value(T::load(v.e[e]), (uint32_t)(at + e));
         });
         flush();
         __syncthreads();
@@ -392,27 +403,44 @@ __global__ __launch_bounds__(kSampleThreads) void k_sample(SampleArgs a)
     // 2. and 3.
     bool summed = false;  // weights outside the list are in the groups' sums
     const bool by_p = p < 1.;
-    if ((k > 0 && k < r.n) || by_p) {
-        // steps over the row's range, or as far as weights are not 0
-        const double range = weigh.max - fmin, reach = 36. * t;
-        const double span = infinite ? 0. : range < reach ? range : reach;
-        const float per = (float)(kBins / span);
-        auto bin = [&](uint32_t key) {
-            const float b = (fmax - key_logit<T>(key)) * per;
-            return (uint32_t)(b < (float)(kBins - 1) ? (int)b : b == b ? kBins - 1 : 0);
-        };
-        whole([&](uint32_t key, uint32_t i) {
-            if (border.keeps(key, i)) atomicAdd(&sh.bins[bin(key)], 1u);
-        });
-        __syncthreads();
-        uint32_t c[4], sum = 0, total;
+    bool by_k = k > 0 && k < r.n;
+    if (by_k || by_p) {
+        // steps as far as weights are not 0, or over the row's range where that is less
+        double span = 36. * t;
+        float per = (float)(kBins / span);
+        if (span > 512.) {
+            float least_x = kInf;
+            whole([&](float x, uint32_t) {
+                least_x = __builtin_fminf(least_x, x > -kInf ? x : kInf);
+            });
 #pragma unroll
-        for (int j = 0; j < 4; ++j) sum += c[j] = sh.bins[4 * tid + j];
-        const uint32_t before = scan_before(sum, wave_a, total);
-        const bool by_k = k > 0 && total > (uint32_t)k;
-        u64 outside = 0;  // weights above the list's
-        u64 target = 0;
-        if (by_k) {
+            for (int d = 1; d < 64; d *= 2) least_x = __builtin_fminf(least_x, __shfl_xor(least_x, d));
+            if (lane == 0) wave_max[wave] = least_x;
+            __syncthreads();
+#pragma unroll
+            for (int w = 0; w < kSampleWaves; ++w) least_x = __builtin_fminf(least_x, wave_max[w]);
+            const double range = weigh.max - least_x;
+            if (range < span) {
+                span = range;
+                per = (float)((kBins - 1) / span);
+            }
+        }
+        const bool stepped = top < kInf && span > 0. && per < kInf;
+        // descending with x; kBins for a masked one or one of no weight
+        auto bin = [&](float x) {
+            return (uint32_t)__builtin_fminf((top - x) * per, (float)kBins);
+        };
+        uint32_t c[4], before = 0;
+        auto count = [&]() {
+            uint32_t sum[1] = {0}, all[1];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) sum[0] += c[j] = sh.bins[4 * tid + j];
+            scan_before(sum, wave32, all);
+            before = sum[0];
+            return all[0];
+        };
+        // the step in which the k-th counted token lies, and the tokens up to it
+        auto find_k = [&]() {
             uint32_t at = before;
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
@@ -420,45 +448,71 @@ __global__ __launch_bounds__(kSampleThreads) void k_sample(SampleArgs a)
                 at += c[j];
             }
             __syncthreads();
-            if (s_c2 <= kList) {
-                const uint32_t b2 = s_b2;
-                whole([&](uint32_t key, uint32_t i) {
-                    if (border.keeps(key, i) && bin(key) <= b2) append(key, i);
-                });
-                __syncthreads();
-                in_list = true;
+        };
+        auto list_to = [&](uint32_t last) {
+            whole([&](float x, uint32_t i) {
+                if ((top - x) * per < (float)(last + 1)) append(x, i);
+            });
+            __syncthreads();
+            in_list = s_n <= kList;
+        };
+        if (by_k && stepped && k <= kSampleThreads) {
+            if (const uint32_t b = bin(mine); b < kBins) atomicAdd(&sh.bins[b], 1u);
+            __syncthreads();
+            if (count() >= (uint32_t)k) {
+                find_k();
+                list_to(s_b2);
             }
-            select(std::false_type{}, (u64)k);
-            if (by_p) {
-                u64 s = 0;
-                tokens([&](uint32_t key, uint32_t i) {
-                    if (border.keeps(key, i)) s += weigh(key_logit<T>(key));
-                });
-                target = sum_all(s);
+        }
+        u64 target = 0, outside = 0;  // weights; outside: of those above the list's
+        bool counted = false;
+        if (!in_list && stepped) {
+            __syncthreads();
+            for (int b = tid; b < kBins; b += kSampleThreads) sh.bins[b] = 0;
+            if (tid == 0) s_n = 0, s_b2 = kBins - 1;
+            __syncthreads();
+            whole([&](float x, uint32_t) {
+                if (const uint32_t b = bin(x); b < kBins) atomicAdd(&sh.bins[b], 1u);
+            });
+            __syncthreads();
+            const uint32_t n = count();
+            by_k = by_k && n > (uint32_t)k;  // else all that have a weight
+            counted = true;
+            if (by_k) {
+                find_k();
+                if (s_c2 <= kList) list_to(s_b2);
             }
-        } else if (by_p) {
+        } else if (!stepped && by_k) {
+            u64 n[1] = {0}, all[1];
+            whole([&](float x, uint32_t i) { n[0] += border.keeps(x, i); });
+            __syncthreads();
+            scan_before(n, wave64, all);
+            by_k = all[0] > (u64)k;
+        }
+        if (by_k) select(std::false_type{}, (u64)k);
+        if (by_p && !by_k && counted) {
             // bounds of the weights of each step, and of their sums
-            const float step = (float)(span * weigh.scale / kBins);
-            double lo[4], hi[4], lo4 = 0., hi4 = 0., lo_all, hi_all;
+            const float step = (float)(weigh.scale / (double)per);
+            double lo[4], hi[4], sum[2] = {0., 0.}, all[2];
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 const float b = (float)(4 * tid + j);
-                lo[j] = b < (float)(kBins - 1) ? c[j] * (double)exp2_hw(-step * (b + 1.f)) * 0.9999 : 0.;
+                lo[j] = c[j] * (double)exp2_hw(-step * (b + 1.f)) * 0.9999;
                 hi[j] = c[j] * (double)exp2_hw(-step * b) * 1.0001;
-                lo4 += lo[j];
-                hi4 += hi[j];
+                sum[0] += lo[j];
+                sum[1] += hi[j];
             }
-            double l = scan_before(lo4, wave_lo, lo_all), h = scan_before(hi4, wave_hi, hi_all);
+            scan_before(sum, bounds, all);
             uint32_t b1 = kBins - 1, b2 = kBins - 1;
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                l += lo[j];
-                h += hi[j];
-                if (h >= p * lo_all && b1 == kBins - 1) b1 = 4 * tid + j;
-                if (l >= p * hi_all && b2 == kBins - 1) b2 = 4 * tid + j;
+                sum[0] += lo[j];
+                sum[1] += hi[j];
+                if (sum[1] >= p * all[0] && b1 == kBins - 1) b1 = 4 * tid + j;
+                if (sum[0] >= p * all[1] && b2 == kBins - 1) b2 = 4 * tid + j;
             }
-            atomicMin(&s_b1, b1);
-            atomicMin(&s_b2, b2);
+            if (b1 < kBins - 1) atomicMin(&s_b1, b1);
+            if (b2 < kBins - 1) atomicMin(&s_b2, b2);
             __syncthreads();
             b1 = s_b1;
             b2 = s_b2;
@@ -470,87 +524,81 @@ __global__ __launch_bounds__(kSampleThreads) void k_sample(SampleArgs a)
                 if ((uint32_t)(4 * tid + j) == b2) s_c2 = at;
             }
             __syncthreads();
-            const bool fits = s_c2 - s_c1 <= kList;
-            u64 weights = 0, listed = 0;
-            group_sums([&](E raw, uint32_t i) -> u64 {
-                const uint32_t key = logit_key<T>(raw);
-                if (!border.keeps(key, i)) return 0;
-                const u64 v = weigh(T::load(raw));
-                const uint32_t b = bin(key);
-                weights += v;
-                if (b < b1) {
-                    outside += v;
-                } else if (b <= b2) {
-                    listed += v;
-                    if (fits) append(key, i);
+            const bool fits = s_c2 - s_c1 <= kList;  // before the list, not to fill it in vain
+            u64 w[3] = {0, 0, 0}, sums[3];  // of all, above the list, in it
+            const float f1 = (float)b1, f2 = (float)(b2 + 1);
+            group_sums([&](float x, uint32_t i) -> u64 {
+                const u64 v = weigh(x);
+                const float d = (top - x) * per;
+                w[0] += v;
+                if (d < f1) {
+                    w[1] += v;
+                    return v >= least ? v : 0;
                 }
-                return b < b1 && v >= least ? v : 0;
+                if (d < f2) {
+                    w[2] += v;
+                    if (fits) append(x, i);
+                }
+                return 0;
             });
-            target = sum_all(weights);
-            outside = sum_all(outside);
-            listed = sum_all(listed);
-            const u64 want = min_share(p, target);
+            scan_before(w, wave64, sums);
+            target = min_share(p, sums[0]);
             // the bounds are rounded: the sums decide
-            in_list = summed = fits && outside < want && want - outside <= listed;
-            if (!in_list) outside = 0;
+            in_list = summed = fits && s_n <= kList && sums[1] < target && target - sums[1] <= sums[2];
+            if (in_list) outside = sums[1];
+        } else if (by_p) {
+            u64 w[1] = {0}, all[1];
+            tokens([&](float x, uint32_t i) { w[0] += border.keeps(x, i) ? weigh(x) : 0; });
+            __syncthreads();
+            scan_before(w, wave64, all);
+            target = min_share(p, all[0]);
         }
-        if (by_p) select(std::true_type{}, min_share(p, target) - outside);
+        if (by_p) select(std::true_type{}, target - outside);
     }
 
     // 5. sums of what is kept
-    auto kept = [&](uint32_t key, uint32_t i) -> u64 {
-        if (!border.keeps(key, i)) return 0;
-        const u64 v = weigh(key_logit<T>(key));
+    auto kept = [&](float x, uint32_t i) -> u64 {
+        if (!border.keeps(x, i)) return 0;
+        const u64 v = weigh(x);
         return v >= least ? v : 0;
     };
+    __syncthreads();
     if (in_list) {
-        if (!summed) {
-            __syncthreads();
+        if (!summed)
             for (int i = tid; i < kSums; i += kSampleThreads) sh.sums[i] = 0;
-        }
         __syncthreads();
-        tokens([&](uint32_t key, uint32_t i) {
-            if (const u64 v = kept(key, i)) atomicAdd(&sh.sums[i / R::kPiece / r.G], v);
+        tokens([&](float x, uint32_t i) {
+            if (const u64 v = kept(x, i)) atomicAdd(&sh.sums[i / R::kPiece / r.G], v);
         });
         __syncthreads();
+    } else if (border.x == -kMaxF && border.idx == 0xffffffffu && least == 0) {
+        group_sums([&](float x, uint32_t) { return weigh(x); });
     } else {
-        __syncthreads();
-        group_sums([&](E raw, uint32_t i) { return kept(logit_key<T>(raw), i); });
+        group_sums(kept);
     }
     // each wave finds the group, whose wave goes on
     static_assert(kSums == 128, "two sums a lane");
     const u64 s0 = sh.sums[2 * lane], s1 = sh.sums[2 * lane + 1];
-    u64 upto = s0 + s1;
-#pragma unroll
-    for (int d = 1; d < 64; d *= 2) {
-        const u64 o = __shfl_up(upto, d);
-        if (lane >= d) upto += o;
-    }
-    const u64 sum = __shfl(upto, 63);
+    const u64 upto = wave_upto(s0 + s1), sum = lane64(upto, 63);
     double share = (double)a.u[row];
     share = share > 0. ? share : 0.;
     u64 target = share < 1. ? (u64)(share * (double)sum) : sum - 1;
     target = target < sum ? target : sum - 1;
-    const u64 hit = __ballot(upto > target);
-    const int win = __builtin_ctzll(hit);
+    const int win = __builtin_ctzll(__ballot(upto > target));
     u64 before = upto - s0 - s1;
     const bool second = before + s0 <= target;
     if (second) before += s0;
-    const int group = __shfl(2 * lane + second, win);
-    before = __shfl(before, win);
+    const int group = __builtin_amdgcn_readlane(2 * lane + second, win);
+    before = lane64(before, win);
     if (group % kSampleWaves != wave) return;
     for (int32_t i = 0; i < r.G; ++i) {
-        const int32_t at = (group * r.G + i) * R::kPiece + lane * V;
-        const Vec<T, V> v = r.load(at);
+        const int32_t first = (group * r.G + i) * R::kPiece, at = first + lane * V;
+        if (first >= r.n) return;
+        const Vec<T, V> v = r.load(first);
         u64 x[V], mine = 0;
 #pragma unroll
-        for (int e = 0; e < V; ++e) mine += x[e] = kept(logit_key<T>(v.e[e]), (uint32_t)(at + e));
-        u64 up = mine;
-#pragma unroll
-        for (int d = 1; d < 64; d *= 2) {
-            const u64 o = __shfl_up(up, d);
-            if (lane >= d) up += o;
-        }
+        for (int e = 0; e < V; ++e) mine += x[e] = kept(T::load(v.e[e]), (uint32_t)(at + e));
+        const u64 up = wave_upto(mine);
         const u64 mask = __ballot(before + up > target);
         if (mask) {
             if (lane != __builtin_ctzll(mask)) return;
@@ -564,7 +612,7 @@ __global__ __launch_bounds__(kSampleThreads) void k_sample(SampleArgs a)
                 before += x[e];
             }
         }
-        before += __shfl(up, 63);
+        before += lane64(up, 63);
     }
 }
 
