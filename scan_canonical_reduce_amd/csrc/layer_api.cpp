@@ -327,6 +327,7 @@ canon_status_t canon_sample(const canon_sample_t* c, void* ws, size_t ws_bytes, 
     int log = 0;
     while (((int64_t)1 << log) < c->vocab) ++log;
     a.bits = log < 12 ? 50 : 62 - log;
+    a.share_bits = log < 16 ? 15 : 31 - log;
     a.u = c->u;
     a.temperature = c->temperature;
     a.top_p = c->top_p;

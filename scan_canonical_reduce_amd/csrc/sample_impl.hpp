@@ -10,11 +10,12 @@
 //   1. Each thread's largest logit, and the row's.
 //   2. With a filter, tokens counted in kBins equal steps of the logit from the largest
 //      down.  For top_k the threads' largest ones suffice: where k of them lie, k
-//      tokens do, and not many more.  For top_p (or a large k) all are counted; as a
-//      step's weights are known to a step, the border lies between two known steps.
+//      tokens do, and not many more.  For a larger k all are counted; for top_p their
+//      weights are added up, to 14 bits, which tells the border's step (or two).
 //   3. The tokens in question go to a list in LDS: for top_k all from the border's step
 //      up, for top_p those of its steps, while all weights are summed.
-//   4. The border is found in the list digit by digit, by counts or sums of weights.
+//   4. In a short list every token is compared with every other; in a longer one the
+//      border is found digit by digit, by counts or sums of weights.
 //   5. Sums of the kept weights by pieces of the row in index order, the piece in
 //      which u's share falls, and the token in it.
 // Where a list does not fit (thousands of tokens in a step, as where all are equal),
@@ -35,6 +36,7 @@ constexpr int kSampleThreads = 1024;
 constexpr int kSampleWaves = kSampleThreads / 64;
 constexpr int kBins = 4 * kSampleThreads;
 constexpr int kList = 6144;
+constexpr int kRank = 256;  // tokens of a list that are compared with each other
 constexpr int kSums = 8 * kSampleWaves;
 constexpr float kInf = __builtin_inff();
 
@@ -252,11 +254,15 @@ __global__ __launch_bounds__(kSampleThreads) void k_sample(SampleArgs a)
     } sh;
     __shared__ uint32_t lkey[kList], lidx[kList];
     __shared__ u64 hist[256], wave64[3][kSampleWaves];
-    __shared__ double bounds[2][kSampleWaves];
+    __shared__ double bounds[1][kSampleWaves];
+    __shared__ struct {
+        u64 place, weight;
+    } entry[kRank];
+    __shared__ Border s_border;
     __shared__ uint32_t wave32[1][kSampleWaves];
     __shared__ float wave_max[kSampleWaves];
     __shared__ Picked picked;
-    __shared__ uint32_t s_n, s_first, s_b1, s_b2, s_c1, s_c2;
+    __shared__ uint32_t s_n, s_first, s_b1, s_b2, s_c2;
     const int64_t row = blockIdx.x;
     const int tid = threadIdx.x, lane = tid & 63, wave = uniform((int32_t)(tid >> 6));
     R r;
@@ -379,6 +385,46 @@ __global__ __launch_bounds__(kSampleThreads) void k_sample(SampleArgs a)
         }
         border = Border{at, idx};
     };
+    // the same for a list of up to kRank tokens, all kept by the border so far: the
+    // first `most` of them (at least one), and with by_p of those the first whose
+    // weights, with those outside the list, make target (0: their share p)
+    auto rank = [&](uint32_t most, bool by_p, u64 target, u64 outside) {
+        const uint32_t n = s_n;
+        int each = kSampleThreads / kRank;  // threads a token
+        while (n * each * 2 <= kSampleThreads && each < 64) each *= 2;
+        const uint32_t i = tid / each, q = tid & (each - 1);
+        if (tid < n) {
+            entry[tid].place = (u64)lkey[tid] << 32 | ~lidx[tid];
+            entry[tid].weight = weigh(key_logit<T>(lkey[tid]));
+        }
+        __syncthreads();
+        const bool on = i < n;
+        const u64 place = on ? entry[i].place : 0;
+        u64 before = 0;
+        uint32_t place_no = 0;
+        for (uint32_t j = q; j < n; j += each) {
+            const bool first = entry[j].place > place;
+            before += first ? entry[j].weight : 0;
+            place_no += first;
+        }
+        for (int d = 1; d < each; d *= 2) {
+            before += __shfl_xor(before, d);
+            place_no += __shfl_xor(place_no, d);
+        }
+        const u64 mine = on ? entry[i].weight : 0;
+        most = most < n ? most : n;
+        const bool first = on && q == 0 && place_no < most;
+        if (by_p && target == 0) {
+            u64 v[1] = {first ? mine : 0}, all[1];
+            scan_before(v, wave64, all);
+            target = min_share(p, all[0]);
+        }
+        if (first && (!by_p || outside + before < target) &&
+            (place_no + 1 == most || (by_p && outside + before + mine >= target)))
+            s_border = Border{key_logit<T>((uint32_t)(place >> 32)), ~(uint32_t)place};
+        __syncthreads();
+        border = s_border;
+    };
     // sums of value(x, index) by group
     auto group_sums = [&](auto value) {
         for (int i = tid; i < kSums; i += kSampleThreads) sh.sums[i] = 0;
@@ -430,24 +476,20 @@ __global__ __launch_bounds__(kSampleThreads) void k_sample(SampleArgs a)
         auto bin = [&](float x) {
             return (uint32_t)__builtin_fminf((top - x) * per, (float)kBins);
         };
-        uint32_t c[4], before = 0;
-        auto count = [&]() {
-            uint32_t sum[1] = {0}, all[1];
+        // the step in which the k-th counted token lies goes to s_b2; or false
+        auto find_k = [&]() {
+            uint32_t c[4], sum[1] = {0}, all[1];
 #pragma unroll
             for (int j = 0; j < 4; ++j) sum[0] += c[j] = sh.bins[4 * tid + j];
             scan_before(sum, wave32, all);
-            before = sum[0];
-            return all[0];
-        };
-        // the step in which the k-th counted token lies, and the tokens up to it
-        auto find_k = [&]() {
-            uint32_t at = before;
+            uint32_t at = sum[0];
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 if (at < (uint32_t)k && at + c[j] >= (uint32_t)k) s_b2 = 4 * tid + j, s_c2 = at + c[j];
                 at += c[j];
             }
             __syncthreads();
+            return all[0] >= (uint32_t)k;
         };
         auto list_to = [&](uint32_t last) {
             whole([&](float x, uint32_t i) {
@@ -456,104 +498,106 @@ __global__ __launch_bounds__(kSampleThreads) void k_sample(SampleArgs a)
             __syncthreads();
             in_list = s_n <= kList;
         };
-        if (by_k && stepped && k <= kSampleThreads) {
-            if (const uint32_t b = bin(mine); b < kBins) atomicAdd(&sh.bins[b], 1u);
-            __syncthreads();
-            if (count() >= (uint32_t)k) {
-                find_k();
-                list_to(s_b2);
-            }
-        }
-        u64 target = 0, outside = 0;  // weights; outside: of those above the list's
-        bool counted = false;
-        if (!in_list && stepped) {
+        auto clear = [&]() {
             __syncthreads();
             for (int b = tid; b < kBins; b += kSampleThreads) sh.bins[b] = 0;
             if (tid == 0) s_n = 0, s_b2 = kBins - 1;
             __syncthreads();
-            whole([&](float x, uint32_t) {
-                if (const uint32_t b = bin(x); b < kBins) atomicAdd(&sh.bins[b], 1u);
-            });
-            __syncthreads();
-            const uint32_t n = count();
-            by_k = by_k && n > (uint32_t)k;  // else all that have a weight
-            counted = true;
-            if (by_k) {
-                find_k();
-                if (s_c2 <= kList) list_to(s_b2);
+        };
+        if (by_k && stepped) {
+            if (k <= kSampleThreads) {
+                if (const uint32_t b = bin(mine); b < kBins) atomicAdd(&sh.bins[b], 1u);
+                __syncthreads();
+                if (find_k()) list_to(s_b2);
             }
-        } else if (!stepped && by_k) {
+            if (!in_list) {
+                clear();
+                whole([&](float x, uint32_t) {
+                    if (const uint32_t b = bin(x); b < kBins) atomicAdd(&sh.bins[b], 1u);
+                });
+                __syncthreads();
+                by_k = find_k();  // else all that have a weight
+                if (by_k && s_c2 <= kList) list_to(s_b2);
+            }
+        } else if (by_k) {
             u64 n[1] = {0}, all[1];
             whole([&](float x, uint32_t i) { n[0] += border.keeps(x, i); });
             __syncthreads();
             scan_before(n, wave64, all);
             by_k = all[0] > (u64)k;
         }
-        if (by_k) select(std::false_type{}, (u64)k);
-        if (by_p && !by_k && counted) {
-            // bounds of the weights of each step, and of their sums
-            const float step = (float)(weigh.scale / (double)per);
-            double lo[4], hi[4], sum[2] = {0., 0.}, all[2];
+        if (by_k && in_list && s_n <= kRank) {
+            rank((uint32_t)k, by_p, 0, 0);
+        } else {
+            if (by_k) select(std::false_type{}, (u64)k);
+            u64 target = 0, outside = 0;  // weights; outside: of those above the list's
+            if (by_p && !by_k && stepped) {
+                clear();
+                // A weight is its step's largest, 2^(-step b), times 1 - frac step ln 2, less
+                // than 2^-14 off (a step is 52 / 4096 at most): integers again, whose
+                // sums stay below 2^32 (adding 32-bit floats here takes 10 times as long)
+                const float step = (float)(weigh.scale / (double)per);
+                const float whole_step = __uint_as_float((uint32_t)(127 + a.share_bits) << 23);
+                const float slope = -step * kLn2 * whole_step;
+                whole([&](float x, uint32_t) {
+                    const float d = (top - x) * per;
+                    if (d < (float)kBins)
+                        atomicAdd(&sh.bins[(uint32_t)d],
+                                  (uint32_t)fma32(__builtin_amdgcn_fractf(d), slope, whole_step));
+                });
+                __syncthreads();
+                double c[4], sum[1] = {0.}, all[1];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const float b = (float)(4 * tid + j);
-                lo[j] = c[j] * (double)exp2_hw(-step * (b + 1.f)) * 0.9999;
-                hi[j] = c[j] * (double)exp2_hw(-step * b) * 1.0001;
-                sum[0] += lo[j];
-                sum[1] += hi[j];
-            }
-            scan_before(sum, bounds, all);
-            uint32_t b1 = kBins - 1, b2 = kBins - 1;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                sum[0] += lo[j];
-                sum[1] += hi[j];
-                if (sum[1] >= p * all[0] && b1 == kBins - 1) b1 = 4 * tid + j;
-                if (sum[0] >= p * all[1] && b2 == kBins - 1) b2 = 4 * tid + j;
-            }
-            if (b1 < kBins - 1) atomicMin(&s_b1, b1);
-            if (b2 < kBins - 1) atomicMin(&s_b2, b2);
-            __syncthreads();
-            b1 = s_b1;
-            b2 = s_b2;
-            uint32_t at = before;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                if ((uint32_t)(4 * tid + j) == b1) s_c1 = at;
-                at += c[j];
-                if ((uint32_t)(4 * tid + j) == b2) s_c2 = at;
-            }
-            __syncthreads();
-            const bool fits = s_c2 - s_c1 <= kList;  // before the list, not to fill it in vain
-            u64 w[3] = {0, 0, 0}, sums[3];  // of all, above the list, in it
-            const float f1 = (float)b1, f2 = (float)(b2 + 1);
-            group_sums([&](float x, uint32_t i) -> u64 {
-                const u64 v = weigh(x);
-                const float d = (top - x) * per;
-                w[0] += v;
-                if (d < f1) {
-                    w[1] += v;
-                    return v >= least ? v : 0;
+                for (int j = 0; j < 4; ++j) {
+                    c[j] = (double)sh.bins[4 * tid + j] *
+                           (double)exp2_hw(-step * (float)(4 * tid + j));
+                    sum[0] += c[j];
                 }
-                if (d < f2) {
-                    w[2] += v;
-                    if (fits) append(x, i);
+                scan_before(sum, bounds, all);
+                uint32_t b1 = kBins - 1, b2 = kBins - 1;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    sum[0] += c[j];
+                    if (sum[0] >= p * 0.9999 * all[0] && b1 == kBins - 1) b1 = 4 * tid + j;
+                    if (sum[0] >= p * 1.0001 * all[0] && b2 == kBins - 1) b2 = 4 * tid + j;
                 }
-                return 0;
-            });
-            scan_before(w, wave64, sums);
-            target = min_share(p, sums[0]);
-            // the bounds are rounded: the sums decide
-            in_list = summed = fits && s_n <= kList && sums[1] < target && target - sums[1] <= sums[2];
-            if (in_list) outside = sums[1];
-        } else if (by_p) {
-            u64 w[1] = {0}, all[1];
-            tokens([&](float x, uint32_t i) { w[0] += border.keeps(x, i) ? weigh(x) : 0; });
-            __syncthreads();
-            scan_before(w, wave64, all);
-            target = min_share(p, all[0]);
+                if (b1 < kBins - 1) atomicMin(&s_b1, b1);
+                if (b2 < kBins - 1) atomicMin(&s_b2, b2);
+                __syncthreads();
+                u64 w[3] = {0, 0, 0}, sums[3];  // of all, above the list, in it
+                const float f1 = (float)s_b1, f2 = (float)(s_b2 + 1);
+                group_sums([&](float x, uint32_t i) -> u64 {
+                    const u64 v = weigh(x);
+                    const float d = (top - x) * per;
+                    w[0] += v;
+                    if (d < f1) {
+                        w[1] += v;
+                        return v >= least ? v : 0;
+                    }
+                    if (d < f2) {
+                        w[2] += v;
+                        append(x, i);
+                    }
+                    return 0;
+                });
+                scan_before(w, wave64, sums);
+                target = min_share(p, sums[0]);
+                // the steps' sums are rounded: these decide
+                in_list = summed =
+                    s_n <= kList && sums[1] < target && target - sums[1] <= sums[2];
+                if (in_list) outside = sums[1];
+            } else if (by_p) {
+                u64 w[1] = {0}, all[1];
+                tokens([&](float x, uint32_t i) { w[0] += border.keeps(x, i) ? weigh(x) : 0; });
+                __syncthreads();
+                scan_before(w, wave64, all);
+                target = min_share(p, all[0]);
+            }
+            if (by_p && summed && s_n <= kRank)
+                rank(kRank, true, target, outside);
+            else if (by_p)
+                select(std::true_type{}, target - outside);
         }
-        if (by_p) select(std::true_type{}, target - outside);
     }
 
     // 5. sums of what is kept
@@ -571,8 +615,11 @@ __global__ __launch_bounds__(kSampleThreads) void k_sample(SampleArgs a)
             if (const u64 v = kept(x, i)) atomicAdd(&sh.sums[i / R::kPiece / r.G], v);
         });
         __syncthreads();
-    } else if (border.x == -kMaxF && border.idx == 0xffffffffu && least == 0) {
-        group_sums([&](float x, uint32_t) { return weigh(x); });
+    } else if (border.x == -kMaxF && border.idx == 0xffffffffu) {  // all, masked ones weigh 0
+        group_sums([&](float x, uint32_t) {
+            const u64 v = weigh(x);
+            return v >= least ? v : 0;
+        });
     } else {
         group_sums(kept);
     }
