@@ -44,12 +44,13 @@ __device__ __forceinline__ void column_sum_block(const ColumnSums& a, int64_t bl
     if (c < j.cols) {
         const float* p = j.part + c;
         int64_t r = w;
-        for (; r + 3 * kColLanes < a.rows; r += 4 * kColLanes) {
-            float v[4];
+        constexpr int U = 8;  // rows in flight
+        for (; r + (U - 1) * kColLanes < a.rows; r += U * kColLanes) {
+            float v[U];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) v[i] = p[(r + i * kColLanes) * j.cols];
+            for (int i = 0; i < U; ++i) v[i] = p[(r + i * kColLanes) * j.cols];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) s += v[i];
+            for (int i = 0; i < U; ++i) s += v[i];
         }
         for (; r < a.rows; r += kColLanes) s += p[r * j.cols];
     }

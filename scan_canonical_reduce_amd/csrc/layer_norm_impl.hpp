@@ -13,32 +13,106 @@ namespace seq {
 template <typename T>
 constexpr int kNormV = 16 / sizeof(typename T::store_t);
 
-// Columns [col, col + V) of a row as 32-bit values, 0 beyond its width.
-template <typename T, int V>
-__device__ __forceinline__ void ld_cols(const typename T::store_t* p, int col, int width,
-                                        float (&v)[V])
+// 16 bytes of a row, as words: kNormV elements.
+typedef uint32_t Words16 __attribute__((ext_vector_type(4)));
+
+template <typename T>
+__device__ __forceinline__ float element(const Words16& w, int j)
 {
-    if (col + V <= width) {
-        const Vec<T, V> r = ld_any<T, V, false>(p + col);
+    if constexpr (std::is_same<T, F32>::value)
+        return __uint_as_float(w[j]);
+    else if constexpr (std::is_same<T, BF16>::value)
+        return __uint_as_float(j & 1 ? w[j / 2] & 0xffff0000u : w[j / 2] << 16);
+    else
+        return T::load((uint16_t)(w[j / 2] >> 16 * (j & 1)));
+}
+template <typename T>
+__device__ __forceinline__ Words16 rounded(const float* v)
+{
+    Words16 w;
 #pragma unroll
-        for (int j = 0; j < V; ++j) v[j] = T::load(r.e[j]);
+    for (int i = 0; i < 4; ++i) {
+        if constexpr (std::is_same<T, F32>::value)
+            w[i] = __float_as_uint(v[i]);
+        else
+            w[i] = T::round(v[2 * i]) | (uint32_t)T::round(v[2 * i + 1]) << 16;
+    }
+    return w;
+}
+// The words moved up by one element, and down.
+template <typename T>
+__device__ __forceinline__ Words16 push(Words16 w, typename T::store_t e)
+{
+    if constexpr (std::is_same<T, F32>::value) return Words16{__float_as_uint(e), w.x, w.y, w.z};
+    return Words16{w.x << 16 | (uint32_t)e, w.y << 16 | w.x >> 16, w.z << 16 | w.y >> 16,
+                   w.w << 16 | w.z >> 16};
+}
+template <typename T>
+__device__ __forceinline__ Words16 pop(Words16 w)
+{
+    if constexpr (std::is_same<T, F32>::value) return Words16{w.y, w.z, w.w, 0};
+    return Words16{w.x >> 16 | w.y << 16, w.y >> 16 | w.z << 16, w.z >> 16 | w.w << 16, w.w >> 16};
+}
+
+// Element c of a row: a base that a wave shares and an offset of 32 bits (a width is
+// below 2^24), so that no lane holds addresses of 64 bits.
+template <typename E>
+__device__ __forceinline__ E* row_at(E* row, int c)
+{
+    return (E*)((char*)row + (uint32_t)(c * (int)sizeof(E)));
+}
+
+// The 16 bytes from column c on, zero beyond the row's width; and their store.  The
+// elements of a vector that the row's end cuts are taken one by one.
+template <typename T>
+__device__ __forceinline__ Words16 ld16(const typename T::store_t* row, int c, int width)
+{
+    constexpr int V = kNormV<T>;
+    Words16 w = {0, 0, 0, 0};
+    if (c + V <= width) {
+        __builtin_memcpy(&w, row_at(row, c), 16);
+    } else if (c < width) {
+#pragma unroll 1
+        for (int j = width - 1; j >= c; --j) w = push<T>(w, *row_at(row, j));
+    }
+    return w;
+}
+template <typename T>
+__device__ __forceinline__ void st16(typename T::store_t* row, int c, int width, Words16 w)
+{
+    constexpr int V = kNormV<T>;
+    if (c + V <= width) {
+        __builtin_memcpy(row_at(row, c), &w, 16);
     } else {
-#pragma unroll
-        for (int j = 0; j < V; ++j) v[j] = col + j < width ? T::load(p[col + j]) : 0.f;
+#pragma unroll 1
+        for (; c < width; ++c, w = pop<T>(w)) {
+            if constexpr (std::is_same<T, F32>::value)
+                *row_at(row, c) = __uint_as_float(w.x);
+            else
+                *row_at(row, c) = (uint16_t)w.x;
+        }
     }
 }
 
+// Columns [c, c + V) as 32-bit values, 0 beyond the row's width; and their store.
 template <typename T, int V>
-__device__ __forceinline__ void st_cols(typename T::store_t* p, int col, int width,
+__device__ __forceinline__ void ld_cols(const typename T::store_t* row, int c, int width,
+                                        float (&v)[V])
+{
+    constexpr int N = kNormV<T>;
+#pragma unroll
+    for (int h = 0; h < V; h += N) {
+        const Words16 w = ld16<T>(row, c + h, width);
+#pragma unroll
+        for (int j = 0; j < N; ++j) v[h + j] = element<T>(w, j);
+    }
+}
+template <typename T, int V>
+__device__ __forceinline__ void st_cols(typename T::store_t* row, int c, int width,
                                         const float (&v)[V])
 {
-    if (col + V <= width) {
-        st_any<T, V, false>(p + col, v);
-    } else {
 #pragma unroll
-        for (int j = 0; j < V; ++j)
-            if (col + j < width) p[col + j] = T::round(v[j]);
-    }
+    for (int h = 0; h < V; h += kNormV<T>) st16<T>(row, c + h, width, rounded<T>(v + h));
 }
 
 template <int V>
@@ -54,24 +128,46 @@ __device__ __forceinline__ float tree(const float (&v)[V])
     return t[0];
 }
 
-// The pairwise tree over the lanes of a team (a power of two of lanes that lie
-// together, whole waves beyond 64), in every lane.  lds: the team's waves' values;
-// not to be used again before the next barrier but one.
-template <int TEAM>
-__device__ __forceinline__ float team_sum(float v, float* lds)
+// Sums over the lanes of a team (a power of two of lanes that lie together, whole waves
+// beyond 64) by the pairwise tree, in every lane, N of them with one barrier.  lds: each
+// wave's sums; not to be used again before the next barrier but one.
+template <int TEAM, int N>
+__device__ __forceinline__ void team_sums(float (&v)[N], float (*lds)[N])
 {
+    static_assert(TEAM >= 16, "rows of 16 lanes");
 #pragma unroll
-    for (int d = 1; d < (TEAM < 64 ? TEAM : 64); d *= 2) v += __shfl_xor(v, d);
+    for (int i = 0; i < N; ++i) {
+        v[i] += dpp<0xb1>(v[i]);   // quads: the neighbour,
+        v[i] += dpp<0x4e>(v[i]);   // the other pair;
+        v[i] += dpp<0x141>(v[i]);  // the other quad of eight, mirrored,
+        v[i] += dpp<0x140>(v[i]);  // the other eight of sixteen
+        if constexpr (TEAM >= 64) {
+            v[i] = fold_rows(v[i], v[i]);
+            v[i] = fold_halves(v[i], v[i]);
+        }
+    }
     if constexpr (TEAM > 64) {
         constexpr int W = TEAM / 64;
-        if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = v;
-        __syncthreads();
-        float w[W];
+        if ((threadIdx.x & 63) == 0) {
 #pragma unroll
-        for (int i = 0; i < W; ++i) w[i] = lds[i];
-        v = tree(w);
+            for (int i = 0; i < N; ++i) lds[threadIdx.x >> 6][i] = v[i];
+        }
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            float w[W];
+#pragma unroll
+            for (int j = 0; j < W; ++j) w[j] = lds[j][i];
+            v[i] = tree(w);
+        }
     }
-    return v;
+}
+template <int TEAM>
+__device__ __forceinline__ float team_sum(float v, float (*lds)[1])
+{
+    float s[1] = {v};
+    team_sums<TEAM>(s, lds);
+    return s[0];
 }
 
 template <typename T>
@@ -90,26 +186,24 @@ __device__ __forceinline__ typename T::store_t* norm_row(const canon_rows_t& r, 
 // in registers.  A row's sum adds each vector by a tree, a lane's vectors in order, and
 // the lanes by the pairwise tree: the team, and with it the expression, goes by the
 // width and the type alone.
-template <typename T, int NV>
-using Raw = Vec<T, kNormV<T>>[NV];
+template <int NV>
+using Raw = Words16[NV];
 
 template <typename T, int TEAM, int NV>
-__device__ __forceinline__ void ld_row(const typename T::store_t* p, int lane, int width,
-                                       Raw<T, NV>& r)
+__device__ __forceinline__ void ld_row(const typename T::store_t* row, int lane, int width,
+                                       Raw<NV>& r)
 {
-    constexpr int V = kNormV<T>;
 #pragma unroll
-    for (int k = 0; k < NV; ++k) {
-        const int c = (k * TEAM + lane) * V;
-        if (c + V <= width) {
-            r[k] = ld_any<T, V, false>(p + c);
-        } else {
-            r[k] = Vec<T, V>{};
+    for (int k = 0; k < NV; ++k) r[k] = ld16<T>(row, (k * TEAM + lane) * kNormV<T>, width);
+}
+
+// The same values, as if loaded again: what was computed from them before is computed
+// anew instead of waiting in registers.
+template <int NV>
+__device__ __forceinline__ void afresh(Raw<NV>& r)
+{
 #pragma unroll
-            for (int j = 0; j < V; ++j)
-                if (c + j < width) r[k].e[j] = p[c + j];
-        }
-    }
+    for (int k = 0; k < NV; ++k) asm("" : "+v"(r[k]));
 }
 
 // Rows of up to TEAM NV vectors.  A workgroup walks its rows with the parameters and the
@@ -120,8 +214,9 @@ __global__ __launch_bounds__(TEAM < 256 ? 256 : TEAM) void k_norm(NormArgs a)
     constexpr int V = kNormV<T>, THREADS = TEAM < 256 ? 256 : TEAM, TEAMS = THREADS / TEAM;
     using E = typename T::store_t;
     using W = typename P::store_t;
-    __shared__ float lds[2][THREADS / 64];
-    const int lane = threadIdx.x % TEAM, team = threadIdx.x / TEAM;
+    __shared__ float lds[2][THREADS / 64][1];
+    const int lane = threadIdx.x % TEAM;
+    const int team = TEAM < 64 ? threadIdx.x / TEAM : uniform((int32_t)(threadIdx.x / TEAM));
     float w[NV][V], b[NV][V];
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
@@ -133,7 +228,7 @@ __global__ __launch_bounds__(TEAM < 256 ? 256 : TEAM) void k_norm(NormArgs a)
     }
     const int32_t step = gridDim.x * TEAMS;
     int32_t row = blockIdx.x * TEAMS + team;
-    Raw<T, NV> x, res;
+    Raw<NV> x, res;
     auto fetch = [&](int32_t at) {
         ld_row<T, TEAM, NV>(norm_row<T>(a.x, a, at), lane, a.width, x);
         if (RES) ld_row<T, TEAM, NV>(norm_row<T>(a.residual, a, at), lane, a.width, res);
@@ -145,8 +240,8 @@ __global__ __launch_bounds__(TEAM < 256 ? 256 : TEAM) void k_norm(NormArgs a)
         for (int k = 0; k < NV; ++k) {
 #pragma unroll
             for (int j = 0; j < V; ++j) {
-                v[k][j] = T::load(x[k].e[j]);
-                if (RES) v[k][j] = T::load(T::round(v[k][j] + T::load(res[k].e[j])));
+                v[k][j] = element<T>(x[k], j);
+                if (RES) v[k][j] = T::load(T::round(v[k][j] + element<T>(res[k], j)));
             }
             s += tree(v[k]);
         }
@@ -185,82 +280,247 @@ __global__ __launch_bounds__(TEAM < 256 ? 256 : TEAM) void k_norm(NormArgs a)
 
 // Backward for rows of up to TEAM NV vectors, with the sums of dweight and dbias over a
 // chunk of rows in registers: row i of the chunk to team i mod TEAMS, the teams by the
-// pairwise tree.
-template <typename T, typename P, int TEAM, int NV>
+// pairwise tree.  A team takes RB rows at a time, whose sums share a barrier, while the
+// next ones arrive.
+template <typename T, int NV, int RB>
+struct NormRows {
+    Raw<NV> x[RB], g[RB], ds[RB];
+    float mean[RB], rstd[RB];
+};
+template <typename T, typename P, int TEAM, int NV, int RB>
 __global__ __launch_bounds__(TEAM < 256 ? 256 : TEAM) void k_norm_grad(NormArgs a, int32_t chunk)
 {
     constexpr int V = kNormV<T>, THREADS = TEAM < 256 ? 256 : TEAM, TEAMS = THREADS / TEAM;
     using E = typename T::store_t;
     using W = typename P::store_t;
-    __shared__ float lds[2][THREADS / 64];
-    __shared__ float part[TEAMS > 1 ? THREADS * V : 1];
-    const int lane = threadIdx.x % TEAM, team = threadIdx.x / TEAM;
+    __shared__ float lds[2][THREADS / 64][2 * RB];
+    __shared__ float part[TEAMS > 1 ? 2 : 1][TEAMS][TEAMS > 1 ? TEAM * NV * V : 1];
+    const int lane = threadIdx.x % TEAM;
+    const int team = TEAM < 64 ? threadIdx.x / TEAM : uniform((int32_t)(threadIdx.x / TEAM));
+    const int32_t first = blockIdx.x * chunk;
+    const int32_t end = a.total - first < chunk ? a.total : first + chunk;
+    auto fetch = [&](NormRows<T, NV, RB>& r, int32_t row) {
+#pragma unroll
+        for (int u = 0; u < RB; ++u) {
+            const int32_t at = row + u * TEAMS;
+            if (at >= end) break;
+            r.mean[u] = a.stats[2 * (int64_t)at];
+            r.rstd[u] = a.stats[2 * (int64_t)at + 1];
+            ld_row<T, TEAM, NV>(norm_row<T>(a.x, a, at), lane, a.width, r.x[u]);
+            ld_row<T, TEAM, NV>(norm_row<T>(a.dout, a, at), lane, a.width, r.g[u]);
+            if (a.dsum.p) ld_row<T, TEAM, NV>(norm_row<T>(a.dsum, a, at), lane, a.width, r.ds[u]);
+        }
+    };
+    // whole waves that need no barrier hide their loads behind each other's work
+    constexpr bool AHEAD = TEAM > 64;
+    NormRows<T, NV, RB> now, next;
+    int32_t row = first + team;
+    if (AHEAD) fetch(next, row);
     float w[NV][V], dw[NV][V] = {}, db[NV][V] = {};
 #pragma unroll
     for (int k = 0; k < NV; ++k)
         ld_cols<P, V>(static_cast<const W*>(a.weight), (k * TEAM + lane) * V, a.width, w[k]);
-    const int32_t first = blockIdx.x * chunk;
-    const int32_t end = a.total - first < chunk ? a.total : first + chunk;
-    Raw<T, NV> x, g, ds;
-    auto fetch = [&](int32_t at) {
-        ld_row<T, TEAM, NV>(norm_row<T>(a.x, a, at), lane, a.width, x);
-        ld_row<T, TEAM, NV>(norm_row<T>(a.dout, a, at), lane, a.width, g);
-        if (a.dsum.p) ld_row<T, TEAM, NV>(norm_row<T>(a.dsum, a, at), lane, a.width, ds);
-    };
-    int32_t row = first + team;
-    if (row < end) fetch(row);
-    for (; row < end; row += TEAMS) {
-        const float mean = a.stats[2 * (int64_t)row], rstd = a.stats[2 * (int64_t)row + 1];
-        float n[NV][V], d[NV][V], e[NV][V], s = 0.f, q = 0.f;
+    for (int buf = 0; row < end; row += RB * TEAMS, buf ^= 1) {
+        if (AHEAD) {
+            now = next;
+            if (row + RB * TEAMS < end) fetch(next, row + RB * TEAMS);
+        } else {
+            fetch(now, row);
+        }
+        float sums[2 * RB] = {};
+#pragma unroll
+        for (int u = 0; u < RB; ++u) {
+            if (row + u * TEAMS >= end) break;
+#pragma unroll
+            for (int k = 0; k < NV; ++k) {
+                float d[V], t[V];
+#pragma unroll
+                for (int j = 0; j < V; ++j) {
+                    const float dout = element<T>(now.g[u][k], j);
+                    const float n = (element<T>(now.x[u][k], j) - now.mean[u]) * now.rstd[u];
+                    dw[k][j] = fma32(n, dout, dw[k][j]);
+                    db[k][j] += dout;
+                    d[j] = dout * w[k][j];
+                    t[j] = n * d[j];
+                }
+                sums[2 * u] += tree(d);
+                sums[2 * u + 1] += tree(t);
+            }
+        }
+        team_sums<TEAM>(sums, lds[buf]);
+#pragma unroll
+        for (int u = 0; u < RB; ++u) {
+            if (row + u * TEAMS >= end) break;
+            afresh<NV>(now.x[u]);
+            afresh<NV>(now.g[u]);
+            E* dx = norm_row<T>(a.dx, a, row + u * TEAMS);
+            const float s = sums[2 * u] * a.inv_width, q = sums[2 * u + 1] * a.inv_width;
+#pragma unroll
+            for (int k = 0; k < NV; ++k) {
+                float d[V];
+#pragma unroll
+                for (int j = 0; j < V; ++j) {
+                    const float n = (element<T>(now.x[u][k], j) - now.mean[u]) * now.rstd[u];
+                    const float g = fma32(-n, q, element<T>(now.g[u][k], j) * w[k][j] - s);
+                    d[j] = fma32(now.rstd[u], g, a.dsum.p ? element<T>(now.ds[u][k], j) : 0.f);
+                }
+                st_cols<T, V>(dx, (k * TEAM + lane) * V, a.width, d);
+            }
+        }
+    }
+    if constexpr (TEAMS == 1) {
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
-            float t[V];
+            const int c = (k * TEAM + lane) * V;
+            const int64_t at = (int64_t)blockIdx.x * a.width;
+            st_cols<F32, V>(a.ws_w + at, c, a.width, dw[k]);
+            if (a.dbias) st_cols<F32, V>(a.ws_b + at, c, a.width, db[k]);
+        }
+    } else {
+        constexpr int COLS = TEAM * NV * V;
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            const int c = (k * TEAM + lane) * V;
 #pragma unroll
             for (int j = 0; j < V; ++j) {
-                const float dout = T::load(g[k].e[j]);
-                n[k][j] = (T::load(x[k].e[j]) - mean) * rstd;
-                dw[k][j] = fma32(n[k][j], dout, dw[k][j]);
-                db[k][j] += dout;
-                d[k][j] = dout * w[k][j];
-                t[j] = n[k][j] * d[k][j];
-                e[k][j] = a.dsum.p ? T::load(ds[k].e[j]) : 0.f;
+                part[0][team][c + j] = dw[k][j];
+                part[1][team][c + j] = db[k][j];
             }
-            s += tree(d[k]);
+        }
+        __syncthreads();
+        for (int i = threadIdx.x; i < 2 * COLS; i += THREADS) {
+            const int which = i / COLS, c = i % COLS;
+            if (c >= a.width || (which && !a.dbias)) continue;
+            float v[TEAMS];
+#pragma unroll
+            for (int t = 0; t < TEAMS; ++t) v[t] = part[which][t][c];
+            (which ? a.ws_b : a.ws_w)[(int64_t)blockIdx.x * a.width + c] = tree(v);
+        }
+    }
+}
+
+// Rows of up to 32 columns a lane of 1024: a row each, the parameters read where they
+// are used (they stay in the caches), no row ahead.
+template <typename T, typename P>
+__global__ __launch_bounds__(1024) void k_norm_wide(NormArgs a)
+{
+    constexpr int V = kNormV<T>, NV = 32 / V;
+    using E = typename T::store_t;
+    using W = typename P::store_t;
+    __shared__ float lds[2][16][1];
+    const int lane = threadIdx.x;
+    for (int32_t row = blockIdx.x; row < a.total; row += gridDim.x) {
+        Raw<NV> x;
+        ld_row<T, 1024, NV>(norm_row<T>(a.x, a, row), lane, a.width, x);
+        if (a.residual.p) {
+            Raw<NV> res;
+            ld_row<T, 1024, NV>(norm_row<T>(a.residual, a, row), lane, a.width, res);
+#pragma unroll
+            for (int k = 0; k < NV; ++k) {
+                float v[V];
+#pragma unroll
+                for (int j = 0; j < V; ++j) v[j] = element<T>(x[k], j) + element<T>(res[k], j);
+                x[k] = rounded<T>(v);
+            }
+        }
+        float s = 0.f, q = 0.f;
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            float v[V];
+#pragma unroll
+            for (int j = 0; j < V; ++j) v[j] = element<T>(x[k], j);
+            s += tree(v);
+        }
+        const float mean = team_sum<1024>(s, lds[0]) * a.inv_width;
+        afresh<NV>(x);
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            float d[V];
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                d[j] = (k * 1024 + lane) * V + j < a.width ? element<T>(x[k], j) - mean : 0.f;
+                d[j] *= d[j];
+            }
+            q += tree(d);
+        }
+        const float rstd =
+            __builtin_amdgcn_rsqf(fma32(team_sum<1024>(q, lds[1]), a.inv_width, a.eps));
+        if (a.stats && lane == 0) {
+            a.stats[2 * (int64_t)row] = mean;
+            a.stats[2 * (int64_t)row + 1] = rstd;
+        }
+        afresh<NV>(x);
+        E* out = norm_row<T>(a.out, a, row);
+        E* sum = a.sum.p ? norm_row<T>(a.sum, a, row) : nullptr;
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            const int c = (k * 1024 + lane) * V;
+            if (c >= a.width) continue;
+            __builtin_amdgcn_sched_barrier(0);  // else all parameters are read at once
+            float v[V], w[V], b[V] = {};
+#pragma unroll
+            for (int j = 0; j < V; ++j) v[j] = element<T>(x[k], j);
+            if (sum) st_cols<T, V>(sum, c, a.width, v);
+            ld_cols<P, V>(static_cast<const W*>(a.weight), c, a.width, w);
+            if (a.bias) ld_cols<P, V>(static_cast<const W*>(a.bias), c, a.width, b);
+#pragma unroll
+            for (int j = 0; j < V; ++j) v[j] = fma32((v[j] - mean) * rstd, w[j], b[j]);
+            st_cols<T, V>(out, c, a.width, v);
+        }
+    }
+}
+
+// dx of such rows.
+template <typename T, typename P>
+__global__ __launch_bounds__(1024) void k_norm_dx_wide(NormArgs a)
+{
+    constexpr int V = kNormV<T>, NV = 32 / V;
+    using E = typename T::store_t;
+    using W = typename P::store_t;
+    __shared__ float lds[2][16][1];
+    const int lane = threadIdx.x;
+    for (int32_t row = blockIdx.x; row < a.total; row += gridDim.x) {
+        Raw<NV> x, g;
+        ld_row<T, 1024, NV>(norm_row<T>(a.x, a, row), lane, a.width, x);
+        ld_row<T, 1024, NV>(norm_row<T>(a.dout, a, row), lane, a.width, g);
+        const float mean = a.stats[2 * (int64_t)row], rstd = a.stats[2 * (int64_t)row + 1];
+        float s = 0.f, q = 0.f;
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            const int c = (k * 1024 + lane) * V;
+            if (c >= a.width) continue;
+            __builtin_amdgcn_sched_barrier(0);  // else all parameters are read at once
+            float d[V], t[V], w[V];
+            ld_cols<P, V>(static_cast<const W*>(a.weight), c, a.width, w);
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                d[j] = element<T>(g[k], j) * w[j];
+                t[j] = (element<T>(x[k], j) - mean) * rstd * d[j];
+            }
+            s += tree(d);
             q += tree(t);
         }
-        if (row + TEAMS < end) fetch(row + TEAMS);
-        s = team_sum<TEAM>(s, lds[0]) * a.inv_width;
-        q = team_sum<TEAM>(q, lds[1]) * a.inv_width;
+        s = team_sum<1024>(s, lds[0]) * a.inv_width;
+        q = team_sum<1024>(q, lds[1]) * a.inv_width;
+        afresh<NV>(x);
+        afresh<NV>(g);
+        const E* ds = a.dsum.p ? norm_row<T>(a.dsum, a, row) : nullptr;
         E* dx = norm_row<T>(a.dx, a, row);
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
+            const int c = (k * 1024 + lane) * V;
+            if (c >= a.width) continue;
+            __builtin_amdgcn_sched_barrier(0);
+            float v[V], w[V], e[V] = {};
+            ld_cols<P, V>(static_cast<const W*>(a.weight), c, a.width, w);
+            if (ds) ld_cols<T, V>(ds, c, a.width, e);
 #pragma unroll
-            for (int j = 0; j < V; ++j)
-                d[k][j] = fma32(rstd, fma32(-n[k][j], q, d[k][j] - s), e[k][j]);
-            st_cols<T, V>(dx, (k * TEAM + lane) * V, a.width, d[k]);
-        }
-    }
-    // the teams' sums, a vector at a time
-#pragma unroll
-    for (int k = 0; k < 2 * NV; ++k) {
-        float(&sum)[V] = k < NV ? dw[k % NV] : db[k % NV];
-        if (k >= NV && !a.dbias) break;
-        if (TEAMS > 1) {
-#pragma unroll
-            for (int d = 1; d < TEAMS; d *= 2) {
-                __syncthreads();
-                if (team & d)
-#pragma unroll
-                    for (int j = 0; j < V; ++j) part[j * THREADS + threadIdx.x] = sum[j];
-                __syncthreads();
-                if (!(team & d))
-#pragma unroll
-                    for (int j = 0; j < V; ++j) sum[j] += part[j * THREADS + threadIdx.x + d * TEAM];
+            for (int j = 0; j < V; ++j) {
+                const float n = (element<T>(x[k], j) - mean) * rstd;
+                v[j] = fma32(rstd, fma32(-n, q, element<T>(g[k], j) * w[j] - s), e[j]);
             }
+            st_cols<T, V>(dx, c, a.width, v);
         }
-        if (team == 0)
-            st_cols<F32, V>((k < NV ? a.ws_w : a.ws_b) + (int64_t)blockIdx.x * a.width,
-                            (k % NV * TEAM + lane) * V, a.width, sum);
     }
 }
 
@@ -271,7 +531,7 @@ __global__ __launch_bounds__(256) void k_norm_loop(NormArgs a)
     constexpr int V = kNormV<T>, STEP = 256 * V;
     using E = typename T::store_t;
     using W = typename P::store_t;
-    __shared__ float lds[2][4];
+    __shared__ float lds[2][4][1];
     const int c0 = threadIdx.x * V;
     for (int32_t row = blockIdx.x; row < a.total; row += gridDim.x) {
         const E* x = norm_row<T>(a.x, a, row);
@@ -329,7 +589,7 @@ __global__ __launch_bounds__(256) void k_norm_dx_loop(NormArgs a)
     constexpr int V = kNormV<T>, STEP = 256 * V;
     using E = typename T::store_t;
     using W = typename P::store_t;
-    __shared__ float lds[2][4];
+    __shared__ float lds[2][4][1];
     const int c0 = threadIdx.x * V;
     for (int32_t row = blockIdx.x; row < a.total; row += gridDim.x) {
         const E* x = norm_row<T>(a.x, a, row);
@@ -406,6 +666,17 @@ hipError_t with_team(int32_t width, F&& f)
     return f(std::integral_constant<int, 0>{});
 }
 
+template <class F>
+hipError_t with_grad_team(int32_t width, F&& f)
+{
+    if (width <= 256) return f(std::integral_constant<int, 16>{});
+    if (width <= 1024) return f(std::integral_constant<int, 64>{});
+    if (width <= 2048) return f(std::integral_constant<int, 256>{});
+    if (width <= 4096) return f(std::integral_constant<int, 512>{});
+    if (width <= 8192) return f(std::integral_constant<int, 1024>{});
+    return f(std::integral_constant<int, 0>{});
+}
+
 template <auto KERN>
 hipError_t launch_norm_rows(const NormArgs& a, int threads, int32_t teams, hipStream_t st)
 {
@@ -421,6 +692,7 @@ hipError_t launch_layer_norm(const NormArgs& a, hipStream_t st)
     return with_team(a.width, [&](auto t) {
         constexpr int TEAM = decltype(t)::value, NV = 16 / kNormV<T>;
         if constexpr (TEAM == 0) {
+            if (a.width <= 32768) return launch_norm_rows<&k_norm_wide<T, P>>(a, 1024, 1, st);
             return launch_norm_rows<&k_norm_loop<T, P>>(a, 256, 1, st);
         } else {
             constexpr int THREADS = TEAM < 256 ? 256 : TEAM;
@@ -436,22 +708,23 @@ hipError_t launch_layer_norm_grad(const NormArgs& a, hipStream_t st)
 {
     const int64_t chunk = norm_chunk(a.total), chunks = (a.total + chunk - 1) / chunk;
     if (a.total > 0) {
-        const hipError_t e = with_team(a.width, [&](auto t) {
-            // the sums take 32 registers more: no more than 512 threads, 8192 columns
-            constexpr int WIDE = decltype(t)::value, TEAM = WIDE < 1024 ? WIDE : 512;
-            constexpr int NV = 16 / kNormV<T>;
-            if (TEAM == 0 || a.width > TEAM * 16) {
+        const hipError_t e = with_grad_team(a.width, [&](auto t) {
+            constexpr int TEAM = decltype(t)::value, NV = (TEAM < 256 ? 16 : 8) / kNormV<T>;
+            if constexpr (TEAM == 0) {
                 constexpr int64_t cols = 256 * kNormV<T>;
                 const int64_t tiles = (a.width + cols - 1) / cols;
                 k_norm_dw<T><<<dim3((unsigned)(chunks * tiles)), dim3(256), 0, st>>>(
                     a, (int32_t)chunk, (int32_t)tiles);
                 if (hipError_t e = hipGetLastError()) return e;
                 // after the sums, which read dout: dx may be in its place
+                if (a.width <= 32768) return launch_norm_rows<&k_norm_dx_wide<T, P>>(a, 1024, 1, st);
                 return launch_norm_rows<&k_norm_dx_loop<T, P>>(a, 256, 1, st);
             }
             if constexpr (TEAM > 0) {
-                k_norm_grad<T, P, TEAM, NV><<<dim3((unsigned)chunks), dim3(TEAM < 256 ? 256 : TEAM),
-                                              0, st>>>(a, (int32_t)chunk);
+                constexpr int RB = TEAM < 256 || TEAM == 1024 || sizeof(typename T::store_t) == 4 ? 1 : 2;
+                k_norm_grad<T, P, TEAM, NV, RB><<<dim3((unsigned)chunks),
+                                                  dim3(TEAM < 256 ? 256 : TEAM), 0, st>>>(
+                    a, (int32_t)chunk);
             }
             return hipGetLastError();
         });
