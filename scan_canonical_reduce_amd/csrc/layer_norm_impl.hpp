@@ -399,233 +399,130 @@ __global__ __launch_bounds__(TEAM < 256 ? 256 : TEAM) void k_norm_grad(NormArgs 
     }
 }
 
-// Rows of up to 32 columns a lane of 1024: a row each, the parameters read where they
-// are used (they stay in the caches), no row ahead.
+// Rows of any width, a workgroup each, read again for each sum (from the caches), U
+// vectors of a lane in flight.
+constexpr int kLoopU = 4;
+
 template <typename T, typename P>
-__global__ __launch_bounds__(1024) void k_norm_wide(NormArgs a)
+__global__ __launch_bounds__(1024) void k_norm_loop(NormArgs a)
 {
-    constexpr int V = kNormV<T>, NV = 32 / V;
+    constexpr int V = kNormV<T>, STEP = 1024 * V, U = kLoopU;
     using E = typename T::store_t;
     using W = typename P::store_t;
     __shared__ float lds[2][16][1];
-    const int lane = threadIdx.x;
-    for (int32_t row = blockIdx.x; row < a.total; row += gridDim.x) {
-        Raw<NV> x;
-        ld_row<T, 1024, NV>(norm_row<T>(a.x, a, row), lane, a.width, x);
-        if (a.residual.p) {
-            Raw<NV> res;
-            ld_row<T, 1024, NV>(norm_row<T>(a.residual, a, row), lane, a.width, res);
-#pragma unroll
-            for (int k = 0; k < NV; ++k) {
-                float v[V];
-#pragma unroll
-                for (int j = 0; j < V; ++j) v[j] = element<T>(x[k], j) + element<T>(res[k], j);
-                x[k] = rounded<T>(v);
-            }
-        }
-        float s = 0.f, q = 0.f;
-#pragma unroll
-        for (int k = 0; k < NV; ++k) {
-            float v[V];
-#pragma unroll
-            for (int j = 0; j < V; ++j) v[j] = element<T>(x[k], j);
-            s += tree(v);
-        }
-        const float mean = team_sum<1024>(s, lds[0]) * a.inv_width;
-        afresh<NV>(x);
-#pragma unroll
-        for (int k = 0; k < NV; ++k) {
-            float d[V];
-#pragma unroll
-            for (int j = 0; j < V; ++j) {
-                d[j] = (k * 1024 + lane) * V + j < a.width ? element<T>(x[k], j) - mean : 0.f;
-                d[j] *= d[j];
-            }
-            q += tree(d);
-        }
-        const float rstd =
-            __builtin_amdgcn_rsqf(fma32(team_sum<1024>(q, lds[1]), a.inv_width, a.eps));
-        if (a.stats && lane == 0) {
-            a.stats[2 * (int64_t)row] = mean;
-            a.stats[2 * (int64_t)row + 1] = rstd;
-        }
-        afresh<NV>(x);
-        E* out = norm_row<T>(a.out, a, row);
-        E* sum = a.sum.p ? norm_row<T>(a.sum, a, row) : nullptr;
-#pragma unroll
-        for (int k = 0; k < NV; ++k) {
-            const int c = (k * 1024 + lane) * V;
-            if (c >= a.width) continue;
-            __builtin_amdgcn_sched_barrier(0);  // else all parameters are read at once
-            float v[V], w[V], b[V] = {};
-#pragma unroll
-            for (int j = 0; j < V; ++j) v[j] = element<T>(x[k], j);
-            if (sum) st_cols<T, V>(sum, c, a.width, v);
-            ld_cols<P, V>(static_cast<const W*>(a.weight), c, a.width, w);
-            if (a.bias) ld_cols<P, V>(static_cast<const W*>(a.bias), c, a.width, b);
-#pragma unroll
-            for (int j = 0; j < V; ++j) v[j] = fma32((v[j] - mean) * rstd, w[j], b[j]);
-            st_cols<T, V>(out, c, a.width, v);
-        }
-    }
-}
-
-// dx of such rows.
-template <typename T, typename P>
-__global__ __launch_bounds__(1024) void k_norm_dx_wide(NormArgs a)
-{
-    constexpr int V = kNormV<T>, NV = 32 / V;
-    using E = typename T::store_t;
-    using W = typename P::store_t;
-    __shared__ float lds[2][16][1];
-    const int lane = threadIdx.x;
-    for (int32_t row = blockIdx.x; row < a.total; row += gridDim.x) {
-        Raw<NV> x, g;
-        ld_row<T, 1024, NV>(norm_row<T>(a.x, a, row), lane, a.width, x);
-        ld_row<T, 1024, NV>(norm_row<T>(a.dout, a, row), lane, a.width, g);
-        const float mean = a.stats[2 * (int64_t)row], rstd = a.stats[2 * (int64_t)row + 1];
-        float s = 0.f, q = 0.f;
-#pragma unroll
-        for (int k = 0; k < NV; ++k) {
-            const int c = (k * 1024 + lane) * V;
-            if (c >= a.width) continue;
-            __builtin_amdgcn_sched_barrier(0);  // else all parameters are read at once
-            float d[V], t[V], w[V];
-            ld_cols<P, V>(static_cast<const W*>(a.weight), c, a.width, w);
-#pragma unroll
-            for (int j = 0; j < V; ++j) {
-                d[j] = element<T>(g[k], j) * w[j];
-                t[j] = (element<T>(x[k], j) - mean) * rstd * d[j];
-            }
-            s += tree(d);
-            q += tree(t);
-        }
-        s = team_sum<1024>(s, lds[0]) * a.inv_width;
-        q = team_sum<1024>(q, lds[1]) * a.inv_width;
-        afresh<NV>(x);
-        afresh<NV>(g);
-        const E* ds = a.dsum.p ? norm_row<T>(a.dsum, a, row) : nullptr;
-        E* dx = norm_row<T>(a.dx, a, row);
-#pragma unroll
-        for (int k = 0; k < NV; ++k) {
-            const int c = (k * 1024 + lane) * V;
-            if (c >= a.width) continue;
-            __builtin_amdgcn_sched_barrier(0);
-            float v[V], w[V], e[V] = {};
-            ld_cols<P, V>(static_cast<const W*>(a.weight), c, a.width, w);
-            if (ds) ld_cols<T, V>(ds, c, a.width, e);
-#pragma unroll
-            for (int j = 0; j < V; ++j) {
-                const float n = (element<T>(x[k], j) - mean) * rstd;
-                v[j] = fma32(rstd, fma32(-n, q, element<T>(g[k], j) * w[j] - s), e[j]);
-            }
-            st_cols<T, V>(dx, c, a.width, v);
-        }
-    }
-}
-
-// One workgroup per row, which is read again for each sum: any width.
-template <typename T, typename P>
-__global__ __launch_bounds__(256) void k_norm_loop(NormArgs a)
-{
-    constexpr int V = kNormV<T>, STEP = 256 * V;
-    using E = typename T::store_t;
-    using W = typename P::store_t;
-    __shared__ float lds[2][4][1];
     const int c0 = threadIdx.x * V;
     for (int32_t row = blockIdx.x; row < a.total; row += gridDim.x) {
         const E* x = norm_row<T>(a.x, a, row);
         const E* res = a.residual.p ? norm_row<T>(a.residual, a, row) : nullptr;
         E* sum = a.sum.p ? norm_row<T>(a.sum, a, row) : nullptr;
         E* out = norm_row<T>(a.out, a, row);
-        auto load = [&](int c, float(&v)[V]) {
-            ld_cols<T, V>(x, c, a.width, v);
-            if (!res) return;
-            float r[V];
-            ld_cols<T, V>(res, c, a.width, r);
+        // f(column, the vector s there), in order
+        auto each = [&](auto f) {
+            for (int c = c0; c < a.width; c += U * STEP) {
+                Words16 w[U], r[U];
 #pragma unroll
-            for (int j = 0; j < V; ++j) v[j] = T::load(T::round(v[j] + r[j]));
+                for (int u = 0; u < U; ++u) w[u] = ld16<T>(x, c + u * STEP, a.width);
+                if (res) {
+#pragma unroll
+                    for (int u = 0; u < U; ++u) r[u] = ld16<T>(res, c + u * STEP, a.width);
+                }
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    if (c + u * STEP >= a.width) break;
+                    float v[V];
+#pragma unroll
+                    for (int j = 0; j < V; ++j) {
+                        v[j] = element<T>(w[u], j);
+                        if (res) v[j] = T::load(T::round(v[j] + element<T>(r[u], j)));
+                    }
+                    f(c + u * STEP, v);
+                }
+            }
         };
         float s = 0.f, q = 0.f;
-        for (int c = c0; c < a.width; c += STEP) {
-            float v[V];
-            load(c, v);
-            s += tree(v);
-        }
-        const float mean = team_sum<256>(s, lds[0]) * a.inv_width;
-        for (int c = c0; c < a.width; c += STEP) {
-            float v[V];
-            load(c, v);
+        each([&](int, float(&v)[V]) { s += tree(v); });
+        const float mean = team_sum<1024>(s, lds[0]) * a.inv_width;
+        each([&](int c, float(&v)[V]) {
 #pragma unroll
             for (int j = 0; j < V; ++j) {
                 v[j] = c + j < a.width ? v[j] - mean : 0.f;
                 v[j] *= v[j];
             }
             q += tree(v);
-        }
+        });
         const float rstd =
-            __builtin_amdgcn_rsqf(fma32(team_sum<256>(q, lds[1]), a.inv_width, a.eps));
+            __builtin_amdgcn_rsqf(fma32(team_sum<1024>(q, lds[1]), a.inv_width, a.eps));
         if (a.stats && threadIdx.x == 0) {
             a.stats[2 * (int64_t)row] = mean;
             a.stats[2 * (int64_t)row + 1] = rstd;
         }
-        for (int c = c0; c < a.width; c += STEP) {
-            float v[V], w[V], b[V] = {};
-            load(c, v);
+        each([&](int c, float(&v)[V]) {
+            float w[V], b[V] = {};
             if (sum) st_cols<T, V>(sum, c, a.width, v);
             ld_cols<P, V>(static_cast<const W*>(a.weight), c, a.width, w);
             if (a.bias) ld_cols<P, V>(static_cast<const W*>(a.bias), c, a.width, b);
 #pragma unroll
             for (int j = 0; j < V; ++j) v[j] = fma32((v[j] - mean) * rstd, w[j], b[j]);
             st_cols<T, V>(out, c, a.width, v);
-        }
+        });
     }
 }
 
-// dx of a row by one workgroup, which reads the row twice: any width.
+// dx of such rows.
 template <typename T, typename P>
-__global__ __launch_bounds__(256) void k_norm_dx_loop(NormArgs a)
+__global__ __launch_bounds__(1024) void k_norm_dx_loop(NormArgs a)
 {
-    constexpr int V = kNormV<T>, STEP = 256 * V;
+    constexpr int V = kNormV<T>, STEP = 1024 * V, U = kLoopU;
     using E = typename T::store_t;
     using W = typename P::store_t;
-    __shared__ float lds[2][4][1];
+    __shared__ float lds[2][16][2];
     const int c0 = threadIdx.x * V;
-    for (int32_t row = blockIdx.x; row < a.total; row += gridDim.x) {
+    int buf = 0;
+    for (int32_t row = blockIdx.x; row < a.total; row += gridDim.x, buf ^= 1) {
         const E* x = norm_row<T>(a.x, a, row);
         const E* dout = norm_row<T>(a.dout, a, row);
         const E* dsum = a.dsum.p ? norm_row<T>(a.dsum, a, row) : nullptr;
         E* dx = norm_row<T>(a.dx, a, row);
         const float mean = a.stats[2 * (int64_t)row], rstd = a.stats[2 * (int64_t)row + 1];
-        float s = 0.f, q = 0.f;
-        for (int c = c0; c < a.width; c += STEP) {
-            float v[V], g[V], w[V];
-            ld_cols<T, V>(x, c, a.width, v);
-            ld_cols<T, V>(dout, c, a.width, g);
-            ld_cols<P, V>(static_cast<const W*>(a.weight), c, a.width, w);
+        // f(column, n and dout weight there), in order
+        auto each = [&](auto f) {
+            for (int c = c0; c < a.width; c += U * STEP) {
+                Words16 v[U], g[U];
 #pragma unroll
-            for (int j = 0; j < V; ++j) {
-                g[j] *= w[j];
-                v[j] = c + j < a.width ? (v[j] - mean) * rstd * g[j] : 0.f;
-            }
-            s += tree(g);
-            q += tree(v);
-        }
-        s = team_sum<256>(s, lds[0]) * a.inv_width;
-        q = team_sum<256>(q, lds[1]) * a.inv_width;
-        for (int c = c0; c < a.width; c += STEP) {
-            float v[V], g[V], w[V], d[V] = {};
-            ld_cols<T, V>(x, c, a.width, v);
-            ld_cols<T, V>(dout, c, a.width, g);
-            if (dsum) ld_cols<T, V>(dsum, c, a.width, d);
-            ld_cols<P, V>(static_cast<const W*>(a.weight), c, a.width, w);
+                for (int u = 0; u < U; ++u) v[u] = ld16<T>(x, c + u * STEP, a.width);
 #pragma unroll
-            for (int j = 0; j < V; ++j) {
-                const float n = (v[j] - mean) * rstd;
-                v[j] = fma32(rstd, fma32(-n, q, fma32(g[j], w[j], -s)), d[j]);
+                for (int u = 0; u < U; ++u) g[u] = ld16<T>(dout, c + u * STEP, a.width);
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    const int at = c + u * STEP;
+                    if (at >= a.width) break;
+                    float n[V], d[V], w[V];
+                    ld_cols<P, V>(static_cast<const W*>(a.weight), at, a.width, w);
+#pragma unroll
+                    for (int j = 0; j < V; ++j) {
+                        n[j] = (element<T>(v[u], j) - mean) * rstd;
+                        d[j] = element<T>(g[u], j) * w[j];
+                    }
+                    f(at, n, d);
+                }
             }
-            st_cols<T, V>(dx, c, a.width, v);
-        }
+        };
+        float sums[2] = {0.f, 0.f};
+        each([&](int, float(&n)[V], float(&d)[V]) {
+            sums[0] += tree(d);
+#pragma unroll
+            for (int j = 0; j < V; ++j) n[j] *= d[j];  // 0 beyond the width, as d is
+            sums[1] += tree(n);
+        });
+        team_sums<1024>(sums, lds[buf]);
+        const float s = sums[0] * a.inv_width, q = sums[1] * a.inv_width;
+        each([&](int c, float(&n)[V], float(&d)[V]) {
+            float e[V] = {};
+            if (dsum) ld_cols<T, V>(dsum, c, a.width, e);
+#pragma unroll
+            for (int j = 0; j < V; ++j) n[j] = fma32(rstd, fma32(-n[j], q, d[j] - s), e[j]);
+            st_cols<T, V>(dx, c, a.width, n);
+        });
     }
 }
 
@@ -692,8 +589,7 @@ hipError_t launch_layer_norm(const NormArgs& a, hipStream_t st)
     return with_team(a.width, [&](auto t) {
         constexpr int TEAM = decltype(t)::value, NV = 16 / kNormV<T>;
         if constexpr (TEAM == 0) {
-            if (a.width <= 32768) return launch_norm_rows<&k_norm_wide<T, P>>(a, 1024, 1, st);
-            return launch_norm_rows<&k_norm_loop<T, P>>(a, 256, 1, st);
+            return launch_norm_rows<&k_norm_loop<T, P>>(a, 1024, 1, st);
         } else {
             constexpr int THREADS = TEAM < 256 ? 256 : TEAM;
             if (a.residual.p)
@@ -717,8 +613,7 @@ hipError_t launch_layer_norm_grad(const NormArgs& a, hipStream_t st)
                     a, (int32_t)chunk, (int32_t)tiles);
                 if (hipError_t e = hipGetLastError()) return e;
                 // after the sums, which read dout: dx may be in its place
-                if (a.width <= 32768) return launch_norm_rows<&k_norm_dx_wide<T, P>>(a, 1024, 1, st);
-                return launch_norm_rows<&k_norm_dx_loop<T, P>>(a, 256, 1, st);
+                return launch_norm_rows<&k_norm_dx_loop<T, P>>(a, 1024, 1, st);
             }
             if constexpr (TEAM > 0) {
                 constexpr int RB = TEAM < 256 || TEAM == 1024 || sizeof(typename T::store_t) == 4 ? 1 : 2;
