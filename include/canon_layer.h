@@ -118,8 +118,9 @@ typedef struct {
  * row on not finite (a gate of minus or plus infinity is its limit, and one that
  * makes c zero shuts out finite x only).
  * Limits (CANON_EUNSUPPORTED): those of canon_seq.h on seqs, rows and channels;
- * blocks (seqs ceil(rows / CANON_RECUR_BLOCK), packed seqs + rows /
- * CANON_RECUR_BLOCK, single rows seqs) times ceil(channels / 64) below 2^22. */
+ * row pitches below 2^24 elements (but for single rows); blocks (seqs ceil(rows /
+ * CANON_RECUR_BLOCK), packed seqs + rows / CANON_RECUR_BLOCK, single rows seqs) times
+ * ceil(channels / 64) below 2^22. */
 size_t canon_gated_recurrence_states(size_t seqs, size_t rows, int packed, size_t channels);
 size_t canon_gated_recurrence_workspace_bytes(size_t seqs, size_t rows, int packed,
                                               size_t channels);

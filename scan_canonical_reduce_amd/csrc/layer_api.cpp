@@ -171,6 +171,9 @@ canon_status_t recur_args(const canon_recur_t* c, bool step, bool grad, RecurArg
         return CANON_EINVAL;
     if (grad && c->d_init_state != nullptr && c->d_init_state == c->d_final_state)
         return CANON_EINVAL;
+    for (const canon_rows_t* r : {&c->x, &c->gate, &c->input_gate, &c->out, &c->dout, &c->dx,
+                                  &c->dgate, &c->dinput_gate})
+        if (r->p != nullptr && r->row >= kRecurPitch && !step) return CANON_EUNSUPPORTED;
     *a = RecurArgs{};
     a->q = Seqs{c->seqs, rows, c->starts};
     a->x = c->x;

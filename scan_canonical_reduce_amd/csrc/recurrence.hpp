@@ -14,6 +14,9 @@ constexpr int kRecurWaves = 8;                                // chunks of a rou
 constexpr int kRecurRound = kRecurWaves * CANON_RECUR_CHUNK;  // rows between kept states
 constexpr int kRecurRounds = CANON_RECUR_BLOCK / kRecurRound;
 
+// Byte offsets within a chunk are 32-bit: row pitches below this many elements.
+constexpr int64_t kRecurPitch = (int64_t)1 << 24;
+
 struct RecurArgs {
     Seqs q;
     canon_rows_t x, gate, input, out;

@@ -14,6 +14,8 @@
 // bits inside a block and rounded to 32 between blocks.
 #pragma once
 
+#include <type_traits>
+
 #include "column_sum.hpp"
 #include "launch.hpp"
 #include "recurrence.hpp"
@@ -28,7 +30,7 @@ __device__ __forceinline__ double fma64(double a, double b, double c) { return _
 // exp(l) - 1 for l <= 0: the series, whose next term is below 2^-25 of l up to
 // 0.35, or the exponential less 1, which loses a bit and a half there.
 template <typename T>
-__device__ __forceinline__ float expm1_f(float l)
+__device__ __forceinline__ float expm1_f(float l, bool near_only)
 {
     float p = fma32(l, 0x1.a01a02p-13f, 0x1.6c16c2p-10f);  // 1/7!, 1/6!
     p = fma32(p, l, 0x1.111112p-7f);
@@ -36,18 +38,30 @@ __device__ __forceinline__ float expm1_f(float l)
     p = fma32(p, l, 0x1.555556p-3f);
     p = fma32(p, l, 0.5f);
     const float near = fma32(l * l, p, l);
+    if (near_only) return near;
     return l > -0.35f ? near : exp_f<T>(l) - 1.f;
 }
 
-struct Gates {
-    float e, r;  // a - 1, and the sigmoid of the gate (with a decay)
+// A channel's decay, and whether no lane of the wave has one above 0.35: then the
+// logarithm of a, between -decay and 0, needs the series alone.
+struct Decay {
+    float d;
+    bool near_only;
 };
-template <typename T, bool DECAY>
-__device__ __forceinline__ Gates gates(float gate, float decay)
+template <bool DECAY>
+__device__ __forceinline__ Decay load_decay(const float* decay, int32_t ch)
 {
-    if (!DECAY) return Gates{-sigmoid_f<T>(-gate), 0.f};
-    const float r = sigmoid_f<T>(gate);
-    return Gates{expm1_f<T>(-decay * r), r};
+    if (!DECAY) return Decay{0.f, false};
+    const float d = decay[ch];
+    return Decay{d, __ballot(d < 0.35f) == ~0ull};
+}
+
+// e = a - 1
+template <typename T, bool DECAY>
+__device__ __forceinline__ float gate_e(float gate, const Decay& d)
+{
+    if (!DECAY) return -sigmoid_f<T>(-gate);
+    return expm1_f<T>(-d.d * sigmoid_f<T>(gate), d.near_only);
 }
 // sqrt(1 - a^2) = sqrt((1 - a)(1 + a)), or 1 - a
 template <bool DECAY>
@@ -73,40 +87,104 @@ __device__ __forceinline__ Lane recur_lane(const RecurArgs& a, int32_t slab)
     return l;
 }
 
-// Rows of a chunk (n of them valid, at least one), the others a copy of the last.
+// The rows of a chunk in the lane's channel.  Byte offsets within a chunk are 32-bit:
+// fewer than 16 rows of a pitch below 2^24 elements, and a channel below 2^24 (the host
+// checks both).
 template <typename T>
-__device__ __forceinline__ void load_rows(typename T::store_t (&v)[kCh],
-                                          const typename T::store_t* p, int64_t pitch, int32_t ch,
-                                          int n)
-{
-#pragma unroll
-    for (int r = 0; r < kCh; ++r) v[r] = p[(r < n ? r : n - 1) * pitch + ch];
-}
-
-// e and v of a chunk's rows; rows beyond n leave the state as it is.
-template <typename T, bool DECAY>
-__device__ __forceinline__ void load_chunk(const RecurArgs& a, const Lane& l, int64_t s,
-                                           int64_t row, int n, float decay, float (&e)[kCh],
-                                           float (&v)[kCh])
-{
+struct ChunkRows {
     using E = typename T::store_t;
-    E x[kCh], g[kCh], in[kCh];
-    load_rows<T>(x, rows_ptr<T>(a.x, s, a.q, row), a.x.row, l.ch, n);
-    load_rows<T>(g, rows_ptr<T>(a.gate, s, a.q, row), a.gate.row, l.ch, n);
-    if (a.input.p) load_rows<T>(in, rows_ptr<T>(a.input, s, a.q, row), a.input.row, l.ch, n);
+    uint32_t v[kCh];  // bits
+
+    // n rows are valid, at least one; the others are a copy of the last
+    __device__ __forceinline__ void load(const canon_rows_t& a, const Seqs& q, int64_t s, int64_t row,
+                                         const Lane& l, int n)
+    {
+        const __amdgpu_buffer_rsrc_t b = tile_rsrc(rows_ptr<T>(a, s, q, row));
+        const uint32_t pitch = (uint32_t)a.row * (uint32_t)sizeof(E);
+        const uint32_t off = (uint32_t)l.ch * (uint32_t)sizeof(E);
+        if (n >= kCh) {
+#pragma unroll
+            for (int r = 0; r < kCh; ++r) v[r] = bits(b, off, r * pitch);
+        } else {
+#pragma unroll
+            for (int r = 0; r < kCh; ++r) v[r] = bits(b, off, (r < n ? r : n - 1) * pitch);
+        }
+    }
+    static __device__ __forceinline__ uint32_t bits(__amdgpu_buffer_rsrc_t b, uint32_t off,
+                                                    uint32_t row)
+    {
+        if constexpr (sizeof(E) == 2)
+            return __builtin_amdgcn_raw_buffer_load_b16(b, off, row, 0);
+        else
+            return __builtin_amdgcn_raw_buffer_load_b32(b, off, row, 0);
+    }
+    __device__ __forceinline__ float operator[](int r) const
+    {
+        if constexpr (sizeof(E) == 2)
+            return T::load((uint16_t)v[r]);
+        else
+            return __uint_as_float(v[r]);
+    }
+    // The same values, as if loaded again: what was computed from them before is
+    // computed anew instead of waiting in registers.
+    __device__ __forceinline__ void afresh()
+    {
+#pragma unroll
+        for (int r = 0; r < kCh; ++r) asm("" : "+v"(v[r]));
+    }
+};
+
+// The rows of a chunk of an output.
+template <typename T>
+struct ChunkOut {
+    using E = typename T::store_t;
+    __amdgpu_buffer_rsrc_t b;
+    uint32_t pitch, off;
+    __device__ __forceinline__ ChunkOut(const canon_rows_t& a, const Seqs& q, int64_t s, int64_t row,
+                                        const Lane& l)
+        : b(tile_rsrc(rows_ptr<T>(a, s, q, row))),
+          pitch((uint32_t)a.row * (uint32_t)sizeof(E)),
+          off((uint32_t)l.c * (uint32_t)sizeof(E))
+    {
+    }
+    __device__ __forceinline__ void store(int r, float v) const
+    {
+        rsrc_store(b, off, r * pitch, T::round(v));
+    }
+};
+
+// What a chunk reads.
+template <typename T>
+struct ChunkIn {
+    ChunkRows<T> x, g, in;
+    __device__ __forceinline__ void load(const RecurArgs& a, const Lane& l, int64_t s, int64_t row,
+                                         int n)
+    {
+        g.load(a.gate, a.q, s, row, l, n);
+        x.load(a.x, a.q, s, row, l, n);
+        if (a.input.p) in.load(a.input, a.q, s, row, l, n);
+    }
+};
+
+// e and m = c i of a chunk's rows; rows beyond n leave the state as it is.
+template <typename T, bool DECAY>
+__device__ __forceinline__ void chunk_gates(const RecurArgs& a, const ChunkIn<T>& c, int n,
+                                            const Decay& d, float (&e)[kCh], float (&m)[kCh])
+{
 #pragma unroll
     for (int r = 0; r < kCh; ++r) {
-        e[r] = gates<T, DECAY>(T::load(g[r]), decay).e;
-        v[r] = factor<DECAY>(e[r]) * T::load(x[r]);
+        if (r % 4 == 0) __builtin_amdgcn_sched_barrier(0);  // else more registers
+        e[r] = gate_e<T, DECAY>(c.g[r], d);
+        m[r] = factor<DECAY>(e[r]);
     }
     if (a.input.p) {
 #pragma unroll
-        for (int r = 0; r < kCh; ++r) v[r] *= sigmoid_f<T>(T::load(in[r]));
+        for (int r = 0; r < kCh; ++r) m[r] *= sigmoid_f<T>(c.in[r]);
     }
     if (n < kCh) {
 #pragma unroll
         for (int r = 0; r < kCh; ++r)
-            if (r >= n) e[r] = v[r] = 0.f;
+            if (r >= n) e[r] = m[r] = 0.f;
     }
 }
 
@@ -121,13 +199,12 @@ enum { kRecurSum, kRecurOut, kRecurWhole };
 // kRecurSum: Q and S of each block.  kRecurOut: the outputs of each block, from its
 // start state.  kRecurWhole: the outputs of whole sequences, block after block.
 template <typename T, bool DECAY, int MODE>
-__global__ __launch_bounds__(64 * kRecurWaves) void k_recurrence(RecurArgs a)
+__global__ __launch_bounds__(64 * kRecurWaves, 4) void k_recurrence(RecurArgs a)
 {
-    using E = typename T::store_t;
     __shared__ float lq[2][kRecurWaves][64], ls[2][kRecurWaves][64], lh[64];
     const int64_t job = blockIdx.x / (uint32_t)a.slabs;
     const Lane l = recur_lane(a, blockIdx.x - (uint32_t)job * a.slabs);
-    const float decay = DECAY ? a.decay[l.ch] : 0.f;
+    const Decay decay = load_decay<DECAY>(a.decay, l.ch);
     Chunk k;
     int64_t slot = job;
     if (MODE == kRecurWhole) {
@@ -148,17 +225,30 @@ __global__ __launch_bounds__(64 * kRecurWaves) void k_recurrence(RecurArgs a)
         h0 = a.ws_h[slot * a.channels + l.ch];
     else if (MODE != kRecurSum && a.init)
         h0 = a.init[k.s * a.channels + l.ch];
+    // the wave's rows of the round at `from`, none beyond `end`
+    const int32_t end = MODE == kRecurWhole ? k.span.len : k.row + k.len;
+    auto rows_of = [&](int32_t from) {
+        const int32_t left = end - from - l.wave * kCh;
+        return left < kCh ? left : kCh;
+    };
     int buf = 0;
+    ChunkIn<T> in;
+    if (const int n = rows_of(k.row); n > 0)
+        in.load(a, l, k.s, k.span.first + k.row + l.wave * kCh, n);
     for (;;) {
         double h = h0, Q = 0., S = 0.;
         const int rounds = (k.len + kRecurRound - 1) / kRecurRound;
-        for (int rd = 0; rd < rounds; ++rd) {
-            const int32_t at = k.row + rd * kRecurRound + l.wave * kCh;  // the wave's chunk
-            const int32_t left = k.row + k.len - at;
-            const int n = left < kCh ? left : kCh;
+        for (int rd = 0; rd < rounds; ++rd, buf ^= 1) {
+            const int32_t from = k.row + rd * kRecurRound, at = from + l.wave * kCh;
+            const int n = rows_of(from);
             float e[kCh], v[kCh];
             if (n > 0) {
-                load_chunk<T, DECAY>(a, l, k.s, k.span.first + at, n, decay, e, v);
+                chunk_gates<T, DECAY>(a, in, n, decay, e, v);
+#pragma unroll
+                for (int r = 0; r < kCh; ++r) v[r] *= in.x[r];
+                // the next round's rows arrive meanwhile
+                if (const int m = rows_of(from + kRecurRound); m > 0)
+                    in.load(a, l, k.s, k.span.first + at + kRecurRound, m);
                 float q = 0.f, s = 0.f;
 #pragma unroll
                 for (int r = 0; r < kCh; ++r) {
@@ -175,6 +265,7 @@ __global__ __launch_bounds__(64 * kRecurWaves) void k_recurrence(RecurArgs a)
             const int chunks =
                 rows_left < kRecurRound ? (rows_left + kCh - 1) / kCh : kRecurWaves;
             double mine = h;
+#pragma unroll 1
             for (int c = 0; c < chunks; ++c) {
                 const double q = lq[buf][c][l.lane], s = ls[buf][c][l.lane];
                 if (MODE != kRecurSum) {
@@ -186,14 +277,23 @@ __global__ __launch_bounds__(64 * kRecurWaves) void k_recurrence(RecurArgs a)
                     Q += fma64(q, Q, q);
                 }
             }
-            buf ^= 1;
             if (MODE != kRecurSum && n > 0) {
                 float y = (float)mine;
-                E* out = rows_ptr<T>(a.out, k.s, a.q, k.span.first + at) + l.c;
+                const ChunkOut<T> out(a.out, a.q, k.s, k.span.first + at, l);
 #pragma unroll
                 for (int r = 0; r < kCh; ++r) {
                     y += fma32(e[r], y, v[r]);
-                    if (l.on && r < n) st<T>(out + r * a.out.row, y);
+                    v[r] = y;
+                }
+                if (l.on) {
+                    if (n >= kCh) {
+#pragma unroll
+                        for (int r = 0; r < kCh; ++r) out.store(r, v[r]);
+                    } else {
+#pragma unroll
+                        for (int r = 0; r < kCh; ++r)
+                            if (r < n) out.store(r, v[r]);
+                    }
                 }
             }
         }
@@ -264,7 +364,7 @@ __global__ __launch_bounds__(256) void k_recurrence_step(RecurArgs a)
     auto row = [&](const canon_rows_t& r) {
         return static_cast<typename T::store_t*>(r.p) + s * r.seq + c;
     };
-    const float e = gates<T, DECAY>(ld<T>(row(a.gate)), DECAY ? a.decay[c] : 0.f).e;
+    const float e = gate_e<T, DECAY>(ld<T>(row(a.gate)), Decay{DECAY ? a.decay[c] : 0.f, false});
     float v = factor<DECAY>(e) * ld<T>(row(a.x));
     if (a.input.p) v *= sigmoid_f<T>(ld<T>(row(a.input)));
     float h = a.init ? a.init[i] : 0.f;
@@ -281,11 +381,10 @@ __global__ __launch_bounds__(256) void k_recurrence_step(RecurArgs a)
 template <typename T, bool DECAY>
 __global__ __launch_bounds__(64 * kRecurWaves) void k_recur_back_sum(RecurArgs a)
 {
-    using E = typename T::store_t;
     __shared__ float lq[2][kRecurWaves][64], lt[2][kRecurWaves][64];
     const int64_t slot = blockIdx.x / (uint32_t)a.slabs;
     const Lane l = recur_lane(a, blockIdx.x - (uint32_t)slot * a.slabs);
-    const float decay = DECAY ? a.decay[l.ch] : 0.f;
+    const Decay decay = load_decay<DECAY>(a.decay, l.ch);
     const Chunk k = wave_slot_chunk<CANON_RECUR_BLOCK>(a.q, slot);
     if (k.len <= 0 || k.row == 0) return;  // the first block's fold serves no other
     double Q = 0., G = 0.;
@@ -296,13 +395,13 @@ __global__ __launch_bounds__(64 * kRecurWaves) void k_recur_back_sum(RecurArgs a
         const int n = left < kCh ? left : kCh;
         float q = 0.f, t = 0.f;
         if (n > 0) {
-            E g[kCh], d[kCh];
-            load_rows<T>(g, rows_ptr<T>(a.gate, k.s, a.q, k.span.first + at), a.gate.row, l.ch, n);
-            load_rows<T>(d, rows_ptr<T>(a.dout, k.s, a.q, k.span.first + at), a.dout.row, l.ch, n);
+            ChunkRows<T> g, d;
+            g.load(a.gate, a.q, k.s, k.span.first + at, l, n);
+            d.load(a.dout, a.q, k.s, k.span.first + at, l, n);
 #pragma unroll
             for (int r = kCh - 1; r >= 0; --r) {
-                const float e = r < n ? gates<T, DECAY>(T::load(g[r]), decay).e : 0.f;
-                const float lam = r < n ? T::load(d[r]) + t : t;
+                const float e = r < n ? gate_e<T, DECAY>(g[r], decay) : 0.f;
+                const float lam = r < n ? d[r] + t : t;
                 t = fma32(e, lam, lam);
                 q += fma32(e, q, e);
             }
@@ -323,16 +422,30 @@ __global__ __launch_bounds__(64 * kRecurWaves) void k_recur_back_sum(RecurArgs a
     }
 }
 
-// The gradients, block by block (MODE kRecurOut) or of whole sequences (kRecurWhole).
-template <typename T, bool DECAY, int MODE>
-__global__ __launch_bounds__(64 * kRecurWaves) void k_recurrence_grad(RecurArgs a)
+// sigmoid(y) and 1 - sigmoid(y), the latter without cancellation.
+struct Sigmoid {
+    float s, rest;
+};
+template <typename T>
+__device__ __forceinline__ Sigmoid sigmoid_both(float y)
 {
-    using E = typename T::store_t;
+    const float e = exp_f<T>(-y), s = rcp_hw(1.f + e);
+    return Sigmoid{s, clamp_f(e, 0.f, kMaxF) * s};
+}
+
+// The gradients, block by block (MODE kRecurOut) or of whole sequences (kRecurWhole).
+// A row keeps e and v = c i x in registers, and h[t-1] in LDS;
+//   d log a = lam (a h[t-1] - a^2 v / c^2),   c^2 = -e (2 + e),   and without decay
+//   d gate  = lam a (c h[t-1] - v).
+template <typename T, bool DECAY, int MODE>
+__global__ __launch_bounds__(64 * kRecurWaves, sizeof(typename T::store_t) == 2 ? 4 : 2) void
+k_recurrence_grad(RecurArgs a)
+{
     __shared__ float lq[2][kRecurWaves][64], ls[2][kRecurWaves][64], lt[2][kRecurWaves][64],
-        lh[64], ld[kRecurWaves][64];
+        lh[64], ldd[kRecurWaves][64], before[kRecurWaves][kCh][64];
     const int64_t job = blockIdx.x / (uint32_t)a.slabs;
     const Lane l = recur_lane(a, blockIdx.x - (uint32_t)job * a.slabs);
-    const float decay = DECAY ? a.decay[l.ch] : 0.f;
+    const Decay decay = load_decay<DECAY>(a.decay, l.ch);
     Chunk k;
     int64_t slot = job;
     if (MODE == kRecurWhole) {
@@ -362,27 +475,25 @@ __global__ __launch_bounds__(64 * kRecurWaves) void k_recurrence_grad(RecurArgs 
             const int32_t at = k.row + rd * kRecurRound + l.wave * kCh;
             const int32_t left = k.row + k.len - at;
             const int n = left < kCh ? left : kCh;
-            E x[kCh], g[kCh], in[kCh], d[kCh];
-            float e[kCh];
             const int64_t row = k.span.first + at;
+            ChunkIn<T> in;
+            ChunkRows<T> dout;
+            float e[kCh], v[kCh];
             float q = 0.f, s = 0.f, t = 0.f;
             if (n > 0) {
-                load_rows<T>(x, rows_ptr<T>(a.x, k.s, a.q, row), a.x.row, l.ch, n);
-                load_rows<T>(g, rows_ptr<T>(a.gate, k.s, a.q, row), a.gate.row, l.ch, n);
-                load_rows<T>(d, rows_ptr<T>(a.dout, k.s, a.q, row), a.dout.row, l.ch, n);
-                if (a.input.p)
-                    load_rows<T>(in, rows_ptr<T>(a.input, k.s, a.q, row), a.input.row, l.ch, n);
+                in.load(a, l, k.s, row, n);
+                dout.load(a.dout, a.q, k.s, row, l, n);
+                chunk_gates<T, DECAY>(a, in, n, decay, e, v);
 #pragma unroll
                 for (int r = 0; r < kCh; ++r) {
-                    e[r] = r < n ? gates<T, DECAY>(T::load(g[r]), decay).e : 0.f;
-                    float v = factor<DECAY>(e[r]) * T::load(x[r]);
-                    if (a.input.p) v *= sigmoid_f<T>(T::load(in[r]));
-                    if (r >= n) v = 0.f;
-                    s += fma32(e[r], s, v);
+                    if (r % 4 == 0) __builtin_amdgcn_sched_barrier(0);
+                    v[r] *= in.x[r];
+                    s += fma32(e[r], s, v[r]);
                 }
 #pragma unroll
                 for (int r = kCh - 1; r >= 0; --r) {
-                    const float lam = r < n ? T::load(d[r]) + t : t;
+                    if (r % 4 == 3) __builtin_amdgcn_sched_barrier(0);
+                    const float lam = r < n ? dout[r] + t : t;
                     t = fma32(e[r], lam, lam);
                     q += fma32(e[r], q, e[r]);
                 }
@@ -392,9 +503,11 @@ __global__ __launch_bounds__(64 * kRecurWaves) void k_recurrence_grad(RecurArgs 
             lt[buf][l.wave][l.lane] = t;
             __syncthreads();
             double h = a.kept[(slot * kRecurRounds + rd) * a.channels + l.ch];
+#pragma unroll 1
             for (int c = 0; c < l.wave; ++c)
                 h += fma64(lq[buf][c][l.lane], h, ls[buf][c][l.lane]);
             double mine = G;
+#pragma unroll 1
             for (int c = kRecurWaves - 1; c >= 0; --c) {
                 const double cq = lq[buf][c][l.lane], ct = lt[buf][c][l.lane];
                 if (c == l.wave) mine = G;
@@ -405,57 +518,57 @@ __global__ __launch_bounds__(64 * kRecurWaves) void k_recurrence_grad(RecurArgs 
                 }
             }
             if (n <= 0) continue;
-            float hp[kCh];
             float y = (float)h;
 #pragma unroll
             for (int r = 0; r < kCh; ++r) {
-                hp[r] = y;
-                float v = factor<DECAY>(e[r]) * T::load(x[r]);
-                if (a.input.p) v *= sigmoid_f<T>(T::load(in[r]));
-                y += fma32(e[r], y, v);
+                before[l.wave][r][l.lane] = y;
+                y += fma32(e[r], y, v[r]);
             }
-            E* dx = rows_ptr<T>(a.dx, k.s, a.q, row) + l.c;
-            E* dg = rows_ptr<T>(a.dgate, k.s, a.q, row) + l.c;
-            E* di = a.input.p ? rows_ptr<T>(a.dinput, k.s, a.q, row) + l.c : nullptr;
+            in.g.afresh();
+            if (a.input.p) in.in.afresh();
+            dout.afresh();
+            const ChunkOut<T> dx(a.dx, a.q, k.s, row, l), dg(a.dgate, a.q, k.s, row, l),
+                di(a.dinput, a.q, k.s, row, l);
             float R = (float)mine;  // what reaches h[t] from the rows behind
 #pragma unroll
             for (int r = kCh - 1; r >= 0; --r) {
                 if (r >= n) continue;
-                const float lam = T::load(d[r]) + R, c = factor<DECAY>(e[r]);
-                const float xr = T::load(x[r]);
-                const float i = a.input.p ? sigmoid_f<T>(T::load(in[r])) : 1.f;
-                const float ix = i * xr;
+                // rows side by side would need more registers than there are
+                if (r % 2) __builtin_amdgcn_sched_barrier(0);
+                const float lam = dout[r] + R, hp = before[l.wave][r][l.lane];
                 R = fma32(e[r], lam, lam);
-                float out;
+                const Sigmoid g = sigmoid_both<T>(in.g[r]);
+                float out, m;
                 if (DECAY) {
-                    // d log a = a (lam h) - (a^2 / c) (lam i x)
-                    const float al = 1.f + e[r];
-                    const float slope = c > 0.f ? al * al * rcp_hw(c) : 0.f;
-                    const float dlog = lam * fma32(al, hp[r], -(slope * ix));
-                    const float sg = sigmoid_f<T>(T::load(g[r]));
-                    const float rr = dlog * sg;
+                    const float al = 1.f + e[r], z = -e[r] * (2.f + e[r]);
+                    const float slope = z > 0.f ? al * al * rcp_hw(z) : 0.f;
+                    const float rr = lam * fma32(al, hp, -(slope * v[r])) * g.s;
                     dd -= rr;
-                    out = -decay * rr * sigmoid_f<T>(-T::load(g[r]));
+                    out = -decay.d * rr * g.rest;
+                    m = __builtin_amdgcn_sqrtf(z);
                 } else {
                     // a itself, which 1 + e loses where it is small
-                    out = lam * (hp[r] - ix) * sigmoid_f<T>(T::load(g[r])) * c;
+                    out = lam * g.s * fma32(-e[r], hp, -v[r]);
+                    m = -e[r];
                 }
                 if (l.on) {
-                    st<T>(dx + r * a.dx.row, lam * c * i);
-                    st<T>(dg + r * a.dgate.row, out);
-                    if (di)
-                        st<T>(di + r * a.dinput.row,
-                              lam * c * ix * sigmoid_f<T>(-T::load(in[r])));
+                    dg.store(r, out);
+                    if (a.input.p) {
+                        const Sigmoid i = sigmoid_both<T>(in.in[r]);
+                        m *= i.s;
+                        di.store(r, lam * v[r] * i.rest);
+                    }
+                    dx.store(r, lam * m);
                 }
             }
         }
         if (DECAY) {
-            ld[l.wave][l.lane] = dd;
+            ldd[l.wave][l.lane] = dd;
             __syncthreads();
             if (l.wave == 0 && l.on) {
                 float v[kRecurWaves];
 #pragma unroll
-                for (int w = 0; w < kRecurWaves; ++w) v[w] = ld[w][l.lane];
+                for (int w = 0; w < kRecurWaves; ++w) v[w] = ldd[w][l.lane];
 #pragma unroll
                 for (int p = 1; p < kRecurWaves; p *= 2)
 #pragma unroll

@@ -68,34 +68,6 @@ __device__ __forceinline__ uint32_t tile_off(const canon_rows_t& r, uint32_t t, 
     return (t * (uint32_t)r.row + col) * (uint32_t)sizeof(typename T::store_t);
 }
 
-// Accesses relative to a wave-uniform address, which stays in scalar registers
-// with the offset of the row: base + row offset + the lane's offset, without
-// vector additions (the buffer form; its range is not limited).
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t tile_rsrc(const void* base)
-{
-    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), 0, -1, 0x00020000);
-}
-__device__ __forceinline__ void rsrc_load(__amdgpu_buffer_rsrc_t b, uint32_t off, uint32_t row,
-                                          uint16_t& v)
-{
-    v = __builtin_amdgcn_raw_buffer_load_b16(b, off, row, 0);
-}
-__device__ __forceinline__ void rsrc_load(__amdgpu_buffer_rsrc_t b, uint32_t off, uint32_t row,
-                                          float& v)
-{
-    v = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(b, off, row, 0));
-}
-__device__ __forceinline__ void rsrc_store(__amdgpu_buffer_rsrc_t b, uint32_t off, uint32_t row,
-                                           uint16_t v)
-{
-    __builtin_amdgcn_raw_buffer_store_b16(v, b, off, row, 0);
-}
-__device__ __forceinline__ void rsrc_store(__amdgpu_buffer_rsrc_t b, uint32_t off, uint32_t row,
-                                           float v)
-{
-    __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(v), b, off, row, 0);
-}
-
 // A lane's rows 4 r + q of one activation's current 16-row tile.
 template <typename T>
 struct LaneRows {
