@@ -92,7 +92,7 @@ canon_status_t canon_layer_norm_grad(const canon_norm_t* c, void* ws, size_t ws_
                                      void* stream);
 
 /* ------------------------------------------------- gated linear recurrence */
-#define CANON_RECUR_CHUNK 16
+#define CANON_RECUR_CHUNK 8
 #define CANON_RECUR_BLOCK 512
 
 typedef struct {

@@ -181,7 +181,6 @@ canon_status_t recur_args(const canon_recur_t* c, bool step, bool grad, RecurArg
     a->input = c->input_gate;
     a->decay = c->decay;
     a->channels = (int32_t)c->channels;
-    a->slabs = (a->channels + 63) / 64;
     a->kept = c->kept_states;
     if (!grad) {
         a->out = c->out;
@@ -196,9 +195,16 @@ canon_status_t recur_args(const canon_recur_t* c, bool step, bool grad, RecurArg
         a->dfinal = c->d_final_state;
         a->dinit = c->d_init_state;
     }
+    a->pairs = c->dtype != CANON_F32 && c->channels % 2 == 0;
+    for (const canon_rows_t* r : {&a->x, &a->gate, &a->input, &a->out, &a->dout, &a->dx, &a->dgate,
+                                  &a->dinput})
+        a->pairs = a->pairs && rows_aligned(*r, 2, 4, false);
+    const int32_t width = a->pairs ? 128 : 64;
+    a->slabs = (a->channels + width - 1) / width;
     const int64_t slots =
         step ? c->seqs : slot_count<CANON_RECUR_BLOCK>(c->seqs, rows, packed);
-    if (!mul_fits(slots, a->slabs, ((int64_t)1 << 22) - 1)) return CANON_EUNSUPPORTED;
+    if (!mul_fits(slots, (c->channels + 63) / 64, ((int64_t)1 << 22) - 1))
+        return CANON_EUNSUPPORTED;
     return CANON_OK;
 }
 

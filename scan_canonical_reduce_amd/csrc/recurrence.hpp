@@ -10,7 +10,7 @@
 namespace canon {
 namespace seq {
 
-constexpr int kRecurWaves = 8;                                // chunks of a round
+constexpr int kRecurWaves = 16;                               // chunks of a round
 constexpr int kRecurRound = kRecurWaves * CANON_RECUR_CHUNK;  // rows between kept states
 constexpr int kRecurRounds = CANON_RECUR_BLOCK / kRecurRound;
 
@@ -22,7 +22,8 @@ struct RecurArgs {
     canon_rows_t x, gate, input, out;
     const float *decay, *init;
     float *final, *kept;  // kept: per slot, kRecurRounds x channels
-    int32_t channels, slabs;
+    int32_t channels, slabs;  // slabs: 64 lanes' channels each
+    bool pairs;  // 16-bit values: two channels a lane, aligned in every row
     float *ws_q, *ws_s, *ws_h;  // per slot: channels; NULL where no sequence has two blocks
     // backward
     canon_rows_t dout, dx, dgate, dinput;

@@ -1,11 +1,12 @@
 // The gated linear recurrence h[t] = a h[t-1] + c i x[t], elementwise over the
 // channels: forward, backward and single rows.
 //
-// A lane holds one channel; a wave walks a chunk of 16 rows, whose inputs it loads
-// at once.  The waves of a workgroup take the chunks of a round (128 rows), fold
-// each from zero, exchange the folds through LDS, and fold again from their chunks'
-// start states, with e = a - 1 and v = c i x still in registers: one pass over
-// memory.  Rounds of a block (512 rows) follow each other in the workgroup.
+// A lane holds V channels; a wave walks a chunk of 8 rows, whose inputs it loads at
+// once.  The 16 waves of a workgroup take the chunks of a round (128 rows), fold each
+// from zero, exchange the folds through LDS, and fold again from their chunks' start
+// states, with e = a - 1 and v = c i x still in registers: one pass over memory.  Rounds
+// of a block (512 rows) follow each other in the workgroup; the next round's rows are on
+// their way all the while.
 //
 // a is near 1 for a long memory, and a rounding of h at every row would add up over
 // that memory.  So everything is kept as differences from 1: with e = a - 1,
@@ -48,12 +49,17 @@ struct Decay {
     float d;
     bool near_only;
 };
-template <bool DECAY>
-__device__ __forceinline__ Decay load_decay(const float* decay, int32_t ch)
+template <bool DECAY, int V>
+__device__ __forceinline__ void load_decay(const float* decay, int32_t ch, Decay (&d)[V])
 {
-    if (!DECAY) return Decay{0.f, false};
-    const float d = decay[ch];
-    return Decay{d, __ballot(d < 0.35f) == ~0ull};
+    bool near_only = DECAY;
+#pragma unroll
+    for (int k = 0; k < V; ++k) {
+        d[k].d = DECAY ? decay[ch + k] : 0.f;
+        near_only = near_only && __ballot(d[k].d < 0.35f) == ~0ull;
+    }
+#pragma unroll
+    for (int k = 0; k < V; ++k) d[k].near_only = near_only;
 }
 
 // e = a - 1
@@ -70,29 +76,45 @@ __device__ __forceinline__ float factor(float e)
     return DECAY ? __builtin_amdgcn_sqrtf(-e * (2.f + e)) : -e;
 }
 
-// A wave's channel and place in its workgroup.
+// A wave's channels and place in its workgroup.
 struct Lane {
     int lane, wave;
-    int32_t c, ch;  // channel, and one that may be read
+    int32_t c, ch;  // the lane's first channel, and one from which V may be read
     bool on;        // c is a channel
 };
+template <int V>
 __device__ __forceinline__ Lane recur_lane(const RecurArgs& a, int32_t slab)
 {
     Lane l;
     l.lane = threadIdx.x & 63;
     l.wave = uniform((int32_t)(threadIdx.x >> 6));
-    l.c = slab * 64 + l.lane;
+    l.c = (slab * 64 + l.lane) * V;
     l.on = l.c < a.channels;
-    l.ch = l.on ? l.c : a.channels - 1;
+    l.ch = l.on ? l.c : a.channels - V;
     return l;
 }
 
-// The rows of a chunk in the lane's channel.  Byte offsets within a chunk are 32-bit:
-// fewer than 16 rows of a pitch below 2^24 elements, and a channel below 2^24 (the host
-// checks both).
-template <typename T>
+// A float of each of the lane's channels.
+template <int V>
+__device__ __forceinline__ void ld_channels(const float* p, float (&v)[V])
+{
+#pragma unroll
+    for (int k = 0; k < V; ++k) v[k] = p[k];
+}
+template <int V>
+__device__ __forceinline__ void st_channels(float* p, const float (&v)[V])
+{
+#pragma unroll
+    for (int k = 0; k < V; ++k) p[k] = v[k];
+}
+
+// The rows of a chunk in the lane's channels, a register each (V is 1, or 2 of 16 bits).
+// Byte offsets within a chunk are 32-bit: fewer than 8 rows of a pitch below 2^24
+// elements, and a channel below 2^24 (the host checks both).
+template <typename T, int V>
 struct ChunkRows {
     using E = typename T::store_t;
+    static constexpr int kBytes = V * sizeof(E);
     uint32_t v[kCh];  // bits
 
     // n rows are valid, at least one; the others are a copy of the last
@@ -113,17 +135,17 @@ struct ChunkRows {
     static __device__ __forceinline__ uint32_t bits(__amdgpu_buffer_rsrc_t b, uint32_t off,
                                                     uint32_t row)
     {
-        if constexpr (sizeof(E) == 2)
+        if constexpr (kBytes == 2)
             return __builtin_amdgcn_raw_buffer_load_b16(b, off, row, 0);
         else
             return __builtin_amdgcn_raw_buffer_load_b32(b, off, row, 0);
     }
-    __device__ __forceinline__ float operator[](int r) const
+    __device__ __forceinline__ float get(int r, int k) const
     {
-        if constexpr (sizeof(E) == 2)
-            return T::load((uint16_t)v[r]);
-        else
+        if constexpr (sizeof(E) == 4)
             return __uint_as_float(v[r]);
+        else
+            return T::load((uint16_t)(v[r] >> 16 * k));
     }
     // The same values, as if loaded again: what was computed from them before is
     // computed anew instead of waiting in registers.
@@ -135,7 +157,7 @@ struct ChunkRows {
 };
 
 // The rows of a chunk of an output.
-template <typename T>
+template <typename T, int V>
 struct ChunkOut {
     using E = typename T::store_t;
     __amdgpu_buffer_rsrc_t b;
@@ -147,16 +169,20 @@ struct ChunkOut {
           off((uint32_t)l.c * (uint32_t)sizeof(E))
     {
     }
-    __device__ __forceinline__ void store(int r, float v) const
+    __device__ __forceinline__ void store(int r, const float (&y)[V]) const
     {
-        rsrc_store(b, off, r * pitch, T::round(v));
+        if constexpr (V == 2)
+            __builtin_amdgcn_raw_buffer_store_b32(
+                (uint32_t)T::round(y[0]) | (uint32_t)T::round(y[V - 1]) << 16, b, off, r * pitch, 0);
+        else
+            rsrc_store(b, off, r * pitch, T::round(y[0]));
     }
 };
 
 // What a chunk reads.
-template <typename T>
+template <typename T, int V>
 struct ChunkIn {
-    ChunkRows<T> x, g, in;
+    ChunkRows<T, V> g, x, in;
     __device__ __forceinline__ void load(const RecurArgs& a, const Lane& l, int64_t s, int64_t row,
                                          int n)
     {
@@ -166,25 +192,31 @@ struct ChunkIn {
     }
 };
 
-// e and m = c i of a chunk's rows; rows beyond n leave the state as it is.
-template <typename T, bool DECAY>
-__device__ __forceinline__ void chunk_gates(const RecurArgs& a, const ChunkIn<T>& c, int n,
-                                            const Decay& d, float (&e)[kCh], float (&m)[kCh])
+// e and v of a chunk's rows; rows beyond n leave the state as it is.
+template <typename T, int V, bool DECAY>
+__device__ __forceinline__ void chunk_values(const RecurArgs& a, const ChunkIn<T, V>& c, int n,
+                                             const Decay (&d)[V], float (&e)[kCh][V],
+                                             float (&v)[kCh][V])
 {
 #pragma unroll
-    for (int r = 0; r < kCh; ++r) {
-        if (r % 4 == 0) __builtin_amdgcn_sched_barrier(0);  // else more registers
-        e[r] = gate_e<T, DECAY>(c.g[r], d);
-        m[r] = factor<DECAY>(e[r]);
-    }
+    for (int r = 0; r < kCh; ++r)
+#pragma unroll
+        for (int k = 0; k < V; ++k) {
+            e[r][k] = gate_e<T, DECAY>(c.g.get(r, k), d[k]);
+            v[r][k] = factor<DECAY>(e[r][k]) * c.x.get(r, k);
+        }
     if (a.input.p) {
 #pragma unroll
-        for (int r = 0; r < kCh; ++r) m[r] *= sigmoid_f<T>(c.in[r]);
+        for (int r = 0; r < kCh; ++r)
+#pragma unroll
+            for (int k = 0; k < V; ++k) v[r][k] *= sigmoid_f<T>(c.in.get(r, k));
     }
     if (n < kCh) {
 #pragma unroll
         for (int r = 0; r < kCh; ++r)
-            if (r >= n) e[r] = m[r] = 0.f;
+#pragma unroll
+            for (int k = 0; k < V; ++k)
+                if (r >= n) e[r][k] = v[r][k] = 0.f;
     }
 }
 
@@ -194,17 +226,27 @@ __device__ __forceinline__ float carry(float h, float q, float s)
     return (float)((double)h + fma64(q, h, s));
 }
 
+// Rows of a wave in the round that starts at `from`, of those before `end`.
+__device__ __forceinline__ int chunk_rows(const Lane& l, int32_t from, int32_t end)
+{
+    const int32_t left = end - from - l.wave * kCh;
+    return left < kCh ? left : kCh;
+}
+
 enum { kRecurSum, kRecurOut, kRecurWhole };
 
 // kRecurSum: Q and S of each block.  kRecurOut: the outputs of each block, from its
 // start state.  kRecurWhole: the outputs of whole sequences, block after block.
-template <typename T, bool DECAY, int MODE>
-__global__ __launch_bounds__(64 * kRecurWaves, 4) void k_recurrence(RecurArgs a)
+// Wave 0 carries the state from round to round.
+template <typename T, int V, bool DECAY, int MODE>
+__global__ __launch_bounds__(64 * kRecurWaves) void k_recurrence(RecurArgs a)
 {
-    __shared__ float lq[2][kRecurWaves][64], ls[2][kRecurWaves][64], lh[64];
+    constexpr int W = 64 * V;
+    __shared__ float lq[2][kRecurWaves][W], ls[2][kRecurWaves][W];
+    __shared__ double lh[2][W];
     const int64_t job = blockIdx.x / (uint32_t)a.slabs;
-    const Lane l = recur_lane(a, blockIdx.x - (uint32_t)job * a.slabs);
-    const Decay decay = load_decay<DECAY>(a.decay, l.ch);
+    const Lane l = recur_lane<V>(a, blockIdx.x - (uint32_t)job * a.slabs);
+    const int at_lds = l.lane * V;
     Chunk k;
     int64_t slot = job;
     if (MODE == kRecurWhole) {
@@ -218,102 +260,116 @@ __global__ __launch_bounds__(64 * kRecurWaves, 4) void k_recurrence(RecurArgs a)
         // the last block's fold serves no other
         if (MODE == kRecurSum && k.row + k.len >= k.span.len) return;
     }
-    float h0 = 0.f;
+    const int32_t end = MODE == kRecurWhole ? k.span.len : k.row + k.len;
+    ChunkIn<T, V> next;
+    if (const int n = chunk_rows(l, k.row, end); n > 0)
+        next.load(a, l, k.s, k.span.first + k.row + l.wave * kCh, n);
+    Decay decay[V];
+    load_decay<DECAY, V>(a.decay, l.ch, decay);
+    float h0[V] = {};
     // a block reads its start state where k_recur_carry has put it, also the first one:
     // the last one's workgroup may have overwritten init with final
     if (MODE == kRecurOut && a.ws_h)
-        h0 = a.ws_h[slot * a.channels + l.ch];
+        ld_channels<V>(a.ws_h + slot * a.channels + l.ch, h0);
     else if (MODE != kRecurSum && a.init)
-        h0 = a.init[k.s * a.channels + l.ch];
-    // the wave's rows of the round at `from`, none beyond `end`
-    const int32_t end = MODE == kRecurWhole ? k.span.len : k.row + k.len;
-    auto rows_of = [&](int32_t from) {
-        const int32_t left = end - from - l.wave * kCh;
-        return left < kCh ? left : kCh;
-    };
+        ld_channels<V>(a.init + k.s * a.channels + l.ch, h0);
+    if (MODE != kRecurSum && l.wave == 0) {
+#pragma unroll
+        for (int j = 0; j < V; ++j) lh[0][at_lds + j] = h0[j];
+    }
     int buf = 0;
-    ChunkIn<T> in;
-    if (const int n = rows_of(k.row); n > 0)
-        in.load(a, l, k.s, k.span.first + k.row + l.wave * kCh, n);
     for (;;) {
-        double h = h0, Q = 0., S = 0.;
-        const int rounds = (k.len + kRecurRound - 1) / kRecurRound;
-        for (int rd = 0; rd < rounds; ++rd, buf ^= 1) {
-            const int32_t from = k.row + rd * kRecurRound, at = from + l.wave * kCh;
-            const int n = rows_of(from);
-            float e[kCh], v[kCh];
+        double Q[V] = {}, S[V] = {};  // in wave 0
+        for (int32_t from = k.row; from < k.row + k.len; from += kRecurRound, buf ^= 1) {
+            const int32_t at = from + l.wave * kCh;
+            const int n = chunk_rows(l, from, end);
+            float e[kCh][V], v[kCh][V];
             if (n > 0) {
-                chunk_gates<T, DECAY>(a, in, n, decay, e, v);
+                const ChunkIn<T, V> in = next;
+                if (const int m = chunk_rows(l, from + kRecurRound, end); m > 0)
+                    next.load(a, l, k.s, k.span.first + at + kRecurRound, m);
+                chunk_values<T, V, DECAY>(a, in, n, decay, e, v);
 #pragma unroll
-                for (int r = 0; r < kCh; ++r) v[r] *= in.x[r];
-                // the next round's rows arrive meanwhile
-                if (const int m = rows_of(from + kRecurRound); m > 0)
-                    in.load(a, l, k.s, k.span.first + at + kRecurRound, m);
-                float q = 0.f, s = 0.f;
+                for (int j = 0; j < V; ++j) {
+                    float q = 0.f, s = 0.f;
 #pragma unroll
-                for (int r = 0; r < kCh; ++r) {
-                    s += fma32(e[r], s, v[r]);
-                    q += fma32(e[r], q, e[r]);
+                    for (int r = 0; r < kCh; ++r) {
+                        s += fma32(e[r][j], s, v[r][j]);
+                        q += fma32(e[r][j], q, e[r][j]);
+                    }
+                    lq[buf][l.wave][at_lds + j] = q;
+                    ls[buf][l.wave][at_lds + j] = s;
                 }
-                lq[buf][l.wave][l.lane] = q;
-                ls[buf][l.wave][l.lane] = s;
             }
             __syncthreads();
-            if (MODE != kRecurSum && a.kept && l.wave == 0 && l.on)
-                a.kept[(slot * kRecurRounds + rd) * a.channels + l.c] = (float)h;
-            const int32_t rows_left = k.len - rd * kRecurRound;
-            const int chunks =
-                rows_left < kRecurRound ? (rows_left + kCh - 1) / kCh : kRecurWaves;
-            double mine = h;
-#pragma unroll 1
-            for (int c = 0; c < chunks; ++c) {
-                const double q = lq[buf][c][l.lane], s = ls[buf][c][l.lane];
-                if (MODE != kRecurSum) {
-                    if (c == l.wave) mine = h;
-                    h += fma64(q, h, s);
+            double h[V];
+            if (MODE != kRecurSum) {
+#pragma unroll
+                for (int j = 0; j < V; ++j) h[j] = lh[buf][at_lds + j];
+#pragma unroll 2
+                for (int c = 0; c < l.wave; ++c)
+#pragma unroll
+                    for (int j = 0; j < V; ++j)
+                        h[j] += fma64(lq[buf][c][at_lds + j], h[j], ls[buf][c][at_lds + j]);
+            }
+            if (l.wave == 0) {
+                if (MODE != kRecurSum && a.kept && l.on) {
+                    float kept[V];
+#pragma unroll
+                    for (int j = 0; j < V; ++j) kept[j] = (float)h[j];
+                    st_channels<V>(a.kept + (slot * kRecurRounds + (from - k.row) / kRecurRound) *
+                                                a.channels + l.c, kept);
                 }
-                if (l.wave == 0) {
-                    S += fma64(q, S, s);
-                    Q += fma64(q, Q, q);
+                const int32_t rows = k.row + k.len - from;
+                const int chunks = rows < kRecurRound ? (rows + kCh - 1) / kCh : kRecurWaves;
+                double hn[V];
+#pragma unroll
+                for (int j = 0; j < V; ++j) hn[j] = MODE == kRecurSum ? 0. : h[j];
+#pragma unroll 2
+                for (int c = 0; c < chunks; ++c)
+#pragma unroll
+                    for (int j = 0; j < V; ++j) {
+                        const double q = lq[buf][c][at_lds + j], s = ls[buf][c][at_lds + j];
+                        if (MODE != kRecurSum) hn[j] += fma64(q, hn[j], s);
+                        S[j] += fma64(q, S[j], s);
+                        Q[j] += fma64(q, Q[j], q);
+                    }
+                if (from + kRecurRound >= k.row + k.len) {  // the block's end
+#pragma unroll
+                    for (int j = 0; j < V; ++j)
+                        hn[j] = h0[j] = carry(h0[j], (float)Q[j], (float)S[j]);
+                }
+                if (MODE != kRecurSum) {
+#pragma unroll
+                    for (int j = 0; j < V; ++j) lh[buf ^ 1][at_lds + j] = hn[j];
                 }
             }
             if (MODE != kRecurSum && n > 0) {
-                float y = (float)mine;
-                const ChunkOut<T> out(a.out, a.q, k.s, k.span.first + at, l);
+                float y[V];
+#pragma unroll
+                for (int j = 0; j < V; ++j) y[j] = (float)h[j];
+                const ChunkOut<T, V> out(a.out, a.q, k.s, k.span.first + at, l);
 #pragma unroll
                 for (int r = 0; r < kCh; ++r) {
-                    y += fma32(e[r], y, v[r]);
-                    v[r] = y;
-                }
-                if (l.on) {
-                    if (n >= kCh) {
 #pragma unroll
-                        for (int r = 0; r < kCh; ++r) out.store(r, v[r]);
-                    } else {
-#pragma unroll
-                        for (int r = 0; r < kCh; ++r)
-                            if (r < n) out.store(r, v[r]);
-                    }
+                    for (int j = 0; j < V; ++j) y[j] += fma32(e[r][j], y[j], v[r][j]);
+                    if (l.on && r < n) out.store(r, y);
                 }
             }
         }
         const bool last = k.row + k.len >= k.span.len;
-        if (MODE == kRecurSum) {
-            if (l.wave == 0 && l.on) {
-                a.ws_q[slot * a.channels + l.c] = (float)Q;
-                a.ws_s[slot * a.channels + l.c] = (float)S;
+        if (l.wave == 0 && l.on) {
+            if (MODE == kRecurSum) {
+                float q[V], s[V];
+#pragma unroll
+                for (int j = 0; j < V; ++j) q[j] = (float)Q[j], s[j] = (float)S[j];
+                st_channels<V>(a.ws_q + slot * a.channels + l.c, q);
+                st_channels<V>(a.ws_s + slot * a.channels + l.c, s);
+            } else if (last && a.final) {
+                st_channels<V>(a.final + k.s * a.channels + l.c, h0);
             }
-            return;
         }
-        if (l.wave == 0) {
-            if (k.len > 0) h0 = carry(h0, (float)Q, (float)S);
-            if (last && a.final && l.on) a.final[k.s * a.channels + l.c] = h0;
-        }
-        if (MODE == kRecurOut || last) return;
-        // wave 0's value for all; the next round's barrier is before the next write
-        if (l.wave == 0) lh[l.lane] = h0;
-        __syncthreads();
-        h0 = lh[l.lane];
+        if (MODE != kRecurWhole || last) return;
         k.row += CANON_RECUR_BLOCK;
         k.len = k.span.len - k.row < CANON_RECUR_BLOCK ? k.span.len - k.row : CANON_RECUR_BLOCK;
         ++slot;
@@ -325,8 +381,9 @@ __global__ __launch_bounds__(64 * kRecurWaves, 4) void k_recurrence(RecurArgs a)
 template <bool BACK>
 __global__ __launch_bounds__(64) void k_recur_carry(RecurArgs a)
 {
-    const int64_t s = blockIdx.x / (uint32_t)a.slabs;
-    const int32_t c = (blockIdx.x - (uint32_t)s * a.slabs) * 64 + threadIdx.x;
+    const uint32_t slabs = (a.channels + 63) / 64;
+    const int64_t s = blockIdx.x / slabs;
+    const int32_t c = (blockIdx.x - (uint32_t)s * slabs) * 64 + threadIdx.x;
     if (c >= a.channels) return;
     const Span span = seq_span(a.q, s);
     const int64_t slot = slot_base<CANON_RECUR_BLOCK>(a.q, s);
@@ -376,49 +433,59 @@ __global__ __launch_bounds__(256) void k_recurrence_step(RecurArgs a)
 // Backward.  With lam[t] = dout[t] + a[t+1] lam[t+1], the gradient of h[t]:
 //   dx = lam c i,   da = lam h[t-1],   d(c i x) = lam,
 // where h is folded again from the states kept at every round.  The fold of lam goes
-// backwards over chunks, rounds and blocks just as h's does forwards.
+// backwards over chunks, rounds and blocks just as h's does forwards; the last wave
+// carries it.
 // k_recur_back_sum: Q and the fold from zero of each block.
-template <typename T, bool DECAY>
+template <typename T, int V, bool DECAY>
 __global__ __launch_bounds__(64 * kRecurWaves) void k_recur_back_sum(RecurArgs a)
 {
-    __shared__ float lq[2][kRecurWaves][64], lt[2][kRecurWaves][64];
+    constexpr int W = 64 * V;
+    __shared__ float lq[2][kRecurWaves][W], lt[2][kRecurWaves][W];
     const int64_t slot = blockIdx.x / (uint32_t)a.slabs;
-    const Lane l = recur_lane(a, blockIdx.x - (uint32_t)slot * a.slabs);
-    const Decay decay = load_decay<DECAY>(a.decay, l.ch);
+    const Lane l = recur_lane<V>(a, blockIdx.x - (uint32_t)slot * a.slabs);
+    const int at_lds = l.lane * V;
+    Decay decay[V];
+    load_decay<DECAY, V>(a.decay, l.ch, decay);
     const Chunk k = wave_slot_chunk<CANON_RECUR_BLOCK>(a.q, slot);
     if (k.len <= 0 || k.row == 0) return;  // the first block's fold serves no other
-    double Q = 0., G = 0.;
+    double Q[V] = {}, G[V] = {};
     int buf = 0;
     for (int rd = (k.len - 1) / kRecurRound; rd >= 0; --rd, buf ^= 1) {
-        const int32_t at = k.row + rd * kRecurRound + l.wave * kCh;
-        const int32_t left = k.row + k.len - at;
-        const int n = left < kCh ? left : kCh;
-        float q = 0.f, t = 0.f;
+        const int32_t from = k.row + rd * kRecurRound, at = from + l.wave * kCh;
+        const int n = chunk_rows(l, from, k.row + k.len);
+        float q[V] = {}, t[V] = {};
         if (n > 0) {
-            ChunkRows<T> g, d;
+            ChunkRows<T, V> g, d;
             g.load(a.gate, a.q, k.s, k.span.first + at, l, n);
             d.load(a.dout, a.q, k.s, k.span.first + at, l, n);
 #pragma unroll
-            for (int r = kCh - 1; r >= 0; --r) {
-                const float e = r < n ? gate_e<T, DECAY>(g[r], decay) : 0.f;
-                const float lam = r < n ? d[r] + t : t;
-                t = fma32(e, lam, lam);
-                q += fma32(e, q, e);
-            }
+            for (int r = kCh - 1; r >= 0; --r)
+#pragma unroll
+                for (int j = 0; j < V; ++j) {
+                    const float e = r < n ? gate_e<T, DECAY>(g.get(r, j), decay[j]) : 0.f;
+                    const float lam = r < n ? d.get(r, j) + t[j] : t[j];
+                    t[j] = fma32(e, lam, lam);
+                    q[j] += fma32(e, q[j], e);
+                }
         }
-        lq[buf][l.wave][l.lane] = q;
-        lt[buf][l.wave][l.lane] = t;
+        st_channels<V>(&lq[buf][l.wave][at_lds], q);
+        st_channels<V>(&lt[buf][l.wave][at_lds], t);
         __syncthreads();
         if (l.wave == 0)
-            for (int c = kRecurWaves - 1; c >= 0; --c) {
-                const double cq = lq[buf][c][l.lane], ct = lt[buf][c][l.lane];
-                G += fma64(cq, G, ct);
-                Q += fma64(cq, Q, cq);
-            }
+            for (int c = kRecurWaves - 1; c >= 0; --c)
+#pragma unroll
+                for (int j = 0; j < V; ++j) {
+                    const double cq = lq[buf][c][at_lds + j], ct = lt[buf][c][at_lds + j];
+                    G[j] += fma64(cq, G[j], ct);
+                    Q[j] += fma64(cq, Q[j], cq);
+                }
     }
     if (l.wave == 0 && l.on) {
-        a.ws_q[slot * a.channels + l.c] = (float)Q;
-        a.ws_s[slot * a.channels + l.c] = (float)G;
+        float q[V], g[V];
+#pragma unroll
+        for (int j = 0; j < V; ++j) q[j] = (float)Q[j], g[j] = (float)G[j];
+        st_channels<V>(a.ws_q + slot * a.channels + l.c, q);
+        st_channels<V>(a.ws_s + slot * a.channels + l.c, g);
     }
 }
 
@@ -437,15 +504,17 @@ __device__ __forceinline__ Sigmoid sigmoid_both(float y)
 // A row keeps e and v = c i x in registers, and h[t-1] in LDS;
 //   d log a = lam (a h[t-1] - a^2 v / c^2),   c^2 = -e (2 + e),   and without decay
 //   d gate  = lam a (c h[t-1] - v).
-template <typename T, bool DECAY, int MODE>
-__global__ __launch_bounds__(64 * kRecurWaves, sizeof(typename T::store_t) == 2 ? 4 : 2) void
-k_recurrence_grad(RecurArgs a)
+template <typename T, int V, bool DECAY, int MODE>
+__global__ __launch_bounds__(64 * kRecurWaves) void k_recurrence_grad(RecurArgs a)
 {
-    __shared__ float lq[2][kRecurWaves][64], ls[2][kRecurWaves][64], lt[2][kRecurWaves][64],
-        lh[64], ldd[kRecurWaves][64], before[kRecurWaves][kCh][64];
+    constexpr int W = 64 * V;
+    __shared__ float lq[2][kRecurWaves][W], ls[2][kRecurWaves][W], lt[2][kRecurWaves][W],
+        ldd[kRecurWaves][W], before[kRecurWaves][kCh][W];
+    __shared__ double lg[2][W];
     const int64_t job = blockIdx.x / (uint32_t)a.slabs;
-    const Lane l = recur_lane(a, blockIdx.x - (uint32_t)job * a.slabs);
-    const Decay decay = load_decay<DECAY>(a.decay, l.ch);
+    const Lane l = recur_lane<V>(a, blockIdx.x - (uint32_t)job * a.slabs);
+    const int at_lds = l.lane * V;
+    const bool carrier = l.wave == kRecurWaves - 1;
     Chunk k;
     int64_t slot = job;
     if (MODE == kRecurWhole) {
@@ -458,133 +527,176 @@ k_recurrence_grad(RecurArgs a)
         k = wave_slot_chunk<CANON_RECUR_BLOCK>(a.q, slot);
         if (k.len < 0) k.len = 0;
         if (k.len == 0 && k.row != 0) {  // no block has this slot
-            if (DECAY && l.wave == 0 && l.on) a.ws_dd[slot * a.channels + l.c] = 0.f;
+            const float zero[V] = {};
+            if (DECAY && l.wave == 0 && l.on)
+                st_channels<V>(a.ws_dd + slot * a.channels + l.c, zero);
             return;
         }
     }
-    float g0 = 0.f;
+    const int32_t end = k.row + k.len;
+    Decay decay[V];
+    load_decay<DECAY, V>(a.decay, l.ch, decay);
+    float g0[V] = {};
     if (MODE == kRecurOut && a.ws_h)
-        g0 = a.ws_h[slot * a.channels + l.ch];
+        ld_channels<V>(a.ws_h + slot * a.channels + l.ch, g0);
     else if (a.dfinal)
-        g0 = a.dfinal[k.s * a.channels + l.ch];
+        ld_channels<V>(a.dfinal + k.s * a.channels + l.ch, g0);
+    if (carrier) {
+#pragma unroll
+        for (int j = 0; j < V; ++j) lg[0][at_lds + j] = g0[j];
+    }
     int buf = 0;
     for (;;) {
-        double G = g0, Q = 0., S = 0.;
-        float dd = 0.f;
+        double Q[V] = {}, S[V] = {};  // in the carrier
+        float dd[V] = {};
         for (int rd = (k.len + kRecurRound - 1) / kRecurRound - 1; rd >= 0; --rd, buf ^= 1) {
-            const int32_t at = k.row + rd * kRecurRound + l.wave * kCh;
-            const int32_t left = k.row + k.len - at;
-            const int n = left < kCh ? left : kCh;
-            const int64_t row = k.span.first + at;
-            ChunkIn<T> in;
-            ChunkRows<T> dout;
-            float e[kCh], v[kCh];
-            float q = 0.f, s = 0.f, t = 0.f;
+            const int32_t from = k.row + rd * kRecurRound;
+            const int n = chunk_rows(l, from, end);
+            const int64_t row = k.span.first + from + l.wave * kCh;
+            ChunkIn<T, V> in;
+            ChunkRows<T, V> dout;
+            float e[kCh][V], v[kCh][V];
+            float q[V] = {}, s[V] = {}, t[V] = {};
             if (n > 0) {
                 in.load(a, l, k.s, row, n);
                 dout.load(a.dout, a.q, k.s, row, l, n);
-                chunk_gates<T, DECAY>(a, in, n, decay, e, v);
+                chunk_values<T, V, DECAY>(a, in, n, decay, e, v);
 #pragma unroll
-                for (int r = 0; r < kCh; ++r) {
-                    if (r % 4 == 0) __builtin_amdgcn_sched_barrier(0);
-                    v[r] *= in.x[r];
-                    s += fma32(e[r], s, v[r]);
-                }
+                for (int r = 0; r < kCh; ++r)
 #pragma unroll
-                for (int r = kCh - 1; r >= 0; --r) {
-                    if (r % 4 == 3) __builtin_amdgcn_sched_barrier(0);
-                    const float lam = r < n ? dout[r] + t : t;
-                    t = fma32(e[r], lam, lam);
-                    q += fma32(e[r], q, e[r]);
-                }
+                    for (int j = 0; j < V; ++j) s[j] += fma32(e[r][j], s[j], v[r][j]);
+#pragma unroll
+                for (int r = kCh - 1; r >= 0; --r)
+#pragma unroll
+                    for (int j = 0; j < V; ++j) {
+                        const float lam = r < n ? dout.get(r, j) + t[j] : t[j];
+                        t[j] = fma32(e[r][j], lam, lam);
+                        q[j] += fma32(e[r][j], q[j], e[r][j]);
+                    }
             }
-            lq[buf][l.wave][l.lane] = q;
-            ls[buf][l.wave][l.lane] = s;
-            lt[buf][l.wave][l.lane] = t;
+            st_channels<V>(&lq[buf][l.wave][at_lds], q);
+            st_channels<V>(&ls[buf][l.wave][at_lds], s);
+            st_channels<V>(&lt[buf][l.wave][at_lds], t);
             __syncthreads();
-            double h = a.kept[(slot * kRecurRounds + rd) * a.channels + l.ch];
-#pragma unroll 1
-            for (int c = 0; c < l.wave; ++c)
-                h += fma64(lq[buf][c][l.lane], h, ls[buf][c][l.lane]);
-            double mine = G;
-#pragma unroll 1
-            for (int c = kRecurWaves - 1; c >= 0; --c) {
-                const double cq = lq[buf][c][l.lane], ct = lt[buf][c][l.lane];
-                if (c == l.wave) mine = G;
-                G += fma64(cq, G, ct);
-                if (l.wave == 0) {
-                    S += fma64(cq, S, ct);
-                    Q += fma64(cq, Q, cq);
+            double G[V];
+#pragma unroll
+            for (int j = 0; j < V; ++j) G[j] = lg[buf][at_lds + j];
+            if (carrier) {
+                double gn[V];
+#pragma unroll
+                for (int j = 0; j < V; ++j) gn[j] = G[j];
+#pragma unroll 2
+                for (int c = kRecurWaves - 1; c >= 0; --c)
+#pragma unroll
+                    for (int j = 0; j < V; ++j) {
+                        const double cq = lq[buf][c][at_lds + j], ct = lt[buf][c][at_lds + j];
+                        gn[j] += fma64(cq, gn[j], ct);
+                        S[j] += fma64(cq, S[j], ct);
+                        Q[j] += fma64(cq, Q[j], cq);
+                    }
+                if (rd == 0) {  // the block's start
+#pragma unroll
+                    for (int j = 0; j < V; ++j)
+                        gn[j] = g0[j] = carry(g0[j], (float)Q[j], (float)S[j]);
                 }
+#pragma unroll
+                for (int j = 0; j < V; ++j) lg[buf ^ 1][at_lds + j] = gn[j];
             }
             if (n <= 0) continue;
-            float y = (float)h;
+#pragma unroll 2
+            for (int c = kRecurWaves - 1; c > l.wave; --c)
+#pragma unroll
+                for (int j = 0; j < V; ++j)
+                    G[j] += fma64(lq[buf][c][at_lds + j], G[j], lt[buf][c][at_lds + j]);
+            float y[V];
+            {
+                float kept[V];
+                ld_channels<V>(a.kept + (slot * kRecurRounds + rd) * a.channels + l.ch, kept);
+                double h[V];
+#pragma unroll
+                for (int j = 0; j < V; ++j) h[j] = kept[j];
+#pragma unroll 2
+                for (int c = 0; c < l.wave; ++c)
+#pragma unroll
+                    for (int j = 0; j < V; ++j)
+                        h[j] += fma64(lq[buf][c][at_lds + j], h[j], ls[buf][c][at_lds + j]);
+#pragma unroll
+                for (int j = 0; j < V; ++j) y[j] = (float)h[j];
+            }
 #pragma unroll
             for (int r = 0; r < kCh; ++r) {
-                before[l.wave][r][l.lane] = y;
-                y += fma32(e[r], y, v[r]);
+                st_channels<V>(&before[l.wave][r][at_lds], y);
+#pragma unroll
+                for (int j = 0; j < V; ++j) y[j] += fma32(e[r][j], y[j], v[r][j]);
             }
             in.g.afresh();
             if (a.input.p) in.in.afresh();
             dout.afresh();
-            const ChunkOut<T> dx(a.dx, a.q, k.s, row, l), dg(a.dgate, a.q, k.s, row, l),
+            const ChunkOut<T, V> dx(a.dx, a.q, k.s, row, l), dg(a.dgate, a.q, k.s, row, l),
                 di(a.dinput, a.q, k.s, row, l);
-            float R = (float)mine;  // what reaches h[t] from the rows behind
+            float R[V];  // what reaches h[t] from the rows behind
+#pragma unroll
+            for (int j = 0; j < V; ++j) R[j] = (float)G[j];
 #pragma unroll
             for (int r = kCh - 1; r >= 0; --r) {
                 if (r >= n) continue;
                 // rows side by side would need more registers than there are
                 if (r % 2) __builtin_amdgcn_sched_barrier(0);
-                const float lam = dout[r] + R, hp = before[l.wave][r][l.lane];
-                R = fma32(e[r], lam, lam);
-                const Sigmoid g = sigmoid_both<T>(in.g[r]);
-                float out, m;
-                if (DECAY) {
-                    const float al = 1.f + e[r], z = -e[r] * (2.f + e[r]);
-                    const float slope = z > 0.f ? al * al * rcp_hw(z) : 0.f;
-                    const float rr = lam * fma32(al, hp, -(slope * v[r])) * g.s;
-                    dd -= rr;
-                    out = -decay.d * rr * g.rest;
-                    m = __builtin_amdgcn_sqrtf(z);
-                } else {
-                    // a itself, which 1 + e loses where it is small
-                    out = lam * g.s * fma32(-e[r], hp, -v[r]);
-                    m = -e[r];
+                float out[V], m[V], dinput[V];
+#pragma unroll
+                for (int j = 0; j < V; ++j) {
+                    const float lam = dout.get(r, j) + R[j], hp = before[l.wave][r][at_lds + j];
+                    const float er = e[r][j], vr = v[r][j];
+                    R[j] = fma32(er, lam, lam);
+                    const Sigmoid g = sigmoid_both<T>(in.g.get(r, j));
+                    if (DECAY) {
+                        const float al = 1.f + er, z = -er * (2.f + er);
+                        const float slope = z > 0.f ? al * al * rcp_hw(z) : 0.f;
+                        const float rr = lam * fma32(al, hp, -(slope * vr)) * g.s;
+                        dd[j] -= rr;
+                        out[j] = -decay[j].d * rr * g.rest;
+                        m[j] = __builtin_amdgcn_sqrtf(z);
+                    } else {
+                        // a itself, which 1 + e loses where it is small
+                        out[j] = lam * g.s * fma32(-er, hp, -vr);
+                        m[j] = -er;
+                    }
+                    if (a.input.p) {
+                        const Sigmoid i = sigmoid_both<T>(in.in.get(r, j));
+                        m[j] *= i.s;
+                        dinput[j] = lam * vr * i.rest;
+                    }
+                    m[j] *= lam;
                 }
                 if (l.on) {
                     dg.store(r, out);
-                    if (a.input.p) {
-                        const Sigmoid i = sigmoid_both<T>(in.in[r]);
-                        m *= i.s;
-                        di.store(r, lam * v[r] * i.rest);
-                    }
-                    dx.store(r, lam * m);
+                    if (a.input.p) di.store(r, dinput);
+                    dx.store(r, m);
                 }
             }
         }
         if (DECAY) {
-            ldd[l.wave][l.lane] = dd;
+            st_channels<V>(&ldd[l.wave][at_lds], dd);
             __syncthreads();
             if (l.wave == 0 && l.on) {
-                float v[kRecurWaves];
 #pragma unroll
-                for (int w = 0; w < kRecurWaves; ++w) v[w] = ldd[w][l.lane];
+                for (int j = 0; j < V; ++j) {
+                    float v[kRecurWaves];
 #pragma unroll
-                for (int p = 1; p < kRecurWaves; p *= 2)
+                    for (int w = 0; w < kRecurWaves; ++w) v[w] = ldd[w][at_lds + j];
 #pragma unroll
-                    for (int w = 0; w < kRecurWaves; w += 2 * p) v[w] += v[w + p];
-                a.ws_dd[slot * a.channels + l.c] = v[0];
+                    for (int p = 1; p < kRecurWaves; p *= 2)
+#pragma unroll
+                        for (int w = 0; w < kRecurWaves; w += 2 * p) v[w] += v[w + p];
+                    dd[j] = v[0];
+                }
+                st_channels<V>(a.ws_dd + slot * a.channels + l.c, dd);
             }
         }
         const bool first = k.row == 0;
-        if (l.wave == 0) {
-            if (k.len > 0) g0 = carry(g0, (float)Q, (float)S);
-            if (first && a.dinit && l.on) a.dinit[k.s * a.channels + l.c] = g0;
-        }
+        if (carrier && first && a.dinit && l.on)
+            st_channels<V>(a.dinit + k.s * a.channels + l.c, g0);
         if (MODE == kRecurOut || first) return;
-        if (l.wave == 0) lh[l.lane] = g0;
-        __syncthreads();
-        g0 = lh[l.lane];
         k.row -= CANON_RECUR_BLOCK;
         k.len = CANON_RECUR_BLOCK;
         --slot;
@@ -598,50 +710,67 @@ inline bool recur_whole(const RecurArgs& a)
     return a.q.starts == nullptr && a.q.seqs * a.slabs >= (int64_t)device_cus();
 }
 
-template <typename T, bool DECAY>
+// f(DECAY, V): two channels a lane where they fill a register and every row has them
+// aligned.
+template <typename T, class F>
+hipError_t with_recur(const RecurArgs& a, F&& f)
+{
+    if constexpr (sizeof(typename T::store_t) == 2) {
+        using Two = std::integral_constant<int, 2>;
+        if (a.pairs) return a.decay ? f(std::true_type{}, Two{}) : f(std::false_type{}, Two{});
+    }
+    using One = std::integral_constant<int, 1>;
+    return a.decay ? f(std::true_type{}, One{}) : f(std::false_type{}, One{});
+}
+
+template <typename T, bool DECAY, int V>
 hipError_t launch_recurrence_t(const RecurArgs& a, hipStream_t st)
 {
     const dim3 threads(64 * kRecurWaves);
     const unsigned seqs = (unsigned)(a.q.seqs * a.slabs);
+    const unsigned carries = (unsigned)(a.q.seqs * ((a.channels + 63) / 64));
     const int64_t slots = slot_count<CANON_RECUR_BLOCK>(a.q.seqs, a.q.rows, a.q.starts != nullptr);
     const unsigned blocks = (unsigned)(slots * a.slabs);
     if (a.ws_h && recur_whole(a)) {
-        k_recurrence<T, DECAY, kRecurWhole><<<dim3(seqs), threads, 0, st>>>(a);
+        k_recurrence<T, V, DECAY, kRecurWhole><<<dim3(seqs), threads, 0, st>>>(a);
         return hipGetLastError();
     }
     if (a.ws_h) {
-        k_recurrence<T, DECAY, kRecurSum><<<dim3(blocks), threads, 0, st>>>(a);
+        k_recurrence<T, V, DECAY, kRecurSum><<<dim3(blocks), threads, 0, st>>>(a);
         if (hipError_t e = hipGetLastError()) return e;
-        k_recur_carry<false><<<dim3(seqs), dim3(64), 0, st>>>(a);
+        k_recur_carry<false><<<dim3(carries), dim3(64), 0, st>>>(a);
         if (hipError_t e = hipGetLastError()) return e;
     }
-    k_recurrence<T, DECAY, kRecurOut><<<dim3(blocks), threads, 0, st>>>(a);
+    k_recurrence<T, V, DECAY, kRecurOut><<<dim3(blocks), threads, 0, st>>>(a);
     return hipGetLastError();
 }
 
 template <typename T>
 hipError_t launch_recurrence(const RecurArgs& a, hipStream_t st)
 {
-    return a.decay ? launch_recurrence_t<T, true>(a, st) : launch_recurrence_t<T, false>(a, st);
+    return with_recur<T>(a, [&](auto d, auto v) {
+        return launch_recurrence_t<T, decltype(d)::value, decltype(v)::value>(a, st);
+    });
 }
 
-template <typename T, bool DECAY>
+template <typename T, bool DECAY, int V>
 hipError_t launch_recurrence_grad_t(const RecurArgs& a, hipStream_t st)
 {
     const dim3 threads(64 * kRecurWaves);
     const unsigned seqs = (unsigned)(a.q.seqs * a.slabs);
+    const unsigned carries = (unsigned)(a.q.seqs * ((a.channels + 63) / 64));
     const int64_t slots = slot_count<CANON_RECUR_BLOCK>(a.q.seqs, a.q.rows, a.q.starts != nullptr);
     const unsigned blocks = (unsigned)(slots * a.slabs);
     if (a.ws_h && recur_whole(a)) {
-        k_recurrence_grad<T, DECAY, kRecurWhole><<<dim3(seqs), threads, 0, st>>>(a);
+        k_recurrence_grad<T, V, DECAY, kRecurWhole><<<dim3(seqs), threads, 0, st>>>(a);
     } else if (slots > 0) {
         if (a.ws_h) {
-            k_recur_back_sum<T, DECAY><<<dim3(blocks), threads, 0, st>>>(a);
+            k_recur_back_sum<T, V, DECAY><<<dim3(blocks), threads, 0, st>>>(a);
             if (hipError_t e = hipGetLastError()) return e;
-            k_recur_carry<true><<<dim3(seqs), dim3(64), 0, st>>>(a);
+            k_recur_carry<true><<<dim3(carries), dim3(64), 0, st>>>(a);
             if (hipError_t e = hipGetLastError()) return e;
         }
-        k_recurrence_grad<T, DECAY, kRecurOut><<<dim3(blocks), threads, 0, st>>>(a);
+        k_recurrence_grad<T, V, DECAY, kRecurOut><<<dim3(blocks), threads, 0, st>>>(a);
     }
     if (hipError_t e = hipGetLastError()) return e;
     if (!DECAY) return hipSuccess;
@@ -652,8 +781,9 @@ hipError_t launch_recurrence_grad_t(const RecurArgs& a, hipStream_t st)
 template <typename T>
 hipError_t launch_recurrence_grad(const RecurArgs& a, hipStream_t st)
 {
-    return a.decay ? launch_recurrence_grad_t<T, true>(a, st)
-                   : launch_recurrence_grad_t<T, false>(a, st);
+    return with_recur<T>(a, [&](auto d, auto v) {
+        return launch_recurrence_grad_t<T, decltype(d)::value, decltype(v)::value>(a, st);
+    });
 }
 
 template <typename T>
