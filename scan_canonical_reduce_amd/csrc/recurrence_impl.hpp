@@ -28,46 +28,49 @@ constexpr int kCh = CANON_RECUR_CHUNK;
 
 __device__ __forceinline__ double fma64(double a, double b, double c) { return __builtin_fma(a, b, c); }
 
-// exp(l) - 1 for l <= 0: the series, whose next term is below 2^-25 of l up to
-// 0.35, or the exponential less 1, which loses a bit and a half there.
-template <typename T>
-__device__ __forceinline__ float expm1_f(float l, bool near_only)
+// exp(l) - 1 for l <= 0: down to -1 by l + l^2 q(l), where q interpolates
+// (exp(l) - 1 - l) / l^2 at the Chebyshev nodes of [-1, 0] (off by 2^-25 of the result);
+// below it the exponential less 1, which loses less than a bit there.
+template <typename T, bool NEAR>
+__device__ __forceinline__ float expm1_f(float l)
 {
-    float p = fma32(l, 0x1.a01a02p-13f, 0x1.6c16c2p-10f);  // 1/7!, 1/6!
-    p = fma32(p, l, 0x1.111112p-7f);
-    p = fma32(p, l, 0x1.555556p-5f);
-    p = fma32(p, l, 0x1.555556p-3f);
+    float p = fma32(l, 0x1.20330cp-13f, 0x1.5b4b08p-10f);
+    p = fma32(p, l, 0x1.100344p-7f);
+    p = fma32(p, l, 0x1.5545cap-5f);
+    p = fma32(p, l, 0x1.5555p-3f);
     p = fma32(p, l, 0.5f);
     const float near = fma32(l * l, p, l);
-    if (near_only) return near;
-    return l > -0.35f ? near : exp_f<T>(l) - 1.f;
+    if (NEAR) return near;
+    return l > -1.f ? near : exp_f<T>(l) - 1.f;
 }
 
-// A channel's decay, and whether no lane of the wave has one above 0.35: then the
-// logarithm of a, between -decay and 0, needs the series alone.
+// The decays of a lane's channels, and whether no lane of the wave has one above 1:
+// then the logarithm of a, between -decay and 0, needs the polynomial alone.
+template <int V>
 struct Decay {
-    float d;
-    bool near_only;
+    float d[V];
+    bool near;
 };
 template <bool DECAY, int V>
-__device__ __forceinline__ void load_decay(const float* decay, int32_t ch, Decay (&d)[V])
+__device__ __forceinline__ Decay<V> load_decay(const float* decay, int32_t ch)
 {
-    bool near_only = DECAY;
+    Decay<V> d{{}, DECAY};
+    if (DECAY) {
 #pragma unroll
-    for (int k = 0; k < V; ++k) {
-        d[k].d = DECAY ? decay[ch + k] : 0.f;
-        near_only = near_only && __ballot(d[k].d < 0.35f) == ~0ull;
+        for (int k = 0; k < V; ++k) {
+            d.d[k] = decay[ch + k];
+            d.near = d.near && __ballot(d.d[k] <= 1.f) == ~0ull;
+        }
     }
-#pragma unroll
-    for (int k = 0; k < V; ++k) d[k].near_only = near_only;
+    return d;
 }
 
 // e = a - 1
-template <typename T, bool DECAY>
-__device__ __forceinline__ float gate_e(float gate, const Decay& d)
+template <typename T, bool DECAY, bool NEAR>
+__device__ __forceinline__ float gate_e(float gate, float decay)
 {
     if (!DECAY) return -sigmoid_f<T>(-gate);
-    return expm1_f<T>(-d.d * sigmoid_f<T>(gate), d.near_only);
+    return expm1_f<T, NEAR>(-decay * sigmoid_f<T>(gate));
 }
 // sqrt(1 - a^2) = sqrt((1 - a)(1 + a)), or 1 - a
 template <bool DECAY>
@@ -117,20 +120,20 @@ struct ChunkRows {
     static constexpr int kBytes = V * sizeof(E);
     uint32_t v[kCh];  // bits
 
-    // n rows are valid, at least one; the others are a copy of the last
+    // from the rows at b, of which n are valid, at least one; the others are a copy of
+    // the last
+    __device__ __forceinline__ void load_row(__amdgpu_buffer_rsrc_t b, const canon_rows_t& a,
+                                             const Lane& l, int r, int n)
+    {
+        v[r] = bits(b, (uint32_t)l.ch * (uint32_t)sizeof(E),
+                    (r < n ? r : n - 1) * ((uint32_t)a.row * (uint32_t)sizeof(E)));
+    }
     __device__ __forceinline__ void load(const canon_rows_t& a, const Seqs& q, int64_t s, int64_t row,
                                          const Lane& l, int n)
     {
         const __amdgpu_buffer_rsrc_t b = tile_rsrc(rows_ptr<T>(a, s, q, row));
-        const uint32_t pitch = (uint32_t)a.row * (uint32_t)sizeof(E);
-        const uint32_t off = (uint32_t)l.ch * (uint32_t)sizeof(E);
-        if (n >= kCh) {
 #pragma unroll
-            for (int r = 0; r < kCh; ++r) v[r] = bits(b, off, r * pitch);
-        } else {
-#pragma unroll
-            for (int r = 0; r < kCh; ++r) v[r] = bits(b, off, (r < n ? r : n - 1) * pitch);
-        }
+        for (int r = 0; r < kCh; ++r) load_row(b, a, l, r, n);
     }
     static __device__ __forceinline__ uint32_t bits(__amdgpu_buffer_rsrc_t b, uint32_t off,
                                                     uint32_t row)
@@ -156,60 +159,90 @@ struct ChunkRows {
     }
 };
 
-// The rows of a chunk of an output.
+// Two values rounded to 16 bits, the first in the lower half.
+__device__ __forceinline__ uint32_t round_two(BF16, float a, float b)
+{
+    typedef float f32x2 __attribute__((ext_vector_type(2)));
+    typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2{a, b}), bf16x2));
+}
+__device__ __forceinline__ uint32_t round_two(F16, float a, float b)
+{
+    return (uint32_t)F16::round(a) | (uint32_t)F16::round(b) << 16;
+}
+
+// The n rows of a chunk of an output.  Every lane stores every row, with an offset out
+// of the buffer's range, which drops it, where there is no such row or channel: without
+// branches the loads in flight are waited for by their number.
 template <typename T, int V>
 struct ChunkOut {
     using E = typename T::store_t;
+    static constexpr uint32_t kDropped = 0x80000000u;
     __amdgpu_buffer_rsrc_t b;
     uint32_t pitch, off;
+    int n;
     __device__ __forceinline__ ChunkOut(const canon_rows_t& a, const Seqs& q, int64_t s, int64_t row,
-                                        const Lane& l)
-        : b(tile_rsrc(rows_ptr<T>(a, s, q, row))),
+                                        const Lane& l, int rows)
+        : b(__builtin_amdgcn_make_buffer_rsrc(rows_ptr<T>(a, s, q, row), 0, 0x7fffffff, 0x00020000)),
           pitch((uint32_t)a.row * (uint32_t)sizeof(E)),
-          off((uint32_t)l.c * (uint32_t)sizeof(E))
+          off(l.on ? (uint32_t)l.c * (uint32_t)sizeof(E) : kDropped),
+          n(rows)
     {
     }
     __device__ __forceinline__ void store(int r, const float (&y)[V]) const
     {
+        const uint32_t to = r < n ? off : kDropped;
         if constexpr (V == 2)
-            __builtin_amdgcn_raw_buffer_store_b32(
-                (uint32_t)T::round(y[0]) | (uint32_t)T::round(y[V - 1]) << 16, b, off, r * pitch, 0);
+            __builtin_amdgcn_raw_buffer_store_b32(round_two(T{}, y[0], y[1]), b, to, r * pitch, 0);
         else
-            rsrc_store(b, off, r * pitch, T::round(y[0]));
+            rsrc_store(b, to, r * pitch, T::round(y[0]));
     }
 };
 
-// What a chunk reads.
+// What a chunk reads, and where its rows are.
 template <typename T, int V>
 struct ChunkIn {
     ChunkRows<T, V> g, x, in;
     __device__ __forceinline__ void load(const RecurArgs& a, const Lane& l, int64_t s, int64_t row,
                                          int n)
     {
-        g.load(a.gate, a.q, s, row, l, n);
-        x.load(a.x, a.q, s, row, l, n);
-        if (a.input.p) in.load(a.input, a.q, s, row, l, n);
+        const From from(a, s, row);
+#pragma unroll
+        for (int r = 0; r < kCh; ++r) load_row(a, l, from, r, n);
+    }
+    struct From {
+        __amdgpu_buffer_rsrc_t g, x, in;
+        __device__ __forceinline__ From(const RecurArgs& a, int64_t s, int64_t row)
+            : g(tile_rsrc(rows_ptr<T>(a.gate, s, a.q, row))),
+              x(tile_rsrc(rows_ptr<T>(a.x, s, a.q, row))),
+              in(tile_rsrc(rows_ptr<T>(a.input, s, a.q, row)))
+        {
+        }
+    };
+    __device__ __forceinline__ void load_row(const RecurArgs& a, const Lane& l, const From& f, int r,
+                                             int n)
+    {
+        g.load_row(f.g, a.gate, l, r, n);
+        x.load_row(f.x, a.x, l, r, n);
+        if (a.input.p) in.load_row(f.in, a.input, l, r, n);
     }
 };
 
-// e and v of a chunk's rows; rows beyond n leave the state as it is.
-template <typename T, int V, bool DECAY>
-__device__ __forceinline__ void chunk_values(const RecurArgs& a, const ChunkIn<T, V>& c, int n,
-                                             const Decay (&d)[V], float (&e)[kCh][V],
-                                             float (&v)[kCh][V])
+// e and v of a chunk's n rows; those beyond leave the state as it is.  after(r) follows
+// the last use of row r.
+template <typename T, int V, bool DECAY, bool NEAR, bool INPUT, class F>
+__device__ __forceinline__ void chunk_values(ChunkIn<T, V>& c, int n, const Decay<V>& d,
+                                             float (&e)[kCh][V], float (&v)[kCh][V], F&& after)
 {
 #pragma unroll
-    for (int r = 0; r < kCh; ++r)
+    for (int r = 0; r < kCh; ++r) {
 #pragma unroll
         for (int k = 0; k < V; ++k) {
-            e[r][k] = gate_e<T, DECAY>(c.g.get(r, k), d[k]);
+            e[r][k] = gate_e<T, DECAY, NEAR>(c.g.get(r, k), d.d[k]);
             v[r][k] = factor<DECAY>(e[r][k]) * c.x.get(r, k);
+            if (INPUT) v[r][k] *= sigmoid_f<T>(c.in.get(r, k));
         }
-    if (a.input.p) {
-#pragma unroll
-        for (int r = 0; r < kCh; ++r)
-#pragma unroll
-            for (int k = 0; k < V; ++k) v[r][k] *= sigmoid_f<T>(c.in.get(r, k));
+        after(r);
     }
     if (n < kCh) {
 #pragma unroll
@@ -219,11 +252,35 @@ __device__ __forceinline__ void chunk_values(const RecurArgs& a, const ChunkIn<T
                 if (r >= n) e[r][k] = v[r][k] = 0.f;
     }
 }
+template <typename T, int V, bool DECAY, class F>
+__device__ __forceinline__ void chunk_values(const RecurArgs& a, ChunkIn<T, V>& c, int n,
+                                             const Decay<V>& d, float (&e)[kCh][V],
+                                             float (&v)[kCh][V], F&& after)
+{
+    if (DECAY && d.near) {
+        if (a.input.p)
+            chunk_values<T, V, DECAY, true, true>(c, n, d, e, v, after);
+        else
+            chunk_values<T, V, DECAY, true, false>(c, n, d, e, v, after);
+    } else {
+        if (a.input.p)
+            chunk_values<T, V, DECAY, false, true>(c, n, d, e, v, after);
+        else
+            chunk_values<T, V, DECAY, false, false>(c, n, d, e, v, after);
+    }
+}
 
 // A value at the start of the next block, given the block's Q and S.
 __device__ __forceinline__ float carry(float h, float q, float s)
 {
     return (float)((double)h + fma64(q, h, s));
+}
+
+// A value further on in a block that starts with h, given the Q and S between; past
+// the block's end it is rounded to 32 bits.
+__device__ __forceinline__ double carried(float h, double q, double s, bool end)
+{
+    return end ? (double)carry(h, (float)q, (float)s) : (double)h + fma64(q, h, s);
 }
 
 // Rows of a wave in the round that starts at `from`, of those before `end`.
@@ -244,8 +301,8 @@ __global__ __launch_bounds__(64 * kRecurWaves) void k_recurrence(RecurArgs a)
     constexpr int W = 64 * V;
     __shared__ float lq[2][kRecurWaves][W], ls[2][kRecurWaves][W];
     __shared__ double lh[2][W];
-    const int64_t job = blockIdx.x / (uint32_t)a.slabs;
-    const Lane l = recur_lane<V>(a, blockIdx.x - (uint32_t)job * a.slabs);
+    const int32_t job = uniform((int32_t)(blockIdx.x / (uint32_t)a.slabs));
+    const Lane l = recur_lane<V>(a, blockIdx.x - job * a.slabs);
     const int at_lds = l.lane * V;
     Chunk k;
     int64_t slot = job;
@@ -261,11 +318,10 @@ __global__ __launch_bounds__(64 * kRecurWaves) void k_recurrence(RecurArgs a)
         if (MODE == kRecurSum && k.row + k.len >= k.span.len) return;
     }
     const int32_t end = MODE == kRecurWhole ? k.span.len : k.row + k.len;
-    ChunkIn<T, V> next;
+    ChunkIn<T, V> in;
     if (const int n = chunk_rows(l, k.row, end); n > 0)
-        next.load(a, l, k.s, k.span.first + k.row + l.wave * kCh, n);
-    Decay decay[V];
-    load_decay<DECAY, V>(a.decay, l.ch, decay);
+        in.load(a, l, k.s, k.span.first + k.row + l.wave * kCh, n);
+    const Decay<V> decay = load_decay<DECAY, V>(a.decay, l.ch);
     float h0[V] = {};
     // a block reads its start state where k_recur_carry has put it, also the first one:
     // the last one's workgroup may have overwritten init with final
@@ -285,10 +341,13 @@ __global__ __launch_bounds__(64 * kRecurWaves) void k_recurrence(RecurArgs a)
             const int n = chunk_rows(l, from, end);
             float e[kCh][V], v[kCh][V];
             if (n > 0) {
-                const ChunkIn<T, V> in = next;
-                if (const int m = chunk_rows(l, from + kRecurRound, end); m > 0)
-                    next.load(a, l, k.s, k.span.first + at + kRecurRound, m);
-                chunk_values<T, V, DECAY>(a, in, n, decay, e, v);
+                // The next round's row takes the place of the one just used; where there is
+                // none the last row is read again.
+                const int32_t to = at + kRecurRound < end ? at + kRecurRound : end - 1;
+                const int m = end - to < kCh ? end - to : kCh;
+                const typename ChunkIn<T, V>::From rows(a, k.s, k.span.first + to);
+                chunk_values<T, V, DECAY>(a, in, n, decay, e, v,
+                                          [&](int r) { in.load_row(a, l, rows, r, m); });
 #pragma unroll
                 for (int j = 0; j < V; ++j) {
                     float q = 0.f, s = 0.f;
@@ -322,38 +381,33 @@ __global__ __launch_bounds__(64 * kRecurWaves) void k_recurrence(RecurArgs a)
                 }
                 const int32_t rows = k.row + k.len - from;
                 const int chunks = rows < kRecurRound ? (rows + kCh - 1) / kCh : kRecurWaves;
-                double hn[V];
-#pragma unroll
-                for (int j = 0; j < V; ++j) hn[j] = MODE == kRecurSum ? 0. : h[j];
 #pragma unroll 2
                 for (int c = 0; c < chunks; ++c)
 #pragma unroll
                     for (int j = 0; j < V; ++j) {
                         const double q = lq[buf][c][at_lds + j], s = ls[buf][c][at_lds + j];
-                        if (MODE != kRecurSum) hn[j] += fma64(q, hn[j], s);
                         S[j] += fma64(q, S[j], s);
                         Q[j] += fma64(q, Q[j], q);
                     }
-                if (from + kRecurRound >= k.row + k.len) {  // the block's end
+                const bool done = from + kRecurRound >= k.row + k.len;  // the block's end
 #pragma unroll
-                    for (int j = 0; j < V; ++j)
-                        hn[j] = h0[j] = carry(h0[j], (float)Q[j], (float)S[j]);
-                }
-                if (MODE != kRecurSum) {
-#pragma unroll
-                    for (int j = 0; j < V; ++j) lh[buf ^ 1][at_lds + j] = hn[j];
+                for (int j = 0; j < V; ++j) {
+                    if (MODE == kRecurSum) continue;
+                    const double hn = carried(h0[j], Q[j], S[j], done);
+                    if (done) h0[j] = (float)hn;
+                    lh[buf ^ 1][at_lds + j] = hn;
                 }
             }
             if (MODE != kRecurSum && n > 0) {
                 float y[V];
 #pragma unroll
                 for (int j = 0; j < V; ++j) y[j] = (float)h[j];
-                const ChunkOut<T, V> out(a.out, a.q, k.s, k.span.first + at, l);
+                const ChunkOut<T, V> out(a.out, a.q, k.s, k.span.first + at, l, n);
 #pragma unroll
                 for (int r = 0; r < kCh; ++r) {
 #pragma unroll
                     for (int j = 0; j < V; ++j) y[j] += fma32(e[r][j], y[j], v[r][j]);
-                    if (l.on && r < n) out.store(r, y);
+                    out.store(r, y);
                 }
             }
         }
@@ -421,7 +475,7 @@ __global__ __launch_bounds__(256) void k_recurrence_step(RecurArgs a)
     auto row = [&](const canon_rows_t& r) {
         return static_cast<typename T::store_t*>(r.p) + s * r.seq + c;
     };
-    const float e = gate_e<T, DECAY>(ld<T>(row(a.gate)), Decay{DECAY ? a.decay[c] : 0.f, false});
+    const float e = gate_e<T, DECAY, false>(ld<T>(row(a.gate)), DECAY ? a.decay[c] : 0.f);
     float v = factor<DECAY>(e) * ld<T>(row(a.x));
     if (a.input.p) v *= sigmoid_f<T>(ld<T>(row(a.input)));
     float h = a.init ? a.init[i] : 0.f;
@@ -441,11 +495,10 @@ __global__ __launch_bounds__(64 * kRecurWaves) void k_recur_back_sum(RecurArgs a
 {
     constexpr int W = 64 * V;
     __shared__ float lq[2][kRecurWaves][W], lt[2][kRecurWaves][W];
-    const int64_t slot = blockIdx.x / (uint32_t)a.slabs;
-    const Lane l = recur_lane<V>(a, blockIdx.x - (uint32_t)slot * a.slabs);
+    const int64_t slot = uniform((int32_t)(blockIdx.x / (uint32_t)a.slabs));
+    const Lane l = recur_lane<V>(a, blockIdx.x - (int32_t)slot * a.slabs);
     const int at_lds = l.lane * V;
-    Decay decay[V];
-    load_decay<DECAY, V>(a.decay, l.ch, decay);
+    const Decay<V> decay = load_decay<DECAY, V>(a.decay, l.ch);
     const Chunk k = wave_slot_chunk<CANON_RECUR_BLOCK>(a.q, slot);
     if (k.len <= 0 || k.row == 0) return;  // the first block's fold serves no other
     double Q[V] = {}, G[V] = {};
@@ -462,7 +515,7 @@ __global__ __launch_bounds__(64 * kRecurWaves) void k_recur_back_sum(RecurArgs a
             for (int r = kCh - 1; r >= 0; --r)
 #pragma unroll
                 for (int j = 0; j < V; ++j) {
-                    const float e = r < n ? gate_e<T, DECAY>(g.get(r, j), decay[j]) : 0.f;
+                    const float e = r < n ? gate_e<T, DECAY, false>(g.get(r, j), decay.d[j]) : 0.f;
                     const float lam = r < n ? d.get(r, j) + t[j] : t[j];
                     t[j] = fma32(e, lam, lam);
                     q[j] += fma32(e, q[j], e);
@@ -511,8 +564,8 @@ __global__ __launch_bounds__(64 * kRecurWaves) void k_recurrence_grad(RecurArgs 
     __shared__ float lq[2][kRecurWaves][W], ls[2][kRecurWaves][W], lt[2][kRecurWaves][W],
         ldd[kRecurWaves][W], before[kRecurWaves][kCh][W];
     __shared__ double lg[2][W];
-    const int64_t job = blockIdx.x / (uint32_t)a.slabs;
-    const Lane l = recur_lane<V>(a, blockIdx.x - (uint32_t)job * a.slabs);
+    const int32_t job = uniform((int32_t)(blockIdx.x / (uint32_t)a.slabs));
+    const Lane l = recur_lane<V>(a, blockIdx.x - job * a.slabs);
     const int at_lds = l.lane * V;
     const bool carrier = l.wave == kRecurWaves - 1;
     Chunk k;
@@ -534,8 +587,7 @@ __global__ __launch_bounds__(64 * kRecurWaves) void k_recurrence_grad(RecurArgs 
         }
     }
     const int32_t end = k.row + k.len;
-    Decay decay[V];
-    load_decay<DECAY, V>(a.decay, l.ch, decay);
+    const Decay<V> decay = load_decay<DECAY, V>(a.decay, l.ch);
     float g0[V] = {};
     if (MODE == kRecurOut && a.ws_h)
         ld_channels<V>(a.ws_h + slot * a.channels + l.ch, g0);
@@ -555,12 +607,13 @@ __global__ __launch_bounds__(64 * kRecurWaves) void k_recurrence_grad(RecurArgs 
             const int64_t row = k.span.first + from + l.wave * kCh;
             ChunkIn<T, V> in;
             ChunkRows<T, V> dout;
-            float e[kCh][V], v[kCh][V];
+            float e[kCh][V], v[kCh][V], kept[V];
             float q[V] = {}, s[V] = {}, t[V] = {};
             if (n > 0) {
                 in.load(a, l, k.s, row, n);
                 dout.load(a.dout, a.q, k.s, row, l, n);
-                chunk_values<T, V, DECAY>(a, in, n, decay, e, v);
+                ld_channels<V>(a.kept + (slot * kRecurRounds + rd) * a.channels + l.ch, kept);
+                chunk_values<T, V, DECAY>(a, in, n, decay, e, v, [](int) {});
 #pragma unroll
                 for (int r = 0; r < kCh; ++r)
 #pragma unroll
@@ -582,25 +635,20 @@ __global__ __launch_bounds__(64 * kRecurWaves) void k_recurrence_grad(RecurArgs 
 #pragma unroll
             for (int j = 0; j < V; ++j) G[j] = lg[buf][at_lds + j];
             if (carrier) {
-                double gn[V];
-#pragma unroll
-                for (int j = 0; j < V; ++j) gn[j] = G[j];
 #pragma unroll 2
                 for (int c = kRecurWaves - 1; c >= 0; --c)
 #pragma unroll
                     for (int j = 0; j < V; ++j) {
                         const double cq = lq[buf][c][at_lds + j], ct = lt[buf][c][at_lds + j];
-                        gn[j] += fma64(cq, gn[j], ct);
                         S[j] += fma64(cq, S[j], ct);
                         Q[j] += fma64(cq, Q[j], cq);
                     }
-                if (rd == 0) {  // the block's start
 #pragma unroll
-                    for (int j = 0; j < V; ++j)
-                        gn[j] = g0[j] = carry(g0[j], (float)Q[j], (float)S[j]);
+                for (int j = 0; j < V; ++j) {
+                    const double gn = carried(g0[j], Q[j], S[j], rd == 0);  // the block's start
+                    if (rd == 0) g0[j] = (float)gn;
+                    lg[buf ^ 1][at_lds + j] = gn;
                 }
-#pragma unroll
-                for (int j = 0; j < V; ++j) lg[buf ^ 1][at_lds + j] = gn[j];
             }
             if (n <= 0) continue;
 #pragma unroll 2
@@ -610,8 +658,6 @@ __global__ __launch_bounds__(64 * kRecurWaves) void k_recurrence_grad(RecurArgs 
                     G[j] += fma64(lq[buf][c][at_lds + j], G[j], lt[buf][c][at_lds + j]);
             float y[V];
             {
-                float kept[V];
-                ld_channels<V>(a.kept + (slot * kRecurRounds + rd) * a.channels + l.ch, kept);
                 double h[V];
 #pragma unroll
                 for (int j = 0; j < V; ++j) h[j] = kept[j];
@@ -632,30 +678,30 @@ __global__ __launch_bounds__(64 * kRecurWaves) void k_recurrence_grad(RecurArgs 
             in.g.afresh();
             if (a.input.p) in.in.afresh();
             dout.afresh();
-            const ChunkOut<T, V> dx(a.dx, a.q, k.s, row, l), dg(a.dgate, a.q, k.s, row, l),
-                di(a.dinput, a.q, k.s, row, l);
+            const ChunkOut<T, V> dx(a.dx, a.q, k.s, row, l, n), dg(a.dgate, a.q, k.s, row, l, n),
+                di(a.dinput, a.q, k.s, row, l, n);
             float R[V];  // what reaches h[t] from the rows behind
 #pragma unroll
             for (int j = 0; j < V; ++j) R[j] = (float)G[j];
 #pragma unroll
             for (int r = kCh - 1; r >= 0; --r) {
-                if (r >= n) continue;
                 // rows side by side would need more registers than there are
                 if (r % 2) __builtin_amdgcn_sched_barrier(0);
                 float out[V], m[V], dinput[V];
 #pragma unroll
                 for (int j = 0; j < V; ++j) {
-                    const float lam = dout.get(r, j) + R[j], hp = before[l.wave][r][at_lds + j];
+                    const float lam = r < n ? dout.get(r, j) + R[j] : R[j], hp = before[l.wave][r][at_lds + j];
                     const float er = e[r][j], vr = v[r][j];
                     R[j] = fma32(er, lam, lam);
                     const Sigmoid g = sigmoid_both<T>(in.g.get(r, j));
                     if (DECAY) {
                         const float al = 1.f + er, z = -er * (2.f + er);
-                        const float slope = z > 0.f ? al * al * rcp_hw(z) : 0.f;
-                        const float rr = lam * fma32(al, hp, -(slope * vr)) * g.s;
-                        dd[j] -= rr;
-                        out[j] = -decay[j].d * rr * g.rest;
-                        m[j] = __builtin_amdgcn_sqrtf(z);
+                        const float rc = z > 0.f ? __builtin_amdgcn_rsqf(z) : 0.f;  // 1 / c
+                        const float q1 = al * rc;
+                        const float rr = lam * fma32(al, hp, -(q1 * q1 * vr)) * g.s;
+                        dd[j] -= r < n ? rr : 0.f;
+                        out[j] = -decay.d[j] * rr * g.rest;
+                        m[j] = z * rc;
                     } else {
                         // a itself, which 1 + e loses where it is small
                         out[j] = lam * g.s * fma32(-er, hp, -vr);
@@ -668,11 +714,9 @@ __global__ __launch_bounds__(64 * kRecurWaves) void k_recurrence_grad(RecurArgs 
                     }
                     m[j] *= lam;
                 }
-                if (l.on) {
-                    dg.store(r, out);
-                    if (a.input.p) di.store(r, dinput);
-                    dx.store(r, m);
-                }
+                dg.store(r, out);
+                if (a.input.p) di.store(r, dinput);
+                dx.store(r, m);
             }
         }
         if (DECAY) {
