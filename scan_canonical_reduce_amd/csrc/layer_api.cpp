@@ -116,8 +116,10 @@ canon_status_t with_params(int64_t dtype, int64_t param, F&& f)
 struct RecurLayout : Layout {
     size_t q = 0, s = 0, h = 0, dd = 0;
     bool carried;  // some sequence may have more than one block
+    bool launch;   // and some more than kRecurFold
     RecurLayout(int64_t seqs, int64_t rows, bool packed, int64_t channels, bool grad)
-        : carried(rows > CANON_RECUR_BLOCK && seqs > 0)
+        : carried(rows > CANON_RECUR_BLOCK && seqs > 0),
+          launch(rows > CANON_RECUR_BLOCK * kRecurFold)
     {
         const size_t n =
             4 * (size_t)slot_count<CANON_RECUR_BLOCK>(seqs, rows, packed) * (size_t)channels;
@@ -131,6 +133,7 @@ struct RecurLayout : Layout {
     void place(RecurArgs* a, void* ws) const
     {
         if (!carried) return;
+        a->carry = launch;
         a->ws_q = at<float>(ws, q);
         a->ws_s = at<float>(ws, s);
         a->ws_h = at<float>(ws, h);
@@ -199,8 +202,6 @@ canon_status_t recur_args(const canon_recur_t* c, bool step, bool grad, RecurArg
     for (const canon_rows_t* r : {&a->x, &a->gate, &a->input, &a->out, &a->dout, &a->dx, &a->dgate,
                                   &a->dinput})
         a->pairs = a->pairs && rows_aligned(*r, 2, 4, false);
-    const int32_t width = a->pairs ? 128 : 64;
-    a->slabs = (a->channels + width - 1) / width;
     const int64_t slots =
         step ? c->seqs : slot_count<CANON_RECUR_BLOCK>(c->seqs, rows, packed);
     if (!mul_fits(slots, (c->channels + 63) / 64, ((int64_t)1 << 22) - 1))

@@ -14,6 +14,9 @@ constexpr int kRecurWaves = 16;                               // chunks of a rou
 constexpr int kRecurRound = kRecurWaves * CANON_RECUR_CHUNK;  // rows between kept states
 constexpr int kRecurRounds = CANON_RECUR_BLOCK / kRecurRound;
 
+// Blocks of a sequence up to which each folds those before it itself.
+constexpr int64_t kRecurFold = 32;
+
 // Byte offsets within a chunk are 32-bit: row pitches below this many elements.
 constexpr int64_t kRecurPitch = (int64_t)1 << 24;
 
@@ -22,9 +25,11 @@ struct RecurArgs {
     canon_rows_t x, gate, input, out;
     const float *decay, *init;
     float *final, *kept;  // kept: per slot, kRecurRounds x channels
-    int32_t channels, slabs;  // slabs: 64 lanes' channels each
-    bool pairs;  // 16-bit values: two channels a lane, aligned in every row
+    int32_t channels;
+    int32_t slabs;  // of 64 lanes' channels each; set by the launcher
+    bool pairs;     // 16-bit values: two channels a lane, aligned in every row
     float *ws_q, *ws_s, *ws_h;  // per slot: channels; NULL where no sequence has two blocks
+    bool carry;  // a launch of its own makes the blocks' start states
     // backward
     canon_rows_t dout, dx, dgate, dinput;
     float *ddecay, *dinit;

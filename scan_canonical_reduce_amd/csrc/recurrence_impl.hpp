@@ -193,7 +193,7 @@ struct ChunkOut {
     {
         const uint32_t to = r < n ? off : kDropped;
         if constexpr (V == 2)
-            __builtin_amdgcn_raw_buffer_store_b32(round_two(T{}, y[0], y[1]), b, to, r * pitch, 0);
+            __builtin_amdgcn_raw_buffer_store_b32(round_two(T{}, y[0], y[1]), b, to, r * pitch, 2);
         else
             rsrc_store(b, to, r * pitch, T::round(y[0]));
     }
@@ -283,6 +283,34 @@ __device__ __forceinline__ double carried(float h, double q, double s, bool end)
     return end ? (double)carry(h, (float)q, (float)s) : (double)h + fma64(q, h, s);
 }
 
+// The state that a block starts with, given those of the first one in ws_h: where
+// sequences have few blocks, from the folds of the n before it, which are step slots apart
+// (else k_recur_carry has folded them, into its own ws_h).  With 32 blocks the outputs take
+// 62 us so, against 59 and a launch of 6 (16384 x 2048 bf16); the reads grow with the
+// square.
+template <int V>
+__device__ __forceinline__ void block_start(const RecurArgs& a, const Lane& l, int64_t slot, int32_t n,
+                                            int32_t step, float (&h)[V])
+{
+    if (a.carry) n = 0;
+    ld_channels<V>(a.ws_h + (slot + (int64_t)n * step) * a.channels + l.ch, h);
+    constexpr int U = 8;
+    for (int32_t left = n; left > 0; left -= U) {
+        float q[U][V], s[U][V];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int64_t i = (slot + (int64_t)(left - u > 1 ? left - u : 1) * step) * a.channels + l.ch;
+            ld_channels<V>(a.ws_q + i, q[u]);
+            ld_channels<V>(a.ws_s + i, s[u]);
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int j = 0; j < V; ++j)
+                if (u < left) h[j] = carry(h[j], q[u][j], s[u][j]);
+    }
+}
+
 // Rows of a wave in the round that starts at `from`, of those before `end`.
 __device__ __forceinline__ int chunk_rows(const Lane& l, int32_t from, int32_t end)
 {
@@ -323,12 +351,16 @@ __global__ __launch_bounds__(64 * kRecurWaves) void k_recurrence(RecurArgs a)
         in.load(a, l, k.s, k.span.first + k.row + l.wave * kCh, n);
     const Decay<V> decay = load_decay<DECAY, V>(a.decay, l.ch);
     float h0[V] = {};
-    // a block reads its start state where k_recur_carry has put it, also the first one:
-    // the last one's workgroup may have overwritten init with final
-    if (MODE == kRecurOut && a.ws_h)
-        ld_channels<V>(a.ws_h + slot * a.channels + l.ch, h0);
-    else if (MODE != kRecurSum && a.init)
+    // Where there are more blocks, the first one's fold keeps init in ws_h: the last one's
+    // outputs may overwrite init with final while others begin.
+    const bool cut = MODE != kRecurWhole && k.span.len > CANON_RECUR_BLOCK;
+    if (MODE == kRecurOut && cut) {
+        if (l.wave == 0) block_start<V>(a, l, slot, k.row / CANON_RECUR_BLOCK, -1, h0);
+    } else if (a.init && (MODE != kRecurSum || k.row == 0)) {
         ld_channels<V>(a.init + k.s * a.channels + l.ch, h0);
+    }
+    if (MODE == kRecurSum && k.row == 0 && l.wave == 0 && l.on)
+        st_channels<V>(a.ws_h + slot * a.channels + l.c, h0);
     if (MODE != kRecurSum && l.wave == 0) {
 #pragma unroll
         for (int j = 0; j < V; ++j) lh[0][at_lds + j] = h0[j];
@@ -430,8 +462,9 @@ __global__ __launch_bounds__(64 * kRecurWaves) void k_recurrence(RecurArgs a)
     }
 }
 
-// The start states of each sequence's blocks from the blocks' Q and S (in ws_q,
-// ws_s), into ws_h; backwards: the gradients that come in past their ends.
+// The start states of each sequence's blocks from the first one's (in ws_h) and the
+// blocks' Q and S (in ws_q, ws_s), into ws_h; backwards: the gradients that come in past
+// their ends.
 template <bool BACK>
 __global__ __launch_bounds__(64) void k_recur_carry(RecurArgs a)
 {
@@ -442,9 +475,8 @@ __global__ __launch_bounds__(64) void k_recur_carry(RecurArgs a)
     const Span span = seq_span(a.q, s);
     const int64_t slot = slot_base<CANON_RECUR_BLOCK>(a.q, s);
     const int32_t blocks = (span.len + CANON_RECUR_BLOCK - 1) / CANON_RECUR_BLOCK;
-    const float* from = BACK ? a.dfinal : a.init;
-    float h = from ? from[s * a.channels + c] : 0.f;
-    a.ws_h[(slot + (BACK && blocks > 0 ? blocks - 1 : 0)) * a.channels + c] = h;
+    if (blocks < 2) return;
+    float h = a.ws_h[(slot + (BACK ? blocks - 1 : 0)) * a.channels + c];
     constexpr int U = 8;
     for (int32_t b0 = 0; b0 < blocks - 1; b0 += U) {
         float q[U], v[U];
@@ -501,6 +533,11 @@ __global__ __launch_bounds__(64 * kRecurWaves) void k_recur_back_sum(RecurArgs a
     const Decay<V> decay = load_decay<DECAY, V>(a.decay, l.ch);
     const Chunk k = wave_slot_chunk<CANON_RECUR_BLOCK>(a.q, slot);
     if (k.len <= 0 || k.row == 0) return;  // the first block's fold serves no other
+    if (k.row + k.len >= k.span.len && l.wave == 0 && l.on) {
+        float g0[V] = {};
+        if (a.dfinal) ld_channels<V>(a.dfinal + k.s * a.channels + l.c, g0);
+        st_channels<V>(a.ws_h + slot * a.channels + l.c, g0);
+    }
     double Q[V] = {}, G[V] = {};
     int buf = 0;
     for (int rd = (k.len - 1) / kRecurRound; rd >= 0; --rd, buf ^= 1) {
@@ -589,9 +626,10 @@ __global__ __launch_bounds__(64 * kRecurWaves) void k_recurrence_grad(RecurArgs 
     const int32_t end = k.row + k.len;
     const Decay<V> decay = load_decay<DECAY, V>(a.decay, l.ch);
     float g0[V] = {};
-    if (MODE == kRecurOut && a.ws_h)
-        ld_channels<V>(a.ws_h + slot * a.channels + l.ch, g0);
-    else if (a.dfinal)
+    if (MODE == kRecurOut && k.span.len > CANON_RECUR_BLOCK) {
+        const int32_t last = (k.span.len - 1) / CANON_RECUR_BLOCK;
+        if (carrier) block_start<V>(a, l, slot, last - k.row / CANON_RECUR_BLOCK, 1, g0);
+    } else if (a.dfinal)
         ld_channels<V>(a.dfinal + k.s * a.channels + l.ch, g0);
     if (carrier) {
 #pragma unroll
@@ -747,42 +785,58 @@ __global__ __launch_bounds__(64 * kRecurWaves) void k_recurrence_grad(RecurArgs 
     }
 }
 
-// Sequences that are walked whole by a workgroup each: where that gives every
-// compute unit one.  Packed ones never are (their lengths are not known here).
-inline bool recur_whole(const RecurArgs& a)
-{
-    return a.q.starts == nullptr && a.q.seqs * a.slabs >= (int64_t)device_cus();
-}
-
-// f(DECAY, V): two channels a lane where they fill a register and every row has them
-// aligned.
+// f(a, DECAY, V, whole): how the work is laid over the compute units, of which a workgroup
+// takes one.
+//
+// Sequences of several blocks are walked whole by a workgroup each, where three quarters of
+// the units get one, or else in blocks side by side, for which the folds of the blocks take
+// a second pass over x and the gates.  2048 rows of 4096 channels, bf16, both gates, forward
+// and backward, whole against side by side: 6 sequences 93 + 203 us against 145 + 210, 3
+// sequences 58 + 128 against 88 + 126; but 2 sequences 56 + 114 against 49 + 73.  (Lengths of
+// packed sequences are not known here.)
+//
+// A lane takes two channels where they fill a register and are aligned in every row, but
+// one where that leaves no unit two workgroups: 8 sequences 124 + 235 us with two and
+// 132 + 263 with one, 4 sequences 80 + 179 and 61 + 132; side by side, 2
+// sequences 49 + 73 and 61 + 83, one of 2048 channels 44 + 66 and 33 + 47.
 template <typename T, class F>
-hipError_t with_recur(const RecurArgs& a, F&& f)
+hipError_t with_recur(RecurArgs a, F&& f)
 {
+    const int64_t cus = device_cus();
+    const bool packed = a.q.starts != nullptr;
+    // about as many as have rows: the last block of a packed sequence is short
+    const int64_t blocks = slot_count<CANON_RECUR_BLOCK>(a.q.seqs, a.q.rows, packed) -
+                           (packed ? a.q.seqs / 2 : 0);
+    auto slabs = [&](int v) { return (a.channels + 64 * v - 1) / (64 * v); };
+    const bool whole = a.ws_h && !packed && a.q.seqs * slabs(1) >= cus - cus / 4;
+    const int v = a.pairs && (whole ? a.q.seqs : blocks) * slabs(1) > cus ? 2 : 1;
+    a.slabs = slabs(v);
     if constexpr (sizeof(typename T::store_t) == 2) {
         using Two = std::integral_constant<int, 2>;
-        if (a.pairs) return a.decay ? f(std::true_type{}, Two{}) : f(std::false_type{}, Two{});
+        if (v == 2)
+            return a.decay ? f(a, std::true_type{}, Two{}, whole)
+                           : f(a, std::false_type{}, Two{}, whole);
     }
     using One = std::integral_constant<int, 1>;
-    return a.decay ? f(std::true_type{}, One{}) : f(std::false_type{}, One{});
+    return a.decay ? f(a, std::true_type{}, One{}, whole) : f(a, std::false_type{}, One{}, whole);
 }
 
 template <typename T, bool DECAY, int V>
-hipError_t launch_recurrence_t(const RecurArgs& a, hipStream_t st)
+hipError_t launch_recurrence_t(const RecurArgs& a, bool whole, hipStream_t st)
 {
     const dim3 threads(64 * kRecurWaves);
     const unsigned seqs = (unsigned)(a.q.seqs * a.slabs);
     const unsigned carries = (unsigned)(a.q.seqs * ((a.channels + 63) / 64));
     const int64_t slots = slot_count<CANON_RECUR_BLOCK>(a.q.seqs, a.q.rows, a.q.starts != nullptr);
     const unsigned blocks = (unsigned)(slots * a.slabs);
-    if (a.ws_h && recur_whole(a)) {
+    if (whole) {
         k_recurrence<T, V, DECAY, kRecurWhole><<<dim3(seqs), threads, 0, st>>>(a);
         return hipGetLastError();
     }
     if (a.ws_h) {
         k_recurrence<T, V, DECAY, kRecurSum><<<dim3(blocks), threads, 0, st>>>(a);
         if (hipError_t e = hipGetLastError()) return e;
-        k_recur_carry<false><<<dim3(carries), dim3(64), 0, st>>>(a);
+        if (a.carry) k_recur_carry<false><<<dim3(carries), dim3(64), 0, st>>>(a);
         if (hipError_t e = hipGetLastError()) return e;
     }
     k_recurrence<T, V, DECAY, kRecurOut><<<dim3(blocks), threads, 0, st>>>(a);
@@ -792,26 +846,26 @@ hipError_t launch_recurrence_t(const RecurArgs& a, hipStream_t st)
 template <typename T>
 hipError_t launch_recurrence(const RecurArgs& a, hipStream_t st)
 {
-    return with_recur<T>(a, [&](auto d, auto v) {
-        return launch_recurrence_t<T, decltype(d)::value, decltype(v)::value>(a, st);
+    return with_recur<T>(a, [&](const RecurArgs& b, auto d, auto v, bool whole) {
+        return launch_recurrence_t<T, decltype(d)::value, decltype(v)::value>(b, whole, st);
     });
 }
 
 template <typename T, bool DECAY, int V>
-hipError_t launch_recurrence_grad_t(const RecurArgs& a, hipStream_t st)
+hipError_t launch_recurrence_grad_t(const RecurArgs& a, bool whole, hipStream_t st)
 {
     const dim3 threads(64 * kRecurWaves);
     const unsigned seqs = (unsigned)(a.q.seqs * a.slabs);
     const unsigned carries = (unsigned)(a.q.seqs * ((a.channels + 63) / 64));
     const int64_t slots = slot_count<CANON_RECUR_BLOCK>(a.q.seqs, a.q.rows, a.q.starts != nullptr);
     const unsigned blocks = (unsigned)(slots * a.slabs);
-    if (a.ws_h && recur_whole(a)) {
+    if (whole) {
         k_recurrence_grad<T, V, DECAY, kRecurWhole><<<dim3(seqs), threads, 0, st>>>(a);
     } else if (slots > 0) {
         if (a.ws_h) {
             k_recur_back_sum<T, V, DECAY><<<dim3(blocks), threads, 0, st>>>(a);
             if (hipError_t e = hipGetLastError()) return e;
-            k_recur_carry<true><<<dim3(carries), dim3(64), 0, st>>>(a);
+            if (a.carry) k_recur_carry<true><<<dim3(carries), dim3(64), 0, st>>>(a);
             if (hipError_t e = hipGetLastError()) return e;
         }
         k_recurrence_grad<T, V, DECAY, kRecurOut><<<dim3(blocks), threads, 0, st>>>(a);
@@ -825,8 +879,8 @@ hipError_t launch_recurrence_grad_t(const RecurArgs& a, hipStream_t st)
 template <typename T>
 hipError_t launch_recurrence_grad(const RecurArgs& a, hipStream_t st)
 {
-    return with_recur<T>(a, [&](auto d, auto v) {
-        return launch_recurrence_grad_t<T, decltype(d)::value, decltype(v)::value>(a, st);
+    return with_recur<T>(a, [&](const RecurArgs& b, auto d, auto v, bool whole) {
+        return launch_recurrence_grad_t<T, decltype(d)::value, decltype(v)::value>(b, whole, st);
     });
 }
 
