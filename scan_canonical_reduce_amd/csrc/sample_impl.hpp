@@ -446,6 +446,13 @@ __global__ __launch_bounds__(kSampleThreads) void k_sample(SampleArgs a)
         __syncthreads();
     };
 
+    auto by_least = [&](auto f) {  // f(whether no weight is too small)
+        if (least == 0)
+            f(std::true_type{});
+        else
+            f(std::false_type{});
+    };
+
     // 2. and 3.
     bool summed = false;  // weights outside the list are in the groups' sums
     const bool by_p = p < 1.;
@@ -566,20 +573,22 @@ __global__ __launch_bounds__(kSampleThreads) void k_sample(SampleArgs a)
                 __syncthreads();
                 u64 w[3] = {0, 0, 0}, sums[3];  // of all, above the list, in it
                 const float f1 = (float)s_b1, f2 = (float)(s_b2 + 1);
-                group_sums([&](float x, uint32_t i) -> u64 {
-                    const u64 v = weigh(x);
-                    const float d = (top - x) * per;
-                    w[0] += v;
-                    if (d < f1) {
-                        w[1] += v;
-                        return v >= least ? v : 0;
-                    }
-                    if (d < f2) {
-                        w[2] += v;
-                        append(x, i);
-                    }
-                    return 0;
+                by_least([&](auto all) {
+                    group_sums([&](float x, uint32_t i) -> u64 {
+                        const u64 v = weigh(x);
+                        const float d = (top - x) * per;
+                        const u64 up = d < f1 ? v : 0;
+                        w[0] += v;
+                        if (d >= f1 && d < f2) {
+                            w[2] += v;
+                            append(x, i);
+                        }
+                        if (all.value) return up;
+                        w[1] += up;
+                        return up >= least ? up : 0;
+                    });
                 });
+                if (least == 0) w[1] = tid < kSums ? sh.sums[tid] : 0;
                 scan_before(w, wave64, sums);
                 target = min_share(p, sums[0]);
                 // the steps' sums are rounded: these decide
@@ -616,9 +625,11 @@ __global__ __launch_bounds__(kSampleThreads) void k_sample(SampleArgs a)
         });
         __syncthreads();
     } else if (border.x == -kMaxF && border.idx == 0xffffffffu) {  // all, masked ones weigh 0
-        group_sums([&](float x, uint32_t) {
-            const u64 v = weigh(x);
-            return v >= least ? v : 0;
+        by_least([&](auto all) {
+            group_sums([&](float x, uint32_t) {
+                const u64 v = weigh(x);
+                return all.value || v >= least ? v : 0;
+            });
         });
     } else {
         group_sums(kept);
