@@ -41,7 +41,7 @@ __device__ __forceinline__ float expm1_f(float l)
     p = fma32(p, l, 0.5f);
     const float near = fma32(l * l, p, l);
     if (NEAR) return near;
-    return l > -1.f ? near : exp_f<T>(l) - 1.f;
+    return l >= -1.f ? near : exp_f<T>(l) - 1.f;
 }
 
 // The decays of a lane's channels, and whether no lane of the wave has one above 1:
@@ -733,7 +733,11 @@ __global__ __launch_bounds__(64 * kRecurWaves) void k_recurrence_grad(RecurArgs 
                     R[j] = fma32(er, lam, lam);
                     const Sigmoid g = sigmoid_both<T>(in.g.get(r, j));
                     if (DECAY) {
-                        const float al = 1.f + er, z = -er * (2.f + er);
+                        // a itself, which 1 + e loses where it is small; by the channel's
+                        // decay alone, not its wave's
+                        float al = 1.f + er;
+                        if (!decay.near && decay.d[j] > 1.f) al = exp_f<T>(-decay.d[j] * g.s);
+                        const float z = -er * (2.f + er);
                         const float rc = z > 0.f ? __builtin_amdgcn_rsqf(z) : 0.f;  // 1 / c
                         const float q1 = al * rc;
                         const float rr = lam * fma32(al, hp, -(q1 * q1 * vr)) * g.s;
@@ -741,7 +745,6 @@ __global__ __launch_bounds__(64 * kRecurWaves) void k_recurrence_grad(RecurArgs 
                         out[j] = -decay.d[j] * rr * g.rest;
                         m[j] = z * rc;
                     } else {
-                        // a itself, which 1 + e loses where it is small
                         out[j] = lam * g.s * fma32(-er, hp, -vr);
                         m[j] = -er;
                     }

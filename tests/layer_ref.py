@@ -102,11 +102,17 @@ def recur(x, gate, input_gate=None, decay=None, init=None, dout=None, dfinal=Non
     Bounds, in float32 roundings U.  The sigmoid of y has a relative error of (|y| + 4) U
     (its exponential's is |y| U and an ulp, the reciprocal's an ulp), e = a - 1 one of
     (|gate| + 16) U, c i x one of (|gate| + |input_gate| + 26) U.  A chunk folds 16 rows
-    with two roundings each, relative to the absolute sum, and its ends go on as
+    at most with two roundings each, relative to the absolute sum, and its ends go on as
     32-bit values into a carry in 64 bits, rounded 3 times a block of 512 rows; an
     output adds its own chunk's 32 roundings.  So with A the recurrence of absolute
     values, an error E obeys
-      E <- a E + (48 + |gate|) U |e| A + (64 + |gate| + |input_gate|) U |c i x|."""
+      E <- a E + (48 + |gate|) U |e| A + (64 + |gate| + |input_gate|) U |c i x|.
+    The decay's and its gate's gradients take a itself, as exp(l), l = log a, with a
+    relative error of (|l| (|gate| + 5) + 1) U, or as 1 + e where |l| <= 1, with
+    (|e| (|gate| + 16) + 1) U / a, at most (1.72 |l| (|gate| + 16) + 2.72) U: the latter
+    bounds both, and counts twice for a^2.  An exp(l) below 2^-126, the least normal
+    float32, is 0, off by less than 2^-126: a decay of 100 reaches l = -87.4, and its
+    gradient that many times the least number."""
     f = {k: None if v is None else v.detach().double().cpu()
          for k, v in dict(x=x, g=gate, n=input_gate, D=decay, h=init, o=dout, F=dfinal).items()}
     x, g, n = f["x"], f["g"], f["n"]
@@ -156,7 +162,9 @@ def recur(x, gate, input_gate=None, decay=None, init=None, dout=None, dfinal=Non
                                 + L * (Ap + ix.abs()) * U * (2 * g.abs() + 16)))
     else:
         B, absB = a * hp - slope * ix, a * Ap + slope * ix.abs()
-        bound = (TL * absB + L * (a * Tp + slope * ix.abs() * 2 * kv + 8 * U * absB))
+        ka = 2 * U * (1.72 * f["D"] * r * (g.abs() + 16) + 2.72)
+        bound = (TL * absB + L * (a * Tp + slope * ix.abs() * 2 * kv + (8 * U + ka) * absB
+                                  + 2.0 ** -126 * Ap))
         dr = f["D"] * r * (1 - r)
         res["gate"] = (-dr * lam * B, dr * (bound + L * absB * U * (2 * g.abs() + 16)))
         blocks = x.shape[0] * (rows // BLOCK + 1)

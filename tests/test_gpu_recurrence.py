@@ -135,6 +135,27 @@ def test_whole_sequences(canon, dtype, decay, gated):
     check(canon, inputs(dtype, [530] * 16, 1100, False, decay, gated, 6), init=False, dfinal=False)
 
 
+@pytest.mark.parametrize("dtype", [F32, BF16, F16])
+def test_large_decays(canon, dtype):
+    """Decays from 0 to 100, 1 and its neighbours among them: in waves of channels with
+    none above 1, with some, and with large ones only."""
+    small = [0.0, 1e-6, 0.01, 0.35, 0.9, 1 - 2.0 ** -24, 1.0]
+    large = [1 + 2.0 ** -23, 1.5, 3.0, 8.0, 30.0, 100.0]
+    decay = torch.tensor((small * 19)[:128] + (small + large) * 10 + large * 20)
+    for lens in ([200] * 2, [600]):
+        d = inputs(dtype, lens, len(decay), seed=lens[0])
+        d["decay"] = decay.cuda()
+        check(canon, d)
+    d = inputs(dtype, [1] * 5, len(decay), seed=2)
+    d["decay"] = decay.cuda()
+    r = layer_ref.recur(d["x"], d["gate"], d["input_gate"], d["decay"], d["init"])
+    state = d["init"].clone()
+    out = canon.gated_recurrence_step(state, d["x"][:, 0], d["gate"][:, 0], d["decay"],
+                                      d["input_gate"][:, 0])
+    layer_ref.within(out[:, None], *r["out"], "out")
+    layer_ref.within(state, *r["final"], "state")
+
+
 def test_a_long_memory(canon):
     """a of 0.9999 and more over 9000 rows in float32."""
     for lens, packed in (([9000], False), ([3000, 6000], True)):
@@ -191,6 +212,58 @@ def test_same_bits_however_it_is_spread(canon, dtype, decay):
         b["init"] = state
         ob = forward(canon, b, final_state=state)
         assert torch.equal(torch.cat([oa, ob], 1), o2) and torch.equal(state, f2)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_same_bits_with_any_number_of_sequences(canon, dtype):
+    """Whole with two channels a lane where they fit, and with one; in blocks so and
+    so; 2 blocks and a row, an even and an odd number of channels."""
+    for ch in (130, 129):
+        d = inputs(dtype, [2 * BLOCK + 1] * 110, ch, seed=ch)
+        d["decay"][5], d["decay"][100] = 1.0, 3.0  # one alone in some waves, not in others
+        d["gate"][:, ::10, 5] = 40.0
+        for k in GATES + ("init", "dfinal", "dout"):
+            d[k] = torch.cat([d[k]] * 2)
+        want = None
+        for n in (220, 80, 64, 3, 1):  # 3 slabs of 64 channels each
+            p = {k: v if v is None or k in ("decay", "starts") else v[:n] for k, v in d.items()}
+            final, states = torch.empty_like(p["init"]), canon.gated_recurrence_states(p["x"])
+            got = [forward(canon, p, final_state=final, states=states), final]
+            g = backward(canon, p, states)
+            got += [g.dx, g.dgate, g.dinput_gate, g.dinit_state]
+            if want is None:
+                want = got
+            assert all(torch.equal(a, b[:n]) for a, b in zip(got, want)), (ch, n)
+        assert all(torch.equal(t[:110], t[110:]) for t in want)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("packed", [False, True])
+def test_many_blocks(canon, dtype, packed):
+    """More blocks than each folds those before it: the same bits, forward and backward,
+    as two calls that pass the state and its gradient on."""
+    blocks, cut = 35, 17 * BLOCK
+    d = inputs(dtype, [blocks * BLOCK - 100], 6, packed, slow=True, seed=8)
+    final, states = torch.empty_like(d["init"]), canon.gated_recurrence_states(d["x"], d["starts"])
+    out = forward(canon, d, final_state=final, states=states)
+    g = backward(canon, d, states)
+    rows = (lambda t, s: t[s]) if packed else (lambda t, s: t[:, s])
+    parts, state = [], d["init"]
+    for s in (slice(0, cut), slice(cut, None)):
+        p = dict(d, init=state, **{k: rows(d[k], s).contiguous() for k in GATES + ("dout",)})
+        if packed:
+            p["starts"] = torch.tensor([0, p["x"].shape[0]], dtype=torch.int32, device="cuda")
+        state, keep = torch.empty_like(state), canon.gated_recurrence_states(p["x"], p["starts"])
+        assert torch.equal(forward(canon, p, final_state=state, states=keep), rows(out, s))
+        parts.append((s, p, keep))
+    assert torch.equal(state, final)
+    dfinal = d["dfinal"]
+    for s, p, keep in reversed(parts):
+        b = backward(canon, dict(p, dfinal=dfinal), keep)
+        dfinal = b.dinit_state
+        for x, y in ((b.dx, g.dx), (b.dgate, g.dgate), (b.dinput_gate, g.dinput_gate)):
+            assert torch.equal(x, rows(y, s))
+    assert torch.equal(dfinal, g.dinit_state)
 
 
 @pytest.mark.parametrize("dtype", [F32, BF16, F16])
@@ -292,7 +365,7 @@ def test_gates_at_their_limits(canon):
         states = canon.gated_recurrence_states(d["x"])
         out = forward(canon, d, states=states)
         assert torch.isfinite(out).all()
-        # kept inside a chunk of 16 rows; the next one starts from its own carry
+        # kept inside a chunk of 8 rows; the next one starts from its own carry
         assert (out[:, 10:16] == out[:, 9:10]).all() and (out[:, 17:20] == out[:, 16:17]).all()
         if decay:
             assert (out[..., :8] == d["init"][:, None, :8]).all()

@@ -232,6 +232,16 @@ def test_recur_launch_limits(layer):
     p = dict(starts=FAKE)
     assert call(1, 512 * most - 1, 64 * 16383, **p) == 3
     assert call(1, 512 * most, 64 * 16383, **p) == 2
+    # row pitches, but for single rows
+    wide = 1 << 24
+    for name in ("x", "gate", "input_gate", "out"):
+        ok, far = ({name: Rows(FAKE * (3 if name == "out" else 1), 600 * p, p)}
+                   for p in (wide - 1, wide))
+        c = dict(seqs=1, rows=600, channels=64, x=Rows(FAKE, 64 * 600, 64),
+                 gate=Rows(FAKE, 64 * 600, 64), input_gate=Rows(FAKE, 64 * 600, 64),
+                 out=Rows(3 * FAKE, 64 * 600, 64))
+        assert L.canon_gated_recurrence(recur(**{**c, **ok}), None, 0, None) == 3, name
+        assert L.canon_gated_recurrence(recur(**{**c, **far}), None, 0, None) == 2, name
     r = Rows(FAKE, 64, 64)
     assert L.canon_gated_recurrence_step(recur(seqs=1 << 22, channels=64, x=r, gate=r, input_gate=r,
                                                out=Rows(3 * FAKE, 64, 64)), None) == 2
