@@ -61,6 +61,12 @@ def _lib() -> ctypes.CDLL:
     return L
 
 
+def _new(x: torch.Tensor) -> torch.Tensor:
+    """A contiguous uninitialised tensor like x (empty_like takes half a microsecond less
+    than new_empty, a twentieth of a small call)."""
+    return torch.empty_like(x) if x.is_contiguous() else x.new_empty(x.shape)
+
+
 # ------------------------------------------------------------------ layer norm
 class LayerNormGrads(NamedTuple):
     dx: torch.Tensor
@@ -93,7 +99,7 @@ def _layer_norm(what, x, residual, weight, bias, eps, stats, total, out):
     head, lead, params = _norm(what, x, weight, bias)
     shape, dtype = x.shape, x.dtype
     if out is None:
-        out = x.new_empty(shape)
+        out = _new(x)
     c = NORM.pack(*head, eps, *_rows(what, "x", x, shape, dtype, lead),
                   *(_NONE if residual is None else
                     _rows(what, "residual", residual, shape, dtype, lead)),
@@ -122,7 +128,7 @@ def add_layer_norm(x: torch.Tensor, residual: torch.Tensor, weight: torch.Tensor
     """(layer_norm(s, ...), s) with s = x + residual, rounded to their type, in one
     pass.  sum_out and out may each be x or residual (not the same one)."""
     if sum_out is None:
-        sum_out = x.new_empty(x.shape)
+        sum_out = _new(x)
     return _layer_norm("add_layer_norm", x, residual, weight, bias, eps, stats, sum_out,
                        out), sum_out
 
@@ -144,7 +150,7 @@ def layer_norm_grad(dout: torch.Tensor, x: torch.Tensor, weight: torch.Tensor,
     head, lead, params = _norm(what, x, weight, bias)
     shape, dtype, device = x.shape, x.dtype, x.device
     if dx is None:
-        dx = x.new_empty(shape)
+        dx = _new(x)
     dw = torch.empty(head[4], dtype=torch.float32, device=device)
     db = None if bias is None else torch.empty(head[4], dtype=torch.float32, device=device)
     c = NORM.pack(*head, 0.0, *_rows(what, "x", x, shape, dtype, lead), *_NONE, *_NONE, *_NONE,
@@ -213,7 +219,7 @@ def gated_recurrence(x: torch.Tensor, gate: torch.Tensor, decay: Optional[torch.
                      (L.canon_gated_recurrence_states(seqs, rows, packed, channels),), f32)
     d = _dtype(x, what)
     if out is None:
-        out = x.new_empty(shape)
+        out = _new(x)
     state = (seqs, channels)
     c = RECUR.pack(d, seqs, rows, channels, sp, *_rows(what, "x", x, shape, dtype, lead),
                    *_rows(what, "gate", gate, shape, dtype, lead),
@@ -253,9 +259,9 @@ def gated_recurrence_grad(dout: torch.Tensor, x: torch.Tensor, gate: torch.Tenso
         return torch.empty(s, dtype=f32, device=device)
 
     g = GatedRecurrenceGrads(
-        dx=x.new_empty(shape), dgate=x.new_empty(shape),
+        dx=_new(x), dgate=_new(x),
         ddecay=None if decay is None else empty(channels),
-        dinput_gate=None if input_gate is None else x.new_empty(shape),
+        dinput_gate=None if input_gate is None else _new(x),
         dinit_state=empty(seqs, channels))
     gi = _NONE, _NONE
     if input_gate is not None:
@@ -293,7 +299,7 @@ def gated_recurrence_step(state: torch.Tensor, x: torch.Tensor, gate: torch.Tens
     d = _dtype(x, what)
     old = _flat(what, "state", state, shape, f32)
     if out is None:
-        out = x.new_empty(shape)
+        out = _new(x)
     c = RECUR.pack(d, shape[0], 1, shape[1], 0, *_step_rows(what, "x", x, shape, dtype),
                    *_step_rows(what, "gate", gate, shape, dtype),
                    *(_NONE if input_gate is None else
