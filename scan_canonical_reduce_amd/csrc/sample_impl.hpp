@@ -425,7 +425,7 @@ __global__ __launch_bounds__(kSampleThreads) void k_sample(SampleArgs a)
         __syncthreads();
         border = s_border;
     };
-    // sums of value(x, index) by group
+    // sums of value(first index, vector) by group
     auto group_sums = [&](auto value) {
         for (int i = tid; i < kSums; i += kSampleThreads) sh.sums[i] = 0;
         __syncthreads();
@@ -439,8 +439,7 @@ __global__ __launch_bounds__(kSampleThreads) void k_sample(SampleArgs a)
         r.each([&](int g, int32_t at, const Vec<T, V>& v) {
             if (g != of) flush();
             of = g;
-#pragma unroll
-            for (int e = 0; e < V; ++e) sum += value(T::load(v.e[e]), (uint32_t)(at + e));
+            sum += value(at, v);
         });
         flush();
         __syncthreads();
@@ -572,20 +571,33 @@ __global__ __launch_bounds__(kSampleThreads) void k_sample(SampleArgs a)
                 if (b2 < kBins - 1) atomicMin(&s_b2, b2);
                 __syncthreads();
                 u64 w[3] = {0, 0, 0}, sums[3];  // of all, above the list, in it
-                const float f1 = (float)s_b1, f2 = (float)(s_b2 + 1);
+                const float x1 = top - (float)s_b1 / per, x2 = top - (float)(s_b2 + 1) / per;
                 by_least([&](auto all) {
-                    group_sums([&](float x, uint32_t i) -> u64 {
-                        const u64 v = weigh(x);
-                        const float d = (top - x) * per;
-                        const u64 up = d < f1 ? v : 0;
-                        w[0] += v;
-                        if (d >= f1 && d < f2) {
-                            w[2] += v;
-                            append(x, i);
+                    group_sums([&](int32_t at, const Vec<T, V>& x) {
+                        u64 up = 0;
+                        u64 any = 0;  // lanes with tokens in the steps, which are seen to
+                                      // afterwards: a branch for each holds up the others'
+                                      // weights (100 us against 90)
+#pragma unroll
+                        for (int e = 0; e < V; ++e) {
+                            const float y = T::load(x.e[e]);
+                            const u64 v = weigh(y);
+                            const u64 above = y > x1 ? v : 0;
+                            w[0] += v;
+                            if (!all.value) w[1] += above;
+                            up += all.value || above >= least ? above : 0;
+                            any |= __ballot(y <= x1 && y > x2);
                         }
-                        if (all.value) return up;
-                        w[1] += up;
-                        return up >= least ? up : 0;
+                        if (any) {
+#pragma unroll
+                            for (int e = 0; e < V; ++e) {
+                                const float y = T::load(x.e[e]);
+                                if (!(y <= x1 && y > x2)) continue;
+                                w[2] += weigh(y);
+                                append(y, (uint32_t)(at + e));
+                            }
+                        }
+                        return up;
                     });
                 });
                 if (least == 0) w[1] = tid < kSums ? sh.sums[tid] : 0;
@@ -626,13 +638,23 @@ __global__ __launch_bounds__(kSampleThreads) void k_sample(SampleArgs a)
         __syncthreads();
     } else if (border.x == -kMaxF && border.idx == 0xffffffffu) {  // all, masked ones weigh 0
         by_least([&](auto all) {
-            group_sums([&](float x, uint32_t) {
-                const u64 v = weigh(x);
-                return all.value || v >= least ? v : 0;
+            group_sums([&](int32_t, const Vec<T, V>& x) {
+                u64 sum = 0;
+#pragma unroll
+                for (int e = 0; e < V; ++e) {
+                    const u64 v = weigh(T::load(x.e[e]));
+                    sum += all.value || v >= least ? v : 0;
+                }
+                return sum;
             });
         });
     } else {
-        group_sums(kept);
+        group_sums([&](int32_t at, const Vec<T, V>& x) {
+            u64 sum = 0;
+#pragma unroll
+            for (int e = 0; e < V; ++e) sum += kept(T::load(x.e[e]), (uint32_t)(at + e));
+            return sum;
+        });
     }
     // each wave finds the group, whose wave goes on
     static_assert(kSums == 128, "two sums a lane");
