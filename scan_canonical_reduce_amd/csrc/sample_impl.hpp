@@ -205,7 +205,7 @@ __device__ __forceinline__ void scan_before(V (&v)[N], V (*lds)[kSampleWaves], V
 template <typename T>
 struct Row {
     using E = typename T::store_t;
-    static constexpr int V = 16 / sizeof(E), kPiece = 64 * V, U = 4;
+    static constexpr int V = 16 / sizeof(E), kPiece = 64 * V, U = 2;
     const E* x;
     int32_t n, G, groups;
     // the vector of this lane in a piece that starts at `first` (below n)
@@ -224,20 +224,31 @@ struct Row {
     {
         const int wave = uniform((int32_t)(threadIdx.x >> 6));
         int g = 0, i = 0;
-        while (g < groups) {
+        struct Batch {
             Vec<T, V> v[U];
             int32_t first[U];
             int gs[U];
+        };
+        auto fetch = [&](Batch& b) {
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                first[u] = ((g * kSampleWaves + wave) * G + i) * kPiece;
-                gs[u] = g < groups && first[u] < n ? g : -1;
-                if (gs[u] >= 0) v[u] = load(first[u]);
+                b.first[u] = ((g * kSampleWaves + wave) * G + i) * kPiece;
+                b.gs[u] = g < groups && b.first[u] < n ? g : -1;
+                if (b.gs[u] >= 0) b.v[u] = load(b.first[u]);
                 if (++i == G) i = 0, ++g;
             }
+        };
+        auto use = [&](const Batch& b) {
 #pragma unroll
             for (int u = 0; u < U; ++u)
-                if (gs[u] >= 0) f(gs[u], first[u] + (int32_t)(threadIdx.x & 63) * V, v[u]);
+                if (b.gs[u] >= 0) f(b.gs[u], b.first[u] + (int32_t)(threadIdx.x & 63) * V, b.v[u]);
+        };
+        Batch x, y;
+        fetch(x);
+        while (x.gs[0] >= 0) {
+            fetch(y);
+            use(x);
+            x = y;
         }
     }
 };
@@ -571,7 +582,7 @@ __global__ __launch_bounds__(kSampleThreads) void k_sample(SampleArgs a)
                 if (b2 < kBins - 1) atomicMin(&s_b2, b2);
                 __syncthreads();
                 u64 w[3] = {0, 0, 0}, sums[3];  // of all, above the list, in it
-                const float x1 = top - (float)s_b1 / per, x2 = top - (float)(s_b2 + 1) / per;
+                const float f1 = (float)s_b1, f2 = (float)(s_b2 + 1);
                 by_least([&](auto all) {
                     group_sums([&](int32_t at, const Vec<T, V>& x) {
                         u64 up = 0;
@@ -582,17 +593,18 @@ __global__ __launch_bounds__(kSampleThreads) void k_sample(SampleArgs a)
                         for (int e = 0; e < V; ++e) {
                             const float y = T::load(x.e[e]);
                             const u64 v = weigh(y);
-                            const u64 above = y > x1 ? v : 0;
+                            const float d = (top - y) * per;
+                            const u64 above = d < f1 ? v : 0;
                             w[0] += v;
                             if (!all.value) w[1] += above;
                             up += all.value || above >= least ? above : 0;
-                            any |= __ballot(y <= x1 && y > x2);
+                            any |= __ballot(d >= f1 && d < f2);
                         }
                         if (any) {
 #pragma unroll
                             for (int e = 0; e < V; ++e) {
-                                const float y = T::load(x.e[e]);
-                                if (!(y <= x1 && y > x2)) continue;
+                                const float y = T::load(x.e[e]), d = (top - y) * per;
+                                if (!(d >= f1 && d < f2)) continue;
                                 w[2] += weigh(y);
                                 append(y, (uint32_t)(at + e));
                             }
