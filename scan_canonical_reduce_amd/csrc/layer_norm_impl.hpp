@@ -399,8 +399,8 @@ __global__ __launch_bounds__(TEAM < 256 ? 256 : TEAM) void k_norm_grad(NormArgs 
     }
 }
 
-// Rows of any width, a workgroup each, read again for each sum (from the caches), U
-// vectors of a lane in flight.
+// Rows of any width, a workgroup each: the first U vectors of a lane in registers, the
+// others read again for each sum (from the caches), U of them in flight.
 constexpr int kLoopU = 4;
 
 template <typename T, typename P>
@@ -416,27 +416,42 @@ __global__ __launch_bounds__(1024) void k_norm_loop(NormArgs a)
         const E* res = a.residual.p ? norm_row<T>(a.residual, a, row) : nullptr;
         E* sum = a.sum.p ? norm_row<T>(a.sum, a, row) : nullptr;
         E* out = norm_row<T>(a.out, a, row);
+        // the vectors s of a lane from c on
+        auto fetch = [&](int c, Words16(&w)[U]) {
+#pragma unroll
+            for (int u = 0; u < U; ++u) w[u] = ld16<T>(x, c + u * STEP, a.width);
+            if (res) {
+                Words16 r[U];
+#pragma unroll
+                for (int u = 0; u < U; ++u) r[u] = ld16<T>(res, c + u * STEP, a.width);
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    float v[V];
+#pragma unroll
+                    for (int j = 0; j < V; ++j) v[j] = element<T>(w[u], j) + element<T>(r[u], j);
+                    w[u] = rounded<T>(v);
+                }
+            }
+        };
+        Words16 kept[U];
+        fetch(c0, kept);
         // f(column, the vector s there), in order
         auto each = [&](auto f) {
-            for (int c = c0; c < a.width; c += U * STEP) {
-                Words16 w[U], r[U];
-#pragma unroll
-                for (int u = 0; u < U; ++u) w[u] = ld16<T>(x, c + u * STEP, a.width);
-                if (res) {
-#pragma unroll
-                    for (int u = 0; u < U; ++u) r[u] = ld16<T>(res, c + u * STEP, a.width);
-                }
+            auto use = [&](int c, const Words16(&w)[U]) {
 #pragma unroll
                 for (int u = 0; u < U; ++u) {
                     if (c + u * STEP >= a.width) break;
                     float v[V];
 #pragma unroll
-                    for (int j = 0; j < V; ++j) {
-                        v[j] = element<T>(w[u], j);
-                        if (res) v[j] = T::load(T::round(v[j] + element<T>(r[u], j)));
-                    }
+                    for (int j = 0; j < V; ++j) v[j] = element<T>(w[u], j);
                     f(c + u * STEP, v);
                 }
+            };
+            use(c0, kept);
+            for (int c = c0 + U * STEP; c < a.width; c += U * STEP) {
+                Words16 w[U];
+                fetch(c, w);
+                use(c, w);
             }
         };
         float s = 0.f, q = 0.f;
@@ -484,14 +499,17 @@ __global__ __launch_bounds__(1024) void k_norm_dx_loop(NormArgs a)
         const E* dsum = a.dsum.p ? norm_row<T>(a.dsum, a, row) : nullptr;
         E* dx = norm_row<T>(a.dx, a, row);
         const float mean = a.stats[2 * (int64_t)row], rstd = a.stats[2 * (int64_t)row + 1];
+        auto fetch = [&](int c, Words16(&v)[U], Words16(&g)[U]) {
+#pragma unroll
+            for (int u = 0; u < U; ++u) v[u] = ld16<T>(x, c + u * STEP, a.width);
+#pragma unroll
+            for (int u = 0; u < U; ++u) g[u] = ld16<T>(dout, c + u * STEP, a.width);
+        };
+        Words16 kept_x[U], kept_g[U];
+        fetch(c0, kept_x, kept_g);
         // f(column, n and dout weight there), in order
         auto each = [&](auto f) {
-            for (int c = c0; c < a.width; c += U * STEP) {
-                Words16 v[U], g[U];
-#pragma unroll
-                for (int u = 0; u < U; ++u) v[u] = ld16<T>(x, c + u * STEP, a.width);
-#pragma unroll
-                for (int u = 0; u < U; ++u) g[u] = ld16<T>(dout, c + u * STEP, a.width);
+            auto use = [&](int c, const Words16(&v)[U], const Words16(&g)[U]) {
 #pragma unroll
                 for (int u = 0; u < U; ++u) {
                     const int at = c + u * STEP;
@@ -505,6 +523,12 @@ __global__ __launch_bounds__(1024) void k_norm_dx_loop(NormArgs a)
                     }
                     f(at, n, d);
                 }
+            };
+            use(c0, kept_x, kept_g);
+            for (int c = c0 + U * STEP; c < a.width; c += U * STEP) {
+                Words16 v[U], g[U];
+                fetch(c, v, g);
+                use(c, v, g);
             }
         };
         float sums[2] = {0.f, 0.f};
