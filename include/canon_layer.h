@@ -80,7 +80,7 @@ typedef struct {
 /* seqs x rows rows (there is no `starts`: rows are independent).  Reads x, residual,
  * weight, bias; writes sum, out, stats.  out and sum may each be x's or residual's
  * buffer with the same strides (in place), not each other's.
- * Limits (CANON_EUNSUPPORTED): seqs, rows < 2^30, seqs x rows < 2^31, width < 2^24,
+ * Limits (CANON_EUNSUPPORTED): seqs, rows and seqs x rows < 2^30, width < 2^24,
  * backward also max(512, seqs rows / 64) times ceil(width / 1024) below 2^24. */
 canon_status_t canon_layer_norm(const canon_norm_t* c, void* stream);
 
@@ -100,7 +100,7 @@ typedef struct {
     int64_t seqs, rows, channels;
     const int32_t* starts;
     canon_rows_t x, gate, input_gate, out; /* input_gate.p may be NULL (i = 1) */
-    const float* decay;      /* channels, not negative, or NULL (a = sigmoid(gate)) */
+    const float* decay;      /* channels, finite, not negative, or NULL (a = sigmoid(gate)) */
     const float* init_state; /* seqs x channels, or NULL (zero) */
     float* final_state;      /* the same shape, or NULL */
     float* kept_states;      /* canon_gated_recurrence_states(...) elements that the

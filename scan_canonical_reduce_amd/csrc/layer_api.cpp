@@ -24,10 +24,11 @@ bool in_place_ok(const canon_rows_t& out, const canon_rows_t& in)
 }
 
 // ----------------------------------------------------------------- layer norm
+// A row index and a step of the whole grid add up to less than 2^31.
 bool norm_sizes_ok(int64_t seqs, int64_t rows, int64_t width)
 {
     return seqs < kMaxRows && rows < kMaxRows && width < ((int64_t)1 << 24) &&
-           mul_fits(seqs, rows, ((int64_t)1 << 31) - 1);
+           mul_fits(seqs, rows, kMaxRows - 1);
 }
 
 int64_t norm_chunks(int64_t total)

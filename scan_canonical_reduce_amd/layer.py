@@ -203,7 +203,7 @@ def gated_recurrence(x: torch.Tensor, gate: torch.Tensor, decay: Optional[torch.
     a = exp(-decay sigmoid(gate)) and c = sqrt(1 - a^2), or without decay
     a = sigmoid(gate) and c = 1 - a; i = sigmoid(input_gate), or 1 without.
 
-    x, gate, input_gate: activations of one shape; decay [channels] float32, not
+    x, gate, input_gate: activations of one shape; decay [channels] float32, finite, not
     negative.  init_state, final_state [sequences, channels] float32: h before the
     first row and after the last (written, and may be init_state).  states: a buffer of
     gated_recurrence_states for the backward pass."""

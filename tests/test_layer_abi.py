@@ -140,8 +140,17 @@ def test_norm_in_place(layer):
 
 
 def test_norm_launch_limits(layer):
-    """Backward: chunks of rows times column tiles below 2^24."""
+    """Rows of all sequences below 2^30; backward: chunks of rows times column tiles
+    below 2^24."""
     L, n = layer._lib(), (1 << 24) - 1
+    for seqs, rows, want in ((1 << 15, (1 << 15) - 1, 3), (1 << 15, 1 << 15, 2),
+                             ((1 << 30) - 128, 1, 3), (2, 1 << 29, 2)):
+        x, out = Rows(FAKE, rows, 1), Rows(FAKE + 512, rows, 1)
+        kw = dict(seqs=seqs, rows=rows, width=1, x=x, dout=x, dsum=x, dx=out)
+        assert L.canon_layer_norm_grad(norm(**kw), None, 0, None) == want
+        assert (L.canon_layer_norm_grad_workspace_bytes(seqs, rows, 1) == 0) == (want == 2)
+        if want == 2:
+            assert L.canon_layer_norm(norm(**dict(kw, residual=x, sum=out, out=out)), None) == 2
     wide = Rows(FAKE, n, n)
     out = Rows(FAKE + 512, n, n)
     rows = 64 * 1023
