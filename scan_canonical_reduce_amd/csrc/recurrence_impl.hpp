@@ -5,14 +5,22 @@
 // once.  The 16 waves of a workgroup take the chunks of a round (128 rows), fold each
 // from zero, exchange the folds through LDS, and fold again from their chunks' start
 // states, with e = a - 1 and v = c i x still in registers: one pass over memory.  Rounds
-// of a block (512 rows) follow each other in the workgroup; the next round's rows are on
-// their way all the while.
+// of a block (512 rows) follow each other in the workgroup; forward, a row of the next
+// round is loaded where one of this round has been used.
+//
+// Memory bounds it, and about as much vector issue: 40 instructions a value forward, 5
+// of them transcendental, and 85 backward.  8 x 2048 x 4096 bf16, both gates: forward
+// 111 us (4.9 TB/s), backward 232 (4.1).  8 waves of 16 rows, at 256 registers a lane,
+// took 131 and 255 where these took 122 and 243; rows of the next round in flight in the
+// backward pass too cost spilled registers at 16 waves (338), and nothing was gained at 8
+// (260).
 //
 // a is near 1 for a long memory, and a rounding of h at every row would add up over
 // that memory.  So everything is kept as differences from 1: with e = a - 1,
 //   h <- h + (e h + v),   and for the product of a, Q = P - 1:  Q <- Q + (e Q + e),
-// and the start states of chunks, which see one rounding per chunk, are carried in 64
-// bits inside a block and rounded to 32 between blocks.
+// and the start states of rounds are carried in 64 bits inside a block and rounded to 32
+// between blocks.  Inside a round chunks fold on in 32 bits (64 took 4 instructions more a
+// value backward).
 #pragma once
 
 #include <type_traits>
@@ -149,6 +157,11 @@ struct ChunkRows {
             return __uint_as_float(v[r]);
         else
             return T::load((uint16_t)(v[r] >> 16 * k));
+    }
+    __device__ __forceinline__ void set(int r, float x)
+    {
+        v[r] = __float_as_uint(x);
+        if constexpr (sizeof(E) == 2) v[r] = T::round(x) * 0x10001u;
     }
     // The same values, as if loaded again: what was computed from them before is
     // computed anew instead of waiting in registers.
@@ -393,24 +406,20 @@ __global__ __launch_bounds__(64 * kRecurWaves) void k_recurrence(RecurArgs a)
                 }
             }
             __syncthreads();
-            double h[V];
+            float y[V];
             if (MODE != kRecurSum) {
 #pragma unroll
-                for (int j = 0; j < V; ++j) h[j] = lh[buf][at_lds + j];
+                for (int j = 0; j < V; ++j) y[j] = (float)lh[buf][at_lds + j];
 #pragma unroll 2
                 for (int c = 0; c < l.wave; ++c)
 #pragma unroll
                     for (int j = 0; j < V; ++j)
-                        h[j] += fma64(lq[buf][c][at_lds + j], h[j], ls[buf][c][at_lds + j]);
+                        y[j] += fma32(lq[buf][c][at_lds + j], y[j], ls[buf][c][at_lds + j]);
             }
             if (l.wave == 0) {
-                if (MODE != kRecurSum && a.kept && l.on) {
-                    float kept[V];
-#pragma unroll
-                    for (int j = 0; j < V; ++j) kept[j] = (float)h[j];
+                if (MODE != kRecurSum && a.kept && l.on)
                     st_channels<V>(a.kept + (slot * kRecurRounds + (from - k.row) / kRecurRound) *
-                                                a.channels + l.c, kept);
-                }
+                                                a.channels + l.c, y);
                 const int32_t rows = k.row + k.len - from;
                 const int chunks = rows < kRecurRound ? (rows + kCh - 1) / kCh : kRecurWaves;
 #pragma unroll 2
@@ -431,9 +440,6 @@ __global__ __launch_bounds__(64 * kRecurWaves) void k_recurrence(RecurArgs a)
                 }
             }
             if (MODE != kRecurSum && n > 0) {
-                float y[V];
-#pragma unroll
-                for (int j = 0; j < V; ++j) y[j] = (float)h[j];
                 const ChunkOut<T, V> out(a.out, a.q, k.s, k.span.first + at, l, n);
 #pragma unroll
                 for (int r = 0; r < kCh; ++r) {
@@ -652,6 +658,11 @@ __global__ __launch_bounds__(64 * kRecurWaves) void k_recurrence_grad(RecurArgs 
                 dout.load(a.dout, a.q, k.s, row, l, n);
                 ld_channels<V>(a.kept + (slot * kRecurRounds + rd) * a.channels + l.ch, kept);
                 chunk_values<T, V, DECAY>(a, in, n, decay, e, v, [](int) {});
+                if (n < kCh) {  // rows that add nothing to lam or to the decay's gradient
+#pragma unroll
+                    for (int r = 1; r < kCh; ++r)
+                        if (r >= n) dout.set(r, 0.f), in.g.set(r, -__builtin_inff());
+                }
 #pragma unroll
                 for (int r = 0; r < kCh; ++r)
 #pragma unroll
@@ -660,7 +671,7 @@ __global__ __launch_bounds__(64 * kRecurWaves) void k_recurrence_grad(RecurArgs 
                 for (int r = kCh - 1; r >= 0; --r)
 #pragma unroll
                     for (int j = 0; j < V; ++j) {
-                        const float lam = r < n ? dout.get(r, j) + t[j] : t[j];
+                        const float lam = dout.get(r, j) + t[j];
                         t[j] = fma32(e[r][j], lam, lam);
                         q[j] += fma32(e[r][j], q[j], e[r][j]);
                     }
@@ -669,9 +680,9 @@ __global__ __launch_bounds__(64 * kRecurWaves) void k_recurrence_grad(RecurArgs 
             st_channels<V>(&ls[buf][l.wave][at_lds], s);
             st_channels<V>(&lt[buf][l.wave][at_lds], t);
             __syncthreads();
-            double G[V];
+            float R[V];  // what reaches h[t] from the rows behind
 #pragma unroll
-            for (int j = 0; j < V; ++j) G[j] = lg[buf][at_lds + j];
+            for (int j = 0; j < V; ++j) R[j] = (float)lg[buf][at_lds + j];
             if (carrier) {
 #pragma unroll 2
                 for (int c = kRecurWaves - 1; c >= 0; --c)
@@ -693,20 +704,15 @@ __global__ __launch_bounds__(64 * kRecurWaves) void k_recurrence_grad(RecurArgs 
             for (int c = kRecurWaves - 1; c > l.wave; --c)
 #pragma unroll
                 for (int j = 0; j < V; ++j)
-                    G[j] += fma64(lq[buf][c][at_lds + j], G[j], lt[buf][c][at_lds + j]);
+                    R[j] += fma32(lq[buf][c][at_lds + j], R[j], lt[buf][c][at_lds + j]);
             float y[V];
-            {
-                double h[V];
 #pragma unroll
-                for (int j = 0; j < V; ++j) h[j] = kept[j];
+            for (int j = 0; j < V; ++j) y[j] = kept[j];
 #pragma unroll 2
-                for (int c = 0; c < l.wave; ++c)
+            for (int c = 0; c < l.wave; ++c)
 #pragma unroll
-                    for (int j = 0; j < V; ++j)
-                        h[j] += fma64(lq[buf][c][at_lds + j], h[j], ls[buf][c][at_lds + j]);
-#pragma unroll
-                for (int j = 0; j < V; ++j) y[j] = (float)h[j];
-            }
+                for (int j = 0; j < V; ++j)
+                    y[j] += fma32(lq[buf][c][at_lds + j], y[j], ls[buf][c][at_lds + j]);
 #pragma unroll
             for (int r = 0; r < kCh; ++r) {
                 st_channels<V>(&before[l.wave][r][at_lds], y);
@@ -718,9 +724,6 @@ __global__ __launch_bounds__(64 * kRecurWaves) void k_recurrence_grad(RecurArgs 
             dout.afresh();
             const ChunkOut<T, V> dx(a.dx, a.q, k.s, row, l, n), dg(a.dgate, a.q, k.s, row, l, n),
                 di(a.dinput, a.q, k.s, row, l, n);
-            float R[V];  // what reaches h[t] from the rows behind
-#pragma unroll
-            for (int j = 0; j < V; ++j) R[j] = (float)G[j];
 #pragma unroll
             for (int r = kCh - 1; r >= 0; --r) {
                 // rows side by side would need more registers than there are
@@ -728,7 +731,7 @@ __global__ __launch_bounds__(64 * kRecurWaves) void k_recurrence_grad(RecurArgs 
                 float out[V], m[V], dinput[V];
 #pragma unroll
                 for (int j = 0; j < V; ++j) {
-                    const float lam = r < n ? dout.get(r, j) + R[j] : R[j], hp = before[l.wave][r][at_lds + j];
+                    const float lam = dout.get(r, j) + R[j], hp = before[l.wave][r][at_lds + j];
                     const float er = e[r][j], vr = v[r][j];
                     R[j] = fma32(er, lam, lam);
                     const Sigmoid g = sigmoid_both<T>(in.g.get(r, j));
@@ -738,10 +741,11 @@ __global__ __launch_bounds__(64 * kRecurWaves) void k_recurrence_grad(RecurArgs 
                         float al = 1.f + er;
                         if (!decay.near && decay.d[j] > 1.f) al = exp_f<T>(-decay.d[j] * g.s);
                         const float z = -er * (2.f + er);
-                        const float rc = z > 0.f ? __builtin_amdgcn_rsqf(z) : 0.f;  // 1 / c
+                        // 1 / c; where c is 0, so is v, and the slope counts as 0
+                        const float rc = __builtin_amdgcn_rsqf(__builtin_fmaxf(z, 0x1p-126f));
                         const float q1 = al * rc;
                         const float rr = lam * fma32(al, hp, -(q1 * q1 * vr)) * g.s;
-                        dd[j] -= r < n ? rr : 0.f;
+                        dd[j] -= rr;
                         out[j] = -decay.d[j] * rr * g.rest;
                         m[j] = z * rc;
                     } else {

@@ -20,6 +20,14 @@
 //      which u's share falls, and the token in it.
 // Where a list does not fit (thousands of tokens in a step, as where all are equal),
 // the whole row is read again for every digit instead.
+//
+// What bounds it: of a row of 131072 in bfloat16, of which 256 fill the chip, the
+// largest takes 12 us (memory), the weights 31 (27 instructions in 64 bits a token, 23 us
+// of issue), the steps of top_p 23 (LDS atomics and the passes' start), their list and
+// the digits 10.  Adding up the weights themselves by steps with 64-bit atomics, so that
+// they need not be computed again, took 50 instead of 23, and paid only where top_p keeps
+// few tokens (0.5: 88 us for 92; 0.9: 119 for 100).  A small row costs its latency: 10 us
+// from call to call with no filter, 20 with top_p.
 #pragma once
 
 #include <type_traits>

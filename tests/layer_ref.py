@@ -101,11 +101,12 @@ def recur(x, gate, input_gate=None, decay=None, init=None, dout=None, dfinal=Non
 
     Bounds, in float32 roundings U.  The sigmoid of y has a relative error of (|y| + 4) U
     (its exponential's is |y| U and an ulp, the reciprocal's an ulp), e = a - 1 one of
-    (|gate| + 16) U, c i x one of (|gate| + |input_gate| + 26) U.  A chunk folds 16 rows
-    at most with two roundings each, relative to the absolute sum, and its ends go on as
-    32-bit values into a carry in 64 bits, rounded 3 times a block of 512 rows; an
-    output adds its own chunk's 32 roundings.  So with A the recurrence of absolute
-    values, an error E obeys
+    (|gate| + 16) U, c i x one of (|gate| + |input_gate| + 26) U.  A chunk folds 8 rows
+    with two roundings each, relative to the absolute sum; the state at a round's start
+    goes through a carry in 64 bits that takes the chunks' folds in 32 and is rounded 3
+    times a block of 512 rows; an output adds the rounding of that state to 32 bits, two
+    for each of at most 15 chunks of the round and the 16 of its own chunk, 47.  So with
+    A the recurrence of absolute values, an error E obeys
       E <- a E + (48 + |gate|) U |e| A + (64 + |gate| + |input_gate|) U |c i x|.
     The decay's and its gate's gradients take a itself, as exp(l), l = log a, with a
     relative error of (|l| (|gate| + 5) + 1) U, or as 1 + e where |l| <= 1, with
@@ -133,8 +134,8 @@ def recur(x, gate, input_gate=None, decay=None, init=None, dout=None, dfinal=Non
         if t % BLOCK == BLOCK - 1:
             E = E + 3 * U * A[-1]
         out.append(h[-1])
-        tol.append(E + 34 * U * A[-1])
-        T.append(E + 34 * U * A[-1])
+        tol.append(E + 48 * U * A[-1])
+        T.append(E + 48 * U * A[-1])
     res = {"out": (torch.stack(out, 1), torch.stack(tol, 1)) if rows else (x, x),
            "final": (h[-1], E + 4 * U * A[-1])}
     if f["o"] is None:
@@ -147,8 +148,8 @@ def recur(x, gate, input_gate=None, decay=None, init=None, dout=None, dfinal=Non
     for t in range(rows - 1, -1, -1):
         lam[:, t] = dout[:, t] + R
         L[:, t] = dout[:, t].abs() + absR
-        TL[:, t] = E + 34 * U * L[:, t]
-        E = a[:, t] * (E + 34 * U * dout[:, t].abs()) + ke[:, t] * L[:, t]
+        TL[:, t] = E + 48 * U * L[:, t]
+        E = a[:, t] * (E + 48 * U * dout[:, t].abs()) + ke[:, t] * L[:, t]
         R, absR = a[:, t] * lam[:, t], a[:, t] * L[:, t]
         if t % BLOCK == 0:
             E = E + 3 * U * absR
