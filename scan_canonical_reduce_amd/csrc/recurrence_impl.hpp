@@ -8,12 +8,11 @@
 // of a block (512 rows) follow each other in the workgroup; forward, a row of the next
 // round is loaded where one of this round has been used.
 //
-// Memory bounds it, and about as much vector issue: 40 instructions a value forward, 5
-// of them transcendental, and 85 backward.  8 x 2048 x 4096 bf16, both gates: forward
-// 111 us (4.9 TB/s), backward 232 (4.1).  8 waves of 16 rows, at 256 registers a lane,
-// took 131 and 255 where these took 122 and 243; rows of the next round in flight in the
-// backward pass too cost spilled registers at 16 waves (338), and nothing was gained at 8
-// (260).
+// Memory bounds it, and vector issue nearly as much: 36 instructions a value forward (66%
+// of the time), 82 backward (75%).  8 x 2048 x 4096 bf16, both gates: forward 113 us (4.8
+// TB/s), backward 233 (4.0).  8 waves of 16 rows, at 256 registers a lane, took 131 and
+// 255 where these then took 122 and 243; rows of the next round in flight in the backward
+// pass too cost spilled registers at 16 waves (338), and gained nothing at 8 (260).
 //
 // a is near 1 for a long memory, and a rounding of h at every row would add up over
 // that memory.  So everything is kept as differences from 1: with e = a - 1,
