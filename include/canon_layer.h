@@ -42,7 +42,8 @@
  *     the work is spread, and cutting a sequence at a multiple of CANON_RECUR_BLOCK
  *     rows and passing the state on changes no bit;
  *   - sums over rows (dweight, dbias, ddecay) go by chunks of rows and then over the
- *     chunks as the convolution's of canon_seq.h.
+ *     chunks as the convolution's of canon_seq.h; ddecay's depend on the number of
+ *     sequences, rows and channels.
  *
  * Conventions are those of canon_seq.h: canon_rows_t, dtype, sequences and starts,
  * workspaces, streams, capture and errors; columns are contiguous, any element

@@ -115,24 +115,37 @@ canon_status_t with_params(int64_t dtype, int64_t param, F&& f)
 
 // ----------------------------------------------------------------- recurrence
 struct RecurLayout : Layout {
-    size_t q = 0, s = 0, h = 0, dd = 0;
+    size_t q = 0, s = 0, h = 0, cq = 0, cs = 0, dd = 0;
     bool carried;  // some sequence may have more than one block
     bool launch;   // and some more than kRecurFold
+    bool spread;
     RecurLayout(int64_t seqs, int64_t rows, bool packed, int64_t channels, bool grad)
         : carried(rows > CANON_RECUR_BLOCK && seqs > 0),
           launch(rows > CANON_RECUR_BLOCK * kRecurFold)
     {
-        const size_t n =
-            4 * (size_t)slot_count<CANON_RECUR_BLOCK>(seqs, rows, packed) * (size_t)channels;
-        if (carried) {
+        const int64_t slots = slot_count<CANON_RECUR_BLOCK>(seqs, rows, packed);
+        const size_t n = 4 * (size_t)slots * (size_t)channels;
+        spread = recur_spread(slots, rows, channels) && seqs > 0;
+        if (spread) {
+            cq = take(kRecurBlockChunks * n);
+            cs = take(kRecurBlockChunks * n);
+            if (!grad) h = take(n);
+        } else if (carried) {
             q = take(n);
             s = take(n);
             h = take(n);
         }
-        if (grad) dd = take(n);
+        if (grad) dd = take(spread ? kRecurRounds * n : n);
     }
     void place(RecurArgs* a, void* ws) const
     {
+        a->spread = spread;
+        if (spread) {
+            a->ws_cq = at<float>(ws, cq);
+            a->ws_cs = at<float>(ws, cs);
+            a->ws_h = at<float>(ws, h);
+            return;
+        }
         if (!carried) return;
         a->carry = launch;
         a->ws_q = at<float>(ws, q);

@@ -336,26 +336,126 @@ __device__ __forceinline__ int chunk_rows(const Lane& l, int32_t from, int32_t e
     return left < kCh ? left : kCh;
 }
 
-enum { kRecurSum, kRecurOut, kRecurWhole };
+enum { kRecurSum, kRecurOut, kRecurWhole, kRecurSpreadOut };
+
+// The block and round of a workgroup, where each round has one; false if there are no
+// such rows.
+struct Round {
+    Chunk k;
+    int32_t rd, rounds;  // of the block
+    bool some;
+};
+__device__ __forceinline__ Round round_of(const RecurArgs& a, int32_t job)
+{
+    Round r;
+    r.k = wave_slot_chunk<CANON_RECUR_BLOCK>(a.q, job / kRecurRounds);
+    r.rd = job % kRecurRounds;
+    if (r.k.len < 0) r.k.len = 0;
+    r.rounds = (r.k.len + kRecurRound - 1) / kRecurRound;
+    r.some = r.rd < r.rounds;
+    return r;
+}
+
+// Q and S of a wave's chunks of a slot, n of them from c on (step 1), or up to c (step
+// -1), from their folds in ws_cq and ws_cs.
+__device__ __forceinline__ void fold_chunks(const RecurArgs& a, const Lane& l, int64_t slot, int c,
+                                            int n, int step, double& Q, double& S)
+{
+    constexpr int U = 16;  // of a round
+    Q = S = 0.;
+    for (; n > 0; n -= U) {
+        float q[U], s[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u, c += step) {
+            const int64_t i = (slot * kRecurBlockChunks + c) * a.channels + l.ch;
+            q[u] = a.ws_cq[i];
+            s[u] = a.ws_cs[i];
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            S += fma64(q[u], S, s[u]);
+            Q += fma64(q[u], Q, q[u]);
+        }
+    }
+}
+
+// The folds of the chunks of each round, for k_recurrence and k_recurrence_grad with a
+// workgroup for each round; those that serve no other are left out.
+template <typename T, bool DECAY, bool BACK>
+__global__ __launch_bounds__(64 * kRecurWaves) void k_recur_chunks(RecurArgs a)
+{
+    const int32_t job = uniform((int32_t)(blockIdx.x / (uint32_t)a.slabs));
+    const Lane l = recur_lane<1>(a, blockIdx.x - job * a.slabs);
+    const Round r = round_of(a, job);
+    if (!r.some) return;
+    const Chunk& k = r.k;
+    const int64_t slot = job / kRecurRounds;
+    const int32_t from = k.row + r.rd * kRecurRound, end = k.row + k.len;
+    const bool first = from == 0, last = from + kRecurRound >= k.span.len;
+    // the last workgroup of a sequence may overwrite init with final while others begin
+    if (!BACK && first && l.wave == 0 && l.on)
+        a.ws_h[slot * a.channels + l.c] = a.init ? a.init[k.s * a.channels + l.c] : 0.f;
+    if (BACK ? first : last) return;
+    const int n = chunk_rows(l, from, end);
+    const int64_t row = k.span.first + from + l.wave * kCh;
+    const Decay<1> decay = load_decay<DECAY, 1>(a.decay, l.ch);
+    float q = 0.f, s = 0.f;
+    if (n > 0 && !BACK) {
+        ChunkIn<T, 1> in;
+        float e[kCh][1], v[kCh][1];
+        in.load(a, l, k.s, row, n);
+        chunk_values<T, 1, DECAY>(a, in, n, decay, e, v, [](int) {});
+#pragma unroll
+        for (int i = 0; i < kCh; ++i) {
+            s += fma32(e[i][0], s, v[i][0]);
+            q += fma32(e[i][0], q, e[i][0]);
+        }
+    }
+    if (n > 0 && BACK) {
+        ChunkRows<T, 1> g, d;
+        g.load(a.gate, a.q, k.s, row, l, n);
+        d.load(a.dout, a.q, k.s, row, l, n);
+#pragma unroll
+        for (int i = kCh - 1; i >= 0; --i) {
+            if (i >= n) continue;
+            const float e = gate_e<T, DECAY, false>(g.get(i, 0), decay.d[0]);
+            const float lam = d.get(i, 0) + s;
+            s = fma32(e, lam, lam);
+            q += fma32(e, q, e);
+        }
+    }
+    if (!l.on) return;
+    const int64_t i = (slot * kRecurBlockChunks + r.rd * kRecurWaves + l.wave) * a.channels + l.c;
+    a.ws_cq[i] = q;
+    a.ws_cs[i] = s;
+}
 
 // kRecurSum: Q and S of each block.  kRecurOut: the outputs of each block, from its
 // start state.  kRecurWhole: the outputs of whole sequences, block after block.
-// Wave 0 carries the state from round to round.
+// Wave 0 carries the state from round to round.  kRecurSpreadOut: the outputs of each
+// round, to whose start the waves fold what is before, a block each.
 template <typename T, int V, bool DECAY, int MODE>
 __global__ __launch_bounds__(64 * kRecurWaves) void k_recurrence(RecurArgs a)
 {
     constexpr int W = 64 * V;
     __shared__ float lq[2][kRecurWaves][W], ls[2][kRecurWaves][W];
-    __shared__ double lh[2][W];
+    __shared__ double lh[2][W], lc[MODE == kRecurSpreadOut ? kRecurWaves : 1][2][W];
     const int32_t job = uniform((int32_t)(blockIdx.x / (uint32_t)a.slabs));
     const Lane l = recur_lane<V>(a, blockIdx.x - job * a.slabs);
     const int at_lds = l.lane * V;
     Chunk k;
+    int32_t rd = 0;
     int64_t slot = job;
     if (MODE == kRecurWhole) {
         k = Chunk{job, Span{0, (int32_t)a.q.rows}, 0, (int32_t)a.q.rows};
         if (k.len > CANON_RECUR_BLOCK) k.len = CANON_RECUR_BLOCK;
         slot = job * chunks_per_seq<CANON_RECUR_BLOCK>(a.q.rows);
+    } else if (MODE == kRecurSpreadOut) {
+        const Round r = round_of(a, job);
+        if (!r.some && (r.k.row != 0 || r.rd != 0)) return;
+        k = r.k;
+        rd = r.rd;
+        slot = job / kRecurRounds;
     } else {
         k = wave_slot_chunk<CANON_RECUR_BLOCK>(a.q, slot);
         if (k.len <= 0 && k.row != 0) return;  // no block has this slot
@@ -364,29 +464,47 @@ __global__ __launch_bounds__(64 * kRecurWaves) void k_recurrence(RecurArgs a)
         if (MODE == kRecurSum && k.row + k.len >= k.span.len) return;
     }
     const int32_t end = MODE == kRecurWhole ? k.span.len : k.row + k.len;
+    const int32_t start = k.row + rd * kRecurRound;
     ChunkIn<T, V> in;
-    if (const int n = chunk_rows(l, k.row, end); n > 0)
-        in.load(a, l, k.s, k.span.first + k.row + l.wave * kCh, n);
+    if (const int n = chunk_rows(l, start, end); n > 0)
+        in.load(a, l, k.s, k.span.first + start + l.wave * kCh, n);
     const Decay<V> decay = load_decay<DECAY, V>(a.decay, l.ch);
     float h0[V] = {};
     // Where there are more blocks, the first one's fold keeps init in ws_h: the last one's
     // outputs may overwrite init with final while others begin.
     const bool cut = MODE != kRecurWhole && k.span.len > CANON_RECUR_BLOCK;
-    if (MODE == kRecurOut && cut) {
+    const int32_t before = k.row / CANON_RECUR_BLOCK;
+    if (MODE == kRecurSpreadOut) {
+        if (k.len == 0) {
+            if (a.init) ld_channels<V>(a.init + k.s * a.channels + l.ch, h0);
+            if (a.final && l.wave == 0 && l.on)
+                st_channels<V>(a.final + k.s * a.channels + l.c, h0);
+            return;
+        }
+        ld_channels<V>(a.ws_h + (slot - before) * a.channels + l.ch, h0);
+        if (l.wave <= before) {
+            double Q, S;
+            fold_chunks(a, l, slot - before + l.wave, 0,
+                        l.wave < before ? kRecurBlockChunks : rd * kRecurWaves, 1, Q, S);
+            lc[l.wave][0][at_lds] = Q;
+            lc[l.wave][1][at_lds] = S;
+        }
+    } else if (MODE == kRecurOut && cut) {
         if (l.wave == 0) block_start<V>(a, l, slot, k.row / CANON_RECUR_BLOCK, -1, h0);
     } else if (a.init && (MODE != kRecurSum || k.row == 0)) {
         ld_channels<V>(a.init + k.s * a.channels + l.ch, h0);
     }
     if (MODE == kRecurSum && k.row == 0 && l.wave == 0 && l.on)
         st_channels<V>(a.ws_h + slot * a.channels + l.c, h0);
-    if (MODE != kRecurSum && l.wave == 0) {
+    if (MODE != kRecurSum && MODE != kRecurSpreadOut && l.wave == 0) {
 #pragma unroll
         for (int j = 0; j < V; ++j) lh[0][at_lds + j] = h0[j];
     }
     int buf = 0;
     for (;;) {
         double Q[V] = {}, S[V] = {};  // in wave 0
-        for (int32_t from = k.row; from < k.row + k.len; from += kRecurRound, buf ^= 1) {
+        for (int32_t from = MODE == kRecurSpreadOut ? start : k.row; from < k.row + k.len;
+             from += kRecurRound, buf ^= 1) {
             const int32_t at = from + l.wave * kCh;
             const int n = chunk_rows(l, from, end);
             float e[kCh][V], v[kCh][V];
@@ -396,8 +514,9 @@ __global__ __launch_bounds__(64 * kRecurWaves) void k_recurrence(RecurArgs a)
                 const int32_t to = at + kRecurRound < end ? at + kRecurRound : end - 1;
                 const int m = end - to < kCh ? end - to : kCh;
                 const typename ChunkIn<T, V>::From rows(a, k.s, k.span.first + to);
-                chunk_values<T, V, DECAY>(a, in, n, decay, e, v,
-                                          [&](int r) { in.load_row(a, l, rows, r, m); });
+                chunk_values<T, V, DECAY>(a, in, n, decay, e, v, [&](int r) {
+                    if (MODE != kRecurSpreadOut) in.load_row(a, l, rows, r, m);
+                });
 #pragma unroll
                 for (int j = 0; j < V; ++j) {
                     float q = 0.f, s = 0.f;
@@ -411,18 +530,30 @@ __global__ __launch_bounds__(64 * kRecurWaves) void k_recurrence(RecurArgs a)
                 }
             }
             __syncthreads();
+            if (MODE == kRecurSpreadOut) {
+                for (int32_t b = 0; b < before; ++b)
+                    h0[0] = carry(h0[0], (float)lc[b][0][at_lds], (float)lc[b][1][at_lds]);
+                Q[0] = lc[before][0][at_lds];
+                S[0] = lc[before][1][at_lds];
+            }
             float y[V];
             if (MODE != kRecurSum) {
 #pragma unroll
-                for (int j = 0; j < V; ++j) y[j] = (float)lh[buf][at_lds + j];
+                for (int j = 0; j < V; ++j)
+                    y[j] = MODE == kRecurSpreadOut
+                               ? (float)(rd ? carried(h0[j], Q[j], S[j], false) : (double)h0[j])
+                               : (float)lh[buf][at_lds + j];
 #pragma unroll 2
                 for (int c = 0; c < l.wave; ++c)
 #pragma unroll
                     for (int j = 0; j < V; ++j)
                         y[j] += fma32(lq[buf][c][at_lds + j], y[j], ls[buf][c][at_lds + j]);
             }
-            if (l.wave == 0) {
-                if (MODE != kRecurSum && a.kept && l.on)
+            const bool ends = from + kRecurRound >= k.span.len;
+            if (l.wave == 0 && a.kept && l.on && MODE == kRecurSpreadOut)
+                st_channels<V>(a.kept + (slot * kRecurRounds + rd) * a.channels + l.c, y);
+            if (l.wave == 0 && (MODE != kRecurSpreadOut || ends)) {
+                if (MODE != kRecurSum && MODE != kRecurSpreadOut && a.kept && l.on)
                     st_channels<V>(a.kept + (slot * kRecurRounds + (from - k.row) / kRecurRound) *
                                                 a.channels + l.c, y);
                 const int32_t rows = k.row + k.len - from;
@@ -441,7 +572,7 @@ __global__ __launch_bounds__(64 * kRecurWaves) void k_recurrence(RecurArgs a)
                     if (MODE == kRecurSum) continue;
                     const double hn = carried(h0[j], Q[j], S[j], done);
                     if (done) h0[j] = (float)hn;
-                    lh[buf ^ 1][at_lds + j] = hn;
+                    if (MODE != kRecurSpreadOut) lh[buf ^ 1][at_lds + j] = hn;
                 }
             }
             if (MODE != kRecurSum && n > 0) {
@@ -452,6 +583,11 @@ __global__ __launch_bounds__(64 * kRecurWaves) void k_recurrence(RecurArgs a)
                     for (int j = 0; j < V; ++j) y[j] += fma32(e[r][j], y[j], v[r][j]);
                     out.store(r, y);
                 }
+            }
+            if (MODE == kRecurSpreadOut) {
+                if (ends && l.wave == 0 && l.on && a.final)
+                    st_channels<V>(a.final + k.s * a.channels + l.c, h0);
+                return;
             }
         }
         const bool last = k.row + k.len >= k.span.len;
@@ -611,14 +747,28 @@ __global__ __launch_bounds__(64 * kRecurWaves) void k_recurrence_grad(RecurArgs 
     constexpr int W = 64 * V;
     __shared__ float lq[2][kRecurWaves][W], ls[2][kRecurWaves][W], lt[2][kRecurWaves][W],
         ldd[kRecurWaves][W], before[kRecurWaves][kCh][W];
-    __shared__ double lg[2][W];
+    __shared__ double lg[2][W], lc[MODE == kRecurSpreadOut ? kRecurWaves : 1][2][W];
     const int32_t job = uniform((int32_t)(blockIdx.x / (uint32_t)a.slabs));
     const Lane l = recur_lane<V>(a, blockIdx.x - job * a.slabs);
     const int at_lds = l.lane * V;
     const bool carrier = l.wave == kRecurWaves - 1;
     Chunk k;
     int64_t slot = job;
-    if (MODE == kRecurWhole) {
+    int32_t mine = 0;  // the round, where each has a workgroup
+    if (MODE == kRecurSpreadOut) {
+        const Round r = round_of(a, job);
+        k = r.k;
+        slot = job / kRecurRounds;
+        mine = r.rd;
+        if (!r.some) {
+            if (!l.on || l.wave != 0) return;
+            if (DECAY) a.ws_dd[(int64_t)job * a.channels + l.c] = 0.f;
+            if (k.row == 0 && mine == 0 && a.dinit)  // an empty sequence
+                a.dinit[k.s * a.channels + l.c] =
+                    a.dfinal ? a.dfinal[k.s * a.channels + l.c] : 0.f;
+            return;
+        }
+    } else if (MODE == kRecurWhole) {
         const int32_t rows = (int32_t)a.q.rows;
         const int32_t blocks = (int32_t)chunks_per_seq<CANON_RECUR_BLOCK>(rows);
         const int32_t row = (blocks - 1) * CANON_RECUR_BLOCK;
@@ -637,12 +787,28 @@ __global__ __launch_bounds__(64 * kRecurWaves) void k_recurrence_grad(RecurArgs 
     const int32_t end = k.row + k.len;
     const Decay<V> decay = load_decay<DECAY, V>(a.decay, l.ch);
     float g0[V] = {};
-    if (MODE == kRecurOut && k.span.len > CANON_RECUR_BLOCK) {
+    const int32_t rounds = (k.len + kRecurRound - 1) / kRecurRound;
+    const int32_t behind = (k.span.len - 1) / CANON_RECUR_BLOCK - k.row / CANON_RECUR_BLOCK;
+    if (MODE == kRecurSpreadOut) {
+        if (a.dfinal) ld_channels<V>(a.dfinal + k.s * a.channels + l.ch, g0);
+        if (l.wave <= behind) {  // from the last block on
+            const bool own = l.wave == behind;
+            const int32_t row = own ? k.row : k.row + (behind - l.wave) * CANON_RECUR_BLOCK;
+            const int32_t len =
+                k.span.len - row < CANON_RECUR_BLOCK ? k.span.len - row : CANON_RECUR_BLOCK;
+            const int32_t chunks = (len + kRecurRound - 1) / kRecurRound * kRecurWaves;
+            double Q, S;
+            fold_chunks(a, l, slot + behind - l.wave, chunks - 1,
+                        own ? chunks - (mine + 1) * kRecurWaves : chunks, -1, Q, S);
+            lc[l.wave][0][at_lds] = Q;
+            lc[l.wave][1][at_lds] = S;
+        }
+    } else if (MODE == kRecurOut && k.span.len > CANON_RECUR_BLOCK) {
         const int32_t last = (k.span.len - 1) / CANON_RECUR_BLOCK;
         if (carrier) block_start<V>(a, l, slot, last - k.row / CANON_RECUR_BLOCK, 1, g0);
     } else if (a.dfinal)
         ld_channels<V>(a.dfinal + k.s * a.channels + l.ch, g0);
-    if (carrier) {
+    if (carrier && MODE != kRecurSpreadOut) {
 #pragma unroll
         for (int j = 0; j < V; ++j) lg[0][at_lds + j] = g0[j];
     }
@@ -650,7 +816,8 @@ __global__ __launch_bounds__(64 * kRecurWaves) void k_recurrence_grad(RecurArgs 
     for (;;) {
         double Q[V] = {}, S[V] = {};  // in the carrier
         float dd[V] = {};
-        for (int rd = (k.len + kRecurRound - 1) / kRecurRound - 1; rd >= 0; --rd, buf ^= 1) {
+        for (int rd = MODE == kRecurSpreadOut ? mine : (k.len + kRecurRound - 1) / kRecurRound - 1;
+             rd >= (MODE == kRecurSpreadOut ? mine : 0); --rd, buf ^= 1) {
             const int32_t from = k.row + rd * kRecurRound;
             const int n = chunk_rows(l, from, end);
             const int64_t row = k.span.first + from + l.wave * kCh;
@@ -686,9 +853,17 @@ __global__ __launch_bounds__(64 * kRecurWaves) void k_recurrence_grad(RecurArgs 
             st_channels<V>(&lt[buf][l.wave][at_lds], t);
             __syncthreads();
             float R[V];  // what reaches h[t] from the rows behind
+            if (MODE == kRecurSpreadOut) {
+                for (int32_t b = 0; b < behind; ++b)
+                    g0[0] = carry(g0[0], (float)lc[b][0][at_lds], (float)lc[b][1][at_lds]);
+                Q[0] = lc[behind][0][at_lds];
+                S[0] = lc[behind][1][at_lds];
+                R[0] = (float)(rd < rounds - 1 ? carried(g0[0], Q[0], S[0], false) : (double)g0[0]);
+            } else {
 #pragma unroll
-            for (int j = 0; j < V; ++j) R[j] = (float)lg[buf][at_lds + j];
-            if (carrier) {
+                for (int j = 0; j < V; ++j) R[j] = (float)lg[buf][at_lds + j];
+            }
+            if (carrier && (MODE != kRecurSpreadOut || from == 0)) {
 #pragma unroll 2
                 for (int c = kRecurWaves - 1; c >= 0; --c)
 #pragma unroll
@@ -701,7 +876,7 @@ __global__ __launch_bounds__(64 * kRecurWaves) void k_recurrence_grad(RecurArgs 
                 for (int j = 0; j < V; ++j) {
                     const double gn = carried(g0[j], Q[j], S[j], rd == 0);  // the block's start
                     if (rd == 0) g0[j] = (float)gn;
-                    lg[buf ^ 1][at_lds + j] = gn;
+                    if (MODE != kRecurSpreadOut) lg[buf ^ 1][at_lds + j] = gn;
                 }
             }
             if (n <= 0) continue;
@@ -784,13 +959,14 @@ __global__ __launch_bounds__(64 * kRecurWaves) void k_recurrence_grad(RecurArgs 
                         for (int w = 0; w < kRecurWaves; w += 2 * p) v[w] += v[w + p];
                     dd[j] = v[0];
                 }
-                st_channels<V>(a.ws_dd + slot * a.channels + l.c, dd);
+                st_channels<V>(a.ws_dd + (MODE == kRecurSpreadOut ? job : slot) * a.channels + l.c,
+                               dd);
             }
         }
-        const bool first = k.row == 0;
+        const bool first = MODE == kRecurSpreadOut ? k.row == 0 && mine == 0 : k.row == 0;
         if (carrier && first && a.dinit && l.on)
             st_channels<V>(a.dinit + k.s * a.channels + l.c, g0);
-        if (MODE == kRecurOut || first) return;
+        if (MODE != kRecurWhole || first) return;
         k.row -= CANON_RECUR_BLOCK;
         k.len = CANON_RECUR_BLOCK;
         --slot;
@@ -820,8 +996,8 @@ hipError_t with_recur(RecurArgs a, F&& f)
     const int64_t blocks = slot_count<CANON_RECUR_BLOCK>(a.q.seqs, a.q.rows, packed) -
                            (packed ? a.q.seqs / 2 : 0);
     auto slabs = [&](int v) { return (a.channels + 64 * v - 1) / (64 * v); };
-    const bool whole = a.ws_h && !packed && a.q.seqs * slabs(1) >= cus - cus / 4;
-    const int v = a.pairs && (whole ? a.q.seqs : blocks) * slabs(1) > cus ? 2 : 1;
+    const bool whole = a.ws_h && !a.spread && !packed && a.q.seqs * slabs(1) >= cus - cus / 4;
+    const int v = a.pairs && !a.spread && (whole ? a.q.seqs : blocks) * slabs(1) > cus ? 2 : 1;
     a.slabs = slabs(v);
     if constexpr (sizeof(typename T::store_t) == 2) {
         using Two = std::integral_constant<int, 2>;
@@ -841,6 +1017,15 @@ hipError_t launch_recurrence_t(const RecurArgs& a, bool whole, hipStream_t st)
     const unsigned carries = (unsigned)(a.q.seqs * ((a.channels + 63) / 64));
     const int64_t slots = slot_count<CANON_RECUR_BLOCK>(a.q.seqs, a.q.rows, a.q.starts != nullptr);
     const unsigned blocks = (unsigned)(slots * a.slabs);
+    if constexpr (V == 1) {
+        if (a.spread) {
+            const dim3 rounds((unsigned)(blocks * kRecurRounds));
+            k_recur_chunks<T, DECAY, false><<<rounds, threads, 0, st>>>(a);
+            if (hipError_t e = hipGetLastError()) return e;
+            k_recurrence<T, 1, DECAY, kRecurSpreadOut><<<rounds, threads, 0, st>>>(a);
+            return hipGetLastError();
+        }
+    }
     if (whole) {
         k_recurrence<T, V, DECAY, kRecurWhole><<<dim3(seqs), threads, 0, st>>>(a);
         return hipGetLastError();
@@ -871,7 +1056,14 @@ hipError_t launch_recurrence_grad_t(const RecurArgs& a, bool whole, hipStream_t 
     const unsigned carries = (unsigned)(a.q.seqs * ((a.channels + 63) / 64));
     const int64_t slots = slot_count<CANON_RECUR_BLOCK>(a.q.seqs, a.q.rows, a.q.starts != nullptr);
     const unsigned blocks = (unsigned)(slots * a.slabs);
-    if (whole) {
+    if (a.spread) {
+        if constexpr (V == 1) {
+            const dim3 rounds((unsigned)(blocks * kRecurRounds));
+            k_recur_chunks<T, DECAY, true><<<rounds, threads, 0, st>>>(a);
+            if (hipError_t e = hipGetLastError()) return e;
+            k_recurrence_grad<T, 1, DECAY, kRecurSpreadOut><<<rounds, threads, 0, st>>>(a);
+        }
+    } else if (whole) {
         k_recurrence_grad<T, V, DECAY, kRecurWhole><<<dim3(seqs), threads, 0, st>>>(a);
     } else if (slots > 0) {
         if (a.ws_h) {
@@ -884,7 +1076,8 @@ hipError_t launch_recurrence_grad_t(const RecurArgs& a, bool whole, hipStream_t 
     }
     if (hipError_t e = hipGetLastError()) return e;
     if (!DECAY) return hipSuccess;
-    ColumnSums sums{{{a.ws_dd, a.channels, 1, 1, a.ddecay}, {}, {}}, slots};
+    ColumnSums sums{{{a.ws_dd, a.channels, 1, 1, a.ddecay}, {}, {}},
+                    a.spread ? slots * kRecurRounds : slots};
     return launch_column_sums(sums, st);
 }
 

@@ -238,6 +238,46 @@ def test_same_bits_with_any_number_of_sequences(canon, dtype):
 
 
 @pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("rows", [257, 384, 500, 512, 1000, 7 * BLOCK + 130])
+def test_same_bits_by_rounds(canon, dtype, rows):
+    """Few sequences, whose rounds have a workgroup each, and many, packed or not; the
+    decays' gradients within the sums' roundings."""
+    few, ch = 2, 68
+    d = inputs(dtype, [rows] * (40 if rows > BLOCK else 70), ch, seed=rows)
+    out, g, final = [], [], []
+    for n in (len(d["x"]), few):
+        p = {k: v if v is None or k in ("decay", "starts") else v[:n] for k, v in d.items()}
+        final.append(torch.empty_like(p["init"]))
+        states = canon.gated_recurrence_states(p["x"])
+        out.append(forward(canon, p, final_state=final[-1], states=states))
+        g.append(backward(canon, p, states))
+    p["starts"] = torch.tensor([0, rows, rows, 2 * rows], dtype=torch.int32, device="cuda")
+    for k in GATES + ("dout",):
+        p[k] = p[k].reshape(-1, ch)
+    for k in ("init", "dfinal"):
+        p[k] = torch.cat([p[k][:1], torch.full_like(p[k][:1], 3.0), p[k][1:]])
+    state, states = p["init"].clone(), canon.gated_recurrence_states(p["x"], p["starts"])
+    h = canon.gated_recurrence(p["x"], p["gate"], p["decay"], p["input_gate"], p["starts"], state,
+                               state, states)
+    b = backward(canon, p, states)
+    assert torch.equal(out[1], out[0][:few]) and torch.equal(final[1], final[0][:few])
+    assert torch.equal(h.reshape(out[1].shape), out[1]) and torch.equal(state[[0, 2]], final[1])
+    assert (state[1] == 3).all() and (b.dinit_state[1] == 3).all()
+    assert torch.equal(b.dinit_state[[0, 2]], g[1].dinit_state)
+    for name in ("dx", "dgate", "dinput_gate", "dinit_state"):
+        one = getattr(g[1], name)
+        assert torch.equal(one, getattr(g[0], name)[:few])
+        if name != "dinit_state":
+            assert torch.equal(getattr(b, name).reshape(one.shape), one)
+    # the sum over a few thousand rows in two orders: gate's gradient is its term times
+    # decay (1 - sigmoid(gate)), so the absolute sum is at most that of |dgate| over it
+    share = (d["decay"] * torch.sigmoid(-d["gate"][:few].double())).clamp(min=1e-9)
+    size = (g[1].dgate.double().abs() / share).sum((0, 1)) + 1e-3
+    bound = 2 * (128 + 64) * layer_ref.U * size * (1 + 2 ** -7)
+    assert ((g[1].ddecay.double() - b.ddecay.double()).abs() <= bound).all()
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
 @pytest.mark.parametrize("packed", [False, True])
 def test_many_blocks(canon, dtype, packed):
     """More blocks than each folds those before it: the same bits, forward and backward,

@@ -175,9 +175,18 @@ def recur(**kw):
 def test_recur_workspace(layer):
     w, g = layer.gated_recurrence_workspace_bytes, layer.gated_recurrence_grad_workspace_bytes
     s = layer._lib().canon_gated_recurrence_states
-    assert w(3, 512, False, 64) == 0 and g(3, 512, False, 64) == 3 * 256
-    assert w(3, 513, False, 64) == 3 * 6 * 256 and g(3, 513, False, 64) == 4 * 6 * 256
-    assert w(3, 1024, True, 64) == 3 * 5 * 256 and w(3, 512, True, 64) == 0
+    # a workgroup for each round (of up to 64 slots of 64 channels, 128 where sequences
+    # have 2 to 15 blocks): two folds of each of 64 chunks a slot, and the start states
+    assert w(3, 256, False, 64) == 0 and g(3, 256, False, 64) == 3 * 256
+    assert w(3, 257, False, 64) == 3 * 129 * 256 and g(3, 257, False, 64) == 3 * 132 * 256
+    assert w(64, 512, False, 64) == 64 * 129 * 256 and w(65, 512, False, 64) == 0
+    assert w(64, 513, False, 64) == 128 * 129 * 256 and w(65, 513, False, 64) == 3 * 130 * 256
+    assert w(3, 1024, True, 64) == 5 * 129 * 256
+    assert w(1, 15 * 512, False, 64) == 15 * 129 * 256
+    assert w(1, 15 * 512 + 1, False, 64) == 3 * 16 * 256
+    # two folds and the start state of each block
+    assert w(200, 513, False, 64) == 3 * 400 * 256 and g(200, 513, False, 64) == 4 * 400 * 256
+    assert w(200, 1024, True, 64) == 3 * 202 * 256 and w(200, 512, True, 64) == 0
     assert s(3, 513, 0, 64) == 6 * 4 * 64 and s(3, 1024, 1, 64) == 5 * 4 * 64
     assert w(0, 1024, True, 64) == 0 and g(0, 1024, True, 64) == 0 and s(0, 99, 1, 64) == 0
     for bad in ((1 << 30, 1, False, 8), (1, 1 << 30, False, 8), (1, 1, False, 1 << 24)):
