@@ -230,9 +230,10 @@ def core_inputs(seed, seqs, rows, width):
     return {k: v.cuda() for k, v in p.items()}
 
 
-@pytest.mark.parametrize("seqs,rows,width", [(3, 130, 128), (2, 1100, 512), (50, 600, 320)])
+@pytest.mark.parametrize("seqs,rows,width", [(3, 130, 128), (2, 1100, 512), (30, 1100, 96),
+                                            (50, 600, 320)])
 def test_graph_capture(canon, seqs, rows, width):
-    """One block, blocks side by side, whole sequences: captured, replayed on changed
+    """One block, rounds side by side, blocks, whole sequences: captured, replayed on changed
     inputs with eager work and synchronisations between the replays."""
     p = core_inputs(3, seqs, rows, width)
     core(canon, p)
@@ -287,15 +288,16 @@ def test_same_bits_every_run(canon):
         assert all(torch.equal(a, b) for a, b in zip(core(canon, q), want))
 
 
-def test_workspaces_of_the_caller(canon):
+@pytest.mark.parametrize("seqs", [2, 30, 100])
+def test_workspaces_of_the_caller(canon, seqs):
     """A workspace of the caller's, larger than needed and full of other values, serves
     every call; one that is too small is left alone."""
-    q = core_inputs(5, 2, 1100, 96)
+    q = core_inputs(5, seqs, 1100, 96)
     want = core(canon, q)
     y, h = want[0], want[1]
-    n = max(canon.gated_recurrence_workspace_bytes(2, 1100, False, 96),
-            canon.gated_recurrence_grad_workspace_bytes(2, 1100, False, 96),
-            canon.layer_norm_grad_workspace_bytes(2, 1100, 96))
+    n = max(canon.gated_recurrence_workspace_bytes(seqs, 1100, False, 96),
+            canon.gated_recurrence_grad_workspace_bytes(seqs, 1100, False, 96),
+            canon.layer_norm_grad_workspace_bytes(seqs, 1100, 96))
     ws = torch.full((n + 64,), 0xff, dtype=torch.uint8, device="cuda")
     keep, st = canon.gated_recurrence_states(y), canon.layer_norm_stats(y)
     assert torch.equal(canon.gated_recurrence(y, q["gate"], q["decay"], q["inp"], None, q["init"],
