@@ -67,6 +67,12 @@ def _new(x: torch.Tensor) -> torch.Tensor:
     return torch.empty_like(x) if x.is_contiguous() else x.new_empty(x.shape)
 
 
+def _new_rows(t: torch.Tensor, shape, lead: int):
+    """canon_rows_t of what _new gave: nothing to check."""
+    width = shape[-1]
+    return t.data_ptr(), shape[1] * width if lead == 2 else 0, width
+
+
 # ------------------------------------------------------------------ layer norm
 class LayerNormGrads(NamedTuple):
     dx: torch.Tensor
@@ -91,7 +97,7 @@ def _norm(what, x, weight, bias):
 def layer_norm_stats(x: torch.Tensor) -> torch.Tensor:
     """An uninitialised buffer for the `stats` of layer_norm of x: each row's mean
     and 1 / standard deviation, for the backward pass."""
-    return torch.empty(x.shape[:-1] + (2,), dtype=torch.float32, device=x.device)
+    return torch.empty((*x.shape[:-1], 2), dtype=torch.float32, device=x.device)
 
 
 def _layer_norm(what, x, residual, weight, bias, eps, stats, total, out):
@@ -100,15 +106,22 @@ def _layer_norm(what, x, residual, weight, bias, eps, stats, total, out):
     shape, dtype = x.shape, x.dtype
     if out is None:
         out = _new(x)
-    c = NORM.pack(*head, eps, *_rows(what, "x", x, shape, dtype, lead),
-                  *(_NONE if residual is None else
-                    _rows(what, "residual", residual, shape, dtype, lead)),
-                  *(_NONE if total is None else _rows(what, "sum_out", total, shape, dtype, lead)),
-                  *_rows(what, "out", out, shape, dtype, lead), *params,
-                  _flat(what, "stats", stats, shape[:-1] + (2,), torch.float32),
-                  *_NONE, *_NONE, *_NONE, 0, 0)
+        o = _new_rows(out, shape, lead)
+    else:
+        o = _rows(what, "out", out, shape, dtype, lead)
+    r = t = _NONE
+    if residual is not None:
+        r = _rows(what, "residual", residual, shape, dtype, lead)
+        if total is None:
+            total = _new(x)
+            t = _new_rows(total, shape, lead)
+        else:
+            t = _rows(what, "sum_out", total, shape, dtype, lead)
+    c = NORM.pack(*head, eps, *_rows(what, "x", x, shape, dtype, lead), *r, *t, *o, *params,
+                  _flat(what, "stats", stats, (*shape[:lead], 2), torch.float32) if stats is not None
+                  else 0, *_NONE, *_NONE, *_NONE, 0, 0)
     _call(what, x.device, _lib().canon_layer_norm, c)
-    return out
+    return out, total
 
 
 def layer_norm(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Tensor] = None,
@@ -118,7 +131,7 @@ def layer_norm(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Tenso
     strides) less its mean, over its standard deviation, times weight, plus bias
     (float32 or x's type).  stats: a buffer of layer_norm_stats that is written for
     layer_norm_grad.  out may be x."""
-    return _layer_norm("layer_norm", x, None, weight, bias, eps, stats, None, out)
+    return _layer_norm("layer_norm", x, None, weight, bias, eps, stats, None, out)[0]
 
 
 def add_layer_norm(x: torch.Tensor, residual: torch.Tensor, weight: torch.Tensor,
@@ -127,10 +140,7 @@ def add_layer_norm(x: torch.Tensor, residual: torch.Tensor, weight: torch.Tensor
                    out: Optional[torch.Tensor] = None) -> tuple[torch.Tensor, torch.Tensor]:
     """(layer_norm(s, ...), s) with s = x + residual, rounded to their type, in one
     pass.  sum_out and out may each be x or residual (not the same one)."""
-    if sum_out is None:
-        sum_out = _new(x)
-    return _layer_norm("add_layer_norm", x, residual, weight, bias, eps, stats, sum_out,
-                       out), sum_out
+    return _layer_norm("add_layer_norm", x, residual, weight, bias, eps, stats, sum_out, out)
 
 
 def layer_norm_grad_workspace_bytes(seqs: int, rows: int, width: int) -> int:
@@ -151,13 +161,16 @@ def layer_norm_grad(dout: torch.Tensor, x: torch.Tensor, weight: torch.Tensor,
     shape, dtype, device = x.shape, x.dtype, x.device
     if dx is None:
         dx = _new(x)
+        d = _new_rows(dx, shape, lead)
+    else:
+        d = _rows(what, "dx", dx, shape, dtype, lead)
     dw = torch.empty(head[4], dtype=torch.float32, device=device)
     db = None if bias is None else torch.empty(head[4], dtype=torch.float32, device=device)
     c = NORM.pack(*head, 0.0, *_rows(what, "x", x, shape, dtype, lead), *_NONE, *_NONE, *_NONE,
-                  *params, _flat(what, "stats", stats, shape[:-1] + (2,), torch.float32),
+                  *params, _flat(what, "stats", stats, (*shape[:lead], 2), torch.float32),
                   *_rows(what, "dout", dout, shape, dtype, lead),
                   *(_NONE if dsum is None else _rows(what, "dsum", dsum, shape, dtype, lead)),
-                  *_rows(what, "dx", dx, shape, dtype, lead), dw.data_ptr(),
+                  *d, dw.data_ptr(),
                   0 if db is None else db.data_ptr())
     L = _lib()
     w = _workspace(L.canon_layer_norm_grad_workspace_bytes(*head[2:5]), device, ws)
@@ -220,12 +233,14 @@ def gated_recurrence(x: torch.Tensor, gate: torch.Tensor, decay: Optional[torch.
     d = _dtype(x, what)
     if out is None:
         out = _new(x)
+        o = _new_rows(out, shape, lead)
+    else:
+        o = _rows(what, "out", out, shape, dtype, lead)
     state = (seqs, channels)
     c = RECUR.pack(d, seqs, rows, channels, sp, *_rows(what, "x", x, shape, dtype, lead),
                    *_rows(what, "gate", gate, shape, dtype, lead),
                    *(_NONE if input_gate is None else
-                     _rows(what, "input_gate", input_gate, shape, dtype, lead)),
-                   *_rows(what, "out", out, shape, dtype, lead),
+                     _rows(what, "input_gate", input_gate, shape, dtype, lead)), *o,
                    _flat(what, "decay", decay, (channels,), f32),
                    _flat(what, "init_state", init_state, state, f32),
                    _flat(what, "final_state", final_state, state, f32), kept,
@@ -266,14 +281,13 @@ def gated_recurrence_grad(dout: torch.Tensor, x: torch.Tensor, gate: torch.Tenso
     gi = _NONE, _NONE
     if input_gate is not None:
         gi = (_rows(what, "input_gate", input_gate, shape, dtype, lead),
-              _rows(what, "dinput_gate", g.dinput_gate, shape, dtype, lead))
+              _new_rows(g.dinput_gate, shape, lead))
     c = RECUR.pack(d, seqs, rows, channels, sp, *_rows(what, "x", x, shape, dtype, lead),
                    *_rows(what, "gate", gate, shape, dtype, lead), *gi[0], *_NONE,
                    _flat(what, "decay", decay, (channels,), f32), 0, 0,
                    _flat(what, "states", states, (size,), f32),
                    *_rows(what, "dout", dout, shape, dtype, lead),
-                   *_rows(what, "dx", g.dx, shape, dtype, lead),
-                   *_rows(what, "dgate", g.dgate, shape, dtype, lead), *gi[1],
+                   *_new_rows(g.dx, shape, lead), *_new_rows(g.dgate, shape, lead), *gi[1],
                    0 if decay is None else g.ddecay.data_ptr(),
                    _flat(what, "d_final_state", d_final_state, (seqs, channels), f32),
                    g.dinit_state.data_ptr())
@@ -300,12 +314,14 @@ def gated_recurrence_step(state: torch.Tensor, x: torch.Tensor, gate: torch.Tens
     old = _flat(what, "state", state, shape, f32)
     if out is None:
         out = _new(x)
+        o = out.data_ptr(), shape[1], 0
+    else:
+        o = _step_rows(what, "out", out, shape, dtype)
     c = RECUR.pack(d, shape[0], 1, shape[1], 0, *_step_rows(what, "x", x, shape, dtype),
                    *_step_rows(what, "gate", gate, shape, dtype),
                    *(_NONE if input_gate is None else
                      _step_rows(what, "input_gate", input_gate, shape, dtype)),
-                   *_step_rows(what, "out", out, shape, dtype),
-                   _flat(what, "decay", decay, shape[1:], f32), old,
+                   *o, _flat(what, "decay", decay, shape[1:], f32), old,
                    old if out_state is None else _flat(what, "out_state", out_state, shape, f32),
                    0, *_NONE, *_NONE, *_NONE, *_NONE, 0, 0, 0)
     _call(what, x.device, _lib().canon_gated_recurrence_step, c)
