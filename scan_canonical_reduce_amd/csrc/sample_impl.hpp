@@ -23,7 +23,7 @@
 //
 // What bounds it: of a row of 131072 in bfloat16, of which 256 fill the chip, the
 // largest takes 12 us (memory), the weights 31 (27 instructions in 64 bits a token, 23 us
-// of issue), the steps of top_p 23 (LDS atomics and the passes' start), their list and
+// of issue), the steps of top_p 21 (LDS atomics and the pass's start), their list and
 // the digits 10.  Adding up the weights themselves by steps with 64-bit atomics, so that
 // they need not be computed again, took 50 instead of 23, and paid only where top_p keeps
 // few tokens (0.5: 88 us for 92; 0.9: 119 for 100).  A small row costs its latency: 10 us
@@ -268,7 +268,7 @@ __global__ __launch_bounds__(kSampleThreads) void k_sample(SampleArgs a)
     using E = typename T::store_t;
     constexpr int V = R::V, kDigits = sizeof(E);
     __shared__ union {
-        uint32_t bins[kBins];
+        uint32_t bins[kBins + 64];  // and one a lane for what has no step
         u64 sums[kSums];
     } sh;
     __shared__ uint32_t lkey[kList], lidx[kList];
@@ -566,9 +566,9 @@ __global__ __launch_bounds__(kSampleThreads) void k_sample(SampleArgs a)
                 const float slope = -step * kLn2 * whole_step;
                 whole([&](float x, uint32_t) {
                     const float d = (top - x) * per;
-                    if (d < (float)kBins)
-                        atomicAdd(&sh.bins[(uint32_t)d],
-                                  (uint32_t)fma32(__builtin_amdgcn_fractf(d), slope, whole_step));
+                    const uint32_t b = d < (float)kBins ? (uint32_t)d : kBins + lane;
+                    atomicAdd(&sh.bins[b],
+                              (uint32_t)fma32(__builtin_amdgcn_fractf(d), slope, whole_step));
                 });
                 __syncthreads();
                 double c[4], sum[1] = {0.}, all[1];
