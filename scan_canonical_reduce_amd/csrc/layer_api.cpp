@@ -31,9 +31,9 @@ bool norm_sizes_ok(int64_t seqs, int64_t rows, int64_t width)
            mul_fits(seqs, rows, kMaxRows - 1);
 }
 
-int64_t norm_chunks(int64_t total)
+int64_t norm_chunks(int64_t total, int64_t width)
 {
-    const int64_t chunk = norm_chunk(total);
+    const int64_t chunk = norm_chunk(total, width);
     return (total + chunk - 1) / chunk;
 }
 
@@ -41,7 +41,7 @@ struct NormLayout : Layout {
     size_t w, b;
     NormLayout(int64_t total, int64_t width)
     {
-        const size_t part = 4 * (size_t)norm_chunks(total) * (size_t)width;
+        const size_t part = 4 * (size_t)norm_chunks(total, width) * (size_t)width;
         w = take(part);
         b = take(part);
     }
@@ -97,7 +97,7 @@ canon_status_t norm_args(const canon_norm_t* c, bool grad, NormArgs* a)
     a->dx = c->dx;
     a->dweight = c->dweight;
     a->dbias = c->dbias;
-    if (!mul_fits(norm_chunks(a->total), (c->width + 1023) / 1024, kMaxGrid256 - 1))
+    if (!mul_fits(norm_chunks(a->total, a->width), (c->width + 1023) / 1024, kMaxGrid256 - 1))
         return CANON_EUNSUPPORTED;
     return CANON_OK;
 }

@@ -22,13 +22,16 @@ struct NormArgs {
     float *ws_w, *ws_b;  // per chunk of rows: width
 };
 
-// Rows of a chunk of the sums over rows: as many chunks as fill the chip twice,
-// then longer ones, whose partial sums are at most a 24th of the rows' bytes.
+// Rows of a chunk of the sums over rows: as many chunks as fill the chip twice (of rows
+// wider than kNormGradWide, which are cut into 5 parts or more, a quarter), then longer
+// ones, whose partial sums are at most a 24th of the rows' bytes.
 constexpr int64_t kNormChunks = 512;
 constexpr int64_t kNormChunkMost = 64;
-inline int64_t norm_chunk(int64_t total)
+constexpr int32_t kNormGradWide = 8192;
+inline int64_t norm_chunk(int64_t total, int64_t width)
 {
-    const int64_t n = (total + kNormChunks - 1) / kNormChunks;
+    const int64_t most = width > kNormGradWide ? kNormChunks / 4 : kNormChunks;
+    const int64_t n = (total + most - 1) / most;
     return n < 1 ? 1 : n > kNormChunkMost ? kNormChunkMost : n;
 }
 

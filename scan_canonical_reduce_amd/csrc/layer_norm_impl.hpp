@@ -560,6 +560,7 @@ __global__ __launch_bounds__(256) void k_norm_dw(NormArgs a, int32_t chunk, int3
     if (c >= a.width) return;
     float dw[V] = {}, db[V] = {};
     const int32_t end = a.total - k * chunk < chunk ? a.total : (k + 1) * chunk;
+#pragma unroll 4
     for (int32_t row = k * chunk; row < end; ++row) {
         float v[V], g[V];
         ld_cols<T, V>(norm_row<T>(a.x, a, row), c, a.width, v);
@@ -594,7 +595,7 @@ hipError_t with_grad_team(int32_t width, F&& f)
     if (width <= 1024) return f(std::integral_constant<int, 64>{});
     if (width <= 2048) return f(std::integral_constant<int, 256>{});
     if (width <= 4096) return f(std::integral_constant<int, 512>{});
-    if (width <= 8192) return f(std::integral_constant<int, 1024>{});
+    if (width <= kNormGradWide) return f(std::integral_constant<int, 1024>{});
     return f(std::integral_constant<int, 0>{});
 }
 
@@ -626,7 +627,7 @@ hipError_t launch_layer_norm(const NormArgs& a, hipStream_t st)
 template <typename T, typename P>
 hipError_t launch_layer_norm_grad(const NormArgs& a, hipStream_t st)
 {
-    const int64_t chunk = norm_chunk(a.total), chunks = (a.total + chunk - 1) / chunk;
+    const int64_t chunk = norm_chunk(a.total, a.width), chunks = (a.total + chunk - 1) / chunk;
     if (a.total > 0) {
         const hipError_t e = with_grad_team(a.width, [&](auto t) {
             constexpr int TEAM = decltype(t)::value, NV = (TEAM < 256 ? 16 : 8) / kNormV<T>;
