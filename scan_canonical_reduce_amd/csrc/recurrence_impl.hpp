@@ -380,7 +380,9 @@ __device__ __forceinline__ void fold_chunks(const RecurArgs& a, const Lane& l, i
 }
 
 // The folds of the chunks of each round, for k_recurrence and k_recurrence_grad with a
-// workgroup for each round; those that serve no other are left out.
+// workgroup for each round; those that serve no other are left out.  999 x 520 float32: 4.7
+// us forward and 4.4 backward, before 6.5 and 9.8 of outputs; a workgroup for each block
+// took 11 + 13 and 4 + 21.
 template <typename T, bool DECAY, bool BACK>
 __global__ __launch_bounds__(64 * kRecurWaves) void k_recur_chunks(RecurArgs a)
 {
@@ -611,7 +613,8 @@ __global__ __launch_bounds__(64 * kRecurWaves) void k_recurrence(RecurArgs a)
 
 // The start states of each sequence's blocks from the first one's (in ws_h) and the
 // blocks' Q and S (in ws_q, ws_s), into ws_h; backwards: the gradients that come in past
-// their ends.
+// their ends.  Latency: a chain of loads, eight blocks at a time (6 us for 32 blocks of
+// 2048 channels).
 template <bool BACK>
 __global__ __launch_bounds__(64) void k_recur_carry(RecurArgs a)
 {
@@ -644,6 +647,8 @@ __global__ __launch_bounds__(64) void k_recur_carry(RecurArgs a)
     }
 }
 
+// One row of each sequence, a thread a channel: 256 x 4096 bf16 6.0 us, 2.8 TB/s, of which a
+// launch is half.
 template <typename T, bool DECAY>
 __global__ __launch_bounds__(256) void k_recurrence_step(RecurArgs a)
 {
