@@ -279,7 +279,8 @@ __global__ __launch_bounds__(kSampleThreads) void k_sample(SampleArgs a)
     } entry[kRank];
     __shared__ Border s_border;
     __shared__ uint32_t wave32[1][kSampleWaves];
-    __shared__ float wave_max[kSampleWaves];
+    // not one array: a wave may be at the minimum while others still read the maxima
+    __shared__ float wave_max[kSampleWaves], wave_min[kSampleWaves];
     __shared__ Picked picked;
     __shared__ uint32_t s_n, s_first, s_b1, s_b2, s_c2;
     const int64_t row = blockIdx.x;
@@ -486,10 +487,10 @@ __global__ __launch_bounds__(kSampleThreads) void k_sample(SampleArgs a)
             });
 #pragma unroll
             for (int d = 1; d < 64; d *= 2) least_x = __builtin_fminf(least_x, __shfl_xor(least_x, d));
-            if (lane == 0) wave_max[wave] = least_x;
+            if (lane == 0) wave_min[wave] = least_x;
             __syncthreads();
 #pragma unroll
-            for (int w = 0; w < kSampleWaves; ++w) least_x = __builtin_fminf(least_x, wave_max[w]);
+            for (int w = 0; w < kSampleWaves; ++w) least_x = __builtin_fminf(least_x, wave_min[w]);
             const double range = weigh.max - least_x;
             if (range < span) {
                 span = range;
