@@ -497,7 +497,8 @@ __global__ __launch_bounds__(kSampleThreads) void k_sample(SampleArgs a)
                 per = (float)((kBins - 1) / span);
             }
         }
-        const bool stepped = top < kInf && span > 0. && per < kInf;
+        // differences of logits within the span are 32-bit numbers, not infinite
+        const bool stepped = top < kInf && span > 0. && span <= (double)kMaxF && per < kInf;
         // descending with x; kBins for a masked one or one of no weight
         auto bin = [&](float x) {
             return (uint32_t)__builtin_fminf((top - x) * per, (float)kBins);

@@ -66,3 +66,25 @@ def test_high_temperatures(canon, dtype, vocab):
         order = torch.randperm(kinds * copies, generator=g) % kinds
         many = canon.sample(x[order].cuda(), u[order].cuda(), **s).cpu()
         assert torch.equal(many, one[order]), s
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("vocab", [5, 300, 9000])
+def test_logits_further_apart_than_the_largest_number(canon, dtype, vocab):
+    """Temperatures at which a logit of -3e38 weighs something beside one of 3e38: the
+    difference is beyond 32 bits, and filters count the low ones as any others."""
+    u = torch.arange(40) / 40 + 1 / 80
+    x = torch.full((40, vocab), -3e38)
+    x[:, 2] = 3e38
+    x = x.to(dtype)
+    for t in (INF, 2e38):
+        got = check(canon, x, u, temperature=t, top_k=2)
+        assert set(got.tolist()) == {0, 2}
+        check(canon, x, u, temperature=t, top_k=4)
+        check(canon, x, u, temperature=t, top_k=4, top_p=0.7)
+        check(canon, x, u, temperature=t, top_p=0.4137)
+        check(canon, x, u, temperature=t)
+    many = logits(dtype, 40, vocab, seed=vocab, scale=1e38)[0].clamp(-3.3e38, 3.3e38)
+    for s in (dict(top_k=3), dict(top_k=3, top_p=0.8), dict(top_p=0.6137)):
+        check(canon, many, u, least=0.5, temperature=1e38, **s)
+        check(canon, many, u, least=0.5, temperature=1e30, **s)
