@@ -8,6 +8,7 @@ types, streams and workspaces are those of the sequence operators (``seq.py``).
 from __future__ import annotations
 
 import ctypes
+import operator
 import struct
 from typing import NamedTuple, Optional
 
@@ -332,6 +333,11 @@ def gated_recurrence_step(state: torch.Tensor, x: torch.Tensor, gate: torch.Tens
 def _setting(what: str, name: str, v, rows: int, dtype: torch.dtype):
     """(pointer, value) of a number for all rows, or one per row"""
     if not torch.is_tensor(v):
+        if dtype == torch.int32:
+            try:
+                v = operator.index(v)
+            except TypeError:
+                raise TypeError(f"{what}: {name} must be an integer, not {v!r}") from None
         return 0, v
     return _flat(what, name, v, (rows,), dtype), 0
 
@@ -368,6 +374,7 @@ def sample(logits: torch.Tensor, u: torch.Tensor, temperature=1.0, top_k=0, top_
     if tv < 0 or kv < 0 or not 0 <= pv <= 1 or not 0 <= mv <= 1 or tv != tv:
         raise ValueError(f"{what}: temperature and top_k must not be negative, top_p and min_p "
                          "lie in [0, 1]")
+    kv = min(kv, vocab)  # no more than there are
     if out is None:
         out = torch.empty(rows, dtype=torch.int64, device=logits.device)
     elif out.dtype not in (torch.int64, i32):

@@ -88,3 +88,17 @@ def test_logits_further_apart_than_the_largest_number(canon, dtype, vocab):
     for s in (dict(top_k=3), dict(top_k=3, top_p=0.8), dict(top_p=0.6137)):
         check(canon, many, u, least=0.5, temperature=1e38, **s)
         check(canon, many, u, least=0.5, temperature=1e30, **s)
+
+
+def test_top_k_of_other_kinds(canon):
+    """Integers of any kind and size; nothing else."""
+    import numpy as np
+    x, u = (t.cuda() for t in logits(F32, 3, 20))
+    want = canon.sample(x, u, top_k=4)
+    assert torch.equal(canon.sample(x, u, top_k=np.int64(4)), want)
+    everything = canon.sample(x, u)
+    for k in (20, 21, 1 << 31, (1 << 32) + 1, 1 << 70):
+        assert torch.equal(canon.sample(x, u, top_k=k), everything)
+    for k in (4.0, "4", None):
+        with pytest.raises(TypeError):
+            canon.sample(x, u, top_k=k)
