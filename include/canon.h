@@ -298,8 +298,9 @@ canon_status_t canon_scan_noalloc_f64(const double* x, double* y, size_t n, int 
  *                                kernel: single-pass scans, the pipelined
  *                                iterated_pairwise pass, the three-kernel
  *                                iterated_pairwise path, row reduces and row
- *                                scans (kernels with one workgroup per tile
- *                                keep their grid)
+ *                                scans, embedding gradients, layer norms
+ *                                (kernels with one workgroup per tile keep
+ *                                their grid)
  *   CANON_SCHED_REDUCE_PARTIALS  workgroups (row ranges, hence partials) the
  *                                streaming reduce aims for; the reduce
  *                                workspace size follows it

@@ -608,7 +608,8 @@ hipError_t launch_norm_rows(const NormArgs& a, int threads, int32_t teams, hipSt
 {
     const int64_t most = (int64_t)resident_grid<KERN>(threads);
     const int64_t need = (a.total + teams - 1) / teams;
-    KERN<<<dim3((unsigned)(need < most ? need : most)), dim3(threads), 0, st>>>(a);
+    const dim3 grid((unsigned)capped_grid(need < most ? need : most));
+    KERN<<<grid, dim3(threads), 0, st>>>(a);
     return hipGetLastError();
 }
 
