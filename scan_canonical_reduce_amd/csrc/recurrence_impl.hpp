@@ -14,10 +14,11 @@
 // 255 where these then took 122 and 243; rows of the next round in flight in the backward
 // pass too cost spilled registers at 16 waves (338), and gained nothing at 8 (260).
 //
-// a is near 1 for a long memory, and a rounding of h at every row would add up over
-// that memory.  So everything is kept as differences from 1: with e = a - 1,
-//   h <- h + (e h + v),   and for the product of a, Q = P - 1:  Q <- Q + (e Q + e),
-// and the start states of rounds are carried in 64 bits inside a block and rounded to 32
+// a is near 1 for a long memory, so it is kept as its difference from 1: with e = a - 1,
+//   h <- (h + e h) + v,   and for the product of a, Q = P - 1:  Q <- Q + (e Q + e),
+// h + e h with one rounding.  An a of 0 (e and Q of -1, which the folds keep exactly) so
+// leaves nothing of any finite h, as h + (e h + v), whose rounding is that of e h, would.
+// The start states of rounds are carried in 64 bits inside a block and rounded to 32
 // between blocks.  Inside a round chunks fold on in 32 bits (64 took 4 instructions more a
 // value backward).
 #pragma once
@@ -291,14 +292,14 @@ __device__ __forceinline__ void chunk_values(const RecurArgs& a, ChunkIn<T, V>& 
 // A value at the start of the next block, given the block's Q and S.
 __device__ __forceinline__ float carry(float h, float q, float s)
 {
-    return (float)((double)h + fma64(q, h, s));
+    return (float)(fma64(q, h, h) + s);
 }
 
 // A value further on in a block that starts with h, given the Q and S between; past
 // the block's end it is rounded to 32 bits.
 __device__ __forceinline__ double carried(float h, double q, double s, bool end)
 {
-    return end ? (double)carry(h, (float)q, (float)s) : (double)h + fma64(q, h, s);
+    return end ? (double)carry(h, (float)q, (float)s) : fma64(q, h, h) + s;
 }
 
 // The state that a block starts with, given those of the first one in ws_h: where
@@ -373,7 +374,7 @@ __device__ __forceinline__ void fold_chunks(const RecurArgs& a, const Lane& l, i
         }
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            S += fma64(q[u], S, s[u]);
+            S = fma64(q[u], S, S) + s[u];
             Q += fma64(q[u], Q, q[u]);
         }
     }
@@ -409,7 +410,7 @@ __global__ __launch_bounds__(64 * kRecurWaves) void k_recur_chunks(RecurArgs a)
         chunk_values<T, 1, DECAY>(a, in, n, decay, e, v, [](int) {});
 #pragma unroll
         for (int i = 0; i < kCh; ++i) {
-            s += fma32(e[i][0], s, v[i][0]);
+            s = fma32(e[i][0], s, s) + v[i][0];
             q += fma32(e[i][0], q, e[i][0]);
         }
     }
@@ -524,7 +525,7 @@ __global__ __launch_bounds__(64 * kRecurWaves) void k_recurrence(RecurArgs a)
                     float q = 0.f, s = 0.f;
 #pragma unroll
                     for (int r = 0; r < kCh; ++r) {
-                        s += fma32(e[r][j], s, v[r][j]);
+                        s = fma32(e[r][j], s, s) + v[r][j];
                         q += fma32(e[r][j], q, e[r][j]);
                     }
                     lq[buf][l.wave][at_lds + j] = q;
@@ -549,7 +550,7 @@ __global__ __launch_bounds__(64 * kRecurWaves) void k_recurrence(RecurArgs a)
                 for (int c = 0; c < l.wave; ++c)
 #pragma unroll
                     for (int j = 0; j < V; ++j)
-                        y[j] += fma32(lq[buf][c][at_lds + j], y[j], ls[buf][c][at_lds + j]);
+                        y[j] = fma32(lq[buf][c][at_lds + j], y[j], y[j]) + ls[buf][c][at_lds + j];
             }
             const bool ends = from + kRecurRound >= k.span.len;
             if (l.wave == 0 && a.kept && l.on && MODE == kRecurSpreadOut)
@@ -565,7 +566,7 @@ __global__ __launch_bounds__(64 * kRecurWaves) void k_recurrence(RecurArgs a)
 #pragma unroll
                     for (int j = 0; j < V; ++j) {
                         const double q = lq[buf][c][at_lds + j], s = ls[buf][c][at_lds + j];
-                        S[j] += fma64(q, S[j], s);
+                        S[j] = fma64(q, S[j], S[j]) + s;
                         Q[j] += fma64(q, Q[j], q);
                     }
                 const bool done = from + kRecurRound >= k.row + k.len;  // the block's end
@@ -582,7 +583,7 @@ __global__ __launch_bounds__(64 * kRecurWaves) void k_recurrence(RecurArgs a)
 #pragma unroll
                 for (int r = 0; r < kCh; ++r) {
 #pragma unroll
-                    for (int j = 0; j < V; ++j) y[j] += fma32(e[r][j], y[j], v[r][j]);
+                    for (int j = 0; j < V; ++j) y[j] = fma32(e[r][j], y[j], y[j]) + v[r][j];
                     out.store(r, y);
                 }
             }
@@ -662,7 +663,7 @@ __global__ __launch_bounds__(256) void k_recurrence_step(RecurArgs a)
     float v = factor<DECAY>(e) * ld<T>(row(a.x));
     if (a.input.p) v *= sigmoid_f<T>(ld<T>(row(a.input)));
     float h = a.init ? a.init[i] : 0.f;
-    h += fma32(e, h, v);
+    h = fma32(e, h, h) + v;
     st<T>(row(a.out), h);
     if (a.final) a.final[i] = h;
 }
@@ -717,7 +718,7 @@ __global__ __launch_bounds__(64 * kRecurWaves) void k_recur_back_sum(RecurArgs a
 #pragma unroll
                 for (int j = 0; j < V; ++j) {
                     const double cq = lq[buf][c][at_lds + j], ct = lt[buf][c][at_lds + j];
-                    G[j] += fma64(cq, G[j], ct);
+                    G[j] = fma64(cq, G[j], G[j]) + ct;
                     Q[j] += fma64(cq, Q[j], cq);
                 }
     }
@@ -842,7 +843,7 @@ __global__ __launch_bounds__(64 * kRecurWaves) void k_recurrence_grad(RecurArgs 
 #pragma unroll
                 for (int r = 0; r < kCh; ++r)
 #pragma unroll
-                    for (int j = 0; j < V; ++j) s[j] += fma32(e[r][j], s[j], v[r][j]);
+                    for (int j = 0; j < V; ++j) s[j] = fma32(e[r][j], s[j], s[j]) + v[r][j];
 #pragma unroll
                 for (int r = kCh - 1; r >= 0; --r)
 #pragma unroll
@@ -873,7 +874,7 @@ __global__ __launch_bounds__(64 * kRecurWaves) void k_recurrence_grad(RecurArgs 
 #pragma unroll
                     for (int j = 0; j < V; ++j) {
                         const double cq = lq[buf][c][at_lds + j], ct = lt[buf][c][at_lds + j];
-                        S[j] += fma64(cq, S[j], ct);
+                        S[j] = fma64(cq, S[j], S[j]) + ct;
                         Q[j] += fma64(cq, Q[j], cq);
                     }
 #pragma unroll
@@ -888,7 +889,7 @@ __global__ __launch_bounds__(64 * kRecurWaves) void k_recurrence_grad(RecurArgs 
             for (int c = kRecurWaves - 1; c > l.wave; --c)
 #pragma unroll
                 for (int j = 0; j < V; ++j)
-                    R[j] += fma32(lq[buf][c][at_lds + j], R[j], lt[buf][c][at_lds + j]);
+                    R[j] = fma32(lq[buf][c][at_lds + j], R[j], R[j]) + lt[buf][c][at_lds + j];
             float y[V];
 #pragma unroll
             for (int j = 0; j < V; ++j) y[j] = kept[j];
@@ -896,12 +897,12 @@ __global__ __launch_bounds__(64 * kRecurWaves) void k_recurrence_grad(RecurArgs 
             for (int c = 0; c < l.wave; ++c)
 #pragma unroll
                 for (int j = 0; j < V; ++j)
-                    y[j] += fma32(lq[buf][c][at_lds + j], y[j], ls[buf][c][at_lds + j]);
+                    y[j] = fma32(lq[buf][c][at_lds + j], y[j], y[j]) + ls[buf][c][at_lds + j];
 #pragma unroll
             for (int r = 0; r < kCh; ++r) {
                 st_channels<V>(&before[l.wave][r][at_lds], y);
 #pragma unroll
-                for (int j = 0; j < V; ++j) y[j] += fma32(e[r][j], y[j], v[r][j]);
+                for (int j = 0; j < V; ++j) y[j] = fma32(e[r][j], y[j], y[j]) + v[r][j];
             }
             in.g.afresh();
             if (a.input.p) in.in.afresh();
