@@ -18,9 +18,10 @@
 //   h <- (h + e h) + v,   and for the product of a, Q = P - 1:  Q <- Q + (e Q + e),
 // h + e h with one rounding.  An a of 0 (e and Q of -1, which the folds keep exactly) so
 // leaves nothing of any finite h, as h + (e h + v), whose rounding is that of e h, would.
-// The start states of rounds are carried in 64 bits inside a block and rounded to 32
-// between blocks.  Inside a round chunks fold on in 32 bits (64 took 4 instructions more a
-// value backward).
+// The start states of rounds and chunks are folded in 64 bits inside a block and rounded to
+// 32 between blocks: an h that loses less than its last bit in a chunk would stay as it is
+// otherwise.  (Chunks of a round folded on in 32 bits take 2 us less of the backward pass's
+// 228.)
 #pragma once
 
 #include <type_traits>
@@ -541,16 +542,19 @@ __global__ __launch_bounds__(64 * kRecurWaves) void k_recurrence(RecurArgs a)
             }
             float y[V];
             if (MODE != kRecurSum) {
+                double h[V];
 #pragma unroll
                 for (int j = 0; j < V; ++j)
-                    y[j] = MODE == kRecurSpreadOut
-                               ? (float)(rd ? carried(h0[j], Q[j], S[j], false) : (double)h0[j])
-                               : (float)lh[buf][at_lds + j];
+                    h[j] = MODE != kRecurSpreadOut ? lh[buf][at_lds + j]
+                           : rd                    ? carried(h0[j], Q[j], S[j], false)
+                                                   : (double)h0[j];
 #pragma unroll 2
                 for (int c = 0; c < l.wave; ++c)
 #pragma unroll
                     for (int j = 0; j < V; ++j)
-                        y[j] = fma32(lq[buf][c][at_lds + j], y[j], y[j]) + ls[buf][c][at_lds + j];
+                        h[j] = fma64(lq[buf][c][at_lds + j], h[j], h[j]) + ls[buf][c][at_lds + j];
+#pragma unroll
+                for (int j = 0; j < V; ++j) y[j] = (float)h[j];
             }
             const bool ends = from + kRecurRound >= k.span.len;
             if (l.wave == 0 && a.kept && l.on && MODE == kRecurSpreadOut)
@@ -857,16 +861,16 @@ __global__ __launch_bounds__(64 * kRecurWaves) void k_recurrence_grad(RecurArgs 
             st_channels<V>(&ls[buf][l.wave][at_lds], s);
             st_channels<V>(&lt[buf][l.wave][at_lds], t);
             __syncthreads();
-            float R[V];  // what reaches h[t] from the rows behind
+            double G[V];  // what reaches h[t] from the rows behind
             if (MODE == kRecurSpreadOut) {
                 for (int32_t b = 0; b < behind; ++b)
                     g0[0] = carry(g0[0], (float)lc[b][0][at_lds], (float)lc[b][1][at_lds]);
                 Q[0] = lc[behind][0][at_lds];
                 S[0] = lc[behind][1][at_lds];
-                R[0] = (float)(rd < rounds - 1 ? carried(g0[0], Q[0], S[0], false) : (double)g0[0]);
+                G[0] = rd < rounds - 1 ? carried(g0[0], Q[0], S[0], false) : (double)g0[0];
             } else {
 #pragma unroll
-                for (int j = 0; j < V; ++j) R[j] = (float)lg[buf][at_lds + j];
+                for (int j = 0; j < V; ++j) G[j] = lg[buf][at_lds + j];
             }
             if (carrier && (MODE != kRecurSpreadOut || from == 0)) {
 #pragma unroll 2
@@ -889,15 +893,20 @@ __global__ __launch_bounds__(64 * kRecurWaves) void k_recurrence_grad(RecurArgs 
             for (int c = kRecurWaves - 1; c > l.wave; --c)
 #pragma unroll
                 for (int j = 0; j < V; ++j)
-                    R[j] = fma32(lq[buf][c][at_lds + j], R[j], R[j]) + lt[buf][c][at_lds + j];
-            float y[V];
+                    G[j] = fma64(lq[buf][c][at_lds + j], G[j], G[j]) + lt[buf][c][at_lds + j];
+            float R[V], y[V];
+            {
+                double h[V];
 #pragma unroll
-            for (int j = 0; j < V; ++j) y[j] = kept[j];
+                for (int j = 0; j < V; ++j) h[j] = kept[j];
 #pragma unroll 2
-            for (int c = 0; c < l.wave; ++c)
+                for (int c = 0; c < l.wave; ++c)
 #pragma unroll
-                for (int j = 0; j < V; ++j)
-                    y[j] = fma32(lq[buf][c][at_lds + j], y[j], y[j]) + ls[buf][c][at_lds + j];
+                    for (int j = 0; j < V; ++j)
+                        h[j] = fma64(lq[buf][c][at_lds + j], h[j], h[j]) + ls[buf][c][at_lds + j];
+#pragma unroll
+                for (int j = 0; j < V; ++j) R[j] = (float)G[j], y[j] = (float)h[j];
+            }
 #pragma unroll
             for (int r = 0; r < kCh; ++r) {
                 st_channels<V>(&before[l.wave][r][at_lds], y);

@@ -91,3 +91,25 @@ def test_packed(canon):
     for a, b in zip(ends, ends[1:]):
         r = layer_ref.recur(x[None, a:b], gate[None, a:b].clamp(min=-80))
         layer_ref.within(one[None, a:b], *r["out"], f"rows {a} to {b}")
+
+
+@pytest.mark.parametrize("n,rows,channels", [(1, 512, 66), (2, 1500, 66), (70, 512, 70),
+                                             (260, 1100, 20)])
+def test_a_slow_loss_is_not_rounded_away(canon, n, rows, channels):
+    """An a of 1 - 2^-28 over many rows of no input: a chunk of 8 rows takes less than half
+    of the state's last bit, which chunk by chunk in 32 bits would all be lost, 7 of these
+    roundings U within a round.  An output is off by the rounding of its chunk's start, U / 2,
+    and by up to 8 rows' loss, 0.48 U.  Gradients of x are the state's, times a constant: two
+    roundings more of each of the two that are compared."""
+    x = torch.zeros(n, rows, channels, device="cuda")
+    gate = torch.full_like(x, 19.45)
+    ones = torch.ones(n, channels, device="cuda")
+    states = canon.gated_recurrence_states(x)
+    out = canon.gated_recurrence(x, gate, init_state=ones, states=states)
+    e = torch.sigmoid(-gate[0, 0, 0].double())
+    t = torch.arange(1, rows + 1, device="cuda", dtype=torch.float64)
+    want = torch.exp(t * torch.log1p(-e))[:, None]
+    assert ((out - want).abs() <= 1.25 * layer_ref.U).all()
+    g = canon.gated_recurrence_grad(x, x, gate, states, d_final_state=ones)
+    ratio = g.dx.double() / g.dx[:, -1:].double()
+    assert ((ratio - want.flip(0) / want[0]).abs() <= 4 * layer_ref.U).all()
