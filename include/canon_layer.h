@@ -137,7 +137,8 @@ canon_status_t canon_gated_recurrence_grad(const canon_recur_t* c, void* ws, siz
                                            void* stream);
 
 /* One row of each of `seqs` sequences (rows is ignored; canon_rows_t.seq apart): h from
- * init_state (NULL: zero), written to final_state, which may be the same buffer. */
+ * init_state (NULL: zero), written to final_state, which may be the same buffer.  out may
+ * be the buffer of x, gate or input_gate with the same strides. */
 canon_status_t canon_gated_recurrence_step(const canon_recur_t* c, void* stream);
 
 /* --------------------------------------------------------------- sampling */

@@ -177,9 +177,12 @@ canon_status_t recur_args(const canon_recur_t* c, bool step, bool grad, RecurArg
         if (grad && (!rows_valid(c->dout) || c->kept_states == nullptr)) return CANON_EINVAL;
         for (int o = 0; o < outs; ++o) {
             if (!out_ok(*out[o])) return CANON_EINVAL;
-            // rows are read again by other workgroups, or by a second pass
-            for (int i = 0; i < ins && !step; ++i)
-                if (out[o]->p == in[i]->p) return CANON_EINVAL;
+            // rows are read again by other workgroups, or by a second pass; single ones by
+            // the thread that writes there
+            for (int i = 0; i < ins; ++i)
+                if (out[o]->p == in[i]->p &&
+                    !(step && (c->seqs == 1 || out[o]->seq == in[i]->seq)))
+                    return CANON_EINVAL;
             for (int p = 0; p < o; ++p)
                 if (out[o]->p == out[p]->p) return CANON_EINVAL;
         }

@@ -3,6 +3,8 @@ import pytest
 
 torch = pytest.importorskip("torch")
 
+from test_layer_abi import FAKE, Rows, norm, recur  # noqa: E402
+
 
 @pytest.fixture(scope="module")
 def layer():
@@ -18,3 +20,15 @@ def test_top_k_is_an_integer(layer):
     for v in (50, np.int64(50), np.int32(50)):
         assert layer._setting("sample", "top_k", v, 3, torch.int32) == (0, 50)
     assert layer._setting("sample", "top_p", 0.5, 3, torch.float32) == (0, 0.5)
+
+
+def test_a_step_in_place_has_the_same_rows(layer):
+    """In an input's place a shifted or strided row would be read after it was written.  With
+    sizes beyond a launch, so that what is not refused for that is refused for them."""
+    L, big = layer._lib(), 1 << 22
+    x = Rows(9 * FAKE, 64, 0)
+    for name in ("x", "gate", "input_gate"):
+        for seqs, seq, want in ((big, 64, 2), (big, 65, 1), (3, 65, 1)):
+            c = recur(seqs=seqs, channels=64, **{name: x}, out=Rows(9 * FAKE, seq, 0),
+                      **{k: Rows(2 * FAKE, 64, 0) for k in ("x", "gate", "input_gate") if k != name})
+            assert L.canon_gated_recurrence_step(c, None) == want, (name, seqs, seq)
