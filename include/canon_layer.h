@@ -8,6 +8,9 @@
  *   layer_norm       s = x, or x + residual rounded to the type dtype;
  *                    m = mean(s), v = mean((s - m)^2), r = 1 / sqrt(v + eps),
  *                    out = (s - m) r weight + bias, over the columns of each row.
+ *                    A row whose v + eps is outside [2^-126, 2^128), as with
+ *                    deviations of 2^64, or of 2^-64 at an eps of 0, is not
+ *                    normalised: its r is 0, infinite or imprecise.
  *   layer_norm_grad  with n = (s - m) r and g = dout weight:
  *                    dx = r (g - mean(g) - n mean(g n)) + dsum (the gradient that
  *                    reaches s itself; of both x and residual),
@@ -66,7 +69,7 @@ typedef struct {
     int64_t dtype;       /* canon_dtype_t of the canon_rows_t below */
     int64_t param_dtype; /* of weight and bias: dtype or CANON_F32 */
     int64_t seqs, rows, width;
-    double eps;
+    double eps; /* at least 0, at most the largest float */
     canon_rows_t x, residual; /* residual.p may be NULL (none) */
     canon_rows_t sum;         /* s, with residual only; .p may be NULL (not wanted) */
     canon_rows_t out;

@@ -60,6 +60,7 @@ canon_status_t norm_args(const canon_norm_t* c, bool grad, NormArgs* a)
     a->width = (int32_t)c->width;
     if (c->width > 0 && c->weight == nullptr) return CANON_EINVAL;
     if (grad && c->width > 0 && c->dweight == nullptr) return CANON_EINVAL;
+    if (!grad && !(c->eps >= 0. && c->eps <= (double)kMaxF)) return CANON_EINVAL;  // NaN too
     if (a->total > 0 && a->width > 0) {
         auto out_ok = [&](const canon_rows_t& r) {
             return out_valid(r, c->width, c->seqs, c->rows);

@@ -28,3 +28,19 @@ def test_a_step_in_place(canon):
         with pytest.raises(ValueError):
             canon.gated_recurrence_step(state.clone(), big[:9, :70], row[1], decay, row[2],
                                         out=big[:18:2, :70])
+
+
+def test_norm_eps(canon):
+    """Any finite eps that is not negative; without one a row of deviations of 2^-60."""
+    x, w = torch.randn(5, 300, device="cuda"), torch.ones(300, device="cuda")
+    for eps in (-1e-6, float("nan"), float("inf")):
+        with pytest.raises(ValueError):
+            canon.layer_norm(x, w, eps=eps)
+        with pytest.raises(ValueError):
+            canon.add_layer_norm(x, x, w, eps=eps)
+    for scale in (2.0 ** -60, 1.0, 2.0 ** 60):
+        d = (x.double() - x.double().mean(1, keepdim=True)) * scale
+        want = d / d.pow(2).mean(1, keepdim=True).sqrt()
+        got = canon.layer_norm(x * scale, w, eps=0.0)
+        # some 40 roundings of the row's sums and of each value
+        assert ((got - want).abs() <= 64 * 2.0 ** -24 * (1 + want.abs())).all()

@@ -32,3 +32,13 @@ def test_a_step_in_place_has_the_same_rows(layer):
             c = recur(seqs=seqs, channels=64, **{name: x}, out=Rows(9 * FAKE, seq, 0),
                       **{k: Rows(2 * FAKE, 64, 0) for k in ("x", "gate", "input_gate") if k != name})
             assert L.canon_gated_recurrence_step(c, None) == want, (name, seqs, seq)
+
+
+def test_norm_eps(layer):
+    """Neither negative nor NaN nor infinite; the backward pass does not read it."""
+    L, nan, inf = layer._lib(), float("nan"), float("inf")
+    for eps in (-1e-5, -inf, nan, inf, 1e39):
+        assert L.canon_layer_norm(norm(eps=eps), None) == 1, eps
+        assert L.canon_layer_norm_grad(norm(eps=eps), None, 0, None) == 3
+    for eps in (0.0, -0.0, 1e-5, 1e38):
+        assert L.canon_layer_norm(norm(eps=eps, rows=0), None) == 0, eps
