@@ -8,9 +8,8 @@
  *   layer_norm       s = x, or x + residual rounded to the type dtype;
  *                    m = mean(s), v = mean((s - m)^2), r = 1 / sqrt(v + eps),
  *                    out = (s - m) r weight + bias, over the columns of each row.
- *                    A row whose v + eps is outside [2^-126, 2^128), as with
- *                    deviations of 2^64, or of 2^-64 at an eps of 0, is not
- *                    normalised: its r is 0, infinite or imprecise.
+ *                    Of any size of the deviations whose r is a float; the
+ *                    row's sum has to be one too.
  *   layer_norm_grad  with n = (s - m) r and g = dout weight:
  *                    dx = r (g - mean(g) - n mean(g n)) + dsum (the gradient that
  *                    reaches s itself; of both x and residual),

@@ -170,6 +170,12 @@ __device__ __forceinline__ float team_sum(float v, float (*lds)[1])
     return s[0];
 }
 
+// Deviations whose squares are beyond 32 bits, or too small for them, are squared again
+// times a power of two: from z, the mean square and eps (NaN in a row that has one), the
+// factor, which is the same in a whole team.
+__device__ __forceinline__ bool norm_fits(float z) { return z >= 0x1p-100f && z <= kMaxF; }
+__device__ __forceinline__ float norm_factor(float z) { return z < 1.f ? 0x1p100f : 0x1p-80f; }
+
 template <typename T>
 __device__ __forceinline__ typename T::store_t* norm_row(const canon_rows_t& r, const NormArgs& a,
                                                          int32_t row)
@@ -214,7 +220,7 @@ __global__ __launch_bounds__(TEAM < 256 ? 256 : TEAM) void k_norm(NormArgs a)
     constexpr int V = kNormV<T>, THREADS = TEAM < 256 ? 256 : TEAM, TEAMS = THREADS / TEAM;
     using E = typename T::store_t;
     using W = typename P::store_t;
-    __shared__ float lds[2][THREADS / 64][1];
+    __shared__ float lds[3][THREADS / 64][1];
     const int lane = threadIdx.x % TEAM;
     const int team = TEAM < 64 ? threadIdx.x / TEAM : uniform((int32_t)(threadIdx.x / TEAM));
     float w[NV][V], b[NV][V];
@@ -262,8 +268,21 @@ __global__ __launch_bounds__(TEAM < 256 ? 256 : TEAM) void k_norm(NormArgs a)
             }
             q += tree(d);
         }
-        const float rstd =
-            __builtin_amdgcn_rsqf(fma32(team_sum<TEAM>(q, lds[1]), a.inv_width, a.eps));
+        const float z = fma32(team_sum<TEAM>(q, lds[1]), a.inv_width, a.eps);
+        float rstd = __builtin_amdgcn_rsqf(z);
+        if (!norm_fits(z)) {
+            const float c = norm_factor(z);
+            q = 0.f;
+#pragma unroll
+            for (int k = 0; k < NV; ++k) {
+                float d[V];
+#pragma unroll
+                for (int j = 0; j < V; ++j) d[j] = v[k][j] * c * (v[k][j] * c);
+                q += tree(d);
+            }
+            q = team_sum<TEAM>(q, lds[2]);
+            rstd = __builtin_amdgcn_rsqf(fma32(q, a.inv_width, a.eps * c * c)) * c;
+        }
         if (a.stats && lane == 0) {
             a.stats[2 * (int64_t)row] = mean;
             a.stats[2 * (int64_t)row + 1] = rstd;
@@ -411,7 +430,7 @@ __global__ __launch_bounds__(1024) void k_norm_loop(NormArgs a)
     constexpr int V = kNormV<T>, STEP = 1024 * V, U = kLoopU;
     using E = typename T::store_t;
     using W = typename P::store_t;
-    __shared__ float lds[2][16][1];
+    __shared__ float lds[3][16][1];
     const int c0 = threadIdx.x * V;
     for (int32_t row = blockIdx.x; row < a.total; row += gridDim.x) {
         const E* x = norm_row<T>(a.x, a, row);
@@ -459,16 +478,25 @@ __global__ __launch_bounds__(1024) void k_norm_loop(NormArgs a)
         float s = 0.f, q = 0.f;
         each([&](int, float(&v)[V]) { s += tree(v); });
         const float mean = team_sum<1024>(s, lds[0]) * a.inv_width;
-        each([&](int c, float(&v)[V]) {
+        auto squares = [&](float by) {
+            q = 0.f;
+            each([&](int c, float(&v)[V]) {
 #pragma unroll
-            for (int j = 0; j < V; ++j) {
-                v[j] = c + j < a.width ? v[j] - mean : 0.f;
-                v[j] *= v[j];
-            }
-            q += tree(v);
-        });
-        const float rstd =
-            __builtin_amdgcn_rsqf(fma32(team_sum<1024>(q, lds[1]), a.inv_width, a.eps));
+                for (int j = 0; j < V; ++j) {
+                    v[j] = c + j < a.width ? (v[j] - mean) * by : 0.f;
+                    v[j] *= v[j];
+                }
+                q += tree(v);
+            });
+            return q;
+        };
+        const float z = fma32(team_sum<1024>(squares(1.f), lds[1]), a.inv_width, a.eps);
+        float rstd = __builtin_amdgcn_rsqf(z);
+        if (!norm_fits(z)) {
+            const float by = norm_factor(z);
+            q = team_sum<1024>(squares(by), lds[2]);
+            rstd = __builtin_amdgcn_rsqf(fma32(q, a.inv_width, a.eps * by * by)) * by;
+        }
         if (a.stats && threadIdx.x == 0) {
             a.stats[2 * (int64_t)row] = mean;
             a.stats[2 * (int64_t)row + 1] = rstd;

@@ -44,3 +44,24 @@ def test_norm_eps(canon):
         got = canon.layer_norm(x * scale, w, eps=0.0)
         # some 40 roundings of the row's sums and of each value
         assert ((got - want).abs() <= 64 * 2.0 ** -24 * (1 + want.abs())).all()
+
+
+@pytest.mark.parametrize("width", [60, 700, 4000, 9000, 20001])
+def test_norm_of_any_size(canon, width):
+    """Rows whose squares leave 32 bits on either side have the outputs of the same rows times
+    a power of two, whose steps are all exact, and leave the rows beside them as they are."""
+    x = torch.randn(24, width, device="cuda")
+    w, b = torch.rand(width, device="cuda"), torch.rand(width, device="cuda")
+    x -= x.mean(1, keepdim=True)
+    scale = torch.tensor([2.0 ** k for k in (0, -90, 0, 55, 80, -60, 0, 100, -100, 30, -30, 0)] * 2,
+                         device="cuda")[:, None]
+    stats, own = canon.layer_norm_stats(x), canon.layer_norm_stats(x)
+    want = canon.layer_norm(x, w, b, eps=0.0, stats=own)
+    out = canon.layer_norm(x * scale, w, b, eps=0.0, stats=stats)
+    assert torch.equal(out, want) and torch.equal(stats[:, 0], own[:, 0] * scale[:, 0])
+    assert torch.equal(stats[:, 1], own[:, 1] / scale[:, 0])
+    dout = torch.randn_like(x)
+    g = canon.layer_norm_grad(dout, x * scale, w, stats, b)
+    h = canon.layer_norm_grad(dout, x, w, own, b)
+    assert torch.equal(g.dx, h.dx / scale)
+    assert torch.equal(g.dweight, h.dweight) and torch.equal(g.dbias, h.dbias)
