@@ -2,6 +2,7 @@
 a sort in 80-bit numbers."""
 import math
 
+import numpy as np
 import pytest
 
 pytestmark = pytest.mark.gpu
@@ -20,13 +21,15 @@ def canon():
     return c
 
 
-def margin(vocab):
-    """What the kernel's rounding can shift a border by, as a share of the whole, which is
-    one at least: a weight is off by 2^-51 of itself and by half a step of 2^-S, S = 62 -
-    ceil(log2 vocab), 50 at most; a sum's other roundings (u or top_p times it in 64 bits)
-    add 2^-52.  2^-28 at 2^17 tokens, 2^-36 at 2^13."""
-    steps = min(50, 62 - max(0, math.ceil(math.log2(max(vocab, 1)))))
-    return 2.0 ** -50 + vocab * 2.0 ** -(steps + 1)
+def margin(x, temperature=1.0):
+    """What the kernel's rounding can shift a border of row x by, as a share of the sum of
+    what is kept.  A weight is off by 2^-51 of itself and by half a step of 2^-S, S = 62 -
+    ceil(log2 vocab), 50 at most; other roundings (of u or top_p times the sum in 64 bits) add
+    2^-52.  What filters keep are the largest weights, whose mean is at least that of all: so
+    the half steps are at most 2^-(S + 1) over the mean weight of all."""
+    steps = min(50, 62 - max(0, math.ceil(math.log2(max(x.size, 1)))))
+    x = x[x > -INF].astype("float64")
+    return 2.0 ** -50 + 2.0 ** -(steps + 1) / np.exp((x - x.max()) / temperature).mean()
 
 
 def check(canon, x, u, least=0.9, **settings):
@@ -38,7 +41,7 @@ def check(canon, x, u, least=0.9, **settings):
     for i in range(len(x)):
         s = {k: v[i].item() if torch.is_tensor(v) else v for k, v in settings.items()}
         want, gap = layer_ref.sample(values[i], float(u[i]), **s)
-        if gap > margin(x.shape[1]):
+        if gap > margin(values[i], s.get("temperature", 1.0)):
             compared += 1
             assert got[i] == want, (settings, i, int(got[i]), want)
     assert compared >= max(1, least * len(x)), (settings, compared, len(x))
@@ -92,7 +95,6 @@ def test_logits_further_apart_than_the_largest_number(canon, dtype, vocab):
 
 def test_top_k_of_other_kinds(canon):
     """Integers of any kind and size; nothing else."""
-    import numpy as np
     x, u = (t.cuda() for t in logits(F32, 3, 20))
     want = canon.sample(x, u, top_k=4)
     assert torch.equal(canon.sample(x, u, top_k=np.int64(4)), want)
@@ -102,3 +104,13 @@ def test_top_k_of_other_kinds(canon):
     for k in (4.0, "4", None):
         with pytest.raises(TypeError):
             canon.sample(x, u, top_k=k)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16, F16])
+@pytest.mark.parametrize("vocab", [131072, 700001, (1 << 20) + 3])
+def test_large_vocabularies(canon, dtype, vocab):
+    """Four rows in five and more further from every border than the weights' rounding."""
+    x, u = logits(dtype, 5, vocab, seed=vocab)
+    for s in (dict(), dict(top_p=0.9), dict(top_k=50), dict(top_k=3000, top_p=0.8),
+              dict(temperature=0.7, min_p=0.01), dict(temperature=30.0, top_k=40000)):
+        check(canon, x, u, least=0.8, **s)
