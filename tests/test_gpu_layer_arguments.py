@@ -65,3 +65,17 @@ def test_norm_of_any_size(canon, width):
     h = canon.layer_norm_grad(dout, x, w, own, b)
     assert torch.equal(g.dx, h.dx / scale)
     assert torch.equal(g.dweight, h.dweight) and torch.equal(g.dbias, h.dbias)
+
+
+@pytest.mark.parametrize("decay", [False, True])
+def test_sequences_without_rows(canon, decay):
+    """States and their gradients pass through; a decay's gradient is zero."""
+    x = torch.empty(3, 0, 70, device="cuda")
+    init, dfinal = torch.randn(3, 70, device="cuda"), torch.randn(3, 70, device="cuda")
+    d = torch.rand(70, device="cuda") if decay else None
+    final, keep = torch.zeros_like(init), canon.gated_recurrence_states(x)
+    out = canon.gated_recurrence(x, x, d, x, init_state=init, final_state=final, states=keep)
+    assert out.shape == x.shape and torch.equal(final, init)
+    g = canon.gated_recurrence_grad(x, x, x, keep, d, x, d_final_state=dfinal)
+    assert torch.equal(g.dinit_state, dfinal) and g.dx.shape == x.shape
+    assert g.ddecay is None if d is None else not g.ddecay.any()
