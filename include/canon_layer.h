@@ -19,7 +19,10 @@
  *                    a = r, c = 1 - r;
  *                    h[t,d] = a h[t-1,d] + c i x[t,d], out = h.
  *                    Gradients are the formula's; where c is 0 (an a of 1), the
- *                    slope of the square root counts as 0.
+ *                    slope of the square root counts as 0.  a is 1 + e with e in
+ *                    32 bits: one near 0 is off by some 2^-24, and an a of 0 (a
+ *                    gate of minus infinity without decay) leaves nothing of any
+ *                    finite h[t-1].
  *   sample           w[j] = exp((logits[j] - max) / temperature), held as a multiple
  *                    of 2^-S, S = 62 - ceil(log2 vocab), 50 at most; tokens ranked by
  *                    logits, the lowest index first among equals; kept are
@@ -29,6 +32,7 @@
  *                      of those the ones whose weight is at least min_p;
  *                    the token is the first one in index order at which the sum of
  *                    the kept weights up to it exceeds u times their whole sum.
+ *                    (top_p and u times a sum: in 64-bit floats.)
  *
  * Everything is computed in 32 bits and rounded once where it is stored, but for
  * the recurrence's carried state and the sampling's weights, in 64.  Each sum is

@@ -24,7 +24,9 @@ struct NormArgs {
 
 // Rows of a chunk of the sums over rows: as many chunks as fill the chip twice (of rows
 // wider than kNormGradWide, which are cut into 5 parts or more, a quarter), then longer
-// ones, whose partial sums are at most a 24th of the rows' bytes.
+// ones, whose partial sums are at most a 24th of the rows' bytes.  Backward passes with
+// all chunks and with a quarter: 777 x 20000 float32 65 and 53 us, 1024 x 32768 141 and 87,
+// 4096 x 12288 bf16 88 and 77, but 2000 x 8192 float32 44 and 57, 3001 x 1021 bf16 17 and 21.
 constexpr int64_t kNormChunks = 512;
 constexpr int64_t kNormChunkMost = 64;
 constexpr int32_t kNormGradWide = 8192;

@@ -8,9 +8,9 @@
 // of a block (512 rows) follow each other in the workgroup; forward, a row of the next
 // round is loaded where one of this round has been used.
 //
-// Memory bounds it, and vector issue nearly as much: 36 instructions a value forward (66%
-// of the time), 82 backward (75%).  8 x 2048 x 4096 bf16, both gates: forward 113 us (4.8
-// TB/s), backward 233 (4.0).  8 waves of 16 rows, at 256 registers a lane, took 131 and
+// Memory bounds it, and vector issue nearly as much: 38 instructions a value forward (69%
+// of the time), 86 backward (81%).  8 x 2048 x 4096 bf16, both gates: forward 113 us (4.8
+// TB/s), backward 227 (4.1).  8 waves of 16 rows, at 256 registers a lane, took 131 and
 // 255 where these then took 122 and 243; rows of the next round in flight in the backward
 // pass too cost spilled registers at 16 waves (338), and gained nothing at 8 (260).
 //
@@ -20,8 +20,7 @@
 // leaves nothing of any finite h, as h + (e h + v), whose rounding is that of e h, would.
 // The start states of rounds and chunks are folded in 64 bits inside a block and rounded to
 // 32 between blocks: an h that loses less than its last bit in a chunk would stay as it is
-// otherwise.  (Chunks of a round folded on in 32 bits take 2 us less of the backward pass's
-// 228.)
+// otherwise.  (Chunks of a round folded on in 32 bits take 2 us less of the backward pass.)
 #pragma once
 
 #include <type_traits>
@@ -305,9 +304,8 @@ __device__ __forceinline__ double carried(float h, double q, double s, bool end)
 
 // The state that a block starts with, given those of the first one in ws_h: where
 // sequences have few blocks, from the folds of the n before it, which are step slots apart
-// (else k_recur_carry has folded them, into its own ws_h).  With 32 blocks the outputs take
-// 62 us so, against 59 and a launch of 6 (16384 x 2048 bf16); the reads grow with the
-// square.
+// (else k_recur_carry has folded them, into its own ws_h).  The reads grow with the square;
+// kRecurFold has both ways' times.
 template <int V>
 __device__ __forceinline__ void block_start(const RecurArgs& a, const Lane& l, int64_t slot, int32_t n,
                                             int32_t step, float (&h)[V])

@@ -21,13 +21,13 @@
 // Where a list does not fit (thousands of tokens in a step, as where all are equal),
 // the whole row is read again for every digit instead.
 //
-// What bounds it: of a row of 131072 in bfloat16, of which 256 fill the chip, the
-// largest takes 12 us (memory), the weights 31 (27 instructions in 64 bits a token, 23 us
-// of issue), the steps of top_p 21 (LDS atomics and the pass's start), their list and
-// the digits 10.  Adding up the weights themselves by steps with 64-bit atomics, so that
-// they need not be computed again, took 50 instead of 23, and paid only where top_p keeps
-// few tokens (0.5: 88 us for 92; 0.9: 119 for 100).  A small row costs its latency: 10 us
-// from call to call with no filter, 20 with top_p.
+// What bounds it: passes over a row by one compute unit, and in those over weights vector
+// issue (27 instructions in 64 bits a token).  256 rows of 131072 in bfloat16, which fill
+// the chip, and one such row: the largest logit alone 18 and 11 us, no filter 48 and 34,
+// top_k 50 31 and 22, top_p 0.9 86 and 70, which goes over the row for the steps and again
+// for their list.  64 rows of 32000: 6, 15, 13 and 32.  (In an earlier version, where top_p
+// 0.5 took 92 us and 0.9 100, adding up the weights themselves by steps with 64-bit atomics,
+// so that they need not be computed again, took 88 and 119.)
 #pragma once
 
 #include <type_traits>
@@ -581,6 +581,8 @@ __global__ __launch_bounds__(kSampleThreads) void k_sample(SampleArgs a)
                     sum[0] += c[j];
                 }
                 scan_before(sum, bounds, all);
+                // (beyond some 2^19 tokens a share's rounding may pass these margins, and
+                // the border lie outside the steps: then the whole row is searched)
                 uint32_t b1 = kBins - 1, b2 = kBins - 1;
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
