@@ -19,6 +19,11 @@ def canon():
     torch.cuda.empty_cache()
 
 
+@pytest.fixture(autouse=True)
+def seed():
+    torch.manual_seed(5)
+
+
 def normal(*shape, dtype=BF16):
     return torch.empty(*shape, dtype=dtype, device="cuda").normal_()
 
