@@ -305,7 +305,7 @@ def gated_recurrence_step(state: torch.Tensor, x: torch.Tensor, gate: torch.Tens
                           out: Optional[torch.Tensor] = None) -> torch.Tensor:
     """gated_recurrence for one row of each sequence: x, gate, input_gate [sequences,
     channels].  The state [sequences, channels] is updated in place, or, with
-    out_state, read and written there."""
+    out_state, read and written there.  out may be x or a gate."""
     what = "gated_recurrence_step"
     _same(what, x.device, state, gate, decay, input_gate, out_state, out)
     if x.dim() != 2:
